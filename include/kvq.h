@@ -53,7 +53,8 @@ typedef enum kvq_status {
   KVQ_ERR_SCRATCH_TOO_SMALL = 4 /* kvq_decode_attn_int4_noalloc: request needs more than its fixed scratch */
 } kvq_status;
 
-typedef enum kvq_dtype { KVQ_F32 = 0, KVQ_BF16 = 1 } kvq_dtype;
+/* KVQ_F16 is taken by kvq_prompt_attn only. */
+typedef enum kvq_dtype { KVQ_F32 = 0, KVQ_BF16 = 1, KVQ_F16 = 2 } kvq_dtype;
 
 #define KVQ_HEAD_DIM 128
 #define KVQ_PAGE_SIZE 64
@@ -65,6 +66,7 @@ typedef enum kvq_dtype { KVQ_F32 = 0, KVQ_BF16 = 1 } kvq_dtype;
 #define KVQ_DEVERR_NONFINITE 0x4 /* NaN/Inf in a key, value or query row (row skipped) */
 #define KVQ_DEVERR_RANGE 0x8     /* fp16 scale or offset saturated at +-65504 */
 #define KVQ_DEVERR_TIMEOUT 0x10  /* a bounded wait on a copy gave up (results invalid) */
+#define KVQ_DEVERR_POOL 0x20     /* no free page left, or a page freed more often than it is held */
 
 /*
  * Paged int4 cache of one full-attention layer.
@@ -322,6 +324,172 @@ kvq_status kvq_decode_attn_int4_noalloc(const kvq_int4_cache* cache, const float
                                         kvq_dtype dtype, int B, int S, int num_q_heads, const int32_t* ctx_len,
                                         const void* k_new, const void* v_new, float sm_scale, float eps, float* out,
                                         float* q_rot_out, int32_t* dev_err, kvq_stream_t stream);
+
+/* ------------------------------------------------------------------ a prompt's attention */
+
+/*
+ * kvq_prompt_attn -- causal attention over whole prompts, packed end to end without padding.
+ *   Sequence b (0..B-1) holds tokens cu_seqlens[b] .. cu_seqlens[b+1]-1 of the packed tensors; its
+ *   token i attends to its tokens max(0, i-window+1)..i (window <= 0: 0..i):
+ *     out_i = sum_j softmax_j(sm_scale q_i.k_j) v_j .
+ *   q, k and v are used as given, as in kvq_decode_attn_fp8_swa: for a full-attention layer pass
+ *   g_q*g_k*n(q) and n(k) (scores do not change under the rotation, so none is applied), and the
+ *   same n(k) to kvq_rotate_quant_append (its norm leaves a normalised row as it is, up to eps).
+ *   q:        device [T][num_q_heads][128] of `dtype` (KVQ_BF16 or KVQ_F16); query head hq reads
+ *             KV head hq / (num_q_heads/num_kv_heads).
+ *   k, v:     device [T][num_kv_heads][128] of `dtype`.
+ *   strides:  host int64[8] or NULL (packed): elements between tokens and between heads of q, k, v
+ *             and out, in this order (q token, q head, k token, ...). Each a positive multiple of 8;
+ *             rows of 128 elements are contiguous.
+ *   cu_seqlens: device int32[B+1], 0 = cu_seqlens[0] <= ... <= cu_seqlens[B] <= T (else the
+ *             sequences outside that are skipped, KVQ_DEVERR_POS). Empty sequences are allowed.
+ *             Rows of out behind cu_seqlens[B] are left as they were.
+ *   out:      device [T][num_q_heads][128] of `dtype`, rounded once from fp32. It must not overlap
+ *             the inputs.
+ *   workspace: device, >= kvq_prompt_workspace_bytes(T, B, num_q_heads, num_kv_heads), 256-byte
+ *             aligned; contents need no initialisation. Calls that may overlap need one each.
+ *   A row is NaN only where a key or value that it attends to makes it so: non-finite values in
+ *   masked places do not reach it. Nothing is skipped for non-finite inputs.
+ * Requires 1 <= B <= KVQ_MAX_SEQS, 0 <= T (T == 0 is a no-op), sm_scale > 0; q, k, v and out
+ * 16-byte aligned; T*num_q_heads <= 2^30.
+ */
+size_t kvq_prompt_workspace_bytes(int T, int B, int num_q_heads, int num_kv_heads);
+kvq_status kvq_prompt_attn(const void* q, const void* k, const void* v, kvq_dtype dtype, int T, int B,
+                           int num_q_heads, int num_kv_heads, const int64_t* strides, const int32_t* cu_seqlens,
+                           int window, float sm_scale, void* out, void* workspace, size_t workspace_bytes,
+                           int32_t* dev_err, kvq_stream_t stream);
+
+/* ------------------------------------------------------------------ a tree of drafted tokens */
+
+#define KVQ_MAX_TREE 64 /* drafted tokens of one sequence's tree */
+#define KVQ_MAX_CACHES 64 /* layers of one kvq_tree_commit_* or kvq_pages_copy call */
+
+/*
+ * kvq_tree_attn_int4 -- attention of a tree of drafted tokens over the int4 cache.
+ *   Sequence b has ctx_len[b] cached tokens and N drafted ones, whose keys and values lie behind
+ *   the context: drafted token i in the slot of position ctx_len[b] + i. Its query attends to
+ *   the whole context and to the drafted tokens of its mask:
+ *     tree_mask: device uint64[B][N]; bit j of word [b][i] set: token i attends to drafted token j
+ *             (its own bit as well, where it attends to itself; bits from N on are ignored). A row
+ *             that attends to nothing (no context, no bit) gives 0. A batch of smaller trees is
+ *             padded with tokens that no mask names; their own rows may be ignored.
+ *   q:        device [B][N][num_q_heads][128] of `dtype`, pre-norm: q~ = M_q n(q).
+ *   k_new, v_new: device [B][N][num_kv_heads][128] of `dtype`, or both NULL: appended at positions
+ *             ctx_len[b] + i first, as by kvq_rotate_quant_append.
+ *   out:      device [B][N][num_q_heads][128] of out_dtype (KVQ_F32 or KVQ_BF16).
+ *   workspace: device, >= kvq_tree_workspace_bytes(B, N, num_q_heads, num_kv_heads), 256-byte
+ *             aligned; contents need no initialisation.
+ *   Other arguments, readings of positions and errors as kvq_decode_attn_int4. A position whose
+ *   block-table entry is outside the pool is skipped (KVQ_DEVERR_PAGE).
+ * Requires 1 <= B <= KVQ_MAX_SEQS, 1 <= N <= KVQ_MAX_TREE, num_q_heads/num_kv_heads <= 64.
+ */
+size_t kvq_tree_workspace_bytes(int B, int N, int num_q_heads, int num_kv_heads);
+kvq_status kvq_tree_attn_int4(const kvq_int4_cache* cache, const float* Mq, const float* Mk, const void* q,
+                              kvq_dtype dtype, int B, int N, int num_q_heads, const int32_t* ctx_len,
+                              const uint64_t* tree_mask, const void* k_new, const void* v_new, float sm_scale,
+                              float eps, void* out, kvq_dtype out_dtype, void* workspace, size_t workspace_bytes,
+                              int32_t* dev_err, kvq_stream_t stream);
+/* The same with the FWHT prologue (wq, wk: device float[128], 16-byte aligned; kvq_fold_qk_fwht). */
+kvq_status kvq_tree_attn_int4_fwht(const kvq_int4_cache* cache, const float* wq, const float* wk, const void* q,
+                                   kvq_dtype dtype, int B, int N, int num_q_heads, const int32_t* ctx_len,
+                                   const uint64_t* tree_mask, const void* k_new, const void* v_new, float sm_scale,
+                                   float eps, void* out, kvq_dtype out_dtype, void* workspace, size_t workspace_bytes,
+                                   int32_t* dev_err, kvq_stream_t stream);
+
+/*
+ * kvq_tree_attn_fp8_swa -- the same over the e4m3 ring of a sliding-window layer. Drafted token i
+ *   lies in slot (pos0[b] + i) % capacity; it stands at position
+ *     pos0[b] + max(1, number of drafted tokens it attends to) - 1
+ *   (its depth in the tree), and its window reaches back from there: context positions above that
+ *   position - window, and the drafted tokens of its mask.
+ *   q is used as given; workspace and out as above; other arguments as kvq_decode_attn_fp8_swa.
+ * Requires window >= N and capacity >= window + N - 1.
+ */
+kvq_status kvq_tree_attn_fp8_swa(const kvq_fp8_ring* ring, const void* q, kvq_dtype dtype, int B, int N,
+                                 int num_q_heads, const int32_t* pos0, const uint64_t* tree_mask, int window,
+                                 const void* k_new, const void* v_new, float k_scale, float v_scale, float sm_scale,
+                                 void* out, kvq_dtype out_dtype, void* workspace, size_t workspace_bytes,
+                                 int32_t* dev_err, kvq_stream_t stream);
+
+/*
+ * kvq_tree_commit_int4 / kvq_tree_commit_fp8 -- the accepted branch of each tree becomes context:
+ *   the record (codes, scales, offsets) of drafted token path[b][i], at position
+ *   ctx_len[b] + path[b][i], moves to position ctx_len[b] + i, for i < n_accept[b], in every one
+ *   of num_caches layers in one launch. All of a sequence's records are read before any is
+ *   written, so any path (also with repeated tokens) gives the records as they were before.
+ *   caches / rings: host array of num_caches descriptors (1..KVQ_MAX_CACHES), of the same number of
+ *             KV heads (rings: of the same capacity); each with its own block table.
+ *   path:     device int32[B][N], the accepted tokens in order; an entry outside 0..N-1 within the
+ *             first n_accept[b] is skipped (KVQ_DEVERR_POS).
+ *   n_accept: device int32[B], clamped to 0..N (KVQ_DEVERR_POS if it had to be).
+ *   ctx_out:  device int32[B] or NULL: receives ctx_len[b] + n_accept[b]; must not overlap ctx_len.
+ * Requires 1 <= B <= KVQ_MAX_SEQS, 1 <= N <= KVQ_MAX_TREE.
+ */
+kvq_status kvq_tree_commit_int4(const kvq_int4_cache* caches, int num_caches, int B, int N, const int32_t* ctx_len,
+                                const int32_t* path, const int32_t* n_accept, int32_t* ctx_out, int32_t* dev_err,
+                                kvq_stream_t stream);
+kvq_status kvq_tree_commit_fp8(const kvq_fp8_ring* rings, int num_caches, int B, int N, const int32_t* pos0,
+                               const int32_t* path, const int32_t* n_accept, int32_t* ctx_out, int32_t* dev_err,
+                               kvq_stream_t stream);
+
+/* ------------------------------------------------------------------ the page pool */
+
+/*
+ * The pool of an int4 cache's pages is one reference count per page on the device:
+ *   page_refs: device int32[num_pages]; 0: free, n: held by n block-table entries. All zero at first.
+ * Layers that share a block table share the pool. Unused block-table entries hold -1. The calls
+ * below change counts and tables only, in one or two launches; kvq_pages_copy moves the data of the
+ * layers. New pages are always the lowest free ones, in ascending order, handed to the requests in
+ * theirs, so the outcome does not depend on timing.
+ *   block_table: device int32[num_seqs][max_pages_per_seq], written.
+ *   n (0..KVQ_MAX_SEQS) rows are named by seq_ids (or parents / children): device int32[n]. A row
+ *   outside the table, a length outside 0..64*max_pages_per_seq or the second naming of a row
+ *   (the lower index counts) skips the request (KVQ_DEVERR_POS).
+ * Requires 1 <= num_pages, num_seqs*max_pages_per_seq <= 2^30, max_pages_per_seq <= 2^24.
+ */
+
+/* kvq_pages_alloc -- sequence seq_ids[i] grows from len_old[i] to len_new[i] tokens: its pages
+ * ceil(len_old/64) .. ceil(len_new/64)-1 get free pages (count 1). Entries for which none is left
+ * are set to -1 (KVQ_DEVERR_POOL). */
+kvq_status kvq_pages_alloc(int32_t* page_refs, int num_pages, int32_t* block_table, int num_seqs,
+                           int max_pages_per_seq, int n, const int32_t* seq_ids, const int32_t* len_old,
+                           const int32_t* len_new, int32_t* dev_err, kvq_stream_t stream);
+
+/* kvq_pages_fork -- sequence children[i] (whose row holds no pages) becomes a copy of the first
+ * len[i] tokens of parents[i]: full pages are shared (count + 1), a last page that is only partly
+ * filled is replaced by a free one. copy_src[i] / copy_dst[i] (device int32[n]) receive that page of
+ * the parent and of the child for kvq_pages_copy, -1 where there is none. A row may not be parent
+ * and child in one call (KVQ_DEVERR_POS, skipped). No free page: entry -1, KVQ_DEVERR_POOL. An
+ * entry of the parent's outside the pool: entry -1, KVQ_DEVERR_PAGE. */
+kvq_status kvq_pages_fork(int32_t* page_refs, int num_pages, int32_t* block_table, int num_seqs,
+                          int max_pages_per_seq, int n, const int32_t* parents, const int32_t* children,
+                          const int32_t* len, int32_t* copy_src, int32_t* copy_dst, int32_t* dev_err,
+                          kvq_stream_t stream);
+
+/* kvq_pages_free -- sequence seq_ids[i] shrinks from len_old[i] to len_new[i] tokens: its pages
+ * ceil(len_new/64) .. ceil(len_old/64)-1 are given back (count - 1; free at 0) and their entries set
+ * to -1. An entry outside the pool is passed over (KVQ_DEVERR_PAGE), a count that is 0 already stays
+ * (KVQ_DEVERR_POOL). */
+kvq_status kvq_pages_free(int32_t* page_refs, int num_pages, int32_t* block_table, int num_seqs,
+                          int max_pages_per_seq, int n, const int32_t* seq_ids, const int32_t* len_old,
+                          const int32_t* len_new, int32_t* dev_err, kvq_stream_t stream);
+
+/* kvq_pages_compact -- the L pages in use move to pages 0..L-1: those behind, in ascending order, to
+ * the free ones in front, in ascending order. Counts and every entry of the table are rewritten.
+ * copy_src / copy_dst (device int32[num_pages/2]) receive the moves and *n_moves (device) their
+ * number; a page is never both source and destination. Entries that name a page with count 0 stay
+ * (KVQ_DEVERR_PAGE). Every table that names pages of the pool has to be rewritten: there is one. */
+kvq_status kvq_pages_compact(int32_t* page_refs, int num_pages, int32_t* block_table, int num_seqs,
+                             int max_pages_per_seq, int32_t* copy_src, int32_t* copy_dst, int32_t* n_moves,
+                             int32_t* dev_err, kvq_stream_t stream);
+
+/* kvq_pages_copy -- page src[i] to page dst[i], all KV heads, in every one of num_caches layers, in
+ * one launch, for i < n, or i < min(n, *count) where count (device, may be NULL) is given. A pair
+ * with -1 on either side is passed over; one with a page outside the pool too (KVQ_DEVERR_PAGE). A
+ * page that is the destination of one pair may not be in another pair: its bytes are unspecified.
+ *   caches: host array of num_caches descriptors (1..KVQ_MAX_CACHES); block tables are not read. */
+kvq_status kvq_pages_copy(const kvq_int4_cache* caches, int num_caches, int n, const int32_t* src,
+                          const int32_t* dst, const int32_t* count, int32_t* dev_err, kvq_stream_t stream);
 
 #ifdef __cplusplus
 }

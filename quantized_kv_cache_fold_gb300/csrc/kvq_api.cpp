@@ -29,6 +29,15 @@ int popcount32(uint32_t x) {
   return c;
 }
 
+bool heads_ok(int Hq, int Hkv, int S) {
+  if (Hq < 1 || Hkv < 1 || Hq % Hkv) return false;
+  return S * (Hq / Hkv) <= kvq::kMaxRows;
+}
+
+}  // namespace
+
+namespace kvq {
+
 kvq_status check_int4_cache(const kvq_int4_cache* c) {
   if (!c) return KVQ_ERR_INVALID_ARG;
   if (c->head_dim != KVQ_HEAD_DIM || c->page_size != KVQ_PAGE_SIZE) return KVQ_ERR_UNSUPPORTED;
@@ -48,12 +57,10 @@ kvq_status check_ring(const kvq_fp8_ring* r) {
   return KVQ_OK;
 }
 
-bool heads_ok(int Hq, int Hkv, int S) {
-  if (Hq < 1 || Hkv < 1 || Hq % Hkv) return false;
-  return S * (Hq / Hkv) <= kvq::kMaxRows;
-}
+}  // namespace kvq
 
-}  // namespace
+using kvq::check_int4_cache;
+using kvq::check_ring;
 
 extern "C" {
 

@@ -101,6 +101,80 @@ kvq_status check_decode_int4_args(const kvq_int4_cache* cache, const float* Mq, 
 // Limit of the split-K attention kernel's stage waits for later launches (kvq_set_stage_wait_limit_ns).
 void set_stage_wait_limit_ns(unsigned long long ns);
 
+// SMs of the current device (cached).
+int device_sms();
+
+// ---- prompt attention (kvq_prompt.cu)
+struct PromptJob {
+  const void *q, *k, *v;
+  void* out;
+  int f16;  // 1: fp16, 0: bf16
+  int T, B, Hq, Hkv;
+  long long qs_t, qs_h, ks_t, ks_h, vs_t, vs_h, os_t, os_h;  // elements
+  const int32_t* cu_seqlens;
+  int window;  // 0: none
+  float sm_scale;
+  void* workspace;
+  int32_t* dev_err;
+};
+size_t workspace_prompt_bytes(int T, int B, int Hq, int Hkv);
+cudaError_t launch_prompt(const PromptJob& job, cudaStream_t stream);
+
+// ---- tree attention (kvq_tree.cu)
+struct TreeJob {
+  int fmt;  // 0 = int4 paged, 1 = fp8 ring
+  kvq_int4_cache cache;
+  kvq_fp8_ring ring;
+  int window;
+  float k_scale, v_scale;
+  int B, N, Hq, Hkv;
+  const int32_t* ctx;
+  const uint64_t* mask;
+  const float* q_rot;  // int4: rotated queries (workspace)
+  const void* q;       // fp8: queries as given
+  int q_bf16;
+  float sm_scale;
+  void* out;
+  int out_bf16;
+  float* partials;  // workspace
+  int32_t* dev_err;
+};
+size_t workspace_tree_partials_bytes(int B, int N, int Hq, int Hkv);
+cudaError_t launch_tree(const TreeJob& job, cudaStream_t stream);
+
+// ---- page pool, page copies and commits (kvq_pages.cu)
+struct PoolJob {
+  int32_t* page_refs;
+  int num_pages;
+  int32_t* block_table;
+  int num_seqs, max_pages_per_seq;
+  int n;
+  const int32_t *a, *b, *c;  // alloc, free: ids, old and new lengths; fork: parents, children, lengths
+  int32_t *copy_src, *copy_dst, *n_moves;
+  int32_t* dev_err;
+};
+cudaError_t launch_pages_alloc(const PoolJob& job, cudaStream_t stream);
+cudaError_t launch_pages_fork(const PoolJob& job, cudaStream_t stream);
+cudaError_t launch_pages_free(const PoolJob& job, cudaStream_t stream);
+cudaError_t launch_pages_compact(const PoolJob& job, cudaStream_t stream);
+
+// The caches or rings of one call over several layers (a kernel parameter). Rings: max_pages is the
+// number of 64-slot blocks.
+struct CacheSet {
+  uint8_t* pages[KVQ_MAX_CACHES];
+  const int32_t* table[KVQ_MAX_CACHES];
+  int32_t num_pages[KVQ_MAX_CACHES], num_seqs[KVQ_MAX_CACHES], max_pages[KVQ_MAX_CACHES];
+  int32_t count, heads;
+};
+cudaError_t launch_pages_copy(const CacheSet& cs, int n, const int32_t* src, const int32_t* dst, const int32_t* count,
+                              int32_t* dev_err, cudaStream_t stream);
+cudaError_t launch_tree_commit(int fmt, const CacheSet& cs, int B, int N, const int32_t* ctx_len, const int32_t* path,
+                               const int32_t* n_accept, int32_t* ctx_out, int32_t* dev_err, cudaStream_t stream);
+
+// Argument checks shared by the C-ABI translation units.
+kvq_status check_int4_cache(const kvq_int4_cache* c);
+kvq_status check_ring(const kvq_fp8_ring* r);
+
 size_t workspace_qrot_bytes(int B, int S, int Hq);
 size_t workspace_partials_bytes(int B, int S, int Hq, int Hkv);
 
