@@ -2,103 +2,547 @@
 //
 //   o_i = sum_j softmax_j(sm_scale q_i.k_j) v_j, j in [max(0, i - window + 1), i] of i's sequence.
 //
-// One warp per (token, query head): every lane holds four dims of q, of the running sum and of each
-// key and value row; the softmax keeps a running maximum and sum in fp32.
+// Bound by the tensor cores for all but short prompts: 4 x 128 operations per visible pair of tokens
+// and query head. One persistent CTA per SM. A work item is 256 consecutive query rows of one sequence
+// and query head, as two tiles of 128 rows that share every key and value block (128 tokens) of the
+// item; both score tiles, both output tiles and (over the scores) the weights live in tensor memory:
+//
+//   S_t = Q_t K_j'           tcgen05.mma, Q and K in shared memory (K-major)
+//   P_t = 2^(c S_t - base)   one thread per row, no exchange between threads; c = sm_scale log2(e)
+//   O_t += P_t V_j           tcgen05.mma, P read from tensor memory, V in shared memory (MN-major)
+//
+// The two tiles alternate: while the warps of one turn scores into weights, the tensor cores run the
+// other's products. The base of a row moves only when a score passes it by more than 8 (in powers of
+// two), so P stays below 2^8 and O is rescaled a few times at the start of a row, by the softmax warps
+// themselves: S of a block is complete only after the products issued before it, so O is at rest then.
+//
+//   warps 0-3, 4-7  softmax and output of tile 0 and 1 (thread = row = tensor-memory lane)
+//   warp 8          loads: Q tiles once an item, then K and V blocks into a ring (tensor-map copies)
+//   warp 9          the products (one issuing thread)
+//   warp 10         the schedule: the next item, while this one runs
+//   warp 11         looks over the V blocks that hold masked places for some row (see below)
+//
+// Masked places and non-finite values: scores are masked by selection, so a key that a row does not
+// see cannot reach it. A weight of exactly 0 times a NaN or infinite value would; warp 11 therefore
+// replaces non-finite elements of V by 0 in the blocks at an edge of the mask (the diagonal, the
+// window's start, the end of a sequence), and the rows that do see such an element get it added in the
+// output step. Blocks that every row of both tiles sees are left as they are.
+//
+// Work order: items by descending row block, so the longest run first, heads of a row block next to each
+// other (they share K and V in L2); CTAs take them in turns, back and forth (c, 2n-1-c, 2n+c, ...),
+// which evens out the descending lengths without a counter in memory.
 
 #include <algorithm>
+#include <mutex>
 
-#include <cuda_bf16.h>
-
-#include "kvq_device.cuh"
 #include "kvq_internal.h"
+#include "kvq_umma.cuh"
 
 namespace kvq {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kRows = 128;                 // rows of a tile, tokens of a block
+constexpr int kItemRows = 2 * kRows;
+constexpr int kTileBytes = kRows * kD * 2;  // 32 KB: two 64-dim halves of 128 rows of 128 bytes
+constexpr int kRing = 4;                   // K and V blocks in flight (K in even, V in odd slots)
+constexpr int kThreads = 384;
+// registers a thread: 256 softmax threads and 128 others, from 168 at launch
+constexpr int kRegSoftmax = 208, kRegAux = 88;
+static_assert(256 * kRegSoftmax + 128 * kRegAux <= kThreads * 168, "register shares above the launch's allocation");
+constexpr uint32_t kColS = 0, kColO = 256;  // tile t at + 128 t; P over the first 64 columns of S
 
 struct PromptParams {
+  CUtensorMap mq, mk, mv;
   PromptJob j;
   float scale2;  // sm_scale * log2(e)
 };
 
-__device__ __forceinline__ void unpack4(uint2 u, bool f16, float (&x)[4]) {
-  if (f16) {
-    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&u.x));
-    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&u.y));
-    x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
-  } else {
-    x[0] = bf16_bits_to_f32(u.x & 0xFFFFu);
-    x[1] = bf16_bits_to_f32(u.x >> 16);
-    x[2] = bf16_bits_to_f32(u.y & 0xFFFFu);
-    x[3] = bf16_bits_to_f32(u.y >> 16);
+struct Item {
+  int s, n;    // first token and length of the sequence (n < 0: no more items)
+  int r0, hq;  // first row, query head
+};
+
+struct Smem {
+  uint8_t q[2][kTileBytes];
+  uint8_t kv[kRing][kTileBytes];
+  uint64_t q_full, q_empty;
+  uint64_t kv_full[kRing], kv_empty[kRing];
+  uint64_t v_ok[kRing / 2];
+  uint64_t s_full[2], p_ready[2], o_full[2];
+  uint64_t item_full[2], item_empty[2];
+  uint64_t fin;
+  Item item[2];
+  int bad[2];   // count of the last item (by parity) in whose edge blocks a value was replaced
+  int failed;
+  uint32_t taddr;
+  int nblk[KVQ_MAX_SEQS];  // row blocks (256 rows) of each sequence
+};
+
+// The blocks [jb, je) of tile t of an item.
+struct Range {
+  int jb, je;
+  __device__ Range(const Item& it, int t, int window) {
+    const int R = it.r0 + t * kRows;
+    if (R >= it.n) {
+      jb = je = 0;
+    } else {
+      jb = window ? max(0, R - window + 1) / kRows : 0;
+      je = (min(R + kRows, it.n) + kRows - 1) / kRows;
+    }
   }
+};
+
+// Whether some row of the tile (rows R..R+127 of a sequence of n) misses a token of block j.
+__device__ __forceinline__ bool edge_block(int R, int n, int j, int window) {
+  const int c = j * kRows;
+  return c + kRows - 1 > R || (window && c < R + kRows - window);
 }
 
-__device__ __forceinline__ uint2 pack4(const float (&x)[4], bool f16) {
-  uint2 u;
-  if (f16) {
-    u.x = pack_f16x2(x[0], x[1]);
-    u.y = pack_f16x2(x[2], x[3]);
-  } else {
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u.x) : "f"(x[1]), "f"(x[0]));
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u.y) : "f"(x[3]), "f"(x[2]));
-  }
-  return u;
-}
+__device__ __forceinline__ int warp_sum_int(int v) { return __reduce_add_sync(0xffffffffu, v); }
 
-// One row by one warp: keys first..row of the sequence that begins at token `base`.
-__device__ void attend_row(const PromptParams& p, int base, int row, int hq) {
-  const PromptJob& j = p.j;
+// Pair number `pr` (row blocks of all sequences by descending block index m, then sequence) -> sequence
+// and m. The number of pairs with a larger block index than m is sum_b max(0, nblk_b - m - 1). Pairs
+// come in ascending order, so m never exceeds m_top, the last answer. Whole warp.
+__device__ __forceinline__ void find_pair(const int* nblk, int B, int pr, int& m_top, int& b) {
   const int lane = threadIdx.x & 31;
-  const int hkv = hq / (j.Hq / j.Hkv);
-  auto at = [&](const void* t, long long st, long long sh, int tok, int h) {
-    return reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(t) + tok * st + h * sh)[lane];
+  auto above = [&](int m) {
+    int v = 0;
+    for (int i = lane; i < B; i += 32) v += max(0, nblk[i] - m - 1);
+    return warp_sum_int(v);
   };
-  float q[4], o[4] = {0.f, 0.f, 0.f, 0.f}, m = -INFINITY, l = 0.f;
-  unpack4(at(j.q, j.qs_t, j.qs_h, base + row, hq), j.f16, q);
-  const int first = j.window ? max(0, row - j.window + 1) : 0;
-  for (int i = first; i <= row; ++i) {
-    float k[4], v[4];
-    unpack4(at(j.k, j.ks_t, j.ks_h, base + i, hkv), j.f16, k);
-    unpack4(at(j.v, j.vs_t, j.vs_h, base + i, hkv), j.f16, v);
-    float d = q[0] * k[0] + q[1] * k[1] + q[2] * k[2] + q[3] * k[3];
-#pragma unroll
-    for (int s = 16; s >= 1; s >>= 1) d += __shfl_xor_sync(0xffffffffu, d, s);
-    const float z = d * p.scale2;
-    const float mn = fmaxf(m, z);
-    const float a = m == mn ? 1.0f : exp2f(m - mn);
-    const float e = z == -INFINITY ? 0.0f : exp2f(z - mn);  // NaN stays NaN; +inf - +inf too
-    m = mn;
-    l = l * a + e;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) o[c] = o[c] * a + e * v[c];
+  int lo = 0, hi = m_top;
+  while (lo < hi) {  // the smallest m with above(m) <= pr
+    const int mid = (lo + hi) >> 1;
+    if (above(mid) <= pr) hi = mid;
+    else lo = mid + 1;
   }
-  const float inv = 1.0f / l;
-#pragma unroll
-  for (int c = 0; c < 4; ++c) o[c] *= inv;
-  reinterpret_cast<uint2*>(static_cast<uint16_t*>(j.out) + (base + row) * j.os_t + hq * j.os_h)[lane] = pack4(o, j.f16);
+  m_top = lo;
+  int r = pr - above(lo);
+  b = 0;
+  for (int i0 = 0; i0 < B; i0 += 32) {
+    const bool has = i0 + lane < B && nblk[i0 + lane] > lo;
+    const uint32_t v = __ballot_sync(0xffffffffu, has);
+    const int c = __popc(v);
+    if (r < c) {
+      b = i0 + (int)__fns(v, 0, r + 1);
+      break;
+    }
+    r -= c;
+  }
 }
 
-__global__ void __launch_bounds__(128) prompt_rows_kernel(const PromptParams p) {
+template <bool F16>
+__device__ __forceinline__ bool has_nonfinite(uint32_t w) {
+  constexpr uint32_t kExp = F16 ? 0x7C007C00u : 0x7F807F80u, kOne = F16 ? 0x04000400u : 0x00800080u;
+  return (((w & kExp) + kOne) & 0x80008000u) != 0;
+}
+template <bool F16>
+__device__ __forceinline__ uint32_t drop_nonfinite(uint32_t w) {
+  constexpr uint32_t kExp = F16 ? 0x7C00u : 0x7F80u;
+  if ((w & kExp) == kExp) w &= 0xFFFF0000u;
+  if (((w >> 16) & kExp) == kExp) w &= 0x0000FFFFu;
+  return w;
+}
+template <bool F16>
+__device__ __forceinline__ float value16(uint32_t bits) {
+  return F16 ? __half2float(__ushort_as_half((unsigned short)bits)) : __uint_as_float(bits << 16);
+}
+
+// The output step's slow part: adds the non-finite values of the edge blocks that this row sees to the
+// row as written (the sums are infinite or NaN, so nothing is rounded twice).
+template <bool F16>
+__device__ __noinline__ void add_nonfinite(const PromptJob& j, const Item& it, int row) {
+  const Range r0(it, 0, j.window), r1(it, 1, j.window);
+  const int lo = j.window ? max(0, row - j.window + 1) : 0;
+  const int hkv = it.hq / (j.Hq / j.Hkv);
+  uint16_t* o = static_cast<uint16_t*>(j.out) + (it.s + row) * j.os_t + it.hq * j.os_h;
+  for (int jb = r0.jb; jb < max(r0.je, r1.je); ++jb) {
+    bool edge = false;
+    for (int t = 0; t < 2; ++t) {
+      const Range& r = t ? r1 : r0;
+      edge |= jb >= r.jb && jb < r.je && edge_block(it.r0 + t * kRows, it.n, jb, j.window);
+    }
+    if (!edge) continue;
+    for (int tok = max(lo, jb * kRows); tok <= min(row, jb * kRows + kRows - 1); ++tok) {
+      const uint16_t* v = static_cast<const uint16_t*>(j.v) + (it.s + tok) * j.vs_t + hkv * j.vs_h;
+      for (int c = 0; c < kD; ++c) {
+        const float x = value16<F16>(v[c]);
+        if (!isfinite(x)) o[c] = (uint16_t)pack16x2<F16>(value16<F16>(o[c]) + x, 0.0f);
+      }
+    }
+  }
+}
+
+template <bool F16>
+__global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_constant__ PromptParams p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  Smem& sm = *reinterpret_cast<Smem*>(smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u));
+  const PromptJob& j = p.j;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* failed = &sm.failed;
+
+  if (threadIdx.x == 0) {
+    mbar_init(&sm.q_full, 1);
+    mbar_init(&sm.q_empty, 1);
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&sm.kv_full[i], 1);
+      mbar_init(&sm.kv_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.v_ok[i], 1);
+      mbar_init(&sm.s_full[i], 1);
+      mbar_init(&sm.p_ready[i], 4);
+      mbar_init(&sm.o_full[i], 1);
+      mbar_init(&sm.item_full[i], 1);
+      mbar_init(&sm.item_empty[i], 11);  // loads, products, V check and the 8 softmax warps
+      sm.bad[i] = -1;
+    }
+    mbar_init(&sm.fin, 1);
+    sm.failed = 0;
+  }
+  fence_barrier_init();
   griddep_wait();
   griddep_launch_dependents();
-  const PromptJob& j = p.j;
-  const int hq = blockIdx.y;
-  if (blockIdx.x == 0 && hq == 0)
-    for (int b = threadIdx.x; b < j.B; b += blockDim.x)
-      if (j.cu_seqlens[b] < 0 || j.cu_seqlens[b + 1] < j.cu_seqlens[b] || j.cu_seqlens[b + 1] > j.T) set_err(j.dev_err, KVQ_DEVERR_POS);
-  for (int tok = blockIdx.x * 4 + (threadIdx.x >> 5); tok < j.T; tok += gridDim.x * 4) {
-    int lo = 0, hi = j.B;  // the last b with cu_seqlens[b] <= tok
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (j.cu_seqlens[mid] <= tok) lo = mid;
-      else hi = mid;
-    }
-    const int s = j.cu_seqlens[lo], e = j.cu_seqlens[lo + 1];
-    if (s < 0 || e > j.T || tok < s || tok >= e) continue;
-    attend_row(p, s, tok - s, hq);
+  int npairs = 0;
+  for (int b = threadIdx.x; b < j.B; b += kThreads) {
+    const int s = j.cu_seqlens[b], e = j.cu_seqlens[b + 1];
+    const bool ok = s >= 0 && e >= s && e <= j.T;
+    if (!ok && blockIdx.x == 0) set_err(j.dev_err, KVQ_DEVERR_POS);
+    sm.nblk[b] = ok ? (e - s + kItemRows - 1) / kItemRows : 0;
   }
+  if (warp == 9) tmem_alloc_512(&sm.taddr);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.taddr;
+
+  if (warp >= 8) {
+    reg_dealloc<kRegAux>();
+    if (warp == 10) {
+      // ------------------------------------------------------------ schedule
+      int top = 0;
+      for (int b = lane; b < j.B; b += 32) {
+        npairs += sm.nblk[b];
+        top = max(top, sm.nblk[b] - 1);
+      }
+      npairs = warp_sum_int(npairs);
+      top = __reduce_max_sync(0xffffffffu, top);
+      const long long items = (long long)npairs * j.Hq;
+      const int n = gridDim.x, c = blockIdx.x;
+      for (int k = 0;; ++k) {
+        const long long idx = (long long)k * n + (k & 1 ? n - 1 - c : c);
+        Item it{0, -1, 0, 0};
+        if (idx < items) {
+          int b;
+          find_pair(sm.nblk, j.B, (int)(idx / j.Hq), top, b);
+          it.s = j.cu_seqlens[b];
+          it.n = j.cu_seqlens[b + 1] - it.s;
+          it.r0 = top * kItemRows;
+          it.hq = (int)(idx % j.Hq);
+        }
+        bool ok = k < 2 || role_wait(&sm.item_empty[k & 1], (uint32_t)(k / 2 - 1) & 1u, failed);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        if (lane == 0) {
+          sm.item[k & 1] = it;
+          mbar_arrive(&sm.item_full[k & 1]);
+        }
+        if (it.n < 0) break;
+      }
+    } else if (warp == 8 && lane == 0) {
+      // ------------------------------------------------------------ loads
+      int slot = 0, used = 0;  // next ring slot, blocks loaded so far
+      auto load = [&](const CUtensorMap* map, int head, int tok) {
+        if (used >= kRing && !role_wait(&sm.kv_empty[slot], (uint32_t)(used / kRing - 1) & 1u, failed)) return false;
+        mbar_arrive_expect_tx(&sm.kv_full[slot], kTileBytes);
+        tma_load_3d(sm.kv[slot], map, 0, head, tok, &sm.kv_full[slot]);
+        tma_load_3d(sm.kv[slot] + kTileBytes / 2, map, 64, head, tok, &sm.kv_full[slot]);
+        ++used;
+        slot = (slot + 1) % kRing;
+        return true;
+      };
+      bool ok = true;
+      int nq = 0;
+      for (int k = 0; ok; ++k) {
+        if (!(ok = role_wait(&sm.item_full[k & 1], (uint32_t)(k / 2) & 1u, failed))) break;
+        const Item it = sm.item[k & 1];
+        mbar_arrive(&sm.item_empty[k & 1]);
+        if (it.n < 0) break;
+        const Range a(it, 0, j.window), b(it, 1, j.window);
+        if (k > 0 && !(ok = role_wait(&sm.q_empty, (uint32_t)(k - 1) & 1u, failed))) break;
+        const int tiles = b.je > 0 ? 2 : 1;
+        mbar_arrive_expect_tx(&sm.q_full, tiles * kTileBytes);
+        for (int t = 0; t < tiles; ++t)
+          for (int h = 0; h < 2; ++h)
+            tma_load_3d(sm.q[t] + h * (kTileBytes / 2), &p.mq, 64 * h, it.hq, it.s + it.r0 + t * kRows, &sm.q_full);
+        ++nq;
+        const int hkv = it.hq / (j.Hq / j.Hkv);
+        for (int jb = a.jb; ok && jb < max(a.je, b.je); ++jb)
+          ok = load(&p.mk, hkv, it.s + jb * kRows) && load(&p.mv, hkv, it.s + jb * kRows);
+      }
+      if (!ok) {  // no copy may be in flight when the CTA ends
+        if (nq > 0) mbar_wait_bounded(&sm.q_full, (uint32_t)(nq - 1) & 1u);
+        for (int u = max(0, used - kRing); u < used; ++u) mbar_wait_bounded(&sm.kv_full[u % kRing], (uint32_t)(u / kRing) & 1u);
+      }
+    } else if (warp == 9 && lane == 0) {
+      // ------------------------------------------------------------ products
+      constexpr uint32_t kIdQK = umma_idesc_16(F16, kRows, false), kIdPV = umma_idesc_16(F16, kD, true);
+      const uint64_t dq[2] = {umma_sdesc(smem_addr(sm.q[0]), 16, 1024), umma_sdesc(smem_addr(sm.q[1]), 16, 1024)};
+      const uint64_t dk0 = umma_sdesc(smem_addr(sm.kv[0]), 16, 1024);
+      const uint64_t dv0 = umma_sdesc(smem_addr(sm.kv[0]), kTileBytes / 2, 1024);
+      bool ok = true;
+      int kv = 0;                  // ring uses before the item: K of its block i is use kv + 2 i, V the next
+      uint32_t pph[2] = {0, 0};    // phase of p_ready
+      auto qk = [&](int t, int slot) {
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {  // 16 dims each: 32 bytes within a 64-dim half
+          const uint64_t off = (uint64_t)(((kk >> 2) * (kTileBytes / 2) + (kk & 3) * 32) >> 4);
+          umma_f16(tmem + kColS + 128 * t, dq[t] + off, dk0 + (uint64_t)(slot * (kTileBytes >> 4)) + off, kIdQK, kk > 0);
+        }
+        umma_commit(&sm.s_full[t]);
+      };
+      for (int k = 0; ok; ++k) {
+        if (!(ok = role_wait(&sm.item_full[k & 1], (uint32_t)(k / 2) & 1u, failed))) break;
+        const Item it = sm.item[k & 1];
+        mbar_arrive(&sm.item_empty[k & 1]);
+        if (it.n < 0) break;
+        const Range rg[2] = {Range(it, 0, j.window), Range(it, 1, j.window)};
+        const int jb = rg[0].jb, je = max(rg[0].je, rg[1].je);
+        auto active = [&](int t, int b) { return b >= rg[t].jb && b < rg[t].je; };
+        auto full = [&](int use) { return role_wait(&sm.kv_full[use % kRing], (uint32_t)(use / kRing) & 1u, failed); };
+        ok = role_wait(&sm.q_full, (uint32_t)k & 1u, failed) && full(kv);
+        if (!ok) break;
+        tc_fence_after();
+        for (int t = 0; t < 2; ++t)
+          if (active(t, jb)) qk(t, kv % kRing);
+        umma_commit(&sm.kv_empty[kv % kRing]);
+        if (je == jb + 1) umma_commit(&sm.q_empty);
+        for (int b = jb; ok && b < je; ++b) {
+          const int uv = kv + 2 * (b - jb) + 1, uk = uv + 1;
+          ok = full(uv) && role_wait(&sm.v_ok[(uv % kRing) >> 1], (uint32_t)(uv / kRing) & 1u, failed);
+          if (ok && b + 1 < je) ok = full(uk);
+          for (int t = 0; ok && t < 2; ++t) {
+            if (active(t, b)) {
+              ok = role_wait(&sm.p_ready[t], pph[t], failed);
+              if (!ok) break;
+              pph[t] ^= 1u;
+              tc_fence_after();
+              const uint64_t dv = dv0 + (uint64_t)((uv % kRing) * (kTileBytes >> 4));
+              const uint32_t acc = b > rg[t].jb;
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk)  // 16 tokens each: 2048 bytes of a half of V, 8 columns of P
+                umma_f16_ts(tmem + kColO + 128 * t, tmem + kColS + 128 * t + 8 * kk, dv + (uint64_t)(kk * (2048 >> 4)), kIdPV, kk > 0 ? 1u : acc);
+              if (b == rg[t].je - 1) umma_commit(&sm.o_full[t]);
+            }
+            if (active(t, b + 1)) {
+              tc_fence_after();
+              qk(t, uk % kRing);
+            }
+          }
+          if (!ok) break;
+          umma_commit(&sm.kv_empty[uv % kRing]);
+          if (b + 1 < je) umma_commit(&sm.kv_empty[uk % kRing]);
+          if (b + 2 == je) umma_commit(&sm.q_empty);
+        }
+        kv += 2 * (je - jb);
+      }
+      umma_commit(&sm.fin);  // arrives once every product issued has completed
+      mbar_wait_bounded(&sm.fin, 0);
+    } else if (warp == 11) {
+      // ------------------------------------------------------------ V check
+      int kv = 0;
+      bool ok = true;
+      for (int k = 0; ok; ++k) {
+        ok = __all_sync(0xffffffffu, role_wait(&sm.item_full[k & 1], (uint32_t)(k / 2) & 1u, failed));
+        if (!ok) break;
+        const Item it = sm.item[k & 1];
+        __syncwarp();
+        if (it.n < 0) break;
+        const Range a(it, 0, j.window), b(it, 1, j.window);
+        const int jb = a.jb, je = max(a.je, b.je);
+        for (int blk = jb; blk < je; ++blk) {
+          const int use = kv + 2 * (blk - jb) + 1, slot = use % kRing;
+          ok = __all_sync(0xffffffffu, role_wait(&sm.kv_full[slot], (uint32_t)(use / kRing) & 1u, failed));
+          if (!ok) break;
+          const bool edge = (blk >= a.jb && blk < a.je && edge_block(it.r0, it.n, blk, j.window)) ||
+                            (blk >= b.jb && blk < b.je && edge_block(it.r0 + kRows, it.n, blk, j.window));
+          if (edge) {
+            uint4* tile = reinterpret_cast<uint4*>(sm.kv[slot]);
+            bool bad = false;
+#pragma unroll 8
+            for (int i = lane; i < kTileBytes / 16; i += 32) {
+              const uint4 w = tile[i];
+              bad |= has_nonfinite<F16>(w.x) | has_nonfinite<F16>(w.y) | has_nonfinite<F16>(w.z) | has_nonfinite<F16>(w.w);
+            }
+            if (__any_sync(0xffffffffu, bad)) {
+              for (int i = lane; i < kTileBytes / 16; i += 32) {
+                uint4 w = tile[i];
+                w.x = drop_nonfinite<F16>(w.x);
+                w.y = drop_nonfinite<F16>(w.y);
+                w.z = drop_nonfinite<F16>(w.z);
+                w.w = drop_nonfinite<F16>(w.w);
+                tile[i] = w;
+              }
+              if (lane == 0) sm.bad[k & 1] = k;
+              fence_proxy_async_shared();
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.v_ok[slot >> 1]);
+        }
+        kv += 2 * (je - jb);
+        if (lane == 0) mbar_arrive(&sm.item_empty[k & 1]);
+      }
+    }
+  } else {
+    // -------------------------------------------------------------- softmax and output
+    reg_alloc<kRegSoftmax>();
+    const int t = warp >> 2;
+    const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t ts = tmem + lane_base + kColS + 128 * t, to = tmem + lane_base + kColO + 128 * t;
+    const float c = p.scale2;
+    uint32_t sph = 0, oph = 0;
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      ok = __all_sync(0xffffffffu, role_wait(&sm.item_full[k & 1], (uint32_t)(k / 2) & 1u, failed));
+      if (!ok) break;
+      const Item it = sm.item[k & 1];
+      __syncwarp();
+      if (it.n < 0) break;
+      const Range rg(it, t, j.window);
+      const int R = it.r0 + t * kRows, row = R + 32 * (warp & 3) + lane;
+      float base = -INFINITY;  // in powers of two, as the weights take it
+      uint64_t l2[2] = {0ull, 0ull};
+      for (int b = rg.jb; b < rg.je; ++b) {
+        ok = __all_sync(0xffffffffu, role_wait(&sm.s_full[t], sph, failed));
+        if (!ok) break;
+        sph ^= 1u;
+        tc_fence_after();
+        uint32_t s[128];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_ld32u(ts + 32 * i, s + 32 * i);
+        tmem_wait_ld_all();
+        if (edge_block(R, it.n, b, j.window)) {
+          const int hi = row - b * kRows, lo = j.window ? hi - j.window + 1 : 0;
+#pragma unroll
+          for (int i = 0; i < 128; ++i)
+            if (i > hi || i < lo) s[i] = 0xFF800000u;
+        }
+        float mx[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mx[i] = __uint_as_float(s[i]);
+#pragma unroll
+        for (int i = 4; i < 124; i += 8)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) mx[u] = fmax3(mx[u], __uint_as_float(s[i + 2 * u]), __uint_as_float(s[i + 2 * u + 1]));
+#pragma unroll
+        for (int u = 0; u < 4; ++u) mx[u] = fmaxf(mx[u], __uint_as_float(s[124 + u]));
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+        const bool move = top > base + 8.0f || (base == -INFINITY && top > -INFINITY);
+        if (__any_sync(0xffffffffu, move)) {
+          const float alpha = move ? fast_exp2(base - top) : 1.0f;
+          if (move) base = top;
+          l2[0] = mul_f2(l2[0], f2(alpha, alpha));
+          l2[1] = mul_f2(l2[1], f2(alpha, alpha));
+          if (b > rg.jb) {  // O of the first block starts anew
+#pragma unroll 1
+            for (int i = 0; i < 4; ++i) {
+              uint32_t o[32];
+              tmem_ld32u(to + 32 * i, o);
+              tmem_wait_ld_all();
+#pragma unroll
+              for (int u = 0; u < 32; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * alpha);
+              tmem_st32u(to + 32 * i, o);
+            }
+          }
+        }
+        const float neg = base == -INFINITY ? 0.0f : -base;
+        const uint64_t c2 = f2(c, c), n2 = f2(neg, neg);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const uint64_t x = fma_f2(f2(__uint_as_float(s[64 * h + 2 * i]), __uint_as_float(s[64 * h + 2 * i + 1])), c2, n2);
+            const float e0 = fast_exp2(f2lo(x)), e1 = fast_exp2(f2hi(x));
+            l2[i & 1] = add_f2(l2[i & 1], f2(e0, e1));
+            pk[i] = pack16x2<F16>(e0, e1);
+          }
+          tmem_st32u(ts + 32 * h, pk);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.p_ready[t]);
+      }
+      if (!ok) break;
+      if (rg.je > 0) {
+        ok = __all_sync(0xffffffffu, role_wait(&sm.o_full[t], oph, failed));
+        if (!ok) break;
+        oph ^= 1u;
+        tc_fence_after();
+        uint32_t o[128];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_ld32u(to + 32 * i, o + 32 * i);
+        tmem_wait_ld_all();
+        const float l = (f2lo(l2[0]) + f2hi(l2[0])) + (f2lo(l2[1]) + f2hi(l2[1]));
+        const float inv = 1.0f / l;
+        if (row < it.n) {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(j.out) + (it.s + row) * j.os_t + it.hq * j.os_h);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            uint32_t w[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              w[u] = pack16x2<F16>(__uint_as_float(o[8 * i + 2 * u]) * inv, __uint_as_float(o[8 * i + 2 * u + 1]) * inv);
+            dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          if (__builtin_expect(sm.bad[k & 1] == k, 0)) add_nonfinite<F16>(j, it, row);
+        }
+        tc_fence_before();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.item_empty[k & 1]);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 9) tmem_dealloc_512(tmem);
+  if (threadIdx.x == 0 && *failed) set_err(j.dev_err, KVQ_DEVERR_TIMEOUT);
+}
+
+std::mutex g_mu;  // guards the caches below
+bool g_attr[64][2] = {{false}};
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiled g_encode = nullptr;
+
+cudaError_t encoder(EncodeTiled& f) {
+  std::lock_guard<std::mutex> lock(g_mu);
+  if (!g_encode) {
+    void* sym = nullptr;
+    cudaDriverEntryPointQueryResult got;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &sym, 12000, cudaEnableDefault, &got);
+    if (e != cudaSuccess) return e;
+    if (got != cudaDriverEntryPointSuccess || !sym) return cudaErrorNotSupported;
+    g_encode = reinterpret_cast<EncodeTiled>(sym);
+  }
+  f = g_encode;
+  return cudaSuccess;
+}
+
+// Map of a [T][heads][128] tensor: boxes of 64 dims x 1 head x 128 tokens, 128-byte swizzle, zeros
+// outside (tokens from T on).
+bool encode(EncodeTiled f, CUtensorMap* m, bool f16, const void* base, int T, int heads, long long st, long long sh) {
+  const cuuint64_t dims[3] = {kD, (cuuint64_t)heads, (cuuint64_t)T};
+  const cuuint64_t strides[2] = {(cuuint64_t)sh * 2, (cuuint64_t)st * 2};
+  const cuuint32_t box[3] = {64, 1, kRows}, one[3] = {1, 1, 1};
+  return f(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
+           strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
@@ -106,17 +550,41 @@ __global__ void __launch_bounds__(128) prompt_rows_kernel(const PromptParams p) 
 size_t workspace_prompt_bytes(int T, int B, int Hq, int Hkv) { return 256; }
 
 cudaError_t launch_prompt(const PromptJob& job, cudaStream_t stream) {
-  PromptParams p{job, job.sm_scale * kLog2e};
+  EncodeTiled f;
+  cudaError_t e = encoder(f);
+  if (e != cudaSuccess) return e;
+  PromptParams p;
+  p.j = job;
+  p.scale2 = job.sm_scale * kLog2e;
+  if (!encode(f, &p.mq, job.f16, job.q, job.T, job.Hq, job.qs_t, job.qs_h) ||
+      !encode(f, &p.mk, job.f16, job.k, job.T, job.Hkv, job.ks_t, job.ks_h) ||
+      !encode(f, &p.mv, job.f16, job.v, job.T, job.Hkv, job.vs_t, job.vs_h))
+    return cudaErrorInvalidValue;
+  const auto kern = job.f16 ? prompt_kernel<true> : prompt_kernel<false>;
+  const size_t smem = sizeof(Smem) + 1024;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  {
+    std::lock_guard<std::mutex> lock(g_mu);
+    if (dev < 0 || dev >= 64 || !g_attr[dev][job.f16]) {
+      e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      if (e != cudaSuccess) return e;
+      if (dev >= 0 && dev < 64) g_attr[dev][job.f16] = true;
+    }
+  }
+  // no more CTAs than items: T tokens in B sequences make at most T / 256 + B row blocks
+  const long long most = ((long long)job.T / kItemRows + job.B) * job.Hq;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)std::min((job.T + 3) / 4, 1 << 20), (unsigned)job.Hq, 1);
-  cfg.blockDim = dim3(128, 1, 1);
+  cfg.gridDim = dim3((unsigned)std::min<long long>(most, device_sms()), 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, prompt_rows_kernel, p);
+  return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 }  // namespace kvq
