@@ -56,6 +56,7 @@ kvq_status tree_int4_impl(const kvq_int4_cache* cache, const float* Mq, const fl
   st = check_tree(B, N, num_q_heads, cache->num_kv_heads, cache->num_seqs, dtype, q, ctx_len, tree_mask, k_new, v_new,
                   sm_scale, out, out_dtype, workspace, workspace_bytes, dev_err);
   if (st != KVQ_OK) return st;
+  if ((long long)B * (cache->max_pages_per_seq + 2) > (1LL << 31)) return KVQ_ERR_UNSUPPORTED;
   if (!Mq || !aligned(Mq, 16) || (k_new && (!Mk || !aligned(Mk, 16)))) return KVQ_ERR_INVALID_ARG;
   if (!(eps >= 0.0f) || std::isinf(eps)) return KVQ_ERR_INVALID_ARG;
   uint8_t* ws = static_cast<uint8_t*>(workspace);

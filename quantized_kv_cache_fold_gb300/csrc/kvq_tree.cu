@@ -1,123 +1,904 @@
 // Attention of a tree of drafted tokens over the int4 cache or the e4m3 ring (kvq_tree_attn_*).
 //
-// Row i of sequence b attends to the context (the ring: to its window's part of it) and to the
-// drafted tokens of its mask. One warp per (token, query head): every lane holds four dims.
+// Row i of sequence b attends to the context (the ring: to its window's part of it) and to the drafted
+// tokens of its mask. The N x G query rows of a KV head share every key and value, so the cache is read
+// and converted once for up to 256 rows, and both products run on the tensor cores:
+//
+//   K, V  4-bit codes -> c s + o in fp16 (one rounding), e4m3 -> fp16 (exact), 128 tokens a block,
+//         converted by four warps into shared memory (K: K-major, V: MN-major, 128-byte swizzle)
+//   S = Q' K^T     tcgen05.mma, 128 rows x 128 tokens, accumulators in tensor memory
+//   P = 2^(c S - base) in fp16 over S, one thread per row (as in kvq_prompt.cu: the base moves only
+//         when a score passes it by more than 8, so P < 2^8)
+//   O += P V       tcgen05.mma, P read from tensor memory
+//
+// The rounding of q~, K, V and P to fp16 is what keeps both products on the tensor cores: 2^-11 each,
+// against the 2^-8 of a bf16 result; sums, bases and O stay in fp32.
+//
+// Two streams of (S, P, O) take turns, so that the tensor cores work on one while the softmax warps have
+// the other: with more than 128 rows they are two row tiles over the same blocks, else two halves of the
+// blocks (even, odd) over the same rows, joined at the end of a segment in tensor memory.
+//
+// Work split: a segment is (sequence, KV head, group of 256 rows); the segments' blocks are laid end to
+// end and each CTA (one per SM) takes a contiguous part of equal weight (a block counts its row tiles). A
+// segment that one CTA has whole is finished there; of the others each CTA leaves an unnormalised partial,
+// two at most (its first and its last piece), and tree_combine_kernel joins them.
+//
+//   warps 0-3, 4-7  softmax of stream 0 and 1, Q' tiles, output (thread = row = tensor-memory lane)
+//   warps 8-11      conversion (thread = token of the block)
+//   warp 12         copies of pages / ring blocks into shared-memory stages
+//   warp 13         the products (one issuing thread)
 
 #include <algorithm>
+#include <mutex>
 
-#include "kvq_device.cuh"
 #include "kvq_internal.h"
+#include "kvq_umma.cuh"
 
 namespace kvq {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kBlk = 128;                  // tokens of a block: two pages
+constexpr int kGroup = 256;                // rows of a segment
+constexpr int kTileBytes = kBlk * kD * 2;  // fp16 tile: two 64-dim halves of 128 rows of 128 bytes
+constexpr int kHalf = kTileBytes / 2;
+constexpr int kThreads = 512;
+constexpr int kRegSoftmax = 168, kRegConv = 88, kRegAux = 88;
+static_assert(256 * kRegSoftmax + 128 * kRegConv + 128 * kRegAux <= kThreads * 128, "register shares above the launch's allocation");
+constexpr uint32_t kColS = 0, kColO = 256;  // stream t at + 128 t; P over the first 64 columns of S
+constexpr int kMaxTreeCtas = 256;           // sizes the partials
+constexpr int kMaxStages = 8;
+constexpr size_t kSmemMax = 227 * 1024;
 
 struct TreeParams {
   TreeJob j;
-  float scale2;  // sm_scale * log2(e) (* k_scale)
+  float c;      // |sm_scale| log2(e) (times k_scale), 1 where that is 0
+  float qmul;   // sign of the scale (0 where it is 0), applied to q
+  float vmul;   // applied to the output
+  int G, R;     // query heads per KV head, rows of a KV head
+  int ng;       // row groups
+  int w_last;   // row tiles of the last group (all others: 2)
+  int nst;      // copy stages
+  float2* ml;   // partials: base and sum of each row, [2 CTAs][rows]
+  float* acc;   // and its 128 sums
+  int prow;     // rows of a partial slot: 128 or 256
 };
 
-__global__ void __launch_bounds__(128) tree_rows_kernel(const TreeParams p) {
-  griddep_wait();
-  griddep_launch_dependents();
-  const TreeJob& j = p.j;
+__host__ __device__ constexpr int stage_bytes(int fmt) { return fmt == 0 ? KVQ_INT4_BLOCK_BYTES : 2 * kPage * kRec8; }
+
+struct Layout {  // offsets from the 1024-byte aligned start of dynamic shared memory
+  uint32_t q, k, v, raw, bars, valid, bvalid, state, pre, total;
+  __host__ __device__ Layout(int fmt, int qtiles, int nst, int B) {
+    q = 0;
+    k = q + qtiles * kTileBytes;
+    v = k + 2 * kTileBytes;
+    raw = v + 2 * kTileBytes;
+    bars = raw + nst * stage_bytes(fmt);  // a multiple of 16
+    valid = bars + 8 * 40;
+    bvalid = valid + 4 * kMaxStages;
+    state = bvalid + 4 * 8;  // failed flag, tensor-memory address
+    pre = state + 8;
+    total = pre + 4 * (B + 1);
+  }
+};
+
+// Context length of sequence b: clamped into what the cache can hold (`bad` reports that).
+__device__ __forceinline__ int tree_ctx(const TreeJob& j, int b, bool& bad) {
+  int c = __ldg(j.ctx + b);
+  const int most = j.fmt == 0 ? j.cache.max_pages_per_seq * kPage - j.N : 1 << 30;
+  if (c < 0 || c > most) {
+    bad = true;
+    c = max(0, min(c, most));
+  }
+  return c;
+}
+// First position that some row may see, and the page it lies in.
+__device__ __forceinline__ int first_pos(const TreeJob& j, int ctx) { return j.fmt == 0 ? 0 : max(0, ctx - j.window + 1); }
+__device__ __forceinline__ int num_blocks(const TreeJob& j, int ctx) {
+  const int p0 = first_pos(j, ctx) / kPage, p1 = (ctx + j.N + kPage - 1) / kPage;
+  return (p1 - p0 + 1) / 2;
+}
+
+// pre[b] = blocks of the sequences before b, by one warp (all of its lanes).
+__device__ __forceinline__ void build_pre(const TreeJob& j, int* pre, bool report) {
   const int lane = threadIdx.x & 31;
-  const int item = blockIdx.x * 4 + (threadIdx.x >> 5);  // (b, i, hq)
-  if (item >= j.B * j.N * j.Hq) return;
-  const int hq = item % j.Hq, i = item / j.Hq % j.N, b = item / j.Hq / j.N;
-  const int hkv = hq / (j.Hq / j.Hkv);
-  const uint64_t all = j.N == 64 ? ~0ull : (1ull << j.N) - 1;
-  const uint64_t mask = j.mask[(size_t)b * j.N + i] & all;
-  const int cap = j.fmt == 0 ? j.cache.max_pages_per_seq * kPage : j.ring.capacity;
-  int ctx = j.ctx[b];
-  const int most = j.fmt == 0 ? cap - j.N : 1 << 30;
-  if (ctx < 0 || ctx > most) {
-    if (lane == 0) set_err(j.dev_err, KVQ_DEVERR_POS);
-    ctx = min(max(ctx, 0), max(most, 0));
-  }
-  float q[4], o[4] = {0.f, 0.f, 0.f, 0.f}, m = -INFINITY, l = 0.f;
-  if (j.fmt == 0) load_row4(j.q_rot, 0, (size_t)item, lane, q);
-  else load_row4(j.q, j.q_bf16, (size_t)item, lane, q);
-  const int first = j.fmt == 0 ? 0 : max(0, ctx + max(1, __popcll(mask)) - j.window);
-  for (int pos = first; pos < ctx + j.N && pos < (j.fmt == 0 ? cap : ctx + j.N); ++pos) {
-    if (pos >= ctx && !((mask >> (pos - ctx)) & 1)) continue;
-    float k[4], v[4];
-    if (j.fmt == 0) {
-      const int page = j.cache.block_table[(size_t)b * j.cache.max_pages_per_seq + pos / kPage];
-      if (page < 0 || page >= j.cache.num_pages) {
-        if (lane == 0) set_err(j.dev_err, KVQ_DEVERR_PAGE);
-        continue;
-      }
-      const int slot = pos % kPage;
-      const uint8_t* blk = j.cache.pages + ((size_t)page * j.Hkv + hkv) * KVQ_INT4_BLOCK_BYTES;
-      const uint32_t* meta = reinterpret_cast<const uint32_t*>(blk + 2 * kPage * kRec4);
-      const uint32_t kb = *reinterpret_cast<const uint16_t*>(blk + slot * kRec4 + 16 * ((lane >> 3) ^ k_chunk_swz(slot)) + ((2 * lane) & 15));
-      const uint32_t vb = *reinterpret_cast<const uint16_t*>(blk + kPage * kRec4 + slot * kRec4 + 16 * ((lane >> 3) ^ ((slot >> 1) & 3)) + ((2 * lane) & 15));
-      const uint32_t km = meta[slot], vm = meta[kPage + slot];
-      const float ks = __half2float(__ushort_as_half((unsigned short)km)), ko = __half2float(__ushort_as_half((unsigned short)(km >> 16)));
-      const float vs = __half2float(__ushort_as_half((unsigned short)vm)), vo = __half2float(__ushort_as_half((unsigned short)(vm >> 16)));
-      const int eb[4] = {1, 4, 11, 8}, sb[4] = {15, 14, 7, 0};
+  int sum = 0;
+  bool bad = false;
+  for (int b0 = 0; b0 < j.B; b0 += 32) {
+    const int b = b0 + lane;
+    int v = b < j.B ? num_blocks(j, tree_ctx(j, b, bad)) : 0;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        k[c] = fmaf((float)((kb >> (4 * c)) & 15), ks, ko);
-        const int e = (vb >> eb[c]) & 7;
-        v[c] = fmaf((float)((vb >> sb[c]) & 1 ? 7 - e : 8 + e), vs, vo);
-      }
-    } else {
-      const int slot = pos % cap;
-      const uint8_t* blk = j.ring.data + (((size_t)b * j.Hkv + hkv) * (cap / kPage) + slot / kPage) * (2 * kPage * kRec8);
-      const uint32_t kb = *reinterpret_cast<const uint32_t*>(blk + fp8_lane_offset(slot, lane));
-      const uint32_t vb = *reinterpret_cast<const uint32_t*>(blk + kPage * kRec8 + fp8_lane_offset(slot, lane));
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const uint32_t k2 = e4m3x2_to_f16x2(kb >> (16 * c)), v2 = e4m3x2_to_f16x2(vb >> (16 * c));
-        const float2 kf = __half22float2(*reinterpret_cast<const __half2*>(&k2)), vf = __half22float2(*reinterpret_cast<const __half2*>(&v2));
-        k[2 * c] = kf.x, k[2 * c + 1] = kf.y;
-        v[2 * c] = vf.x * j.v_scale, v[2 * c + 1] = vf.y * j.v_scale;
-      }
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += u;
     }
-    float d = q[0] * k[0] + q[1] * k[1] + q[2] * k[2] + q[3] * k[3];
-#pragma unroll
-    for (int s = 16; s >= 1; s >>= 1) d += __shfl_xor_sync(0xffffffffu, d, s);
-    const float z = d * p.scale2;
-    const float mn = fmaxf(m, z);
-    const float a = m == mn ? 1.0f : exp2f(m - mn);
-    const float e = z == -INFINITY ? 0.0f : exp2f(z - mn);
-    m = mn;
-    l = l * a + e;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) o[c] = o[c] * a + e * v[c];
+    if (b < j.B) pre[b + 1] = sum + v;
+    sum += __shfl_sync(0xffffffffu, v, 31);
   }
-  const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;  // a row that attends to nothing: 0
+  if (lane == 0) pre[0] = 0;
+  if (__any_sync(0xffffffffu, bad) && report && lane == 0) set_err(j.dev_err, KVQ_DEVERR_POS);
+}
+
+// The split of the weight line: W in all, n CTAs in use, CTA c from X(c) on. A block belongs to the CTA in
+// whose part its start lies; n is at most W over the largest weight, so every CTA of a segment's span has
+// some of its blocks.
+struct Split {
+  long long W;
+  int n, per_seq;  // weight of one block in all heads and groups of a sequence
+  __device__ Split(const TreeParams& p, const int* pre, int ctas) {
+    const int wg = 2 * (p.ng - 1) + p.w_last;
+    per_seq = p.j.Hkv * wg;
+    W = (long long)per_seq * pre[p.j.B];
+    const int wmax = p.ng > 1 ? 2 : p.w_last;
+    n = (int)min((long long)ctas, W / wmax);
+  }
+  __device__ long long X(int c) const { return (long long)c * W / n; }
+  __device__ int owner(long long x) const { return (int)(((x + 1) * n - 1) / W); }
+};
+
+struct Piece {
+  int b, h, g, w;   // segment and its row tiles
+  int j0, j1, nb;   // blocks [j0, j1) of nb
+  long long xs;     // the segment's place on the weight line
+};
+
+// The pieces of a CTA in order; every role walks them by itself.
+struct Pieces {
+  const TreeParams& p;
+  const int* pre;
+  const Split& s;
+  long long x, x1;
+  __device__ Pieces(const TreeParams& p_, const int* pre_, const Split& s_, int c) : p(p_), pre(pre_), s(s_) {
+    x = c < s.n ? s.X(c) : 0;
+    x1 = c < s.n ? s.X(c + 1) : 0;
+  }
+  __device__ bool next(Piece& o) {
+    while (x < x1) {
+      int lo = 0, hi = p.j.B;  // the last b with pre[b] * per_seq <= x
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if ((long long)pre[mid] * s.per_seq <= x) lo = mid;
+        else hi = mid;
+      }
+      o.b = lo;
+      o.nb = pre[lo + 1] - pre[lo];
+      long long rem = x - (long long)pre[lo] * s.per_seq;
+      const long long per_head = (long long)o.nb * (s.per_seq / p.j.Hkv);
+      o.h = (int)(rem / per_head);
+      rem -= o.h * per_head;
+      o.g = (int)min(rem / (2 * o.nb), (long long)(p.ng - 1));
+      const long long off = rem - (long long)o.g * 2 * o.nb;
+      o.w = o.g < p.ng - 1 ? 2 : p.w_last;
+      o.xs = x - off;
+      const long long xe = o.xs + (long long)o.nb * o.w;
+      o.j0 = (int)((off + o.w - 1) / o.w);
+      o.j1 = xe <= x1 ? o.nb : (int)((x1 - o.xs + o.w - 1) / o.w);
+      x = xe;
+      if (o.j0 < o.j1) return true;
+    }
+    return false;
+  }
+};
+
+// Rows of the group, and of its first tile (two tiles: about half each, whole warps).
+__device__ __forceinline__ int group_rows(const TreeParams& p, int g) { return min(kGroup, p.R - g * kGroup); }
+__device__ __forceinline__ int tile0_rows(int rows, int w) { return w == 1 ? rows : min(kBlk, ((rows + 1) / 2 + 31) & ~31); }
+
+__device__ __forceinline__ float half_lo(uint32_t x) { return __half2float(__ushort_as_half((unsigned short)x)); }
+__device__ __forceinline__ float half_hi(uint32_t x) { return __half2float(__ushort_as_half((unsigned short)(x >> 16))); }
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t both(float x) { return pack_f16x2(x, x); }
+
+// Place of 8-dim word w (0..15) of row r in an fp16 tile.
+__device__ __forceinline__ uint32_t tile_offset(int r, int w) { return (w >> 3) * kHalf + r * 128 + 16 * ((w & 7) ^ (r & 7)); }
+
+// One token's K record -> its row of the K tile. Word w holds dims 8w..8w+7 in the order 0, 4, 1, 5, 2, 6, 3,
+// 7 (as the nibbles pair up in 32 bits; Q' takes the same). A code is the subnormal c 2^-24 (even nibbles)
+// or c 2^-20 (odd ones): one exact product by 2^15, then c s + o rounded once.
+__device__ __forceinline__ void convert_k4(const uint8_t* rec, int slot, float s, float o, uint8_t* tile, int row) {
+  const int sw = k_chunk_swz(slot);
+  const uint32_t up = 0x78007800u;  // 2^15
+  const uint32_t s0 = both(s * 512.0f), s1 = both(s * 32.0f), oo = both(o);
 #pragma unroll
-  for (int c = 0; c < 4; ++c) o[c] *= inv;
-  if (j.out_bf16) {
-    uint2 u;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u.x) : "f"(o[1]), "f"(o[0]));
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u.y) : "f"(o[3]), "f"(o[2]));
-    reinterpret_cast<uint2*>(static_cast<uint16_t*>(j.out) + (size_t)item * kD)[lane] = u;
-  } else {
-    reinterpret_cast<float4*>(static_cast<float*>(j.out) + (size_t)item * kD)[lane] = make_float4(o[0], o[1], o[2], o[3]);
+  for (int c = 0; c < 4; ++c) {
+    const uint4 r = *reinterpret_cast<const uint4*>(rec + 16 * (c ^ sw));
+    const uint32_t wd[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t h[4];
+      unpack8_sub(wd[i], h);
+      uint4 out;
+      out.x = hfma2(hmul2(h[0], up), s0, oo);
+      out.y = hfma2(hmul2(h[1], up), s1, oo);
+      out.z = hfma2(hmul2(h[2], up), s0, oo);
+      out.w = hfma2(hmul2(h[3], up), s1, oo);
+      *reinterpret_cast<uint4*>(tile + tile_offset(row, 4 * c + i)) = out;
+    }
   }
 }
 
-}  // namespace
+// One token's V record -> its row of the V tile, dims in the same order. A code is the subnormal
+// (c - 7.5) 2^(k - 23), k = 0, 4, 2, 6: times 2^15 plus 7.5 2^(k - 8) gives c 2^(k - 8) exactly, times
+// s 2^(8 - k) plus o the value, rounded once. Scales from 255 on (s 2^8 would pass fp16's range) take fp32
+// and saturate.
+__device__ __forceinline__ void convert_v4(const uint8_t* rec, int slot, float s, float o, uint8_t* tile, int row) {
+  const int sw = (slot >> 1) & 3;
+  const uint32_t up = 0x78007800u;
+  const bool wide = s >= 255.0f || fabsf(o) > 60000.0f;
+  const uint32_t s0 = both(s * 256.0f), s1 = both(s * 16.0f), s2 = both(s * 64.0f), s3 = both(s * 4.0f), oo = both(o);
+  const uint32_t m0 = both(7.5f / 256.0f), m1 = both(7.5f / 16.0f), m2 = both(7.5f / 64.0f), m3 = both(7.5f / 4.0f);
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const uint4 r = *reinterpret_cast<const uint4*>(rec + 16 * (c ^ sw));
+    const uint32_t wd[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t h[4];
+      unpack8_v(wd[i], h);
+      uint32_t v[4];
+      h[0] = hfma2(h[0], up, m0);
+      h[1] = hfma2(h[1], up, m1);
+      h[2] = hfma2(h[2], up, m2);
+      h[3] = hfma2(h[3], up, m3);
+      if (__builtin_expect(!wide, 1)) {
+        v[0] = hfma2(h[0], s0, oo);
+        v[1] = hfma2(h[1], s1, oo);
+        v[2] = hfma2(h[2], s2, oo);
+        v[3] = hfma2(h[3], s3, oo);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float f = s * (e == 0 ? 256.0f : e == 1 ? 16.0f : e == 2 ? 64.0f : 4.0f);
+          v[e] = pack_f16x2_sat(fmaf(half_lo(h[e]), f, o), fmaf(half_hi(h[e]), f, o));
+        }
+      }
+      *reinterpret_cast<uint4*>(tile + tile_offset(row, 4 * c + i)) = make_uint4(v[0], v[1], v[2], v[3]);
+    }
+  }
+}
 
-size_t workspace_tree_partials_bytes(int B, int N, int Hq, int Hkv) { return 256; }
+// One token's 128 e4m3 values -> its row of a tile, dims in order.
+__device__ __forceinline__ void convert8(const uint8_t* rec, int slot, uint8_t* tile, int row) {
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    const uint4 r = *reinterpret_cast<const uint4*>(rec + 16 * (c ^ (slot & 7)));
+    const uint32_t wd[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint4 out;
+      out.x = e4m3x2_to_f16x2(wd[2 * i]);
+      out.y = e4m3x2_to_f16x2(wd[2 * i] >> 16);
+      out.z = e4m3x2_to_f16x2(wd[2 * i + 1]);
+      out.w = e4m3x2_to_f16x2(wd[2 * i + 1] >> 16);
+      *reinterpret_cast<uint4*>(tile + tile_offset(row, 2 * c + i)) = out;
+    }
+  }
+}
 
-cudaError_t launch_tree(const TreeJob& job, cudaStream_t stream) {
-  TreeParams p{job, job.sm_scale * kLog2e * (job.fmt == 1 ? job.k_scale : 1.0f)};
+__device__ __forceinline__ void zero_row(uint8_t* tile, int row) {
+#pragma unroll
+  for (int w = 0; w < 16; ++w) *reinterpret_cast<uint4*>(tile + tile_offset(row, w)) = make_uint4(0u, 0u, 0u, 0u);
+}
+
+// Column of dim d (0..7 of a word) in the tiles, and its inverse order for the output.
+template <int FMT>
+__device__ __forceinline__ constexpr int col_of(int d) {
+  return FMT == 0 ? 2 * (d & 3) + (d >> 2) : d;
+}
+
+// Stores 8 dims of a row (columns col .. col + 7 of the tile in v) times f.
+template <int FMT>
+__device__ __forceinline__ void store8(void* out, bool bf16, size_t at, const float* v, float f) {
+  float x[8];
+#pragma unroll
+  for (int d = 0; d < 8; ++d) x[d] = v[col_of<FMT>(d)] * f;
+  if (bf16) {
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at) =
+        make_uint4(pack16x2<false>(x[0], x[1]), pack16x2<false>(x[2], x[3]), pack16x2<false>(x[4], x[5]), pack16x2<false>(x[6], x[7]));
+  } else {
+    float4* d = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
+    d[0] = make_float4(x[0], x[1], x[2], x[3]);
+    d[1] = make_float4(x[4], x[5], x[6], x[7]);
+  }
+}
+
+// Output row (of [B][N][Hq]) of row r of KV head h.
+__device__ __forceinline__ size_t out_row(const TreeParams& p, int b, int h, int r) {
+  return ((size_t)b * p.j.N + r / p.G) * p.j.Hq + h * p.G + r % p.G;
+}
+
+template <int FMT>
+__global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant__ TreeParams p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+  const TreeJob& j = p.j;
+  const Layout L(FMT, p.prow / 128, p.nst, j.B);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L.bars);
+  uint64_t* raw_full = bars;             // [8] a page copied
+  uint64_t* raw_empty = bars + 8;        // [8] and read (the two warps of its tokens)
+  uint64_t* k_ready = bars + 16;         // [2] K tile written
+  uint64_t* v_ready = bars + 18;         // [2]
+  uint64_t* k_free = bars + 20;          // [2] products over it complete
+  uint64_t* v_free = bars + 22;          // [2]
+  uint64_t* s_full = bars + 24;          // [2] scores of a stream complete
+  uint64_t* p_ready = bars + 26;         // [2] weights written
+  uint64_t* o_full = bars + 28;          // [2] a piece's last product of a stream complete
+  uint64_t* q_ready = bars + 30;         // Q' of a piece written
+  uint64_t* fin = bars + 31;
+  volatile int* valid = reinterpret_cast<volatile int*>(smem + L.valid);    // [stage] the page was copied
+  volatile int* bvalid = reinterpret_cast<volatile int*>(smem + L.bvalid);  // [block % 4][page] it exists in the pool
+  // [2][128] base and sum, joining streams: over Q', which no product reads any more by then (all score
+  // products of a piece are issued before its last two weighted sums, and a stream that had none leaves
+  // the region alone until the barrier)
+  float2* mlx = reinterpret_cast<float2*>(smem + L.q);
+  volatile int* failed = reinterpret_cast<volatile int*>(smem + L.state);
+  uint32_t* taddr = reinterpret_cast<uint32_t*>(smem + L.state + 4);
+  int* pre = reinterpret_cast<int*>(smem + L.pre);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kMaxStages; ++i) {
+      mbar_init(raw_full + i, 1);
+      mbar_init(raw_empty + i, 2);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(k_ready + i, 4);
+      mbar_init(v_ready + i, 4);
+      mbar_init(k_free + i, 1);
+      mbar_init(v_free + i, 1);
+      mbar_init(s_full + i, 1);
+      mbar_init(p_ready + i, 4);
+      mbar_init(o_full + i, 1);
+    }
+    mbar_init(q_ready, 8);
+    mbar_init(fin, 1);
+    *failed = 0;
+  }
+  fence_barrier_init();
+  griddep_wait();
+  griddep_launch_dependents();
+  if (warp == 0) build_pre(j, pre, blockIdx.x == 0);
+  if (warp == 13) tmem_alloc_512(taddr);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *taddr;
+  const Split sp(p, pre, gridDim.x);
+  Pieces it(p, pre, sp, blockIdx.x);
+  Piece pc;
+
+  if (warp >= 12) {
+    reg_dealloc<kRegAux>();
+    if (warp == 12) {
+      // ------------------------------------------------------------ copies
+      const uint64_t pol = policy_evict_first();
+      int issued = 0;  // pages so far
+      bool ok = true;
+      while (ok && it.next(pc)) {
+        bool bad = false;
+        const int ctx = tree_ctx(j, pc.b, bad);
+        const int p0 = first_pos(j, ctx) / kPage, p1 = (ctx + j.N + kPage - 1) / kPage;
+        const int pg1 = min(p0 + 2 * pc.j1, p1);
+        for (int base = p0 + 2 * pc.j0; ok && base < pg1; base += 32) {
+          const uint8_t* src = nullptr;  // null: a page outside the pool
+          const int pg = base + lane;
+          if (pg < pg1) {
+            if (FMT == 0) {
+              const int phys = j.cache.block_table[(size_t)pc.b * j.cache.max_pages_per_seq + pg];
+              if (phys >= 0 && phys < j.cache.num_pages) src = j.cache.pages + ((size_t)phys * j.Hkv + pc.h) * KVQ_INT4_BLOCK_BYTES;
+              else set_err(j.dev_err, KVQ_DEVERR_PAGE);
+            } else {
+              const int nblk = j.ring.capacity / kPage;
+              src = j.ring.data + (((size_t)pc.b * j.Hkv + pc.h) * nblk + pg % nblk) * (size_t)stage_bytes(1);
+            }
+          }
+          const int n = min(32, pg1 - base);
+          for (int i = 0; i < n; ++i) {
+            const uint8_t* s = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), i));
+            if (lane == 0 && ok) {
+              const int st = issued % p.nst, round = issued / p.nst;
+              ok = round == 0 || role_wait(raw_empty + st, (uint32_t)(round - 1) & 1u, failed);
+              if (ok) {
+                valid[st] = s != nullptr;
+                if (s) {
+                  mbar_arrive_expect_tx(raw_full + st, stage_bytes(FMT));
+                  bulk_g2s(smem + L.raw + st * stage_bytes(FMT), s, stage_bytes(FMT), raw_full + st, pol);
+                } else {
+                  mbar_arrive(raw_full + st);
+                }
+                ++issued;
+              }
+            }
+          }
+          ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+        }
+      }
+      if (!ok && lane == 0)  // no copy may be in flight when the CTA ends
+        for (int u = max(0, issued - p.nst); u < issued; ++u) mbar_wait_bounded(raw_full + u % p.nst, (uint32_t)(u / p.nst) & 1u);
+    } else if (warp == 13 && lane == 0) {
+      // ------------------------------------------------------------ products
+      constexpr uint32_t kIdQK = umma_idesc_16(true, kBlk, false), kIdPV = umma_idesc_16(true, kD, true);
+      const uint64_t dq = umma_sdesc(smem_addr(smem + L.q), 16, 1024);
+      const uint64_t dk = umma_sdesc(smem_addr(smem + L.k), 16, 1024);
+      const uint64_t dv = umma_sdesc(smem_addr(smem + L.v), kHalf, 1024);
+      auto qk = [&](int t, int qt, int cnt) {
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint64_t off = (uint64_t)(((kk >> 2) * kHalf + (kk & 3) * 32) >> 4);
+          umma_f16(tmem + kColS + 128 * t, dq + (uint64_t)(qt * (kTileBytes >> 4)) + off, dk + (uint64_t)((cnt & 1) * (kTileBytes >> 4)) + off, kIdQK, kk > 0);
+        }
+        umma_commit(s_full + t);
+      };
+      auto pv = [&](int t, int cnt, uint32_t acc) {
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          umma_f16_ts(tmem + kColO + 128 * t, tmem + kColS + 128 * t + 8 * kk, dv + (uint64_t)(((cnt & 1) * kTileBytes + kk * 2048) >> 4), kIdPV, kk > 0 ? 1u : acc);
+      };
+      auto wait2 = [&](uint64_t* bar, int cnt) { return role_wait(bar + (cnt & 1), (uint32_t)(cnt >> 1) & 1u, failed); };
+      bool ok = true;
+      int cnt = 0;  // blocks before the piece
+      uint32_t pph[2] = {0u, 0u};
+      for (int k = 0; ok && it.next(pc); ++k) {
+        const int nb = pc.j1 - pc.j0;
+        if (!(ok = role_wait(q_ready, (uint32_t)k & 1u, failed))) break;
+        if (pc.w == 2) {
+          if (!(ok = wait2(k_ready, cnt))) break;
+          tc_fence_after();
+          qk(0, 0, cnt);
+          qk(1, 1, cnt);
+          umma_commit(k_free + (cnt & 1));
+          for (int i = 0; ok && i < nb; ++i) {
+            ok = wait2(v_ready, cnt + i);
+            for (int t = 0; ok && t < 2; ++t) {
+              ok = role_wait(p_ready + t, pph[t], failed);
+              if (!ok) break;
+              pph[t] ^= 1u;
+              tc_fence_after();
+              pv(t, cnt + i, i > 0);
+              if (i == nb - 1) {
+                umma_commit(o_full + t);
+              } else {
+                if (t == 0 && !(ok = wait2(k_ready, cnt + i + 1))) break;
+                tc_fence_after();
+                qk(t, t, cnt + i + 1);
+              }
+            }
+            if (!ok) break;
+            umma_commit(v_free + ((cnt + i) & 1));
+            if (i < nb - 1) umma_commit(k_free + ((cnt + i + 1) & 1));
+          }
+        } else {
+          for (int i = 0; ok && i < min(2, nb); ++i) {
+            if (!(ok = wait2(k_ready, cnt + i))) break;
+            tc_fence_after();
+            qk(i & 1, 0, cnt + i);
+            umma_commit(k_free + ((cnt + i) & 1));
+          }
+          for (int i = 0; ok && i < nb; ++i) {
+            const int t = i & 1;
+            ok = wait2(v_ready, cnt + i) && role_wait(p_ready + t, pph[t], failed);
+            if (!ok) break;
+            pph[t] ^= 1u;
+            tc_fence_after();
+            pv(t, cnt + i, i >= 2);
+            umma_commit(v_free + ((cnt + i) & 1));
+            if (i + 2 >= nb) {
+              umma_commit(o_full + t);
+            } else {
+              if (!(ok = wait2(k_ready, cnt + i + 2))) break;
+              tc_fence_after();
+              qk(t, 0, cnt + i + 2);
+              umma_commit(k_free + ((cnt + i + 2) & 1));
+            }
+          }
+        }
+        cnt += nb;
+      }
+      umma_commit(fin);  // arrives once every product issued has completed
+      mbar_wait_bounded(fin, 0);
+    }
+  } else if (warp >= 8) {
+    // -------------------------------------------------------------- conversion
+    reg_dealloc<kRegConv>();
+    const int tok = threadIdx.x - 256, half = tok >> 6, slot = tok & 63;
+    int cnt = 0, pages = 0;  // blocks and pages so far
+    bool ok = true;
+    while (ok && it.next(pc)) {
+      bool bad = false;
+      const int ctx = tree_ctx(j, pc.b, bad);
+      const int first = first_pos(j, ctx), p0 = first / kPage, p1 = (ctx + j.N + kPage - 1) / kPage;
+      for (int jb = pc.j0; ok && jb < pc.j1; ++jb, ++cnt) {
+        const int pg = p0 + 2 * jb, have = min(2, p1 - pg);  // pages of the block
+        const int cb = cnt & 1;
+        const uint32_t ph = (uint32_t)((cnt >> 1) - 1) & 1u;
+        uint8_t* kt = smem + L.k + cb * kTileBytes;
+        uint8_t* vt = smem + L.v + cb * kTileBytes;
+        const int st = (pages + half) % p.nst;
+        const uint8_t* raw = smem + L.raw + st * stage_bytes(FMT);
+        bool use = half < have;
+        if (use) {
+          ok = __all_sync(0xffffffffu, role_wait(raw_full + st, (uint32_t)((pages + half) / p.nst) & 1u, failed));
+          use = valid[st] != 0;
+          if (slot == 0) bvalid[2 * (cnt & 3) + half] = use;
+        }
+        const int pos = (pg + half) * kPage + slot;
+        const bool live = use && pos >= first && pos < ctx + j.N;  // a token that some row may see
+        ok = ok && __all_sync(0xffffffffu, cnt < 2 || role_wait(k_free + cb, ph, failed));
+        if (!ok) break;
+        uint32_t mk = 0, mv = 0;
+        if (FMT == 0 && live) {
+          mk = reinterpret_cast<const uint32_t*>(raw + 2 * kPage * kRec4)[slot];
+          mv = reinterpret_cast<const uint32_t*>(raw + 2 * kPage * kRec4)[kPage + slot];
+        }
+        if (!live) zero_row(kt, tok);
+        else if (FMT == 0) convert_k4(raw + slot * kRec4, slot, half_lo(mk), half_hi(mk), kt, tok);
+        else convert8(raw + slot * kRec8, slot, kt, tok);
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(k_ready + cb);
+        ok = __all_sync(0xffffffffu, cnt < 2 || role_wait(v_free + cb, ph, failed));
+        if (!ok) break;
+        if (!live) zero_row(vt, tok);
+        else if (FMT == 0) convert_v4(raw + kPage * kRec4 + slot * kRec4, slot, half_lo(mv), half_hi(mv), vt, tok);
+        else convert8(raw + kPage * kRec8 + slot * kRec8, slot, vt, tok);
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(v_ready + cb);
+          if (half < have) mbar_arrive(raw_empty + st);
+        }
+        pages += have;
+      }
+    }
+  } else {
+    // -------------------------------------------------------------- softmax and output
+    reg_alloc<kRegSoftmax>();
+    const int t = warp >> 2, r = threadIdx.x & 127;
+    const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t ts = tmem + lane_base + kColS + 128 * t;
+    const uint64_t all = j.N == 64 ? ~0ull : (1ull << j.N) - 1;
+    uint32_t sph = 0, oph = 0;
+    int cnt0 = 0;
+    bool ok = true, first_piece = true;
+    for (; ok && it.next(pc); first_piece = false) {
+      bool bad = false;
+      const int ctx = tree_ctx(j, pc.b, bad);
+      const int rows = group_rows(p, pc.g), rows0 = tile0_rows(rows, pc.w);
+      // ---- Q' rows of the tile (both groups of warps together where there is one)
+      {
+        const int tile = pc.w == 2 ? t : 0;
+        const int nthr = pc.w == 2 ? 128 : 256, me = pc.w == 2 ? r : (int)threadIdx.x;
+        const int r0 = pc.g * kGroup + tile * rows0, nr = tile ? rows - rows0 : rows0;
+        for (int e = me; e < 128 * 16; e += nthr) {
+          const int row = e >> 4, w = e & 15;
+          uint4 o = make_uint4(0u, 0u, 0u, 0u);
+          if (row < nr) {
+            const size_t src = out_row(p, pc.b, pc.h, r0 + row) * kD + 8 * w;
+            float x[8];
+            if (FMT == 1 && j.q_bf16) {
+              const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(j.q) + src);
+              const uint32_t ww[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                x[2 * i] = bf16_bits_to_f32(ww[i] & 0xFFFFu);
+                x[2 * i + 1] = bf16_bits_to_f32(ww[i] >> 16);
+              }
+            } else {
+              const float4* q4 = reinterpret_cast<const float4*>((FMT == 0 ? j.q_rot : static_cast<const float*>(j.q)) + src);
+              const float4 a = q4[0], b4 = q4[1];
+              x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b4.x, x[5] = b4.y, x[6] = b4.z, x[7] = b4.w;
+            }
+            float y[8];
+#pragma unroll
+            for (int d = 0; d < 8; ++d) y[col_of<FMT>(d)] = x[d] * p.qmul;
+            o = make_uint4(pack_f16x2_sat(y[0], y[1]), pack_f16x2_sat(y[2], y[3]), pack_f16x2_sat(y[4], y[5]), pack_f16x2_sat(y[6], y[7]));
+          }
+          *reinterpret_cast<uint4*>(smem + L.q + tile * kTileBytes + tile_offset(row, w)) = o;
+        }
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_ready);
+      }
+      // ---- this thread's row
+      const int nr = pc.w == 2 && t ? rows - rows0 : rows0;
+      const int grow = pc.g * kGroup + (pc.w == 2 && t ? rows0 : 0) + r;  // row of the KV head
+      const bool mine = r < nr;
+      const uint64_t mask = mine ? j.mask[(size_t)pc.b * j.N + grow / p.G] & all : 0ull;
+      const int first = first_pos(j, ctx);
+      // first position that the row sees, and whether that differs from the block range's
+      const int lo = FMT == 0 ? 0 : max(0, ctx + max(1, __popcll(mask)) - j.window);
+      const bool warp_rows = (r & ~31) < nr;
+      float base = -INFINITY;
+      uint64_t l2[2] = {0ull, 0ull};
+      const int step = pc.w == 2 ? 1 : 2, jfirst = pc.j0 + (pc.w == 2 ? 0 : t);
+      for (int jb = jfirst; jb < pc.j1; jb += step) {
+        ok = __all_sync(0xffffffffu, role_wait(s_full + t, sph, failed));
+        if (!ok) break;
+        sph ^= 1u;
+        tc_fence_after();
+        if (warp_rows) {
+          const int pos0 = (first / kPage + 2 * jb) * kPage;
+          const int bi = 2 * ((cnt0 + jb - pc.j0) & 3);
+          const bool pages_ok = bvalid[bi] != 0 && (bvalid[bi + 1] != 0 || pos0 + kPage >= ctx + j.N);
+          // which of the block's tokens the row sees, where some may be hidden
+          const bool edge = pos0 + kBlk > ctx || !pages_ok || (FMT == 1 && pos0 < ctx + j.N - j.window);
+          uint64_t see[2] = {~0ull, ~0ull};
+          if (edge) {
+            const int cut = ctx - pos0;  // tokens from here on are drafted ones
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int cc = cut - 64 * h;
+              uint64_t m = cc <= 0 ? 0ull : cc >= 64 ? ~0ull : (1ull << cc) - 1;
+              if (FMT == 1) {
+                const int ll = lo - pos0 - 64 * h;  // context tokens before this are outside the window
+                if (ll > 0) m = ll >= 64 ? 0ull : m & ~((1ull << ll) - 1);
+              }
+              if (cc >= 0) m |= cc >= 64 ? 0ull : mask << cc;
+              else if (cc > -64) m |= mask >> -cc;
+              if (!bvalid[bi + h]) m = 0ull;
+              see[h] = m;
+            }
+          }
+          float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t s[32];
+            tmem_ld32u(ts + 32 * q, s);
+            tmem_wait_ld_all();
+            if (edge) {
+              const uint32_t m = (uint32_t)(see[q >> 1] >> (32 * (q & 1)));
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (!((m >> i) & 1u)) s[i] = 0xFF800000u;
+            }
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+              mx0 = fmax3(mx0, __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+              mx1 = fmax3(mx1, __uint_as_float(s[i + 2]), __uint_as_float(s[i + 3]));
+            }
+          }
+          const float top = fmaxf(mx0, mx1) * p.c;
+          const bool move = top > base + 8.0f || (base == -INFINITY && top > -INFINITY);
+          if (__any_sync(0xffffffffu, move)) {
+            const float alpha = move ? fast_exp2(base - top) : 1.0f;
+            if (move) base = top;
+            l2[0] = mul_f2(l2[0], f2(alpha, alpha));
+            l2[1] = mul_f2(l2[1], f2(alpha, alpha));
+            if (jb > jfirst) {  // O of the first block starts anew
+              const uint32_t to = tmem + lane_base + kColO + 128 * t;
+#pragma unroll 1
+              for (int i = 0; i < 4; ++i) {
+                uint32_t o[32];
+                tmem_ld32u(to + 32 * i, o);
+                tmem_wait_ld_all();
+#pragma unroll
+                for (int u = 0; u < 32; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * alpha);
+                tmem_st32u(to + 32 * i, o);
+              }
+            }
+          }
+          const float neg = base == -INFINITY ? 0.0f : -base;
+          const uint64_t c2 = f2(p.c, p.c), n2 = f2(neg, neg);
+          // P of 32 tokens takes 16 columns: behind the scores read so far
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t s[32], pk[16];
+            tmem_ld32u(ts + 32 * q, s);
+            tmem_wait_ld_all();
+            if (edge) {
+              const uint32_t m = (uint32_t)(see[q >> 1] >> (32 * (q & 1)));
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (!((m >> i) & 1u)) s[i] = 0xFF800000u;
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const uint64_t x = fma_f2(f2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), c2, n2);
+              const float e0 = fast_exp2(f2lo(x)), e1 = fast_exp2(f2hi(x));
+              l2[i & 1] = add_f2(l2[i & 1], f2(e0, e1));
+              pk[i] = pack16x2<true>(e0, e1);
+            }
+            tmem_st16u(ts + 16 * q, pk);
+          }
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_ready + t);
+      }
+      cnt0 += pc.j1 - pc.j0;
+      if (ok && jfirst < pc.j1) {
+        ok = __all_sync(0xffffffffu, role_wait(o_full + t, oph, failed));
+        oph ^= 1u;
+      }
+      float l = (f2lo(l2[0]) + f2hi(l2[0])) + (f2lo(l2[1]) + f2hi(l2[1]));
+      // ---- end of the piece: two streams over the same rows are joined, each group of warps taking half of
+      // the dims. A warp that gave up takes all eight with it, so that none waits here for another.
+      const bool join = pc.w == 1;
+      const bool two = join && pc.j1 - pc.j0 > 1;  // the second stream had blocks
+      if (join && ok && jfirst < pc.j1) mlx[t * 128 + r] = make_float2(base, l);
+      tc_fence_before();
+      if (named_barrier_or(1, 256, !ok)) {
+        ok = false;
+        break;
+      }
+      float a0 = t == 0 ? 1.0f : 0.0f, a1 = 1.0f - a0;
+      int c0 = 0, c1 = 128;
+      if (join) {
+        const float2 m0 = mlx[r], m1 = two ? mlx[128 + r] : make_float2(-INFINITY, 0.0f);
+        base = fmaxf(m0.x, m1.x);
+        a0 = m0.x == -INFINITY ? 0.0f : fast_exp2(m0.x - base);
+        a1 = m1.x == -INFINITY ? 0.0f : fast_exp2(m1.x - base);
+        l = m0.y * a0 + m1.y * a1;
+        if (m0.y != m0.y || m1.y != m1.y) l = m0.y + m1.y;  // NaN
+        c0 = 64 * t;
+        c1 = c0 + 64;
+      }
+      tc_fence_after();
+      const bool whole = pc.j0 == 0 && pc.j1 == pc.nb;
+      const float f = whole ? (l > 0.0f || l != l ? p.vmul / l : 0.0f) : 1.0f;
+      const size_t row = mine ? out_row(p, pc.b, pc.h, grow) : 0;
+      const size_t slot = (size_t)(2 * blockIdx.x + (first_piece ? 0 : 1)) * p.prow + (join ? r : t * 128 + r);
+      if (!whole && mine && (!join || t == 0)) p.ml[slot] = make_float2(base, l);
+      const uint32_t to = tmem + lane_base + kColO;
+      if (warp_rows) {
+#pragma unroll 1
+        for (int cc = c0; cc < c1; cc += 32) {
+          uint32_t x[32], y[32];
+          tmem_ld32u(to + cc + (join ? 0 : 128 * t), x);
+          if (two) tmem_ld32u(to + cc + 128, y);
+          tmem_wait_ld_all();
+          float v[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            v[i] = __uint_as_float(x[i]);
+            if (join) v[i] *= a0;
+            if (two) v[i] = fmaf(__uint_as_float(y[i]), a1, v[i]);
+            if (l == 0.0f) v[i] = 0.0f;  // nothing seen: O holds 0, or (no product yet) anything
+          }
+          if (mine) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (whole) store8<FMT>(j.out, j.out_bf16, row * kD + cc + 8 * i, v + 8 * i, f);
+              else store8<FMT>(p.acc, false, slot * kD + cc + 8 * i, v + 8 * i, 1.0f);
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      if (join) named_barrier(1, 256);  // both have read both streams' O, and mlx
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 13) tmem_dealloc_512(tmem);
+  if (threadIdx.x == 0 && *failed) set_err(j.dev_err, KVQ_DEVERR_TIMEOUT);
+}
+
+// Joins the partials of the segments that several CTAs shared: one warp per row, four dims a lane, in
+// the order of the CTAs.
+constexpr int kCombineWarps = 8;
+template <int FMT>
+__global__ void __launch_bounds__(kCombineWarps * 32) tree_combine_kernel(const __grid_constant__ TreeParams p, int ctas) {
+  extern __shared__ int pre_s[];
+  const TreeJob& j = p.j;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == 0) build_pre(j, pre_s, false);
+  __syncthreads();
+  const Split sp(p, pre_s, ctas);
+  const long long items = (long long)j.B * j.Hkv * p.R;
+  for (long long e = (long long)blockIdx.x * kCombineWarps + warp; e < items; e += (long long)gridDim.x * kCombineWarps) {
+    const int rr = (int)(e % p.R), h = (int)(e / p.R % j.Hkv), b = (int)(e / p.R / j.Hkv);
+    const int g = rr / kGroup, w = g < p.ng - 1 ? 2 : p.w_last, nb = pre_s[b + 1] - pre_s[b];
+    const long long xs = (long long)pre_s[b] * sp.per_seq + (long long)h * nb * (sp.per_seq / j.Hkv) + 2LL * g * nb;
+    const int ca = sp.owner(xs), cb = sp.owner(xs + (long long)(nb - 1) * w);
+    if (ca == cb) continue;
+    const int rows0 = tile0_rows(group_rows(p, g), w);
+    int r = rr - g * kGroup;
+    if (w == 2 && r >= rows0) r += 128 - rows0;
+    // the segment's first block is its CTA's first one unless the block before it lies there as well
+    const long long before = xs - (g > 0 ? 2 : p.w_last);
+    float m = -INFINITY, l = 0.0f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = ca; c <= cb; ++c) {
+      const bool last = c == ca && xs > 0 && before >= sp.X(ca);
+      const size_t slot = (size_t)(2 * c + (last ? 1 : 0)) * p.prow + r;
+      const float2 ml = p.ml[slot];
+      const float4 a = reinterpret_cast<const float4*>(p.acc + slot * kD)[lane];
+      const float mn = fmaxf(m, ml.x);
+      const float f0 = m == -INFINITY ? 0.0f : exp2f(m - mn), f1 = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - mn);
+      l = l * f0 + (ml.y != ml.y ? ml.y : ml.y * f1);
+      o.x = o.x * f0 + a.x * f1, o.y = o.y * f0 + a.y * f1, o.z = o.z * f0 + a.z * f1, o.w = o.w * f0 + a.w * f1;
+      m = mn;
+    }
+    const float f = l > 0.0f || l != l ? p.vmul / l : 0.0f;
+    const size_t at = out_row(p, b, h, rr) * kD + 4 * lane;
+    if (j.out_bf16)
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(j.out) + at) = make_uint2(pack16x2<false>(o.x * f, o.y * f), pack16x2<false>(o.z * f, o.w * f));
+    else
+      *reinterpret_cast<float4*>(static_cast<float*>(j.out) + at) = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+  }
+}
+
+std::mutex g_mu;  // guards the cache below
+bool g_attr[64][2] = {{false}};
+
+int partial_rows(int N, int Hq, int Hkv) { return N * (Hq / Hkv) <= 128 ? 128 : 256; }
+
+template <int FMT>
+cudaError_t launch_t(TreeParams& p, long long blocks_max, cudaStream_t stream) {
+  int dev = 0;
+  cudaGetDevice(&dev);
+  cudaError_t e;
+  {
+    std::lock_guard<std::mutex> lock(g_mu);
+    if (dev < 0 || dev >= 64 || !g_attr[dev][FMT]) {
+      e = cudaFuncSetAttribute(tree_kernel<FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax);
+      if (e != cudaSuccess) return e;
+      if (dev >= 0 && dev < 64) g_attr[dev][FMT] = true;
+    }
+  }
+  const size_t fixed = Layout(FMT, p.prow / 128, 0, p.j.B).total + 1024;  // + alignment to 1024 bytes
+  p.nst = std::min<int>(kMaxStages, (int)((kSmemMax - fixed) / stage_bytes(FMT)));
+  if (p.nst < 1) return cudaErrorInvalidConfiguration;
+  const size_t smem = fixed + (size_t)p.nst * stage_bytes(FMT);
+  const int sms = device_sms();
+  const int ctas = (int)std::max<long long>(1, std::min<long long>(blocks_max, std::min(sms, kMaxTreeCtas)));
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(((long long)job.B * job.N * job.Hq + 3) / 4), 1, 1);
-  cfg.blockDim = dim3(128, 1, 1);
+  cfg.gridDim = dim3((unsigned)ctas, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tree_rows_kernel, p);
+  e = cudaLaunchKernelEx(&cfg, tree_kernel<FMT>, p);
+  if (e != cudaSuccess) return e;
+  const long long items = (long long)p.j.B * p.j.Hkv * p.R;
+  cfg.gridDim = dim3((unsigned)std::min<long long>((items + kCombineWarps - 1) / kCombineWarps, 8LL * sms), 1, 1);
+  cfg.blockDim = dim3(kCombineWarps * 32, 1, 1);
+  cfg.dynamicSmemBytes = 4 * (p.j.B + 1);
+  return cudaLaunchKernelEx(&cfg, tree_combine_kernel<FMT>, p, ctas);
+}
+
+}  // namespace
+
+size_t workspace_tree_partials_bytes(int B, int N, int Hq, int Hkv) {
+  return (size_t)2 * kMaxTreeCtas * partial_rows(N, Hq, Hkv) * (2 + kD) * 4;
+}
+
+cudaError_t launch_tree(const TreeJob& job, cudaStream_t stream) {
+  TreeParams p{};
+  p.j = job;
+  float c = job.sm_scale * kLog2e * (job.fmt == 1 ? job.k_scale : 1.0f);
+  p.qmul = c > 0.0f ? 1.0f : c < 0.0f ? -1.0f : 0.0f;
+  p.c = c == 0.0f ? 1.0f : (c < 0.0f ? -c : c);
+  p.vmul = job.fmt == 1 ? job.v_scale : 1.0f;
+  p.G = job.Hq / job.Hkv;
+  p.R = job.N * p.G;
+  p.ng = (p.R + kGroup - 1) / kGroup;
+  p.w_last = p.R - (p.ng - 1) * kGroup > 128 ? 2 : 1;
+  p.prow = partial_rows(job.N, job.Hq, job.Hkv);
+  p.ml = reinterpret_cast<float2*>(job.partials);
+  p.acc = job.partials + (size_t)2 * 2 * kMaxTreeCtas * p.prow;
+  const long long pages = job.fmt == 0 ? job.cache.max_pages_per_seq : job.ring.capacity / kPage + 1;
+  const long long blocks = (pages + 1) / 2 * job.B * job.Hkv * p.ng;
+  return job.fmt == 0 ? launch_t<0>(p, blocks, stream) : launch_t<1>(p, blocks, stream);
 }
 
 }  // namespace kvq
