@@ -24,9 +24,12 @@
 // two at most (its first and its last piece), and tree_combine_kernel joins them.
 //
 //   warps 0-3, 4-7  softmax of stream 0 and 1, Q' tiles, output (thread = row = tensor-memory lane)
-//   warps 8-11      conversion (thread = token of the block)
-//   warp 12         copies of pages / ring blocks into shared-memory stages
-//   warp 13         the products (one issuing thread)
+//   warps 8-11      conversion of K (thread = token of the block)
+//   warps 12-15     conversion of V
+//   warp 16         copies of pages / ring blocks into shared-memory stages
+//   warp 17         the products (one issuing thread)
+//   warp 18         the CTA's pieces of segments, one ahead (kept out of the other roles' registers: spilled
+//                   ones would miss the little L1 that this much shared memory leaves)
 
 #include <algorithm>
 #include <mutex>
@@ -42,9 +45,9 @@ constexpr int kBlk = 128;                  // tokens of a block: two pages
 constexpr int kGroup = 256;                // rows of a segment
 constexpr int kTileBytes = kBlk * kD * 2;  // fp16 tile: two 64-dim halves of 128 rows of 128 bytes
 constexpr int kHalf = kTileBytes / 2;
-constexpr int kThreads = 512;
-constexpr int kRegSoftmax = 168, kRegConv = 88, kRegAux = 88;
-static_assert(256 * kRegSoftmax + 128 * kRegConv + 128 * kRegAux <= kThreads * 128, "register shares above the launch's allocation");
+constexpr int kThreads = 640;
+constexpr int kRegSoftmax = 144, kRegConv = 64, kRegAux = 64;  // from 96 at launch
+static_assert(256 * kRegSoftmax + 256 * kRegConv + 128 * kRegAux <= kThreads * 96, "register shares above the launch's allocation");
 constexpr uint32_t kColS = 0, kColO = 256;  // stream t at + 128 t; P over the first 64 columns of S
 constexpr int kMaxTreeCtas = 256;           // sizes the partials
 constexpr int kMaxStages = 8;
@@ -67,14 +70,15 @@ struct TreeParams {
 __host__ __device__ constexpr int stage_bytes(int fmt) { return fmt == 0 ? KVQ_INT4_BLOCK_BYTES : 2 * kPage * kRec8; }
 
 struct Layout {  // offsets from the 1024-byte aligned start of dynamic shared memory
-  uint32_t q, k, v, raw, bars, valid, bvalid, state, pre, total;
+  uint32_t q, k, v, raw, bars, piece, valid, bvalid, state, pre, total;
   __host__ __device__ Layout(int fmt, int qtiles, int nst, int B) {
     q = 0;
     k = q + qtiles * kTileBytes;
     v = k + 2 * kTileBytes;
     raw = v + 2 * kTileBytes;
     bars = raw + nst * stage_bytes(fmt);  // a multiple of 16
-    valid = bars + 8 * 40;
+    piece = bars + 8 * 40;
+    valid = piece + 2 * 64;
     bvalid = valid + 4 * kMaxStages;
     state = bvalid + 4 * 8;  // failed flag, tensor-memory address
     pre = state + 8;
@@ -137,22 +141,26 @@ struct Split {
 };
 
 struct Piece {
-  int b, h, g, w;   // segment and its row tiles
-  int j0, j1, nb;   // blocks [j0, j1) of nb
-  long long xs;     // the segment's place on the weight line
+  int b, h, g, w;    // segment and its row tiles; w = 0: no more pieces
+  int j0, j1;        // its blocks of this CTA
+  int ctx, first;    // context length, first position that some row sees
+  int p0, p1;        // pages that hold positions first .. ctx + N - 1
+  int rows, rows0;   // rows of the group and of its first tile
+  int whole, slot;   // whether these are all of the segment's blocks; else the partial's slot
 };
 
-// The pieces of a CTA in order; every role walks them by itself.
+// The pieces of a CTA in order.
 struct Pieces {
   const TreeParams& p;
   const int* pre;
   const Split& s;
   long long x, x1;
+  int nb;  // blocks of the piece's segment
   __device__ Pieces(const TreeParams& p_, const int* pre_, const Split& s_, int c) : p(p_), pre(pre_), s(s_) {
     x = c < s.n ? s.X(c) : 0;
     x1 = c < s.n ? s.X(c + 1) : 0;
   }
-  __device__ bool next(Piece& o) {
+  __device__ __noinline__ bool next(Piece& o) {
     while (x < x1) {
       int lo = 0, hi = p.j.B;  // the last b with pre[b] * per_seq <= x
       while (hi - lo > 1) {
@@ -161,18 +169,17 @@ struct Pieces {
         else hi = mid;
       }
       o.b = lo;
-      o.nb = pre[lo + 1] - pre[lo];
+      nb = pre[lo + 1] - pre[lo];
       long long rem = x - (long long)pre[lo] * s.per_seq;
-      const long long per_head = (long long)o.nb * (s.per_seq / p.j.Hkv);
+      const long long per_head = (long long)nb * (s.per_seq / p.j.Hkv);
       o.h = (int)(rem / per_head);
       rem -= o.h * per_head;
-      o.g = (int)min(rem / (2 * o.nb), (long long)(p.ng - 1));
-      const long long off = rem - (long long)o.g * 2 * o.nb;
+      o.g = (int)min(rem / (2 * nb), (long long)(p.ng - 1));
+      const long long off = rem - (long long)o.g * 2 * nb;
       o.w = o.g < p.ng - 1 ? 2 : p.w_last;
-      o.xs = x - off;
-      const long long xe = o.xs + (long long)o.nb * o.w;
+      const long long xs = x - off, xe = xs + (long long)nb * o.w;
       o.j0 = (int)((off + o.w - 1) / o.w);
-      o.j1 = xe <= x1 ? o.nb : (int)((x1 - o.xs + o.w - 1) / o.w);
+      o.j1 = xe <= x1 ? nb : (int)((x1 - xs + o.w - 1) / o.w);
       x = xe;
       if (o.j0 < o.j1) return true;
     }
@@ -204,13 +211,16 @@ __device__ __forceinline__ uint32_t tile_offset(int r, int w) { return (w >> 3) 
 // One token's K record -> its row of the K tile. Word w holds dims 8w..8w+7 in the order 0, 4, 1, 5, 2, 6, 3,
 // 7 (as the nibbles pair up in 32 bits; Q' takes the same). A code is the subnormal c 2^-24 (even nibbles)
 // or c 2^-20 (odd ones): one exact product by 2^15, then c s + o rounded once.
-__device__ __forceinline__ void convert_k4(const uint8_t* rec, int slot, float s, float o, uint8_t* tile, int row) {
+__device__ __forceinline__ void convert_k4(const uint8_t* rec, int slot, uint32_t meta, uint8_t* tile, int row) {
   const int sw = k_chunk_swz(slot);
   const uint32_t up = 0x78007800u;  // 2^15
-  const uint32_t s0 = both(s * 512.0f), s1 = both(s * 32.0f), oo = both(o);
-#pragma unroll
+  const float s = half_lo(meta);
+  const uint32_t s0 = both(s * 512.0f), s1 = both(s * 32.0f), oo = both(half_hi(meta));
+  // a loop, not unrolled: the roles of the CTA together are more code than the instruction caches hold
+  uint4 r = *reinterpret_cast<const uint4*>(rec + 16 * sw);
+#pragma unroll 1
   for (int c = 0; c < 4; ++c) {
-    const uint4 r = *reinterpret_cast<const uint4*>(rec + 16 * (c ^ sw));
+    const uint4 next = *reinterpret_cast<const uint4*>(rec + 16 * (((c + 1) & 3) ^ sw));
     const uint32_t wd[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -223,69 +233,77 @@ __device__ __forceinline__ void convert_k4(const uint8_t* rec, int slot, float s
       out.w = hfma2(hmul2(h[3], up), s1, oo);
       *reinterpret_cast<uint4*>(tile + tile_offset(row, 4 * c + i)) = out;
     }
+    r = next;
   }
 }
 
 // One token's V record -> its row of the V tile, dims in the same order. A code is the subnormal
 // (c - 7.5) 2^(k - 23), k = 0, 4, 2, 6: times 2^15 plus 7.5 2^(k - 8) gives c 2^(k - 8) exactly, times
-// s 2^(8 - k) plus o the value, rounded once. Scales from 255 on (s 2^8 would pass fp16's range) take fp32
-// and saturate.
-__device__ __forceinline__ void convert_v4(const uint8_t* rec, int slot, float s, float o, uint8_t* tile, int row) {
+// s 2^(8 - k) plus o the value, rounded once. WIDE: scales from 255 on (s 2^8 would pass fp16's range) and
+// offsets near it, in fp32 and saturating.
+template <bool WIDE>
+__device__ __forceinline__ void convert_v4_as(const uint8_t* rec, int slot, uint32_t meta, uint8_t* tile, int row) {
   const int sw = (slot >> 1) & 3;
   const uint32_t up = 0x78007800u;
-  const bool wide = s >= 255.0f || fabsf(o) > 60000.0f;
-  const uint32_t s0 = both(s * 256.0f), s1 = both(s * 16.0f), s2 = both(s * 64.0f), s3 = both(s * 4.0f), oo = both(o);
-  const uint32_t m0 = both(7.5f / 256.0f), m1 = both(7.5f / 16.0f), m2 = both(7.5f / 64.0f), m3 = both(7.5f / 4.0f);
+  const float s = half_lo(meta), o = half_hi(meta);
+  const float mul[4] = {256.0f, 16.0f, 64.0f, 4.0f};  // 2^(8 - k)
+  uint32_t sc[4];
 #pragma unroll
+  for (int e = 0; e < 4; ++e) sc[e] = both(s * mul[e]);
+  const uint32_t oo = both(o);
+  uint4 r = *reinterpret_cast<const uint4*>(rec + 16 * sw);
+#pragma unroll 1
   for (int c = 0; c < 4; ++c) {
-    const uint4 r = *reinterpret_cast<const uint4*>(rec + 16 * (c ^ sw));
+    const uint4 next = *reinterpret_cast<const uint4*>(rec + 16 * (((c + 1) & 3) ^ sw));
     const uint32_t wd[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       uint32_t h[4];
       unpack8_v(wd[i], h);
-      uint32_t v[4];
-      h[0] = hfma2(h[0], up, m0);
-      h[1] = hfma2(h[1], up, m1);
-      h[2] = hfma2(h[2], up, m2);
-      h[3] = hfma2(h[3], up, m3);
-      if (__builtin_expect(!wide, 1)) {
-        v[0] = hfma2(h[0], s0, oo);
-        v[1] = hfma2(h[1], s1, oo);
-        v[2] = hfma2(h[2], s2, oo);
-        v[3] = hfma2(h[3], s3, oo);
-      } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float f = s * (e == 0 ? 256.0f : e == 1 ? 16.0f : e == 2 ? 64.0f : 4.0f);
-          v[e] = pack_f16x2_sat(fmaf(half_lo(h[e]), f, o), fmaf(half_hi(h[e]), f, o));
-        }
+      for (int e = 0; e < 4; ++e) {
+        h[e] = hfma2(h[e], up, both(7.5f / mul[e]));
+        if (WIDE) h[e] = pack_f16x2_sat(fmaf(half_lo(h[e]), s * mul[e], o), fmaf(half_hi(h[e]), s * mul[e], o));
+        else h[e] = hfma2(h[e], sc[e], oo);
       }
-      *reinterpret_cast<uint4*>(tile + tile_offset(row, 4 * c + i)) = make_uint4(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<uint4*>(tile + tile_offset(row, 4 * c + i)) = make_uint4(h[0], h[1], h[2], h[3]);
     }
+    r = next;
   }
+}
+__device__ __noinline__ void convert_v4_wide(const uint8_t* rec, int slot, uint32_t meta, uint8_t* tile, int row) {
+  convert_v4_as<true>(rec, slot, meta, tile, row);
+}
+__device__ __forceinline__ void convert_v4(const uint8_t* rec, int slot, uint32_t meta, uint8_t* tile, int row) {
+  if (__builtin_expect(half_lo(meta) >= 255.0f || fabsf(half_hi(meta)) > 60000.0f, 0)) convert_v4_wide(rec, slot, meta, tile, row);
+  else convert_v4_as<false>(rec, slot, meta, tile, row);
 }
 
 // One token's 128 e4m3 values -> its row of a tile, dims in order.
 __device__ __forceinline__ void convert8(const uint8_t* rec, int slot, uint8_t* tile, int row) {
+#pragma unroll 1
+  for (int c0 = 0; c0 < 8; c0 += 2) {
+    uint4 r[2];
 #pragma unroll
-  for (int c = 0; c < 8; ++c) {
-    const uint4 r = *reinterpret_cast<const uint4*>(rec + 16 * (c ^ (slot & 7)));
-    const uint32_t wd[4] = {r.x, r.y, r.z, r.w};
+    for (int c = 0; c < 2; ++c) r[c] = *reinterpret_cast<const uint4*>(rec + 16 * ((c0 + c) ^ (slot & 7)));
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      uint4 out;
-      out.x = e4m3x2_to_f16x2(wd[2 * i]);
-      out.y = e4m3x2_to_f16x2(wd[2 * i] >> 16);
-      out.z = e4m3x2_to_f16x2(wd[2 * i + 1]);
-      out.w = e4m3x2_to_f16x2(wd[2 * i + 1] >> 16);
-      *reinterpret_cast<uint4*>(tile + tile_offset(row, 2 * c + i)) = out;
+    for (int c = 0; c < 2; ++c) {
+      const uint32_t wd[4] = {r[c].x, r[c].y, r[c].z, r[c].w};
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        uint4 out;
+        out.x = e4m3x2_to_f16x2(wd[2 * i]);
+        out.y = e4m3x2_to_f16x2(wd[2 * i] >> 16);
+        out.z = e4m3x2_to_f16x2(wd[2 * i + 1]);
+        out.w = e4m3x2_to_f16x2(wd[2 * i + 1] >> 16);
+        *reinterpret_cast<uint4*>(tile + tile_offset(row, 2 * (c0 + c) + i)) = out;
+      }
     }
   }
 }
 
 __device__ __forceinline__ void zero_row(uint8_t* tile, int row) {
-#pragma unroll
+#pragma unroll 1
   for (int w = 0; w < 16; ++w) *reinterpret_cast<uint4*>(tile + tile_offset(row, w)) = make_uint4(0u, 0u, 0u, 0u);
 }
 
@@ -324,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   const Layout L(FMT, p.prow / 128, p.nst, j.B);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L.bars);
   uint64_t* raw_full = bars;             // [8] a page copied
-  uint64_t* raw_empty = bars + 8;        // [8] and read (the two warps of its tokens)
+  uint64_t* raw_empty = bars + 8;        // [8] and read (the two K and two V warps of its tokens)
   uint64_t* k_ready = bars + 16;         // [2] K tile written
   uint64_t* v_ready = bars + 18;         // [2]
   uint64_t* k_free = bars + 20;          // [2] products over it complete
@@ -334,6 +352,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   uint64_t* o_full = bars + 28;          // [2] a piece's last product of a stream complete
   uint64_t* q_ready = bars + 30;         // Q' of a piece written
   uint64_t* fin = bars + 31;
+  uint64_t* piece_full = bars + 32;      // [2] a piece announced
+  uint64_t* piece_empty = bars + 34;     // [2] and left behind by every role
+  Piece* pieces = reinterpret_cast<Piece*>(smem + L.piece);
+  static_assert(sizeof(Piece) <= 64, "pieces larger than their shared-memory region");
   volatile int* valid = reinterpret_cast<volatile int*>(smem + L.valid);    // [stage] the page was copied
   volatile int* bvalid = reinterpret_cast<volatile int*>(smem + L.bvalid);  // [block % 4][page] it exists in the pool
   // [2][128] base and sum, joining streams: over Q', which no product reads any more by then (all score
@@ -348,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   if (threadIdx.x == 0) {
     for (int i = 0; i < kMaxStages; ++i) {
       mbar_init(raw_full + i, 1);
-      mbar_init(raw_empty + i, 2);
+      mbar_init(raw_empty + i, 4);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(k_ready + i, 4);
@@ -358,6 +380,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       mbar_init(s_full + i, 1);
       mbar_init(p_ready + i, 4);
       mbar_init(o_full + i, 1);
+      mbar_init(piece_full + i, 1);
+      mbar_init(piece_empty + i, 18);  // copies, products, 8 conversion and 8 softmax warps
     }
     mbar_init(q_ready, 8);
     mbar_init(fin, 1);
@@ -367,28 +391,52 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   griddep_wait();
   griddep_launch_dependents();
   if (warp == 0) build_pre(j, pre, blockIdx.x == 0);
-  if (warp == 13) tmem_alloc_512(taddr);
+  if (warp == 17) tmem_alloc_512(taddr);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *taddr;
-  const Split sp(p, pre, gridDim.x);
-  Pieces it(p, pre, sp, blockIdx.x);
-  Piece pc;
+  // Piece k as the schedule announced it; false at the end or after a wait that gave up.
+  auto piece_at = [&](int k) {
+    return role_wait(piece_full + (k & 1), (uint32_t)(k >> 1) & 1u, failed) && pieces[k & 1].w != 0;
+  };
 
-  if (warp >= 12) {
+  if (warp >= 16) {
     reg_dealloc<kRegAux>();
-    if (warp == 12) {
+    if (warp == 18 && lane == 0) {
+      // ------------------------------------------------------------ schedule
+      const Split sp(p, pre, gridDim.x);
+      Pieces it(p, pre, sp, blockIdx.x);
+      for (int k = 0;; ++k) {
+        Piece pc;
+        if (it.next(pc)) {
+          bool bad = false;
+          pc.ctx = tree_ctx(j, pc.b, bad);
+          pc.first = first_pos(j, pc.ctx);
+          pc.p0 = pc.first / kPage;
+          pc.p1 = (pc.ctx + j.N + kPage - 1) / kPage;
+          pc.rows = group_rows(p, pc.g);
+          pc.rows0 = tile0_rows(pc.rows, pc.w);
+          pc.whole = pc.j0 == 0 && pc.j1 == it.nb;
+          pc.slot = (2 * blockIdx.x + (k > 0)) * p.prow;
+        } else {
+          pc.w = 0;
+        }
+        if (k >= 2 && !role_wait(piece_empty + (k & 1), (uint32_t)(k / 2 - 1) & 1u, failed)) break;
+        pieces[k & 1] = pc;
+        mbar_arrive(piece_full + (k & 1));
+        if (pc.w == 0) break;
+      }
+    } else if (warp == 16) {
       // ------------------------------------------------------------ copies
       const uint64_t pol = policy_evict_first();
       int issued = 0;  // pages so far
       bool ok = true;
-      while (ok && it.next(pc)) {
-        bool bad = false;
-        const int ctx = tree_ctx(j, pc.b, bad);
-        const int p0 = first_pos(j, ctx) / kPage, p1 = (ctx + j.N + kPage - 1) / kPage;
-        const int pg1 = min(p0 + 2 * pc.j1, p1);
-        for (int base = p0 + 2 * pc.j0; ok && base < pg1; base += 32) {
+      for (int k = 0; ok; ++k) {
+        if (!__all_sync(0xffffffffu, piece_at(k))) break;
+        const Piece& pc = pieces[k & 1];
+        const int pg1 = min(pc.p0 + 2 * pc.j1, pc.p1);
+        for (int base = pc.p0 + 2 * pc.j0; ok && base < pg1; base += 32) {
           const uint8_t* src = nullptr;  // null: a page outside the pool
           const int pg = base + lane;
           if (pg < pg1) {
@@ -421,10 +469,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           }
           ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(piece_empty + (k & 1));
       }
-      if (!ok && lane == 0)  // no copy may be in flight when the CTA ends
+      if (*failed && lane == 0)  // no copy may be in flight when the CTA ends
         for (int u = max(0, issued - p.nst); u < issued; ++u) mbar_wait_bounded(raw_full + u % p.nst, (uint32_t)(u / p.nst) & 1u);
-    } else if (warp == 13 && lane == 0) {
+    } else if (warp == 17 && lane == 0) {
       // ------------------------------------------------------------ products
       constexpr uint32_t kIdQK = umma_idesc_16(true, kBlk, false), kIdPV = umma_idesc_16(true, kD, true);
       const uint64_t dq = umma_sdesc(smem_addr(smem + L.q), 16, 1024);
@@ -447,10 +497,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       bool ok = true;
       int cnt = 0;  // blocks before the piece
       uint32_t pph[2] = {0u, 0u};
-      for (int k = 0; ok && it.next(pc); ++k) {
-        const int nb = pc.j1 - pc.j0;
+      for (int k = 0; ok && piece_at(k); ++k) {
+        const int nb = pieces[k & 1].j1 - pieces[k & 1].j0, tiles = pieces[k & 1].w;
+        mbar_arrive(piece_empty + (k & 1));
         if (!(ok = role_wait(q_ready, (uint32_t)k & 1u, failed))) break;
-        if (pc.w == 2) {
+        if (tiles == 2) {
           if (!(ok = wait2(k_ready, cnt))) break;
           tc_fence_after();
           qk(0, 0, cnt);
@@ -509,51 +560,48 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   } else if (warp >= 8) {
     // -------------------------------------------------------------- conversion
     reg_dealloc<kRegConv>();
-    const int tok = threadIdx.x - 256, half = tok >> 6, slot = tok & 63;
+    const bool is_v = warp >= 12;
+    const int tok = threadIdx.x & 127, half = tok >> 6, slot = tok & 63;
+    uint64_t* ready = is_v ? v_ready : k_ready;
+    uint64_t* freed = is_v ? v_free : k_free;
     int cnt = 0, pages = 0;  // blocks and pages so far
     bool ok = true;
-    while (ok && it.next(pc)) {
-      bool bad = false;
-      const int ctx = tree_ctx(j, pc.b, bad);
-      const int first = first_pos(j, ctx), p0 = first / kPage, p1 = (ctx + j.N + kPage - 1) / kPage;
-      for (int jb = pc.j0; ok && jb < pc.j1; ++jb, ++cnt) {
+    for (int k = 0; ok; ++k) {
+      if (!__all_sync(0xffffffffu, piece_at(k))) break;
+      const Piece& pc = pieces[k & 1];
+      const int first = pc.first, p0 = pc.p0, p1 = pc.p1, end = pc.ctx + j.N, j1 = pc.j1;
+      int jb = pc.j0;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(piece_empty + (k & 1));
+      for (; ok && jb < j1; ++jb, ++cnt) {
         const int pg = p0 + 2 * jb, have = min(2, p1 - pg);  // pages of the block
         const int cb = cnt & 1;
-        const uint32_t ph = (uint32_t)((cnt >> 1) - 1) & 1u;
-        uint8_t* kt = smem + L.k + cb * kTileBytes;
-        uint8_t* vt = smem + L.v + cb * kTileBytes;
+        uint8_t* tile = smem + (is_v ? L.v : L.k) + cb * kTileBytes;
         const int st = (pages + half) % p.nst;
-        const uint8_t* raw = smem + L.raw + st * stage_bytes(FMT);
+        const uint8_t* raw = smem + L.raw + st * stage_bytes(FMT) + (is_v ? kPage * (FMT == 0 ? kRec4 : kRec8) : 0);
         bool use = half < have;
         if (use) {
           ok = __all_sync(0xffffffffu, role_wait(raw_full + st, (uint32_t)((pages + half) / p.nst) & 1u, failed));
           use = valid[st] != 0;
-          if (slot == 0) bvalid[2 * (cnt & 3) + half] = use;
+          if (slot == 0 && !is_v) bvalid[2 * (cnt & 3) + half] = use;
         }
         const int pos = (pg + half) * kPage + slot;
-        const bool live = use && pos >= first && pos < ctx + j.N;  // a token that some row may see
-        ok = ok && __all_sync(0xffffffffu, cnt < 2 || role_wait(k_free + cb, ph, failed));
+        const bool live = use && pos >= first && pos < end;  // a token that some row may see
+        ok = ok && __all_sync(0xffffffffu, cnt < 2 || role_wait(freed + cb, (uint32_t)((cnt >> 1) - 1) & 1u, failed));
         if (!ok) break;
-        uint32_t mk = 0, mv = 0;
-        if (FMT == 0 && live) {
-          mk = reinterpret_cast<const uint32_t*>(raw + 2 * kPage * kRec4)[slot];
-          mv = reinterpret_cast<const uint32_t*>(raw + 2 * kPage * kRec4)[kPage + slot];
+        if (!live) {
+          zero_row(tile, tok);
+        } else if (FMT == 0) {
+          const uint32_t meta = reinterpret_cast<const uint32_t*>(smem + L.raw + st * stage_bytes(FMT) + 2 * kPage * kRec4)[(is_v ? kPage : 0) + slot];
+          if (is_v) convert_v4(raw + slot * kRec4, slot, meta, tile, tok);
+          else convert_k4(raw + slot * kRec4, slot, meta, tile, tok);
+        } else {
+          convert8(raw + slot * kRec8, slot, tile, tok);
         }
-        if (!live) zero_row(kt, tok);
-        else if (FMT == 0) convert_k4(raw + slot * kRec4, slot, half_lo(mk), half_hi(mk), kt, tok);
-        else convert8(raw + slot * kRec8, slot, kt, tok);
-        fence_proxy_async_shared();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(k_ready + cb);
-        ok = __all_sync(0xffffffffu, cnt < 2 || role_wait(v_free + cb, ph, failed));
-        if (!ok) break;
-        if (!live) zero_row(vt, tok);
-        else if (FMT == 0) convert_v4(raw + kPage * kRec4 + slot * kRec4, slot, half_lo(mv), half_hi(mv), vt, tok);
-        else convert8(raw + kPage * kRec8 + slot * kRec8, slot, vt, tok);
         fence_proxy_async_shared();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(v_ready + cb);
+          mbar_arrive(ready + cb);
           if (half < have) mbar_arrive(raw_empty + st);
         }
         pages += have;
@@ -568,16 +616,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     const uint64_t all = j.N == 64 ? ~0ull : (1ull << j.N) - 1;
     uint32_t sph = 0, oph = 0;
     int cnt0 = 0;
-    bool ok = true, first_piece = true;
-    for (; ok && it.next(pc); first_piece = false) {
-      bool bad = false;
-      const int ctx = tree_ctx(j, pc.b, bad);
-      const int rows = group_rows(p, pc.g), rows0 = tile0_rows(rows, pc.w);
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      if (!__all_sync(0xffffffffu, piece_at(k))) break;
+      const Piece& pc = pieces[k & 1];
       // ---- Q' rows of the tile (both groups of warps together where there is one)
       {
         const int tile = pc.w == 2 ? t : 0;
         const int nthr = pc.w == 2 ? 128 : 256, me = pc.w == 2 ? r : (int)threadIdx.x;
-        const int r0 = pc.g * kGroup + tile * rows0, nr = tile ? rows - rows0 : rows0;
+        const int r0 = pc.g * kGroup + tile * pc.rows0, nr = tile ? pc.rows - pc.rows0 : pc.rows0;
         for (int e = me; e < 128 * 16; e += nthr) {
           const int row = e >> 4, w = e & 15;
           uint4 o = make_uint4(0u, 0u, 0u, 0u);
@@ -609,25 +656,26 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         if (lane == 0) mbar_arrive(q_ready);
       }
       // ---- this thread's row
-      const int nr = pc.w == 2 && t ? rows - rows0 : rows0;
-      const int grow = pc.g * kGroup + (pc.w == 2 && t ? rows0 : 0) + r;  // row of the KV head
+      const int nr = pc.w == 2 && t ? pc.rows - pc.rows0 : pc.rows0;
+      const int grow = pc.g * kGroup + (pc.w == 2 && t ? pc.rows0 : 0) + r;  // row of the KV head
       const bool mine = r < nr;
       const uint64_t mask = mine ? j.mask[(size_t)pc.b * j.N + grow / p.G] & all : 0ull;
-      const int first = first_pos(j, ctx);
+      const int ctx = pc.ctx, pages0 = pc.p0 * kPage, j1 = pc.j1;
       // first position that the row sees, and whether that differs from the block range's
       const int lo = FMT == 0 ? 0 : max(0, ctx + max(1, __popcll(mask)) - j.window);
       const bool warp_rows = (r & ~31) < nr;
       float base = -INFINITY;
       uint64_t l2[2] = {0ull, 0ull};
       const int step = pc.w == 2 ? 1 : 2, jfirst = pc.j0 + (pc.w == 2 ? 0 : t);
-      for (int jb = jfirst; jb < pc.j1; jb += step) {
+      const int cntj = cnt0 - pc.j0;
+      for (int jb = jfirst; jb < j1; jb += step) {
         ok = __all_sync(0xffffffffu, role_wait(s_full + t, sph, failed));
         if (!ok) break;
         sph ^= 1u;
         tc_fence_after();
         if (warp_rows) {
-          const int pos0 = (first / kPage + 2 * jb) * kPage;
-          const int bi = 2 * ((cnt0 + jb - pc.j0) & 3);
+          const int pos0 = pages0 + 2 * kPage * jb;
+          const int bi = 2 * ((cntj + jb) & 3);
           const bool pages_ok = bvalid[bi] != 0 && (bvalid[bi + 1] != 0 || pos0 + kPage >= ctx + j.N);
           // which of the block's tokens the row sees, where some may be hidden
           const bool edge = pos0 + kBlk > ctx || !pages_ok || (FMT == 1 && pos0 < ctx + j.N - j.window);
@@ -648,10 +696,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
               see[h] = m;
             }
           }
-          float mx0 = -INFINITY, mx1 = -INFINITY;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t s[32];
+          // 32 scores at a time, read once for the maximum and once for the weights
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          uint32_t s[32];
+          auto load = [&](int q) {
             tmem_ld32u(ts + 32 * q, s);
             tmem_wait_ld_all();
             if (edge) {
@@ -660,13 +708,16 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
               for (int i = 0; i < 32; ++i)
                 if (!((m >> i) & 1u)) s[i] = 0xFF800000u;
             }
+          };
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            load(q);
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              mx0 = fmax3(mx0, __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
-              mx1 = fmax3(mx1, __uint_as_float(s[i + 2]), __uint_as_float(s[i + 3]));
-            }
+            for (int i = 0; i < 32; i += 8)
+#pragma unroll
+              for (int u = 0; u < 4; ++u) mx[u] = fmax3(mx[u], __uint_as_float(s[i + 2 * u]), __uint_as_float(s[i + 2 * u + 1]));
           }
-          const float top = fmaxf(mx0, mx1) * p.c;
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.c;
           const bool move = top > base + 8.0f || (base == -INFINITY && top > -INFINITY);
           if (__any_sync(0xffffffffu, move)) {
             const float alpha = move ? fast_exp2(base - top) : 1.0f;
@@ -676,30 +727,23 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             if (jb > jfirst) {  // O of the first block starts anew
               const uint32_t to = tmem + lane_base + kColO + 128 * t;
 #pragma unroll 1
-              for (int i = 0; i < 4; ++i) {
-                uint32_t o[32];
-                tmem_ld32u(to + 32 * i, o);
+              for (int i = 0; i < 8; ++i) {
+                uint32_t o[16];
+                tmem_ld16u(to + 16 * i, o);
                 tmem_wait_ld_all();
 #pragma unroll
-                for (int u = 0; u < 32; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * alpha);
-                tmem_st32u(to + 32 * i, o);
+                for (int u = 0; u < 16; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * alpha);
+                tmem_st16u(to + 16 * i, o);
               }
             }
           }
           const float neg = base == -INFINITY ? 0.0f : -base;
           const uint64_t c2 = f2(p.c, p.c), n2 = f2(neg, neg);
-          // P of 32 tokens takes 16 columns: behind the scores read so far
-#pragma unroll
+          // P of 32 tokens takes 16 columns, always behind the scores still to be read
+#pragma unroll 1
           for (int q = 0; q < 4; ++q) {
-            uint32_t s[32], pk[16];
-            tmem_ld32u(ts + 32 * q, s);
-            tmem_wait_ld_all();
-            if (edge) {
-              const uint32_t m = (uint32_t)(see[q >> 1] >> (32 * (q & 1)));
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (!((m >> i) & 1u)) s[i] = 0xFF800000u;
-            }
+            load(q);
+            uint32_t pk[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               const uint64_t x = fma_f2(f2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), c2, n2);
@@ -744,22 +788,22 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         c1 = c0 + 64;
       }
       tc_fence_after();
-      const bool whole = pc.j0 == 0 && pc.j1 == pc.nb;
+      const bool whole = pc.whole != 0;
       const float f = whole ? (l > 0.0f || l != l ? p.vmul / l : 0.0f) : 1.0f;
       const size_t row = mine ? out_row(p, pc.b, pc.h, grow) : 0;
-      const size_t slot = (size_t)(2 * blockIdx.x + (first_piece ? 0 : 1)) * p.prow + (join ? r : t * 128 + r);
+      const size_t slot = (size_t)pc.slot + (join ? r : t * 128 + r);
       if (!whole && mine && (!join || t == 0)) p.ml[slot] = make_float2(base, l);
       const uint32_t to = tmem + lane_base + kColO;
       if (warp_rows) {
 #pragma unroll 1
-        for (int cc = c0; cc < c1; cc += 32) {
-          uint32_t x[32], y[32];
-          tmem_ld32u(to + cc + (join ? 0 : 128 * t), x);
-          if (two) tmem_ld32u(to + cc + 128, y);
+        for (int cc = c0; cc < c1; cc += 16) {
+          uint32_t x[16], y[16];
+          tmem_ld16u(to + cc + (join ? 0 : 128 * t), x);
+          if (two) tmem_ld16u(to + cc + 128, y);
           tmem_wait_ld_all();
-          float v[32];
+          float v[16];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
+          for (int i = 0; i < 16; ++i) {
             v[i] = __uint_as_float(x[i]);
             if (join) v[i] *= a0;
             if (two) v[i] = fmaf(__uint_as_float(y[i]), a1, v[i]);
@@ -767,7 +811,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           }
           if (mine) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 2; ++i) {
               if (whole) store8<FMT>(j.out, j.out_bf16, row * kD + cc + 8 * i, v + 8 * i, f);
               else store8<FMT>(p.acc, false, slot * kD + cc + 8 * i, v + 8 * i, 1.0f);
             }
@@ -776,13 +820,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       }
       tc_fence_before();
       if (join) named_barrier(1, 256);  // both have read both streams' O, and mlx
+      __syncwarp();
+      if (lane == 0) mbar_arrive(piece_empty + (k & 1));
     }
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 13) tmem_dealloc_512(tmem);
+  if (warp == 17) tmem_dealloc_512(tmem);
   if (threadIdx.x == 0 && *failed) set_err(j.dev_err, KVQ_DEVERR_TIMEOUT);
 }
 

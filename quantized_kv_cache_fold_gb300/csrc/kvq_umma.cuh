@@ -9,6 +9,14 @@
 
 namespace kvq {
 
+// 16 consecutive 32-bit columns of this thread's lane, raw words (valid after tmem_wait_ld).
+__device__ __forceinline__ void tmem_ld16u(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
 // 32 consecutive 32-bit columns of this thread's lane, raw words (valid after tmem_wait_ld).
 __device__ __forceinline__ void tmem_ld32u(uint32_t taddr, uint32_t* r) {
   asm volatile(
@@ -49,10 +57,17 @@ __device__ __forceinline__ uint32_t pack16x2(float lo, float hi) {
   return d;
 }
 
-// Bounded wait that also gives up once another role of the CTA did (flag set).
+// Bounded wait for a phase; notes a wait that gave up in *failed. Plain try_wait (the hardware suspends the
+// thread for a while by itself): with a suspend hint the wait becomes a polling loop with sleeps, which
+// costs the other warps issue slots and the hand-over latency (tree kernel, 64 x 16,384 tokens x 16 drafted:
+// half of the instructions executed were polls).
 __device__ __forceinline__ bool role_wait(uint64_t* bar, uint32_t parity, volatile int* failed) {
   if (mbar_try_wait(bar, parity)) return true;
-  if (mbar_wait_bounded(bar, parity)) return true;
+  const uint64_t t0 = globaltimer();
+  for (uint32_t it = 1; it < (1u << 30); ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 63u) == 0 && globaltimer() - t0 > kWaitLimitNs) break;
+  }
   *failed = 1;
   return false;
 }
