@@ -96,9 +96,9 @@ def _load():
     L.kvq_tree_attn_fp8_swa.argtypes = [ctypes.POINTER(Fp8Ring), vp, i32, i32, i32, i32, vp, vp, i32, vp, vp, f32,
                                         f32, f32, vp, i32, vp, sz, vp, vp]
     L.kvq_tree_commit_int4.restype = i32
-    L.kvq_tree_commit_int4.argtypes = [ctypes.POINTER(Int4Cache), i32, i32, i32, vp, vp, vp, vp, vp, vp]
+    L.kvq_tree_commit_int4.argtypes = [vp, i32, i32, i32, vp, vp, vp, vp, vp, vp]
     L.kvq_tree_commit_fp8.restype = i32
-    L.kvq_tree_commit_fp8.argtypes = [ctypes.POINTER(Fp8Ring), i32, i32, i32, vp, vp, vp, vp, vp, vp]
+    L.kvq_tree_commit_fp8.argtypes = [vp, i32, i32, i32, vp, vp, vp, vp, vp, vp]
     for name in ("kvq_pages_alloc", "kvq_pages_free"):
         getattr(L, name).restype = i32
         getattr(L, name).argtypes = [vp, i32, vp, i32, i32, i32, vp, vp, vp, vp, vp]
@@ -107,7 +107,7 @@ def _load():
     L.kvq_pages_compact.restype = i32
     L.kvq_pages_compact.argtypes = [vp, i32, vp, i32, i32, vp, vp, vp, vp, vp]
     L.kvq_pages_copy.restype = i32
-    L.kvq_pages_copy.argtypes = [ctypes.POINTER(Int4Cache), i32, i32, vp, vp, vp, vp, vp]
+    L.kvq_pages_copy.argtypes = [vp, i32, i32, vp, vp, vp, vp, vp]
     return L
 
 
@@ -308,6 +308,20 @@ def alloc_workspace(B: int, S: int, num_q_heads: int, num_kv_heads: int, device=
 
 
 # ---------------------------------------------------------------- around decoding: prompt, tree, pages
+#
+# These calls take a few microseconds on the GPU for small batches, so their checks are written to cost
+# little on the host: one comparison chain per tensor, the raw stream handle, addresses passed as they are.
+
+_th = None  # torch, imported by the first call
+
+
+def _torch():
+    global _th
+    if _th is None:
+        import torch
+        _th = torch
+    return _th
+
 
 def _need(ok, what):
     if not ok:
@@ -315,11 +329,27 @@ def _need(ok, what):
 
 
 def _is(t, dtype, shape, name):
-    """`t` is a contiguous device tensor of this type and shape (None in the shape: any extent)."""
-    _need(t.is_cuda and t.is_contiguous(), f"{name} must be a contiguous device tensor")
-    _need(t.dtype in (dtype if isinstance(dtype, tuple) else (dtype,)), f"{name}: unsupported dtype {t.dtype}")
-    _need(t.dim() == len(shape) and all(n is None or n == m for n, m in zip(shape, t.shape)),
-          f"{name} has shape {tuple(t.shape)}, wanted {shape}")
+    """Address of `t`, a contiguous device tensor of this type and shape."""
+    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name} must be a contiguous device tensor of {dtype} and shape {tuple(shape)}, got {t.dtype} "
+                     f"{tuple(t.shape)} on {t.device}")
+
+
+def _here(t, stream):
+    """The raw stream of a call on `t`'s device, which has to be the current one (kvq.h)."""
+    torch = _th
+    dev = t.get_device()
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"tensors on cuda:{dev}, but cuda:{torch.cuda.current_device()} is the current device")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _bytes(workspace):
+    _need(workspace.is_cuda and workspace.is_contiguous(), "the workspace must be a contiguous device tensor")
+    return workspace.numel() * workspace.element_size()
 
 
 def kvq_prompt_workspace_bytes(T: int, B: int, num_q_heads: int, num_kv_heads: int) -> int:
@@ -327,10 +357,10 @@ def kvq_prompt_workspace_bytes(T: int, B: int, num_q_heads: int, num_kv_heads: i
 
 
 def alloc_prompt_workspace(T: int, B: int, num_q_heads: int, num_kv_heads: int, device="cuda"):
-    import torch
     n = kvq_prompt_workspace_bytes(T, B, num_q_heads, num_kv_heads)
     if n == 0:
         raise KvqError("kvq_prompt_workspace_bytes", 2)
+    torch = _torch()
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
@@ -339,27 +369,34 @@ def kvq_prompt_attn(q, k, v, cu_seqlens, out, workspace, dev_err, window: int = 
     """Causal attention over packed prompts. q, out [T, Hq, 128], k, v [T, Hkv, 128] (bf16 or fp16; any
     token and head strides that are multiples of 8, such as views of one projection's output),
     cu_seqlens int32[B + 1]; window <= 0: none."""
-    import torch
-    T, Hq, Hkv = q.shape[0], q.shape[1], k.shape[1]
-    for name, t, h in (("q", q, Hq), ("k", k, Hkv), ("v", v, Hkv), ("out", out, Hq)):
-        _need(t.is_cuda and t.dtype == q.dtype, f"{name} must be a device tensor of q's dtype")
-        _need(tuple(t.shape) == (T, h, HEAD_DIM), f"{name} has shape {tuple(t.shape)}, wanted {(T, h, HEAD_DIM)}")
-        _need(t.stride(2) == 1, f"the rows of {name} must be contiguous")
-    if q.dtype not in (torch.bfloat16, torch.float16):
-        raise TypeError(f"unsupported dtype {q.dtype}")
-    _is(cu_seqlens, torch.int32, (None,), "cu_seqlens")
+    torch = _torch()
+    dtype = q.dtype
+    if dtype is not torch.bfloat16 and dtype is not torch.float16:
+        raise TypeError(f"unsupported dtype {dtype}")
+    T, Hq, D = q.shape
+    Hkv = k.shape[1]
+    if not (D == HEAD_DIM and out.shape == q.shape and k.shape == v.shape == (T, Hkv, D)):
+        raise ValueError(f"shapes: q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)}, out {tuple(out.shape)}")
+    if not (k.dtype is v.dtype is out.dtype is dtype and q.is_cuda and k.is_cuda and v.is_cuda and out.is_cuda):
+        raise ValueError("q, k, v and out must be device tensors of one dtype")
     B = cu_seqlens.shape[0] - 1
+    cu = _is(cu_seqlens, torch.int32, (B + 1,), "cu_seqlens")
+    sq, sk, sv, so = q.stride(), k.stride(), v.stride(), out.stride()
+    if not sq[2] == sk[2] == sv[2] == so[2] == 1:
+        raise ValueError("the rows of q, k, v and out must be contiguous")
+    if T > 1 and Hq > 1 and Hkv > 1:
+        strides = _Strides(sq[0], sq[1], sk[0], sk[1], sv[0], sv[1], so[0], so[1])
+    else:  # of an extent of one the stride does not matter: the packed one
+        strides = _Strides(*(x for st, h in ((sq, Hq), (sk, Hkv), (sv, Hkv), (so, Hq))
+                             for x in (st[0] if T > 1 else max(1, h) * D, st[1] if h > 1 else D)))
+    status = lib.kvq_prompt_attn(q.data_ptr(), k.data_ptr(), v.data_ptr(), BF16 if dtype is torch.bfloat16 else F16, T,
+                                 B, Hq, Hkv, strides, cu, window, sm_scale, out.data_ptr(), workspace.data_ptr(),
+                                 _bytes(workspace), dev_err.data_ptr(), _here(q, stream))
+    if status:
+        raise KvqError("kvq_prompt_attn", status)
 
-    def stride(t):  # of an extent of one the stride does not matter: the packed one
-        return (t.stride(0) if t.shape[0] > 1 else max(8, t.shape[1] * HEAD_DIM),
-                t.stride(1) if t.shape[1] > 1 else HEAD_DIM)
 
-    strides = (ctypes.c_int64 * 8)(*(s for t in (q, k, v, out) for s in stride(t)))
-    ws_bytes = workspace.numel() * workspace.element_size()
-    _check("kvq_prompt_attn",
-           lib.kvq_prompt_attn(_ptr(q), _ptr(k), _ptr(v), BF16 if q.dtype == torch.bfloat16 else F16, T, B, Hq, Hkv,
-                               strides, _ptr(cu_seqlens), int(window), sm_scale, _ptr(out), _ptr(workspace), ws_bytes,
-                               _ptr(dev_err), _stream(stream)))
+_Strides = ctypes.c_int64 * 8
 
 
 def kvq_tree_workspace_bytes(B: int, N: int, num_q_heads: int, num_kv_heads: int) -> int:
@@ -367,24 +404,30 @@ def kvq_tree_workspace_bytes(B: int, N: int, num_q_heads: int, num_kv_heads: int
 
 
 def alloc_tree_workspace(B: int, N: int, num_q_heads: int, num_kv_heads: int, device="cuda"):
-    import torch
     n = kvq_tree_workspace_bytes(B, N, num_q_heads, num_kv_heads)
     if n == 0:
         raise KvqError("kvq_tree_workspace_bytes", 2)
+    torch = _torch()
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
 def _tree_args(q, ctx_len, tree_mask, out, k_new, v_new, Hkv):
-    import torch
-    B, N, Hq, _ = q.shape
-    _is(q, (torch.float32, torch.bfloat16), (B, N, Hq, HEAD_DIM), "q")
-    _is(ctx_len, torch.int32, (B,), "ctx_len")
-    _is(tree_mask, (torch.int64, torch.uint64), (B, N), "tree_mask")
-    _is(out, (torch.float32, torch.bfloat16), (B, N, Hq, HEAD_DIM), "out")
-    for name, t in (("k_new", k_new), ("v_new", v_new)):
-        if t is not None:
-            _is(t, q.dtype, (B, N, Hkv, HEAD_DIM), name)
-    return B, N, Hq
+    """(B, N, Hq, dtype code, addresses of ctx_len, mask, k_new, v_new, out's dtype code)."""
+    torch = _torch()
+    B, N, Hq, D = q.shape
+    if not (q.dtype is torch.bfloat16 or q.dtype is torch.float32) or D != HEAD_DIM or not (q.is_cuda and q.is_contiguous()):
+        raise ValueError(f"q must be a contiguous device tensor [B, N, Hq, 128] of fp32 or bf16, got {q.dtype} {tuple(q.shape)}")
+    if not (out.dtype is torch.bfloat16 or out.dtype is torch.float32):
+        raise ValueError(f"out must be fp32 or bf16, got {out.dtype}")
+    _is(out, out.dtype, q.shape, "out")
+    if k_new is not None:
+        _is(k_new, q.dtype, (B, N, Hkv, D), "k_new")
+    if v_new is not None:
+        _is(v_new, q.dtype, (B, N, Hkv, D), "v_new")
+    mask = _is(tree_mask, torch.uint64 if tree_mask.dtype is torch.uint64 else torch.int64, (B, N), "tree_mask")
+    return (B, N, Hq, BF16 if q.dtype is torch.bfloat16 else F32, _is(ctx_len, torch.int32, (B,), "ctx_len"), mask,
+            None if k_new is None else k_new.data_ptr(), None if v_new is None else v_new.data_ptr(),
+            BF16 if out.dtype is torch.bfloat16 else F32)
 
 
 def kvq_tree_attn_int4(cache: Int4Cache, Mq, Mk, q, ctx_len, tree_mask, out, workspace, dev_err, k_new=None,
@@ -393,103 +436,109 @@ def kvq_tree_attn_int4(cache: Int4Cache, Mq, Mk, q, ctx_len, tree_mask, out, wor
     """Attention of N drafted tokens per sequence over the int4 cache: q [B, N, Hq, 128] (fp32 or bf16),
     tree_mask int64 [B, N] (bit j: attends to drafted token j), out fp32 or bf16. fwht as in
     kvq_decode_attn_int4."""
-    B, N, Hq = _tree_args(q, ctx_len, tree_mask, out, k_new, v_new, cache.num_kv_heads)
-    name = "kvq_tree_attn_int4_fwht" if fwht else "kvq_tree_attn_int4"
-    _check(name, getattr(lib, name)(ctypes.byref(cache), _ptr(Mq), _ptr(Mk), _ptr(q), _dtype_code(q), B, N, Hq,
-                                    _ptr(ctx_len), _ptr(tree_mask), _ptr(k_new), _ptr(v_new), sm_scale, eps,
-                                    _ptr(out), _dtype_code(out), _ptr(workspace),
-                                    workspace.numel() * workspace.element_size(), _ptr(dev_err), _stream(stream)))
+    B, N, Hq, dt, ctx, mask, kn, vn, odt = _tree_args(q, ctx_len, tree_mask, out, k_new, v_new, cache.num_kv_heads)
+    fn = lib.kvq_tree_attn_int4_fwht if fwht else lib.kvq_tree_attn_int4
+    status = fn(ctypes.byref(cache), Mq.data_ptr(), None if Mk is None else Mk.data_ptr(), q.data_ptr(), dt, B, N, Hq, ctx,
+                mask, kn, vn, sm_scale, eps, out.data_ptr(), odt, workspace.data_ptr(), _bytes(workspace),
+                dev_err.data_ptr(), _here(q, stream))
+    if status:
+        raise KvqError("kvq_tree_attn_int4_fwht" if fwht else "kvq_tree_attn_int4", status)
 
 
 def kvq_tree_attn_fp8_swa(ring: Fp8Ring, q, pos0, tree_mask, window: int, k_scale: float, v_scale: float, out,
                           workspace, dev_err, k_new=None, v_new=None, sm_scale: float = HEAD_DIM ** -0.5,
                           stream=None):
     """kvq_tree_attn_int4 over the e4m3 ring of a sliding-window layer (q used as given)."""
-    B, N, Hq = _tree_args(q, pos0, tree_mask, out, k_new, v_new, ring.num_kv_heads)
-    _check("kvq_tree_attn_fp8_swa",
-           lib.kvq_tree_attn_fp8_swa(ctypes.byref(ring), _ptr(q), _dtype_code(q), B, N, Hq, _ptr(pos0),
-                                     _ptr(tree_mask), window, _ptr(k_new), _ptr(v_new), k_scale, v_scale, sm_scale,
-                                     _ptr(out), _dtype_code(out), _ptr(workspace),
-                                     workspace.numel() * workspace.element_size(), _ptr(dev_err), _stream(stream)))
+    B, N, Hq, dt, ctx, mask, kn, vn, odt = _tree_args(q, pos0, tree_mask, out, k_new, v_new, ring.num_kv_heads)
+    status = lib.kvq_tree_attn_fp8_swa(ctypes.byref(ring), q.data_ptr(), dt, B, N, Hq, ctx, mask, window, kn, vn, k_scale,
+                                       v_scale, sm_scale, out.data_ptr(), odt, workspace.data_ptr(), _bytes(workspace),
+                                       dev_err.data_ptr(), _here(q, stream))
+    if status:
+        raise KvqError("kvq_tree_attn_fp8_swa", status)
 
 
-def _tree_commit(name, kind, layers, ctx_len, path, n_accept, dev_err, ctx_out, stream):
-    import torch
+def _layers(layers):
+    """The layers' descriptors one behind the other (each a ctypes structure: its bytes)."""
+    return b"".join(layers)
+
+
+def _tree_commit(name, layers, ctx_len, path, n_accept, dev_err, ctx_out, stream):
+    i32 = _torch().int32
     B, N = path.shape
-    _is(path, torch.int32, (B, N), "path")
-    _is(ctx_len, torch.int32, (B,), "ctx_len")
-    _is(n_accept, torch.int32, (B,), "n_accept")
-    if ctx_out is not None:
-        _is(ctx_out, torch.int32, (B,), "ctx_out")
-    _check(name, getattr(lib, name)((kind * len(layers))(*layers), len(layers), B, N, _ptr(ctx_len), _ptr(path),
-                                    _ptr(n_accept), _ptr(ctx_out), _ptr(dev_err), _stream(stream)))
+    status = getattr(lib, name)(_layers(layers), len(layers), B, N, _is(ctx_len, i32, (B,), "ctx_len"),
+                                _is(path, i32, (B, N), "path"), _is(n_accept, i32, (B,), "n_accept"),
+                                None if ctx_out is None else _is(ctx_out, i32, (B,), "ctx_out"), dev_err.data_ptr(),
+                                _here(path, stream))
+    if status:
+        raise KvqError(name, status)
 
 
 def kvq_tree_commit_int4(caches, ctx_len, path, n_accept, dev_err, ctx_out=None, stream=None):
     """Moves the accepted tokens path[b, :n_accept[b]] of each tree right behind the context in every
     one of the layers `caches` (a list of Int4Cache); ctx_out receives the new context lengths."""
-    _tree_commit("kvq_tree_commit_int4", Int4Cache, caches, ctx_len, path, n_accept, dev_err, ctx_out, stream)
+    _tree_commit("kvq_tree_commit_int4", caches, ctx_len, path, n_accept, dev_err, ctx_out, stream)
 
 
 def kvq_tree_commit_fp8(rings, pos0, path, n_accept, dev_err, ctx_out=None, stream=None):
     """kvq_tree_commit_int4 for sliding-window layers (a list of Fp8Ring)."""
-    _tree_commit("kvq_tree_commit_fp8", Fp8Ring, rings, pos0, path, n_accept, dev_err, ctx_out, stream)
+    _tree_commit("kvq_tree_commit_fp8", rings, pos0, path, n_accept, dev_err, ctx_out, stream)
 
 
-def _pool_args(page_refs, block_table, lists):
-    import torch
-    _is(page_refs, torch.int32, (None,), "page_refs")
-    _is(block_table, torch.int32, (None, None), "block_table")
-    n = lists[0][1].shape[0]
-    for name, t in lists:
-        _is(t, torch.int32, (n,), name)
-    return _ptr(page_refs), page_refs.shape[0], _ptr(block_table), block_table.shape[0], block_table.shape[1], n
+def _pool(page_refs, block_table):
+    i32 = _torch().int32
+    S, M = block_table.shape
+    n = page_refs.shape[0]
+    return _is(page_refs, i32, (n,), "page_refs"), n, _is(block_table, i32, (S, M), "block_table"), S, M
 
 
 def kvq_pages_alloc(page_refs, block_table, seq_ids, len_old, len_new, dev_err, stream=None):
     """Gives sequences seq_ids the pages to grow from len_old to len_new tokens (lowest free first)."""
-    a = _pool_args(page_refs, block_table, (("seq_ids", seq_ids), ("len_old", len_old), ("len_new", len_new)))
-    _check("kvq_pages_alloc", lib.kvq_pages_alloc(*a, _ptr(seq_ids), _ptr(len_old), _ptr(len_new), _ptr(dev_err),
-                                                  _stream(stream)))
+    pool, i32, n = _pool(page_refs, block_table), _th.int32, seq_ids.shape[0]
+    status = lib.kvq_pages_alloc(*pool, n, _is(seq_ids, i32, (n,), "seq_ids"), _is(len_old, i32, (n,), "len_old"),
+                                 _is(len_new, i32, (n,), "len_new"), dev_err.data_ptr(), _here(page_refs, stream))
+    if status:
+        raise KvqError("kvq_pages_alloc", status)
 
 
 def kvq_pages_fork(page_refs, block_table, parents, children, lens, copy_src, copy_dst, dev_err, stream=None):
     """Children share their parents' full pages of the first lens tokens and get a page of their own
     for a partly filled last one: kvq_pages_copy(caches, copy_src, copy_dst) then fills it."""
-    a = _pool_args(page_refs, block_table, (("parents", parents), ("children", children), ("lens", lens),
-                                            ("copy_src", copy_src), ("copy_dst", copy_dst)))
-    _check("kvq_pages_fork", lib.kvq_pages_fork(*a, _ptr(parents), _ptr(children), _ptr(lens), _ptr(copy_src),
-                                                _ptr(copy_dst), _ptr(dev_err), _stream(stream)))
+    pool, i32, n = _pool(page_refs, block_table), _th.int32, parents.shape[0]
+    status = lib.kvq_pages_fork(*pool, n, _is(parents, i32, (n,), "parents"), _is(children, i32, (n,), "children"),
+                                _is(lens, i32, (n,), "lens"), _is(copy_src, i32, (n,), "copy_src"),
+                                _is(copy_dst, i32, (n,), "copy_dst"), dev_err.data_ptr(), _here(page_refs, stream))
+    if status:
+        raise KvqError("kvq_pages_fork", status)
 
 
 def kvq_pages_free(page_refs, block_table, seq_ids, len_old, len_new, dev_err, stream=None):
     """Gives back the pages of sequences seq_ids behind len_new tokens."""
-    a = _pool_args(page_refs, block_table, (("seq_ids", seq_ids), ("len_old", len_old), ("len_new", len_new)))
-    _check("kvq_pages_free", lib.kvq_pages_free(*a, _ptr(seq_ids), _ptr(len_old), _ptr(len_new), _ptr(dev_err),
-                                                _stream(stream)))
+    pool, i32, n = _pool(page_refs, block_table), _th.int32, seq_ids.shape[0]
+    status = lib.kvq_pages_free(*pool, n, _is(seq_ids, i32, (n,), "seq_ids"), _is(len_old, i32, (n,), "len_old"),
+                                _is(len_new, i32, (n,), "len_new"), dev_err.data_ptr(), _here(page_refs, stream))
+    if status:
+        raise KvqError("kvq_pages_free", status)
 
 
 def kvq_pages_compact(page_refs, block_table, copy_src, copy_dst, n_moves, dev_err, stream=None):
     """Renames the pages in use to the front of the pool; kvq_pages_copy(caches, copy_src, copy_dst,
     count=n_moves) then moves them. copy_src, copy_dst: int32, at least num_pages // 2 entries."""
-    import torch
-    a = _pool_args(page_refs, block_table, (("n_moves", n_moves),))
-    _need(n_moves.shape[0] == 1, "n_moves holds one number")
-    for name, t in (("copy_src", copy_src), ("copy_dst", copy_dst)):
-        _is(t, torch.int32, (None,), name)
-        _need(t.shape[0] >= page_refs.shape[0] // 2, f"{name} must hold num_pages // 2 entries")
-    _check("kvq_pages_compact", lib.kvq_pages_compact(*a[:5], _ptr(copy_src), _ptr(copy_dst), _ptr(n_moves),
-                                                      _ptr(dev_err), _stream(stream)))
+    pool, i32 = _pool(page_refs, block_table), _th.int32
+    src, dst = _is(copy_src, i32, copy_src.shape, "copy_src"), _is(copy_dst, i32, copy_dst.shape, "copy_dst")
+    _need(min(copy_src.numel(), copy_dst.numel()) >= page_refs.shape[0] // 2,
+          "copy_src and copy_dst must hold num_pages // 2 entries")
+    status = lib.kvq_pages_compact(*pool, src, dst, _is(n_moves, i32, (1,), "n_moves"), dev_err.data_ptr(),
+                                   _here(page_refs, stream))
+    if status:
+        raise KvqError("kvq_pages_compact", status)
 
 
 def kvq_pages_copy(caches, src, dst, dev_err, count=None, stream=None):
     """Copies page src[i] to page dst[i] in every one of the layers `caches` (pairs with -1 are passed
     over), for i < n or i < count (a device int32 tensor of one entry)."""
-    import torch
-    n = src.shape[0]
-    _is(src, torch.int32, (n,), "src")
-    _is(dst, torch.int32, (n,), "dst")
-    if count is not None:
-        _is(count, torch.int32, (1,), "count")
-    _check("kvq_pages_copy", lib.kvq_pages_copy((Int4Cache * len(caches))(*caches), len(caches), n, _ptr(src),
-                                                _ptr(dst), _ptr(count), _ptr(dev_err), _stream(stream)))
+    i32, n = _torch().int32, src.shape[0]
+    status = lib.kvq_pages_copy(_layers(caches), len(caches), n, _is(src, i32, (n,), "src"), _is(dst, i32, (n,), "dst"),
+                                None if count is None else _is(count, i32, (1,), "count"), dev_err.data_ptr(),
+                                _here(src, stream))
+    if status:
+        raise KvqError("kvq_pages_copy", status)
