@@ -64,6 +64,7 @@ struct TreeParams {
   int nst;      // copy stages
   float2* ml;   // partials: base and sum of each row, [2 CTAs][rows]
   float* acc;   // and its 128 sums
+  int* pre;     // blocks of the sequences before each, [B + 1]
   int prow;     // rows of a partial slot: 128 or 256
 };
 
@@ -211,17 +212,31 @@ __device__ __forceinline__ uint32_t tile_offset(int r, int w) { return (w >> 3) 
 // One token's K record -> its row of the K tile. Word w holds dims 8w..8w+7 in the order 0, 4, 1, 5, 2, 6, 3,
 // 7 (as the nibbles pair up in 32 bits; Q' takes the same). A code is the subnormal c 2^-24 (even nibbles)
 // or c 2^-20 (odd ones): one exact product by 2^15, then c s + o rounded once.
+// dst(c, i): address of word 4 c + i of the token's row.
+struct RowWords {
+  uint8_t* row;   // the row in the first half
+  uint32_t off[4];  // 16 (i ^ low bits of the row)
+  uint32_t hi;      // 64 where bit 2 of the row is set
+  __device__ __forceinline__ RowWords(uint8_t* tile, int r) : row(tile + r * 128), hi((uint32_t)(r & 4) << 4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) off[i] = 16u * (uint32_t)(i ^ (r & 3));
+  }
+  __device__ __forceinline__ uint8_t* chunk(int c) const { return row + (c >> 1) * kHalf + (((uint32_t)(c & 1) << 6) ^ hi); }
+};
+
 __device__ __forceinline__ void convert_k4(const uint8_t* rec, int slot, uint32_t meta, uint8_t* tile, int row) {
   const int sw = k_chunk_swz(slot);
   const uint32_t up = 0x78007800u;  // 2^15
   const float s = half_lo(meta);
   const uint32_t s0 = both(s * 512.0f), s1 = both(s * 32.0f), oo = both(half_hi(meta));
   // a loop, not unrolled: the roles of the CTA together are more code than the instruction caches hold
+  const RowWords dst(tile, row);
   uint4 r = *reinterpret_cast<const uint4*>(rec + 16 * sw);
 #pragma unroll 1
   for (int c = 0; c < 4; ++c) {
     const uint4 next = *reinterpret_cast<const uint4*>(rec + 16 * (((c + 1) & 3) ^ sw));
     const uint32_t wd[4] = {r.x, r.y, r.z, r.w};
+    uint8_t* const out_c = dst.chunk(c);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       uint32_t h[4];
@@ -231,7 +246,7 @@ __device__ __forceinline__ void convert_k4(const uint8_t* rec, int slot, uint32_
       out.y = hfma2(hmul2(h[1], up), s1, oo);
       out.z = hfma2(hmul2(h[2], up), s0, oo);
       out.w = hfma2(hmul2(h[3], up), s1, oo);
-      *reinterpret_cast<uint4*>(tile + tile_offset(row, 4 * c + i)) = out;
+      *reinterpret_cast<uint4*>(out_c + dst.off[i]) = out;
     }
     r = next;
   }
@@ -251,11 +266,13 @@ __device__ __forceinline__ void convert_v4_as(const uint8_t* rec, int slot, uint
 #pragma unroll
   for (int e = 0; e < 4; ++e) sc[e] = both(s * mul[e]);
   const uint32_t oo = both(o);
+  const RowWords dst(tile, row);
   uint4 r = *reinterpret_cast<const uint4*>(rec + 16 * sw);
 #pragma unroll 1
   for (int c = 0; c < 4; ++c) {
     const uint4 next = *reinterpret_cast<const uint4*>(rec + 16 * (((c + 1) & 3) ^ sw));
     const uint32_t wd[4] = {r.x, r.y, r.z, r.w};
+    uint8_t* const out_c = dst.chunk(c);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       uint32_t h[4];
@@ -266,7 +283,7 @@ __device__ __forceinline__ void convert_v4_as(const uint8_t* rec, int slot, uint
         if (WIDE) h[e] = pack_f16x2_sat(fmaf(half_lo(h[e]), s * mul[e], o), fmaf(half_hi(h[e]), s * mul[e], o));
         else h[e] = hfma2(h[e], sc[e], oo);
       }
-      *reinterpret_cast<uint4*>(tile + tile_offset(row, 4 * c + i)) = make_uint4(h[0], h[1], h[2], h[3]);
+      *reinterpret_cast<uint4*>(out_c + dst.off[i]) = make_uint4(h[0], h[1], h[2], h[3]);
     }
     r = next;
   }
@@ -313,22 +330,6 @@ __device__ __forceinline__ constexpr int col_of(int d) {
   return FMT == 0 ? 2 * (d & 3) + (d >> 2) : d;
 }
 
-// Stores 8 dims of a row (columns col .. col + 7 of the tile in v) times f.
-template <int FMT>
-__device__ __forceinline__ void store8(void* out, bool bf16, size_t at, const float* v, float f) {
-  float x[8];
-#pragma unroll
-  for (int d = 0; d < 8; ++d) x[d] = v[col_of<FMT>(d)] * f;
-  if (bf16) {
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at) =
-        make_uint4(pack16x2<false>(x[0], x[1]), pack16x2<false>(x[2], x[3]), pack16x2<false>(x[4], x[5]), pack16x2<false>(x[6], x[7]));
-  } else {
-    float4* d = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
-    d[0] = make_float4(x[0], x[1], x[2], x[3]);
-    d[1] = make_float4(x[4], x[5], x[6], x[7]);
-  }
-}
-
 // Output row (of [B][N][Hq]) of row r of KV head h.
 __device__ __forceinline__ size_t out_row(const TreeParams& p, int b, int h, int r) {
   return ((size_t)b * p.j.N + r / p.G) * p.j.Hq + h * p.G + r % p.G;
@@ -358,10 +359,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   static_assert(sizeof(Piece) <= 64, "pieces larger than their shared-memory region");
   volatile int* valid = reinterpret_cast<volatile int*>(smem + L.valid);    // [stage] the page was copied
   volatile int* bvalid = reinterpret_cast<volatile int*>(smem + L.bvalid);  // [block % 4][page] it exists in the pool
-  // [2][128] base and sum, joining streams: over Q', which no product reads any more by then (all score
-  // products of a piece are issued before its last two weighted sums, and a stream that had none leaves
-  // the region alone until the barrier)
-  float2* mlx = reinterpret_cast<float2*>(smem + L.q);
   volatile int* failed = reinterpret_cast<volatile int*>(smem + L.state);
   uint32_t* taddr = reinterpret_cast<uint32_t*>(smem + L.state + 4);
   int* pre = reinterpret_cast<int*>(smem + L.pre);
@@ -390,7 +387,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   fence_barrier_init();
   griddep_wait();
   griddep_launch_dependents();
-  if (warp == 0) build_pre(j, pre, blockIdx.x == 0);
+  if (warp == 0) {
+    build_pre(j, pre, blockIdx.x == 0);
+    if (blockIdx.x == 0)  // for tree_combine_kernel
+      for (int b = lane; b <= j.B; b += 32) p.pre[b] = pre[b];
+  }
   if (warp == 17) tmem_alloc_512(taddr);
   tc_fence_before();
   __syncthreads();
@@ -431,6 +432,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       // ------------------------------------------------------------ copies
       const uint64_t pol = policy_evict_first();
       int issued = 0;  // pages so far
+      int st = 0;      // stage of the next page
+      uint32_t eph = 1;  // phase of its release (first round: none to wait for)
       bool ok = true;
       for (int k = 0; ok; ++k) {
         if (!__all_sync(0xffffffffu, piece_at(k))) break;
@@ -453,8 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           for (int i = 0; i < n; ++i) {
             const uint8_t* s = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), i));
             if (lane == 0 && ok) {
-              const int st = issued % p.nst, round = issued / p.nst;
-              ok = round == 0 || role_wait(raw_empty + st, (uint32_t)(round - 1) & 1u, failed);
+              ok = issued < p.nst || role_wait(raw_empty + st, eph, failed);
               if (ok) {
                 valid[st] = s != nullptr;
                 if (s) {
@@ -464,6 +466,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                   mbar_arrive(raw_full + st);
                 }
                 ++issued;
+                if (++st == p.nst) {
+                  st = 0;
+                  eph ^= 1u;
+                }
               }
             }
           }
@@ -564,7 +570,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     const int tok = threadIdx.x & 127, half = tok >> 6, slot = tok & 63;
     uint64_t* ready = is_v ? v_ready : k_ready;
     uint64_t* freed = is_v ? v_free : k_free;
-    int cnt = 0, pages = 0;  // blocks and pages so far
+    int cnt = 0;         // blocks so far
+    int st0 = 0;         // stage and phase of the block's first page
+    uint32_t sph0 = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
       if (!__all_sync(0xffffffffu, piece_at(k))) break;
@@ -577,11 +585,16 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         const int pg = p0 + 2 * jb, have = min(2, p1 - pg);  // pages of the block
         const int cb = cnt & 1;
         uint8_t* tile = smem + (is_v ? L.v : L.k) + cb * kTileBytes;
-        const int st = (pages + half) % p.nst;
+        int st = st0 + half;
+        uint32_t sph = sph0;
+        while (st >= p.nst) {
+          st -= p.nst;
+          sph ^= 1u;
+        }
         const uint8_t* raw = smem + L.raw + st * stage_bytes(FMT) + (is_v ? kPage * (FMT == 0 ? kRec4 : kRec8) : 0);
         bool use = half < have;
         if (use) {
-          ok = __all_sync(0xffffffffu, role_wait(raw_full + st, (uint32_t)((pages + half) / p.nst) & 1u, failed));
+          ok = __all_sync(0xffffffffu, role_wait(raw_full + st, sph, failed));
           use = valid[st] != 0;
           if (slot == 0 && !is_v) bvalid[2 * (cnt & 3) + half] = use;
         }
@@ -604,7 +617,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           mbar_arrive(ready + cb);
           if (half < have) mbar_arrive(raw_empty + st);
         }
-        pages += have;
+        st0 += have;
+        while (st0 >= p.nst) {
+          st0 -= p.nst;
+          sph0 ^= 1u;
+        }
       }
     }
   } else {
@@ -625,31 +642,37 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         const int tile = pc.w == 2 ? t : 0;
         const int nthr = pc.w == 2 ? 128 : 256, me = pc.w == 2 ? r : (int)threadIdx.x;
         const int r0 = pc.g * kGroup + tile * pc.rows0, nr = tile ? pc.rows - pc.rows0 : pc.rows0;
-        for (int e = me; e < 128 * 16; e += nthr) {
-          const int row = e >> 4, w = e & 15;
-          uint4 o = make_uint4(0u, 0u, 0u, 0u);
-          if (row < nr) {
-            const size_t src = out_row(p, pc.b, pc.h, r0 + row) * kD + 8 * w;
-            float x[8];
-            if (FMT == 1 && j.q_bf16) {
-              const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(j.q) + src);
-              const uint32_t ww[4] = {u.x, u.y, u.z, u.w};
+        // four words of 8 dims a thread in flight
+        for (int e0 = me; e0 < 128 * 16; e0 += 4 * nthr) {
+          uint4 in[4][2];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                x[2 * i] = bf16_bits_to_f32(ww[i] & 0xFFFFu);
-                x[2 * i + 1] = bf16_bits_to_f32(ww[i] >> 16);
+          for (int u = 0; u < 4; ++u) {
+            const int e = e0 + u * nthr, row = e >> 4, w = e & 15;
+            in[u][0] = in[u][1] = make_uint4(0u, 0u, 0u, 0u);
+            if (row < nr) {
+              const size_t src = out_row(p, pc.b, pc.h, r0 + row) * kD + 8 * w;
+              if (FMT == 1 && j.q_bf16) {
+                in[u][0] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(j.q) + src);
+              } else {
+                const uint4* q4 = reinterpret_cast<const uint4*>((FMT == 0 ? j.q_rot : static_cast<const float*>(j.q)) + src);
+                in[u][0] = q4[0];
+                in[u][1] = q4[1];
               }
-            } else {
-              const float4* q4 = reinterpret_cast<const float4*>((FMT == 0 ? j.q_rot : static_cast<const float*>(j.q)) + src);
-              const float4 a = q4[0], b4 = q4[1];
-              x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b4.x, x[5] = b4.y, x[6] = b4.z, x[7] = b4.w;
             }
+          }
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int e = e0 + u * nthr, row = e >> 4, w = e & 15;
+            const uint32_t ww[8] = {in[u][0].x, in[u][0].y, in[u][0].z, in[u][0].w, in[u][1].x, in[u][1].y, in[u][1].z, in[u][1].w};
             float y[8];
 #pragma unroll
-            for (int d = 0; d < 8; ++d) y[col_of<FMT>(d)] = x[d] * p.qmul;
-            o = make_uint4(pack_f16x2_sat(y[0], y[1]), pack_f16x2_sat(y[2], y[3]), pack_f16x2_sat(y[4], y[5]), pack_f16x2_sat(y[6], y[7]));
+            for (int d = 0; d < 8; ++d) {
+              const float x = FMT == 1 && j.q_bf16 ? bf16_bits_to_f32(d & 1 ? ww[d >> 1] >> 16 : ww[d >> 1] & 0xFFFFu) : __uint_as_float(ww[d]);
+              y[col_of<FMT>(d)] = x * p.qmul;
+            }
+            *reinterpret_cast<uint4*>(smem + L.q + tile * kTileBytes + tile_offset(row, w)) =
+                make_uint4(pack_f16x2_sat(y[0], y[1]), pack_f16x2_sat(y[2], y[3]), pack_f16x2_sat(y[4], y[5]), pack_f16x2_sat(y[6], y[7]));
           }
-          *reinterpret_cast<uint4*>(smem + L.q + tile * kTileBytes + tile_offset(row, w)) = o;
         }
         fence_proxy_async_shared();
         __syncwarp();
@@ -769,57 +792,95 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       // the dims. A warp that gave up takes all eight with it, so that none waits here for another.
       const bool join = pc.w == 1;
       const bool two = join && pc.j1 - pc.j0 > 1;  // the second stream had blocks
-      if (join && ok && jfirst < pc.j1) mlx[t * 128 + r] = make_float2(base, l);
+      if (join && ok) {  // base and sum for the other stream's warps, in the first columns of S (read by now)
+        const float bl[4] = {base, l, 0.0f, 0.0f};
+        tmem_st4(ts, bl);
+        tmem_wait_st();
+      }
       tc_fence_before();
       if (named_barrier_or(1, 256, !ok)) {
         ok = false;
         break;
       }
-      float a0 = t == 0 ? 1.0f : 0.0f, a1 = 1.0f - a0;
+      float a0 = 1.0f, a1 = 0.0f;
       int c0 = 0, c1 = 128;
       if (join) {
-        const float2 m0 = mlx[r], m1 = two ? mlx[128 + r] : make_float2(-INFINITY, 0.0f);
-        base = fmaxf(m0.x, m1.x);
-        a0 = m0.x == -INFINITY ? 0.0f : fast_exp2(m0.x - base);
-        a1 = m1.x == -INFINITY ? 0.0f : fast_exp2(m1.x - base);
-        l = m0.y * a0 + m1.y * a1;
-        if (m0.y != m0.y || m1.y != m1.y) l = m0.y + m1.y;  // NaN
+        tc_fence_after();
+        float other[4];
+        tmem_ld4(tmem + lane_base + kColS + 128 * (1 - t), other);
+        tmem_wait_ld();
+        const float b0 = t == 0 ? base : other[0], b1 = t == 0 ? other[0] : base;
+        const float l0 = t == 0 ? l : other[1], l1 = t == 0 ? other[1] : l;
+        base = fmaxf(b0, b1);
+        a0 = b0 == -INFINITY ? 0.0f : fast_exp2(b0 - base);
+        a1 = b1 == -INFINITY ? 0.0f : fast_exp2(b1 - base);
+        l = l0 * a0 + l1 * a1;
+        if (l0 != l0 || l1 != l1) l = l0 + l1;  // NaN
         c0 = 64 * t;
         c1 = c0 + 64;
       }
       tc_fence_after();
       const bool whole = pc.whole != 0;
       const float f = whole ? (l > 0.0f || l != l ? p.vmul / l : 0.0f) : 1.0f;
-      const size_t row = mine ? out_row(p, pc.b, pc.h, grow) : 0;
       const size_t slot = (size_t)pc.slot + (join ? r : t * 128 + r);
       if (!whole && mine && (!join || t == 0)) p.ml[slot] = make_float2(base, l);
       const uint32_t to = tmem + lane_base + kColO;
       if (warp_rows) {
+        // 32 rows x 32 dims at a time through 4 KB of Q' (no product reads it any more: all score products of a
+        // piece are issued before the last weighted sum of either stream), so that 8 lanes write 32 dims of a row
+        uint8_t* stage = smem + L.q + (pc.w == 2 ? t * kTileBytes + (warp & 3) * 4096 : warp * 4096);
+        const int rbase = grow - lane;  // the warp's first row
+        const int have = min(32, nr - (r & ~31));
+        const int lr = lane >> 3, lc = lane & 7;
 #pragma unroll 1
-        for (int cc = c0; cc < c1; cc += 16) {
-          uint32_t x[16], y[16];
-          tmem_ld16u(to + cc + (join ? 0 : 128 * t), x);
-          if (two) tmem_ld16u(to + cc + 128, y);
+        for (int cc = c0; cc < c1; cc += 32) {
+          uint32_t x[32];
+          tmem_ld32u(to + cc + (join ? 0 : 128 * t), x);
           tmem_wait_ld_all();
-          float v[16];
+          float v[32];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            v[i] = __uint_as_float(x[i]);
-            if (join) v[i] *= a0;
-            if (two) v[i] = fmaf(__uint_as_float(y[i]), a1, v[i]);
-            if (l == 0.0f) v[i] = 0.0f;  // nothing seen: O holds 0, or (no product yet) anything
+          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(x[i]) * a0;
+          if (two) {
+            tmem_ld32u(to + cc + 128, x);
+            tmem_wait_ld_all();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = fmaf(__uint_as_float(x[i]), a1, v[i]);
           }
-          if (mine) {
+          if (l == 0.0f) {  // nothing seen: O holds 0, or (no product yet) anything
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              if (whole) store8<FMT>(j.out, j.out_bf16, row * kD + cc + 8 * i, v + 8 * i, f);
-              else store8<FMT>(p.acc, false, slot * kD + cc + 8 * i, v + 8 * i, 1.0f);
+            for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float4 o;  // dims 4 i .. 4 i + 3 of the 32
+            const int g8 = 8 * (i >> 1), d = 4 * (i & 1);
+            o.x = v[g8 + col_of<FMT>(d)] * f;
+            o.y = v[g8 + col_of<FMT>(d + 1)] * f;
+            o.z = v[g8 + col_of<FMT>(d + 2)] * f;
+            o.w = v[g8 + col_of<FMT>(d + 3)] * f;
+            *reinterpret_cast<float4*>(stage + lane * 128 + 16 * (i ^ (lane & 7))) = o;
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int rr = 4 * i + lr;
+            if (rr < have) {
+              const float4 o = *reinterpret_cast<const float4*>(stage + rr * 128 + 16 * (lc ^ (rr & 7)));
+              const int dim = cc + 4 * lc;
+              if (!whole) {
+                *reinterpret_cast<float4*>(p.acc + ((size_t)pc.slot + (join ? 0 : t * 128) + (r & ~31) + rr) * kD + dim) = o;
+              } else {
+                const size_t at = out_row(p, pc.b, pc.h, rbase + rr) * kD + dim;
+                if (j.out_bf16) *reinterpret_cast<uint2*>(static_cast<uint16_t*>(j.out) + at) = make_uint2(pack16x2<false>(o.x, o.y), pack16x2<false>(o.z, o.w));
+                else *reinterpret_cast<float4*>(static_cast<float*>(j.out) + at) = o;
+              }
             }
           }
         }
       }
       tc_fence_before();
-      if (join) named_barrier(1, 256);  // both have read both streams' O, and mlx
+      if (join) named_barrier(1, 256);  // both have read both streams' O, bases and sums
       __syncwarp();
       if (lane == 0) mbar_arrive(piece_empty + (k & 1));
     }
@@ -832,51 +893,56 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   if (threadIdx.x == 0 && *failed) set_err(j.dev_err, KVQ_DEVERR_TIMEOUT);
 }
 
-// Joins the partials of the segments that several CTAs shared: one warp per row, four dims a lane, in
-// the order of the CTAs.
+// Joins the partials of the segments that several CTAs shared, in the order of the CTAs: one block per
+// segment and 8 rows of it, one warp per row, four dims a lane. A first pass (a lane per partial) takes
+// the bases and sums, so that the second has its factors ready and its loads are independent.
 constexpr int kCombineWarps = 8;
 template <int FMT>
 __global__ void __launch_bounds__(kCombineWarps * 32) tree_combine_kernel(const __grid_constant__ TreeParams p, int ctas) {
-  extern __shared__ int pre_s[];
   const TreeJob& j = p.j;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int seg = blockIdx.x, g = seg % p.ng, h = seg / p.ng % j.Hkv, b = seg / p.ng / j.Hkv;
+  const int rows = group_rows(p, g), w = g < p.ng - 1 ? 2 : p.w_last;
+  const int rr = blockIdx.y * kCombineWarps + warp;
+  if (rr >= rows) return;
   griddep_wait();
   griddep_launch_dependents();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (warp == 0) build_pre(j, pre_s, false);
-  __syncthreads();
-  const Split sp(p, pre_s, ctas);
-  const long long items = (long long)j.B * j.Hkv * p.R;
-  for (long long e = (long long)blockIdx.x * kCombineWarps + warp; e < items; e += (long long)gridDim.x * kCombineWarps) {
-    const int rr = (int)(e % p.R), h = (int)(e / p.R % j.Hkv), b = (int)(e / p.R / j.Hkv);
-    const int g = rr / kGroup, w = g < p.ng - 1 ? 2 : p.w_last, nb = pre_s[b + 1] - pre_s[b];
-    const long long xs = (long long)pre_s[b] * sp.per_seq + (long long)h * nb * (sp.per_seq / j.Hkv) + 2LL * g * nb;
-    const int ca = sp.owner(xs), cb = sp.owner(xs + (long long)(nb - 1) * w);
-    if (ca == cb) continue;
-    const int rows0 = tile0_rows(group_rows(p, g), w);
-    int r = rr - g * kGroup;
-    if (w == 2 && r >= rows0) r += 128 - rows0;
-    // the segment's first block is its CTA's first one unless the block before it lies there as well
-    const long long before = xs - (g > 0 ? 2 : p.w_last);
-    float m = -INFINITY, l = 0.0f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = ca; c <= cb; ++c) {
-      const bool last = c == ca && xs > 0 && before >= sp.X(ca);
-      const size_t slot = (size_t)(2 * c + (last ? 1 : 0)) * p.prow + r;
-      const float2 ml = p.ml[slot];
-      const float4 a = reinterpret_cast<const float4*>(p.acc + slot * kD)[lane];
-      const float mn = fmaxf(m, ml.x);
-      const float f0 = m == -INFINITY ? 0.0f : exp2f(m - mn), f1 = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - mn);
-      l = l * f0 + (ml.y != ml.y ? ml.y : ml.y * f1);
-      o.x = o.x * f0 + a.x * f1, o.y = o.y * f0 + a.y * f1, o.z = o.z * f0 + a.z * f1, o.w = o.w * f0 + a.w * f1;
-      m = mn;
+  const Split sp(p, p.pre, ctas);
+  const int pb = p.pre[b], nb = p.pre[b + 1] - pb;
+  const long long xs = (long long)pb * sp.per_seq + (long long)h * nb * (sp.per_seq / j.Hkv) + 2LL * g * nb;
+  const int ca = sp.owner(xs), cb = sp.owner(xs + (long long)(nb - 1) * w);
+  if (ca == cb) return;
+  const int rows0 = tile0_rows(rows, w);
+  const int r = w == 2 && rr >= rows0 ? rr + 128 - rows0 : rr;
+  // the segment's first block is its CTA's first one unless the block before it lies there as well
+  const bool second = xs > 0 && xs - (g > 0 ? 2 : p.w_last) >= sp.X(ca);
+  auto slot = [&](int c) { return (size_t)(2 * c + (c == ca && second ? 1 : 0)) * p.prow + r; };
+  float m = -INFINITY, l = 0.0f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c0 = ca; c0 <= cb; c0 += 32) {
+    const int n = min(32, cb - c0 + 1);
+    const float2 ml = lane < n ? p.ml[slot(c0 + lane)] : make_float2(-INFINITY, 0.0f);
+    const float mn = fmaxf(m, warp_max_all(ml.x));
+    const float f0 = m == -INFINITY ? 0.0f : exp2f(m - mn), f1 = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - mn);
+    float part = ml.y != ml.y ? ml.y : ml.y * f1;
+#pragma unroll
+    for (int s = 16; s >= 1; s >>= 1) part += __shfl_xor_sync(0xffffffffu, part, s);
+    l = l * f0 + part;
+    o.x *= f0, o.y *= f0, o.z *= f0, o.w *= f0;
+    m = mn;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const float f = __shfl_sync(0xffffffffu, f1, i);
+      const float4 a = reinterpret_cast<const float4*>(p.acc + slot(c0 + i) * kD)[lane];
+      o.x = fmaf(a.x, f, o.x), o.y = fmaf(a.y, f, o.y), o.z = fmaf(a.z, f, o.z), o.w = fmaf(a.w, f, o.w);
     }
-    const float f = l > 0.0f || l != l ? p.vmul / l : 0.0f;
-    const size_t at = out_row(p, b, h, rr) * kD + 4 * lane;
-    if (j.out_bf16)
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(j.out) + at) = make_uint2(pack16x2<false>(o.x * f, o.y * f), pack16x2<false>(o.z * f, o.w * f));
-    else
-      *reinterpret_cast<float4*>(static_cast<float*>(j.out) + at) = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
   }
+  const float f = l > 0.0f || l != l ? p.vmul / l : 0.0f;
+  const size_t at = out_row(p, b, h, g * kGroup + rr) * kD + 4 * lane;
+  if (j.out_bf16)
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(j.out) + at) = make_uint2(pack16x2<false>(o.x * f, o.y * f), pack16x2<false>(o.z * f, o.w * f));
+  else
+    *reinterpret_cast<float4*>(static_cast<float*>(j.out) + at) = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
 }
 
 std::mutex g_mu;  // guards the cache below
@@ -915,17 +981,16 @@ cudaError_t launch_t(TreeParams& p, long long blocks_max, cudaStream_t stream) {
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, tree_kernel<FMT>, p);
   if (e != cudaSuccess) return e;
-  const long long items = (long long)p.j.B * p.j.Hkv * p.R;
-  cfg.gridDim = dim3((unsigned)std::min<long long>((items + kCombineWarps - 1) / kCombineWarps, 8LL * sms), 1, 1);
+  cfg.gridDim = dim3((unsigned)(p.j.B * p.j.Hkv * p.ng), (unsigned)((std::min(p.R, kGroup) + kCombineWarps - 1) / kCombineWarps), 1);
   cfg.blockDim = dim3(kCombineWarps * 32, 1, 1);
-  cfg.dynamicSmemBytes = 4 * (p.j.B + 1);
+  cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, tree_combine_kernel<FMT>, p, ctas);
 }
 
 }  // namespace
 
 size_t workspace_tree_partials_bytes(int B, int N, int Hq, int Hkv) {
-  return (size_t)2 * kMaxTreeCtas * partial_rows(N, Hq, Hkv) * (2 + kD) * 4;
+  return (size_t)2 * kMaxTreeCtas * partial_rows(N, Hq, Hkv) * (2 + kD) * 4 + 4 * ((size_t)B + 1);
 }
 
 cudaError_t launch_tree(const TreeJob& job, cudaStream_t stream) {
@@ -942,6 +1007,7 @@ cudaError_t launch_tree(const TreeJob& job, cudaStream_t stream) {
   p.prow = partial_rows(job.N, job.Hq, job.Hkv);
   p.ml = reinterpret_cast<float2*>(job.partials);
   p.acc = job.partials + (size_t)2 * 2 * kMaxTreeCtas * p.prow;
+  p.pre = reinterpret_cast<int*>(p.acc + (size_t)2 * kMaxTreeCtas * p.prow * kD);
   const long long pages = job.fmt == 0 ? job.cache.max_pages_per_seq : job.ring.capacity / kPage + 1;
   const long long blocks = (pages + 1) / 2 * job.B * job.Hkv * p.ng;
   return job.fmt == 0 ? launch_t<0>(p, blocks, stream) : launch_t<1>(p, blocks, stream);

@@ -57,16 +57,32 @@ __device__ __forceinline__ uint32_t pack16x2(float lo, float hi) {
   return d;
 }
 
-// Bounded wait for a phase; notes a wait that gave up in *failed. Plain try_wait (the hardware suspends the
-// thread for a while by itself): with a suspend hint the wait becomes a polling loop with sleeps, which
-// costs the other warps issue slots and the hand-over latency (tree kernel, 64 x 16,384 tokens x 16 drafted:
-// half of the instructions executed were polls).
+// Up to `tries` try_waits (each suspended by the hardware for a while) in the shortest loop there is:
+// waiting warps share their scheduler with working ones.
+__device__ __forceinline__ bool mbar_try_many(uint64_t* bar, uint32_t parity, uint32_t tries) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\tmov.u32 n, %3;\n"
+      "TRY:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "@p bra DONE;\n\t"
+      "sub.u32 n, n, 1;\n\tsetp.ne.u32 q, n, 0;\n\t@q bra TRY;\n"
+      "DONE:\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity), "r"(tries)
+      : "memory");
+  return ok != 0;
+}
+
+// Bounded wait for a phase; notes a wait that gave up in *failed. (With a suspend hint try_wait becomes a
+// polling loop with sleeps, which costs the other warps issue slots and the hand-over latency.)
 __device__ __forceinline__ bool role_wait(uint64_t* bar, uint32_t parity, volatile int* failed) {
-  if (mbar_try_wait(bar, parity)) return true;
+  if (mbar_try_many(bar, parity, 4096)) return true;
   const uint64_t t0 = globaltimer();
-  for (uint32_t it = 1; it < (1u << 30); ++it) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((it & 63u) == 0 && globaltimer() - t0 > kWaitLimitNs) break;
+  for (uint32_t it = 0; it < (1u << 20); ++it) {
+    if (mbar_try_many(bar, parity, 1024)) return true;
+    if (globaltimer() - t0 > kWaitLimitNs) break;
   }
   *failed = 1;
   return false;
