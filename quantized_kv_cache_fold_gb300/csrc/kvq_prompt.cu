@@ -69,7 +69,7 @@ struct Smem {
   uint64_t q_full, q_empty;
   uint64_t kv_full[kRing], kv_empty[kRing];
   uint64_t v_ok[kRing / 2];
-  uint64_t s_full[2], p_ready[2], o_full[2];
+  uint64_t s_full[2], p_half[2], p_ready[2], o_full[2];
   uint64_t item_full[2], item_empty[2];
   uint64_t fin;
   Item item[2];
@@ -192,6 +192,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.v_ok[i], 1);
       mbar_init(&sm.s_full[i], 1);
+      mbar_init(&sm.p_half[i], 4);
       mbar_init(&sm.p_ready[i], 4);
       mbar_init(&sm.o_full[i], 1);
       mbar_init(&sm.item_full[i], 1);
@@ -284,69 +285,84 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         if (nq > 0) mbar_wait_bounded(&sm.q_full, (uint32_t)(nq - 1) & 1u);
         for (int u = max(0, used - kRing); u < used; ++u) mbar_wait_bounded(&sm.kv_full[u % kRing], (uint32_t)(u / kRing) & 1u);
       }
-    } else if (warp == 9 && lane == 0) {
+    } else if (warp == 9) {
       // ------------------------------------------------------------ products
       constexpr uint32_t kIdQK = umma_idesc_16(F16, kRows, false), kIdPV = umma_idesc_16(F16, kD, true);
-      const uint64_t dq[2] = {umma_sdesc(smem_addr(sm.q[0]), 16, 1024), umma_sdesc(smem_addr(sm.q[1]), 16, 1024)};
+      const uint32_t leader = elect_one();
+      const uint32_t tm = (uint32_t)uniform((int)tmem);
+      const uint64_t dq0 = umma_sdesc(smem_addr(sm.q[0]), 16, 1024);
       const uint64_t dk0 = umma_sdesc(smem_addr(sm.kv[0]), 16, 1024);
       const uint64_t dv0 = umma_sdesc(smem_addr(sm.kv[0]), kTileBytes / 2, 1024);
       bool ok = true;
-      int kv = 0;                  // ring uses before the item: K of its block i is use kv + 2 i, V the next
-      uint32_t pph[2] = {0, 0};    // phase of p_ready
+      int kv = 0;          // ring uses before the item: K of its block i is use kv + 2 i, V the next
+      uint32_t pph0 = 0, pph1 = 0;  // phases of p_half and p_ready, tile 0 and 1
+      auto wait = [&](uint64_t* bar, uint32_t ph) { return __all_sync(0xffffffffu, role_wait(bar, ph, failed)) != 0; };
+      auto full = [&](int use) { return wait(&sm.kv_full[use % kRing], (uint32_t)(use / kRing) & 1u); };
       auto qk = [&](int t, int slot) {
+        const uint64_t q = dq0 + (uint64_t)(t * (kTileBytes >> 4)), kb = dk0 + (uint64_t)(slot * (kTileBytes >> 4));
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) {  // 16 dims each: 32 bytes within a 64-dim half
           const uint64_t off = (uint64_t)(((kk >> 2) * (kTileBytes / 2) + (kk & 3) * 32) >> 4);
-          umma_f16(tmem + kColS + 128 * t, dq[t] + off, dk0 + (uint64_t)(slot * (kTileBytes >> 4)) + off, kIdQK, kk > 0);
+          umma_f16_by(leader, tm + kColS + 128 * t, q + off, kb + off, kIdQK, kk > 0);
         }
-        umma_commit(&sm.s_full[t]);
+        umma_commit_by(leader, &sm.s_full[t]);
+      };
+      // 16 tokens a step: 2048 bytes of a half of V, 8 columns of P
+      auto pv = [&](int t, int slot, int half, uint32_t acc) {
+        const uint64_t v = dv0 + (uint64_t)(slot * (kTileBytes >> 4));
+#pragma unroll
+        for (int k4 = 0; k4 < 4; ++k4) {
+          const int kk = 4 * half + k4;
+          umma_f16_ts_by(leader, tm + kColO + 128 * t, tm + kColS + 128 * t + 8 * kk, v + (uint64_t)(kk * (2048 >> 4)), kIdPV, k4 > 0 ? 1u : acc);
+        }
       };
       for (int k = 0; ok; ++k) {
-        if (!(ok = role_wait(&sm.item_full[k & 1], (uint32_t)(k / 2) & 1u, failed))) break;
-        const Item it = sm.item[k & 1];
-        mbar_arrive(&sm.item_empty[k & 1]);
+        if (!(ok = wait(&sm.item_full[k & 1], (uint32_t)(k / 2) & 1u))) break;
+        Item it = sm.item[k & 1];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.item_empty[k & 1]);
+        it.n = uniform(it.n);
+        it.r0 = uniform(it.r0);
         if (it.n < 0) break;
-        const Range rg[2] = {Range(it, 0, j.window), Range(it, 1, j.window)};
-        const int jb = rg[0].jb, je = max(rg[0].je, rg[1].je);
-        auto active = [&](int t, int b) { return b >= rg[t].jb && b < rg[t].je; };
-        auto full = [&](int use) { return role_wait(&sm.kv_full[use % kRing], (uint32_t)(use / kRing) & 1u, failed); };
-        ok = role_wait(&sm.q_full, (uint32_t)k & 1u, failed) && full(kv);
+        const Range r0(it, 0, j.window), r1(it, 1, j.window);
+        const int jb = r0.jb, je = max(r0.je, r1.je);
+        ok = wait(&sm.q_full, (uint32_t)k & 1u) && full(kv);
         if (!ok) break;
         tc_fence_after();
-        for (int t = 0; t < 2; ++t)
-          if (active(t, jb)) qk(t, kv % kRing);
-        umma_commit(&sm.kv_empty[kv % kRing]);
-        if (je == jb + 1) umma_commit(&sm.q_empty);
+        qk(0, kv % kRing);
+        if (r1.je > 0 && r1.jb == jb) qk(1, kv % kRing);
+        umma_commit_by(leader, &sm.kv_empty[kv % kRing]);
+        if (je == jb + 1) umma_commit_by(leader, &sm.q_empty);
         for (int b = jb; ok && b < je; ++b) {
-          const int uv = kv + 2 * (b - jb) + 1, uk = uv + 1;
-          ok = full(uv) && role_wait(&sm.v_ok[(uv % kRing) >> 1], (uint32_t)(uv / kRing) & 1u, failed);
-          if (ok && b + 1 < je) ok = full(uk);
-          for (int t = 0; ok && t < 2; ++t) {
-            if (active(t, b)) {
-              ok = role_wait(&sm.p_ready[t], pph[t], failed);
-              if (!ok) break;
-              pph[t] ^= 1u;
-              tc_fence_after();
-              const uint64_t dv = dv0 + (uint64_t)((uv % kRing) * (kTileBytes >> 4));
-              const uint32_t acc = b > rg[t].jb;
+          const int uv = kv + 2 * (b - jb) + 1, sv = uv % kRing, sk = (uv + 1) % kRing;
+          ok = full(uv) && wait(&sm.v_ok[sv >> 1], (uint32_t)(uv / kRing) & 1u);
+          if (ok && b + 1 < je) ok = full(uv + 1);
+          if (!ok) break;
 #pragma unroll
-              for (int kk = 0; kk < 8; ++kk)  // 16 tokens each: 2048 bytes of a half of V, 8 columns of P
-                umma_f16_ts(tmem + kColO + 128 * t, tmem + kColS + 128 * t + 8 * kk, dv + (uint64_t)(kk * (2048 >> 4)), kIdPV, kk > 0 ? 1u : acc);
-              if (b == rg[t].je - 1) umma_commit(&sm.o_full[t]);
-            }
-            if (active(t, b + 1)) {
+          for (int t = 0; t < 2; ++t) {
+            const Range& r = t ? r1 : r0;
+            uint32_t& ph = t ? pph1 : pph0;
+            if (b >= r.jb && b < r.je) {
+              // the first half of the weights may be multiplied while the second is still computed
+              if (!(ok = wait(&sm.p_half[t], ph))) break;
               tc_fence_after();
-              qk(t, uk % kRing);
+              pv(t, sv, 0, b > r.jb);
+              if (!(ok = wait(&sm.p_ready[t], ph))) break;
+              ph ^= 1u;
+              tc_fence_after();
+              pv(t, sv, 1, 1u);
+              if (b == r.je - 1) umma_commit_by(leader, &sm.o_full[t]);
             }
+            if (b + 1 >= r.jb && b + 1 < r.je) qk(t, sk);
           }
           if (!ok) break;
-          umma_commit(&sm.kv_empty[uv % kRing]);
-          if (b + 1 < je) umma_commit(&sm.kv_empty[uk % kRing]);
-          if (b + 2 == je) umma_commit(&sm.q_empty);
+          umma_commit_by(leader, &sm.kv_empty[sv]);
+          if (b + 1 < je) umma_commit_by(leader, &sm.kv_empty[sk]);
+          if (b + 2 == je) umma_commit_by(leader, &sm.q_empty);
         }
         kv += 2 * (je - jb);
       }
-      umma_commit(&sm.fin);  // arrives once every product issued has completed
+      umma_commit_by(leader, &sm.fin);  // arrives once every product issued has completed
       mbar_wait_bounded(&sm.fin, 0);
     } else if (warp == 11) {
       // ------------------------------------------------------------ V check
@@ -469,11 +485,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             pk[i] = pack16x2<F16>(e0, e1);
           }
           tmem_st32u(ts + 32 * h, pk);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(h ? &sm.p_ready[t] : &sm.p_half[t]);
         }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.p_ready[t]);
       }
       if (!ok) break;
       if (rg.je > 0) {

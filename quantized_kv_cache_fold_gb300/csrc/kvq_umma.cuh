@@ -57,33 +57,44 @@ __device__ __forceinline__ uint32_t pack16x2(float lo, float hi) {
   return d;
 }
 
-// Up to `tries` try_waits (each suspended by the hardware for a while) in the shortest loop there is:
-// waiting warps share their scheduler with working ones.
-__device__ __forceinline__ bool mbar_try_many(uint64_t* bar, uint32_t parity, uint32_t tries) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\tmov.u32 n, %3;\n"
-      "TRY:\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "@p bra DONE;\n\t"
-      "sub.u32 n, n, 1;\n\tsetp.ne.u32 q, n, 0;\n\t@q bra TRY;\n"
-      "DONE:\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_addr(bar)), "r"(parity), "r"(tries)
-      : "memory");
-  return ok != 0;
+// The issuing warp of the products stays converged and one elected lane issues: descriptors and addresses are
+// then warp-uniform values, which the instruction takes from uniform registers. (A branch on one lane
+// instead costs moves to uniform registers for each product: 82 cycles to issue one that runs for 64.)
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e;
 }
+__device__ __forceinline__ void umma_f16_by(uint32_t leader, uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, l;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 l, %5, 0;\n\t"
+      "@l tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void umma_f16_ts_by(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem, uint64_t b,
+                                               uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, l;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 l, %5, 0;\n\t"
+      "@l tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void umma_commit_by(uint32_t leader, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred l;\n\tsetp.ne.b32 l, %1, 0;\n\t"
+      "@l tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar)),
+      "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
-// Bounded wait for a phase; notes a wait that gave up in *failed. (With a suspend hint try_wait becomes a
-// polling loop with sleeps, which costs the other warps issue slots and the hand-over latency.)
+// Bounded wait for a phase; notes a wait that gave up in *failed. (mbar_wait_bounded's suspend hint matters:
+// a tight loop of plain try_waits in its place takes the 32,768-token prompt from 4.11 to 4.72 ms and the
+// tree over 64 x 16,384 tokens from 355 to 370 us.)
 __device__ __forceinline__ bool role_wait(uint64_t* bar, uint32_t parity, volatile int* failed) {
-  if (mbar_try_many(bar, parity, 4096)) return true;
-  const uint64_t t0 = globaltimer();
-  for (uint32_t it = 0; it < (1u << 20); ++it) {
-    if (mbar_try_many(bar, parity, 1024)) return true;
-    if (globaltimer() - t0 > kWaitLimitNs) break;
-  }
+  if (mbar_wait_bounded(bar, parity)) return true;
   *failed = 1;
   return false;
 }
