@@ -46,7 +46,7 @@ constexpr int kGroup = 256;                // rows of a segment
 constexpr int kTileBytes = kBlk * kD * 2;  // fp16 tile: two 64-dim halves of 128 rows of 128 bytes
 constexpr int kHalf = kTileBytes / 2;
 constexpr int kThreads = 640;
-constexpr int kRegSoftmax = 144, kRegConv = 64, kRegAux = 64;  // from 96 at launch
+constexpr int kRegSoftmax = 120, kRegConv = 80, kRegAux = 80;  // from 96 at launch
 static_assert(256 * kRegSoftmax + 256 * kRegConv + 128 * kRegAux <= kThreads * 96, "register shares above the launch's allocation");
 constexpr uint32_t kColS = 0, kColO = 256;  // stream t at + 128 t; P over the first 64 columns of S
 constexpr int kMaxTreeCtas = 256;           // sizes the partials
@@ -212,9 +212,9 @@ __device__ __forceinline__ uint32_t tile_offset(int r, int w) { return (w >> 3) 
 // One token's K record -> its row of the K tile. Word w holds dims 8w..8w+7 in the order 0, 4, 1, 5, 2, 6, 3,
 // 7 (as the nibbles pair up in 32 bits; Q' takes the same). A code is the subnormal c 2^-24 (even nibbles)
 // or c 2^-20 (odd ones): one exact product by 2^15, then c s + o rounded once.
-// dst(c, i): address of word 4 c + i of the token's row.
+// Places of a token's words: word 4 c + i at chunk(c) + off[i].
 struct RowWords {
-  uint8_t* row;   // the row in the first half
+  uint8_t* row;
   uint32_t off[4];  // 16 (i ^ low bits of the row)
   uint32_t hi;      // 64 where bit 2 of the row is set
   __device__ __forceinline__ RowWords(uint8_t* tile, int r) : row(tile + r * 128), hi((uint32_t)(r & 4) << 4) {
@@ -232,7 +232,7 @@ __device__ __forceinline__ void convert_k4(const uint8_t* rec, int slot, uint32_
   // a loop, not unrolled: the roles of the CTA together are more code than the instruction caches hold
   const RowWords dst(tile, row);
   uint4 r = *reinterpret_cast<const uint4*>(rec + 16 * sw);
-#pragma unroll 1
+#pragma unroll 2
   for (int c = 0; c < 4; ++c) {
     const uint4 next = *reinterpret_cast<const uint4*>(rec + 16 * (((c + 1) & 3) ^ sw));
     const uint32_t wd[4] = {r.x, r.y, r.z, r.w};
@@ -268,7 +268,7 @@ __device__ __forceinline__ void convert_v4_as(const uint8_t* rec, int slot, uint
   const uint32_t oo = both(o);
   const RowWords dst(tile, row);
   uint4 r = *reinterpret_cast<const uint4*>(rec + 16 * sw);
-#pragma unroll 1
+#pragma unroll 2
   for (int c = 0; c < 4; ++c) {
     const uint4 next = *reinterpret_cast<const uint4*>(rec + 16 * (((c + 1) & 3) ^ sw));
     const uint32_t wd[4] = {r.x, r.y, r.z, r.w};
@@ -298,30 +298,26 @@ __device__ __forceinline__ void convert_v4(const uint8_t* rec, int slot, uint32_
 
 // One token's 128 e4m3 values -> its row of a tile, dims in order.
 __device__ __forceinline__ void convert8(const uint8_t* rec, int slot, uint8_t* tile, int row) {
-#pragma unroll 1
-  for (int c0 = 0; c0 < 8; c0 += 2) {
-    uint4 r[2];
+  uint8_t* dst = tile + row * 128;
+#pragma unroll 2
+  for (int c = 0; c < 8; ++c) {
+    const uint4 r = *reinterpret_cast<const uint4*>(rec + 16 * (c ^ (slot & 7)));
+    const uint32_t wd[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-    for (int c = 0; c < 2; ++c) r[c] = *reinterpret_cast<const uint4*>(rec + 16 * ((c0 + c) ^ (slot & 7)));
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const uint32_t wd[4] = {r[c].x, r[c].y, r[c].z, r[c].w};
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        uint4 out;
-        out.x = e4m3x2_to_f16x2(wd[2 * i]);
-        out.y = e4m3x2_to_f16x2(wd[2 * i] >> 16);
-        out.z = e4m3x2_to_f16x2(wd[2 * i + 1]);
-        out.w = e4m3x2_to_f16x2(wd[2 * i + 1] >> 16);
-        *reinterpret_cast<uint4*>(tile + tile_offset(row, 2 * (c0 + c) + i)) = out;
-      }
+    for (int i = 0; i < 2; ++i) {
+      uint4 out;
+      out.x = e4m3x2_to_f16x2(wd[2 * i]);
+      out.y = e4m3x2_to_f16x2(wd[2 * i] >> 16);
+      out.z = e4m3x2_to_f16x2(wd[2 * i + 1]);
+      out.w = e4m3x2_to_f16x2(wd[2 * i + 1] >> 16);
+      *reinterpret_cast<uint4*>(dst + (c >> 2) * kHalf + 16 * ((2 * (c & 3) + i) ^ (row & 7))) = out;
     }
   }
 }
 
 __device__ __forceinline__ void zero_row(uint8_t* tile, int row) {
 #pragma unroll 1
-  for (int w = 0; w < 16; ++w) *reinterpret_cast<uint4*>(tile + tile_offset(row, w)) = make_uint4(0u, 0u, 0u, 0u);
+  for (int w = 0; w < 16; ++w) *reinterpret_cast<uint4*>(tile + (w >> 3) * kHalf + row * 128 + 16 * (w & 7)) = make_uint4(0u, 0u, 0u, 0u);
 }
 
 // Column of dim d (0..7 of a word) in the tiles, and its inverse order for the output.
@@ -480,96 +476,82 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       }
       if (*failed && lane == 0)  // no copy may be in flight when the CTA ends
         for (int u = max(0, issued - p.nst); u < issued; ++u) mbar_wait_bounded(raw_full + u % p.nst, (uint32_t)(u / p.nst) & 1u);
-    } else if (warp == 17 && lane == 0) {
+    } else if (warp == 17) {
       // ------------------------------------------------------------ products
       constexpr uint32_t kIdQK = umma_idesc_16(true, kBlk, false), kIdPV = umma_idesc_16(true, kD, true);
+      const uint32_t leader = elect_one();
+      const uint32_t tm = (uint32_t)uniform((int)tmem);
       const uint64_t dq = umma_sdesc(smem_addr(smem + L.q), 16, 1024);
       const uint64_t dk = umma_sdesc(smem_addr(smem + L.k), 16, 1024);
       const uint64_t dv = umma_sdesc(smem_addr(smem + L.v), kHalf, 1024);
+      auto wait = [&](uint64_t* bar, uint32_t ph) { return __all_sync(0xffffffffu, role_wait(bar, ph, failed)) != 0; };
+      auto wait2 = [&](uint64_t* bar, int cnt) { return wait(bar + (cnt & 1), (uint32_t)(cnt >> 1) & 1u); };
       auto qk = [&](int t, int qt, int cnt) {
+        const uint64_t q = dq + (uint64_t)(qt * (kTileBytes >> 4)), kb = dk + (uint64_t)((cnt & 1) * (kTileBytes >> 4));
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) {
           const uint64_t off = (uint64_t)(((kk >> 2) * kHalf + (kk & 3) * 32) >> 4);
-          umma_f16(tmem + kColS + 128 * t, dq + (uint64_t)(qt * (kTileBytes >> 4)) + off, dk + (uint64_t)((cnt & 1) * (kTileBytes >> 4)) + off, kIdQK, kk > 0);
+          umma_f16_by(leader, tm + kColS + 128 * t, q + off, kb + off, kIdQK, kk > 0);
         }
-        umma_commit(s_full + t);
+        umma_commit_by(leader, s_full + t);
       };
       auto pv = [&](int t, int cnt, uint32_t acc) {
+        const uint64_t v = dv + (uint64_t)((cnt & 1) * (kTileBytes >> 4));
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
-          umma_f16_ts(tmem + kColO + 128 * t, tmem + kColS + 128 * t + 8 * kk, dv + (uint64_t)(((cnt & 1) * kTileBytes + kk * 2048) >> 4), kIdPV, kk > 0 ? 1u : acc);
+          umma_f16_ts_by(leader, tm + kColO + 128 * t, tm + kColS + 128 * t + 8 * kk, v + (uint64_t)(kk * (2048 >> 4)), kIdPV, kk > 0 ? 1u : acc);
       };
-      auto wait2 = [&](uint64_t* bar, int cnt) { return role_wait(bar + (cnt & 1), (uint32_t)(cnt >> 1) & 1u, failed); };
       bool ok = true;
       int cnt = 0;  // blocks before the piece
-      uint32_t pph[2] = {0u, 0u};
-      for (int k = 0; ok && piece_at(k); ++k) {
-        const int nb = pieces[k & 1].j1 - pieces[k & 1].j0, tiles = pieces[k & 1].w;
-        mbar_arrive(piece_empty + (k & 1));
-        if (!(ok = role_wait(q_ready, (uint32_t)k & 1u, failed))) break;
-        if (tiles == 2) {
-          if (!(ok = wait2(k_ready, cnt))) break;
+      uint32_t pph0 = 0u, pph1 = 0u;
+      for (int k = 0; ok; ++k) {
+        if (!__all_sync(0xffffffffu, piece_at(k))) break;
+        const int nb = uniform(pieces[k & 1].j1 - pieces[k & 1].j0), tiles = uniform(pieces[k & 1].w);
+        if (lane == 0) mbar_arrive(piece_empty + (k & 1));
+        if (!(ok = wait(q_ready, (uint32_t)k & 1u))) break;
+        const int ahead = tiles == 2 ? 1 : 2;  // blocks whose scores are under way while one is multiplied by V
+        for (int i = 0; ok && i < min(ahead, nb); ++i) {
+          if (!(ok = wait2(k_ready, cnt + i))) break;
           tc_fence_after();
-          qk(0, 0, cnt);
-          qk(1, 1, cnt);
-          umma_commit(k_free + (cnt & 1));
-          for (int i = 0; ok && i < nb; ++i) {
-            ok = wait2(v_ready, cnt + i);
-            for (int t = 0; ok && t < 2; ++t) {
-              ok = role_wait(p_ready + t, pph[t], failed);
-              if (!ok) break;
-              pph[t] ^= 1u;
-              tc_fence_after();
-              pv(t, cnt + i, i > 0);
-              if (i == nb - 1) {
-                umma_commit(o_full + t);
-              } else {
-                if (t == 0 && !(ok = wait2(k_ready, cnt + i + 1))) break;
-                tc_fence_after();
-                qk(t, t, cnt + i + 1);
-              }
-            }
-            if (!ok) break;
-            umma_commit(v_free + ((cnt + i) & 1));
-            if (i < nb - 1) umma_commit(k_free + ((cnt + i + 1) & 1));
-          }
-        } else {
-          for (int i = 0; ok && i < min(2, nb); ++i) {
-            if (!(ok = wait2(k_ready, cnt + i))) break;
+          qk(i, 0, cnt + i);
+          if (tiles == 2) qk(1, 1, cnt + i);
+          umma_commit_by(leader, k_free + ((cnt + i) & 1));
+        }
+        for (int i = 0; ok && i < nb; ++i) {
+          if (!(ok = wait2(v_ready, cnt + i))) break;
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            uint32_t& ph = t ? pph1 : pph0;
+            if (tiles == 1 && t != (i & 1)) continue;
+            if (!(ok = wait(p_ready + t, ph))) break;
+            ph ^= 1u;
             tc_fence_after();
-            qk(i & 1, 0, cnt + i);
-            umma_commit(k_free + ((cnt + i) & 1));
-          }
-          for (int i = 0; ok && i < nb; ++i) {
-            const int t = i & 1;
-            ok = wait2(v_ready, cnt + i) && role_wait(p_ready + t, pph[t], failed);
-            if (!ok) break;
-            pph[t] ^= 1u;
-            tc_fence_after();
-            pv(t, cnt + i, i >= 2);
-            umma_commit(v_free + ((cnt + i) & 1));
-            if (i + 2 >= nb) {
-              umma_commit(o_full + t);
+            pv(t, cnt + i, i >= ahead);
+            if (t == 1 || tiles == 1) umma_commit_by(leader, v_free + ((cnt + i) & 1));
+            if (i + ahead >= nb) {
+              umma_commit_by(leader, o_full + t);
             } else {
-              if (!(ok = wait2(k_ready, cnt + i + 2))) break;
+              if ((t == 0 || tiles == 1) && !(ok = wait2(k_ready, cnt + i + ahead))) break;
               tc_fence_after();
-              qk(t, 0, cnt + i + 2);
-              umma_commit(k_free + ((cnt + i + 2) & 1));
+              qk(t, tiles == 2 ? t : 0, cnt + i + ahead);
+              if (t == 1 || tiles == 1) umma_commit_by(leader, k_free + ((cnt + i + ahead) & 1));
             }
           }
         }
         cnt += nb;
       }
-      umma_commit(fin);  // arrives once every product issued has completed
+      umma_commit_by(leader, fin);  // arrives once every product issued has completed
       mbar_wait_bounded(fin, 0);
     }
   } else if (warp >= 8) {
     // -------------------------------------------------------------- conversion
     reg_dealloc<kRegConv>();
-    const bool is_v = warp >= 12;
+    const bool is_v = warp >= 12, poller = (warp & 3) == 0;
+    const uint32_t gid = is_v ? 5 : 4;  // named barrier of the group
     const int tok = threadIdx.x & 127, half = tok >> 6, slot = tok & 63;
     uint64_t* ready = is_v ? v_ready : k_ready;
     uint64_t* freed = is_v ? v_free : k_free;
+    uint8_t* const tile0 = smem + (is_v ? L.v : L.k);
     int cnt = 0;         // blocks so far
     int st0 = 0;         // stage and phase of the block's first page
     uint32_t sph0 = 0;
@@ -577,50 +559,63 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     for (int k = 0; ok; ++k) {
       if (!__all_sync(0xffffffffu, piece_at(k))) break;
       const Piece& pc = pieces[k & 1];
-      const int first = pc.first, p0 = pc.p0, p1 = pc.p1, end = pc.ctx + j.N, j1 = pc.j1;
-      int jb = pc.j0;
+      const int first = pc.first, end = pc.ctx + j.N;
+      const int blocks = pc.j1 - pc.j0;
+      int pg = pc.p0 + 2 * pc.j0;
+      const int p1 = pc.p1;
       __syncwarp();
       if (lane == 0) mbar_arrive(piece_empty + (k & 1));
-      for (; ok && jb < j1; ++jb, ++cnt) {
-        const int pg = p0 + 2 * jb, have = min(2, p1 - pg);  // pages of the block
+      for (int i = 0; i < blocks; ++i, ++cnt, pg += 2) {
         const int cb = cnt & 1;
-        uint8_t* tile = smem + (is_v ? L.v : L.k) + cb * kTileBytes;
-        int st = st0 + half;
-        uint32_t sph = sph0;
-        while (st >= p.nst) {
-          st -= p.nst;
-          sph ^= 1u;
+        const bool pair = pg + 1 < p1;  // the block has two pages
+        int st1 = st0 + 1;
+        uint32_t sph1 = sph0;
+        if (st1 == p.nst) {
+          st1 = 0;
+          sph1 ^= 1u;
         }
-        const uint8_t* raw = smem + L.raw + st * stage_bytes(FMT) + (is_v ? kPage * (FMT == 0 ? kRec4 : kRec8) : 0);
-        bool use = half < have;
-        if (use) {
-          ok = __all_sync(0xffffffffu, role_wait(raw_full + st, sph, failed));
-          use = valid[st] != 0;
-          if (slot == 0 && !is_v) bvalid[2 * (cnt & 3) + half] = use;
+        // one warp of the group waits for the pages and for the tile
+        bool w = true;
+        if (poller) {
+          w = role_wait(raw_full + st0, sph0, failed);
+          if (p.nst > 1 && pair) w = w && role_wait(raw_full + st1, sph1, failed);
+          if (cnt >= 2) w = w && role_wait(freed + cb, (uint32_t)((cnt >> 1) - 1) & 1u, failed);
         }
+        ok = !named_barrier_or(gid, 128, !w);
+        if (!ok) break;
+        // one stage: the second page comes into it after the first
+        if (p.nst == 1 && half == 1 && pair) {
+          if (!(ok = __all_sync(0xffffffffu, role_wait(raw_full, sph1, failed)))) break;
+        }
+        const int st = half ? st1 : st0;
+        const bool use = (half == 0 || pair) && valid[st] != 0;
+        if (slot == 0 && !is_v) bvalid[2 * (cnt & 3) + half] = use;
         const int pos = (pg + half) * kPage + slot;
         const bool live = use && pos >= first && pos < end;  // a token that some row may see
-        ok = ok && __all_sync(0xffffffffu, cnt < 2 || role_wait(freed + cb, (uint32_t)((cnt >> 1) - 1) & 1u, failed));
-        if (!ok) break;
+        const uint8_t* raw = smem + L.raw + st * stage_bytes(FMT);
+        uint8_t* tile = tile0 + cb * kTileBytes;
         if (!live) {
           zero_row(tile, tok);
         } else if (FMT == 0) {
-          const uint32_t meta = reinterpret_cast<const uint32_t*>(smem + L.raw + st * stage_bytes(FMT) + 2 * kPage * kRec4)[(is_v ? kPage : 0) + slot];
-          if (is_v) convert_v4(raw + slot * kRec4, slot, meta, tile, tok);
+          const uint32_t meta = reinterpret_cast<const uint32_t*>(raw + 2 * kPage * kRec4)[(is_v ? kPage : 0) + slot];
+          if (is_v) convert_v4(raw + kPage * kRec4 + slot * kRec4, slot, meta, tile, tok);
           else convert_k4(raw + slot * kRec4, slot, meta, tile, tok);
         } else {
-          convert8(raw + slot * kRec8, slot, tile, tok);
+          convert8(raw + (is_v ? kPage * kRec8 : 0) + slot * kRec8, slot, tile, tok);
         }
         fence_proxy_async_shared();
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(ready + cb);
-          if (half < have) mbar_arrive(raw_empty + st);
+          if (half == 0 || pair) mbar_arrive(raw_empty + st);
         }
-        st0 += have;
-        while (st0 >= p.nst) {
-          st0 -= p.nst;
-          sph0 ^= 1u;
+        st0 = st1;
+        sph0 = sph1;
+        if (pair) {
+          if (++st0 == p.nst) {
+            st0 = 0;
+            sph0 ^= 1u;
+          }
         }
       }
     }
@@ -692,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       const int step = pc.w == 2 ? 1 : 2, jfirst = pc.j0 + (pc.w == 2 ? 0 : t);
       const int cntj = cnt0 - pc.j0;
       for (int jb = jfirst; jb < j1; jb += step) {
-        ok = __all_sync(0xffffffffu, role_wait(s_full + t, sph, failed));
+        ok = group_wait(s_full + t, sph, failed, (warp & 3) == 0, 2 + t, 128);
         if (!ok) break;
         sph ^= 1u;
         tc_fence_after();

@@ -99,4 +99,13 @@ __device__ __forceinline__ bool role_wait(uint64_t* bar, uint32_t parity, volati
   return false;
 }
 
+// role_wait by a group of `nthreads` threads (whole warps): the warp with `poller` set watches the mbarrier, the
+// others rest in named barrier `id`, which takes no issue slots. The same answer for the whole group.
+__device__ __forceinline__ bool group_wait(uint64_t* bar, uint32_t parity, volatile int* failed, bool poller, uint32_t id,
+                                           uint32_t nthreads) {
+  bool ok = true;
+  if (poller) ok = role_wait(bar, parity, failed);
+  return !named_barrier_or(id, nthreads, !ok);
+}
+
 }  // namespace kvq
