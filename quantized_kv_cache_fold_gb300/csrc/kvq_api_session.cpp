@@ -208,7 +208,7 @@ kvq_status kvq_prompt_attn(const void* q, const void* k, const void* v, kvq_dtyp
 size_t kvq_tree_workspace_bytes(int B, int N, int num_q_heads, int num_kv_heads) {
   if (!tree_sizes_ok(B, N, num_q_heads, num_kv_heads)) return 0;
   return kvq::workspace_qrot_bytes(B, N, num_q_heads) +
-         kvq::workspace_tree_partials_bytes(B, N, num_q_heads, num_kv_heads);
+         kvq::workspace_tree_partials_bytes(B);
 }
 
 kvq_status kvq_tree_attn_int4(const kvq_int4_cache* cache, const float* Mq, const float* Mk, const void* q,

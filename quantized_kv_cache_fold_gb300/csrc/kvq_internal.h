@@ -139,7 +139,7 @@ struct TreeJob {
   float* partials;  // workspace
   int32_t* dev_err;
 };
-size_t workspace_tree_partials_bytes(int B, int N, int Hq, int Hkv);
+size_t workspace_tree_partials_bytes(int B);
 cudaError_t launch_tree(const TreeJob& job, cudaStream_t stream);
 
 // ---- page pool, page copies and commits (kvq_pages.cu)

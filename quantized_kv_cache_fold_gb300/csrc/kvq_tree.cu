@@ -1,12 +1,12 @@
 // Attention of a tree of drafted tokens over the int4 cache or the e4m3 ring (kvq_tree_attn_*).
 //
 // Row i of sequence b attends to the context (the ring: to its window's part of it) and to the drafted
-// tokens of its mask. The N x G query rows of a KV head share every key and value, so the cache is read
-// and converted once for up to 256 rows, and both products run on the tensor cores:
+// tokens of its mask. The N x G query rows of a KV head share every key and value, so a page is read and
+// converted once for up to 128 rows, and both products run on the tensor cores:
 //
-//   K, V  4-bit codes -> c s + o in fp16 (one rounding), e4m3 -> fp16 (exact), 128 tokens a block,
-//         converted by four warps into shared memory (K: K-major, V: MN-major, 128-byte swizzle)
-//   S = Q' K^T     tcgen05.mma, 128 rows x 128 tokens, accumulators in tensor memory
+//   K, V  4-bit codes -> c s + o in fp16 (one rounding), e4m3 -> fp16 (exact), a page (64 tokens) at a time,
+//         by two warps each into shared memory (K: K-major, V: MN-major, 128-byte swizzle)
+//   S = Q' K^T     tcgen05.mma, 128 rows x 64 tokens, Q' read from tensor memory
 //   P = 2^(c S - base) in fp16 over S, one thread per row (as in kvq_prompt.cu: the base moves only
 //         when a score passes it by more than 8, so P < 2^8)
 //   O += P V       tcgen05.mma, P read from tensor memory
@@ -14,22 +14,22 @@
 // The rounding of q~, K, V and P to fp16 is what keeps both products on the tensor cores: 2^-11 each,
 // against the 2^-8 of a bf16 result; sums, bases and O stay in fp32.
 //
-// Two streams of (S, P, O) take turns, so that the tensor cores work on one while the softmax warps have
-// the other: with more than 128 rows they are two row tiles over the same blocks, else two halves of the
-// blocks (even, odd) over the same rows, joined at the end of a segment in tensor memory.
+// Two CTAs per SM, each with half of the tensor memory (S 64 columns, Q' 64, O 128): while one waits for
+// its chain scores -> weights -> products, the other has the tensor cores.
 //
-// Work split: a segment is (sequence, KV head, group of 256 rows); the segments' blocks are laid end to
-// end and each CTA (one per SM) takes a contiguous part of equal weight (a block counts its row tiles). A
-// segment that one CTA has whole is finished there; of the others each CTA leaves an unnormalised partial,
-// two at most (its first and its last piece), and tree_combine_kernel joins them.
+// Work split: a segment is (sequence, KV head, group of 128 rows); the segments' pages are laid end to end
+// and each CTA takes an equal contiguous part. A segment that one CTA has whole is finished there; of the
+// others each CTA leaves an unnormalised partial, two at most (its first and its last piece), and
+// tree_combine_kernel joins them.
 //
-//   warps 0-3, 4-7  softmax of stream 0 and 1, Q' tiles, output (thread = row = tensor-memory lane)
-//   warps 8-11      conversion of K (thread = token of the block)
-//   warps 12-15     conversion of V
-//   warp 16         copies of pages / ring blocks into shared-memory stages
-//   warp 17         the products (one issuing thread)
-//   warp 18         the CTA's pieces of segments, one ahead (kept out of the other roles' registers: spilled
-//                   ones would miss the little L1 that this much shared memory leaves)
+//   warps 0-3   softmax, Q', output (thread = row = tensor-memory lane)
+//   warps 4-5   conversion of K (thread = token of the page), warps 6-7 of V
+//   warp 8      copies of pages / ring blocks into shared-memory stages, K and V parts on rings of their own
+//   warp 9      the products
+//   warp 10     the CTA's pieces of segments, one ahead (kept out of the other roles' registers: spilled ones
+//               would miss the little L1 that this much shared memory leaves)
+// Groups of warps wait through one of them that watches the barrier, the others in a named barrier: with
+// every warp polling, half of the instructions executed were polls.
 
 #include <algorithm>
 #include <mutex>
@@ -41,50 +41,63 @@ namespace kvq {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kBlk = 128;                  // tokens of a block: two pages
-constexpr int kGroup = 256;                // rows of a segment
-constexpr int kTileBytes = kBlk * kD * 2;  // fp16 tile: two 64-dim halves of 128 rows of 128 bytes
+constexpr int kGroup = 128;                 // rows of a segment
+constexpr int kTileBytes = kPage * kD * 2;  // fp16 tile of a page: two 64-dim halves of 64 rows of 128 bytes
 constexpr int kHalf = kTileBytes / 2;
-constexpr int kThreads = 640;
-constexpr int kRegSoftmax = 120, kRegConv = 80, kRegAux = 80;  // from 96 at launch
-static_assert(256 * kRegSoftmax + 256 * kRegConv + 128 * kRegAux <= kThreads * 96, "register shares above the launch's allocation");
-constexpr uint32_t kColS = 0, kColO = 256;  // stream t at + 128 t; P over the first 64 columns of S
-constexpr int kMaxTreeCtas = 256;           // sizes the partials
-constexpr int kMaxStages = 8;
-constexpr size_t kSmemMax = 227 * 1024;
+constexpr int kThreads = 384;
+constexpr int kRegSoftmax = 128, kRegConv = 64, kRegAux = 48;  // from 80 at launch
+static_assert(128 * (kRegSoftmax + kRegConv + kRegAux) <= kThreads * 80, "register shares above the launch's allocation");
+constexpr uint32_t kColS = 0, kColQ = 64, kColO = 128;  // P over the first 32 columns of S
+constexpr int kMaxTreeCtas = 320;                       // sizes the partials
+constexpr int kMaxStages = 6;                           // of each ring
+constexpr size_t kSmemCta = 233472 / 2 - 1024;          // two CTAs per SM (1 KB of each is the system's)
+constexpr int kStageBytes = 2048;                       // output staging of a softmax warp: 32 rows x 16 floats
+// Pages that a CTA takes at least where there are few: below this the fixed cost of a piece (Q', the partial,
+// its share of the join) outweighs the shorter chain.
+#define KVQ_TREE_MIN_PAGES 2
+constexpr int kMinPages = KVQ_TREE_MIN_PAGES;
 
 struct TreeParams {
   TreeJob j;
-  float c;      // |sm_scale| log2(e) (times k_scale), 1 where that is 0
-  float qmul;   // sign of the scale (0 where it is 0), applied to q
-  float vmul;   // applied to the output
-  int G, R;     // query heads per KV head, rows of a KV head
-  int ng;       // row groups
-  int w_last;   // row tiles of the last group (all others: 2)
-  int nst;      // copy stages
-  float2* ml;   // partials: base and sum of each row, [2 CTAs][rows]
-  float* acc;   // and its 128 sums
-  int* pre;     // blocks of the sequences before each, [B + 1]
-  int prow;     // rows of a partial slot: 128 or 256
+  float c;         // |sm_scale| log2(e) (times k_scale), 1 where that is 0
+  float qmul;      // sign of the scale (0 where it is 0), applied to q
+  float vmul;      // applied to the output
+  int G, R;        // query heads per KV head, rows of a KV head
+  uint32_t g_inv;  // ceil(2^32 / G), 0 for G = 1
+  int ng;          // row groups
+  int nst;         // copy stages of each ring
+  float2* ml;      // partials: base and sum of each row, [2 CTAs][128]
+  float* acc;      // and its 128 sums
+  int* pre;        // pages of the sequences before each, [B + 1]
 };
 
-__host__ __device__ constexpr int stage_bytes(int fmt) { return fmt == 0 ? KVQ_INT4_BLOCK_BYTES : 2 * kPage * kRec8; }
+// One part (K or V) of a page in shared memory: int4 the 4096 bytes of codes, then the 256 of scales and offsets.
+__host__ __device__ constexpr int part_bytes(int fmt) { return fmt == 0 ? kPage * kRec4 + kPage * 4 : kPage * kRec8; }
 
-struct Layout {  // offsets from the 1024-byte aligned start of dynamic shared memory
-  uint32_t q, k, v, raw, bars, piece, valid, bvalid, state, pre, total;
-  __host__ __device__ Layout(int fmt, int qtiles, int nst, int B) {
-    q = 0;
-    k = q + qtiles * kTileBytes;
-    v = k + 2 * kTileBytes;
-    raw = v + 2 * kTileBytes;
-    bars = raw + nst * stage_bytes(fmt);  // a multiple of 16
-    piece = bars + 8 * 40;
-    valid = piece + 2 * 64;
-    bvalid = valid + 4 * kMaxStages;
-    state = bvalid + 4 * 8;  // failed flag, tensor-memory address
-    pre = state + 8;
-    total = pre + 4 * (B + 1);
-  }
+struct Piece {
+  int b, h, g;      // segment; b < 0: no more pieces
+  int j0, j1;       // its pages of this CTA, counted from page p0
+  int ctx, first;   // context length, first position that some row sees
+  int p0;           // page of position `first`
+  int rows;         // rows of the group
+  int whole, slot;  // whether these are all of the segment's pages; else the partial's slot
+  int pad;
+};
+
+struct Smem {
+  uint8_t k[2][kTileBytes];
+  uint8_t v[2][kTileBytes];
+  uint8_t stage[4][kStageBytes];
+  uint64_t raw_full[2][kMaxStages], raw_empty[2][kMaxStages];  // [K, V] part copied / read by its two warps
+  uint64_t ready[2][2], freed[2][2];                           // [K, V][tile] written / its products complete
+  uint64_t s_full, p_ready, o_full, q_ready, fin;
+  uint64_t piece_full[2], piece_empty[2];
+  Piece piece[2];
+  int valid[2][kMaxStages];  // the part was copied (its page lies in the pool)
+  int pvalid[4];             // [page % 4] the page lies in the pool
+  int failed;
+  uint32_t taddr;
+  // then: pre[B + 1], the rings
 };
 
 // Context length of sequence b: clamped into what the cache can hold (`bad` reports that).
@@ -97,21 +110,20 @@ __device__ __forceinline__ int tree_ctx(const TreeJob& j, int b, bool& bad) {
   }
   return c;
 }
-// First position that some row may see, and the page it lies in.
+// First position that some row may see.
 __device__ __forceinline__ int first_pos(const TreeJob& j, int ctx) { return j.fmt == 0 ? 0 : max(0, ctx - j.window + 1); }
-__device__ __forceinline__ int num_blocks(const TreeJob& j, int ctx) {
-  const int p0 = first_pos(j, ctx) / kPage, p1 = (ctx + j.N + kPage - 1) / kPage;
-  return (p1 - p0 + 1) / 2;
+__device__ __forceinline__ int num_pages(const TreeJob& j, int ctx) {
+  return (ctx + j.N + kPage - 1) / kPage - first_pos(j, ctx) / kPage;
 }
 
-// pre[b] = blocks of the sequences before b, by one warp (all of its lanes).
+// pre[b] = pages of the sequences before b, by one warp (all of its lanes).
 __device__ __forceinline__ void build_pre(const TreeJob& j, int* pre, bool report) {
   const int lane = threadIdx.x & 31;
   int sum = 0;
   bool bad = false;
   for (int b0 = 0; b0 < j.B; b0 += 32) {
     const int b = b0 + lane;
-    int v = b < j.B ? num_blocks(j, tree_ctx(j, b, bad)) : 0;
+    int v = b < j.B ? num_pages(j, tree_ctx(j, b, bad)) : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int u = __shfl_up_sync(0xffffffffu, v, o);
@@ -124,30 +136,17 @@ __device__ __forceinline__ void build_pre(const TreeJob& j, int* pre, bool repor
   if (__any_sync(0xffffffffu, bad) && report && lane == 0) set_err(j.dev_err, KVQ_DEVERR_POS);
 }
 
-// The split of the weight line: W in all, n CTAs in use, CTA c from X(c) on. A block belongs to the CTA in
-// whose part its start lies; n is at most W over the largest weight, so every CTA of a segment's span has
-// some of its blocks.
+// The split of the line of pages: W in all, n CTAs in use, CTA c from X(c) on. n <= W, so every CTA has some.
 struct Split {
   long long W;
-  int n, per_seq;  // weight of one block in all heads and groups of a sequence
+  int n, per_seq;  // heads and groups of a sequence
   __device__ Split(const TreeParams& p, const int* pre, int ctas) {
-    const int wg = 2 * (p.ng - 1) + p.w_last;
-    per_seq = p.j.Hkv * wg;
+    per_seq = p.j.Hkv * p.ng;
     W = (long long)per_seq * pre[p.j.B];
-    const int wmax = p.ng > 1 ? 2 : p.w_last;
-    n = (int)min((long long)ctas, W / wmax);
+    n = (int)min((long long)ctas, max(1LL, W / kMinPages));
   }
   __device__ long long X(int c) const { return (long long)c * W / n; }
   __device__ int owner(long long x) const { return (int)(((x + 1) * n - 1) / W); }
-};
-
-struct Piece {
-  int b, h, g, w;    // segment and its row tiles; w = 0: no more pieces
-  int j0, j1;        // its blocks of this CTA
-  int ctx, first;    // context length, first position that some row sees
-  int p0, p1;        // pages that hold positions first .. ctx + N - 1
-  int rows, rows0;   // rows of the group and of its first tile
-  int whole, slot;   // whether these are all of the segment's blocks; else the partial's slot
 };
 
 // The pieces of a CTA in order.
@@ -156,41 +155,40 @@ struct Pieces {
   const int* pre;
   const Split& s;
   long long x, x1;
-  int nb;  // blocks of the piece's segment
+  int nb;  // pages of the piece's segment
   __device__ Pieces(const TreeParams& p_, const int* pre_, const Split& s_, int c) : p(p_), pre(pre_), s(s_) {
     x = c < s.n ? s.X(c) : 0;
     x1 = c < s.n ? s.X(c + 1) : 0;
   }
-  __device__ __noinline__ bool next(Piece& o) {
-    while (x < x1) {
-      int lo = 0, hi = p.j.B;  // the last b with pre[b] * per_seq <= x
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if ((long long)pre[mid] * s.per_seq <= x) lo = mid;
-        else hi = mid;
-      }
-      o.b = lo;
-      nb = pre[lo + 1] - pre[lo];
-      long long rem = x - (long long)pre[lo] * s.per_seq;
-      const long long per_head = (long long)nb * (s.per_seq / p.j.Hkv);
-      o.h = (int)(rem / per_head);
-      rem -= o.h * per_head;
-      o.g = (int)min(rem / (2 * nb), (long long)(p.ng - 1));
-      const long long off = rem - (long long)o.g * 2 * nb;
-      o.w = o.g < p.ng - 1 ? 2 : p.w_last;
-      const long long xs = x - off, xe = xs + (long long)nb * o.w;
-      o.j0 = (int)((off + o.w - 1) / o.w);
-      o.j1 = xe <= x1 ? nb : (int)((x1 - xs + o.w - 1) / o.w);
-      x = xe;
-      if (o.j0 < o.j1) return true;
+  __device__ bool next(Piece& o) {
+    if (x >= x1) return false;
+    int lo = 0, hi = p.j.B;  // the last b with pre[b] * per_seq <= x
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if ((long long)pre[mid] * s.per_seq <= x) lo = mid;
+      else hi = mid;
     }
-    return false;
+    o.b = lo;
+    nb = pre[lo + 1] - pre[lo];
+    const long long rem = x - (long long)pre[lo] * s.per_seq;
+    const int hg = (int)(rem / nb);
+    o.h = hg / p.ng;
+    o.g = hg % p.ng;
+    o.j0 = (int)(rem - (long long)hg * nb);
+    o.j1 = (int)min((long long)nb, o.j0 + (x1 - x));
+    x += o.j1 - o.j0;
+    return true;
   }
 };
 
-// Rows of the group, and of its first tile (two tiles: about half each, whole warps).
 __device__ __forceinline__ int group_rows(const TreeParams& p, int g) { return min(kGroup, p.R - g * kGroup); }
-__device__ __forceinline__ int tile0_rows(int rows, int w) { return w == 1 ? rows : min(kBlk, ((rows + 1) / 2 + 31) & ~31); }
+// r / G (r < 4096)
+__device__ __forceinline__ int div_g(const TreeParams& p, int r) { return p.g_inv ? (int)__umulhi((uint32_t)r, p.g_inv) : r; }
+// Output row (of [B][N][Hq]) of row r of KV head h.
+__device__ __forceinline__ size_t out_row(const TreeParams& p, int b, int h, int r) {
+  const int i = div_g(p, r);
+  return ((size_t)b * p.j.N + i) * p.j.Hq + h * p.G + (r - i * p.G);
+}
 
 __device__ __forceinline__ float half_lo(uint32_t x) { return __half2float(__ushort_as_half((unsigned short)x)); }
 __device__ __forceinline__ float half_hi(uint32_t x) { return __half2float(__ushort_as_half((unsigned short)(x >> 16))); }
@@ -206,8 +204,6 @@ __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
 }
 __device__ __forceinline__ uint32_t both(float x) { return pack_f16x2(x, x); }
 
-// Place of 8-dim word w (0..15) of row r in an fp16 tile.
-__device__ __forceinline__ uint32_t tile_offset(int r, int w) { return (w >> 3) * kHalf + r * 128 + 16 * ((w & 7) ^ (r & 7)); }
 
 // One token's K record -> its row of the K tile. Word w holds dims 8w..8w+7 in the order 0, 4, 1, 5, 2, 6, 3,
 // 7 (as the nibbles pair up in 32 bits; Q' takes the same). A code is the subnormal c 2^-24 (even nibbles)
@@ -320,87 +316,65 @@ __device__ __forceinline__ void zero_row(uint8_t* tile, int row) {
   for (int w = 0; w < 16; ++w) *reinterpret_cast<uint4*>(tile + (w >> 3) * kHalf + row * 128 + 16 * (w & 7)) = make_uint4(0u, 0u, 0u, 0u);
 }
 
-// Column of dim d (0..7 of a word) in the tiles, and its inverse order for the output.
+
+// Column of dim d (0..7 of a word) in the tiles.
 template <int FMT>
 __device__ __forceinline__ constexpr int col_of(int d) {
   return FMT == 0 ? 2 * (d & 3) + (d >> 2) : d;
 }
 
-// Output row (of [B][N][Hq]) of row r of KV head h.
-__device__ __forceinline__ size_t out_row(const TreeParams& p, int b, int h, int r) {
-  return ((size_t)b * p.j.N + r / p.G) * p.j.Hq + h * p.G + r % p.G;
-}
-
 template <int FMT>
-__global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant__ TreeParams p) {
+__global__ void __launch_bounds__(kThreads, 2) tree_kernel(const __grid_constant__ TreeParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+  Smem& sm = *reinterpret_cast<Smem*>(smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u));
   const TreeJob& j = p.j;
-  const Layout L(FMT, p.prow / 128, p.nst, j.B);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L.bars);
-  uint64_t* raw_full = bars;             // [8] a page copied
-  uint64_t* raw_empty = bars + 8;        // [8] and read (the two K and two V warps of its tokens)
-  uint64_t* k_ready = bars + 16;         // [2] K tile written
-  uint64_t* v_ready = bars + 18;         // [2]
-  uint64_t* k_free = bars + 20;          // [2] products over it complete
-  uint64_t* v_free = bars + 22;          // [2]
-  uint64_t* s_full = bars + 24;          // [2] scores of a stream complete
-  uint64_t* p_ready = bars + 26;         // [2] weights written
-  uint64_t* o_full = bars + 28;          // [2] a piece's last product of a stream complete
-  uint64_t* q_ready = bars + 30;         // Q' of a piece written
-  uint64_t* fin = bars + 31;
-  uint64_t* piece_full = bars + 32;      // [2] a piece announced
-  uint64_t* piece_empty = bars + 34;     // [2] and left behind by every role
-  Piece* pieces = reinterpret_cast<Piece*>(smem + L.piece);
-  static_assert(sizeof(Piece) <= 64, "pieces larger than their shared-memory region");
-  volatile int* valid = reinterpret_cast<volatile int*>(smem + L.valid);    // [stage] the page was copied
-  volatile int* bvalid = reinterpret_cast<volatile int*>(smem + L.bvalid);  // [block % 4][page] it exists in the pool
-  volatile int* failed = reinterpret_cast<volatile int*>(smem + L.state);
-  uint32_t* taddr = reinterpret_cast<uint32_t*>(smem + L.state + 4);
-  int* pre = reinterpret_cast<int*>(smem + L.pre);
+  uint8_t* const ring = reinterpret_cast<uint8_t*>(&sm) + sizeof(Smem);  // [K, V][nst][part]
+  int* const pre = reinterpret_cast<int*>(ring + 2 * p.nst * part_bytes(FMT));
+  volatile int* failed = &sm.failed;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kMaxStages; ++i) {
-      mbar_init(raw_full + i, 1);
-      mbar_init(raw_empty + i, 4);
+    for (int w = 0; w < 2; ++w) {
+      for (int i = 0; i < kMaxStages; ++i) {
+        mbar_init(&sm.raw_full[w][i], 1);
+        mbar_init(&sm.raw_empty[w][i], 2);
+      }
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&sm.ready[w][i], 2);
+        mbar_init(&sm.freed[w][i], 1);
+      }
+      mbar_init(&sm.piece_full[w], 1);
+      mbar_init(&sm.piece_empty[w], 10);  // copies, products, 4 conversion and 4 softmax warps
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(k_ready + i, 4);
-      mbar_init(v_ready + i, 4);
-      mbar_init(k_free + i, 1);
-      mbar_init(v_free + i, 1);
-      mbar_init(s_full + i, 1);
-      mbar_init(p_ready + i, 4);
-      mbar_init(o_full + i, 1);
-      mbar_init(piece_full + i, 1);
-      mbar_init(piece_empty + i, 18);  // copies, products, 8 conversion and 8 softmax warps
-    }
-    mbar_init(q_ready, 8);
-    mbar_init(fin, 1);
-    *failed = 0;
+    mbar_init(&sm.s_full, 1);
+    mbar_init(&sm.p_ready, 4);
+    mbar_init(&sm.o_full, 1);
+    mbar_init(&sm.q_ready, 4);
+    mbar_init(&sm.fin, 1);
+    sm.failed = 0;
   }
   fence_barrier_init();
   griddep_wait();
   griddep_launch_dependents();
-  if (warp == 0) {
+  if (warp == 10) {
     build_pre(j, pre, blockIdx.x == 0);
+    __syncwarp();
     if (blockIdx.x == 0)  // for tree_combine_kernel
       for (int b = lane; b <= j.B; b += 32) p.pre[b] = pre[b];
   }
-  if (warp == 17) tmem_alloc_512(taddr);
+  if (warp == 9) tmem_alloc_256(&sm.taddr);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *taddr;
+  const uint32_t tmem = sm.taddr;
   // Piece k as the schedule announced it; false at the end or after a wait that gave up.
   auto piece_at = [&](int k) {
-    return role_wait(piece_full + (k & 1), (uint32_t)(k >> 1) & 1u, failed) && pieces[k & 1].w != 0;
+    return __all_sync(0xffffffffu, role_wait(&sm.piece_full[k & 1], (uint32_t)(k >> 1) & 1u, failed)) && sm.piece[k & 1].b >= 0;
   };
 
-  if (warp >= 16) {
+  if (warp >= 8) {
     reg_dealloc<kRegAux>();
-    if (warp == 18 && lane == 0) {
+    if (warp == 10 && lane == 0) {
       // ------------------------------------------------------------ schedule
       const Split sp(p, pre, gridDim.x);
       Pieces it(p, pre, sp, blockIdx.x);
@@ -411,20 +385,18 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           pc.ctx = tree_ctx(j, pc.b, bad);
           pc.first = first_pos(j, pc.ctx);
           pc.p0 = pc.first / kPage;
-          pc.p1 = (pc.ctx + j.N + kPage - 1) / kPage;
           pc.rows = group_rows(p, pc.g);
-          pc.rows0 = tile0_rows(pc.rows, pc.w);
           pc.whole = pc.j0 == 0 && pc.j1 == it.nb;
-          pc.slot = (2 * blockIdx.x + (k > 0)) * p.prow;
+          pc.slot = (2 * blockIdx.x + (k > 0)) * kGroup;
         } else {
-          pc.w = 0;
+          pc.b = -1;
         }
-        if (k >= 2 && !role_wait(piece_empty + (k & 1), (uint32_t)(k / 2 - 1) & 1u, failed)) break;
-        pieces[k & 1] = pc;
-        mbar_arrive(piece_full + (k & 1));
-        if (pc.w == 0) break;
+        if (k >= 2 && !role_wait(&sm.piece_empty[k & 1], (uint32_t)(k / 2 - 1) & 1u, failed)) break;
+        sm.piece[k & 1] = pc;
+        mbar_arrive(&sm.piece_full[k & 1]);
+        if (pc.b < 0) break;
       }
-    } else if (warp == 16) {
+    } else if (warp == 8) {
       // ------------------------------------------------------------ copies
       const uint64_t pol = policy_evict_first();
       int issued = 0;  // pages so far
@@ -432,10 +404,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       uint32_t eph = 1;  // phase of its release (first round: none to wait for)
       bool ok = true;
       for (int k = 0; ok; ++k) {
-        if (!__all_sync(0xffffffffu, piece_at(k))) break;
-        const Piece& pc = pieces[k & 1];
-        const int pg1 = min(pc.p0 + 2 * pc.j1, pc.p1);
-        for (int base = pc.p0 + 2 * pc.j0; ok && base < pg1; base += 32) {
+        if (!piece_at(k)) break;
+        const Piece& pc = sm.piece[k & 1];
+        const int pg1 = pc.p0 + pc.j1;
+        for (int base = pc.p0 + pc.j0; ok && base < pg1; base += 32) {
           const uint8_t* src = nullptr;  // null: a page outside the pool
           const int pg = base + lane;
           if (pg < pg1) {
@@ -445,22 +417,32 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
               else set_err(j.dev_err, KVQ_DEVERR_PAGE);
             } else {
               const int nblk = j.ring.capacity / kPage;
-              src = j.ring.data + (((size_t)pc.b * j.Hkv + pc.h) * nblk + pg % nblk) * (size_t)stage_bytes(1);
+              src = j.ring.data + (((size_t)pc.b * j.Hkv + pc.h) * nblk + pg % nblk) * (size_t)(2 * kPage * kRec8);
             }
           }
           const int n = min(32, pg1 - base);
           for (int i = 0; i < n; ++i) {
             const uint8_t* s = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), i));
             if (lane == 0 && ok) {
-              ok = issued < p.nst || role_wait(raw_empty + st, eph, failed);
-              if (ok) {
-                valid[st] = s != nullptr;
-                if (s) {
-                  mbar_arrive_expect_tx(raw_full + st, stage_bytes(FMT));
-                  bulk_g2s(smem + L.raw + st * stage_bytes(FMT), s, stage_bytes(FMT), raw_full + st, pol);
+#pragma unroll
+              for (int w = 0; w < 2; ++w) {  // K, then V
+                ok = ok && (issued < p.nst || role_wait(&sm.raw_empty[w][st], eph, failed));
+                if (!ok) break;
+                uint64_t* full = &sm.raw_full[w][st];
+                uint8_t* dst = ring + (size_t)(w * p.nst + st) * part_bytes(FMT);
+                sm.valid[w][st] = s != nullptr;
+                if (!s) {
+                  mbar_arrive(full);
+                } else if (FMT == 0) {
+                  mbar_arrive_expect_tx(full, part_bytes(0));
+                  bulk_g2s(dst, s + w * kPage * kRec4, kPage * kRec4, full, pol);
+                  bulk_g2s(dst + kPage * kRec4, s + 2 * kPage * kRec4 + w * kPage * 4, kPage * 4, full, pol);
                 } else {
-                  mbar_arrive(raw_full + st);
+                  mbar_arrive_expect_tx(full, part_bytes(1));
+                  bulk_g2s(dst, s + w * kPage * kRec8, kPage * kRec8, full, pol);
                 }
+              }
+              if (ok) {
                 ++issued;
                 if (++st == p.nst) {
                   st = 0;
@@ -472,269 +454,218 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(piece_empty + (k & 1));
+        if (lane == 0) mbar_arrive(&sm.piece_empty[k & 1]);
       }
-      if (*failed && lane == 0)  // no copy may be in flight when the CTA ends
-        for (int u = max(0, issued - p.nst); u < issued; ++u) mbar_wait_bounded(raw_full + u % p.nst, (uint32_t)(u / p.nst) & 1u);
-    } else if (warp == 17) {
+      if (*failed && lane == 0) {  // no copy may be in flight when the CTA ends (K of page `issued` may be under way as well)
+        for (int u = max(0, issued - p.nst); u <= issued; ++u)
+          for (int w = 0; w < 2; ++w)
+            if (u < issued || w == 0) {
+              const uint64_t t0 = globaltimer();
+              while (!mbar_test(&sm.raw_full[w][u % p.nst], (uint32_t)(u / p.nst) & 1u) && globaltimer() - t0 < 20000000ull) {
+              }
+            }
+      }
+    } else if (warp == 9) {
       // ------------------------------------------------------------ products
-      constexpr uint32_t kIdQK = umma_idesc_16(true, kBlk, false), kIdPV = umma_idesc_16(true, kD, true);
+      constexpr uint32_t kIdQK = umma_idesc_16(true, kPage, false), kIdPV = umma_idesc_16(true, kD, true);
       const uint32_t leader = elect_one();
       const uint32_t tm = (uint32_t)uniform((int)tmem);
-      const uint64_t dq = umma_sdesc(smem_addr(smem + L.q), 16, 1024);
-      const uint64_t dk = umma_sdesc(smem_addr(smem + L.k), 16, 1024);
-      const uint64_t dv = umma_sdesc(smem_addr(smem + L.v), kHalf, 1024);
+      const uint64_t dk = umma_sdesc(smem_addr(sm.k[0]), 16, 1024);
+      const uint64_t dv = umma_sdesc(smem_addr(sm.v[0]), kHalf, 1024);
       auto wait = [&](uint64_t* bar, uint32_t ph) { return __all_sync(0xffffffffu, role_wait(bar, ph, failed)) != 0; };
-      auto wait2 = [&](uint64_t* bar, int cnt) { return wait(bar + (cnt & 1), (uint32_t)(cnt >> 1) & 1u); };
-      auto qk = [&](int t, int qt, int cnt) {
-        const uint64_t q = dq + (uint64_t)(qt * (kTileBytes >> 4)), kb = dk + (uint64_t)((cnt & 1) * (kTileBytes >> 4));
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          const uint64_t off = (uint64_t)(((kk >> 2) * kHalf + (kk & 3) * 32) >> 4);
-          umma_f16_by(leader, tm + kColS + 128 * t, q + off, kb + off, kIdQK, kk > 0);
-        }
-        umma_commit_by(leader, s_full + t);
-      };
-      auto pv = [&](int t, int cnt, uint32_t acc) {
-        const uint64_t v = dv + (uint64_t)((cnt & 1) * (kTileBytes >> 4));
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          umma_f16_ts_by(leader, tm + kColO + 128 * t, tm + kColS + 128 * t + 8 * kk, v + (uint64_t)(kk * (2048 >> 4)), kIdPV, kk > 0 ? 1u : acc);
-      };
       bool ok = true;
-      int cnt = 0;  // blocks before the piece
-      uint32_t pph0 = 0u, pph1 = 0u;
+      int cnt = 0;  // pages so far
       for (int k = 0; ok; ++k) {
-        if (!__all_sync(0xffffffffu, piece_at(k))) break;
-        const int nb = uniform(pieces[k & 1].j1 - pieces[k & 1].j0), tiles = uniform(pieces[k & 1].w);
-        if (lane == 0) mbar_arrive(piece_empty + (k & 1));
-        if (!(ok = wait(q_ready, (uint32_t)k & 1u))) break;
-        const int ahead = tiles == 2 ? 1 : 2;  // blocks whose scores are under way while one is multiplied by V
-        for (int i = 0; ok && i < min(ahead, nb); ++i) {
-          if (!(ok = wait2(k_ready, cnt + i))) break;
+        if (!piece_at(k)) break;
+        const int nb = uniform(sm.piece[k & 1].j1 - sm.piece[k & 1].j0);
+        if (lane == 0) mbar_arrive(&sm.piece_empty[k & 1]);
+        if (!(ok = wait(&sm.q_ready, (uint32_t)k & 1u))) break;
+        for (int i = 0; i < nb; ++i, ++cnt) {
+          const int cb = cnt & 1;
+          const uint32_t ph = (uint32_t)(cnt >> 1) & 1u;
+          if (!(ok = wait(&sm.ready[0][cb], ph))) break;
           tc_fence_after();
-          qk(i, 0, cnt + i);
-          if (tiles == 2) qk(1, 1, cnt + i);
-          umma_commit_by(leader, k_free + ((cnt + i) & 1));
-        }
-        for (int i = 0; ok && i < nb; ++i) {
-          if (!(ok = wait2(v_ready, cnt + i))) break;
+          const uint64_t kb = dk + (uint64_t)(cb * (kTileBytes >> 4));
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            uint32_t& ph = t ? pph1 : pph0;
-            if (tiles == 1 && t != (i & 1)) continue;
-            if (!(ok = wait(p_ready + t, ph))) break;
-            ph ^= 1u;
-            tc_fence_after();
-            pv(t, cnt + i, i >= ahead);
-            if (t == 1 || tiles == 1) umma_commit_by(leader, v_free + ((cnt + i) & 1));
-            if (i + ahead >= nb) {
-              umma_commit_by(leader, o_full + t);
-            } else {
-              if ((t == 0 || tiles == 1) && !(ok = wait2(k_ready, cnt + i + ahead))) break;
-              tc_fence_after();
-              qk(t, tiles == 2 ? t : 0, cnt + i + ahead);
-              if (t == 1 || tiles == 1) umma_commit_by(leader, k_free + ((cnt + i + ahead) & 1));
-            }
-          }
+          for (int kk = 0; kk < 8; ++kk)  // 16 dims each: 32 bytes within a 64-dim half of K, 8 columns of Q'
+            umma_f16_ts_by(leader, tm + kColS, tm + kColQ + 8 * kk, kb + (uint64_t)(((kk >> 2) * kHalf + (kk & 3) * 32) >> 4), kIdQK, kk > 0);
+          umma_commit_by(leader, &sm.s_full);
+          umma_commit_by(leader, &sm.freed[0][cb]);
+          ok = wait(&sm.ready[1][cb], ph) && wait(&sm.p_ready, (uint32_t)cnt & 1u);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t vb = dv + (uint64_t)(cb * (kTileBytes >> 4));
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)  // 16 tokens each: 2048 bytes of a half of V, 8 columns of P
+            umma_f16_ts_by(leader, tm + kColO, tm + kColS + 8 * kk, vb + (uint64_t)(kk * (2048 >> 4)), kIdPV, (kk > 0 || i > 0) ? 1u : 0u);
+          umma_commit_by(leader, &sm.freed[1][cb]);
         }
-        cnt += nb;
+        if (ok) umma_commit_by(leader, &sm.o_full);
       }
-      umma_commit_by(leader, fin);  // arrives once every product issued has completed
-      mbar_wait_bounded(fin, 0);
+      umma_commit_by(leader, &sm.fin);  // arrives once every product issued has completed
+      mbar_wait_bounded(&sm.fin, 0);
     }
-  } else if (warp >= 8) {
+  } else if (warp >= 4) {
     // -------------------------------------------------------------- conversion
     reg_dealloc<kRegConv>();
-    const bool is_v = warp >= 12, poller = (warp & 3) == 0;
-    const uint32_t gid = is_v ? 5 : 4;  // named barrier of the group
-    const int tok = threadIdx.x & 127, half = tok >> 6, slot = tok & 63;
-    uint64_t* ready = is_v ? v_ready : k_ready;
-    uint64_t* freed = is_v ? v_free : k_free;
-    uint8_t* const tile0 = smem + (is_v ? L.v : L.k);
-    int cnt = 0;         // blocks so far
-    int st0 = 0;         // stage and phase of the block's first page
-    uint32_t sph0 = 0;
+    const int is_v = warp >= 6;
+    const bool poller = (warp & 1) == 0;
+    const int slot = threadIdx.x & 63;
+    int cnt = 0, st = 0;
+    uint32_t sph = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
-      if (!__all_sync(0xffffffffu, piece_at(k))) break;
-      const Piece& pc = pieces[k & 1];
-      const int first = pc.first, end = pc.ctx + j.N;
-      const int blocks = pc.j1 - pc.j0;
-      int pg = pc.p0 + 2 * pc.j0;
-      const int p1 = pc.p1;
+      if (!piece_at(k)) break;
+      const Piece& pc = sm.piece[k & 1];
+      const int first = pc.first, end = pc.ctx + j.N, pages = pc.j1 - pc.j0;
+      int pos = (pc.p0 + pc.j0) * kPage + slot;
       __syncwarp();
-      if (lane == 0) mbar_arrive(piece_empty + (k & 1));
-      for (int i = 0; i < blocks; ++i, ++cnt, pg += 2) {
+      if (lane == 0) mbar_arrive(&sm.piece_empty[k & 1]);
+      for (int i = 0; i < pages; ++i, ++cnt, pos += kPage) {
         const int cb = cnt & 1;
-        const bool pair = pg + 1 < p1;  // the block has two pages
-        int st1 = st0 + 1;
-        uint32_t sph1 = sph0;
-        if (st1 == p.nst) {
-          st1 = 0;
-          sph1 ^= 1u;
-        }
-        // one warp of the group waits for the pages and for the tile
         bool w = true;
         if (poller) {
-          w = role_wait(raw_full + st0, sph0, failed);
-          if (p.nst > 1 && pair) w = w && role_wait(raw_full + st1, sph1, failed);
-          if (cnt >= 2) w = w && role_wait(freed + cb, (uint32_t)((cnt >> 1) - 1) & 1u, failed);
+          w = role_wait(&sm.raw_full[is_v][st], sph, failed);
+          if (cnt >= 2) w = w && role_wait(&sm.freed[is_v][cb], (uint32_t)((cnt >> 1) - 1) & 1u, failed);
         }
-        ok = !named_barrier_or(gid, 128, !w);
+        ok = !named_barrier_or(1 + is_v, 64, !w);
         if (!ok) break;
-        // one stage: the second page comes into it after the first
-        if (p.nst == 1 && half == 1 && pair) {
-          if (!(ok = __all_sync(0xffffffffu, role_wait(raw_full, sph1, failed)))) break;
-        }
-        const int st = half ? st1 : st0;
-        const bool use = (half == 0 || pair) && valid[st] != 0;
-        if (slot == 0 && !is_v) bvalid[2 * (cnt & 3) + half] = use;
-        const int pos = (pg + half) * kPage + slot;
-        const bool live = use && pos >= first && pos < end;  // a token that some row may see
-        const uint8_t* raw = smem + L.raw + st * stage_bytes(FMT);
-        uint8_t* tile = tile0 + cb * kTileBytes;
-        if (!live) {
-          zero_row(tile, tok);
+        const bool use = *reinterpret_cast<volatile int*>(&sm.valid[is_v][st]) != 0;
+        if (slot == 0 && !is_v) sm.pvalid[cnt & 3] = use;
+        const uint8_t* raw = ring + (size_t)(is_v * p.nst + st) * part_bytes(FMT);
+        uint8_t* tile = is_v ? sm.v[cb] : sm.k[cb];
+        if (!(use && pos >= first && pos < end)) {  // a token that no row may see
+          zero_row(tile, slot);
         } else if (FMT == 0) {
-          const uint32_t meta = reinterpret_cast<const uint32_t*>(raw + 2 * kPage * kRec4)[(is_v ? kPage : 0) + slot];
-          if (is_v) convert_v4(raw + kPage * kRec4 + slot * kRec4, slot, meta, tile, tok);
-          else convert_k4(raw + slot * kRec4, slot, meta, tile, tok);
+          const uint32_t meta = reinterpret_cast<const uint32_t*>(raw + kPage * kRec4)[slot];
+          if (is_v) convert_v4(raw + slot * kRec4, slot, meta, tile, slot);
+          else convert_k4(raw + slot * kRec4, slot, meta, tile, slot);
         } else {
-          convert8(raw + (is_v ? kPage * kRec8 : 0) + slot * kRec8, slot, tile, tok);
+          convert8(raw + slot * kRec8, slot, tile, slot);
         }
         fence_proxy_async_shared();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(ready + cb);
-          if (half == 0 || pair) mbar_arrive(raw_empty + st);
+          mbar_arrive(&sm.ready[is_v][cb]);
+          mbar_arrive(&sm.raw_empty[is_v][st]);
         }
-        st0 = st1;
-        sph0 = sph1;
-        if (pair) {
-          if (++st0 == p.nst) {
-            st0 = 0;
-            sph0 ^= 1u;
-          }
+        if (++st == p.nst) {
+          st = 0;
+          sph ^= 1u;
         }
       }
     }
   } else {
     // -------------------------------------------------------------- softmax and output
     reg_alloc<kRegSoftmax>();
-    const int t = warp >> 2, r = threadIdx.x & 127;
-    const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
-    const uint32_t ts = tmem + lane_base + kColS + 128 * t;
+    const int r = threadIdx.x;  // row of the group
+    const uint32_t lane_base = (uint32_t)(32 * warp) << 16;
+    const uint32_t ts = tmem + lane_base + kColS, to = tmem + lane_base + kColO;
+    uint8_t* const stage = sm.stage[warp];
+    const int lr = lane >> 2, lc = lane & 3;  // output and Q': 4 lanes per row of 16 floats, 8 rows at a time
     const uint64_t all = j.N == 64 ? ~0ull : (1ull << j.N) - 1;
-    uint32_t sph = 0, oph = 0;
-    int cnt0 = 0;
+    int cnt = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
-      if (!__all_sync(0xffffffffu, piece_at(k))) break;
-      const Piece& pc = pieces[k & 1];
-      // ---- Q' rows of the tile (both groups of warps together where there is one)
-      {
-        const int tile = pc.w == 2 ? t : 0;
-        const int nthr = pc.w == 2 ? 128 : 256, me = pc.w == 2 ? r : (int)threadIdx.x;
-        const int r0 = pc.g * kGroup + tile * pc.rows0, nr = tile ? pc.rows - pc.rows0 : pc.rows0;
-        // four words of 8 dims a thread in flight
-        for (int e0 = me; e0 < 128 * 16; e0 += 4 * nthr) {
-          uint4 in[4][2];
+      if (!piece_at(k)) break;
+      const Piece& pc = sm.piece[k & 1];
+      const int ctx = pc.ctx, rows = pc.rows, r0 = pc.g * kGroup;
+      const bool mine = r < rows, warp_rows = 32 * warp < rows;
+      // ---- Q' of the warp's rows: 16 dims at a time through the staging tile, into 8 columns of each lane
+      if (warp_rows) {
+        size_t src[4];
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int e = e0 + u * nthr, row = e >> 4, w = e & 15;
-            in[u][0] = in[u][1] = make_uint4(0u, 0u, 0u, 0u);
-            if (row < nr) {
-              const size_t src = out_row(p, pc.b, pc.h, r0 + row) * kD + 8 * w;
-              if (FMT == 1 && j.q_bf16) {
-                in[u][0] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(j.q) + src);
-              } else {
-                const uint4* q4 = reinterpret_cast<const uint4*>((FMT == 0 ? j.q_rot : static_cast<const float*>(j.q)) + src);
-                in[u][0] = q4[0];
-                in[u][1] = q4[1];
-              }
-            }
-          }
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int e = e0 + u * nthr, row = e >> 4, w = e & 15;
-            const uint32_t ww[8] = {in[u][0].x, in[u][0].y, in[u][0].z, in[u][0].w, in[u][1].x, in[u][1].y, in[u][1].z, in[u][1].w};
-            float y[8];
-#pragma unroll
-            for (int d = 0; d < 8; ++d) {
-              const float x = FMT == 1 && j.q_bf16 ? bf16_bits_to_f32(d & 1 ? ww[d >> 1] >> 16 : ww[d >> 1] & 0xFFFFu) : __uint_as_float(ww[d]);
-              y[col_of<FMT>(d)] = x * p.qmul;
-            }
-            *reinterpret_cast<uint4*>(smem + L.q + tile * kTileBytes + tile_offset(row, w)) =
-                make_uint4(pack_f16x2_sat(y[0], y[1]), pack_f16x2_sat(y[2], y[3]), pack_f16x2_sat(y[4], y[5]), pack_f16x2_sat(y[6], y[7]));
-          }
+        for (int i = 0; i < 4; ++i) {
+          const int rr = 32 * warp + 8 * i + lr;
+          src[i] = out_row(p, pc.b, pc.h, r0 + min(rr, rows - 1)) * kD + 4 * lc;
         }
-        fence_proxy_async_shared();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(q_ready);
+        const bool half_q = FMT == 1 && j.q_bf16;
+        float4 in[2][4];
+        auto fetch = [&](int c, float4 (&x)[4]) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (half_q) {
+              const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(j.q) + src[i] + 16 * c);
+              x[i] = make_float4(bf16_bits_to_f32(u.x & 0xFFFFu), bf16_bits_to_f32(u.x >> 16), bf16_bits_to_f32(u.y & 0xFFFFu), bf16_bits_to_f32(u.y >> 16));
+            } else {
+              x[i] = *reinterpret_cast<const float4*>((FMT == 0 ? j.q_rot : static_cast<const float*>(j.q)) + src[i] + 16 * c);
+            }
+          }
+        };
+        fetch(0, in[0]);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          if (c < 7) fetch(c + 1, in[(c + 1) & 1]);
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int rr = 8 * i + lr;
+            *reinterpret_cast<float4*>(stage + rr * 64 + 16 * (lc ^ ((rr >> 1) & 3))) = in[c & 1][i];
+          }
+          __syncwarp();
+          float x[16];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float4 f = *reinterpret_cast<const float4*>(stage + lane * 64 + 16 * (i ^ ((lane >> 1) & 3)));
+            x[4 * i] = f.x, x[4 * i + 1] = f.y, x[4 * i + 2] = f.z, x[4 * i + 3] = f.w;
+          }
+          float y[16];
+#pragma unroll
+          for (int d = 0; d < 16; ++d) y[(d & 8) + col_of<FMT>(d & 7)] = x[d] * p.qmul;
+          uint32_t w[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) w[i] = pack_f16x2_sat(y[2 * i], y[2 * i + 1]);
+          float wf[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) wf[i] = __uint_as_float(w[i]);
+          tmem_st8(tmem + lane_base + kColQ + 8 * c, wf);
+        }
+        tmem_wait_st();
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.q_ready);
       // ---- this thread's row
-      const int nr = pc.w == 2 && t ? pc.rows - pc.rows0 : pc.rows0;
-      const int grow = pc.g * kGroup + (pc.w == 2 && t ? pc.rows0 : 0) + r;  // row of the KV head
-      const bool mine = r < nr;
-      const uint64_t mask = mine ? j.mask[(size_t)pc.b * j.N + grow / p.G] & all : 0ull;
-      const int ctx = pc.ctx, pages0 = pc.p0 * kPage, j1 = pc.j1;
-      // first position that the row sees, and whether that differs from the block range's
-      const int lo = FMT == 0 ? 0 : max(0, ctx + max(1, __popcll(mask)) - j.window);
-      const bool warp_rows = (r & ~31) < nr;
+      const uint64_t mask = mine ? __ldg(reinterpret_cast<const unsigned long long*>(j.mask) + (size_t)pc.b * j.N + div_g(p, r0 + r)) & all : 0ull;
+      const int lo = FMT == 0 ? 0 : max(0, ctx + max(1, __popcll(mask)) - j.window);  // first position that it sees
       float base = -INFINITY;
       uint64_t l2[2] = {0ull, 0ull};
-      const int step = pc.w == 2 ? 1 : 2, jfirst = pc.j0 + (pc.w == 2 ? 0 : t);
-      const int cntj = cnt0 - pc.j0;
-      for (int jb = jfirst; jb < j1; jb += step) {
-        ok = group_wait(s_full + t, sph, failed, (warp & 3) == 0, 2 + t, 128);
+      int pos0 = (pc.p0 + pc.j0) * kPage;
+      const int pos1 = (pc.p0 + pc.j1) * kPage, pos_first = pos0;
+      for (; pos0 < pos1; pos0 += kPage, ++cnt) {
+        ok = group_wait(&sm.s_full, (uint32_t)cnt & 1u, failed, warp == 0, 3, 128);
         if (!ok) break;
-        sph ^= 1u;
         tc_fence_after();
         if (warp_rows) {
-          const int pos0 = pages0 + 2 * kPage * jb;
-          const int bi = 2 * ((cntj + jb) & 3);
-          const bool pages_ok = bvalid[bi] != 0 && (bvalid[bi + 1] != 0 || pos0 + kPage >= ctx + j.N);
-          // which of the block's tokens the row sees, where some may be hidden
-          const bool edge = pos0 + kBlk > ctx || !pages_ok || (FMT == 1 && pos0 < ctx + j.N - j.window);
-          uint64_t see[2] = {~0ull, ~0ull};
-          if (edge) {
+          uint32_t s[64];
+          tmem_ld32u(ts, s);
+          tmem_ld32u(ts + 32, s + 32);
+          const bool pv = *reinterpret_cast<volatile int*>(&sm.pvalid[cnt & 3]) != 0;
+          tmem_wait_ld_all();
+          // pages that hold drafted tokens, lie outside the pool, or start before some row's window
+          if (pos0 + kPage > ctx || !pv || (FMT == 1 && pos0 < ctx + j.N - j.window)) {
             const int cut = ctx - pos0;  // tokens from here on are drafted ones
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int cc = cut - 64 * h;
-              uint64_t m = cc <= 0 ? 0ull : cc >= 64 ? ~0ull : (1ull << cc) - 1;
-              if (FMT == 1) {
-                const int ll = lo - pos0 - 64 * h;  // context tokens before this are outside the window
-                if (ll > 0) m = ll >= 64 ? 0ull : m & ~((1ull << ll) - 1);
-              }
-              if (cc >= 0) m |= cc >= 64 ? 0ull : mask << cc;
-              else if (cc > -64) m |= mask >> -cc;
-              if (!bvalid[bi + h]) m = 0ull;
-              see[h] = m;
+            uint64_t m = cut <= 0 ? 0ull : cut >= 64 ? ~0ull : (1ull << cut) - 1;
+            if (FMT == 1) {
+              const int ll = lo - pos0;  // context tokens before this are outside the window
+              if (ll > 0) m = ll >= 64 ? 0ull : m & ~((1ull << ll) - 1);
             }
+            if (cut >= 0) m |= cut >= 64 ? 0ull : mask << cut;
+            else if (cut > -64) m |= mask >> -cut;
+            if (!pv) m = 0ull;
+#pragma unroll
+            for (int i = 0; i < 64; ++i)
+              if (!((m >> i) & 1u)) s[i] = 0xFF800000u;
           }
-          // 32 scores at a time, read once for the maximum and once for the weights
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          uint32_t s[32];
-          auto load = [&](int q) {
-            tmem_ld32u(ts + 32 * q, s);
-            tmem_wait_ld_all();
-            if (edge) {
-              const uint32_t m = (uint32_t)(see[q >> 1] >> (32 * (q & 1)));
+          float mx[4];
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (!((m >> i) & 1u)) s[i] = 0xFF800000u;
-            }
-          };
-#pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
-            load(q);
+          for (int u = 0; u < 4; ++u) mx[u] = __uint_as_float(s[u]);
 #pragma unroll
-            for (int i = 0; i < 32; i += 8)
+          for (int i = 4; i < 60; i += 8)
 #pragma unroll
-              for (int u = 0; u < 4; ++u) mx[u] = fmax3(mx[u], __uint_as_float(s[i + 2 * u]), __uint_as_float(s[i + 2 * u + 1]));
-          }
+            for (int u = 0; u < 4; ++u) mx[u] = fmax3(mx[u], __uint_as_float(s[i + 2 * u]), __uint_as_float(s[i + 2 * u + 1]));
+#pragma unroll
+          for (int u = 0; u < 4; ++u) mx[u] = fmaxf(mx[u], __uint_as_float(s[60 + u]));
           const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.c;
           const bool move = top > base + 8.0f || (base == -INFINITY && top > -INFINITY);
           if (__any_sync(0xffffffffu, move)) {
@@ -742,8 +673,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             if (move) base = top;
             l2[0] = mul_f2(l2[0], f2(alpha, alpha));
             l2[1] = mul_f2(l2[1], f2(alpha, alpha));
-            if (jb > jfirst) {  // O of the first block starts anew
-              const uint32_t to = tmem + lane_base + kColO + 128 * t;
+            if (pos0 > pos_first) {  // O of the first page starts anew
 #pragma unroll 1
               for (int i = 0; i < 8; ++i) {
                 uint32_t o[16];
@@ -757,134 +687,74 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           }
           const float neg = base == -INFINITY ? 0.0f : -base;
           const uint64_t c2 = f2(p.c, p.c), n2 = f2(neg, neg);
-          // P of 32 tokens takes 16 columns, always behind the scores still to be read
-#pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
-            load(q);
-            uint32_t pk[16];
+          uint32_t pk[32];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const uint64_t x = fma_f2(f2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), c2, n2);
-              const float e0 = fast_exp2(f2lo(x)), e1 = fast_exp2(f2hi(x));
-              l2[i & 1] = add_f2(l2[i & 1], f2(e0, e1));
-              pk[i] = pack16x2<true>(e0, e1);
-            }
-            tmem_st16u(ts + 16 * q, pk);
+          for (int i = 0; i < 32; ++i) {
+            const uint64_t x = fma_f2(f2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), c2, n2);
+            const float e0 = fast_exp2(f2lo(x)), e1 = fast_exp2(f2hi(x));
+            l2[i & 1] = add_f2(l2[i & 1], f2(e0, e1));
+            pk[i] = pack16x2<true>(e0, e1);
           }
+          tmem_st32u(ts, pk);
           tmem_wait_st();
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(p_ready + t);
+        if (lane == 0) mbar_arrive(&sm.p_ready);
       }
-      cnt0 += pc.j1 - pc.j0;
-      if (ok && jfirst < pc.j1) {
-        ok = __all_sync(0xffffffffu, role_wait(o_full + t, oph, failed));
-        oph ^= 1u;
-      }
-      float l = (f2lo(l2[0]) + f2hi(l2[0])) + (f2lo(l2[1]) + f2hi(l2[1]));
-      // ---- end of the piece: two streams over the same rows are joined, each group of warps taking half of
-      // the dims. A warp that gave up takes all eight with it, so that none waits here for another.
-      const bool join = pc.w == 1;
-      const bool two = join && pc.j1 - pc.j0 > 1;  // the second stream had blocks
-      if (join && ok) {  // base and sum for the other stream's warps, in the first columns of S (read by now)
-        const float bl[4] = {base, l, 0.0f, 0.0f};
-        tmem_st4(ts, bl);
-        tmem_wait_st();
-      }
-      tc_fence_before();
-      if (named_barrier_or(1, 256, !ok)) {
-        ok = false;
-        break;
-      }
-      float a0 = 1.0f, a1 = 0.0f;
-      int c0 = 0, c1 = 128;
-      if (join) {
-        tc_fence_after();
-        float other[4];
-        tmem_ld4(tmem + lane_base + kColS + 128 * (1 - t), other);
-        tmem_wait_ld();
-        const float b0 = t == 0 ? base : other[0], b1 = t == 0 ? other[0] : base;
-        const float l0 = t == 0 ? l : other[1], l1 = t == 0 ? other[1] : l;
-        base = fmaxf(b0, b1);
-        a0 = b0 == -INFINITY ? 0.0f : fast_exp2(b0 - base);
-        a1 = b1 == -INFINITY ? 0.0f : fast_exp2(b1 - base);
-        l = l0 * a0 + l1 * a1;
-        if (l0 != l0 || l1 != l1) l = l0 + l1;  // NaN
-        c0 = 64 * t;
-        c1 = c0 + 64;
-      }
+      if (!ok) break;
+      ok = group_wait(&sm.o_full, (uint32_t)k & 1u, failed, warp == 0, 3, 128);
+      if (!ok) break;
       tc_fence_after();
+      // ---- end of the piece: the result, or a partial of it
+      const float l = (f2lo(l2[0]) + f2hi(l2[0])) + (f2lo(l2[1]) + f2hi(l2[1]));
       const bool whole = pc.whole != 0;
       const float f = whole ? (l > 0.0f || l != l ? p.vmul / l : 0.0f) : 1.0f;
-      const size_t slot = (size_t)pc.slot + (join ? r : t * 128 + r);
-      if (!whole && mine && (!join || t == 0)) p.ml[slot] = make_float2(base, l);
-      const uint32_t to = tmem + lane_base + kColO;
+      if (!whole && mine) p.ml[(size_t)pc.slot + r] = make_float2(base, l);
       if (warp_rows) {
-        // 32 rows x 32 dims at a time through 4 KB of Q' (no product reads it any more: all score products of a
-        // piece are issued before the last weighted sum of either stream), so that 8 lanes write 32 dims of a row
-        uint8_t* stage = smem + L.q + (pc.w == 2 ? t * kTileBytes + (warp & 3) * 4096 : warp * 4096);
-        const int rbase = grow - lane;  // the warp's first row
-        const int have = min(32, nr - (r & ~31));
-        const int lr = lane >> 3, lc = lane & 7;
+        size_t dst[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int rr = 32 * warp + 8 * i + lr;
+          dst[i] = (whole ? out_row(p, pc.b, pc.h, r0 + min(rr, rows - 1)) : (size_t)pc.slot + rr) * kD + 4 * lc;
+        }
 #pragma unroll 1
-        for (int cc = c0; cc < c1; cc += 32) {
-          uint32_t x[32];
-          tmem_ld32u(to + cc + (join ? 0 : 128 * t), x);
+        for (int c = 0; c < 8; ++c) {  // 16 dims at a time, so that 4 lanes write 16 dims of a row
+          uint32_t x[16];
+          tmem_ld16u(to + 16 * c, x);
           tmem_wait_ld_all();
-          float v[32];
+          float v[16];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(x[i]) * a0;
-          if (two) {
-            tmem_ld32u(to + cc + 128, x);
-            tmem_wait_ld_all();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = fmaf(__uint_as_float(x[i]), a1, v[i]);
-          }
-          if (l == 0.0f) {  // nothing seen: O holds 0, or (no product yet) anything
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = 0.0f;
-          }
+          for (int i = 0; i < 16; ++i) v[i] = l == 0.0f ? 0.0f : __uint_as_float(x[i]) * f;  // nothing seen: 0
           __syncwarp();
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            float4 o;  // dims 4 i .. 4 i + 3 of the 32
+          for (int i = 0; i < 4; ++i) {
             const int g8 = 8 * (i >> 1), d = 4 * (i & 1);
-            o.x = v[g8 + col_of<FMT>(d)] * f;
-            o.y = v[g8 + col_of<FMT>(d + 1)] * f;
-            o.z = v[g8 + col_of<FMT>(d + 2)] * f;
-            o.w = v[g8 + col_of<FMT>(d + 3)] * f;
-            *reinterpret_cast<float4*>(stage + lane * 128 + 16 * (i ^ (lane & 7))) = o;
+            *reinterpret_cast<float4*>(stage + lane * 64 + 16 * (i ^ ((lane >> 1) & 3))) =
+                make_float4(v[g8 + col_of<FMT>(d)], v[g8 + col_of<FMT>(d + 1)], v[g8 + col_of<FMT>(d + 2)], v[g8 + col_of<FMT>(d + 3)]);
           }
           __syncwarp();
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int rr = 4 * i + lr;
-            if (rr < have) {
-              const float4 o = *reinterpret_cast<const float4*>(stage + rr * 128 + 16 * (lc ^ (rr & 7)));
-              const int dim = cc + 4 * lc;
-              if (!whole) {
-                *reinterpret_cast<float4*>(p.acc + ((size_t)pc.slot + (join ? 0 : t * 128) + (r & ~31) + rr) * kD + dim) = o;
-              } else {
-                const size_t at = out_row(p, pc.b, pc.h, rbase + rr) * kD + dim;
-                if (j.out_bf16) *reinterpret_cast<uint2*>(static_cast<uint16_t*>(j.out) + at) = make_uint2(pack16x2<false>(o.x, o.y), pack16x2<false>(o.z, o.w));
-                else *reinterpret_cast<float4*>(static_cast<float*>(j.out) + at) = o;
-              }
-            }
+          for (int i = 0; i < 4; ++i) {
+            const int rr = 8 * i + lr;
+            if (32 * warp + rr >= rows) continue;
+            const float4 o = *reinterpret_cast<const float4*>(stage + rr * 64 + 16 * (lc ^ ((rr >> 1) & 3)));
+            if (!whole) *reinterpret_cast<float4*>(p.acc + dst[i] + 16 * c) = o;
+            else if (j.out_bf16) *reinterpret_cast<uint2*>(static_cast<uint16_t*>(j.out) + dst[i] + 16 * c) = make_uint2(pack16x2<false>(o.x, o.y), pack16x2<false>(o.z, o.w));
+            else *reinterpret_cast<float4*>(static_cast<float*>(j.out) + dst[i] + 16 * c) = o;
           }
         }
       }
       tc_fence_before();
-      if (join) named_barrier(1, 256);  // both have read both streams' O, bases and sums
       __syncwarp();
-      if (lane == 0) mbar_arrive(piece_empty + (k & 1));
+      if (lane == 0) mbar_arrive(&sm.piece_empty[k & 1]);
     }
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 17) tmem_dealloc_512(tmem);
+  if (warp == 9) tmem_dealloc_256(tmem);
   if (threadIdx.x == 0 && *failed) set_err(j.dev_err, KVQ_DEVERR_TIMEOUT);
 }
 
@@ -892,26 +762,21 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
 // segment and 8 rows of it, one warp per row, four dims a lane. A first pass (a lane per partial) takes
 // the bases and sums, so that the second has its factors ready and its loads are independent.
 constexpr int kCombineWarps = 8;
-template <int FMT>
 __global__ void __launch_bounds__(kCombineWarps * 32) tree_combine_kernel(const __grid_constant__ TreeParams p, int ctas) {
   const TreeJob& j = p.j;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int seg = blockIdx.x, g = seg % p.ng, h = seg / p.ng % j.Hkv, b = seg / p.ng / j.Hkv;
-  const int rows = group_rows(p, g), w = g < p.ng - 1 ? 2 : p.w_last;
-  const int rr = blockIdx.y * kCombineWarps + warp;
-  if (rr >= rows) return;
+  const int r = blockIdx.y * kCombineWarps + warp;
+  if (r >= group_rows(p, g)) return;
   griddep_wait();
   griddep_launch_dependents();
   const Split sp(p, p.pre, ctas);
   const int pb = p.pre[b], nb = p.pre[b + 1] - pb;
-  const long long xs = (long long)pb * sp.per_seq + (long long)h * nb * (sp.per_seq / j.Hkv) + 2LL * g * nb;
-  const int ca = sp.owner(xs), cb = sp.owner(xs + (long long)(nb - 1) * w);
+  const long long xs = (long long)pb * sp.per_seq + (long long)(h * p.ng + g) * nb;
+  const int ca = sp.owner(xs), cb = sp.owner(xs + nb - 1);
   if (ca == cb) return;
-  const int rows0 = tile0_rows(rows, w);
-  const int r = w == 2 && rr >= rows0 ? rr + 128 - rows0 : rr;
-  // the segment's first block is its CTA's first one unless the block before it lies there as well
-  const bool second = xs > 0 && xs - (g > 0 ? 2 : p.w_last) >= sp.X(ca);
-  auto slot = [&](int c) { return (size_t)(2 * c + (c == ca && second ? 1 : 0)) * p.prow + r; };
+  const bool second = xs > sp.X(ca);  // the segment starts within its first CTA's part
+  auto slot = [&](int c) { return (size_t)(2 * c + (c == ca && second ? 1 : 0)) * kGroup + r; };
   float m = -INFINITY, l = 0.0f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int c0 = ca; c0 <= cb; c0 += 32) {
@@ -925,7 +790,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) tree_combine_kernel(const 
     l = l * f0 + part;
     o.x *= f0, o.y *= f0, o.z *= f0, o.w *= f0;
     m = mn;
-#pragma unroll 4
+#pragma unroll 8
     for (int i = 0; i < n; ++i) {
       const float f = __shfl_sync(0xffffffffu, f1, i);
       const float4 a = reinterpret_cast<const float4*>(p.acc + slot(c0 + i) * kD)[lane];
@@ -933,7 +798,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) tree_combine_kernel(const 
     }
   }
   const float f = l > 0.0f || l != l ? p.vmul / l : 0.0f;
-  const size_t at = out_row(p, b, h, g * kGroup + rr) * kD + 4 * lane;
+  const size_t at = out_row(p, b, h, g * kGroup + r) * kD + 4 * lane;
   if (j.out_bf16)
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(j.out) + at) = make_uint2(pack16x2<false>(o.x * f, o.y * f), pack16x2<false>(o.z * f, o.w * f));
   else
@@ -943,27 +808,26 @@ __global__ void __launch_bounds__(kCombineWarps * 32) tree_combine_kernel(const 
 std::mutex g_mu;  // guards the cache below
 bool g_attr[64][2] = {{false}};
 
-int partial_rows(int N, int Hq, int Hkv) { return N * (Hq / Hkv) <= 128 ? 128 : 256; }
-
 template <int FMT>
-cudaError_t launch_t(TreeParams& p, long long blocks_max, cudaStream_t stream) {
+cudaError_t launch_t(TreeParams& p, long long pages_max, cudaStream_t stream) {
   int dev = 0;
   cudaGetDevice(&dev);
   cudaError_t e;
   {
     std::lock_guard<std::mutex> lock(g_mu);
     if (dev < 0 || dev >= 64 || !g_attr[dev][FMT]) {
-      e = cudaFuncSetAttribute(tree_kernel<FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax);
+      e = cudaFuncSetAttribute(tree_kernel<FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemCta);
+      if (e == cudaSuccess) e = cudaFuncSetAttribute(tree_kernel<FMT>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
       if (e != cudaSuccess) return e;
       if (dev >= 0 && dev < 64) g_attr[dev][FMT] = true;
     }
   }
-  const size_t fixed = Layout(FMT, p.prow / 128, 0, p.j.B).total + 1024;  // + alignment to 1024 bytes
-  p.nst = std::min<int>(kMaxStages, (int)((kSmemMax - fixed) / stage_bytes(FMT)));
-  if (p.nst < 1) return cudaErrorInvalidConfiguration;
-  const size_t smem = fixed + (size_t)p.nst * stage_bytes(FMT);
+  const size_t fixed = sizeof(Smem) + 4 * ((size_t)p.j.B + 1) + 1024;  // + alignment to 1024 bytes
+  p.nst = std::min<int>(kMaxStages, (int)((kSmemCta - fixed) / (2 * part_bytes(FMT))));
+  const size_t smem = fixed + (size_t)p.nst * 2 * part_bytes(FMT);
+  static_assert(sizeof(Smem) % 16 == 0 && kSmemCta - sizeof(Smem) - 1024 - 4 * (KVQ_MAX_SEQS + 1) >= 2 * part_bytes(1), "no room for a copy stage");
   const int sms = device_sms();
-  const int ctas = (int)std::max<long long>(1, std::min<long long>(blocks_max, std::min(sms, kMaxTreeCtas)));
+  const int ctas = (int)std::max<long long>(1, std::min<long long>(pages_max, std::min(2 * sms, kMaxTreeCtas)));
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -979,33 +843,32 @@ cudaError_t launch_t(TreeParams& p, long long blocks_max, cudaStream_t stream) {
   cfg.gridDim = dim3((unsigned)(p.j.B * p.j.Hkv * p.ng), (unsigned)((std::min(p.R, kGroup) + kCombineWarps - 1) / kCombineWarps), 1);
   cfg.blockDim = dim3(kCombineWarps * 32, 1, 1);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, tree_combine_kernel<FMT>, p, ctas);
+  return cudaLaunchKernelEx(&cfg, tree_combine_kernel, p, ctas);
 }
 
 }  // namespace
 
-size_t workspace_tree_partials_bytes(int B, int N, int Hq, int Hkv) {
-  return (size_t)2 * kMaxTreeCtas * partial_rows(N, Hq, Hkv) * (2 + kD) * 4 + 4 * ((size_t)B + 1);
+size_t workspace_tree_partials_bytes(int B) {
+  return (size_t)2 * kMaxTreeCtas * kGroup * (2 + kD) * 4 + 4 * ((size_t)B + 1);
 }
 
 cudaError_t launch_tree(const TreeJob& job, cudaStream_t stream) {
   TreeParams p{};
   p.j = job;
-  float c = job.sm_scale * kLog2e * (job.fmt == 1 ? job.k_scale : 1.0f);
+  const float c = job.sm_scale * kLog2e * (job.fmt == 1 ? job.k_scale : 1.0f);
   p.qmul = c > 0.0f ? 1.0f : c < 0.0f ? -1.0f : 0.0f;
   p.c = c == 0.0f ? 1.0f : (c < 0.0f ? -c : c);
   p.vmul = job.fmt == 1 ? job.v_scale : 1.0f;
   p.G = job.Hq / job.Hkv;
+  p.g_inv = p.G == 1 ? 0u : (uint32_t)(((1ull << 32) + p.G - 1) / p.G);
   p.R = job.N * p.G;
   p.ng = (p.R + kGroup - 1) / kGroup;
-  p.w_last = p.R - (p.ng - 1) * kGroup > 128 ? 2 : 1;
-  p.prow = partial_rows(job.N, job.Hq, job.Hkv);
   p.ml = reinterpret_cast<float2*>(job.partials);
-  p.acc = job.partials + (size_t)2 * 2 * kMaxTreeCtas * p.prow;
-  p.pre = reinterpret_cast<int*>(p.acc + (size_t)2 * kMaxTreeCtas * p.prow * kD);
+  p.acc = job.partials + (size_t)2 * 2 * kMaxTreeCtas * kGroup;
+  p.pre = reinterpret_cast<int*>(p.acc + (size_t)2 * kMaxTreeCtas * kGroup * kD);
   const long long pages = job.fmt == 0 ? job.cache.max_pages_per_seq : job.ring.capacity / kPage + 1;
-  const long long blocks = (pages + 1) / 2 * job.B * job.Hkv * p.ng;
-  return job.fmt == 0 ? launch_t<0>(p, blocks, stream) : launch_t<1>(p, blocks, stream);
+  const long long most = pages * job.B * job.Hkv * p.ng;
+  return job.fmt == 0 ? launch_t<0>(p, most, stream) : launch_t<1>(p, most, stream);
 }
 
 }  // namespace kvq
