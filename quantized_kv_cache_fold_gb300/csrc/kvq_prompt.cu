@@ -66,6 +66,7 @@ struct Item {
 struct Smem {
   uint8_t q[2][kTileBytes];
   uint8_t kv[kRing][kTileBytes];
+  uint8_t stage[8][2048];  // output, a softmax warp each
   uint64_t q_full, q_empty;
   uint64_t kv_full[kRing], kv_empty[kRing];
   uint64_t v_ok[kRing / 2];
@@ -497,23 +498,36 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         if (!ok) break;
         oph ^= 1u;
         tc_fence_after();
-        uint32_t o[128];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_ld32u(to + 32 * i, o + 32 * i);
-        tmem_wait_ld_all();
         const float l = (f2lo(l2[0]) + f2hi(l2[0])) + (f2lo(l2[1]) + f2hi(l2[1]));
         const float inv = 1.0f / l;
-        if (row < it.n) {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(j.out) + (it.s + row) * j.os_t + it.hq * j.os_h);
+        // 32 dims of the warp's 32 rows at a time through shared memory, so that 4 lanes write 64 bytes of a row
+        uint8_t* const stage = sm.stage[warp];
+        const int lr = lane >> 2, lc = lane & 3, row0 = row - lane;
+        uint16_t* const out = static_cast<uint16_t*>(j.out) + (it.s + row0) * j.os_t + it.hq * j.os_h;
+        const int have = it.n - row0;  // rows of the warp (may be 0 or fewer, or more than 32)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            uint32_t w[4];
+        for (int c = 0; c < 4; ++c) {
+          uint32_t o[32], w[16];
+          tmem_ld32u(to + 32 * c, o);
+          tmem_wait_ld_all();
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-              w[u] = pack16x2<F16>(__uint_as_float(o[8 * i + 2 * u]) * inv, __uint_as_float(o[8 * i + 2 * u + 1]) * inv);
-            dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+          for (int i = 0; i < 16; ++i) w[i] = pack16x2<F16>(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<uint4*>(stage + lane * 64 + 16 * (i ^ ((lane >> 1) & 3))) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int rr = 8 * i + lr;
+            if (rr < have)
+              *reinterpret_cast<uint4*>(out + rr * j.os_t + 32 * c + 8 * lc) = *reinterpret_cast<const uint4*>(stage + rr * 64 + 16 * (lc ^ ((rr >> 1) & 3)));
           }
-          if (__builtin_expect(sm.bad[k & 1] == k, 0)) add_nonfinite<F16>(j, it, row);
+        }
+        if (__builtin_expect(sm.bad[k & 1] == k, 0)) {
+          __syncwarp();  // the row as written by other lanes
+          __threadfence_block();
+          if (row < it.n) add_nonfinite<F16>(j, it, row);
         }
         tc_fence_before();
       }
