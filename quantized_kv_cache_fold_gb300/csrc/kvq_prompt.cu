@@ -3,9 +3,12 @@
 //   o_i = sum_j softmax_j(sm_scale q_i.k_j) v_j, j in [max(0, i - window + 1), i] of i's sequence.
 //
 // Bound by the tensor cores for all but short prompts: 4 x 128 operations per visible pair of tokens
-// and query head. One persistent CTA per SM. A work item is 256 consecutive query rows of one sequence
-// and query head, as two tiles of 128 rows that share every key and value block (128 tokens) of the
-// item; both score tiles, both output tiles and (over the scores) the weights live in tensor memory:
+// and query head. One persistent CTA per SM. A work item is two tiles of 128 query rows that share the key
+// and value blocks (128 tokens): the same rows of two query heads of a KV head, or (the last head of an odd
+// number) 256 consecutive rows of one. Two heads see the same blocks under the same mask, so neither tile
+// waits for the other at an end (256 rows: the first tile ends a block early, and with a window the second
+// starts one late). Both score tiles, both output tiles and (over the scores) the weights live in tensor
+// memory:
 //
 //   S_t = Q_t K_j'           tcgen05.mma, Q and K in shared memory (K-major)
 //   P_t = 2^(c S_t - base)   one thread per row, no exchange between threads; c = sm_scale log2(e)
@@ -28,7 +31,7 @@
 // window's start, the end of a sequence), and the rows that do see such an element get it added in the
 // output step. Blocks that every row of both tiles sees are left as they are.
 //
-// Work order: items by descending row block, so the longest run first, heads of a row block next to each
+// Work order: items by descending block of 256 rows, so the longest run first, heads of a block next to each
 // other (they share K and V in L2); CTAs take them in turns, back and forth (c, 2n-1-c, 2n+c, ...),
 // which evens out the descending lengths without a counter in memory.
 
@@ -59,8 +62,8 @@ struct PromptParams {
 };
 
 struct Item {
-  int s, n;    // first token and length of the sequence (n < 0: no more items)
-  int r0, hq;  // first row, query head
+  int s, n;           // first token and length of the sequence (n < 0: no more items)
+  int r0[2], hq[2];   // first row and query head of each tile (r0 >= n: no tile)
 };
 
 struct Smem {
@@ -84,7 +87,7 @@ struct Smem {
 struct Range {
   int jb, je;
   __device__ Range(const Item& it, int t, int window) {
-    const int R = it.r0 + t * kRows;
+    const int R = it.r0[t];
     if (R >= it.n) {
       jb = je = 0;
     } else {
@@ -153,16 +156,16 @@ __device__ __forceinline__ float value16(uint32_t bits) {
 // The output step's slow part: adds the non-finite values of the edge blocks that this row sees to the
 // row as written (the sums are infinite or NaN, so nothing is rounded twice).
 template <bool F16>
-__device__ __noinline__ void add_nonfinite(const PromptJob& j, const Item& it, int row) {
+__device__ __noinline__ void add_nonfinite(const PromptJob& j, const Item& it, int t, int row) {
   const Range r0(it, 0, j.window), r1(it, 1, j.window);
   const int lo = j.window ? max(0, row - j.window + 1) : 0;
-  const int hkv = it.hq / (j.Hq / j.Hkv);
-  uint16_t* o = static_cast<uint16_t*>(j.out) + (it.s + row) * j.os_t + it.hq * j.os_h;
-  for (int jb = r0.jb; jb < max(r0.je, r1.je); ++jb) {
+  const int hkv = it.hq[t] / (j.Hq / j.Hkv);
+  uint16_t* o = static_cast<uint16_t*>(j.out) + (it.s + row) * j.os_t + it.hq[t] * j.os_h;
+  for (int jb = r0.jb; jb < max(r0.je, r1.je); ++jb) {  // tile 0 starts first
     bool edge = false;
-    for (int t = 0; t < 2; ++t) {
-      const Range& r = t ? r1 : r0;
-      edge |= jb >= r.jb && jb < r.je && edge_block(it.r0 + t * kRows, it.n, jb, j.window);
+    for (int u = 0; u < 2; ++u) {
+      const Range& r = u ? r1 : r0;
+      edge |= jb >= r.jb && jb < r.je && edge_block(it.r0[u], it.n, jb, j.window);
     }
     if (!edge) continue;
     for (int tok = max(lo, jb * kRows); tok <= min(row, jb * kRows + kRows - 1); ++tok) {
@@ -230,18 +233,31 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       }
       npairs = warp_sum_int(npairs);
       top = __reduce_max_sync(0xffffffffu, top);
-      const long long items = (long long)npairs * j.Hq;
+      const long long items = (long long)npairs * j.Hq;  // some of a sequence's last block are empty
       const int n = gridDim.x, c = blockIdx.x;
+      const int G = j.Hq / j.Hkv;
+      long long turn = 0;
       for (int k = 0;; ++k) {
-        const long long idx = (long long)k * n + (k & 1 ? n - 1 - c : c);
-        Item it{0, -1, 0, 0};
-        if (idx < items) {
+        Item it{0, -1, {0, 0}, {0, 0}};
+        for (;; ++turn) {
+          const long long idx = turn * n + (turn & 1 ? n - 1 - c : c);
+          if (idx >= items) break;  // and so are all later ones
           int b;
           find_pair(sm.nblk, j.B, (int)(idx / j.Hq), top, b);
-          it.s = j.cu_seqlens[b];
-          it.n = j.cu_seqlens[b + 1] - it.s;
-          it.r0 = top * kItemRows;
-          it.hq = (int)(idx % j.Hq);
+          const int e = (int)(idx % j.Hq), u = e % G, h = e - u, first = top * kItemRows;
+          const int s0 = j.cu_seqlens[b], len = j.cu_seqlens[b + 1] - s0;
+          const bool rows256 = (u == G - 1) && (G & 1);
+          // two heads: items u and u + 1 (u even) are their second and first 128 rows
+          const int r = first + (rows256 || (u & 1) ? 0 : kRows);
+          if (r >= len) continue;
+          it.s = s0;
+          it.n = len;
+          it.r0[0] = r;
+          it.r0[1] = rows256 ? r + kRows : r;
+          it.hq[0] = h + (rows256 ? u : u & ~1);
+          it.hq[1] = h + (rows256 ? u : (u & ~1) + 1);
+          ++turn;
+          break;
         }
         bool ok = k < 2 || role_wait(&sm.item_empty[k & 1], (uint32_t)(k / 2 - 1) & 1u, failed);
         if (!__all_sync(0xffffffffu, ok)) break;
@@ -276,9 +292,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         mbar_arrive_expect_tx(&sm.q_full, tiles * kTileBytes);
         for (int t = 0; t < tiles; ++t)
           for (int h = 0; h < 2; ++h)
-            tma_load_3d(sm.q[t] + h * (kTileBytes / 2), &p.mq, 64 * h, it.hq, it.s + it.r0 + t * kRows, &sm.q_full);
+            tma_load_3d(sm.q[t] + h * (kTileBytes / 2), &p.mq, 64 * h, it.hq[t], it.s + it.r0[t], &sm.q_full);
         ++nq;
-        const int hkv = it.hq / (j.Hq / j.Hkv);
+        const int hkv = it.hq[0] / (j.Hq / j.Hkv);
         for (int jb = a.jb; ok && jb < max(a.je, b.je); ++jb)
           ok = load(&p.mk, hkv, it.s + jb * kRows) && load(&p.mv, hkv, it.s + jb * kRows);
       }
@@ -323,7 +339,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.item_empty[k & 1]);
         it.n = uniform(it.n);
-        it.r0 = uniform(it.r0);
+        it.r0[0] = uniform(it.r0[0]);
+        it.r0[1] = uniform(it.r0[1]);
         if (it.n < 0) break;
         const Range r0(it, 0, j.window), r1(it, 1, j.window);
         const int jb = r0.jb, je = max(r0.je, r1.je);
@@ -381,8 +398,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           const int use = kv + 2 * (blk - jb) + 1, slot = use % kRing;
           ok = __all_sync(0xffffffffu, role_wait(&sm.kv_full[slot], (uint32_t)(use / kRing) & 1u, failed));
           if (!ok) break;
-          const bool edge = (blk >= a.jb && blk < a.je && edge_block(it.r0, it.n, blk, j.window)) ||
-                            (blk >= b.jb && blk < b.je && edge_block(it.r0 + kRows, it.n, blk, j.window));
+          const bool edge = (blk >= a.jb && blk < a.je && edge_block(it.r0[0], it.n, blk, j.window)) ||
+                            (blk >= b.jb && blk < b.je && edge_block(it.r0[1], it.n, blk, j.window));
           if (edge) {
             uint4* tile = reinterpret_cast<uint4*>(sm.kv[slot]);
             bool bad = false;
@@ -427,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       __syncwarp();
       if (it.n < 0) break;
       const Range rg(it, t, j.window);
-      const int R = it.r0 + t * kRows, row = R + 32 * (warp & 3) + lane;
+      const int R = it.r0[t], row = R + 32 * (warp & 3) + lane;
       float base = -INFINITY;  // in powers of two, as the weights take it
       uint64_t l2[2] = {0ull, 0ull};
       for (int b = rg.jb; b < rg.je; ++b) {
@@ -440,10 +457,16 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         for (int i = 0; i < 4; ++i) tmem_ld32u(ts + 32 * i, s + 32 * i);
         tmem_wait_ld_all();
         if (edge_block(R, it.n, b, j.window)) {
-          const int hi = row - b * kRows, lo = j.window ? hi - j.window + 1 : 0;
+          const int hi = row - b * kRows, lo = j.window ? hi - j.window + 1 : 0;  // seen: lo..hi
 #pragma unroll
-          for (int i = 0; i < 128; ++i)
-            if (i > hi || i < lo) s[i] = 0xFF800000u;
+          for (int w = 0; w < 4; ++w) {
+            const int h = hi - 32 * w, l = lo - 32 * w;
+            uint32_t m = h < 0 ? 0u : h >= 31 ? ~0u : (2u << h) - 1u;
+            if (l > 0) m = l >= 32 ? 0u : m & (~0u << l);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!(m & (1u << i))) s[32 * w + i] = 0xFF800000u;
+          }
         }
         float mx[4];
 #pragma unroll
@@ -503,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         // 32 dims of the warp's 32 rows at a time through shared memory, so that 4 lanes write 64 bytes of a row
         uint8_t* const stage = sm.stage[warp];
         const int lr = lane >> 2, lc = lane & 3, row0 = row - lane;
-        uint16_t* const out = static_cast<uint16_t*>(j.out) + (it.s + row0) * j.os_t + it.hq * j.os_h;
+        uint16_t* const out = static_cast<uint16_t*>(j.out) + (it.s + row0) * j.os_t + it.hq[t] * j.os_h;
         const int have = it.n - row0;  // rows of the warp (may be 0 or fewer, or more than 32)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -527,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         if (__builtin_expect(sm.bad[k & 1] == k, 0)) {
           __syncwarp();  // the row as written by other lanes
           __threadfence_block();
-          if (row < it.n) add_nonfinite<F16>(j, it, row);
+          if (row < it.n) add_nonfinite<F16>(j, it, t, row);
         }
         tc_fence_before();
       }
