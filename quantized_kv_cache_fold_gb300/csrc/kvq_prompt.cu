@@ -528,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         const int lr = lane >> 2, lc = lane & 3, row0 = row - lane;
         uint16_t* const out = static_cast<uint16_t*>(j.out) + (it.s + row0) * j.os_t + it.hq[t] * j.os_h;
         const int have = it.n - row0;  // rows of the warp (may be 0 or fewer, or more than 32)
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           uint32_t o[32], w[16];
           tmem_ld32u(to + 32 * c, o);
@@ -555,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         tc_fence_before();
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.item_empty[k & 1]);
+      if (lane == 0) mbar_arrive_relaxed(&sm.item_empty[k & 1]);
     }
   }
   __syncwarp();

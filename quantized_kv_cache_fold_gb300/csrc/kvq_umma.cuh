@@ -90,6 +90,12 @@ __device__ __forceinline__ void umma_commit_by(uint32_t leader, uint64_t* bar) {
 }
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
+// An arrival that orders nothing but what has completed already (the default one waits for the thread's
+// outstanding global stores).
+__device__ __forceinline__ void mbar_arrive_relaxed(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
 // Bounded wait for a phase; notes a wait that gave up in *failed. (mbar_wait_bounded's suspend hint matters:
 // a tight loop of plain try_waits in its place takes the 32,768-token prompt from 4.11 to 4.72 ms and the
 // tree over 64 x 16,384 tokens from 355 to 370 us.)
