@@ -76,7 +76,8 @@ __device__ __forceinline__ int4 load_refs4(const int32_t* refs, int p, int hi, b
 __device__ __forceinline__ int warp_sum_int(int v) { return __reduce_add_sync(0xffffffffu, v); }
 
 // Exclusive sum of one value per warp over the cluster's warps in order (all lanes of a warp pass the
-// same v), and the total. Contains cluster barriers: every thread of every CTA calls it.
+// same v), and the total. Contains one cluster barrier: every thread of every CTA calls it, once with one `s`; a
+// CTA may leave only after a later cluster barrier (others still read its total).
 struct ClusterScan {
   long long warp_sums[kPoolWarps];
   long long cta_total;
@@ -88,14 +89,15 @@ __device__ __forceinline__ long long cluster_exclusive(int v, ClusterScan& s, lo
   const long long mine = __shfl_sync(0xffffffffu, incl, 31) - v;
   if (threadIdx.x == 0) s.cta_total = s.warp_sums[kPoolWarps - 1];
   cl.sync();
+  const long long t = lane < kPoolCtas ? *cl.map_shared_rank(&s.cta_total, lane) : 0;
   long long before = 0;
   total = 0;
+#pragma unroll
   for (int r = 0; r < kPoolCtas; ++r) {
-    const long long t = *cl.map_shared_rank(&s.cta_total, r);
-    if (r < (int)cluster_ctarank()) before += t;
-    total += t;
+    const long long x = __shfl_sync(0xffffffffu, t, r);
+    if (r < (int)cluster_ctarank()) before += x;
+    total += x;
   }
-  cl.sync();  // nobody leaves or overwrites its total while another reads it
   return before + mine;
 }
 
@@ -210,6 +212,7 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
       p.table[(size_t)s.id[i] * p.max_pages + at] = -1;
     }
   }
+  cg::this_cluster().sync();  // this CTA's total may still be read
 }
 
 __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads, 1)
@@ -281,6 +284,7 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
     p.table[(size_t)ch * p.max_pages + len / kPage] = -1;
     p.dst[t] = -1;
   }
+  cg::this_cluster().sync();  // this CTA's total may still be read
 }
 
 // One block per request; a row named by an earlier request as well is that one's.
@@ -315,10 +319,34 @@ __global__ void __launch_bounds__(128) pages_free_kernel(const PoolParams p) {
   }
 }
 
+// Every entry that names a moved page, by a search in the ascending list of sources; entries e, e + step, ...
+__device__ __forceinline__ void remap(const PoolParams& p, int moves, long long e, long long step) {
+  if (moves == 0) return;
+  const int first = __ldcg(p.src);
+  const long long n = (long long)p.num_seqs * p.max_pages;
+  for (; e < n; e += step) {
+    const int v = p.table[e];
+    if (v < first || v >= p.num_pages) continue;
+    int lo = 0, hi = moves - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (__ldcg(p.src + mid) < v) lo = mid + 1;
+      else hi = mid;
+    }
+    if (__ldcg(p.src + lo) == v) p.table[e] = __ldcg(p.dst + lo);
+    else set_err(p.dev_err, KVQ_DEVERR_PAGE);  // a page that nobody holds
+  }
+}
+
+// Tables up to this many entries are rewritten by the cluster itself (8 entries a thread at most, less than the
+// second launch costs: 2,600 pages, 6,048 entries, compact and copy 29.9 -> 28.8 us), larger ones by a launch
+// over the whole GPU.
+constexpr long long kClusterTable = 1 << 16;
+
 // The moves: the k-th page in use at or behind L goes to the k-th free page before L.
 __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads, 1)
     pages_compact_kernel(const PoolParams p) {
-  __shared__ ClusterScan scan;
+  __shared__ ClusterScan scan, scan2;
   griddep_wait();
   griddep_launch_dependents();
   cg::cluster_group cl = cg::this_cluster();
@@ -339,7 +367,7 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
   }
   fl = warp_sum_int(fl);
   long long moves;
-  cluster_exclusive(fl, scan, moves);
+  cluster_exclusive(fl, scan2, moves);
   for_free_pages(p.refs, lo, min(hi, L), vec, before, moves, [&](int page, long long k) { p.dst[k] = page; });
   // a page in use at q >= L has rank (pages in use before q) - (L - moves)
   long long rank = (long long)lo - before - (L - moves);
@@ -370,28 +398,14 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
     p.refs[to] = __ldcg(p.refs + from);
     p.refs[from] = 0;
   }
+  if ((long long)p.num_seqs * p.max_pages <= kClusterTable)
+    remap(p, (int)moves, cluster_ctarank() * kPoolThreads + threadIdx.x, kPoolCtas * kPoolThreads);
 }
 
-// Every entry that names a moved page, by a search in the ascending list of sources.
 __global__ void __launch_bounds__(256) pages_remap_kernel(const PoolParams p) {
   griddep_wait();
   griddep_launch_dependents();
-  const int moves = *p.moves;
-  if (moves == 0) return;
-  const int first = p.src[0];
-  const long long n = (long long)p.num_seqs * p.max_pages;
-  for (long long e = (long long)blockIdx.x * blockDim.x + threadIdx.x; e < n; e += (long long)gridDim.x * blockDim.x) {
-    const int v = p.table[e];
-    if (v < first || v >= p.num_pages) continue;
-    int lo = 0, hi = moves - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (p.src[mid] < v) lo = mid + 1;
-      else hi = mid;
-    }
-    if (p.src[lo] == v) p.table[e] = p.dst[lo];
-    else set_err(p.dev_err, KVQ_DEVERR_PAGE);  // a page that nobody holds
-  }
+  remap(p, *p.moves, (long long)blockIdx.x * blockDim.x + threadIdx.x, (long long)gridDim.x * blockDim.x);
 }
 
 // ------------------------------------------------------------------ data
@@ -422,41 +436,25 @@ __global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const __grid_c
   }
 }
 
-// One block per (sequence, KV head, layer): the accepted records' 16-byte chunks (8 of an int4 record,
-// 16 of an e4m3 one) are all read into registers before any is written. The chunks sit in a
-// slot-dependent order, so a record moves chunk by chunk, not as bytes.
-constexpr int kCommitThreads = 128;
+// One block per (sequence, KV head) and two layers. The accepted records' 16-byte chunks (8 of an int4 record,
+// 16 of an e4m3 one) go through registers, every load of a pass before any store. A branch of a tree names
+// its tokens in ascending order, so a source never lies before its target: passes of 16 or 32 records may then
+// follow one another. Any other path of more records than a pass holds is read as a whole first
+// (commit_any). The chunks sit in a slot-dependent order, so a record moves chunk by chunk, not as bytes.
+// Latency-bound: path -> (page) -> chunks -> stores; two layers in flight rather than one
+// (64 sequences x 4 heads, up to 16 of 32 tokens, 10 + 40 layers: 19.7 -> 14.3 us; four layers take more
+// registers and with them waves: 16.0 us).
+constexpr int kCommitThreads = 128, kCommitLayers = 2, kCommitUnits = 2;
 constexpr int kMaxPos = 1 << 30;
+
 template <int FMT>
-__global__ void __launch_bounds__(kCommitThreads) commit_kernel(const __grid_constant__ CacheSet cs, int N, const int32_t* ctx_len, const int32_t* path,
-                                                                const int32_t* n_accept, int32_t* ctx_out,
-                                                                int32_t* dev_err) {
-  constexpr int kChunks = FMT == 0 ? 8 : 16;                          // 16-byte chunks of a record, K then V
-  constexpr int kUnits = KVQ_MAX_TREE * kChunks / kCommitThreads;     // of one thread
-  __shared__ int32_t spath[KVQ_MAX_TREE];
-  griddep_wait();
-  griddep_launch_dependents();
-  const int b = blockIdx.x / cs.heads, h = blockIdx.x % cs.heads, l = blockIdx.y;
-  const int t = threadIdx.x;
-  const int ctx = ctx_len[b], got = n_accept[b];
-  const int A = min(max(got, 0), N);
-  const bool lead = h == 0 && l == 0;  // one block reports a sequence's errors
-  if (lead && t == 0) {
-    if (ctx_out) ctx_out[b] = ctx + A;
-    if (A != got || ctx < 0 || ctx > kMaxPos) set_err(dev_err, KVQ_DEVERR_POS);
-  }
-  if (ctx < 0 || ctx > kMaxPos) return;
-  if (t < A) {
-    int x = path[(size_t)b * N + t];
-    if (x < 0 || x >= N) {
-      x = -1;
-      if (lead) set_err(dev_err, KVQ_DEVERR_POS);
-    }
-    spath[t] = x;
-  }
-  __syncthreads();
-  // block of a position, or null
-  auto block_of = [&](int pos) -> uint8_t* {
+struct CommitAt {
+  static constexpr int kChunks = FMT == 0 ? 8 : 16;  // 16-byte chunks of a record, K then V
+  const CacheSet& cs;
+  int b, h, l;
+  int32_t* dev_err;
+  // Block of a position, or null.
+  __device__ __forceinline__ uint8_t* block(int pos) const {
     if (FMT == 0) {
       if (b >= cs.num_seqs[l] || pos >= cs.max_pages[l] * kPage) {
         set_err(dev_err, KVQ_DEVERR_POS);
@@ -469,51 +467,142 @@ __global__ void __launch_bounds__(kCommitThreads) commit_kernel(const __grid_con
       }
       return cs.pages[l] + ((size_t)page * cs.heads + h) * KVQ_INT4_BLOCK_BYTES;
     }
-    const int cap = cs.max_pages[l] * kPage;
-    return cs.pages[l] + (((size_t)b * cs.heads + h) * cs.max_pages[l] + pos % cap / kPage) * (size_t)(2 * kPage * kRec8);
-  };
-  auto chunk_at = [&](int pos, int c) -> size_t {
-    const int slot = FMT == 0 ? pos % kPage : pos % (cs.max_pages[l] * kPage) % kPage;
+    const int nblk = cs.max_pages[l];
+    return cs.pages[l] + (((size_t)b * cs.heads + h) * nblk + (pos / kPage) % nblk) * (size_t)(2 * kPage * kRec8);
+  }
+  // Byte of chunk c of the record in a position's slot (a ring's capacity is a multiple of 64).
+  static __device__ __forceinline__ size_t chunk(int pos, int c) {
+    const int slot = pos % kPage;
     if (FMT == 0) {
       const int half = c >> 2, k = c & 3;
       return (size_t)half * kPage * kRec4 + slot * kRec4 + 16 * (k ^ (half ? (slot >> 1) & 3 : k_chunk_swz(slot)));
     }
     const int half = c >> 3, k = c & 7;
     return (size_t)half * kPage * kRec8 + slot * kRec8 + 16 * (k ^ (slot & 7));
-  };
-  uint4 v[kUnits];
-  bool have[kUnits];
-#pragma unroll
-  for (int u = 0; u < kUnits; ++u) {
-    const int i = (u * kCommitThreads + t) / kChunks, c = t % kChunks;
-    have[u] = i < A && spath[i] >= 0 && spath[i] != i;
-    if (have[u]) {
-      const int pos = ctx + spath[i];
-      const uint8_t* blk = block_of(pos);
-      have[u] = blk != nullptr;
-      if (blk) v[u] = *reinterpret_cast<const uint4*>(blk + chunk_at(pos, c));
+  }
+  // Word of the scales and offsets (int4): K or V of the record in a position's slot.
+  static __device__ __forceinline__ size_t meta(int pos, int v) { return 2 * kPage * kRec4 + 4 * (v * kPage + pos % kPage); }
+};
+
+// Any path: one thread per chunk (and per scale word) of a record takes its chunk of all records, through local memory.
+template <int FMT>
+__device__ __noinline__ void commit_any(const CommitAt<FMT> at, int ctx, int A, const int32_t* path) {
+  const int t = threadIdx.x;
+  if (t < CommitAt<FMT>::kChunks) {
+    uint4 x[KVQ_MAX_TREE];
+#pragma unroll 1
+    for (int i = 0; i < A; ++i) {
+      const uint8_t* blk = path[i] >= 0 ? at.block(ctx + path[i]) : nullptr;
+      if (blk) x[i] = *reinterpret_cast<const uint4*>(blk + at.chunk(ctx + path[i], t));
+    }
+#pragma unroll 1
+    for (int i = 0; i < A; ++i) {
+      if (path[i] < 0 || path[i] == i || !at.block(ctx + path[i])) continue;
+      uint8_t* blk = at.block(ctx + i);
+      if (blk) *reinterpret_cast<uint4*>(blk + at.chunk(ctx + i, t)) = x[i];
+    }
+  } else if (FMT == 0 && t < CommitAt<FMT>::kChunks + 2) {
+    const int v = t - CommitAt<FMT>::kChunks;
+    uint32_t x[KVQ_MAX_TREE];
+#pragma unroll 1
+    for (int i = 0; i < A; ++i) {
+      const uint8_t* blk = path[i] >= 0 ? at.block(ctx + path[i]) : nullptr;
+      if (blk) x[i] = *reinterpret_cast<const uint32_t*>(blk + at.meta(ctx + path[i], v));
+    }
+#pragma unroll 1
+    for (int i = 0; i < A; ++i) {
+      if (path[i] < 0 || path[i] == i || !at.block(ctx + path[i])) continue;
+      uint8_t* blk = at.block(ctx + i);
+      if (blk) *reinterpret_cast<uint32_t*>(blk + at.meta(ctx + i, v)) = x[i];
     }
   }
-  uint32_t meta = 0;  // thread t: K (t even) or V word of record t / 2
-  bool have_meta = false;
-  if (FMT == 0 && t / 2 < A && spath[t / 2] >= 0 && spath[t / 2] != t / 2) {
-    const int pos = ctx + spath[t / 2];
-    const uint8_t* blk = block_of(pos);
-    have_meta = blk != nullptr;
-    if (blk) meta = reinterpret_cast<const uint32_t*>(blk + 2 * kPage * kRec4)[(t & 1) * kPage + pos % kPage];
+}
+
+template <int FMT>
+__global__ void __launch_bounds__(kCommitThreads) commit_kernel(const __grid_constant__ CacheSet cs, int N, const int32_t* ctx_len, const int32_t* path,
+                                                                const int32_t* n_accept, int32_t* ctx_out,
+                                                                int32_t* dev_err) {
+  constexpr int kChunks = CommitAt<FMT>::kChunks;
+  constexpr int kRecs = kCommitThreads * kCommitUnits / kChunks;  // records of a pass
+  __shared__ int32_t spath[KVQ_MAX_TREE];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int b = blockIdx.x / cs.heads, h = blockIdx.x % cs.heads, l0 = blockIdx.y * kCommitLayers;
+  const int t = threadIdx.x;
+  int x = t < N ? path[(size_t)b * N + t] : 0;
+  const int ctx = ctx_len[b], got = n_accept[b];
+  const int A = min(max(got, 0), N);
+  const bool lead = h == 0 && l0 == 0;  // one block reports a sequence's errors
+  if (lead && t == 0) {
+    if (ctx_out) ctx_out[b] = ctx + A;
+    if (A != got || ctx < 0 || ctx > kMaxPos) set_err(dev_err, KVQ_DEVERR_POS);
+  }
+  if (ctx < 0 || ctx > kMaxPos) return;
+  if (t < KVQ_MAX_TREE) {
+    if (t < A && (x < 0 || x >= N)) {
+      x = -1;
+      if (lead) set_err(dev_err, KVQ_DEVERR_POS);
+    }
+    spath[t] = x;
   }
   __syncthreads();
-#pragma unroll
-  for (int u = 0; u < kUnits; ++u) {
-    if (!have[u]) continue;
-    const int i = (u * kCommitThreads + t) / kChunks, c = t % kChunks;
-    uint8_t* blk = block_of(ctx + i);
-    if (blk) *reinterpret_cast<uint4*>(blk + chunk_at(ctx + i, c)) = v[u];
+  if (A > kRecs) {
+    const bool ascending = t >= A || (spath[t] >= t && (t == 0 || spath[t] > spath[t - 1]));
+    if (!__syncthreads_and(ascending)) {
+      for (int l = l0; l < min(l0 + kCommitLayers, cs.count); ++l) commit_any(CommitAt<FMT>{cs, b, h, l, dev_err}, ctx, A, spath);
+      return;
+    }
   }
-  if (have_meta) {
-    const int pos = ctx + t / 2;
-    uint8_t* blk = block_of(pos);
-    if (blk) reinterpret_cast<uint32_t*>(blk + 2 * kPage * kRec4)[(t & 1) * kPage + pos % kPage] = meta;
+  for (int i0 = 0; i0 < A; i0 += kRecs) {
+    uint4 v[kCommitLayers][kCommitUnits];
+    uint8_t* dst[kCommitLayers][kCommitUnits];  // null: nothing to move
+    uint32_t meta[kCommitLayers];
+    uint8_t* mdst[kCommitLayers];
+#pragma unroll
+    for (int ll = 0; ll < kCommitLayers; ++ll) {
+      const CommitAt<FMT> at{cs, b, h, min(l0 + ll, cs.count - 1), dev_err};
+#pragma unroll
+      for (int u = 0; u < kCommitUnits; ++u) {
+        const int i = i0 + (u * kCommitThreads + t) / kChunks, c = t % kChunks;
+        dst[ll][u] = nullptr;
+        if (l0 + ll < cs.count && i < A && spath[i] >= 0 && spath[i] != i) {
+          const uint8_t* from = at.block(ctx + spath[i]);
+          uint8_t* to = at.block(ctx + i);
+          if (from && to) {
+            v[ll][u] = *reinterpret_cast<const uint4*>(from + at.chunk(ctx + spath[i], c));
+            dst[ll][u] = to + at.chunk(ctx + i, c);
+          }
+        }
+      }
+      mdst[ll] = nullptr;
+      if (FMT == 0) {  // thread t: K (t even) or V word of record t / 2
+        const int i = i0 + t / 2;
+        if (t < 2 * kRecs && l0 + ll < cs.count && i < A && spath[i] >= 0 && spath[i] != i) {
+          const uint8_t* from = at.block(ctx + spath[i]);
+          uint8_t* to = at.block(ctx + i);
+          if (from && to) {
+            meta[ll] = *reinterpret_cast<const uint32_t*>(from + at.meta(ctx + spath[i], t & 1));
+            mdst[ll] = to + at.meta(ctx + i, t & 1);
+          }
+        }
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int ll = 0; ll < kCommitLayers; ++ll) {
+#pragma unroll
+      for (int u = 0; u < kCommitUnits; ++u) {
+        if (FMT == 1) {  // the place again: cheaper than keeping it
+          const CommitAt<FMT> at{cs, b, h, min(l0 + ll, cs.count - 1), dev_err};
+          const int i = i0 + (u * kCommitThreads + t) / kChunks;
+          if (dst[ll][u]) *reinterpret_cast<uint4*>(at.block(ctx + i) + at.chunk(ctx + i, t % kChunks)) = v[ll][u];
+        } else if (dst[ll][u]) {
+          *reinterpret_cast<uint4*>(dst[ll][u]) = v[ll][u];
+        }
+      }
+      if (FMT == 0 && mdst[ll]) *reinterpret_cast<uint32_t*>(mdst[ll]) = meta[ll];
+    }
+    __syncthreads();
   }
 }
 
@@ -583,6 +672,7 @@ cudaError_t launch_pages_compact(const PoolJob& j, cudaStream_t stream) {
   const cudaError_t e = launch_pdl(pages_compact_kernel, dim3(kPoolCtas), kPoolThreads, stream, params(j));
   if (e != cudaSuccess) return e;
   const long long n = (long long)j.num_seqs * j.max_pages_per_seq;
+  if (n <= kClusterTable) return e;
   const unsigned grid = (unsigned)std::min<long long>((n + 255) / 256, 8LL * device_sms());
   return launch_pdl(pages_remap_kernel, dim3(grid), 256, stream, params(j));
 }
@@ -596,7 +686,7 @@ cudaError_t launch_pages_copy(const CacheSet& cs, int n, const int32_t* src, con
 
 cudaError_t launch_tree_commit(int fmt, const CacheSet& cs, int B, int N, const int32_t* ctx_len, const int32_t* path,
                                const int32_t* n_accept, int32_t* ctx_out, int32_t* dev_err, cudaStream_t stream) {
-  const dim3 grid((unsigned)(B * cs.heads), (unsigned)cs.count);
+  const dim3 grid((unsigned)(B * cs.heads), (unsigned)((cs.count + kCommitLayers - 1) / kCommitLayers));
   return launch_pdl(fmt == 0 ? commit_kernel<0> : commit_kernel<1>, grid, kCommitThreads, stream, cs, N, ctx_len, path,
                     n_accept, ctx_out, dev_err);
 }

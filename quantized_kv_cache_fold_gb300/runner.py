@@ -14,8 +14,10 @@ from dataclasses import dataclass
 import numpy as np
 import torch
 
-from . import (HEAD_DIM, PAGE_SIZE, alloc_fp8_ring, alloc_int4_cache, alloc_workspace, kvq_build_rotation,
-               kvq_decode_attn_fp8_swa, kvq_decode_attn_int4, kvq_fold_qk, kvq_fold_qk_fwht, kvq_rotate_quant_append)
+from . import (HEAD_DIM, PAGE_SIZE, alloc_fp8_ring, alloc_int4_cache, alloc_prompt_workspace, alloc_tree_workspace,
+               alloc_workspace, kvq_build_rotation, kvq_decode_attn_fp8_swa, kvq_decode_attn_int4, kvq_fold_qk,
+               kvq_fold_qk_fwht, kvq_fp8_append, kvq_prompt_attn, kvq_rotate_quant_append, kvq_tree_attn_fp8_swa,
+               kvq_tree_attn_int4, kvq_tree_commit_fp8, kvq_tree_commit_int4)
 
 
 @dataclass
@@ -117,6 +119,55 @@ class DecodeStack:
         for l in range(len(self.layers)):
             self.decode_layer(l, qs[l], ctx, outs[l], None if k_news is None else k_news[l],
                               None if v_news is None else v_news[l], stream=stream)
+
+    # ---- around decoding
+
+    def prompt_layer(self, l, q, k, v, cu_seqlens, out, workspace=None, stream=None):
+        """Attention of whole prompts, packed end to end, in layer l (windowed in a sliding-window layer);
+        q, k and v as kvq_prompt_attn takes them. The keys and values go into the cache by
+        append_prompt."""
+        L = self.layers[l]
+        if workspace is None:
+            workspace = alloc_prompt_workspace(q.shape[0], cu_seqlens.shape[0] - 1, self.Hq, self.Hkv, self.device)
+        kvq_prompt_attn(q, k, v, cu_seqlens, out, workspace, self.dev_err,
+                        window=0 if isinstance(L, Int4Layer) else L.window, stream=stream)
+
+    def append_prompt(self, l, k, v, seq_ids, positions, stream=None):
+        """Keys (pre-norm in a full-attention layer) and values of prompt tokens into layer l's cache. A ring keeps
+        the last `capacity` positions of a sequence: pass no more of them in one call."""
+        L = self.layers[l]
+        if isinstance(L, Int4Layer):
+            self.append_int4(l, k, v, seq_ids, positions, stream=stream)
+        else:
+            kvq_fp8_append(L.ring, k, v, seq_ids, positions, L.k_scale, L.v_scale, self.dev_err, stream=stream)
+
+    def tree_layer(self, l, q, ctx, tree_mask, out, workspace, k_new=None, v_new=None, stream=None):
+        """Attention of every sequence's tree of drafted tokens in layer l (workspace: alloc_tree_workspace)."""
+        L = self.layers[l]
+        if isinstance(L, Int4Layer):
+            kvq_tree_attn_int4(L.cache, L.Mq, L.Mk, q, ctx, tree_mask, out, workspace, self.dev_err, k_new=k_new,
+                               v_new=v_new, stream=stream, fwht=L.fwht)
+        else:
+            kvq_tree_attn_fp8_swa(L.ring, q, ctx, tree_mask, L.window, L.k_scale, L.v_scale, out, workspace,
+                                  self.dev_err, k_new=k_new, v_new=v_new, stream=stream)
+
+    def tree_step(self, qs, ctx, tree_mask, outs, k_news=None, v_news=None, workspace=None, stream=None):
+        """One verify step over all layers: qs[l], outs[l], k_news[l], v_news[l] per layer."""
+        if workspace is None:
+            workspace = alloc_tree_workspace(qs[0].shape[0], qs[0].shape[1], self.Hq, self.Hkv, self.device)
+        for l in range(len(self.layers)):
+            self.tree_layer(l, qs[l], ctx, tree_mask, outs[l], workspace, None if k_news is None else k_news[l],
+                            None if v_news is None else v_news[l], stream=stream)
+
+    def commit_tree(self, ctx, path, n_accept, ctx_out, stream=None):
+        """The accepted branch of every tree becomes context in all layers; ctx_out: the new lengths."""
+        caches = [self.layers[l].cache for l in self.int4_layers()]
+        rings = [self.layers[l].ring for l in self.swa_layers()]
+        if caches:
+            kvq_tree_commit_int4(caches, ctx, path, n_accept, self.dev_err, ctx_out=ctx_out, stream=stream)
+        if rings:
+            kvq_tree_commit_fp8(rings, ctx, path, n_accept, self.dev_err, ctx_out=None if caches else ctx_out,
+                                stream=stream)
 
     def read_error(self) -> int:
         return int(self.dev_err.item())
