@@ -380,8 +380,10 @@ kvq_status kvq_prompt_attn(const void* q, const void* k, const void* v, kvq_dtyp
  *   workspace: device, >= kvq_tree_workspace_bytes(B, N, num_q_heads, num_kv_heads), 256-byte
  *             aligned; contents need no initialisation.
  *   Other arguments, readings of positions and errors as kvq_decode_attn_int4. A position whose
- *   block-table entry is outside the pool is skipped (KVQ_DEVERR_PAGE).
- * Requires 1 <= B <= KVQ_MAX_SEQS, 1 <= N <= KVQ_MAX_TREE, num_q_heads/num_kv_heads <= 64.
+ *   block-table entry is outside the pool is skipped (KVQ_DEVERR_PAGE). Slots of a page that were
+ *   never written are masked, but their scales are read: a pool is zeroed before its first use.
+ * Requires 1 <= B <= KVQ_MAX_SEQS, 1 <= N <= KVQ_MAX_TREE, num_q_heads/num_kv_heads <= 64,
+ * B*(max_pages_per_seq+2) <= 2^31.
  */
 size_t kvq_tree_workspace_bytes(int B, int N, int num_q_heads, int num_kv_heads);
 kvq_status kvq_tree_attn_int4(const kvq_int4_cache* cache, const float* Mq, const float* Mk, const void* q,

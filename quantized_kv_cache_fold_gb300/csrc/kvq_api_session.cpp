@@ -78,6 +78,24 @@ kvq_status tree_int4_impl(const kvq_int4_cache* cache, const float* Mq, const fl
   j.eps = eps;
   j.dev_err = dev_err;
   if (kvq::launch_prep(j, (cudaStream_t)stream) != cudaSuccess) return KVQ_ERR_CUDA;
+  if (N * (num_q_heads / cache->num_kv_heads) <= kvq::kTreeFewRows) {
+    kvq::AttnJob a{};
+    a.fmt = 0;
+    a.cache = *cache;
+    a.B = B;
+    a.S = N;
+    a.Hq = num_q_heads;
+    a.Hkv = cache->num_kv_heads;
+    a.ctx = ctx_len;
+    a.q_rot = j.q_rot;
+    a.sm_scale = sm_scale;
+    a.out = static_cast<float*>(out);
+    a.tree_mask = tree_mask;
+    a.out_bf16 = out_dtype == KVQ_BF16;
+    a.partials = reinterpret_cast<float*>(ws + kvq::workspace_qrot_bytes(B, N, num_q_heads));
+    a.dev_err = dev_err;
+    return from_cuda(kvq::launch_attention(a, (cudaStream_t)stream));
+  }
   kvq::TreeJob t{};
   t.fmt = 0;
   t.cache = *cache;
@@ -207,8 +225,10 @@ kvq_status kvq_prompt_attn(const void* q, const void* k, const void* v, kvq_dtyp
 
 size_t kvq_tree_workspace_bytes(int B, int N, int num_q_heads, int num_kv_heads) {
   if (!tree_sizes_ok(B, N, num_q_heads, num_kv_heads)) return 0;
+  const bool few = N * (num_q_heads / num_kv_heads) <= kvq::kTreeFewRows;
   return kvq::workspace_qrot_bytes(B, N, num_q_heads) +
-         kvq::workspace_tree_partials_bytes(B);
+         std::max(kvq::workspace_tree_partials_bytes(B),
+                  few ? kvq::workspace_partials_bytes(B, N, num_q_heads, num_kv_heads) : (size_t)0);
 }
 
 kvq_status kvq_tree_attn_int4(const kvq_int4_cache* cache, const float* Mq, const float* Mk, const void* q,

@@ -36,6 +36,8 @@
 #include <cstring>
 #include <mutex>
 
+#include <cuda_bf16.h>
+
 #include "kvq_device.cuh"
 #include "kvq_internal.h"
 
@@ -98,6 +100,9 @@ struct AttnParams {
   float score_scale;
   float* partials;
   float* out;
+  // TREE: bit j of word [b][r]: query row r of sequence b attends to the row at position ctx[b] + j
+  const uint64_t* tree_mask;
+  int out_bf16;  // TREE: out holds bf16
   int32_t* dev_err;
   int ntg, nkg, nstages, rows_pad;
   int n_cta;
@@ -216,6 +221,29 @@ __device__ __forceinline__ void decode_page(const int* pre, int B, int Hkv, long
 // CTA whose page range [floor(i P / n), floor((i+1) P / n)) contains page pg (n <= P).
 __device__ __forceinline__ long long cta_of(long long pg, long long P, int n) { return ((pg + 1) * n - 1) / P; }
 
+// TREE: whether row r of sequence b sees position pos (the context, and the drafted rows of its mask).
+__device__ __forceinline__ bool tree_sees(const AttnParams& p, int b, int r, int ctx, int pos) {
+  const int j = pos - ctx;
+  return j < 0 || (j < p.S && ((__ldg(reinterpret_cast<const unsigned long long*>(p.tree_mask) + (size_t)b * p.S + r) >> j) & 1ull));
+}
+
+// Stores n output values; TREE: of the type asked for, and 0 for rows that saw nothing.
+template <bool TREE>
+__device__ __forceinline__ void store2(const AttnParams& p, size_t at, float x, float y, float lsum) {
+  if (TREE) {
+    const float f = lsum == 0.0f ? 0.0f : 1.0f / lsum;
+    if (p.out_bf16) {
+      uint32_t w;
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(y * f), "f"(x * f));
+      *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(p.out) + at) = w;
+    } else {
+      *reinterpret_cast<float2*>(p.out + at) = make_float2(x * f, y * f);
+    }
+  } else {
+    *reinterpret_cast<float2*>(p.out + at) = make_float2(x / lsum, y / lsum);
+  }
+}
+
 __device__ __forceinline__ float h2f_lo(uint32_t x) {
   return __half2float(__ushort_as_half((unsigned short)(x & 0xFFFFu)));
 }
@@ -298,7 +326,7 @@ __device__ __forceinline__ void produce_pages(const AttnParams& p, const int* pr
 
 // Register caps: the int4 single-tile CTA (5 warps) must fit twice per SM, i.e. 3 warps per
 // SM sub-partition -> at most 170 registers.
-template <int FMT, int NT>
+template <int FMT, int NT, bool TREE>
 __global__ void __maxnreg__(NT == 1 ? (FMT == 0 ? KVQ_INT4_MAXREG : 184) : 255)
     attn_kernel(const AttnParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
@@ -474,7 +502,7 @@ __global__ void __maxnreg__(NT == 1 ? (FMT == 0 ? KVQ_INT4_MAXREG : 184) : 255)
       const int lp = lp0 + (int)(pg - seg_start);
       if (valid[s]) {
         const uint8_t* st = stages + (size_t)s * kStage;
-        const bool need_mask = FMT == 1 || (lp + 1) * kPage > ctxb + 1;
+        const bool need_mask = FMT == 1 || (lp + 1) * kPage > ctxb + (TREE ? 0 : 1);
 
 #pragma unroll
         for (int mt0 = 0; mt0 < 4; mt0 += MTU) {
@@ -600,7 +628,8 @@ __global__ void __maxnreg__(NT == 1 ? (FMT == 0 ? KVQ_INT4_MAXREG : 184) : 255)
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                   for (int j = 0; j < 2; ++j)
-                    if (pos < lim_lo[nt][j] || pos > lim_hi[nt][j]) sc[nt][u][2 * hh + j] = -INFINITY;
+                    if (TREE ? !tree_sees(p, b, lim_hi[nt][j] - ctxb, ctxb, pos) : (pos < lim_lo[nt][j] || pos > lim_hi[nt][j]))
+                      sc[nt][u][2 * hh + j] = -INFINITY;
               }
           }
 
@@ -937,7 +966,7 @@ __device__ __forceinline__ int tc_q_offset(int r, int kd) {
 
 // NR: softmax rows of the CTA (R rounded up to 8, at most 48); the MMAs take N = NR rounded up
 // to 16 (P columns beyond NR are never written: their D columns are not read).
-template <int NR>
+template <int NR, bool TREE>
 __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams p) {
   constexpr int H = NR / 2;  // rows of one softmax group (a multiple of 4)
   constexpr int NM = (NR + 15) & ~15;
@@ -1350,7 +1379,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
       // ---- scores of this token relative to each row's base; branch-free over the rows (padding
       // rows carry a -inf base); the causal limits apply only on a unit that reaches past the context
       const bool tvalid = ok && mt.z >= 0.0f;
-      const bool unit_mask = (ulp + unpg) * kPage - 1 > ctxb;
+      const bool unit_mask = (ulp + unpg) * kPage - (TREE ? 0 : 1) > ctxb;
       float mx = -INFINITY;
       if (!tvalid) {
   #pragma unroll
@@ -1377,7 +1406,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
         for (int i = 0; i < H; ++i) {
           const float4 c = rowc[r0 + i];
           const float sc = fmaf(d[i], mt.x, fmaf(mt.y, c.x, c.y));
-          d[i] = fpos <= c.w ? sc : -INFINITY;
+          const bool sees = TREE ? r0 + i < R && tree_sees(p, ui.x & 0xFFFF, (r0 + i) / G, ctxb, (ulp + jj) * kPage + slot) : fpos <= c.w;
+          d[i] = sees ? sc : -INFINITY;
           mx = fmaxf(mx, d[i]);
         }
       }
@@ -1578,7 +1608,7 @@ constexpr int kCombWarps = 8;
 constexpr int kCombChunkWarp = 4;
 constexpr int kCombChunkBlock = 8;
 
-template <int FMT>
+template <int FMT, bool TREE>
 __global__ void __launch_bounds__(kCombWarps * 32, 4) combine_rows_kernel(const AttnParams p) {
   extern __shared__ __align__(16) int cpre[];
   volatile int* flags = cpre + p.B + 1;
@@ -1648,13 +1678,13 @@ __global__ void __launch_bounds__(kCombWarps * 32, 4) combine_rows_kernel(const 
       }
     }
     const int r = row / p.G, gi = row - (row / p.G) * p.G;
-    float* dst = p.out + (((size_t)b * p.S + r) * p.Hq + h * p.G + gi) * kD;
-    reinterpret_cast<float2*>(dst)[lane] = make_float2(alo.x / lsum, alo.y / lsum);
-    reinterpret_cast<float2*>(dst + 64)[lane] = make_float2(ahi.x / lsum, ahi.y / lsum);
+    const size_t at = (((size_t)b * p.S + r) * p.Hq + h * p.G + gi) * kD + 2 * lane;
+    store2<TREE>(p, at, alo.x, alo.y, lsum);
+    store2<TREE>(p, at + 64, ahi.x, ahi.y, lsum);
   }
 }
 
-template <int FMT>
+template <int FMT, bool TREE>
 __global__ void __launch_bounds__(128, 4) combine_kernel(const AttnParams p) {
   extern __shared__ __align__(16) int cpre[];
   volatile int* flags = cpre + p.B + 1;
@@ -1713,39 +1743,48 @@ __global__ void __launch_bounds__(128, 4) combine_kernel(const AttnParams p) {
       }
     }
     const int r = row / p.G, gi = row - (row / p.G) * p.G;
-    p.out[(((size_t)b * p.S + r) * p.Hq + h * p.G + gi) * kD + d] = a / lsum;
+    const size_t at = (((size_t)b * p.S + r) * p.Hq + h * p.G + gi) * kD + d;
+    if (TREE) {
+      const float x = lsum == 0.0f ? 0.0f : a / lsum;  // a row that saw nothing: 0
+      if (p.out_bf16) reinterpret_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(x);
+      else p.out[at] = x;
+    } else {
+      p.out[at] = a / lsum;
+    }
   }
 }
 
 // Combine launch: a block per item while the items fit in one wave of 4 blocks per SM, else a
 // warp per item over at most one wave.
-template <int FMT>
+template <int FMT, bool TREE>
 cudaError_t launch_combine(cudaLaunchConfig_t& cfg, const AttnParams& p, int sm) {
   const long long items = (long long)p.B * p.Hkv * p.R;
   cfg.dynamicSmemBytes = (p.B + 1 + 4) * sizeof(int);
   if (items <= 4LL * sm) {
     cfg.gridDim = dim3((unsigned)std::max<long long>(1, items), 1, 1);
     cfg.blockDim = dim3(128, 1, 1);
-    return cudaLaunchKernelEx(&cfg, combine_kernel<FMT>, p);
+    return cudaLaunchKernelEx(&cfg, combine_kernel<FMT, TREE>, p);
   }
   cfg.gridDim = dim3((unsigned)std::min<long long>((items + kCombWarps - 1) / kCombWarps, 4LL * sm), 1, 1);
   cfg.blockDim = dim3(kCombWarps * 32, 1, 1);
-  return cudaLaunchKernelEx(&cfg, combine_rows_kernel<FMT>, p);
+  return cudaLaunchKernelEx(&cfg, combine_rows_kernel<FMT, TREE>, p);
 }
 
 struct DevCache {
   int sm = 0;
-  bool attr[2][4] = {{false}};
-  bool tc_attr[4] = {false, false, false, false};  // attn_tc_kernel<24 / 32 / 40 / 48>: shared-memory attribute set
-  size_t occ_smem[2][4] = {{0}};  // occupancy cache: last (smem, threads) queried per instantiation
-  int occ_threads[2][4] = {{0}};
-  int occ[2][4] = {{0}};
+  // by form: int4, fp8 ring, int4 tree
+  bool attr[3][4] = {{false}};
+  bool tc_attr[2][4] = {{false}};  // attn_tc_kernel<24 / 32 / 40 / 48>, verify block and tree: shared-memory attribute set
+  size_t occ_smem[3][4] = {{0}};  // occupancy cache: last (smem, threads) queried per instantiation
+  int occ_threads[3][4] = {{0}};
+  int occ[3][4] = {{0}};
 };
 DevCache g_dev[64];
 std::mutex g_dev_mu;  // guards g_dev (launch-configuration caches shared by host threads)
 
-template <int FMT, int NT>
+template <int FMT, int NT, bool TREE>
 cudaError_t launch_attn_t(AttnParams& p, size_t smem, int threads, long long p_max, cudaStream_t stream) {
+  constexpr int F = TREE ? 2 : FMT;
   int dev = 0;
   cudaGetDevice(&dev);
   cudaError_t e = cudaSuccess;
@@ -1758,20 +1797,20 @@ cudaError_t launch_attn_t(AttnParams& p, size_t smem, int threads, long long p_m
       cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
       dc.sm = n > 0 ? n : 1;
     }
-    if (!dc.attr[FMT][NT]) {
-      e = cudaFuncSetAttribute(attn_kernel<FMT, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024);
+    if (!dc.attr[F][NT]) {
+      e = cudaFuncSetAttribute(attn_kernel<FMT, NT, TREE>, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024);
       if (e != cudaSuccess) return e;
-      dc.attr[FMT][NT] = true;
+      dc.attr[F][NT] = true;
     }
-    if (dc.occ_smem[FMT][NT] != smem || dc.occ_threads[FMT][NT] != threads) {
+    if (dc.occ_smem[F][NT] != smem || dc.occ_threads[F][NT] != threads) {
       int o = 0;
-      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&o, attn_kernel<FMT, NT>, threads, smem);
+      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&o, attn_kernel<FMT, NT, TREE>, threads, smem);
       if (e != cudaSuccess) return e;
-      dc.occ[FMT][NT] = std::max(o, 1);
-      dc.occ_smem[FMT][NT] = smem;
-      dc.occ_threads[FMT][NT] = threads;
+      dc.occ[F][NT] = std::max(o, 1);
+      dc.occ_smem[F][NT] = smem;
+      dc.occ_threads[F][NT] = threads;
     }
-    occ = dc.occ[FMT][NT];
+    occ = dc.occ[F][NT];
     sm = dc.sm;
   }
   long long grid = std::min<long long>((long long)sm * occ, kMaxCtas);
@@ -1789,14 +1828,14 @@ cudaError_t launch_attn_t(AttnParams& p, size_t smem, int threads, long long p_m
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, attn_kernel<FMT, NT>, p);
+  e = cudaLaunchKernelEx(&cfg, attn_kernel<FMT, NT, TREE>, p);
   if (e != cudaSuccess) return e;
-  return launch_combine<FMT>(cfg, p, sm);
+  return launch_combine<FMT, TREE>(cfg, p, sm);
 }
 
 // int4 with more than 8 query rows per KV head: the tcgen05 kernel (NR = rows rounded up to 8),
 // one CTA per SM (it takes all 512 tensor-memory columns), then the same combine.
-template <int NR>
+template <int NR, bool TREE>
 cudaError_t launch_tc_t(AttnParams& p, long long p_max, cudaStream_t stream) {
   int dev = 0;
   cudaGetDevice(&dev);
@@ -1812,10 +1851,10 @@ cudaError_t launch_tc_t(AttnParams& p, long long p_max, cudaStream_t stream) {
       dc.sm = n > 0 ? n : 1;
     }
     static_assert(NR >= 24 && NR <= 48 && NR % 8 == 0, "attn_tc_kernel row counts: 24, 32, 40, 48");
-    if (!dc.tc_attr[NR / 8 - 3]) {
-      e = cudaFuncSetAttribute(attn_tc_kernel<NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+    if (!dc.tc_attr[TREE][NR / 8 - 3]) {
+      e = cudaFuncSetAttribute(attn_tc_kernel<NR, TREE>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
       if (e != cudaSuccess) return e;
-      dc.tc_attr[NR / 8 - 3] = true;
+      dc.tc_attr[TREE][NR / 8 - 3] = true;
     }
     sm = dc.sm;
   }
@@ -1836,9 +1875,9 @@ cudaError_t launch_tc_t(AttnParams& p, long long p_max, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, attn_tc_kernel<NR>, p);
+  e = cudaLaunchKernelEx(&cfg, attn_tc_kernel<NR, TREE>, p);
   if (e != cudaSuccess) return e;
-  return launch_combine<0>(cfg, p, sm);
+  return launch_combine<0, TREE>(cfg, p, sm);
 }
 
 }  // namespace
@@ -1886,15 +1925,20 @@ cudaError_t launch_attention(const AttnJob& job, cudaStream_t stream) {
     p.score_scale = job.sm_scale * kLog2e * job.k_scale;
     p_max = (long long)p.Hkv * p.B * (p.cap / kPage);
   }
+  p.tree_mask = job.tree_mask;
+  p.out_bf16 = job.out_bf16;
+  const bool tree = job.tree_mask != nullptr;
   const int ntiles = (p.R + 7) / 8;
   if (job.fmt == 0 && p.R > kTcMinRows) {
     switch ((p.R + 7) / 8) {
-      case 3: return launch_tc_t<24>(p, p_max, stream);
-      case 4: return launch_tc_t<32>(p, p_max, stream);
-      case 5: return launch_tc_t<40>(p, p_max, stream);
-      default: return launch_tc_t<48>(p, p_max, stream);
+      case 3: return tree ? launch_tc_t<24, true>(p, p_max, stream) : launch_tc_t<24, false>(p, p_max, stream);
+      case 4: return tree ? launch_tc_t<32, true>(p, p_max, stream) : launch_tc_t<32, false>(p, p_max, stream);
+      case 5: return tree ? launch_tc_t<40, true>(p, p_max, stream) : launch_tc_t<40, false>(p, p_max, stream);
+      default: return tree ? launch_tc_t<48, true>(p, p_max, stream) : launch_tc_t<48, false>(p, p_max, stream);
     }
   }
+  // (a tree's rows that get here, at most 16 per KV head, are one or two tiles)
+  static_assert(kTcMinRows == 16, "trees of up to kTcMinRows rows take one or two 8-row tiles");
   int NT;
   if (ntiles <= 3) {
     NT = ntiles;
@@ -1916,17 +1960,18 @@ cudaError_t launch_attention(const AttnJob& job, cudaStream_t stream) {
   const int threads = (p.ntg * p.nkg + 1) * 32;
   const SmemLayout L(job.fmt, p.nstages, p.B, p.nkg, p.rows_pad);
   const size_t smem = L.total;
+  if (tree) return NT == 1 ? launch_attn_t<0, 1, true>(p, smem, threads, p_max, stream) : launch_attn_t<0, 2, true>(p, smem, threads, p_max, stream);
   if (job.fmt == 0) {
     switch (NT) {
-      case 1: return launch_attn_t<0, 1>(p, smem, threads, p_max, stream);
-      case 2: return launch_attn_t<0, 2>(p, smem, threads, p_max, stream);
-      default: return launch_attn_t<0, 3>(p, smem, threads, p_max, stream);
+      case 1: return launch_attn_t<0, 1, false>(p, smem, threads, p_max, stream);
+      case 2: return launch_attn_t<0, 2, false>(p, smem, threads, p_max, stream);
+      default: return launch_attn_t<0, 3, false>(p, smem, threads, p_max, stream);
     }
   }
   switch (NT) {
-    case 1: return launch_attn_t<1, 1>(p, smem, threads, p_max, stream);
-    case 2: return launch_attn_t<1, 2>(p, smem, threads, p_max, stream);
-    default: return launch_attn_t<1, 3>(p, smem, threads, p_max, stream);
+    case 1: return launch_attn_t<1, 1, false>(p, smem, threads, p_max, stream);
+    case 2: return launch_attn_t<1, 2, false>(p, smem, threads, p_max, stream);
+    default: return launch_attn_t<1, 3, false>(p, smem, threads, p_max, stream);
   }
 }
 

@@ -75,6 +75,8 @@ struct AttnJob {
   const void* v_new;
   float sm_scale;
   float* out;
+  const uint64_t* tree_mask;  // int4: a tree of S drafted tokens in place of a verify block (null: none)
+  int out_bf16;               // with tree_mask: out holds bf16
   float* partials;  // workspace
   int32_t* dev_err;
 };
@@ -139,6 +141,12 @@ struct TreeJob {
   float* partials;  // workspace
   int32_t* dev_err;
 };
+// Trees of up to this many rows per KV head (drafted tokens x query heads per KV head) over the int4 cache take the
+// verify block's kernels (launch_attention) with the mask in place of the diagonal: those multiply the codes as they are
+// and scale the scores, so few rows cost little, where launch_tree first makes fp16 tiles of every token. 64 sequences of
+// 16,384 tokens, 4 KV heads, verify kernels / launch_tree: 106 / 265 us with 5 rows, 164 / 268 with 15, 195 / 270 with
+// 20, 254 / 296 with 45; 8 of 8,192: 21 / 35, 31 / 37, 29 / 38, 40 / 43; one of 4,096: 21-25 / 23-24 throughout.
+constexpr int kTreeFewRows = kMaxRows;
 size_t workspace_tree_partials_bytes(int B);
 cudaError_t launch_tree(const TreeJob& job, cudaStream_t stream);
 

@@ -258,6 +258,39 @@ def test_int4_repeats_bitwise_streams_and_graph():
         assert torch.equal(out, first)
 
 
+@pytest.mark.parametrize("rows,heads", [(r, h) for r in (16, 17, 24, 25, 32, 33, 40, 41, 48, 49) for h in [(2, 2)]] +
+                         [(r, (16, 1)) for r in (16, 32, 48, 64)])
+def test_int4_rows_per_kv_head(rows, heads):
+    c = Int4Case([3, 64, 190, 1500, 0, 127], rows // (heads[0] // heads[1]), *heads, seed=rows)
+    masks = [tree(c.N, c.rng) for _ in range(c.B)]
+    c.check(c.call(masks), masks)
+
+
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("N,heads,copies", [(3, (2, 2), 1), (3, (2, 2), 200), (14, (2, 2), 1), (14, (2, 2), 300), (10, (4, 1), 150),
+                                            (20, (4, 1), 1), (20, (4, 1), 150)])
+def test_int4_empty_rows_of_every_size(N, heads, copies, out_dtype):
+    c = Int4Case([0, 70, 0] * copies, N, *heads, seed=N + copies)
+    masks = [[0 if i % 3 else 1 << i for i in range(N)], [0] * N, [0] * N] * copies
+    out = c.call(masks, out_dtype)
+    for b in range(0, c.B, 3):
+        assert bool((out[b + 2] == 0).all()) and all(bool((out[b, i] == 0).all()) for i in range(N) if i % 3)
+    c.B = min(c.B, 9)  # enough of the copies for the plain evaluation
+    c.check(out, masks[:c.B])
+
+
+@pytest.mark.parametrize("N,heads", [(2, (8, 2)), (8, (20, 4)), (16, (20, 4))])
+def test_int4_a_far_larger_key_in_a_hidden_drafted_token(N, heads):
+    """The scores of hidden drafted tokens may pass the visible ones by any amount."""
+    c = Int4Case([130, 4], N, *heads, seed=77)
+    c.v_new[:, N - 1] *= 100.0
+    masks = [[w & ~(1 << (N - 1)) for w in chain(N)]] * 2
+    a = c.call(masks, sm=1.0)
+    c.check(a, masks, sm=1.0)
+    c.k_new[:, N - 1] = -c.k_new[:, N - 1]
+    assert torch.equal(a, c.call(masks, sm=1.0))
+
+
 # ---------------------------------------------------------------- the ring
 
 class RingCase:
