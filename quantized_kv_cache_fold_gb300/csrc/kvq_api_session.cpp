@@ -261,6 +261,32 @@ kvq_status kvq_tree_attn_fp8_swa(const kvq_fp8_ring* ring, const void* q, kvq_dt
   if (st != KVQ_OK) return st;
   if (window < N || (long long)window + N - 1 > ring->capacity) return KVQ_ERR_INVALID_ARG;
   if (!(k_scale > 0.0f) || !(v_scale > 0.0f) || std::isinf(k_scale) || std::isinf(v_scale)) return KVQ_ERR_INVALID_ARG;
+  const bool few_pairs = (long long)B * ring->num_kv_heads < kvq::device_sms();
+  if (N <= kvq::kTreeRingTokens &&
+      N * (num_q_heads / ring->num_kv_heads) <= (few_pairs ? kvq::kTreeRingRowsFewPairs : kvq::kTreeRingRows) &&
+      kvq::swa_cluster_path(ring->capacity, B, N, num_q_heads, ring->num_kv_heads)) {
+    kvq::AttnJob a{};
+    a.fmt = 1;
+    a.ring = *ring;
+    a.window = window;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.B = B;
+    a.S = N;
+    a.Hq = num_q_heads;
+    a.Hkv = ring->num_kv_heads;
+    a.ctx = pos0;
+    a.q = q;
+    a.q_bf16 = dtype == KVQ_BF16;
+    a.k_new = k_new;
+    a.v_new = v_new;
+    a.sm_scale = sm_scale;
+    a.out = static_cast<float*>(out);
+    a.tree_mask = tree_mask;
+    a.out_bf16 = out_dtype == KVQ_BF16;
+    a.dev_err = dev_err;
+    return from_cuda(kvq::launch_swa_cluster(a, (cudaStream_t)stream));
+  }
   if (k_new) {
     kvq::Fp8AppendJob j{};
     j.ring = *ring;

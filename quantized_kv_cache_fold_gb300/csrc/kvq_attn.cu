@@ -233,9 +233,7 @@ __device__ __forceinline__ void store2(const AttnParams& p, size_t at, float x, 
   if (TREE) {
     const float f = lsum == 0.0f ? 0.0f : 1.0f / lsum;
     if (p.out_bf16) {
-      uint32_t w;
-      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(y * f), "f"(x * f));
-      *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(p.out) + at) = w;
+      *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(p.out) + at) = bf16x2_of(x * f, y * f);
     } else {
       *reinterpret_cast<float2*>(p.out + at) = make_float2(x * f, y * f);
     }

@@ -269,6 +269,13 @@ __device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
   return d;
 }
 
+// x in the low half, y in the high half, each rounded to bf16 (off by at most half a step, 2^-8 of the value).
+__device__ __forceinline__ uint32_t bf16x2_of(float x, float y) {
+  uint32_t w;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(y), "f"(x));
+  return w;
+}
+
 __device__ __forceinline__ float bf16_bits_to_f32(uint32_t b) { return __uint_as_float(b << 16); }
 
 __device__ __forceinline__ float fast_exp2(float x) {

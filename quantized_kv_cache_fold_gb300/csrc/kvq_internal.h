@@ -75,7 +75,8 @@ struct AttnJob {
   const void* v_new;
   float sm_scale;
   float* out;
-  const uint64_t* tree_mask;  // int4: a tree of S drafted tokens in place of a verify block (null: none)
+  // A tree of S drafted tokens in place of a verify block (null: none); int4, and rings on the cluster path.
+  const uint64_t* tree_mask;
   int out_bf16;               // with tree_mask: out holds bf16
   float* partials;  // workspace
   int32_t* dev_err;
@@ -147,6 +148,12 @@ struct TreeJob {
 // 16,384 tokens, 4 KV heads, verify kernels / launch_tree: 106 / 265 us with 5 rows, 164 / 268 with 15, 195 / 270 with
 // 20, 254 / 296 with 45; 8 of 8,192: 21 / 35, 31 / 37, 29 / 38, 40 / 43; one of 4,096: 21-25 / 23-24 throughout.
 constexpr int kTreeFewRows = kMaxRows;
+// Over a ring, trees of up to 8 drafted tokens and 16 rows, or 24 rows while there are fewer (sequence, KV head) pairs
+// than SMs, take the verify block's cluster kernel where the ring is small enough for it (swa_cluster_path): one launch
+// with the append in it. Rings of 576 slots (window 513), 4 KV heads, cluster kernel / launch_tree: one sequence 6.4 /
+// 18.1 us with 5 rows, 9.0 / 18.6 with 10, 13.9 / 19.0 with 20; 8 sequences 6.5 / 22.9, 9.5 / 23.2, 14.3 / 24.5; 64
+// sequences 13.5 / 22.4, 20.1 / 22.4, but 30.9 / 23.2 with 20; 256 sequences 37 / 71, 51 / 72, 70 / 74.
+constexpr int kTreeRingRows = 16, kTreeRingRowsFewPairs = 24, kTreeRingTokens = 8;
 size_t workspace_tree_partials_bytes(int B);
 cudaError_t launch_tree(const TreeJob& job, cudaStream_t stream);
 

@@ -81,6 +81,8 @@ struct SwaParams {
   const void* v_new;
   float k_scale, v_scale, score_scale;
   float* out;
+  const uint64_t* tree_mask;  // TREE: bit j of word [b][r]: row r attends to the row at position pos0[b] + j
+  int out_bf16;               // TREE: out holds bf16
   int32_t* dev_err;
   int cs, nws, ntg, nst, rows_pad;
 };
@@ -147,10 +149,11 @@ __device__ __forceinline__ int unit_lane_offset(int slot, int lane) {
 }
 
 // One 32-slot unit (K records then V records at `st`, unit index u) against the warp's query tiles.
-template <int NT>
+template <int NT, bool TREE>
 __device__ __forceinline__ void attend_unit(const uint8_t* st, int u, int p_last, int slot_last, int cap,
                                             float score_scale, const uint32_t (&qf)[NT][8][2],
                                             const int (&lim_lo)[NT][2], const int (&lim_hi)[NT][2],
+                                            const uint32_t (&tm)[NT][2],
                                             float (&m)[NT][2], float (&l)[NT][2], float (&acc)[NT][8][4],
                                             int lane) {
   const int g = lane >> 2, t = lane & 3;
@@ -195,7 +198,9 @@ __device__ __forceinline__ void attend_unit(const uint8_t* st, int u, int p_last
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int jj = 0; jj < 2; ++jj)
-          if (pos < lim_lo[nt][jj] || pos > lim_hi[nt][jj]) sc[nt][mt][2 * hh + jj] = -INFINITY;
+          if (pos < lim_lo[nt][jj] ||
+              (pos > lim_hi[nt][jj] && !(TREE && ((tm[nt][jj] >> (pos - lim_hi[nt][jj] - 1)) & 1u))))
+            sc[nt][mt][2 * hh + jj] = -INFINITY;
     }
   // ---- online softmax
   float muse[NT][2];
@@ -277,7 +282,9 @@ __device__ __forceinline__ int ld_relaxed_s32(const int* p) {
   return v;
 }
 
-template <int NT>
+// TREE: the S rows of a sequence are a tree of drafted tokens. Row r stands at position c0 + (rows it sees) - 1, attends
+// to the context from there back over the window and to the drafted rows of its mask; a row that sees nothing gives 0.
+template <int NT, bool TREE>
 __global__ void __launch_bounds__(256, 1) swa_cluster_kernel(const SwaParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -447,6 +454,7 @@ __global__ void __launch_bounds__(256, 1) swa_cluster_kernel(const SwaParams p) 
 
   // ---- per-row window limits
   int lim_lo[NT][2], lim_hi[NT][2];
+  uint32_t tm[NT][2];  // TREE: drafted rows this one attends to, from position lim_hi + 1 on
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -455,6 +463,12 @@ __global__ void __launch_bounds__(256, 1) swa_cluster_kernel(const SwaParams p) 
       const int r = nC < p.R ? nC / p.G : 0;
       lim_hi[nt][jj] = c0 + r;
       lim_lo[nt][jj] = max(0, c0 + r - p.window + 1);
+      tm[nt][jj] = 0;
+      if (TREE) {
+        tm[nt][jj] = (uint32_t)p.tree_mask[(size_t)b * p.S + r] & ((1u << p.S) - 1u);
+        lim_hi[nt][jj] = c0 - 1;
+        lim_lo[nt][jj] = max(0, c0 + max(1, __popc(tm[nt][jj])) - p.window);
+      }
     }
   }
 
@@ -534,7 +548,7 @@ __global__ void __launch_bounds__(256, 1) swa_cluster_kernel(const SwaParams p) 
       }
       __syncwarp();
     }
-    attend_unit<NT>(st, u, p_last, slot_last, p.cap, p.score_scale, qf, lim_lo, lim_hi, m, l, acc, lane);
+    attend_unit<NT, TREE>(st, u, p_last, slot_last, p.cap, p.score_scale, qf, lim_lo, lim_hi, tm, m, l, acc, lane);
     done = k + 1;
     __syncwarp();
     // refill this stage with the stream's next unit that holds a window position
@@ -566,13 +580,17 @@ __global__ void __launch_bounds__(256, 1) swa_cluster_kernel(const SwaParams p) 
         const float lt = warp_sum_g(l[nt][jj]);
         const int row = (tg * NT + nt) * 8 + 2 * t + jj;
         if (row < p.R) {
-          const float inv = 1.0f / lt;
+          const float inv = TREE && lt == 0.0f ? 0.0f : 1.0f / lt;
           const int r = row / p.G, gi = row - (row / p.G) * p.G;
-          float* dst = p.out + (((size_t)b * p.S + r) * p.Hq + h * p.G + gi) * kD + 2 * g;
+          const size_t at = (((size_t)b * p.S + r) * p.Hq + h * p.G + gi) * kD + 2 * g;
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            *reinterpret_cast<float2*>(dst + 16 * i) =
-                make_float2(acc[nt][i][jj] * p.v_scale * inv, acc[nt][i][2 + jj] * p.v_scale * inv);
+          for (int i = 0; i < 8; ++i) {
+            const float x = acc[nt][i][jj] * p.v_scale * inv, y = acc[nt][i][2 + jj] * p.v_scale * inv;
+            if (TREE && p.out_bf16)
+              *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(p.out) + at + 16 * i) = bf16x2_of(x, y);
+            else
+              *reinterpret_cast<float2*>(p.out + at + 16 * i) = make_float2(x, y);
+          }
         }
       }
     }
@@ -681,15 +699,22 @@ __global__ void __launch_bounds__(256, 1) swa_cluster_kernel(const SwaParams p) 
       a[7] = fmaf(wgt, v1.w, a[7]);
     }
     const int r = row / p.G, gi = row - (row / p.G) * p.G;
-    const float inv = 1.0f / lsum;
-    float4* dst = reinterpret_cast<float4*>(p.out + (((size_t)b * p.S + r) * p.Hq + h * p.G + gi) * kD) + 2 * c8;
+    const float inv = TREE && lsum == 0.0f ? 0.0f : 1.0f / lsum;
+    const size_t at = (((size_t)b * p.S + r) * p.Hq + h * p.G + gi) * kD + 8 * c8;
+    if (TREE && p.out_bf16) {
+      *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + at) =
+          make_uint4(bf16x2_of(a[0] * inv, a[1] * inv), bf16x2_of(a[2] * inv, a[3] * inv),
+                     bf16x2_of(a[4] * inv, a[5] * inv), bf16x2_of(a[6] * inv, a[7] * inv));
+      continue;
+    }
+    float4* dst = reinterpret_cast<float4*>(p.out + at);
     dst[0] = make_float4(a[0] * inv, a[1] * inv, a[2] * inv, a[3] * inv);
     dst[1] = make_float4(a[4] * inv, a[5] * inv, a[6] * inv, a[7] * inv);
   }
 }
 
 struct SwaDevCache {
-  bool attr[4] = {false};
+  bool attr[2][4] = {{false}};  // verify block, tree
   int sm = 0;
   int occ[4][3][kMaxStreams + 1][KVQ_SWA_BATCH_STAGES + 1] = {};  // resident CTAs per SM by [NT][ntg][nws][nst]
 };
@@ -699,22 +724,22 @@ std::mutex g_swa_mu;  // guards g_swa_dev
 SwaDevCache& dev_cache(int dev) { return g_swa_dev[(dev >= 0 && dev < 64) ? dev : 0]; }
 
 // Call with g_swa_mu held: allow the kernel its dynamic shared memory (once per device).
-template <int NT>
+template <int NT, bool TREE>
 cudaError_t ensure_attr(SwaDevCache& dc) {
-  if (dc.attr[NT]) return cudaSuccess;
+  if (dc.attr[TREE][NT]) return cudaSuccess;
   const cudaError_t e =
-      cudaFuncSetAttribute(swa_cluster_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemCap);
-  if (e == cudaSuccess) dc.attr[NT] = true;
+      cudaFuncSetAttribute(swa_cluster_kernel<NT, TREE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemCap);
+  if (e == cudaSuccess) dc.attr[TREE][NT] = true;
   return e;
 }
 
-template <int NT>
+template <int NT, bool TREE>
 cudaError_t launch_swa_t(const SwaParams& p, size_t smem, cudaStream_t stream) {
   int dev = 0;
   cudaGetDevice(&dev);
   {
     std::lock_guard<std::mutex> lock(g_swa_mu);
-    const cudaError_t e = ensure_attr<NT>(dev_cache(dev));
+    const cudaError_t e = ensure_attr<NT, TREE>(dev_cache(dev));
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg{};
@@ -732,13 +757,13 @@ cudaError_t launch_swa_t(const SwaParams& p, size_t smem, cudaStream_t stream) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, swa_cluster_kernel<NT>, p);
+  return cudaLaunchKernelEx(&cfg, swa_cluster_kernel<NT, TREE>, p);
 }
 
 template <int NT>
 int occupancy_t(int threads, size_t smem) {
   int n = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, swa_cluster_kernel<NT>, threads, smem) != cudaSuccess)
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, swa_cluster_kernel<NT, false>, threads, smem) != cudaSuccess)
     return 0;
   return n;
 }
@@ -771,9 +796,9 @@ int ctas_per_sm(int dev, const SwaPlan& pl) {
     const int threads = pl.nws * pl.ntg * 32;
     cudaError_t e;
     switch (pl.NT) {
-      case 1: e = ensure_attr<1>(dc); o = e == cudaSuccess ? occupancy_t<1>(threads, pl.smem) : 0; break;
-      case 2: e = ensure_attr<2>(dc); o = e == cudaSuccess ? occupancy_t<2>(threads, pl.smem) : 0; break;
-      default: e = ensure_attr<3>(dc); o = e == cudaSuccess ? occupancy_t<3>(threads, pl.smem) : 0; break;
+      case 1: e = ensure_attr<1, false>(dc); o = e == cudaSuccess ? occupancy_t<1>(threads, pl.smem) : 0; break;
+      case 2: e = ensure_attr<2, false>(dc); o = e == cudaSuccess ? occupancy_t<2>(threads, pl.smem) : 0; break;
+      default: e = ensure_attr<3, false>(dc); o = e == cudaSuccess ? occupancy_t<3>(threads, pl.smem) : 0; break;
     }
   }
   return o;
@@ -866,10 +891,19 @@ cudaError_t launch_swa_cluster(const AttnJob& job, cudaStream_t stream) {
   p.ntg = pl.ntg;
   p.nst = pl.nst;
   p.rows_pad = pl.rows_pad;
+  p.tree_mask = job.tree_mask;
+  p.out_bf16 = job.out_bf16;
+  if (p.tree_mask) {
+    switch (pl.NT) {
+      case 1: return launch_swa_t<1, true>(p, pl.smem, stream);
+      case 2: return launch_swa_t<2, true>(p, pl.smem, stream);
+      default: return launch_swa_t<3, true>(p, pl.smem, stream);
+    }
+  }
   switch (pl.NT) {
-    case 1: return launch_swa_t<1>(p, pl.smem, stream);
-    case 2: return launch_swa_t<2>(p, pl.smem, stream);
-    default: return launch_swa_t<3>(p, pl.smem, stream);
+    case 1: return launch_swa_t<1, false>(p, pl.smem, stream);
+    case 2: return launch_swa_t<2, false>(p, pl.smem, stream);
+    default: return launch_swa_t<3, false>(p, pl.smem, stream);
   }
 }
 

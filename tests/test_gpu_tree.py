@@ -363,6 +363,26 @@ def test_ring_empty_rows():
     c.check(out, [[0, 1, 0, 2]])
 
 
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("copies", [1, 40])
+@pytest.mark.parametrize("N,heads,window", [(1, (20, 4), 513), (2, (20, 4), 100), (4, (20, 4), 513), (5, (8, 8), 5), (8, (2, 2), 513), (8, (6, 2), 8),
+                                            (8, (3, 1), 4000), (3, (8, 1), 64), (8, (8, 2), 513)])
+def test_ring_few_rows(N, heads, window, copies, out_dtype):
+    """Few rows of one KV head, few and many sequences; trees, tokens that see nothing, tokens without themselves."""
+    c = RingCase([0, 1, 5, window, 700, 5001] * copies, N, *heads, window, seed=N + window, dtype=torch.float32)
+    masks = [[tree(N, c.rng), [0] * N, [(1 << 60) | (1 << (N - 1 - i)) for i in range(N)]][b % 3] for b in range(c.B)]
+    keep = c.tensors["data"].clone()
+    out = c.call(masks, out_dtype)
+    c.B, c.pos0 = min(c.B, 18), c.pos0[:18]
+    c.check(out, [[w & (1 << N) - 1 for w in m] for m in masks])
+    now = c.tensors["data"].clone()
+    c.tensors["data"].copy_(keep)  # the ring after the call: as after the separate append
+    seq = torch.arange(len(masks), device="cuda", dtype=torch.int32).repeat_interleave(N)
+    pos = (c.pos_t[:, None] + torch.arange(N, device="cuda", dtype=torch.int32)).flatten()
+    kvq.kvq_fp8_append(c.ring, c.k_new.flatten(0, 1), c.v_new.flatten(0, 1), seq, pos, c.KS, c.VS, c.err)
+    assert torch.equal(now, c.tensors["data"])
+
+
 # ---------------------------------------------------------------- the commits
 
 def logical4(c, b, L):
