@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(256, 1) swa_cluster_kernel(const SwaParams p) 
         prefetch_l2_bulk(blk + kPage * kRec8, kHalf);
       }
     } else if (tg == 0) {
-      const int ch = max(0, ld_relaxed_s32(p.pos0 + b));
+      const int ch = TREE ? min(max(0, ld_relaxed_s32(p.pos0 + b)), 1 << 30) : max(0, ld_relaxed_s32(p.pos0 + b));
       const int pl = ch + p.S - 1, sl = pl % p.cap, sp = pl - max(0, ch - p.window + 1);
       for (int i = 0, n = 0; i < nu && n < 2 * p.nst; ++i) {
         const int u = stream + i * nstream;
@@ -378,10 +378,12 @@ __global__ void __launch_bounds__(256, 1) swa_cluster_kernel(const SwaParams p) 
   }
 
   int c0 = c0raw;
-  if (c0 < 0) {
+  if (c0 < 0 || (TREE && c0 > 1 << 30)) {
     if (rank == 0 && threadIdx.x == 0) set_err(p.dev_err, KVQ_DEVERR_POS);
-    c0 = 0;
+    c0 = TREE && c0 > 0 ? 1 << 30 : 0;
   }
+  // TREE: as in the separate append, a new row goes where its own position says, or nowhere
+  const int a0 = TREE ? c0raw : c0;
   const int p_last = c0 + p.S - 1;  // newest position after the append
   const int slot_last = p_last % p.cap;
 
@@ -480,7 +482,9 @@ __global__ void __launch_bounds__(256, 1) swa_cluster_kernel(const SwaParams p) 
     for (int r = 0; r < 8; ++r) {
       code[r][0] = code[r][1] = 0;
       if (r >= p.S) continue;
-      const int slot = (c0 + r) % p.cap;
+      const int pos = TREE ? (int)((uint32_t)a0 + (uint32_t)r) : c0 + r;
+      if (TREE && pos < 0) continue;
+      const int slot = pos % p.cap;
       const int u = slot / kUnit;
       if (u < stream || (u - stream) % nstream != 0) continue;
       const size_t row = ((size_t)b * p.S + r) * p.Hkv + h;
@@ -498,7 +502,7 @@ __global__ void __launch_bounds__(256, 1) swa_cluster_kernel(const SwaParams p) 
           continue;
         }
         code[r][which] = fp8_encode4(x, which ? p.v_scale : p.k_scale);
-        have |= 1u << (2 * r + which);
+        if (!TREE || a0 == c0) have |= 1u << (2 * r + which);
         if (tg == 0)  // the ring copy for later steps, written once per unit
           *reinterpret_cast<uint32_t*>(seg + (size_t)(slot / kPage) * kBlk + which * kPage * kRec8 +
                                        fp8_lane_offset(slot, lane)) = code[r][which];

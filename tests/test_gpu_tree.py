@@ -383,6 +383,30 @@ def test_ring_few_rows(N, heads, window, copies, out_dtype):
     assert torch.equal(now, c.tensors["data"])
 
 
+@pytest.mark.parametrize("N", [2, 10])
+@pytest.mark.parametrize("bad", [-3, -(1 << 31), (1 << 31) - 1])
+def test_ring_positions_outside_are_flagged(N, bad):
+    c = RingCase([100, 700], N, 8, 2, 513, seed=6)
+    masks = [tree(N, c.rng) for _ in range(2)]
+    c.pos_t = i32([100, bad])
+    was = c.tensors["data"].clone()
+    out = torch.full((2, N, 8, D), 9.0, device="cuda")
+    kvq.kvq_tree_attn_fp8_swa(c.ring, c.q, c.pos_t, words(masks), 513, c.KS, c.VS, out, kvq.alloc_tree_workspace(2, N, 8, 2), c.err,
+                              k_new=c.k_new, v_new=c.v_new)
+    torch.cuda.synchronize()
+    assert c.err.item() == kvq.DEVERR_POS
+    now = c.tensors["data"].clone()
+    c.tensors["data"].copy_(was)  # new rows are written where their own positions are any
+    rows = [(b, i) for b, p in enumerate([100, bad]) for i in range(N) if 0 <= p + i < 1 << 31]
+    pick = lambda x: torch.stack([x[b, i] for b, i in rows])  # noqa: E731
+    kvq.kvq_fp8_append(c.ring, pick(c.k_new), pick(c.v_new), i32([b for b, _ in rows]), i32([[100, bad][b] + i for b, i in rows]),
+                       c.KS, c.VS, c.err)
+    assert torch.equal(now, c.tensors["data"])
+    c.tensors["data"].copy_(now)
+    c.B, c.pos0 = 1, [100]  # the other sequence is as ever
+    c.check(out, masks)
+
+
 # ---------------------------------------------------------------- the commits
 
 def logical4(c, b, L):

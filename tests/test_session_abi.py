@@ -80,7 +80,7 @@ def test_tree_int4_refuses_bad_caches():
     assert tree4(cache(head_dim=64)) == UNSUPPORTED
     assert tree4(cache(page_size=32)) == UNSUPPORTED
     assert tree4(cache(pages=0x10008)) == INVALID
-    assert tree4(cache(max_pages_per_seq=2 ** 30)) == UNSUPPORTED
+    assert tree4(cache(max_pages_per_seq=2 ** 21, num_seqs=1024), B=1024) == UNSUPPORTED
     assert kvq.kvq_tree_workspace_bytes(2, 65, 20, 4) == 0 == kvq.kvq_tree_workspace_bytes(0, 6, 20, 4)
 
 
