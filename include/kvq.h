@@ -420,7 +420,8 @@ kvq_status kvq_tree_attn_fp8_swa(const kvq_fp8_ring* ring, const void* q, kvq_dt
  *   of num_caches layers in one launch. All of a sequence's records are read before any is
  *   written, so any path (also with repeated tokens) gives the records as they were before.
  *   caches / rings: host array of num_caches descriptors (1..KVQ_MAX_CACHES), of the same number of
- *             KV heads (rings: of the same capacity); each with its own block table.
+ *             KV heads (rings: of the same capacity); each with its own block table. No layer twice,
+ *             and the drafted positions' pages belong to one sequence each.
  *   path:     device int32[B][N], the accepted tokens in order; an entry outside 0..N-1 within the
  *             first n_accept[b] is skipped (KVQ_DEVERR_POS).
  *   n_accept: device int32[B], clamped to 0..N (KVQ_DEVERR_POS if it had to be).

@@ -123,6 +123,14 @@ kvq_status check_commit(int num_caches, int B, int N, const int32_t* ctx, const 
   return KVQ_OK;
 }
 
+// Whether two layers of a call are the same memory (a commit would move its records twice at once).
+bool repeated(const kvq::CacheSet& cs) {
+  for (int i = 1; i < cs.count; ++i)
+    for (int k = 0; k < i; ++k)
+      if (cs.pages[i] == cs.pages[k]) return true;
+  return false;
+}
+
 // The caches of one call, checked; all of one number of KV heads.
 kvq_status cache_set(const kvq_int4_cache* caches, int num_caches, kvq::CacheSet& cs) {
   if (!caches || num_caches < 1) return KVQ_ERR_INVALID_ARG;
@@ -334,6 +342,7 @@ kvq_status kvq_tree_commit_int4(const kvq_int4_cache* caches, int num_caches, in
   if (st != KVQ_OK) return st;
   for (int i = 0; i < num_caches; ++i)
     if (B > caches[i].num_seqs) return KVQ_ERR_INVALID_ARG;
+  if (repeated(cs)) return KVQ_ERR_INVALID_ARG;
   return from_cuda(
       kvq::launch_tree_commit(0, cs, B, N, ctx_len, path, n_accept, ctx_out, dev_err, (cudaStream_t)stream));
 }
@@ -356,6 +365,7 @@ kvq_status kvq_tree_commit_fp8(const kvq_fp8_ring* rings, int num_caches, int B,
     cs.num_seqs[i] = rings[i].num_seqs;
     cs.max_pages[i] = rings[i].capacity / KVQ_PAGE_SIZE;
   }
+  if (repeated(cs)) return KVQ_ERR_INVALID_ARG;
   return from_cuda(
       kvq::launch_tree_commit(1, cs, B, N, pos0, path, n_accept, ctx_out, dev_err, (cudaStream_t)stream));
 }

@@ -108,12 +108,12 @@ def test_tree_ring_refuses_bad_rings():
 
 def test_commit_refuses():
     def c4(cs=None, n=None, B=2, N=8, ctx=0x1000, path=0x2000, acc=0x3000, out=None, err=0x5000):
-        cs = cs or [cache(), cache()]
+        cs = cs or [cache(), cache(pages=0x20000)]
         return L.kvq_tree_commit_int4((kvq.Int4Cache * len(cs))(*cs), len(cs) if n is None else n, B, N, ctx, path, acc, out, err, None)
 
     for over in (dict(n=0), dict(B=0), dict(B=5), dict(B=1025), dict(ctx=0), dict(path=0), dict(acc=0), dict(err=0), dict(out=0x1000),
                  dict(out=0x1004), dict(cs=[cache(), cache(num_kv_heads=2)]), dict(cs=[cache(), cache(num_seqs=1)]),
-                 dict(cs=[cache(pages=0)])):
+                 dict(cs=[cache(pages=0)]), dict(cs=[cache(), cache(pages=0x20000), cache()])):
         assert c4(**over) == INVALID, over
     for over in (dict(N=0), dict(N=65), dict(cs=[cache()] * 65), dict(cs=[cache(head_dim=64)])):
         assert c4(**over) == UNSUPPORTED, over
@@ -132,6 +132,7 @@ def test_commit_refuses():
     assert c8([(0x10000, 1, 4, 576, 128)]) == INVALID
     assert c8([(0x10000, 4, 4, 500, 128)]) == INVALID
     assert c8([ring], N=65) == UNSUPPORTED
+    assert c8([ring, (0x20000, 4, 4, 576, 128), ring]) == INVALID
     assert L.kvq_tree_commit_fp8(None, 1, 2, 8, 0x1000, 0x2000, 0x3000, None, 0x5000, None) == INVALID
 
 
