@@ -56,7 +56,7 @@ static_assert(256 * kRegSoftmax + 128 * kRegAux <= kThreads * 168, "register sha
 constexpr uint32_t kColS = 0, kColO = 256;  // tile t at + 128 t; P over the first 64 columns of S
 
 struct PromptParams {
-  CUtensorMap mq, mk, mv;
+  CUtensorMap mq, mk, mv, mo;
   PromptJob j;
   float scale2;  // sm_scale * log2(e)
 };
@@ -523,10 +523,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         tc_fence_after();
         const float l = (f2lo(l2[0]) + f2hi(l2[0])) + (f2lo(l2[1]) + f2hi(l2[1]));
         const float inv = 1.0f / l;
-        // 32 dims of the warp's 32 rows at a time through shared memory, so that 4 lanes write 64 bytes of a row
+        // 32 dims of the warp's 32 rows at a time through shared memory. Whole ones leave by an asynchronous copy; at
+        // the end of a sequence 4 lanes write 64 bytes of a row.
         uint8_t* const stage = sm.stage[warp];
-        const int lr = lane >> 2, lc = lane & 3, row0 = row - lane;
-        uint16_t* const out = static_cast<uint16_t*>(j.out) + (it.s + row0) * j.os_t + it.hq[t] * j.os_h;
+        const int row0 = row - lane;
         const int have = it.n - row0;  // rows of the warp (may be 0 or fewer, or more than 32)
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
@@ -535,21 +535,29 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           tmem_wait_ld_all();
 #pragma unroll
           for (int i = 0; i < 16; ++i) w[i] = pack16x2<F16>(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
+          if (lane == 0) tma_stores_read();
           __syncwarp();
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             *reinterpret_cast<uint4*>(stage + lane * 64 + 16 * (i ^ ((lane >> 1) & 3))) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int rr = 8 * i + lr;
-            if (rr < have)
+          if (have >= 32) {
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) tma_store_3d(&p.mo, stage, 32 * c, it.hq[t], it.s + row0);
+          } else {
+            __syncwarp();
+            const int lr = lane >> 2, lc = lane & 3;
+            uint16_t* const out = static_cast<uint16_t*>(j.out) + (it.s + row0) * j.os_t + it.hq[t] * j.os_h;
+#pragma unroll 1
+            for (int rr = lr; rr < have; rr += 8)
               *reinterpret_cast<uint4*>(out + rr * j.os_t + 32 * c + 8 * lc) = *reinterpret_cast<const uint4*>(stage + rr * 64 + 16 * (lc ^ ((rr >> 1) & 3)));
           }
         }
         if (__builtin_expect(sm.bad[k & 1] == k, 0)) {
-          __syncwarp();  // the row as written by other lanes
-          __threadfence_block();
+          // the row as written by other lanes
+          if (lane == 0) tma_stores_done();
+          __syncwarp();
+          __threadfence();
           if (row < it.n) add_nonfinite<F16>(j, it, t, row);
         }
         tc_fence_before();
@@ -557,6 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       __syncwarp();
       if (lane == 0) mbar_arrive_relaxed(&sm.item_empty[k & 1]);
     }
+    if (lane == 0) tma_stores_read();  // no copy reads shared memory when the CTA ends
   }
   __syncwarp();
   tc_fence_before();
@@ -588,13 +597,13 @@ cudaError_t encoder(EncodeTiled& f) {
 }
 
 // Map of a [T][heads][128] tensor: boxes of 64 dims x 1 head x 128 tokens, 128-byte swizzle, zeros
-// outside (tokens from T on).
-bool encode(EncodeTiled f, CUtensorMap* m, bool f16, const void* base, int T, int heads, long long st, long long sh) {
+// outside (tokens from T on); the output's: 32 dims x 1 head x 32 tokens, 64-byte swizzle.
+bool encode(EncodeTiled f, CUtensorMap* m, bool f16, const void* base, int T, int heads, long long st, long long sh, bool out = false) {
   const cuuint64_t dims[3] = {kD, (cuuint64_t)heads, (cuuint64_t)T};
   const cuuint64_t strides[2] = {(cuuint64_t)sh * 2, (cuuint64_t)st * 2};
-  const cuuint32_t box[3] = {64, 1, kRows}, one[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {out ? 32u : 64u, 1, out ? 32u : (cuuint32_t)kRows}, one[3] = {1, 1, 1};
   return f(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
-           strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+           strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, out ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -611,7 +620,8 @@ cudaError_t launch_prompt(const PromptJob& job, cudaStream_t stream) {
   p.scale2 = job.sm_scale * kLog2e;
   if (!encode(f, &p.mq, job.f16, job.q, job.T, job.Hq, job.qs_t, job.qs_h) ||
       !encode(f, &p.mk, job.f16, job.k, job.T, job.Hkv, job.ks_t, job.ks_h) ||
-      !encode(f, &p.mv, job.f16, job.v, job.T, job.Hkv, job.vs_t, job.vs_h))
+      !encode(f, &p.mv, job.f16, job.v, job.T, job.Hkv, job.vs_t, job.vs_h) ||
+      !encode(f, &p.mo, job.f16, job.out, job.T, job.Hq, job.os_t, job.os_h, true))
     return cudaErrorInvalidValue;
   const auto kern = job.f16 ? prompt_kernel<true> : prompt_kernel<false>;
   const size_t smem = sizeof(Smem) + 1024;

@@ -44,6 +44,16 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
+// Asynchronous store of a box from shared memory (written, fenced for the async proxy and synchronised before), as a
+// group of its own; the groups of a thread are waited for by the thread itself.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];\n\tcp.async.bulk.commit_group;" ::"l"(map),
+               "r"(x), "r"(y), "r"(z), "r"(smem_addr(src))
+               : "memory");
+}
+__device__ __forceinline__ void tma_stores_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }  // sources free
+__device__ __forceinline__ void tma_stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }       // written
+
 // Instruction descriptor of tcgen05.mma.kind::f16 with bf16 or f16 operands, M = 128, N columns.
 __host__ __device__ constexpr uint32_t umma_idesc_16(bool f16, int n, bool b_mn) {
   return umma_idesc_f16(n, false, b_mn) | (f16 ? 0u : (1u << 7) | (1u << 10));
