@@ -452,31 +452,35 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         if (!ok) break;
         sph ^= 1u;
         tc_fence_after();
-        uint32_t s[128];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_ld32u(ts + 32 * i, s + 32 * i);
-        tmem_wait_ld_all();
         if (edge_block(R, it.n, b, j.window)) {
           const int hi = row - b * kRows, lo = j.window ? hi - j.window + 1 : 0;  // seen: lo..hi
-#pragma unroll
+#pragma unroll 1
           for (int w = 0; w < 4; ++w) {
+            uint32_t s[32];
+            tmem_ld32u(ts + 32 * w, s);
             const int h = hi - 32 * w, l = lo - 32 * w;
             uint32_t m = h < 0 ? 0u : h >= 31 ? ~0u : (2u << h) - 1u;
             if (l > 0) m = l >= 32 ? 0u : m & (~0u << l);
+            tmem_wait_ld_all();
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              if (!(m & (1u << i))) s[32 * w + i] = 0xFF800000u;
+              if (!(m & (1u << i))) s[i] = 0xFF800000u;
+            tmem_st32u(ts + 32 * w, s);
           }
+          tmem_wait_st();
         }
-        float mx[4];
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          uint32_t s[64];
+          tmem_ld32u(ts + 64 * h, s);
+          tmem_ld32u(ts + 64 * h + 32, s + 32);
+          tmem_wait_ld_all();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) mx[i] = __uint_as_float(s[i]);
+          for (int i = 0; i < 64; i += 8)
 #pragma unroll
-        for (int i = 4; i < 124; i += 8)
-#pragma unroll
-          for (int u = 0; u < 4; ++u) mx[u] = fmax3(mx[u], __uint_as_float(s[i + 2 * u]), __uint_as_float(s[i + 2 * u + 1]));
-#pragma unroll
-        for (int u = 0; u < 4; ++u) mx[u] = fmaxf(mx[u], __uint_as_float(s[124 + u]));
+            for (int u = 0; u < 4; ++u) mx[u] = fmax3(mx[u], __uint_as_float(s[i + 2 * u]), __uint_as_float(s[i + 2 * u + 1]));
+        }
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
         const bool move = top > base + 8.0f || (base == -INFINITY && top > -INFINITY);
         if (__any_sync(0xffffffffu, move)) {
@@ -498,12 +502,15 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         }
         const float neg = base == -INFINITY ? 0.0f : -base;
         const uint64_t c2 = f2(c, c), n2 = f2(neg, neg);
-#pragma unroll
+#pragma unroll 1
         for (int h = 0; h < 2; ++h) {
-          uint32_t pk[32];
+          uint32_t s[64], pk[32];
+          tmem_ld32u(ts + 64 * h, s);
+          tmem_ld32u(ts + 64 * h + 32, s + 32);
+          tmem_wait_ld_all();
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            const uint64_t x = fma_f2(f2(__uint_as_float(s[64 * h + 2 * i]), __uint_as_float(s[64 * h + 2 * i + 1])), c2, n2);
+            const uint64_t x = fma_f2(f2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), c2, n2);
             const float e0 = fast_exp2(f2lo(x)), e1 = fast_exp2(f2hi(x));
             l2[i & 1] = add_f2(l2[i & 1], f2(e0, e1));
             pk[i] = pack16x2<F16>(e0, e1);
