@@ -333,15 +333,19 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           umma_f16_ts_by(leader, tm + kColO + 128 * t, tm + kColS + 128 * t + 8 * kk, v + (uint64_t)(kk * (2048 >> 4)), kIdPV, k4 > 0 ? 1u : acc);
         }
       };
-      for (int k = 0; ok; ++k) {
-        if (!(ok = wait(&sm.item_full[k & 1], (uint32_t)(k / 2) & 1u))) break;
+      // Item k, taken while the one before is still at its last block: the switch is on the way of everything else.
+      auto take = [&](int k) {
+        ok = wait(&sm.item_full[k & 1], (uint32_t)(k / 2) & 1u);
         Item it = sm.item[k & 1];
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.item_empty[k & 1]);
-        it.n = uniform(it.n);
+        it.n = ok ? uniform(it.n) : -1;
         it.r0[0] = uniform(it.r0[0]);
         it.r0[1] = uniform(it.r0[1]);
-        if (it.n < 0) break;
+        return it;
+      };
+      Item it = take(0);
+      for (int k = 0; ok && it.n >= 0; ++k) {
         const Range r0(it, 0, j.window), r1(it, 1, j.window);
         const int jb = r0.jb, je = max(r0.je, r1.je);
         ok = wait(&sm.q_full, (uint32_t)k & 1u) && full(kv);
@@ -351,9 +355,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         if (r1.je > 0 && r1.jb == jb) qk(1, kv % kRing);
         umma_commit_by(leader, &sm.kv_empty[kv % kRing]);
         if (je == jb + 1) umma_commit_by(leader, &sm.q_empty);
+        Item next = it;
         for (int b = jb; ok && b < je; ++b) {
+          if (b + 1 == je) next = take(k + 1);
           const int uv = kv + 2 * (b - jb) + 1, sv = uv % kRing, sk = (uv + 1) % kRing;
-          ok = full(uv) && wait(&sm.v_ok[sv >> 1], (uint32_t)(uv / kRing) & 1u);
+          ok = ok && full(uv) && wait(&sm.v_ok[sv >> 1], (uint32_t)(uv / kRing) & 1u);
           if (ok && b + 1 < je) ok = full(uv + 1);
           if (!ok) break;
 #pragma unroll
@@ -379,6 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           if (b + 2 == je) umma_commit_by(leader, &sm.q_empty);
         }
         kv += 2 * (je - jb);
+        it = next;
       }
       umma_commit_by(leader, &sm.fin);  // arrives once every product issued has completed
       mbar_wait_bounded(&sm.fin, 0);
