@@ -444,12 +444,15 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     const float c = p.scale2;
     uint32_t sph = 0, oph = 0;
     bool ok = true;
-    for (int k = 0; ok; ++k) {
+    auto take = [&](int k) {  // item k, taken before the output of the one before
       ok = __all_sync(0xffffffffu, role_wait(&sm.item_full[k & 1], (uint32_t)(k / 2) & 1u, failed));
-      if (!ok) break;
-      const Item it = sm.item[k & 1];
-      __syncwarp();
-      if (it.n < 0) break;
+      Item it = sm.item[k & 1];
+      if (!ok) it.n = -1;
+      return it;
+    };
+    Item next = take(0);
+    for (int k = 0; ok && next.n >= 0; ++k) {
+      const Item it = next;
       const Range rg(it, t, j.window);
       const int R = it.r0[t], row = R + 32 * (warp & 3) + lane;
       float base = -INFINITY;  // in powers of two, as the weights take it
@@ -529,6 +532,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           if (lane == 0) mbar_arrive(h ? &sm.p_ready[t] : &sm.p_half[t]);
         }
       }
+      if (!ok) break;
+      next = take(k + 1);
       if (!ok) break;
       if (rg.je > 0) {
         ok = __all_sync(0xffffffffu, role_wait(&sm.o_full[t], oph, failed));
