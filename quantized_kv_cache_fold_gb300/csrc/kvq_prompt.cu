@@ -480,9 +480,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           tmem_wait_st();
         }
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        uint32_t s[64];
 #pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          uint32_t s[64];
+        for (int h = 1; h >= 0; --h) {  // the first half stays in registers
           tmem_ld32u(ts + 64 * h, s);
           tmem_ld32u(ts + 64 * h + 32, s + 32);
           tmem_wait_ld_all();
@@ -514,10 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         const uint64_t c2 = f2(c, c), n2 = f2(neg, neg);
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
-          uint32_t s[64], pk[32];
-          tmem_ld32u(ts + 64 * h, s);
-          tmem_ld32u(ts + 64 * h + 32, s + 32);
-          tmem_wait_ld_all();
+          uint32_t pk[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             const uint64_t x = fma_f2(f2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), c2, n2);
@@ -526,10 +523,15 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             pk[i] = pack16x2<F16>(e0, e1);
           }
           tmem_st32u(ts + 32 * h, pk);
+          if (h == 0) {
+            tmem_ld32u(ts + 64, s);
+            tmem_ld32u(ts + 96, s + 32);
+          }
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(h ? &sm.p_ready[t] : &sm.p_half[t]);
+          if (h == 0) tmem_wait_ld_all();
         }
       }
       if (!ok) break;
