@@ -11,6 +11,11 @@
 //         when a score passes it by more than 8, so P < 2^8)
 //   O += P V       tcgen05.mma, P read from tensor memory
 //
+// Bound by instruction issue: converting a page, and the exponentials of its scores, take longer than the products, and
+// a page costs the same for 1 row as for 128 (fewer than 49 rows take kvq_attn.cu). 64 sequences of 16,384 tokens, 80
+// rows per KV head (581 MB, 1.7e11 operations): 313 us a call, of which the prologue 30 and the join 15; DRAM 26%, tensor
+// pipe 40%, issue slots 60%. 8 of 32k-65k tokens, 320 rows: 309 us, 0.76 PFLOP/s. 64 windows of 513: 25 us.
+//
 // The rounding of q~, K, V and P to fp16 is what keeps both products on the tensor cores: 2^-11 each,
 // against the 2^-8 of a bf16 result; sums, bases and O stay in fp32.
 //
@@ -650,11 +655,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_kernel(const __grid_constant
         if (!ok) break;
         tc_fence_after();
         if (warp_rows) {
-          uint32_t s[64];
-          tmem_ld32u(ts, s);
-          tmem_ld32u(ts + 32, s + 32);
           const bool pv = *reinterpret_cast<volatile int*>(&sm.pvalid[cnt & 3]) != 0;
-          tmem_wait_ld_all();
           // pages that hold drafted tokens, lie outside the pool, or start before some row's window
           if (pos0 + kPage > ctx || !pv || (FMT == 1 && pos0 < ctx + j.N - j.window)) {
             const int cut = ctx - pos0;  // tokens from here on are drafted ones
@@ -666,19 +667,30 @@ __global__ void __launch_bounds__(kThreads, 2) tree_kernel(const __grid_constant
             if (cut >= 0) m |= cut >= 64 ? 0ull : mask << cut;
             else if (cut > -64) m |= mask >> -cut;
             if (!pv) m = 0ull;
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {  // rolled, over the scores in tensor memory (see kvq_prompt.cu)
+              uint32_t s[32];
+              tmem_ld32u(ts + 32 * h, s);
+              tmem_wait_ld_all();
+              const uint32_t mh = (uint32_t)(m >> (32 * h));
 #pragma unroll
-            for (int i = 0; i < 64; ++i)
-              if (!((m >> i) & 1u)) s[i] = 0xFF800000u;
+              for (int i = 0; i < 32; ++i)
+                if (!((mh >> i) & 1u)) s[i] = 0xFF800000u;
+              tmem_st32u(ts + 32 * h, s);
+            }
+            tmem_wait_st();
           }
-          float mx[4];
+          uint32_t s[32];
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+          for (int h = 1; h >= 0; --h) {  // rolled: less code to fetch (316 -> 313 us); the first half stays in registers
+            tmem_ld32u(ts + 32 * h, s);
+            tmem_wait_ld_all();
 #pragma unroll
-          for (int u = 0; u < 4; ++u) mx[u] = __uint_as_float(s[u]);
+            for (int i = 0; i < 32; i += 8)
 #pragma unroll
-          for (int i = 4; i < 60; i += 8)
-#pragma unroll
-            for (int u = 0; u < 4; ++u) mx[u] = fmax3(mx[u], __uint_as_float(s[i + 2 * u]), __uint_as_float(s[i + 2 * u + 1]));
-#pragma unroll
-          for (int u = 0; u < 4; ++u) mx[u] = fmaxf(mx[u], __uint_as_float(s[60 + u]));
+              for (int u = 0; u < 4; ++u) mx[u] = fmax3(mx[u], __uint_as_float(s[i + 2 * u]), __uint_as_float(s[i + 2 * u + 1]));
+          }
           const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.c;
           const bool move = top > base + 8.0f || (base == -INFINITY && top > -INFINITY);
           if (__any_sync(0xffffffffu, move)) {
@@ -703,15 +715,22 @@ __global__ void __launch_bounds__(kThreads, 2) tree_kernel(const __grid_constant
           }
           const float neg = base == -INFINITY ? 0.0f : -base;
           const uint64_t c2 = f2(p.c, p.c), n2 = f2(neg, neg);
-          uint32_t pk[32];
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            uint32_t pk[16];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const uint64_t x = fma_f2(f2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), c2, n2);
-            const float e0 = fast_exp2(f2lo(x)), e1 = fast_exp2(f2hi(x));
-            l2[i & 1] = add_f2(l2[i & 1], f2(e0, e1));
-            pk[i] = pack16x2<true>(e0, e1);
+            for (int i = 0; i < 16; ++i) {
+              const uint64_t x = fma_f2(f2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), c2, n2);
+              const float e0 = fast_exp2(f2lo(x)), e1 = fast_exp2(f2hi(x));
+              l2[i & 1] = add_f2(l2[i & 1], f2(e0, e1));
+              pk[i] = pack16x2<true>(e0, e1);
+            }
+            tmem_st16u(ts + 16 * h, pk);
+            if (h == 0) {
+              tmem_ld32u(ts + 32, s);
+              tmem_wait_ld_all();
+            }
           }
-          tmem_st32u(ts, pk);
           tmem_wait_st();
         }
         tc_fence_before();
