@@ -75,6 +75,23 @@ def test_trees_at_once(kind, N, heads):
     assert all(torch.equal(a, b) for a, b in zip(outs, want)) and all(c.err.item() == 0 for c in cs)
 
 
+@pytest.mark.parametrize("kind,N,heads", FORMS)
+def test_tree_rows_beside_a_nan_query(kind, N, heads):
+    """A query that is not finite is flagged (int4) or gives NaN, and no other row changes."""
+    c = case(kind, N, heads, 45)
+    masks = [tree(N, c.rng) for _ in range(3)]
+    want = c.call(masks)
+    c.q[1, N - 1, 0, 7] = float("nan")
+    out, ws = torch.zeros_like(want), kvq.alloc_tree_workspace(3, N, *heads)
+    ws.view(torch.float32).fill_(float("nan"))
+    issue(c, words(masks), out, ws)
+    torch.cuda.synchronize()
+    keep = torch.ones(out.shape[:3], dtype=torch.bool, device="cuda")
+    keep[1, N - 1, 0] = False
+    assert torch.equal(out[keep], want[keep])
+    assert c.err.item() == (kvq.DEVERR_NONFINITE if kind == "int4" else 0)
+
+
 def test_tree_padded_batch():
     """Trees of 3 and 6 tokens padded to 9: padding rows of any content change nothing."""
     c = Int4Case([100, 30], 9, 20, 4, seed=50)
