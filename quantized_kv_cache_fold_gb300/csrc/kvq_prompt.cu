@@ -40,9 +40,9 @@
 // Measured (20/4 heads): one prompt of 32,768 tokens, bf16: 3.42-3.49 ms, 1.57-1.61 PFLOP/s; 24 prompts of 100-4,000
 // tokens, 4.1e11 operations: 336-340 us, 1.2 PFLOP/s; 5 of 1,500-9,000, fp16, window 513: 109 us; 4 of up to 96: 10 us.
 //
-// Work order: items by descending block of 256 rows, so the longest run first, heads of a block next to each
-// other (they share K and V in L2); CTAs take them in turns, back and forth (c, 2n-1-c, 2n+c, ...),
-// which evens out the descending lengths without a counter in memory.
+// Work order: items by descending row tile, so the longest run first, heads of a tile next to each other (they share
+// K and V in L2); CTAs take them in turns, back and forth (c, 2n-1-c, 2n+c, ...), which evens out the descending
+// lengths without a counter in memory.
 
 #include <algorithm>
 #include <mutex>
@@ -89,7 +89,7 @@ struct Smem {
   int bad[2];   // count of the last item (by parity) in whose edge blocks a value was replaced
   int failed;
   uint32_t taddr;
-  int nblk[KVQ_MAX_SEQS];  // row blocks (256 rows) of each sequence
+  int nt[KVQ_MAX_SEQS];  // row tiles of each sequence
 };
 
 // The blocks [jb, je) of tile t of an item.
@@ -114,34 +114,44 @@ __device__ __forceinline__ bool edge_block(int R, int n, int j, int window) {
 
 __device__ __forceinline__ int warp_sum_int(int v) { return __reduce_add_sync(0xffffffffu, v); }
 
-// Pair number `pr` (row blocks of all sequences by descending block index m, then sequence) -> sequence
-// and m. The number of pairs with a larger block index than m is sum_b max(0, nblk_b - m - 1). Pairs
-// come in ascending order, so m never exceeds m_top, the last answer. Whole warp.
-__device__ __forceinline__ void find_pair(const int* nblk, int B, int pr, int& m_top, int& b) {
+// The items by descending row tile M, then sequence, KV head and query head: a sequence of nt tiles has at tile M < nt
+// `pairs` items of two heads (all KV heads together), and `odd` of the last heads of an odd number where M is odd (256
+// rows from tile M - 1 on) or the last (128 rows). Item `idx` -> M, the sequence b, and its number r among the
+// sequence's at M. Items come in ascending order, so M never exceeds m_top, the last answer. Whole warp.
+__device__ __forceinline__ void find_item(const int* nt, int B, int pairs, int odd, int idx, int& m_top, int& b, int& r) {
   const int lane = threadIdx.x & 31;
-  auto above = [&](int m) {
+  auto above = [&](int m) {  // items of tiles behind m
     int v = 0;
-    for (int i = lane; i < B; i += 32) v += max(0, nblk[i] - m - 1);
+    for (int i = lane; i < B; i += 32)
+      if (nt[i] > m + 1) v += (nt[i] - m - 1) * pairs + odd * (((nt[i] + 1) >> 1) - ((m + 1) >> 1));
     return warp_sum_int(v);
   };
   int lo = 0, hi = m_top;
-  while (lo < hi) {  // the smallest m with above(m) <= pr
+  while (lo < hi) {  // the smallest m with above(m) <= idx
     const int mid = (lo + hi) >> 1;
-    if (above(mid) <= pr) hi = mid;
+    if (above(mid) <= idx) hi = mid;
     else lo = mid + 1;
   }
   m_top = lo;
-  int r = pr - above(lo);
+  r = idx - above(lo);
   b = 0;
   for (int i0 = 0; i0 < B; i0 += 32) {
-    const bool has = i0 + lane < B && nblk[i0 + lane] > lo;
-    const uint32_t v = __ballot_sync(0xffffffffu, has);
-    const int c = __popc(v);
-    if (r < c) {
-      b = i0 + (int)__fns(v, 0, r + 1);
+    const int t = i0 + lane < B ? nt[i0 + lane] : 0;
+    const int c = t > lo ? pairs + ((lo & 1) || lo == t - 1 ? odd : 0) : 0;
+    int incl = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    const uint32_t hit = __ballot_sync(0xffffffffu, incl > r);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      b = i0 + l;
+      r -= __shfl_sync(0xffffffffu, incl - c, l);
       break;
     }
-    r -= c;
+    r -= __shfl_sync(0xffffffffu, incl, 31);
   }
 }
 
@@ -218,12 +228,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   fence_barrier_init();
   griddep_wait();
   griddep_launch_dependents();
-  int npairs = 0;
   for (int b = threadIdx.x; b < j.B; b += kThreads) {
     const int s = j.cu_seqlens[b], e = j.cu_seqlens[b + 1];
     const bool ok = s >= 0 && e >= s && e <= j.T;
     if (!ok && blockIdx.x == 0) set_err(j.dev_err, KVQ_DEVERR_POS);
-    sm.nblk[b] = ok ? (e - s + kItemRows - 1) / kItemRows : 0;
+    sm.nt[b] = ok ? (e - s + kRows - 1) / kRows : 0;
   }
   if (warp == 9) tmem_alloc_512(&sm.taddr);
   tc_fence_before();
@@ -235,38 +244,30 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     reg_dealloc<kRegAux>();
     if (warp == 10) {
       // ------------------------------------------------------------ schedule
-      int top = 0;
+      const int G = j.Hq / j.Hkv, pairs = G / 2 * j.Hkv, odd = G & 1 ? j.Hkv : 0;
+      int top = 0, items = 0;
       for (int b = lane; b < j.B; b += 32) {
-        npairs += sm.nblk[b];
-        top = max(top, sm.nblk[b] - 1);
+        items += sm.nt[b] * pairs + (sm.nt[b] + 1) / 2 * odd;
+        top = max(top, sm.nt[b] - 1);
       }
-      npairs = warp_sum_int(npairs);
+      items = warp_sum_int(items);
       top = __reduce_max_sync(0xffffffffu, top);
-      const long long items = (long long)npairs * j.Hq;  // some of a sequence's last block are empty
       const int n = gridDim.x, c = blockIdx.x;
-      const int G = j.Hq / j.Hkv;
-      long long turn = 0;
       for (int k = 0;; ++k) {
         Item it{0, -1, {0, 0}, {0, 0}};
-        for (;; ++turn) {
-          const long long idx = turn * n + (turn & 1 ? n - 1 - c : c);
-          if (idx >= items) break;  // and so are all later ones
-          int b;
-          find_pair(sm.nblk, j.B, (int)(idx / j.Hq), top, b);
-          const int e = (int)(idx % j.Hq), u = e % G, h = e - u, first = top * kItemRows;
-          const int s0 = j.cu_seqlens[b], len = j.cu_seqlens[b + 1] - s0;
-          const bool rows256 = (u == G - 1) && (G & 1);
-          // two heads: items u and u + 1 (u even) are their second and first 128 rows
-          const int r = first + (rows256 || (u & 1) ? 0 : kRows);
-          if (r >= len) continue;
-          it.s = s0;
-          it.n = len;
-          it.r0[0] = r;
-          it.r0[1] = rows256 ? r + kRows : r;
-          it.hq[0] = h + (rows256 ? u : u & ~1);
-          it.hq[1] = h + (rows256 ? u : (u & ~1) + 1);
-          ++turn;
-          break;
+        const long long idx = (long long)k * n + (k & 1 ? n - 1 - c : c);
+        if (idx < items) {
+          int b, r;
+          find_item(sm.nt, j.B, pairs, odd, (int)idx, top, b, r);
+          it.s = j.cu_seqlens[b];
+          it.n = j.cu_seqlens[b + 1] - it.s;
+          const int per = G / 2 + (odd && ((top & 1) || top == sm.nt[b] - 1));  // items of a KV head
+          const int h = r / per * G, u = r % per;
+          const bool rows256 = u == G / 2;
+          it.r0[0] = (rows256 ? top & ~1 : top) * kRows;
+          it.r0[1] = it.r0[0] + (rows256 ? kRows : 0);
+          it.hq[0] = h + 2 * u;
+          it.hq[1] = it.hq[0] + (rows256 ? 0 : 1);
         }
         bool ok = k < 2 || role_wait(&sm.item_empty[k & 1], (uint32_t)(k / 2 - 1) & 1u, failed);
         if (!__all_sync(0xffffffffu, ok)) break;
