@@ -297,6 +297,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         mbar_arrive(&sm.item_empty[k & 1]);
         if (it.n < 0) break;
         const Range a(it, 0, j.window), b(it, 1, j.window);
+        const int hkv = it.hq[0] / (j.Hq / j.Hkv);
+        if (!(ok = load(&p.mk, hkv, it.s + a.jb * kRows))) break;  // its place is free before Q's
         if (k > 0 && !(ok = role_wait(&sm.q_empty, (uint32_t)(k - 1) & 1u, failed))) break;
         const int tiles = b.je > 0 ? 2 : 1;
         mbar_arrive_expect_tx(&sm.q_full, tiles * kTileBytes);
@@ -304,9 +306,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           for (int h = 0; h < 2; ++h)
             tma_load_3d(sm.q[t] + h * (kTileBytes / 2), &p.mq, 64 * h, it.hq[t], it.s + it.r0[t], &sm.q_full);
         ++nq;
-        const int hkv = it.hq[0] / (j.Hq / j.Hkv);
         for (int jb = a.jb; ok && jb < max(a.je, b.je); ++jb)
-          ok = load(&p.mk, hkv, it.s + jb * kRows) && load(&p.mv, hkv, it.s + jb * kRows);
+          ok = (jb == a.jb || load(&p.mk, hkv, it.s + jb * kRows)) && load(&p.mv, hkv, it.s + jb * kRows);
       }
       if (!ok) {  // no copy may be in flight when the CTA ends
         if (nq > 0) mbar_wait_bounded(&sm.q_full, (uint32_t)(nq - 1) & 1u);
