@@ -155,6 +155,15 @@ __device__ __forceinline__ void find_item(const int* nt, int B, int pairs, int o
   }
 }
 
+// Of two pairs of 16-bit values: the larger of m (magnitudes) and |w|, NaN where either is.
+template <bool F16>
+__device__ __forceinline__ uint32_t max_magnitude(uint32_t m, uint32_t w) {
+  uint32_t r;
+  if (F16) asm("{\n\t.reg .b32 a;\n\tabs.f16x2 a, %2;\n\tmax.NaN.f16x2 %0, %1, a;\n\t}" : "=r"(r) : "r"(m), "r"(w));
+  else asm("{\n\t.reg .b32 a;\n\tabs.bf16x2 a, %2;\n\tmax.NaN.bf16x2 %0, %1, a;\n\t}" : "=r"(r) : "r"(m), "r"(w));
+  return r;
+}
+
 template <bool F16>
 __device__ __forceinline__ bool has_nonfinite(uint32_t w) {
   constexpr uint32_t kExp = F16 ? 0x7C007C00u : 0x7F807F80u, kOne = F16 ? 0x04000400u : 0x00800080u;
@@ -420,12 +429,16 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                             (blk >= b.jb && blk < b.je && edge_block(it.r0[1], it.n, blk, j.window));
           if (edge) {
             uint4* tile = reinterpret_cast<uint4*>(sm.kv[slot]);
-            bool bad = false;
+            uint32_t m[4] = {0u, 0u, 0u, 0u};  // largest magnitudes, NaN above all
 #pragma unroll 8
             for (int i = lane; i < kTileBytes / 16; i += 32) {
               const uint4 w = tile[i];
-              bad |= has_nonfinite<F16>(w.x) | has_nonfinite<F16>(w.y) | has_nonfinite<F16>(w.z) | has_nonfinite<F16>(w.w);
+              m[0] = max_magnitude<F16>(m[0], w.x);
+              m[1] = max_magnitude<F16>(m[1], w.y);
+              m[2] = max_magnitude<F16>(m[2], w.z);
+              m[3] = max_magnitude<F16>(m[3], w.w);
             }
+            const bool bad = has_nonfinite<F16>(m[0]) | has_nonfinite<F16>(m[1]) | has_nonfinite<F16>(m[2]) | has_nonfinite<F16>(m[3]);
             if (__any_sync(0xffffffffu, bad)) {
               for (int i = lane; i < kTileBytes / 16; i += 32) {
                 uint4 w = tile[i];
