@@ -379,8 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         for (int b = jb; ok && b < je; ++b) {
           if (b + 1 == je) next = take(k + 1);
           const int uv = kv + 2 * (b - jb) + 1, sv = uv % kRing, sk = (uv + 1) % kRing;
-          ok = ok && full(uv) && wait(&sm.v_ok[sv >> 1], (uint32_t)(uv / kRing) & 1u);
-          if (ok && b + 1 < je) ok = full(uv + 1);
+          ok = ok && wait(&sm.v_ok[sv >> 1], (uint32_t)(uv / kRing) & 1u);  // V and the next K are here
           if (!ok) break;
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
@@ -451,6 +450,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
               if (lane == 0) sm.bad[k & 1] = k;
               fence_proxy_async_shared();
             }
+          }
+          if (blk + 1 < je) {
+            ok = __all_sync(0xffffffffu, role_wait(&sm.kv_full[(use + 1) % kRing], (uint32_t)((use + 1) / kRing) & 1u, failed));
+            if (!ok) break;
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.v_ok[slot >> 1]);
