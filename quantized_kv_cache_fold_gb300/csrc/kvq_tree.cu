@@ -13,8 +13,8 @@
 //
 // Bound by instruction issue: converting a page, and the exponentials of its scores, take longer than the products, and
 // a page costs the same for 1 row as for 128 (fewer than 49 rows take kvq_attn.cu). 64 sequences of 16,384 tokens, 80
-// rows per KV head (581 MB, 1.7e11 operations): 313 us a call, of which the prologue 30 and the join 15; DRAM 26%, tensor
-// pipe 40%, issue slots 60%. 8 of 32k-65k tokens, 320 rows: 309 us, 0.76 PFLOP/s. 64 windows of 513: 25 us.
+// rows per KV head (581 MB, 1.7e11 operations): 305 us a call, of which the prologue 30 and the join 15; DRAM 26%, tensor
+// pipe 40%, issue slots 60%. 8 of 32k-65k tokens, 320 rows: 298 us, 0.79 PFLOP/s. 64 windows of 513: 25 us.
 //
 // The rounding of q~, K, V and P to fp16 is what keeps both products on the tensor cores: 2^-11 each,
 // against the 2^-8 of a bf16 result; sums, bases and O stay in fp32.
@@ -52,6 +52,7 @@ constexpr int kHalf = kTileBytes / 2;
 constexpr int kThreads = 512;
 constexpr int kRegSoftmax = 104, kRegConv = 56, kRegAux = 40;  // from 64 at launch
 static_assert(128 * (kRegSoftmax + 2 * kRegConv + kRegAux) <= kThreads * 64, "register shares above the launch's allocation");
+constexpr float kKScale = 1.0f / 512.0f;  // of the int4 cache's K tiles (convert_k4)
 constexpr uint32_t kColS = 0, kColO = 128;  // S of page i at + 64 (i & 1), P over its first 32 columns
 constexpr int kQHalf = kGroup * 128;        // bytes of one 64-dim half of Q'
 // K and V tiles. One of each, and the shared memory for copy stages instead: a second tile of K or V lets its
@@ -217,11 +218,6 @@ __device__ __forceinline__ size_t out_row(const TreeParams& p, int b, int h, int
 
 __device__ __forceinline__ float half_lo(uint32_t x) { return __half2float(__ushort_as_half((unsigned short)x)); }
 __device__ __forceinline__ float half_hi(uint32_t x) { return __half2float(__ushort_as_half((unsigned short)(x >> 16))); }
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
 __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t d;
   asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
@@ -232,7 +228,10 @@ __device__ __forceinline__ uint32_t both(float x) { return pack_f16x2(x, x); }
 
 // Half of a token's K record -> its row of the K tile. Word w holds dims 8w..8w+7 in the order 0, 4, 1, 5, 2, 6, 3,
 // 7 (as the nibbles pair up in 32 bits; Q' takes the same). A code is the subnormal c 2^-24 (even nibbles)
-// or c 2^-20 (odd ones): one exact product by 2^15, then c s + o rounded once.
+// or c 2^-20 (odd ones); the tile holds (c s + o) 2^-9, one fma a pair, rounded once to fp16 (off by at most 2^-11 of
+// the value, or 2^-16 where the value is below 2^-5): so s 2^15 fits fp16 for s < 2, which keys of norm sqrt(128) always
+// have (a larger scale takes fp32). The scores take the 2^9 back. With a product by
+// 2^15 of its own first: 64 x 16,384, 80 rows, 313 instead of 305 us.
 // Places of a token's words of one half of the dims: word 8 part + 4 c + i at chunk(c) + off[i].
 struct RowWords {
   uint8_t* row;     // the row in the part's half of the tile
@@ -245,11 +244,11 @@ struct RowWords {
   __device__ __forceinline__ uint8_t* chunk(int c) const { return row + (((uint32_t)c << 6) ^ hi); }
 };
 
-__device__ __forceinline__ void convert_k4(const uint8_t* rec, int slot, uint32_t meta, uint8_t* tile, int row, int part) {
+template <bool WIDE>
+__device__ __forceinline__ void convert_k4_as(const uint8_t* rec, int slot, uint32_t meta, uint8_t* tile, int row, int part) {
   const int sw = k_chunk_swz(slot);
-  const uint32_t up = 0x78007800u;  // 2^15
-  const float s = half_lo(meta);
-  const uint32_t s0 = both(s * 512.0f), s1 = both(s * 32.0f), oo = both(half_hi(meta));
+  const float s = half_lo(meta) * (16777216.0f * kKScale), o = half_hi(meta) * kKScale;
+  const uint32_t s0 = both(s), s1 = both(s * 0.0625f), oo = both(o);
   const RowWords dst(tile, row, part);
   const uint4 r0 = *reinterpret_cast<const uint4*>(rec + 16 * ((2 * part) ^ sw));
   const uint4 r1 = *reinterpret_cast<const uint4*>(rec + 16 * ((2 * part + 1) ^ sw));
@@ -262,14 +261,22 @@ __device__ __forceinline__ void convert_k4(const uint8_t* rec, int slot, uint32_
     for (int i = 0; i < 4; ++i) {
       uint32_t h[4];
       unpack8_sub(wd[i], h);
-      uint4 out;
-      out.x = hfma2(hmul2(h[0], up), s0, oo);
-      out.y = hfma2(hmul2(h[1], up), s1, oo);
-      out.z = hfma2(hmul2(h[2], up), s0, oo);
-      out.w = hfma2(hmul2(h[3], up), s1, oo);
-      *reinterpret_cast<uint4*>(out_c + dst.off[i]) = out;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float m = e & 1 ? s * 0.0625f : s;
+        if (WIDE) h[e] = pack_f16x2_sat(fmaf(half_lo(h[e]), m, o), fmaf(half_hi(h[e]), m, o));
+        else h[e] = hfma2(h[e], e & 1 ? s1 : s0, oo);
+      }
+      *reinterpret_cast<uint4*>(out_c + dst.off[i]) = make_uint4(h[0], h[1], h[2], h[3]);
     }
   }
+}
+__device__ __noinline__ void convert_k4_wide(const uint8_t* rec, int slot, uint32_t meta, uint8_t* tile, int row, int part) {
+  convert_k4_as<true>(rec, slot, meta, tile, row, part);
+}
+__device__ __forceinline__ void convert_k4(const uint8_t* rec, int slot, uint32_t meta, uint8_t* tile, int row, int part) {
+  if (__builtin_expect(half_lo(meta) >= 2.0f, 0)) convert_k4_wide(rec, slot, meta, tile, row, part);
+  else convert_k4_as<false>(rec, slot, meta, tile, row, part);
 }
 
 // Half of a token's V record -> its row of the V tile, dims in the same order. A code is the subnormal
@@ -896,7 +903,7 @@ size_t workspace_tree_partials_bytes(int B) {
 cudaError_t launch_tree(const TreeJob& job, cudaStream_t stream) {
   TreeParams p{};
   p.j = job;
-  const float c = job.sm_scale * kLog2e * (job.fmt == 1 ? job.k_scale : 1.0f);
+  const float c = job.sm_scale * kLog2e * (job.fmt == 1 ? job.k_scale : 1.0f / kKScale);
   p.qmul = c > 0.0f ? 1.0f : c < 0.0f ? -1.0f : 0.0f;
   p.c = c == 0.0f ? 1.0f : (c < 0.0f ? -c : c);
   p.vmul = job.fmt == 1 ? job.v_scale : 1.0f;

@@ -218,6 +218,16 @@ def test_int4_value_ranges(v_gain):
         assert bool(torch.isfinite(out).all()) and float(out.abs().max()) < 1e-4
 
 
+@pytest.mark.parametrize("N,heads", [(60, (2, 1)), (16, (20, 4)), (12, (4, 2))])
+@pytest.mark.parametrize("gain", [1.0 / 64, 5.0, 300.0])
+def test_int4_key_scales(gain, N, heads):
+    """Key scales on both sides of those that normalised keys have (M_k times a gain)."""
+    c = Int4Case([0, 0], N, *heads, seed=19)
+    c.Mk *= gain
+    masks = [tree(N, c.rng), chain(N)]
+    c.check(c.call(masks, sm=SM / gain), masks, sm=SM / gain)
+
+
 def test_int4_bad_page_is_skipped():
     c = Int4Case([300, 300], 5, 8, 2, seed=10)
     masks = [tree(5, c.rng) for _ in range(2)]
