@@ -37,8 +37,12 @@
 // 116 -> 109). What is left at an item's end is the chain last products -> output -> first scores. Four warps for the
 // output alone, with the next item's scores running meanwhile, were slower (337 -> 351 us, 109 -> 114).
 //
-// Measured (20/4 heads): one prompt of 32,768 tokens, bf16: 3.42-3.49 ms, 1.57-1.61 PFLOP/s; 24 prompts of 100-4,000
-// tokens, 4.1e11 operations: 336-340 us, 1.2 PFLOP/s; 5 of 1,500-9,000, fp16, window 513: 109 us; 4 of up to 96: 10 us.
+// The products' warp is on everything's way: it takes the next item during the last block, and V's look answers for the
+// next keys too, so that it waits five times a block instead of seven (329 -> 322 us). More waits (V in two halves: 337),
+// polling instead of resting (347) or weights handed over whole (332) cost more than they gain.
+//
+// Measured (20/4 heads): one prompt of 32,768 tokens, bf16: 3.36-3.39 ms, 1.62-1.64 PFLOP/s; 24 prompts of 100-4,000
+// tokens, 4.1e11 operations: 324 us, 1.26 PFLOP/s; 5 of 1,500-9,000, fp16, window 513: 104 us; 4 of up to 96: 10 us.
 //
 // Work order: items by descending row tile, so the longest run first, heads of a tile next to each other (they share
 // K and V in L2); CTAs take them in turns, back and forth (c, 2n-1-c, 2n+c, ...), which evens out the descending
