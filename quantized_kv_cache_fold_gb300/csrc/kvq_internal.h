@@ -145,8 +145,9 @@ struct TreeJob {
 // Trees of up to this many rows per KV head (drafted tokens x query heads per KV head) over the int4 cache take the
 // verify block's kernels (launch_attention) with the mask in place of the diagonal: those multiply the codes as they are
 // and scale the scores, so few rows cost little, where launch_tree first makes fp16 tiles of every token. 64 sequences of
-// 16,384 tokens, 4 KV heads, verify kernels / launch_tree: 106 / 265 us with 5 rows, 164 / 268 with 15, 195 / 270 with
-// 20, 254 / 296 with 45; 8 of 8,192: 21 / 35, 31 / 37, 29 / 38, 40 / 43; one of 4,096: 21-25 / 23-24 throughout.
+// 16,384 tokens, 4 KV heads, verify kernels / launch_tree: 106 / 259 us with 5 rows, 164 / 262 with 15, 195 / 263 with
+// 20, 254 / 284 with 45; 8 of 8,192: 21 / 35, 32 / 37, 29 / 37, 40 / 42; one of 4,096: 21-25 / 22-24 throughout; one of
+// 65,536: 24 / 42, 30 / 44, 30 / 46, 37 / 44.
 constexpr int kTreeFewRows = kMaxRows;
 // Over a ring, trees of up to 8 drafted tokens and 16 rows, or 24 rows while there are fewer (sequence, KV head) pairs
 // than SMs, take the verify block's cluster kernel where the ring is small enough for it (swa_cluster_path): one launch

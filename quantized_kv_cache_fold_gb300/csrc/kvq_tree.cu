@@ -57,7 +57,7 @@ constexpr uint32_t kColS = 0, kColO = 128;  // S of page i at + 64 (i & 1), P ov
 constexpr int kQHalf = kGroup * 128;        // bytes of one 64-dim half of Q'
 // K and V tiles. One of each, and the shared memory for copy stages instead: a second tile of K or V lets its
 // conversion run ahead and take issue slots from the chain that everything waits for (64 x 16,384 x 16
-// drafted: 316 us; two of V 335, two of K 353).
+// drafted: 314 us; two of V 333, two of K 350).
 constexpr int kKBuf = 1, kVBuf = 1;
 constexpr int kMaxTreeCtas = 320;                       // sizes the partials
 constexpr int kMaxStages = 6;                           // of each ring
