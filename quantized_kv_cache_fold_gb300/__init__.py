@@ -328,28 +328,43 @@ def _need(ok, what):
         raise ValueError(what)
 
 
-def _is(t, dtype, shape, name):
-    """Address of `t`, a contiguous device tensor of this type and shape."""
-    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
-        return t.data_ptr()
-    raise ValueError(f"{name} must be a contiguous device tensor of {dtype} and shape {tuple(shape)}, got {t.dtype} "
-                     f"{tuple(t.shape)} on {t.device}")
-
-
-def _here(t, stream):
-    """The raw stream of a call on `t`'s device, which has to be the current one (kvq.h)."""
-    torch = _th
+def _dev(t, name):
+    """The device that the call's tensors have to be on: that of `t`, a device tensor (_here asks that it is the current one)."""
     dev = t.get_device()
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"tensors on cuda:{dev}, but cuda:{torch.cuda.current_device()} is the current device")
+    if dev < 0:
+        raise ValueError(f"{name} must be a device tensor")
+    return dev
+
+
+def _is(t, dtype, shape, name, dev):
+    """Address of `t`, a contiguous tensor of this type and shape on device `dev`."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name} must be a contiguous tensor of {dtype} and shape {tuple(shape)} on cuda:{dev}, got "
+                     f"{t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _err(t, dev):
+    """Address of the device error word."""
+    if t.dtype is _th.int32 and t.get_device() == dev and t.numel():
+        return t.data_ptr()
+    raise ValueError(f"dev_err must be int32 on cuda:{dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _here(dev, stream):
+    """The raw stream of a call on device `dev`, which has to be the current one (kvq.h)."""
+    c = _th._C
+    if dev != c._cuda_getDevice():
+        raise ValueError(f"tensors on cuda:{dev}, but cuda:{c._cuda_getDevice()} is the current device")
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
+        return c._cuda_getCurrentRawStream(dev)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _bytes(workspace):
-    _need(workspace.is_cuda and workspace.is_contiguous(), "the workspace must be a contiguous device tensor")
-    return workspace.numel() * workspace.element_size()
+def _bytes(workspace, dev):
+    if workspace.get_device() == dev and workspace.is_contiguous():
+        return workspace.numel() * workspace.element_size()
+    raise ValueError(f"the workspace must be a contiguous tensor on cuda:{dev}")
 
 
 def kvq_prompt_workspace_bytes(T: int, B: int, num_q_heads: int, num_kv_heads: int) -> int:
@@ -377,10 +392,11 @@ def kvq_prompt_attn(q, k, v, cu_seqlens, out, workspace, dev_err, window: int = 
     Hkv = k.shape[1]
     if not (D == HEAD_DIM and out.shape == q.shape and k.shape == v.shape == (T, Hkv, D)):
         raise ValueError(f"shapes: q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)}, out {tuple(out.shape)}")
-    if not (k.dtype is v.dtype is out.dtype is dtype and q.is_cuda and k.is_cuda and v.is_cuda and out.is_cuda):
-        raise ValueError("q, k, v and out must be device tensors of one dtype")
-    B = cu_seqlens.shape[0] - 1
-    cu = _is(cu_seqlens, torch.int32, (B + 1,), "cu_seqlens")
+    if not (k.dtype is v.dtype is out.dtype is dtype and q.is_cuda and
+            q.get_device() == k.get_device() == v.get_device() == out.get_device()):
+        raise ValueError("q, k, v and out must be tensors of one dtype on one device")
+    B, dev = cu_seqlens.shape[0] - 1, q.get_device()
+    cu = _is(cu_seqlens, torch.int32, (B + 1,), "cu_seqlens", dev)
     sq, sk, sv, so = q.stride(), k.stride(), v.stride(), out.stride()
     if not sq[2] == sk[2] == sv[2] == so[2] == 1:
         raise ValueError("the rows of q, k, v and out must be contiguous")
@@ -391,7 +407,7 @@ def kvq_prompt_attn(q, k, v, cu_seqlens, out, workspace, dev_err, window: int = 
                              for x in (st[0] if T > 1 else max(1, h) * D, st[1] if h > 1 else D)))
     status = lib.kvq_prompt_attn(q.data_ptr(), k.data_ptr(), v.data_ptr(), BF16 if dtype is torch.bfloat16 else F16, T,
                                  B, Hq, Hkv, strides, cu, window, sm_scale, out.data_ptr(), workspace.data_ptr(),
-                                 _bytes(workspace), dev_err.data_ptr(), _here(q, stream))
+                                 _bytes(workspace, dev), _err(dev_err, dev), _here(dev, stream))
     if status:
         raise KvqError("kvq_prompt_attn", status)
 
@@ -412,20 +428,21 @@ def alloc_tree_workspace(B: int, N: int, num_q_heads: int, num_kv_heads: int, de
 
 
 def _tree_args(q, ctx_len, tree_mask, out, k_new, v_new, Hkv):
-    """(B, N, Hq, dtype code, addresses of ctx_len, mask, k_new, v_new, out's dtype code)."""
+    """(device, B, N, Hq, dtype code, addresses of ctx_len, mask, k_new, v_new, out's dtype code)."""
     torch = _torch()
     B, N, Hq, D = q.shape
     if not (q.dtype is torch.bfloat16 or q.dtype is torch.float32) or D != HEAD_DIM or not (q.is_cuda and q.is_contiguous()):
         raise ValueError(f"q must be a contiguous device tensor [B, N, Hq, 128] of fp32 or bf16, got {q.dtype} {tuple(q.shape)}")
     if not (out.dtype is torch.bfloat16 or out.dtype is torch.float32):
         raise ValueError(f"out must be fp32 or bf16, got {out.dtype}")
-    _is(out, out.dtype, q.shape, "out")
+    dev = q.get_device()
+    _is(out, out.dtype, q.shape, "out", dev)
     if k_new is not None:
-        _is(k_new, q.dtype, (B, N, Hkv, D), "k_new")
+        _is(k_new, q.dtype, (B, N, Hkv, D), "k_new", dev)
     if v_new is not None:
-        _is(v_new, q.dtype, (B, N, Hkv, D), "v_new")
-    mask = _is(tree_mask, torch.uint64 if tree_mask.dtype is torch.uint64 else torch.int64, (B, N), "tree_mask")
-    return (B, N, Hq, BF16 if q.dtype is torch.bfloat16 else F32, _is(ctx_len, torch.int32, (B,), "ctx_len"), mask,
+        _is(v_new, q.dtype, (B, N, Hkv, D), "v_new", dev)
+    mask = _is(tree_mask, torch.uint64 if tree_mask.dtype is torch.uint64 else torch.int64, (B, N), "tree_mask", dev)
+    return (dev, B, N, Hq, BF16 if q.dtype is torch.bfloat16 else F32, _is(ctx_len, torch.int32, (B,), "ctx_len", dev), mask,
             None if k_new is None else k_new.data_ptr(), None if v_new is None else v_new.data_ptr(),
             BF16 if out.dtype is torch.bfloat16 else F32)
 
@@ -436,11 +453,13 @@ def kvq_tree_attn_int4(cache: Int4Cache, Mq, Mk, q, ctx_len, tree_mask, out, wor
     """Attention of N drafted tokens per sequence over the int4 cache: q [B, N, Hq, 128] (fp32 or bf16),
     tree_mask int64 [B, N] (bit j: attends to drafted token j), out fp32 or bf16. fwht as in
     kvq_decode_attn_int4."""
-    B, N, Hq, dt, ctx, mask, kn, vn, odt = _tree_args(q, ctx_len, tree_mask, out, k_new, v_new, cache.num_kv_heads)
+    dev, B, N, Hq, dt, ctx, mask, kn, vn, odt = _tree_args(q, ctx_len, tree_mask, out, k_new, v_new, cache.num_kv_heads)
     fn = lib.kvq_tree_attn_int4_fwht if fwht else lib.kvq_tree_attn_int4
-    status = fn(ctypes.byref(cache), Mq.data_ptr(), None if Mk is None else Mk.data_ptr(), q.data_ptr(), dt, B, N, Hq, ctx,
-                mask, kn, vn, sm_scale, eps, out.data_ptr(), odt, workspace.data_ptr(), _bytes(workspace),
-                dev_err.data_ptr(), _here(q, stream))
+    fold = (HEAD_DIM,) if fwht else (HEAD_DIM, HEAD_DIM)
+    status = fn(ctypes.byref(cache), _is(Mq, _th.float32, fold, "Mq", dev), None if Mk is None else _is(Mk, _th.float32, fold, "Mk", dev),
+                q.data_ptr(), dt, B, N, Hq, ctx,
+                mask, kn, vn, sm_scale, eps, out.data_ptr(), odt, workspace.data_ptr(), _bytes(workspace, dev),
+                _err(dev_err, dev), _here(dev, stream))
     if status:
         raise KvqError("kvq_tree_attn_int4_fwht" if fwht else "kvq_tree_attn_int4", status)
 
@@ -449,10 +468,10 @@ def kvq_tree_attn_fp8_swa(ring: Fp8Ring, q, pos0, tree_mask, window: int, k_scal
                           workspace, dev_err, k_new=None, v_new=None, sm_scale: float = HEAD_DIM ** -0.5,
                           stream=None):
     """kvq_tree_attn_int4 over the e4m3 ring of a sliding-window layer (q used as given)."""
-    B, N, Hq, dt, ctx, mask, kn, vn, odt = _tree_args(q, pos0, tree_mask, out, k_new, v_new, ring.num_kv_heads)
+    dev, B, N, Hq, dt, ctx, mask, kn, vn, odt = _tree_args(q, pos0, tree_mask, out, k_new, v_new, ring.num_kv_heads)
     status = lib.kvq_tree_attn_fp8_swa(ctypes.byref(ring), q.data_ptr(), dt, B, N, Hq, ctx, mask, window, kn, vn, k_scale,
-                                       v_scale, sm_scale, out.data_ptr(), odt, workspace.data_ptr(), _bytes(workspace),
-                                       dev_err.data_ptr(), _here(q, stream))
+                                       v_scale, sm_scale, out.data_ptr(), odt, workspace.data_ptr(), _bytes(workspace, dev),
+                                       _err(dev_err, dev), _here(dev, stream))
     if status:
         raise KvqError("kvq_tree_attn_fp8_swa", status)
 
@@ -464,11 +483,11 @@ def _layers(layers):
 
 def _tree_commit(name, layers, ctx_len, path, n_accept, dev_err, ctx_out, stream):
     i32 = _torch().int32
-    B, N = path.shape
-    status = getattr(lib, name)(_layers(layers), len(layers), B, N, _is(ctx_len, i32, (B,), "ctx_len"),
-                                _is(path, i32, (B, N), "path"), _is(n_accept, i32, (B,), "n_accept"),
-                                None if ctx_out is None else _is(ctx_out, i32, (B,), "ctx_out"), dev_err.data_ptr(),
-                                _here(path, stream))
+    (B, N), dev = path.shape, _dev(path, "path")
+    status = getattr(lib, name)(_layers(layers), len(layers), B, N, _is(ctx_len, i32, (B,), "ctx_len", dev),
+                                _is(path, i32, (B, N), "path", dev), _is(n_accept, i32, (B,), "n_accept", dev),
+                                None if ctx_out is None else _is(ctx_out, i32, (B,), "ctx_out", dev), _err(dev_err, dev),
+                                _here(dev, stream))
     if status:
         raise KvqError(name, status)
 
@@ -487,15 +506,15 @@ def kvq_tree_commit_fp8(rings, pos0, path, n_accept, dev_err, ctx_out=None, stre
 def _pool(page_refs, block_table):
     i32 = _torch().int32
     S, M = block_table.shape
-    n = page_refs.shape[0]
-    return _is(page_refs, i32, (n,), "page_refs"), n, _is(block_table, i32, (S, M), "block_table"), S, M
+    n, dev = page_refs.shape[0], _dev(page_refs, "page_refs")
+    return dev, _is(page_refs, i32, (n,), "page_refs", dev), n, _is(block_table, i32, (S, M), "block_table", dev), S, M
 
 
 def kvq_pages_alloc(page_refs, block_table, seq_ids, len_old, len_new, dev_err, stream=None):
     """Gives sequences seq_ids the pages to grow from len_old to len_new tokens (lowest free first)."""
-    pool, i32, n = _pool(page_refs, block_table), _th.int32, seq_ids.shape[0]
-    status = lib.kvq_pages_alloc(*pool, n, _is(seq_ids, i32, (n,), "seq_ids"), _is(len_old, i32, (n,), "len_old"),
-                                 _is(len_new, i32, (n,), "len_new"), dev_err.data_ptr(), _here(page_refs, stream))
+    (dev, *pool), i32, n = _pool(page_refs, block_table), _th.int32, seq_ids.shape[0]
+    status = lib.kvq_pages_alloc(*pool, n, _is(seq_ids, i32, (n,), "seq_ids", dev), _is(len_old, i32, (n,), "len_old", dev),
+                                 _is(len_new, i32, (n,), "len_new", dev), _err(dev_err, dev), _here(dev, stream))
     if status:
         raise KvqError("kvq_pages_alloc", status)
 
@@ -503,19 +522,19 @@ def kvq_pages_alloc(page_refs, block_table, seq_ids, len_old, len_new, dev_err, 
 def kvq_pages_fork(page_refs, block_table, parents, children, lens, copy_src, copy_dst, dev_err, stream=None):
     """Children share their parents' full pages of the first lens tokens and get a page of their own
     for a partly filled last one: kvq_pages_copy(caches, copy_src, copy_dst) then fills it."""
-    pool, i32, n = _pool(page_refs, block_table), _th.int32, parents.shape[0]
-    status = lib.kvq_pages_fork(*pool, n, _is(parents, i32, (n,), "parents"), _is(children, i32, (n,), "children"),
-                                _is(lens, i32, (n,), "lens"), _is(copy_src, i32, (n,), "copy_src"),
-                                _is(copy_dst, i32, (n,), "copy_dst"), dev_err.data_ptr(), _here(page_refs, stream))
+    (dev, *pool), i32, n = _pool(page_refs, block_table), _th.int32, parents.shape[0]
+    status = lib.kvq_pages_fork(*pool, n, _is(parents, i32, (n,), "parents", dev), _is(children, i32, (n,), "children", dev),
+                                _is(lens, i32, (n,), "lens", dev), _is(copy_src, i32, (n,), "copy_src", dev),
+                                _is(copy_dst, i32, (n,), "copy_dst", dev), _err(dev_err, dev), _here(dev, stream))
     if status:
         raise KvqError("kvq_pages_fork", status)
 
 
 def kvq_pages_free(page_refs, block_table, seq_ids, len_old, len_new, dev_err, stream=None):
     """Gives back the pages of sequences seq_ids behind len_new tokens."""
-    pool, i32, n = _pool(page_refs, block_table), _th.int32, seq_ids.shape[0]
-    status = lib.kvq_pages_free(*pool, n, _is(seq_ids, i32, (n,), "seq_ids"), _is(len_old, i32, (n,), "len_old"),
-                                _is(len_new, i32, (n,), "len_new"), dev_err.data_ptr(), _here(page_refs, stream))
+    (dev, *pool), i32, n = _pool(page_refs, block_table), _th.int32, seq_ids.shape[0]
+    status = lib.kvq_pages_free(*pool, n, _is(seq_ids, i32, (n,), "seq_ids", dev), _is(len_old, i32, (n,), "len_old", dev),
+                                _is(len_new, i32, (n,), "len_new", dev), _err(dev_err, dev), _here(dev, stream))
     if status:
         raise KvqError("kvq_pages_free", status)
 
@@ -523,12 +542,12 @@ def kvq_pages_free(page_refs, block_table, seq_ids, len_old, len_new, dev_err, s
 def kvq_pages_compact(page_refs, block_table, copy_src, copy_dst, n_moves, dev_err, stream=None):
     """Renames the pages in use to the front of the pool; kvq_pages_copy(caches, copy_src, copy_dst,
     count=n_moves) then moves them. copy_src, copy_dst: int32, at least num_pages // 2 entries."""
-    pool, i32 = _pool(page_refs, block_table), _th.int32
-    src, dst = _is(copy_src, i32, copy_src.shape, "copy_src"), _is(copy_dst, i32, copy_dst.shape, "copy_dst")
+    (dev, *pool), i32 = _pool(page_refs, block_table), _th.int32
+    src, dst = _is(copy_src, i32, copy_src.shape, "copy_src", dev), _is(copy_dst, i32, copy_dst.shape, "copy_dst", dev)
     _need(min(copy_src.numel(), copy_dst.numel()) >= page_refs.shape[0] // 2,
           "copy_src and copy_dst must hold num_pages // 2 entries")
-    status = lib.kvq_pages_compact(*pool, src, dst, _is(n_moves, i32, (1,), "n_moves"), dev_err.data_ptr(),
-                                   _here(page_refs, stream))
+    status = lib.kvq_pages_compact(*pool, src, dst, _is(n_moves, i32, (1,), "n_moves", dev), _err(dev_err, dev),
+                                   _here(dev, stream))
     if status:
         raise KvqError("kvq_pages_compact", status)
 
@@ -536,9 +555,9 @@ def kvq_pages_compact(page_refs, block_table, copy_src, copy_dst, n_moves, dev_e
 def kvq_pages_copy(caches, src, dst, dev_err, count=None, stream=None):
     """Copies page src[i] to page dst[i] in every one of the layers `caches` (pairs with -1 are passed
     over), for i < n or i < count (a device int32 tensor of one entry)."""
-    i32, n = _torch().int32, src.shape[0]
-    status = lib.kvq_pages_copy(_layers(caches), len(caches), n, _is(src, i32, (n,), "src"), _is(dst, i32, (n,), "dst"),
-                                None if count is None else _is(count, i32, (1,), "count"), dev_err.data_ptr(),
-                                _here(src, stream))
+    i32, n, dev = _torch().int32, src.shape[0], _dev(src, "src")
+    status = lib.kvq_pages_copy(_layers(caches), len(caches), n, _is(src, i32, (n,), "src", dev), _is(dst, i32, (n,), "dst", dev),
+                                None if count is None else _is(count, i32, (1,), "count", dev), _err(dev_err, dev),
+                                _here(dev, stream))
     if status:
         raise KvqError("kvq_pages_copy", status)

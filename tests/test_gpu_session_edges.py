@@ -224,3 +224,36 @@ def test_commit_replays():
         torch.cuda.synchronize()
         assert all(torch.equal(x, y) for x, y in zip(data, want)) and out.tolist() == [s + t for s, t in zip(at, a)]
     assert cs[0].err.item() == 0 == r.err.item()
+
+
+def test_tensors_that_do_not_fit_are_refused():
+    """Nothing is launched for a tensor of another type, shape or place."""
+    c = Int4Case([10], 4, 4, 2, seed=70)
+    w, out, ws = words([tree(4, c.rng)]), torch.zeros(1, 4, 4, D, device="cuda"), kvq.alloc_tree_workspace(1, 4, 4, 2)
+
+    def tree_call(**o):
+        a = dict(Mq=c.Mq, Mk=c.Mk, q=c.q, ctx=c.ctx_t, w=w, out=out, ws=ws, err=c.err, fwht=False, k=c.k_new, v=c.v_new)
+        a.update(o)
+        kvq.kvq_tree_attn_int4(c.cache, a["Mq"], a["Mk"], a["q"], a["ctx"], a["w"], a["out"], a["ws"], a["err"], k_new=a["k"],
+                               v_new=a["v"], fwht=a["fwht"])
+
+    for bad in (dict(Mq=c.Mq[0]), dict(Mk=c.Mk[0]), dict(fwht=True), dict(Mq=c.Mq.cpu()), dict(Mq=c.Mq.double()), dict(q=c.q.half()),
+                dict(q=c.q.cpu()), dict(ctx=c.ctx_t.long()), dict(ctx=c.ctx_t.cpu()), dict(w=w[:, :3]), dict(w=w.int()), dict(out=out[:, :3]),
+                dict(out=out.cpu()), dict(ws=ws.cpu()), dict(err=c.err.cpu()), dict(err=c.err.float()), dict(err=c.err[:0]),
+                dict(k=c.k_new.float()), dict(v=c.v_new[:, :, :1])):
+        with pytest.raises(ValueError):
+            tree_call(**bad)
+    q, k, v = inputs([40], 4, 2, torch.bfloat16)
+    pws, err = kvq.alloc_prompt_workspace(40, 1, 4, 2), c.err
+    for bad in ((q.cpu(), k, v, q.clone(), pws, err), (q, k.cpu(), v, q.clone(), pws, err), (q, k, v, q.half(), pws, err),
+                (q, k, v, q[:39], pws, err), (q, k, v, q.clone(), pws.cpu(), err), (q, k, v, q.clone(), pws, err.cpu())):
+        with pytest.raises(ValueError):
+            kvq.kvq_prompt_attn(bad[0], bad[1], bad[2], offsets([40]), bad[3], bad[4], bad[5])
+    with pytest.raises(ValueError):
+        kvq.kvq_tree_commit_int4([c.cache], c.ctx_t, i32([[0, 1, 2, 3]]), i32([1]), c.err.cpu())
+    refs, table, one = i32([0] * 8), i32([[-1] * 4]), i32([0])
+    for bad in ((refs.long(), table, one, c.err), (refs, table[:, ::2], one, c.err), (refs, table, one.cpu(), c.err), (refs, table, one, one.cpu())):
+        with pytest.raises(ValueError):
+            kvq.kvq_pages_alloc(bad[0], bad[1], bad[2], one, one, bad[3])
+    torch.cuda.synchronize()
+    assert c.err.item() == 0 and bool((out == 0).all())
