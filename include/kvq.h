@@ -379,6 +379,9 @@ kvq_status kvq_prompt_attn(const void* q, const void* k, const void* v, kvq_dtyp
  *   out:      device [B][N][num_q_heads][128] of out_dtype (KVQ_F32 or KVQ_BF16).
  *   workspace: device, >= kvq_tree_workspace_bytes(B, N, num_q_heads, num_kv_heads), 256-byte
  *             aligned; contents need no initialisation.
+ *   The products take q~ in fp16. A row whose q~ is not finite, or has an element of magnitude
+ *   65520 or more, is NaN (0 if it attends to nothing); a query that is not finite is flagged
+ *   (KVQ_DEVERR_NONFINITE) as well. No other row changes.
  *   Other arguments, readings of positions and errors as kvq_decode_attn_int4. A position whose
  *   block-table entry is outside the pool is skipped (KVQ_DEVERR_PAGE). Slots of a page that were
  *   never written are masked, but their scales are read: a pool is zeroed before its first use.
@@ -404,7 +407,8 @@ kvq_status kvq_tree_attn_int4_fwht(const kvq_int4_cache* cache, const float* wq,
  *     pos0[b] + max(1, number of drafted tokens it attends to) - 1
  *   (its depth in the tree), and its window reaches back from there: context positions above that
  *   position - window, and the drafted tokens of its mask.
- *   q is used as given; workspace and out as above; other arguments as kvq_decode_attn_fp8_swa.
+ *   q is used as given and in fp16: NaN for rows as above, without a flag. workspace and out as
+ *   above; other arguments as kvq_decode_attn_fp8_swa.
  * Requires window >= N and capacity >= window + N - 1.
  */
 kvq_status kvq_tree_attn_fp8_swa(const kvq_fp8_ring* ring, const void* q, kvq_dtype dtype, int B, int N,

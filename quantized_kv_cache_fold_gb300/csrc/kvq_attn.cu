@@ -425,6 +425,10 @@ __global__ void __maxnreg__(NT == 1 ? (FMT == 0 ? KVQ_INT4_MAXREG : 184) : 255)
 #pragma unroll
         for (int i = 0; i < 32; ++i) qv[i] = 0.0f;
       }
+      if (TREE) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) qv[i] = f16_query(qv[i]);
+      }
       float part = 0.0f;
 #pragma unroll
       for (int i = 0; i < 32; ++i) part += qv[i];
@@ -1303,7 +1307,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
       if (r < R) {
         const float* qrow = p.q_rot + (((size_t)bq * p.S + r / G) * p.Hq + hq * G + r % G) * kD + 8 * w;
         const float4 a = reinterpret_cast<const float4*>(qrow)[0], c4 = reinterpret_cast<const float4*>(qrow)[1];
-        const float qv[8] = {a.x, a.y, a.z, a.w, c4.x, c4.y, c4.z, c4.w};
+        float qv[8] = {a.x, a.y, a.z, a.w, c4.x, c4.y, c4.z, c4.w};
+        if (TREE) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) qv[i] = f16_query(qv[i]);
+        }
 #pragma unroll
         for (int i = 0; i < 8; ++i) part += qv[i];
         hq4[0] = pack_f16x2(qv[0], qv[4]);
@@ -1647,7 +1655,13 @@ __global__ void __launch_bounds__(kCombWarps * 32, 4) combine_rows_kernel(const 
       float Mc = mv[0];
 #pragma unroll
       for (int k = 1; k < kCombChunkWarp; ++k) Mc = fmaxf(Mc, mv[k]);
-      if (Mc == -INFINITY) continue;  // nothing visible in this chunk
+      if (Mc == -INFINITY) {  // nothing visible in this chunk, or scores that are NaN: their sum is kept
+        if (TREE) {
+#pragma unroll
+          for (int k = 0; k < kCombChunkWarp; ++k) lsum += lv[k];
+        }
+        continue;
+      }
       float lc = 0.0f;
       float2 cl = make_float2(0.0f, 0.0f), ch = make_float2(0.0f, 0.0f);
 #pragma unroll
@@ -1720,7 +1734,13 @@ __global__ void __launch_bounds__(128, 4) combine_kernel(const AttnParams p) {
       float Mc = mv[0];
 #pragma unroll
       for (int k = 1; k < kCombChunkBlock; ++k) Mc = fmaxf(Mc, mv[k]);
-      if (Mc == -INFINITY) continue;  // nothing visible in this chunk
+      if (Mc == -INFINITY) {  // nothing visible in this chunk, or scores that are NaN: their sum is kept
+        if (TREE) {
+#pragma unroll
+          for (int k = 0; k < kCombChunkBlock; ++k) lsum += lv[k];
+        }
+        continue;
+      }
       float lc = 0.0f, ac = 0.0f;
 #pragma unroll
       for (int k = 0; k < kCombChunkBlock; ++k) {

@@ -269,6 +269,11 @@ __device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
   return d;
 }
 
+// A tree's query element as the fp16 products take it: NaN where it is not finite or fp16 does not hold it (65520 and
+// above round past 65504). So every score of such a row that some mask lets through is NaN, and with it the row, where an
+// infinity kept as it is could make every score -inf and the row look like one that sees nothing.
+__device__ __forceinline__ float f16_query(float x) { return fabsf(x) < 65520.0f ? x : __int_as_float(0x7FFFFFFF); }
+
 // x in the low half, y in the high half, each rounded to bf16 (off by at most half a step, 2^-8 of the value).
 __device__ __forceinline__ uint32_t bf16x2_of(float x, float y) {
   uint32_t w;

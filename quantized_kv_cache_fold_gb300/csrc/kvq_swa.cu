@@ -445,6 +445,10 @@ __global__ void __launch_bounds__(256, 1) swa_cluster_kernel(const SwaParams p) 
 #pragma unroll
       for (int i = 0; i < 32; ++i) qv[i] = 0.0f;
     }
+    if (TREE) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) qv[i] = f16_query(qv[i]);
+    }
     // k-step ks covers dims 32 t' + 4 ks .. +3 of lane t' (the K words are read in the
     // matching order, so the dot product pairs every dim with itself)
 #pragma unroll

@@ -638,10 +638,10 @@ __global__ void __launch_bounds__(kThreads, 2) tree_kernel(const __grid_constant
 #pragma unroll
             for (int d = 0; d < 8; ++d) {
               const float x = half_q ? bf16_bits_to_f32(d & 1 ? ww[d >> 1] >> 16 : ww[d >> 1] & 0xFFFFu) : __uint_as_float(ww[d]);
-              y[col_of<FMT>(d)] = x * p.qmul;
+              y[col_of<FMT>(d)] = f16_query(x * p.qmul);
             }
             *reinterpret_cast<uint4*>(sm.q + (w >> 3) * kQHalf + rr * 128 + 16 * ((w & 7) ^ (rr & 7))) =
-                make_uint4(pack_f16x2_sat(y[0], y[1]), pack_f16x2_sat(y[2], y[3]), pack_f16x2_sat(y[4], y[5]), pack_f16x2_sat(y[6], y[7]));
+                make_uint4(pack_f16x2(y[0], y[1]), pack_f16x2(y[2], y[3]), pack_f16x2(y[4], y[5]), pack_f16x2(y[6], y[7]));
           }
         }
         fence_proxy_async_shared();
