@@ -227,6 +227,16 @@ __device__ __forceinline__ bool tree_sees(const AttnParams& p, int b, int r, int
   return j < 0 || (j < p.S && ((__ldg(reinterpret_cast<const unsigned long long*>(p.tree_mask) + (size_t)b * p.S + r) >> j) & 1ull));
 }
 
+// TREE: the products take P s_V in fp16. The base of a row is chosen for that product: with s_V < 2^e (scale_exponent) it
+// moves when a score + e passes it by more than 15, to 7 below. So P s_V stays below 2^15 whatever the scales, and as far
+// above the type's smallest step as that allows: small scales and weights far below a row's largest keep their share (keys
+// 17 to 20 nats under one whose value is 0, or values of 1e-3: off by up to all of the output with the base at the
+// maximum). P itself and its sums are fp32.
+constexpr float kTreeLimit = 15.0f, kTreeBelow = 7.0f;
+
+// Exponent e of s < 2^e for a scale (s >= 0), at least -13 (fp16's smallest normal scale): bounds P by 2^28.
+__device__ __forceinline__ float scale_exponent(float s) { return (float)max((int)(__float_as_uint(s) >> 23) - 126, -13); }
+
 // Stores n output values; TREE: of the type asked for, and 0 for rows that saw nothing.
 template <bool TREE>
 __device__ __forceinline__ void store2(const AttnParams& p, size_t at, float x, float y, float lsum) {
@@ -646,11 +656,13 @@ __global__ void __maxnreg__(NT == 1 ? (FMT == 0 ? KVQ_INT4_MAXREG : 184) : 255)
             float mx[NT][2];
             bool need = false;
             bool big = false;
+            float ve = 0.0f;  // TREE: of the largest V scale of this thread's tokens
             if (FMT == 0) {
               float vmax = 0.0f;
 #pragma unroll
               for (int u = 0; u < MTU; ++u) vmax = fmaxf(vmax, fmaxf(va[u][0], va[u][1]));
-              big = vmax >= 255.0f;
+              if (TREE) ve = scale_exponent(vmax);
+              else big = vmax >= 255.0f;
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -659,6 +671,7 @@ __global__ void __maxnreg__(NT == 1 ? (FMT == 0 ? KVQ_INT4_MAXREG : 184) : 255)
                 float v = -INFINITY;
 #pragma unroll
                 for (int u = 0; u < MTU; ++u) v = fmaxf(v, fmaxf(sc[nt][u][j], sc[nt][u][2 + j]));
+                if (TREE) v += ve;
                 mx[nt][j] = v;
                 need |= v > (big ? fminf(thr[nt][j], 0.0f) : thr[nt][j]);
               }
@@ -668,7 +681,7 @@ __global__ void __maxnreg__(NT == 1 ? (FMT == 0 ? KVQ_INT4_MAXREG : 184) : 255)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                   const float mt = warp_max_g(mx[nt][j]);
-                  const float mnew = fmaxf(m[nt][j], muse[nt][j] + mt);
+                  const float mnew = fmaxf(m[nt][j], muse[nt][j] + (TREE ? mt - kTreeBelow : mt));
                   if (mnew != m[nt][j]) {
                     const float mu2 = mnew == -INFINITY ? 0.0f : mnew;
                     const float alpha = fast_exp2(m[nt][j] - mu2);
@@ -687,7 +700,7 @@ __global__ void __maxnreg__(NT == 1 ? (FMT == 0 ? KVQ_INT4_MAXREG : 184) : 255)
                     }
                     m[nt][j] = mnew;
                     muse[nt][j] = mu2;
-                    thr[nt][j] = mnew == -INFINITY ? -INFINITY : 8.0f;
+                    thr[nt][j] = mnew == -INFINITY ? -INFINITY : TREE ? kTreeLimit : 8.0f;
                   }
                 }
             }
@@ -1417,14 +1430,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
           mx = fmaxf(mx, d[i]);
         }
       }
-      const bool need = mx > (mt.z >= 255.0f ? fminf(thr_grp, 0.0f) : thr_grp);  // large V scale: any excess
+      const float ve = TREE ? scale_exponent(fmaxf(mt.z, 0.0f)) : 0.0f;
+      const bool need = TREE ? mx + ve > thr_grp : mx > (mt.z >= 255.0f ? fminf(thr_grp, 0.0f) : thr_grp);  // large V scale: any excess
       if (__builtin_expect(named_barrier_or(kGrpBar, kGrp, need || !ok), 0)) {
         err = named_barrier_or(kGrpBar, kGrp, !ok);
         if (err) break;
         // ---- rare: move the base of the rows whose maximum passed it (row maxima over the 128 tokens)
   #pragma unroll
         for (int i = 0; i < H; ++i) {
-          const float m1 = warp_max_all(d[i]);
+          const float m1 = warp_max_all(TREE ? d[i] + ve : d[i]);
           if (lane == 0) rowm[q * kTcMaxRows + r0 + i] = m1;
         }
         named_barrier(kGrpBar, kGrp);
@@ -1438,7 +1452,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
             const float mt4 = fmaxf(fmaxf(rowm[r], rowm[kTcMaxRows + r]), fmaxf(rowm[2 * kTcMaxRows + r], rowm[3 * kTcMaxRows + r]));
             const float4 c = rowc[r];
             const float mold = rowst[r], muse = -c.y;
-            const float mnew = fmaxf(mold, muse + mt4);
+            const float mnew = fmaxf(mold, muse + (TREE ? mt4 - kTreeBelow : mt4));
             if (mnew != mold) {
               const float mu2 = mnew == -INFINITY ? 0.0f : mnew;
               alpha = fast_exp2(mold - mu2);
@@ -1446,7 +1460,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
               changed = true;
               const float nb = mnew == -INFINITY ? 0.0f : -mnew;
               rowst[r] = mnew;
-              rowc[r] = make_float4(c.x, nb, mnew == -INFINITY ? -INFINITY : 8.0f, c.w);
+              rowc[r] = make_float4(c.x, nb, mnew == -INFINITY ? -INFINITY : TREE ? kTreeLimit : 8.0f, c.w);
               rcy[r] = nb;
             }
           }

@@ -16,7 +16,7 @@
 //
 // The two tiles alternate: while the warps of one turn scores into weights, the tensor cores run the
 // other's products. The base of a row moves only when a score passes it by more than 8 (in powers of
-// two), so P stays below 2^8 and O is rescaled a few times at the start of a row, by the softmax warps
+// two), so P stays below 2^8 (fp16: 2^15, see kWeightRaise) and O is rescaled a few times at the start of a row, by the softmax warps
 // themselves: S of a block is complete only after the products issued before it, so O is at rest then.
 //
 //   warps 0-3, 4-7  softmax and output of tile 0 and 1 (thread = row = tensor-memory lane)
@@ -523,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             for (int u = 0; u < 4; ++u) mx[u] = fmax3(mx[u], __uint_as_float(s[i + 2 * u]), __uint_as_float(s[i + 2 * u + 1]));
         }
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-        const bool move = top > base + 8.0f || (base == -INFINITY && top > -INFINITY);
+        const bool move = top > base + kBaseLag || (base == -INFINITY && top > -INFINITY);
         if (__any_sync(0xffffffffu, move)) {
           const float alpha = move ? fast_exp2(base - top) : 1.0f;
           if (move) base = top;
@@ -541,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             }
           }
         }
-        const float neg = base == -INFINITY ? 0.0f : -base;
+        const float neg = base == -INFINITY ? 0.0f : (F16 ? kWeightRaise : 0.0f) - base;
         const uint64_t c2 = f2(c, c), n2 = f2(neg, neg);
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {

@@ -148,6 +148,10 @@ __device__ __forceinline__ int unit_lane_offset(int slot, int lane) {
   return (slot & (kUnit - 1)) * kRec8 + ((lane >> 2) ^ (slot & 7)) * 16 + ((4 * lane) & 15);
 }
 
+// A tree's weights are 2^(score - maximum + 15): the largest is at fp16's upper end, so that 2^-39 of it is still in the
+// type's range (2^-24 without). The sums carry the factor too, so it cancels.
+constexpr float kTreeRaise = 15.0f;
+
 // One 32-slot unit (K records then V records at `st`, unit index u) against the warp's query tiles.
 template <int NT, bool TREE>
 __device__ __forceinline__ void attend_unit(const uint8_t* st, int u, int p_last, int slot_last, int cap,
@@ -214,6 +218,7 @@ __device__ __forceinline__ void attend_unit(const uint8_t* st, int u, int p_last
       muse[nt][jj] = mnew == -INFINITY ? 0.0f : mnew;
       const float alpha = fast_exp2(m[nt][jj] - muse[nt][jj]);
       m[nt][jj] = mnew;
+      if (TREE) muse[nt][jj] -= kTreeRaise;
       if (alpha != 1.0f) {
         l[nt][jj] *= alpha;
 #pragma unroll

@@ -7,8 +7,8 @@
 //   K, V  4-bit codes -> c s + o in fp16 (one rounding), e4m3 -> fp16 (exact), a page (64 tokens) at a time,
 //         by four warps each into shared memory (K: K-major, V: MN-major, 128-byte swizzle)
 //   S = Q' K^T     tcgen05.mma, 128 rows x 64 tokens, two buffers of S
-//   P = 2^(c S - base) in fp16 over S, one thread per row (as in kvq_prompt.cu: the base moves only
-//         when a score passes it by more than 8, so P < 2^8)
+//   P = 2^(c S - base + 7) in fp16 over S, one thread per row (as in kvq_prompt.cu: the base moves only
+//         when a score passes it by more than 8, so P < 2^15)
 //   O += P V       tcgen05.mma, P read from tensor memory
 //
 // Bound by instruction issue: converting a page, and the exponentials of its scores, take longer than the products, and
@@ -699,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_kernel(const __grid_constant
               for (int u = 0; u < 4; ++u) mx[u] = fmax3(mx[u], __uint_as_float(s[i + 2 * u]), __uint_as_float(s[i + 2 * u + 1]));
           }
           const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.c;
-          const bool move = top > base + 8.0f || (base == -INFINITY && top > -INFINITY);
+          const bool move = top > base + kBaseLag || (base == -INFINITY && top > -INFINITY);
           if (__any_sync(0xffffffffu, move)) {
             const float alpha = move ? fast_exp2(base - top) : 1.0f;
             if (move) base = top;
@@ -720,7 +720,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_kernel(const __grid_constant
               }
             }
           }
-          const float neg = base == -INFINITY ? 0.0f : -base;
+          const float neg = base == -INFINITY ? 0.0f : kWeightRaise - base;
           const uint64_t c2 = f2(p.c, p.c), n2 = f2(neg, neg);
 #pragma unroll 1
           for (int h = 0; h < 2; ++h) {

@@ -32,6 +32,12 @@ __device__ __forceinline__ void tmem_st32u(uint32_t taddr, const uint32_t* r) {
       : "memory");
 }
 
+// The base of a row's weights follows the largest score, in powers of two: it moves when a score passes it by more than
+// kBaseLag. Weights of fp16 are 2^(score - base + kWeightRaise), so the largest lies between 2^7 and 2^15 and the type's
+// smallest step 2^-24 is 2^-31 of it or less: with no raise, weights below 2^-25 of the largest were lost (65,000 keys 17
+// to 20 nats under one whose value is 0: the output off by 4 to 90%). The factor is the sums' as well, so it cancels.
+constexpr float kBaseLag = 8.0f, kWeightRaise = 7.0f;
+
 // Keeps values loaded by tmem_ld*u from being used before the wait after the loads.
 __device__ __forceinline__ void tmem_wait_ld_all() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
