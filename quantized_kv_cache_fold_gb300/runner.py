@@ -122,13 +122,23 @@ class DecodeStack:
 
     # ---- around decoding
 
+    def _alloc_for(self, stream, alloc, *sizes):
+        """A workspace allocated in the order of the stream that will use it (None: the current one; else a stream or its
+        raw handle), so that the allocator hands its memory to nothing else before that stream is done with it."""
+        if stream is None:
+            return alloc(*sizes, self.device)
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream)
+        with torch.cuda.stream(stream):
+            return alloc(*sizes, self.device)
+
     def prompt_layer(self, l, q, k, v, cu_seqlens, out, workspace=None, stream=None):
         """Attention of whole prompts, packed end to end, in layer l (windowed in a sliding-window layer);
         q, k and v as kvq_prompt_attn takes them. The keys and values go into the cache by
         append_prompt."""
         L = self.layers[l]
         if workspace is None:
-            workspace = alloc_prompt_workspace(q.shape[0], cu_seqlens.shape[0] - 1, self.Hq, self.Hkv, self.device)
+            workspace = self._alloc_for(stream, alloc_prompt_workspace, q.shape[0], cu_seqlens.shape[0] - 1, self.Hq, self.Hkv)
         kvq_prompt_attn(q, k, v, cu_seqlens, out, workspace, self.dev_err,
                         window=0 if isinstance(L, Int4Layer) else L.window, stream=stream)
 
@@ -154,7 +164,7 @@ class DecodeStack:
     def tree_step(self, qs, ctx, tree_mask, outs, k_news=None, v_news=None, workspace=None, stream=None):
         """One verify step over all layers: qs[l], outs[l], k_news[l], v_news[l] per layer."""
         if workspace is None:
-            workspace = alloc_tree_workspace(qs[0].shape[0], qs[0].shape[1], self.Hq, self.Hkv, self.device)
+            workspace = self._alloc_for(stream, alloc_tree_workspace, qs[0].shape[0], qs[0].shape[1], self.Hq, self.Hkv)
         for l in range(len(self.layers)):
             self.tree_layer(l, qs[l], ctx, tree_mask, outs[l], workspace, None if k_news is None else k_news[l],
                             None if v_news is None else v_news[l], stream=stream)
