@@ -429,7 +429,8 @@ kvq_status kvq_tree_attn_fp8_swa(const kvq_fp8_ring* ring, const void* q, kvq_dt
  *   path:     device int32[B][N], the accepted tokens in order; an entry outside 0..N-1 within the
  *             first n_accept[b] is skipped (KVQ_DEVERR_POS).
  *   n_accept: device int32[B], clamped to 0..N (KVQ_DEVERR_POS if it had to be).
- *   ctx_out:  device int32[B] or NULL: receives ctx_len[b] + n_accept[b]; must not overlap ctx_len.
+ *   ctx_out:  device int32[B] or NULL: receives ctx_len[b] + n_accept[b]; must not overlap ctx_len,
+ *             path or n_accept.
  * Requires 1 <= B <= KVQ_MAX_SEQS, 1 <= N <= KVQ_MAX_TREE.
  */
 kvq_status kvq_tree_commit_int4(const kvq_int4_cache* caches, int num_caches, int B, int N, const int32_t* ctx_len,
@@ -465,9 +466,10 @@ kvq_status kvq_pages_alloc(int32_t* page_refs, int num_pages, int32_t* block_tab
 /* kvq_pages_fork -- sequence children[i] (whose row holds no pages) becomes a copy of the first
  * len[i] tokens of parents[i]: full pages are shared (count + 1), a last page that is only partly
  * filled is replaced by a free one. copy_src[i] / copy_dst[i] (device int32[n]) receive that page of
- * the parent and of the child for kvq_pages_copy, -1 where there is none. A row may not be parent
- * and child in one call (KVQ_DEVERR_POS, skipped). No free page: entry -1, KVQ_DEVERR_POOL. An
- * entry of the parent's outside the pool: entry -1, KVQ_DEVERR_PAGE. */
+ * the parent and of the child for kvq_pages_copy, -1 where there is none; they must not overlap one
+ * another or the request's lists. A row may not be parent and child in one call (KVQ_DEVERR_POS,
+ * skipped). No free page: entry -1, KVQ_DEVERR_POOL. An entry of the parent's outside the pool: entry
+ * -1, KVQ_DEVERR_PAGE. */
 kvq_status kvq_pages_fork(int32_t* page_refs, int num_pages, int32_t* block_table, int num_seqs,
                           int max_pages_per_seq, int n, const int32_t* parents, const int32_t* children,
                           const int32_t* len, int32_t* copy_src, int32_t* copy_dst, int32_t* dev_err,
@@ -484,8 +486,9 @@ kvq_status kvq_pages_free(int32_t* page_refs, int num_pages, int32_t* block_tabl
 /* kvq_pages_compact -- the L pages in use move to pages 0..L-1: those behind, in ascending order, to
  * the free ones in front, in ascending order. Counts and every entry of the table are rewritten.
  * copy_src / copy_dst (device int32[num_pages/2]) receive the moves and *n_moves (device) their
- * number; a page is never both source and destination. Entries that name a page with count 0 stay
- * (KVQ_DEVERR_PAGE). Every table that names pages of the pool has to be rewritten: there is one. */
+ * number (none of the three overlaps another); a page is never both source and destination. Entries
+ * that name a page with count 0 stay (KVQ_DEVERR_PAGE). Every table that names pages of the pool has
+ * to be rewritten: there is one. */
 kvq_status kvq_pages_compact(int32_t* page_refs, int num_pages, int32_t* block_table, int num_seqs,
                              int max_pages_per_seq, int32_t* copy_src, int32_t* copy_dst, int32_t* n_moves,
                              int32_t* dev_err, kvq_stream_t stream);

@@ -119,7 +119,10 @@ kvq_status check_commit(int num_caches, int B, int N, const int32_t* ctx, const 
   if (num_caches < 1 || B < 1 || B > KVQ_MAX_SEQS) return KVQ_ERR_INVALID_ARG;
   if (num_caches > KVQ_MAX_CACHES || N < 1 || N > KVQ_MAX_TREE) return KVQ_ERR_UNSUPPORTED;
   if (!ctx || !path || !n_accept || !dev_err) return KVQ_ERR_INVALID_ARG;
-  if (ctx_out && overlap(ctx, 4 * (size_t)B, ctx_out, 4 * (size_t)B)) return KVQ_ERR_INVALID_ARG;
+  // ctx_out is written by some blocks while others still read the lists
+  const size_t n = 4 * (size_t)B;
+  if (ctx_out && (overlap(ctx, n, ctx_out, n) || overlap(n_accept, n, ctx_out, n) || overlap(path, n * N, ctx_out, n)))
+    return KVQ_ERR_INVALID_ARG;
   return KVQ_OK;
 }
 
@@ -166,6 +169,12 @@ kvq_status pool_call(cudaError_t (*launch)(const kvq::PoolJob&, cudaStream_t), i
   if (n < 0 || n > KVQ_MAX_SEQS) return KVQ_ERR_INVALID_ARG;
   if (n == 0) return KVQ_OK;
   if (!a || !b || !c) return KVQ_ERR_INVALID_ARG;
+  if (src) {  // fork's lists are written while others still read theirs
+    const size_t bytes = 4 * (size_t)n;
+    if (overlap(src, bytes, dst, bytes)) return KVQ_ERR_INVALID_ARG;
+    for (const int32_t* in : {a, b, c})
+      if (overlap(src, bytes, in, bytes) || overlap(dst, bytes, in, bytes)) return KVQ_ERR_INVALID_ARG;
+  }
   kvq::PoolJob j{refs, num_pages, table, num_seqs, max_pages, n, a, b, c, src, dst, nullptr, dev_err};
   return from_cuda(launch(j, (cudaStream_t)stream));
 }
@@ -399,6 +408,9 @@ kvq_status kvq_pages_compact(int32_t* page_refs, int num_pages, int32_t* block_t
   const kvq_status st = check_pool(page_refs, num_pages, block_table, num_seqs, max_pages_per_seq, dev_err);
   if (st != KVQ_OK) return st;
   if (!copy_src || !copy_dst || !n_moves) return KVQ_ERR_INVALID_ARG;
+  const size_t bytes = 4 * (size_t)(num_pages / 2);
+  if (overlap(copy_src, bytes, copy_dst, bytes) || overlap(copy_src, bytes, n_moves, 4) || overlap(copy_dst, bytes, n_moves, 4))
+    return KVQ_ERR_INVALID_ARG;
   kvq::PoolJob j{page_refs, num_pages, block_table, num_seqs, max_pages_per_seq, 0,       nullptr,
                  nullptr,   nullptr,   copy_src,    copy_dst, n_moves,           dev_err};
   return from_cuda(kvq::launch_pages_compact(j, (cudaStream_t)stream));
