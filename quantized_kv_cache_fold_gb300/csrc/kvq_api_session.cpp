@@ -407,7 +407,7 @@ kvq_status kvq_pages_compact(int32_t* page_refs, int num_pages, int32_t* block_t
                              int32_t* dev_err, kvq_stream_t stream) {
   const kvq_status st = check_pool(page_refs, num_pages, block_table, num_seqs, max_pages_per_seq, dev_err);
   if (st != KVQ_OK) return st;
-  if (!copy_src || !copy_dst || !n_moves) return KVQ_ERR_INVALID_ARG;
+  if (!n_moves || (num_pages > 1 && (!copy_src || !copy_dst))) return KVQ_ERR_INVALID_ARG;  // one page: empty lists
   const size_t bytes = 4 * (size_t)(num_pages / 2);
   if (overlap(copy_src, bytes, copy_dst, bytes) || overlap(copy_src, bytes, n_moves, 4) || overlap(copy_dst, bytes, n_moves, 4))
     return KVQ_ERR_INVALID_ARG;
