@@ -476,15 +476,17 @@ def kvq_tree_attn_fp8_swa(ring: Fp8Ring, q, pos0, tree_mask, window: int, k_scal
         raise KvqError("kvq_tree_attn_fp8_swa", status)
 
 
-def _layers(layers):
-    """The layers' descriptors one behind the other (each a ctypes structure: its bytes)."""
+def _layers(layers, kind):
+    """The layers' descriptors, all of one kind, one behind the other (each a ctypes structure: its bytes)."""
+    if list(map(type, layers)).count(kind) != len(layers):
+        raise TypeError(f"the layers must be {kind.__name__}, got {sorted(t.__name__ for t in set(map(type, layers)))}")
     return b"".join(layers)
 
 
-def _tree_commit(name, layers, ctx_len, path, n_accept, dev_err, ctx_out, stream):
-    i32 = _torch().int32
+def _tree_commit(name, kind, layers, ctx_len, path, n_accept, dev_err, ctx_out, stream):
+    i32, descriptors = _torch().int32, _layers(layers, kind)
     (B, N), dev = path.shape, _dev(path, "path")
-    status = getattr(lib, name)(_layers(layers), len(layers), B, N, _is(ctx_len, i32, (B,), "ctx_len", dev),
+    status = getattr(lib, name)(descriptors, len(layers), B, N, _is(ctx_len, i32, (B,), "ctx_len", dev),
                                 _is(path, i32, (B, N), "path", dev), _is(n_accept, i32, (B,), "n_accept", dev),
                                 None if ctx_out is None else _is(ctx_out, i32, (B,), "ctx_out", dev), _err(dev_err, dev),
                                 _here(dev, stream))
@@ -495,12 +497,12 @@ def _tree_commit(name, layers, ctx_len, path, n_accept, dev_err, ctx_out, stream
 def kvq_tree_commit_int4(caches, ctx_len, path, n_accept, dev_err, ctx_out=None, stream=None):
     """Moves the accepted tokens path[b, :n_accept[b]] of each tree right behind the context in every
     one of the layers `caches` (a list of Int4Cache); ctx_out receives the new context lengths."""
-    _tree_commit("kvq_tree_commit_int4", caches, ctx_len, path, n_accept, dev_err, ctx_out, stream)
+    _tree_commit("kvq_tree_commit_int4", Int4Cache, caches, ctx_len, path, n_accept, dev_err, ctx_out, stream)
 
 
 def kvq_tree_commit_fp8(rings, pos0, path, n_accept, dev_err, ctx_out=None, stream=None):
     """kvq_tree_commit_int4 for sliding-window layers (a list of Fp8Ring)."""
-    _tree_commit("kvq_tree_commit_fp8", rings, pos0, path, n_accept, dev_err, ctx_out, stream)
+    _tree_commit("kvq_tree_commit_fp8", Fp8Ring, rings, pos0, path, n_accept, dev_err, ctx_out, stream)
 
 
 def _pool(page_refs, block_table):
@@ -555,8 +557,9 @@ def kvq_pages_compact(page_refs, block_table, copy_src, copy_dst, n_moves, dev_e
 def kvq_pages_copy(caches, src, dst, dev_err, count=None, stream=None):
     """Copies page src[i] to page dst[i] in every one of the layers `caches` (pairs with -1 are passed
     over), for i < n or i < count (a device int32 tensor of one entry)."""
-    i32, n, dev = _torch().int32, src.shape[0], _dev(src, "src")
-    status = lib.kvq_pages_copy(_layers(caches), len(caches), n, _is(src, i32, (n,), "src", dev), _is(dst, i32, (n,), "dst", dev),
+    i32, descriptors = _torch().int32, _layers(caches, Int4Cache)
+    n, dev = src.shape[0], _dev(src, "src")
+    status = lib.kvq_pages_copy(descriptors, len(caches), n, _is(src, i32, (n,), "src", dev), _is(dst, i32, (n,), "dst", dev),
                                 None if count is None else _is(count, i32, (1,), "count", dev), _err(dev_err, dev),
                                 _here(dev, stream))
     if status:
