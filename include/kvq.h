@@ -408,7 +408,9 @@ kvq_status kvq_tree_attn_int4_fwht(const kvq_int4_cache* cache, const float* wq,
  *   (its depth in the tree), and its window reaches back from there: context positions above that
  *   position - window, and the drafted tokens of its mask.
  *   q is used as given and in fp16: NaN for rows as above, without a flag. workspace and out as
- *   above; other arguments as kvq_decode_attn_fp8_swa.
+ *   above; out must not overlap k_new, v_new, or q but for a q of its own type in its very place
+ *   (over the int4 cache it may: q, k_new and v_new are read first). Other arguments as
+ *   kvq_decode_attn_fp8_swa.
  * Requires window >= N and capacity >= window + N - 1.
  */
 kvq_status kvq_tree_attn_fp8_swa(const kvq_fp8_ring* ring, const void* q, kvq_dtype dtype, int B, int N,

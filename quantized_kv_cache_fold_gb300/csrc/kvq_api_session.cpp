@@ -278,6 +278,12 @@ kvq_status kvq_tree_attn_fp8_swa(const kvq_fp8_ring* ring, const void* q, kvq_dt
   if (st != KVQ_OK) return st;
   if (window < N || (long long)window + N - 1 > ring->capacity) return KVQ_ERR_INVALID_ARG;
   if (!(k_scale > 0.0f) || !(v_scale > 0.0f) || std::isinf(k_scale) || std::isinf(v_scale)) return KVQ_ERR_INVALID_ARG;
+  // Rows of the output are written while other rows of q (and of k_new, v_new) are still read. A row's own query is
+  // read before, so the output may take q's place exactly.
+  const size_t rows = (size_t)B * N * KVQ_HEAD_DIM, in = dtype == KVQ_BF16 ? 2 : 4, res = out_dtype == KVQ_BF16 ? 2 : 4;
+  if (overlap(q, rows * num_q_heads * in, out, rows * num_q_heads * res) && !(q == out && in == res)) return KVQ_ERR_INVALID_ARG;
+  for (const void* x : {k_new, v_new})
+    if (x && overlap(x, rows * ring->num_kv_heads * in, out, rows * num_q_heads * res)) return KVQ_ERR_INVALID_ARG;
   const bool few_pairs = (long long)B * ring->num_kv_heads < kvq::device_sms();
   if (N <= kvq::kTreeRingTokens &&
       N * (num_q_heads / ring->num_kv_heads) <= (few_pairs ? kvq::kTreeRingRowsFewPairs : kvq::kTreeRingRows) &&
