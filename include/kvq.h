@@ -341,9 +341,10 @@ kvq_status kvq_decode_attn_int4_noalloc(const kvq_int4_cache* cache, const float
  *   strides:  host int64[8] or NULL (packed): elements between tokens and between heads of q, k, v
  *             and out, in this order (q token, q head, k token, ...). Each a positive multiple of 8;
  *             rows of 128 elements are contiguous.
- *   cu_seqlens: device int32[B+1], 0 = cu_seqlens[0] <= ... <= cu_seqlens[B] <= T (else the
- *             sequences outside that are skipped, KVQ_DEVERR_POS). Empty sequences are allowed.
- *             Rows of out behind cu_seqlens[B] are left as they were.
+ *   cu_seqlens: device int32[B+1], 0 <= cu_seqlens[0] <= ... <= cu_seqlens[B] <= T (else the
+ *             sequences outside that, or that overlap one before them, are skipped,
+ *             KVQ_DEVERR_POS). Empty sequences are allowed. Rows of out that no sequence has are
+ *             left as they were.
  *   out:      device [T][num_q_heads][128] of `dtype`, rounded once from fp32. It must not overlap
  *             the inputs.
  *   workspace: device, >= kvq_prompt_workspace_bytes(T, B, num_q_heads, num_kv_heads), 256-byte

@@ -159,6 +159,17 @@ __device__ __forceinline__ void find_item(const int* nt, int B, int pairs, int o
   }
 }
 
+// Offsets that go back may name rows twice: a sequence that overlaps an earlier one is skipped too (nt: row tiles of
+// each, 0 where it is skipped), so that every output row has one writer.
+__device__ __noinline__ void drop_overlapping(int* nt, const int32_t* cu, int B) {
+  int end = 0;
+  for (int b = 0; b < B; ++b) {
+    if (nt[b] == 0) continue;
+    if (cu[b] < end) nt[b] = 0;
+    else end = cu[b + 1];
+  }
+}
+
 // Of two pairs of 16-bit values: the larger of m (magnitudes) and |w|, NaN where either is.
 template <bool F16>
 __device__ __forceinline__ uint32_t max_magnitude(uint32_t m, uint32_t w) {
@@ -241,15 +252,20 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   fence_barrier_init();
   griddep_wait();
   griddep_launch_dependents();
+  bool bad = false;
   for (int b = threadIdx.x; b < j.B; b += kThreads) {
     const int s = j.cu_seqlens[b], e = j.cu_seqlens[b + 1];
     const bool ok = s >= 0 && e >= s && e <= j.T;
     if (!ok && blockIdx.x == 0) set_err(j.dev_err, KVQ_DEVERR_POS);
     sm.nt[b] = ok ? (e - s + kRows - 1) / kRows : 0;
+    bad |= !ok;
   }
   if (warp == 9) tmem_alloc_512(&sm.taddr);
   tc_fence_before();
-  __syncthreads();
+  if (__builtin_expect(__syncthreads_or(bad), 0)) {
+    if (threadIdx.x == 0) drop_overlapping(sm.nt, j.cu_seqlens, j.B);
+    __syncthreads();
+  }
   tc_fence_after();
   const uint32_t tmem = sm.taddr;
 
@@ -541,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             }
           }
         }
-        const float neg = base == -INFINITY ? 0.0f : (F16 ? kWeightRaise : 0.0f) - base;
+        const float neg = base == -INFINITY ? 0.0f : F16 ? kWeightRaise - base : -base;
         const uint64_t c2 = f2(c, c), n2 = f2(neg, neg);
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
