@@ -14,7 +14,7 @@ from dataclasses import dataclass
 import numpy as np
 import torch
 
-from . import (HEAD_DIM, PAGE_SIZE, alloc_fp8_ring, alloc_int4_cache, alloc_prompt_workspace, alloc_tree_workspace,
+from . import (HEAD_DIM, MAX_CACHES, PAGE_SIZE, alloc_fp8_ring, alloc_int4_cache, alloc_prompt_workspace, alloc_tree_workspace,
                alloc_workspace, kvq_build_rotation, kvq_decode_attn_fp8_swa, kvq_decode_attn_int4, kvq_fold_qk,
                kvq_fold_qk_fwht, kvq_fp8_append, kvq_prompt_attn, kvq_rotate_quant_append, kvq_tree_attn_fp8_swa,
                kvq_tree_attn_int4, kvq_tree_commit_fp8, kvq_tree_commit_int4)
@@ -171,13 +171,11 @@ class DecodeStack:
 
     def commit_tree(self, ctx, path, n_accept, ctx_out, stream=None):
         """The accepted branch of every tree becomes context in all layers; ctx_out: the new lengths."""
-        caches = [self.layers[l].cache for l in self.int4_layers()]
-        rings = [self.layers[l].ring for l in self.swa_layers()]
-        if caches:
-            kvq_tree_commit_int4(caches, ctx, path, n_accept, self.dev_err, ctx_out=ctx_out, stream=stream)
-        if rings:
-            kvq_tree_commit_fp8(rings, ctx, path, n_accept, self.dev_err, ctx_out=None if caches else ctx_out,
-                                stream=stream)
+        for commit, layers in ((kvq_tree_commit_int4, [self.layers[l].cache for l in self.int4_layers()]),
+                               (kvq_tree_commit_fp8, [self.layers[l].ring for l in self.swa_layers()])):
+            for i in range(0, len(layers), MAX_CACHES):  # as many layers as a call takes
+                commit(layers[i:i + MAX_CACHES], ctx, path, n_accept, self.dev_err, ctx_out=ctx_out, stream=stream)
+                ctx_out = None  # written once
 
     def read_error(self) -> int:
         return int(self.dev_err.item())
