@@ -110,9 +110,11 @@ struct alignas(16) Smem {
   // then: pre[B + 1], the rings
 };
 
-// Context length of sequence b: clamped into what the cache can hold (`bad` reports that).
+// Context length of sequence b: clamped into what the cache can hold (`bad` reports that). It and the masks are read at
+// L2, not as read-only data: without new rows this is a call's first kernel, which starts before the grid ahead of it (a
+// commit that writes the lengths, say) has ended.
 __device__ __forceinline__ int tree_ctx(const TreeJob& j, int b, bool& bad) {
-  int c = __ldg(j.ctx + b);
+  int c = __ldcg(j.ctx + b);
   const int most = j.fmt == 0 ? j.cache.max_pages_per_seq * kPage - j.N : 1 << 30;
   if (c < 0 || c > most) {
     bad = true;
@@ -650,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_kernel(const __grid_constant
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.q_ready);
       // ---- this thread's row
-      const uint64_t mask = mine ? __ldg(reinterpret_cast<const unsigned long long*>(j.mask) + (size_t)pc.b * j.N + div_g(p, r0 + r)) & all : 0ull;
+      const uint64_t mask = mine ? __ldcg(reinterpret_cast<const unsigned long long*>(j.mask) + (size_t)pc.b * j.N + div_g(p, r0 + r)) & all : 0ull;
       const int lo = FMT == 0 ? 0 : max(0, ctx + max(1, __popcll(mask)) - j.window);  // first position that it sees
       float base = -INFINITY;
       uint64_t l2[2] = {0ull, 0ull};
