@@ -383,6 +383,11 @@ kvq_status kvq_prompt_attn(const void* q, const void* k, const void* v, kvq_dtyp
  *   The products take q~ in fp16. A row whose q~ is not finite, or has an element of magnitude
  *   65520 or more, is NaN (0 if it attends to nothing); a query that is not finite is flagged
  *   (KVQ_DEVERR_NONFINITE) as well. No other row changes.
+ *   Precision: sums, maxima and the join are fp32, q~ and the weights enter the products in fp16
+ *   (2^-11 of the value; weights by 2^-31 of the largest at least). With up to 48 rows per KV head
+ *   (N times the query heads of one) the codes enter as they are, scale and offset in fp32; with
+ *   more, keys and values are dequantised to fp16 first (2^-11 of the value, keys by 2^-15 at
+ *   least). So 48 and 49 rows of the same call differ by these roundings.
  *   Other arguments, readings of positions and errors as kvq_decode_attn_int4. A position whose
  *   block-table entry is outside the pool is skipped (KVQ_DEVERR_PAGE). Slots of a page that were
  *   never written are masked, but their scales are read: a pool is zeroed before its first use.

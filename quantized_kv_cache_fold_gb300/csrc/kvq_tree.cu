@@ -230,9 +230,10 @@ __device__ __forceinline__ uint32_t both(float x) { return pack_f16x2(x, x); }
 
 // Half of a token's K record -> its row of the K tile. Word w holds dims 8w..8w+7 in the order 0, 4, 1, 5, 2, 6, 3,
 // 7 (as the nibbles pair up in 32 bits; Q' takes the same). A code is the subnormal c 2^-24 (even nibbles)
-// or c 2^-20 (odd ones); the tile holds (c s + o) 2^-9, one fma a pair, rounded once to fp16 (off by at most 2^-11 of
-// the value, or 2^-16 where the value is below 2^-5): so s 2^15 fits fp16 for s < 2, which keys of norm sqrt(128) always
-// have (a larger scale takes fp32). The scores take the 2^9 back. With a product by
+// or c 2^-20 (odd ones); the tile holds (c s + o) 2^-9, one fma a pair, so that s 2^15 fits fp16 for s < 2, which keys of
+// norm sqrt(128) always have (a larger scale takes fp32). The fma rounds to fp16: off by 2^-11 of the value, or by 2^-16
+// where the value is below 2^-5; o 2^-9 is exact in fp16 where |o| is 2^-5 or more and off by up to 2^-16 below. The
+// scores take the 2^9 back. With a product by
 // 2^15 of its own first: 64 x 16,384, 80 rows, 313 instead of 305 us.
 // Places of a token's words of one half of the dims: word 8 part + 4 c + i at chunk(c) + off[i].
 struct RowWords {
