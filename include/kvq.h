@@ -348,7 +348,9 @@ kvq_status kvq_decode_attn_int4_noalloc(const kvq_int4_cache* cache, const float
  *   out:      device [T][num_q_heads][128] of `dtype`, rounded once from fp32. It must not overlap
  *             the inputs.
  *   workspace: device, >= kvq_prompt_workspace_bytes(T, B, num_q_heads, num_kv_heads), 256-byte
- *             aligned; contents need no initialisation. Calls that may overlap need one each.
+ *             aligned. As every attention call takes one, so does this, but its kernel keeps everything
+ *             on chip: 256 bytes whatever the sizes (0 for arguments that no call accepts), neither
+ *             read nor written, so any calls may share one.
  *   A row is NaN only where a key or value that it attends to makes it so: non-finite values in
  *   masked places do not reach it. Nothing is skipped for non-finite inputs.
  * Requires 1 <= B <= KVQ_MAX_SEQS, 0 <= T (T == 0 is a no-op), sm_scale > 0; q, k, v and out

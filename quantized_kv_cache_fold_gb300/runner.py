@@ -137,7 +137,7 @@ class DecodeStack:
         q, k and v as kvq_prompt_attn takes them. The keys and values go into the cache by
         append_prompt."""
         L = self.layers[l]
-        if workspace is None:
+        if workspace is None:  # (of 256 bytes, see kvq.h)
             workspace = self._alloc_for(stream, alloc_prompt_workspace, q.shape[0], cu_seqlens.shape[0] - 1, self.Hq, self.Hkv)
         kvq_prompt_attn(q, k, v, cu_seqlens, out, workspace, self.dev_err,
                         window=0 if isinstance(L, Int4Layer) else L.window, stream=stream)
