@@ -145,13 +145,17 @@ struct TreeJob {
 // and scale the scores, so few rows cost little, where launch_tree first makes fp16 tiles of every token. 64 sequences of
 // 16,384 tokens, 4 KV heads, verify kernels / launch_tree: 106 / 259 us with 5 rows, 164 / 262 with 15, 195 / 263 with
 // 20, 254 / 284 with 45; 8 of 8,192: 21 / 35, 32 / 37, 29 / 37, 40 / 42; one of 4,096: 21-25 / 22-24 throughout; one of
-// 65,536: 24 / 42, 30 / 44, 30 / 46, 37 / 44.
+// 65,536: 24 / 42, 30 / 44, 30 / 46, 37 / 44. The same with 1 and 8 KV heads (5, 15, 25, 40, 45 rows): 64 sequences (16,384;
+// 8,192) 38-82 / 81-92 and 112-291 / 267-309, 8 of 8,192 17-25 / 28-34 and 26-55 / 51-61; only one of 65,536 with one KV
+// head is slower from 15 rows on, 40-45 / 39-41.
 constexpr int kTreeFewRows = kMaxRows;
 // Over a ring, trees of up to 8 drafted tokens and 16 rows, or 24 rows while there are fewer (sequence, KV head) pairs
 // than SMs, take the verify block's cluster kernel where the ring is small enough for it (swa_cluster_path): one launch
 // with the append in it. Rings of 576 slots (window 513), 4 KV heads, cluster kernel / launch_tree: one sequence 6.4 /
 // 18.1 us with 5 rows, 9.0 / 18.6 with 10, 13.9 / 19.0 with 20; 8 sequences 6.5 / 22.9, 9.5 / 23.2, 14.3 / 24.5; 64
-// sequences 13.5 / 22.4, 20.1 / 22.4, but 30.9 / 23.2 with 20; 256 sequences 37 / 71, 51 / 72, 70 / 74.
+// sequences 13.5 / 22.4, 20.1 / 22.4, but 30.9 / 23.2 with 20; 256 sequences 37 / 71, 51 / 72, 70 / 74. Without new rows, 1
+// and 8 KV heads, 5 to 15 rows: 5-8 / 17-18 and 5-8 / 20-21 (one sequence), 6-15 / 27-28 and 23-27 / 37-38 (64), 12-17 / 22-24
+// and 65-91 / 138-140 (256).
 constexpr int kTreeRingRows = 16, kTreeRingRowsFewPairs = 24, kTreeRingTokens = 8;
 size_t workspace_tree_partials_bytes(int B);
 cudaError_t launch_tree(const TreeJob& job, cudaStream_t stream);

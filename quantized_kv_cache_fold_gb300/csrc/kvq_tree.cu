@@ -11,10 +11,12 @@
 //         when a score passes it by more than 8, so P < 2^15)
 //   O += P V       tcgen05.mma, P read from tensor memory
 //
-// Bound by instruction issue: converting a page, and the exponentials of its scores, take longer than the products, and
-// a page costs the same for 1 row as for 128 (fewer than 49 rows take kvq_attn.cu). 64 sequences of 16,384 tokens, 80
-// rows per KV head (581 MB, 1.7e11 operations): 305 us a call, of which the prologue 30 and the join 15; DRAM 26%, tensor
-// pipe 40%, issue slots 60%. 8 of 32k-65k tokens, 320 rows: 298 us, 0.79 PFLOP/s. 64 windows of 513: 25 us.
+// Bound by the chain of a page's life, not by one unit: its copy, conversion, scores, weights and products hand over
+// through one K and one V tile, so conversion waits until the page before is through (the commonest stall: its warps at
+// their barrier, 4.8 per issue), with the tensor pipe 42% and the issue slots 60% busy, DRAM 27%. A page costs the same for
+// 1 row as for 128 (fewer than 49 rows take kvq_attn.cu). 64 sequences of 16,384 tokens, 80 rows per KV head (581 MB,
+// 1.7e11 operations): 303 us a call, of which the prologue 30 and the join 15. 8 of 32k-65k tokens, 320 rows, three
+// groups that convert every page each: 301 us, 0.78 PFLOP/s. 64 windows of 513: 25.6 us.
 //
 // The rounding of q~, K, V and P to fp16 is what keeps both products on the tensor cores: 2^-11 each,
 // against the 2^-8 of a bf16 result; sums, bases and O stay in fp32.
@@ -57,7 +59,7 @@ constexpr uint32_t kColS = 0, kColO = 128;  // S of page i at + 64 (i & 1), P ov
 constexpr int kQHalf = kGroup * 128;        // bytes of one 64-dim half of Q'
 // K and V tiles. One of each, and the shared memory for copy stages instead: a second tile of K or V lets its
 // conversion run ahead and take issue slots from the chain that everything waits for (64 x 16,384 x 16
-// drafted: 314 us; two of V 333, two of K 350).
+// drafted: 314 us; two of V 333, two of K 350; not measured for short windows).
 constexpr int kKBuf = 1, kVBuf = 1;
 constexpr int kMaxTreeCtas = 320;                       // sizes the partials
 constexpr int kMaxStages = 6;                           // of each ring
