@@ -669,9 +669,15 @@ __global__ void __maxnreg__(NT == 1 ? (FMT == 0 ? KVQ_INT4_MAXREG : 184) : 255)
 #pragma unroll
               for (int j = 0; j < 2; ++j) {
                 float v = -INFINITY;
+                if (TREE && need_mask) {  // token by token: a scale that the row does not see does not count
 #pragma unroll
-                for (int u = 0; u < MTU; ++u) v = fmaxf(v, fmaxf(sc[nt][u][j], sc[nt][u][2 + j]));
-                if (TREE) v += ve;
+                  for (int u = 0; u < MTU; ++u)
+                    v = fmaxf(v, fmaxf(sc[nt][u][j] + scale_exponent(va[u][0]), sc[nt][u][2 + j] + scale_exponent(va[u][1])));
+                } else {
+#pragma unroll
+                  for (int u = 0; u < MTU; ++u) v = fmaxf(v, fmaxf(sc[nt][u][j], sc[nt][u][2 + j]));
+                  if (TREE) v += ve;
+                }
                 mx[nt][j] = v;
                 need |= v > (big ? fminf(thr[nt][j], 0.0f) : thr[nt][j]);
               }

@@ -155,3 +155,36 @@ def expect16(out, q, k, v, seen, sm, dtype):
     tol = (2 * d + 2.0 ** -8) * (p @ v.abs()) + 2.0 ** -8 * o.abs()
     off = (out.double() - o).abs()
     assert bool((off <= tol).all()), f"worst {float((off / tol).max()):.2f} of the tolerance"
+
+
+@pytest.mark.parametrize("below", [12.0, 18.0])
+@pytest.mark.parametrize("N,heads", [(3, (2, 2)), (4, (2, 1)), (12, (1, 1)), (8, (20, 4)), (16, (20, 4))])
+def test_int4_beside_a_hidden_value_of_any_size(N, heads, below):
+    """A drafted token that no row sees, with values and so a scale near the end of fp16, in the page of all the others: in
+    slot 24, which the threads of the row kernels hold together with slot 0, where the heavy key is."""
+    n, B = 24 - (N - 1), 2
+    c = Int4Case([n] * B, N, *heads, seed=N)
+    g = torch.Generator(device="cuda").manual_seed(N)
+    R, _ = kvq.kvq_build_rotation(9)
+    c.Mq = c.Mk = torch.from_numpy(R).cuda()
+    u = direction(g)
+    for b in range(B):
+        k, v = keys_and_values(n, heads[1], u, 64, 1.0, g)
+        kvq.kvq_rotate_quant_append(c.cache, c.Mk, k, v, i32([b] * n), torch.arange(n, device="cuda", dtype=torch.int32), c.err)
+    c.k_new, c.v_new = (x.view(B, N, heads[1], D) for x in keys_and_values(B * N, heads[1], u, 1 << 30, 1.0, g))
+    c.k_new[:, 0], c.v_new[:, 0] = c.k_new[:, 1], c.v_new[:, 1]
+    c.v_new[:, N - 1] *= 4e4
+    c.q = u + 0.02 * torch.randn(B, N, heads[0], D, generator=g, device="cuda")
+    masks = [[1 << (i % (N - 1)) for i in range(N)]] * B
+    sm = below / D
+    out = c.call(masks, sm=sm)
+    q = c.q.double()
+    q = (q / (q.square().mean(-1, keepdim=True) + 1e-6).sqrt()) @ torch.from_numpy(R.astype(np.float64)).cuda().T
+    drafted = torch.tensor([[(m >> j) & 1 for j in range(N - 1)] for m in masks[0]], dtype=torch.bool, device="cuda")
+    seen = torch.cat([torch.ones(N, n, dtype=torch.bool, device="cuda"), drafted], 1)
+    G = heads[0] // heads[1]
+    for b in range(B):
+        for h in range(heads[1]):
+            k, v = (x[:n + N - 1] for x in c.dequantised(b, h, n + N))
+            for hq in range(h * G, (h + 1) * G):
+                expect(out[b, :, hq], q[b, :, hq], k, v, seen, sm, 2)
