@@ -41,8 +41,8 @@
 // next keys too, so that it waits five times a block instead of seven (329 -> 322 us). More waits (V in two halves: 337),
 // polling instead of resting (347) or weights handed over whole (332) cost more than they gain.
 //
-// Measured (20/4 heads): one prompt of 32,768 tokens, bf16: 3.36-3.39 ms, 1.62-1.64 PFLOP/s; 24 prompts of 100-4,000
-// tokens, 4.1e11 operations: 324 us, 1.26 PFLOP/s; 5 of 1,500-9,000, fp16, window 513: 104 us; 4 of up to 96: 10 us.
+// Measured (20/4 heads): one prompt of 32,768 tokens, bf16: 3.28-3.42 ms, 1.61-1.68 PFLOP/s; 24 prompts of 100-4,000
+// tokens, 4.1e11 operations: 318-325 us, 1.25-1.28 PFLOP/s; 5 of 1,500-9,000, fp16, window 513: 104 us; 4 of up to 96: 10 us.
 //
 // Work order: items by descending row tile, so the longest run first, heads of a tile next to each other (they share
 // K and V in L2); CTAs take them in turns, back and forth (c, 2n-1-c, 2n+c, ...), which evens out the descending
