@@ -387,7 +387,8 @@ kvq_status kvq_prompt_attn(const void* q, const void* k, const void* v, kvq_dtyp
  *   (KVQ_DEVERR_NONFINITE) as well. No other row changes.
  *   Precision: sums, maxima and the join are fp32, q~ and the weights enter the products in fp16
  *   (2^-11 of the value; weights by 2^-31 of the largest at least). With up to 48 rows per KV head
- *   (N times the query heads of one) the codes enter as they are, scale and offset in fp32; with
+ *   (N times the query heads of one) the codes enter as they are, counted from the middle of their
+ *   range, scale and offset in fp32: an element is off by 2^-11 of half its record's range; with
  *   more, keys and values are dequantised to fp16 first (2^-11 of the value, keys by 2^-15 at
  *   least). So 48 and 49 rows of the same call differ by these roundings.
  *   Other arguments, readings of positions and errors as kvq_decode_attn_int4. A position whose

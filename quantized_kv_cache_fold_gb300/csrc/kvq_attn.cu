@@ -231,11 +231,15 @@ __device__ __forceinline__ bool tree_sees(const AttnParams& p, int b, int r, int
 // moves when a score + e passes it by more than 15, to 7 below. So P s_V stays below 2^15 whatever the scales, and as far
 // above the type's smallest step as that allows: small scales and weights far below a row's largest keep their share (keys
 // 17 to 20 nats under one whose value is 0, or values of 1e-3: off by up to all of the output with the base at the
-// maximum). P itself and its sums are fp32.
+// maximum). P itself and its sums are fp32. The distance of the largest score to the new base is a whole number (of powers
+// of two) and added last, so that a row of one key has an exact P, and code and offset terms cancel as they should.
 constexpr float kTreeLimit = 15.0f, kTreeBelow = 7.0f;
 
 // Exponent e of s < 2^e for a scale (s >= 0), at least -13 (fp16's smallest normal scale): bounds P by 2^28.
 __device__ __forceinline__ float scale_exponent(float s) { return (float)max((int)(__float_as_uint(s) >> 23) - 126, -13); }
+
+// TREE: that distance, of a row's largest score s and largest score + exponent t (both of the same tokens).
+__device__ __forceinline__ float tree_raise(float s, float t) { return kTreeBelow - ceilf(t - s); }
 
 // Stores n output values; TREE: of the type asked for, and 0 for rows that saw nothing.
 template <bool TREE>
@@ -669,16 +673,10 @@ __global__ void __maxnreg__(NT == 1 ? (FMT == 0 ? KVQ_INT4_MAXREG : 184) : 255)
 #pragma unroll
               for (int j = 0; j < 2; ++j) {
                 float v = -INFINITY;
-                if (TREE && need_mask) {  // token by token: a scale that the row does not see does not count
 #pragma unroll
-                  for (int u = 0; u < MTU; ++u)
-                    v = fmaxf(v, fmaxf(sc[nt][u][j] + scale_exponent(va[u][0]), sc[nt][u][2 + j] + scale_exponent(va[u][1])));
-                } else {
-#pragma unroll
-                  for (int u = 0; u < MTU; ++u) v = fmaxf(v, fmaxf(sc[nt][u][j], sc[nt][u][2 + j]));
-                  if (TREE) v += ve;
-                }
+                for (int u = 0; u < MTU; ++u) v = fmaxf(v, fmaxf(sc[nt][u][j], sc[nt][u][2 + j]));
                 mx[nt][j] = v;
+                if (TREE) v += ve;  // (no less than the largest score + exponent)
                 need |= v > (big ? fminf(thr[nt][j], 0.0f) : thr[nt][j]);
               }
             if (__any_sync(0xffffffffu, need)) {
@@ -687,11 +685,20 @@ __global__ void __maxnreg__(NT == 1 ? (FMT == 0 ? KVQ_INT4_MAXREG : 184) : 255)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                   const float mt = warp_max_g(mx[nt][j]);
-                  const float mnew = fmaxf(m[nt][j], muse[nt][j] + (TREE ? mt - kTreeBelow : mt));
+                  float raise = 0.0f;  // TREE: the largest score's distance to the base
+                  if (TREE) {  // token by token: a scale that the row does not see does not count
+                    float v = -INFINITY;
+#pragma unroll
+                    for (int u = 0; u < MTU; ++u)
+                      v = fmaxf(v, fmaxf(sc[nt][u][j] + scale_exponent(va[u][0]), sc[nt][u][2 + j] + scale_exponent(va[u][1])));
+                    v = warp_max_g(v);
+                    if (mt > -INFINITY) raise = tree_raise(mt, v);
+                  }
+                  const float mnew = fmaxf(m[nt][j], TREE ? muse[nt][j] + mt - raise : muse[nt][j] + mt);
                   if (mnew != m[nt][j]) {
                     const float mu2 = mnew == -INFINITY ? 0.0f : mnew;
                     const float alpha = fast_exp2(m[nt][j] - mu2);
-                    const float delta = muse[nt][j] - mu2;
+                    const float delta = TREE ? -mt : muse[nt][j] - mu2;
                     l[nt][j] *= alpha;
                     ov[nt][j] *= alpha;
 #pragma unroll
@@ -703,6 +710,10 @@ __global__ void __maxnreg__(NT == 1 ? (FMT == 0 ? KVQ_INT4_MAXREG : 184) : 255)
                     for (int u = 0; u < MTU; ++u) {
                       sc[nt][u][j] += delta;
                       sc[nt][u][2 + j] += delta;
+                      if (TREE) {
+                        sc[nt][u][j] += raise;
+                        sc[nt][u][2 + j] += raise;
+                      }
                     }
                     m[nt][j] = mnew;
                     muse[nt][j] = mu2;
@@ -918,7 +929,7 @@ constexpr int kTcBars = 32;                // mbarriers of the kernel (see its l
 
 struct TcLayout {  // offsets from the 1024-byte aligned start of dynamic shared memory
   size_t stages, qt, pt, meta, bars, valid, flags, taddr, uinfo, rowc, rowst, ovrow, red, rowm, rcx, rcy, ralpha, rdelta,
-      pre, total;
+      rowt, pre, total;
   __host__ __device__ explicit TcLayout(int B) {
     stages = 0;
     qt = kTcStages * (size_t)kStage4;  // 69632 = 68 * 1024
@@ -938,7 +949,8 @@ struct TcLayout {  // offsets from the 1024-byte aligned start of dynamic shared
     rcy = rcx + 4 * kTcMaxRows;
     ralpha = rcy + 4 * kTcMaxRows;
     rdelta = ralpha + 4 * kTcMaxRows;
-    pre = rdelta + 4 * kTcMaxRows;
+    rowt = rdelta + 4 * kTcMaxRows;
+    pre = rowt + 5 * 4 * kTcMaxRows;
     total = align_up(pre + 4 * (size_t)(B + 1), 16);
   }
 };
@@ -1024,6 +1036,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
   float* rcy = reinterpret_cast<float*>(smem + L.rcy);
   float* ralpha = reinterpret_cast<float*>(smem + L.ralpha);  // a base move: factor on a row's sums and O
   float* rdelta = reinterpret_cast<float*>(smem + L.rdelta);  // and shift of its scores
+  float* rowt = reinterpret_cast<float*>(smem + L.rowt);      // TREE: maxima of score + exponent as rowm, then a row's raise
   int* pre = reinterpret_cast<int*>(smem + L.pre);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr uint32_t kFinBar = 1;
@@ -1444,8 +1457,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
         // ---- rare: move the base of the rows whose maximum passed it (row maxima over the 128 tokens)
   #pragma unroll
         for (int i = 0; i < H; ++i) {
-          const float m1 = warp_max_all(TREE ? d[i] + ve : d[i]);
+          const float m1 = warp_max_all(d[i]);
           if (lane == 0) rowm[q * kTcMaxRows + r0 + i] = m1;
+          if (TREE) {  // and of score + exponent
+            const float m2 = warp_max_all(d[i] + ve);
+            if (lane == 0) rowt[q * kTcMaxRows + r0 + i] = m2;
+          }
         }
         named_barrier(kGrpBar, kGrp);
         // one thread per row: the new base (published), the factor alpha on the row's sums and O
@@ -1453,16 +1470,20 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
         bool changed = false;
         if (gt < H) {
           const int r = r0 + gt;
-          float alpha = 1.0f, delta = 0.0f;
+          float alpha = 1.0f, delta = 0.0f, raise = 0.0f;
           if (r < R) {
             const float mt4 = fmaxf(fmaxf(rowm[r], rowm[kTcMaxRows + r]), fmaxf(rowm[2 * kTcMaxRows + r], rowm[3 * kTcMaxRows + r]));
             const float4 c = rowc[r];
             const float mold = rowst[r], muse = -c.y;
-            const float mnew = fmaxf(mold, muse + (TREE ? mt4 - kTreeBelow : mt4));
+            float up = 0.0f;
+            if (TREE && mt4 > -INFINITY)
+              up = tree_raise(mt4, fmaxf(fmaxf(rowt[r], rowt[kTcMaxRows + r]), fmaxf(rowt[2 * kTcMaxRows + r], rowt[3 * kTcMaxRows + r])));
+            const float mnew = fmaxf(mold, TREE ? muse + mt4 - up : muse + mt4);
             if (mnew != mold) {
               const float mu2 = mnew == -INFINITY ? 0.0f : mnew;
               alpha = fast_exp2(mold - mu2);
-              delta = muse - mu2;
+              delta = TREE ? -mt4 : muse - mu2;
+              raise = up;
               changed = true;
               const float nb = mnew == -INFINITY ? 0.0f : -mnew;
               rowst[r] = mnew;
@@ -1472,6 +1493,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
           }
           ralpha[r] = alpha;
           rdelta[r] = delta;
+          if (TREE) rowt[4 * kTcMaxRows + r] = raise;
         }
         if (named_barrier_or(kGrpBar, kGrp, changed)) {
   #pragma unroll
@@ -1481,7 +1503,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
             ov2[i] = mul_f2(ov2[i], a2);
           }
   #pragma unroll
-          for (int i = 0; i < H; ++i) d[i] += rdelta[r0 + i];
+          for (int i = 0; i < H; ++i) {
+            d[i] += rdelta[r0 + i];
+            if (TREE) d[i] += rowt[4 * kTcMaxRows + r0 + i];
+          }
           // O (this thread's lane, the half's rows) -- not on a segment's first unit: O starts from
           // zero there. PV(v - 1) must have completed.
           if (!ufirst) {

@@ -144,7 +144,7 @@ struct TreeJob {
 // verify block's kernels (launch_attention) with the mask in place of the diagonal: those multiply the codes as they are
 // and scale the scores, so few rows cost little, where launch_tree first makes fp16 tiles of every token. 64 sequences of
 // 16,384 tokens, 4 KV heads, verify kernels / launch_tree: 106 / 259 us with 5 rows, 164 / 262 with 15, 195 / 263 with
-// 20, 254 / 284 with 45; 8 of 8,192: 21 / 35, 32 / 37, 29 / 37, 40 / 42; one of 4,096: 21-25 / 22-24 throughout; one of
+// 20, 258 / 284 with 45; 8 of 8,192: 21 / 35, 32 / 37, 29 / 37, 40 / 42; one of 4,096: 21-25 / 22-24 throughout; one of
 // 65,536: 24 / 42, 30 / 44, 30 / 46, 37 / 44. The same with 1 and 8 KV heads (5, 15, 25, 40, 45 rows): 64 sequences (16,384;
 // 8,192) 38-82 / 81-92 and 112-291 / 267-309, 8 of 8,192 17-25 / 28-34 and 26-55 / 51-61; only one of 65,536 with one KV
 // head is slower from 15 rows on, 40-45 / 39-41.

@@ -80,3 +80,21 @@ def test_the_stacks_outputs_are_the_calls_outputs(N):
     kvq.kvq_tree_attn_fp8_swa(R.ring, qs[0], i32(lens), masks, 64, R.k_scale, R.v_scale, want[0], ws, st.dev_err)
     kvq.kvq_tree_attn_int4(F.cache, F.Mq, F.Mk, qs[1], i32(lens), masks, want[1], ws, st.dev_err)
     assert all(torch.equal(a, b) for a, b in zip(got, want)) and st.read_error() == 0
+
+
+@pytest.mark.parametrize("v_gain", [1e-3, 1.0, 2e3])
+@pytest.mark.parametrize("N,heads", [(3, (2, 2)), (4, (4, 1)), (7, (12, 4)), (8, (20, 4)), (16, (20, 4))])
+def test_rows_of_one_key_are_its_value(N, heads, v_gain):
+    """No context and one bit: the output is the dequantised value. Row kernels (up to 48 rows per KV head): its weight is a
+    power of two, so code and offset terms are off by fp32 roundings of the record's range; tiles: the value in fp16."""
+    c = Int4Case([0, 0], N, *heads, seed=31, v_gain=v_gain)
+    at = [[(5 * i + b) % N for i in range(N)] for b in range(2)]
+    out = c.call([[1 << j for j in a] for a in at]).double()
+    G = heads[0] // heads[1]
+    few = N * G <= 48
+    for b in range(2):
+        for h in range(heads[1]):
+            _, v = c.dequantised(b, h, N)
+            want = v[at[b]][:, None]
+            tol = 2.0 ** -23 * (v.amax(1) - v.amin(1) + v.abs().amax(1))[at[b]][:, None, None] + (0.0 if few else U * want.abs() + 2.0 ** -25)
+            assert bool(((out[b, :, h * G:(h + 1) * G] - want).abs() <= tol).all())
