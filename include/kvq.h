@@ -362,6 +362,16 @@ kvq_status kvq_prompt_attn(const void* q, const void* k, const void* v, kvq_dtyp
                            int window, float sm_scale, void* out, void* workspace, size_t workspace_bytes,
                            int32_t* dev_err, kvq_stream_t stream);
 
+/*
+ * kvq_prompt_attn_sinks -- kvq_prompt_attn with a window and a few first tokens that stay visible: token i attends to
+ *   its tokens max(0, i-window+1)..i and to tokens 0..min(sinks, i+1)-1 (each once, where the two meet).
+ *   sinks: >= 0 (0, or window <= 0: kvq_prompt_attn). All other arguments as there.
+ */
+kvq_status kvq_prompt_attn_sinks(const void* q, const void* k, const void* v, kvq_dtype dtype, int T, int B,
+                                 int num_q_heads, int num_kv_heads, const int64_t* strides, const int32_t* cu_seqlens,
+                                 int window, int sinks, float sm_scale, void* out, void* workspace,
+                                 size_t workspace_bytes, int32_t* dev_err, kvq_stream_t stream);
+
 /* ------------------------------------------------------------------ a tree of drafted tokens */
 
 #define KVQ_MAX_TREE 64 /* drafted tokens of one sequence's tree */

@@ -88,6 +88,9 @@ def _load():
     L.kvq_prompt_attn.restype = i32
     L.kvq_prompt_attn.argtypes = [vp, vp, vp, i32, i32, i32, i32, i32, ctypes.POINTER(i64), vp, i32, f32, vp, vp, sz,
                                   vp, vp]
+    L.kvq_prompt_attn_sinks.restype = i32
+    L.kvq_prompt_attn_sinks.argtypes = [vp, vp, vp, i32, i32, i32, i32, i32, ctypes.POINTER(i64), vp, i32, i32, f32, vp, vp,
+                                        sz, vp, vp]
     for name in ("kvq_tree_attn_int4", "kvq_tree_attn_int4_fwht"):
         getattr(L, name).restype = i32
         getattr(L, name).argtypes = [ctypes.POINTER(Int4Cache), vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, f32,
@@ -380,10 +383,11 @@ def alloc_prompt_workspace(T: int, B: int, num_q_heads: int, num_kv_heads: int, 
 
 
 def kvq_prompt_attn(q, k, v, cu_seqlens, out, workspace, dev_err, window: int = 0,
-                    sm_scale: float = HEAD_DIM ** -0.5, stream=None):
+                    sm_scale: float = HEAD_DIM ** -0.5, stream=None, sinks: int = 0):
     """Causal attention over packed prompts. q, out [T, Hq, 128], k, v [T, Hkv, 128] (bf16 or fp16; any
     token and head strides that are multiples of 8, such as views of one projection's output),
-    cu_seqlens int32[B + 1]; window <= 0: none."""
+    cu_seqlens int32[B + 1]; window <= 0: none. sinks: first tokens that stay visible outside the window
+    (kvq_prompt_attn_sinks)."""
     torch = _torch()
     dtype = q.dtype
     if dtype is not torch.bfloat16 and dtype is not torch.float16:
@@ -405,11 +409,12 @@ def kvq_prompt_attn(q, k, v, cu_seqlens, out, workspace, dev_err, window: int = 
     else:  # of an extent of one the stride does not matter: the packed one
         strides = _Strides(*(x for st, h in ((sq, Hq), (sk, Hkv), (sv, Hkv), (so, Hq))
                              for x in (st[0] if T > 1 else max(1, h) * D, st[1] if h > 1 else D)))
-    status = lib.kvq_prompt_attn(q.data_ptr(), k.data_ptr(), v.data_ptr(), BF16 if dtype is torch.bfloat16 else F16, T,
-                                 B, Hq, Hkv, strides, cu, window, sm_scale, out.data_ptr(), workspace.data_ptr(),
-                                 _bytes(workspace, dev), _err(dev_err, dev), _here(dev, stream))
+    fn, seen = (lib.kvq_prompt_attn_sinks, (window, sinks)) if sinks else (lib.kvq_prompt_attn, (window,))
+    status = fn(q.data_ptr(), k.data_ptr(), v.data_ptr(), BF16 if dtype is torch.bfloat16 else F16, T, B, Hq, Hkv, strides,
+                cu, *seen, sm_scale, out.data_ptr(), workspace.data_ptr(), _bytes(workspace, dev), _err(dev_err, dev),
+                _here(dev, stream))
     if status:
-        raise KvqError("kvq_prompt_attn", status)
+        raise KvqError("kvq_prompt_attn_sinks" if sinks else "kvq_prompt_attn", status)
 
 
 _Strides = ctypes.c_int64 * 8

@@ -2,6 +2,7 @@
 // tokens, the commit of its accepted branch, and the page pool. Host-side argument checks and
 // dispatch only; see include/kvq.h for the contract of each call.
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -179,19 +180,10 @@ kvq_status pool_call(cudaError_t (*launch)(const kvq::PoolJob&, cudaStream_t), i
   return from_cuda(launch(j, (cudaStream_t)stream));
 }
 
-}  // namespace
-
-extern "C" {
-
-size_t kvq_prompt_workspace_bytes(int T, int B, int num_q_heads, int num_kv_heads) {
-  if (!prompt_sizes_ok(T, B, num_q_heads, num_kv_heads)) return 0;
-  return 256;  // the kernel keeps everything on chip: the size of a valid call's workspace, nothing more
-}
-
-kvq_status kvq_prompt_attn(const void* q, const void* k, const void* v, kvq_dtype dtype, int T, int B,
-                           int num_q_heads, int num_kv_heads, const int64_t* strides, const int32_t* cu_seqlens,
-                           int window, float sm_scale, void* out, void* workspace, size_t workspace_bytes,
-                           int32_t* dev_err, kvq_stream_t stream) {
+kvq_status prompt_impl(const void* q, const void* k, const void* v, kvq_dtype dtype, int T, int B, int num_q_heads,
+                       int num_kv_heads, const int64_t* strides, const int32_t* cu_seqlens, int window, int sinks,
+                       float sm_scale, void* out, void* workspace, size_t workspace_bytes, int32_t* dev_err,
+                       kvq_stream_t stream) {
   if (dtype == KVQ_F32) return KVQ_ERR_UNSUPPORTED;
   if (dtype != KVQ_BF16 && dtype != KVQ_F16) return KVQ_ERR_INVALID_ARG;
   if (!prompt_sizes_ok(T, B, num_q_heads, num_kv_heads)) return KVQ_ERR_INVALID_ARG;
@@ -234,9 +226,36 @@ kvq_status kvq_prompt_attn(const void* q, const void* k, const void* v, kvq_dtyp
   j.vs_t = st[4], j.vs_h = st[5], j.os_t = st[6], j.os_h = st[7];
   j.cu_seqlens = cu_seqlens;
   j.window = window > 0 ? window : 0;
+  j.sinks = std::min(sinks, T);
   j.sm_scale = sm_scale;
   j.dev_err = dev_err;
   return from_cuda(kvq::launch_prompt(j, (cudaStream_t)stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t kvq_prompt_workspace_bytes(int T, int B, int num_q_heads, int num_kv_heads) {
+  if (!prompt_sizes_ok(T, B, num_q_heads, num_kv_heads)) return 0;
+  return 256;  // the kernel keeps everything on chip: the size of a valid call's workspace, nothing more
+}
+
+kvq_status kvq_prompt_attn(const void* q, const void* k, const void* v, kvq_dtype dtype, int T, int B,
+                           int num_q_heads, int num_kv_heads, const int64_t* strides, const int32_t* cu_seqlens,
+                           int window, float sm_scale, void* out, void* workspace, size_t workspace_bytes,
+                           int32_t* dev_err, kvq_stream_t stream) {
+  return prompt_impl(q, k, v, dtype, T, B, num_q_heads, num_kv_heads, strides, cu_seqlens, window, 0, sm_scale, out,
+                     workspace, workspace_bytes, dev_err, stream);
+}
+
+kvq_status kvq_prompt_attn_sinks(const void* q, const void* k, const void* v, kvq_dtype dtype, int T, int B,
+                                 int num_q_heads, int num_kv_heads, const int64_t* strides, const int32_t* cu_seqlens,
+                                 int window, int sinks, float sm_scale, void* out, void* workspace,
+                                 size_t workspace_bytes, int32_t* dev_err, kvq_stream_t stream) {
+  if (sinks < 0) return KVQ_ERR_INVALID_ARG;
+  return prompt_impl(q, k, v, dtype, T, B, num_q_heads, num_kv_heads, strides, cu_seqlens, window, sinks, sm_scale, out,
+                     workspace, workspace_bytes, dev_err, stream);
 }
 
 size_t kvq_tree_workspace_bytes(int B, int N, int num_q_heads, int num_kv_heads) {

@@ -116,6 +116,7 @@ struct PromptJob {
   long long qs_t, qs_h, ks_t, ks_h, vs_t, vs_h, os_t, os_h;  // elements
   const int32_t* cu_seqlens;
   int window;  // 0: none
+  int sinks;   // first tokens that stay visible outside the window (0: none)
   float sm_scale;
   int32_t* dev_err;
 };

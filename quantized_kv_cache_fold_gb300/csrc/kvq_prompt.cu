@@ -1,6 +1,7 @@
-// Causal attention over packed prompts (kvq_prompt_attn).
+// Causal attention over packed prompts (kvq_prompt_attn, kvq_prompt_attn_sinks).
 //
-//   o_i = sum_j softmax_j(sm_scale q_i.k_j) v_j, j in [max(0, i - window + 1), i] of i's sequence.
+//   o_i = sum_j softmax_j(sm_scale q_i.k_j) v_j, j in [max(0, i - window + 1), i] of i's sequence; with first tokens that
+//   stay visible (SINKS) also j < sinks.
 //
 // Bound by the tensor cores for all but short prompts: 4 x 128 operations per visible pair of tokens
 // and query head. One persistent CTA per SM. A work item is two tiles of 128 query rows that share the key
@@ -43,6 +44,11 @@
 //
 // Measured (20/4 heads): one prompt of 32,768 tokens, bf16: 3.28-3.42 ms, 1.61-1.68 PFLOP/s; 24 prompts of 100-4,000
 // tokens, 4.1e11 operations: 318-325 us, 1.25-1.28 PFLOP/s; 5 of 1,500-9,000, fp16, window 513: 104 us; 4 of up to 96: 10 us.
+//
+// First tokens that stay visible: an item's blocks are those that hold them, then its window's (where the two meet, one
+// run). The blocks between are neither loaded nor multiplied. A form of its own (SINKS), so that the other keeps its code.
+// 24 prompts of 100-4,000 tokens, window 513, 64 first tokens: 181 us; one of 32,768, fp16, window 4,096, 4 first tokens:
+// 951 us, 1.36 PFLOP/s; 4 of up to 300: 13 us.
 //
 // Work order: items by descending row tile, so the longest run first, heads of a tile next to each other (they share
 // K and V in L2); CTAs take them in turns, back and forth (c, 2n-1-c, 2n+c, ...), which evens out the descending
@@ -111,10 +117,21 @@ struct Range {
 };
 
 // Whether some row of the tile (rows R..R+127 of a sequence of n) misses a token of block j.
-__device__ __forceinline__ bool edge_block(int R, int n, int j, int window) {
+template <bool SINKS>
+__device__ __forceinline__ bool edge_block(int R, int n, int j, int window, int sinks) {
   const int c = j * kRows;
-  return c + kRows - 1 > R || (window && c < R + kRows - window);
+  return c + kRows - 1 > R || (window && c < R + kRows - window && !(SINKS && c + kRows <= sinks));
 }
+
+// The order of blocks: without first tokens jb, jb + 1, ...; with them 0, 1, ... over the `ns` blocks that hold some, then on
+// from jb. (Tiles of an item may differ in jb: the loads go by the first tile's, each tile's softmax by its own.)
+template <bool SINKS>
+__device__ __forceinline__ int first_block(int jb) { return SINKS ? 0 : jb; }
+template <bool SINKS>
+__device__ __forceinline__ int block_after(int b, int jb, int ns) { return SINKS && b + 1 >= ns && b + 1 < jb ? jb : b + 1; }
+// Whether a tile takes block b.
+template <bool SINKS>
+__device__ __forceinline__ bool takes(const Range& r, int b, int ns) { return b < r.je && (b >= r.jb || (SINKS && b < ns)); }
 
 __device__ __forceinline__ int warp_sum_int(int v) { return __reduce_add_sync(0xffffffffu, v); }
 
@@ -198,20 +215,22 @@ __device__ __forceinline__ float value16(uint32_t bits) {
 
 // The output step's slow part: adds the non-finite values of the edge blocks that this row sees to the
 // row as written (the sums are infinite or NaN, so nothing is rounded twice).
-template <bool F16>
+template <bool F16, bool SINKS>
 __device__ __noinline__ void add_nonfinite(const PromptJob& j, const Item& it, int t, int row) {
   const Range r0(it, 0, j.window), r1(it, 1, j.window);
   const int lo = j.window ? max(0, row - j.window + 1) : 0;
   const int hkv = it.hq[t] / (j.Hq / j.Hkv);
   uint16_t* o = static_cast<uint16_t*>(j.out) + (it.s + row) * j.os_t + it.hq[t] * j.os_h;
-  for (int jb = r0.jb; jb < max(r0.je, r1.je); ++jb) {  // tile 0 starts first
+  const int ns = (j.sinks + kRows - 1) / kRows;
+  for (int jb = first_block<SINKS>(r0.jb); jb < max(r0.je, r1.je); jb = block_after<SINKS>(jb, r0.jb, ns)) {  // tile 0 starts first
     bool edge = false;
     for (int u = 0; u < 2; ++u) {
       const Range& r = u ? r1 : r0;
-      edge |= jb >= r.jb && jb < r.je && edge_block(it.r0[u], it.n, jb, j.window);
+      edge |= takes<SINKS>(r, jb, ns) && edge_block<SINKS>(it.r0[u], it.n, jb, j.window, j.sinks);
     }
     if (!edge) continue;
-    for (int tok = max(lo, jb * kRows); tok <= min(row, jb * kRows + kRows - 1); ++tok) {
+    for (int tok = SINKS ? jb * kRows : max(lo, jb * kRows); tok <= min(row, jb * kRows + kRows - 1); ++tok) {
+      if (SINKS && tok < lo && tok >= j.sinks) continue;
       const uint16_t* v = static_cast<const uint16_t*>(j.v) + (it.s + tok) * j.vs_t + hkv * j.vs_h;
       for (int c = 0; c < kD; ++c) {
         const float x = value16<F16>(v[c]);
@@ -221,13 +240,14 @@ __device__ __noinline__ void add_nonfinite(const PromptJob& j, const Item& it, i
   }
 }
 
-template <bool F16>
+template <bool F16, bool SINKS>
 __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_constant__ PromptParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   Smem& sm = *reinterpret_cast<Smem*>(smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u));
   const PromptJob& j = p.j;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* failed = &sm.failed;
+  const int ns = SINKS ? (j.sinks + kRows - 1) / kRows : 0;  // blocks that hold first tokens
 
   if (threadIdx.x == 0) {
     mbar_init(&sm.q_full, 1);
@@ -327,7 +347,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         if (it.n < 0) break;
         const Range a(it, 0, j.window), b(it, 1, j.window);
         const int hkv = it.hq[0] / (j.Hq / j.Hkv);
-        if (!(ok = load(&p.mk, hkv, it.s + a.jb * kRows))) break;  // its place is free before Q's
+        const int start = first_block<SINKS>(a.jb);
+        if (!(ok = load(&p.mk, hkv, it.s + start * kRows))) break;  // its place is free before Q's
         if (k > 0 && !(ok = role_wait(&sm.q_empty, (uint32_t)(k - 1) & 1u, failed))) break;
         const int tiles = b.je > 0 ? 2 : 1;
         mbar_arrive_expect_tx(&sm.q_full, tiles * kTileBytes);
@@ -335,8 +356,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           for (int h = 0; h < 2; ++h)
             tma_load_3d(sm.q[t] + h * (kTileBytes / 2), &p.mq, 64 * h, it.hq[t], it.s + it.r0[t], &sm.q_full);
         ++nq;
-        for (int jb = a.jb; ok && jb < max(a.je, b.je); ++jb)
-          ok = (jb == a.jb || load(&p.mk, hkv, it.s + jb * kRows)) && load(&p.mv, hkv, it.s + jb * kRows);
+        for (int jb = start; ok && jb < max(a.je, b.je); jb = block_after<SINKS>(jb, a.jb, ns))
+          ok = (jb == start || load(&p.mk, hkv, it.s + jb * kRows)) && load(&p.mv, hkv, it.s + jb * kRows);
       }
       if (!ok) {  // no copy may be in flight when the CTA ends
         if (nq > 0) mbar_wait_bounded(&sm.q_full, (uint32_t)(nq - 1) & 1u);
@@ -387,43 +408,45 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       Item it = take(0);
       for (int k = 0; ok && it.n >= 0; ++k) {
         const Range r0(it, 0, j.window), r1(it, 1, j.window);
-        const int jb = r0.jb, je = max(r0.je, r1.je);
+        const int jb = first_block<SINKS>(r0.jb), je = max(r0.je, r1.je);
         ok = wait(&sm.q_full, (uint32_t)k & 1u) && full(kv);
         if (!ok) break;
         tc_fence_after();
         qk(0, kv % kRing);
-        if (r1.je > 0 && r1.jb == jb) qk(1, kv % kRing);
+        if (r1.je > 0 && (SINKS || r1.jb == jb)) qk(1, kv % kRing);
         umma_commit_by(leader, &sm.kv_empty[kv % kRing]);
-        if (je == jb + 1) umma_commit_by(leader, &sm.q_empty);
+        if (block_after<SINKS>(jb, r0.jb, ns) >= je) umma_commit_by(leader, &sm.q_empty);
         Item next = it;
-        for (int b = jb; ok && b < je; ++b) {
-          if (b + 1 == je) next = take(k + 1);
-          const int uv = kv + 2 * (b - jb) + 1, sv = uv % kRing, sk = (uv + 1) % kRing;
+        int uv = kv + 1;
+        for (int b = jb, after; ok && b < je; b = after, uv += 2) {
+          after = block_after<SINKS>(b, r0.jb, ns);
+          if (after >= je) next = take(k + 1);
+          const int sv = uv % kRing, sk = (uv + 1) % kRing;
           ok = ok && wait(&sm.v_ok[sv >> 1], (uint32_t)(uv / kRing) & 1u);  // V and the next K are here
           if (!ok) break;
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             const Range& r = t ? r1 : r0;
             uint32_t& ph = t ? pph1 : pph0;
-            if (b >= r.jb && b < r.je) {
+            if (takes<SINKS>(r, b, ns)) {
               // the first half of the weights may be multiplied while the second is still computed
               if (!(ok = wait(&sm.p_half[t], ph))) break;
               tc_fence_after();
-              pv(t, sv, 0, b > r.jb);
+              pv(t, sv, 0, b > first_block<SINKS>(r.jb));
               if (!(ok = wait(&sm.p_ready[t], ph))) break;
               ph ^= 1u;
               tc_fence_after();
               pv(t, sv, 1, 1u);
               if (b == r.je - 1) umma_commit_by(leader, &sm.o_full[t]);
             }
-            if (b + 1 >= r.jb && b + 1 < r.je) qk(t, sk);
+            if (takes<SINKS>(r, after, ns)) qk(t, sk);
           }
           if (!ok) break;
           umma_commit_by(leader, &sm.kv_empty[sv]);
-          if (b + 1 < je) umma_commit_by(leader, &sm.kv_empty[sk]);
-          if (b + 2 == je) umma_commit_by(leader, &sm.q_empty);
+          if (after < je) umma_commit_by(leader, &sm.kv_empty[sk]);
+          if (after < je && block_after<SINKS>(after, r0.jb, ns) >= je) umma_commit_by(leader, &sm.q_empty);
         }
-        kv += 2 * (je - jb);
+        kv = uv - 1;
         it = next;
       }
       umma_commit_by(leader, &sm.fin);  // arrives once every product issued has completed
@@ -439,13 +462,15 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         __syncwarp();
         if (it.n < 0) break;
         const Range a(it, 0, j.window), b(it, 1, j.window);
-        const int jb = a.jb, je = max(a.je, b.je);
-        for (int blk = jb; blk < je; ++blk) {
-          const int use = kv + 2 * (blk - jb) + 1, slot = use % kRing;
+        const int jb = first_block<SINKS>(a.jb), je = max(a.je, b.je);
+        int use = kv + 1;
+        for (int blk = jb, after; blk < je; blk = after, use += 2) {
+          after = block_after<SINKS>(blk, a.jb, ns);
+          const int slot = use % kRing;
           ok = __all_sync(0xffffffffu, role_wait(&sm.kv_full[slot], (uint32_t)(use / kRing) & 1u, failed));
           if (!ok) break;
-          const bool edge = (blk >= a.jb && blk < a.je && edge_block(it.r0[0], it.n, blk, j.window)) ||
-                            (blk >= b.jb && blk < b.je && edge_block(it.r0[1], it.n, blk, j.window));
+          const bool edge = (takes<SINKS>(a, blk, ns) && edge_block<SINKS>(it.r0[0], it.n, blk, j.window, j.sinks)) ||
+                            (takes<SINKS>(b, blk, ns) && edge_block<SINKS>(it.r0[1], it.n, blk, j.window, j.sinks));
           if (edge) {
             uint4* tile = reinterpret_cast<uint4*>(sm.kv[slot]);
             uint32_t m[4] = {0u, 0u, 0u, 0u};  // largest magnitudes, NaN above all
@@ -471,14 +496,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
               fence_proxy_async_shared();
             }
           }
-          if (blk + 1 < je) {
+          if (after < je) {
             ok = __all_sync(0xffffffffu, role_wait(&sm.kv_full[(use + 1) % kRing], (uint32_t)((use + 1) / kRing) & 1u, failed));
             if (!ok) break;
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.v_ok[slot >> 1]);
         }
-        kv += 2 * (je - jb);
+        kv = use - 1;
         if (lane == 0) mbar_arrive(&sm.item_empty[k & 1]);
       }
     }
@@ -504,20 +529,27 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       const int R = it.r0[t], row = R + 32 * (warp & 3) + lane;
       float base = -INFINITY;  // in powers of two, as the weights take it
       uint64_t l2[2] = {0ull, 0ull};
-      for (int b = rg.jb; b < rg.je; ++b) {
+      for (int b = first_block<SINKS>(rg.jb); b < rg.je; b = block_after<SINKS>(b, rg.jb, ns)) {
         ok = __all_sync(0xffffffffu, role_wait(&sm.s_full[t], sph, failed));
         if (!ok) break;
         sph ^= 1u;
         tc_fence_after();
-        if (edge_block(R, it.n, b, j.window)) {  // the mask, over the scores in tensor memory
+        if (edge_block<SINKS>(R, it.n, b, j.window, j.sinks)) {  // the mask, over the scores in tensor memory
           const int hi = row - b * kRows, lo = j.window ? hi - j.window + 1 : 0;  // seen: lo..hi
+          const int first = SINKS ? j.sinks - b * kRows : 0;                      // and those before `first`, up to hi
 #pragma unroll 1
           for (int w = 0; w < 4; ++w) {
             uint32_t s[32];
             tmem_ld32u(ts + 32 * w, s);
             const int h = hi - 32 * w, l = lo - 32 * w;
             uint32_t m = h < 0 ? 0u : h >= 31 ? ~0u : (2u << h) - 1u;
-            if (l > 0) m = l >= 32 ? 0u : m & (~0u << l);
+            if (SINKS) {
+              const int f = first - 32 * w;
+              const uint32_t win = l <= 0 ? ~0u : l >= 32 ? 0u : ~0u << l, early = f <= 0 ? 0u : f >= 32 ? ~0u : (1u << f) - 1u;
+              m &= win | early;
+            } else if (l > 0) {
+              m = l >= 32 ? 0u : m & (~0u << l);
+            }
             tmem_wait_ld_all();
 #pragma unroll
             for (int i = 0; i < 32; ++i)
@@ -545,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           if (move) base = top;
           l2[0] = mul_f2(l2[0], f2(alpha, alpha));
           l2[1] = mul_f2(l2[1], f2(alpha, alpha));
-          if (b > rg.jb) {  // O of the first block starts anew
+          if (b > first_block<SINKS>(rg.jb)) {  // O of the first block starts anew
 #pragma unroll 1
             for (int i = 0; i < 4; ++i) {
               uint32_t o[32];
@@ -626,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           if (lane == 0) tma_stores_done();
           __syncwarp();
           __threadfence();
-          if (row < it.n) add_nonfinite<F16>(j, it, t, row);
+          if (row < it.n) add_nonfinite<F16, SINKS>(j, it, t, row);
         }
         tc_fence_before();
       }
@@ -644,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
 }
 
 std::mutex g_mu;  // guards the caches below
-bool g_attr[64][2] = {{false}};
+bool g_attr[64][4] = {{false}};
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -689,16 +721,19 @@ cudaError_t launch_prompt(const PromptJob& job, cudaStream_t stream) {
       !encode(f, &p.mv, job.f16, job.v, job.T, job.Hkv, job.vs_t, job.vs_h) ||
       !encode(f, &p.mo, job.f16, job.out, job.T, job.Hq, job.os_t, job.os_h, true))
     return cudaErrorInvalidValue;
-  const auto kern = job.f16 ? prompt_kernel<true> : prompt_kernel<false>;
+  const bool sinks = job.window > 0 && job.sinks > 0;
+  const int form = 2 * sinks + job.f16;
+  const auto kern = sinks ? (job.f16 ? prompt_kernel<true, true> : prompt_kernel<false, true>)
+                          : (job.f16 ? prompt_kernel<true, false> : prompt_kernel<false, false>);
   const size_t smem = sizeof(Smem) + 1024;
   int dev = 0;
   cudaGetDevice(&dev);
   {
     std::lock_guard<std::mutex> lock(g_mu);
-    if (dev < 0 || dev >= 64 || !g_attr[dev][job.f16]) {
+    if (dev < 0 || dev >= 64 || !g_attr[dev][form]) {
       e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
       if (e != cudaSuccess) return e;
-      if (dev >= 0 && dev < 64) g_attr[dev][job.f16] = true;
+      if (dev >= 0 && dev < 64) g_attr[dev][form] = true;
     }
   }
   // no more CTAs than items: T tokens in B sequences make at most T / 256 + B row blocks
