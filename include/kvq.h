@@ -522,6 +522,81 @@ kvq_status kvq_pages_compact(int32_t* page_refs, int num_pages, int32_t* block_t
 kvq_status kvq_pages_copy(const kvq_int4_cache* caches, int num_caches, int n, const int32_t* src,
                           const int32_t* dst, const int32_t* count, int32_t* dev_err, kvq_stream_t stream);
 
+/* ------------------------------------------------------------------ caches held to a size */
+
+/*
+ * kvq_window_attn_int4 -- kvq_decode_attn_int4 with a window and a few first tokens that stay visible: query row r of
+ *   sequence b, at position i = ctx_len[b] + r, attends to positions max(0, i-window+1)..i and to 0..min(sinks, i+1)-1
+ *   (each once, where the two meet). Pages that hold neither a first token nor one of the rows' windows are not read, and
+ *   their block-table entries may be anything: a session's pages between the two may be given back.
+ *   out:      device [B][S][num_q_heads][128] of out_dtype (KVQ_F32 or KVQ_BF16). A row that sees nothing (its pages
+ *             outside the pool) gives 0.
+ *   workspace: as for kvq_decode_attn_int4 (kvq_decode_workspace_bytes).
+ *   The products take q~ in fp16 and weights as the tree calls of few rows do: the same precision, and the same NaN rows.
+ *   Other arguments, limits and errors as kvq_decode_attn_int4.
+ * Requires window >= 1, sinks >= 0, B*(max_pages_per_seq+2) <= 2^31.
+ */
+kvq_status kvq_window_attn_int4(const kvq_int4_cache* cache, const float* Mq, const float* Mk, const void* q,
+                                kvq_dtype dtype, int B, int S, int num_q_heads, const int32_t* ctx_len, int window,
+                                int sinks, const void* k_new, const void* v_new, float sm_scale, float eps, void* out,
+                                kvq_dtype out_dtype, void* workspace, size_t workspace_bytes, int32_t* dev_err,
+                                kvq_stream_t stream);
+/* The same with the FWHT prologue (wq, wk: device float[128], 16-byte aligned; kvq_fold_qk_fwht). */
+kvq_status kvq_window_attn_int4_fwht(const kvq_int4_cache* cache, const float* wq, const float* wk, const void* q,
+                                     kvq_dtype dtype, int B, int S, int num_q_heads, const int32_t* ctx_len, int window,
+                                     int sinks, const void* k_new, const void* v_new, float sm_scale, float eps,
+                                     void* out, kvq_dtype out_dtype, void* workspace, size_t workspace_bytes,
+                                     int32_t* dev_err, kvq_stream_t stream);
+
+/*
+ * What every slot of an int4 cache of one layer has gathered, beside the cache: slot j of sequence q (position j of its
+ * block-table row) and KV head h has
+ *   mass[q][h][j]: the sum of the attention weights that the queries of that KV head's group have put on it,
+ *   ids[q][h][j]:  the number of its token in the sequence (0, 1, ...). After an eviction the slots of different heads
+ *                  hold different tokens, in no particular order.
+ * mass: device float [num_seqs][num_kv_heads][max_tokens], 16-byte aligned; ids: device int32 of the same shape.
+ * max_tokens: a multiple of 4, at least 64*max_pages_per_seq of the cache. The calls read and write only slots below a
+ * sequence's length (a mass call: the new token's too).
+ */
+typedef struct kvq_token_mass {
+  float* mass;
+  int32_t* ids;
+  int32_t num_seqs;
+  int32_t num_kv_heads;
+  int32_t max_tokens;
+} kvq_token_mass;
+
+/*
+ * kvq_mass_attn_int4 -- kvq_decode_attn_int4 for one new token per sequence, with its weights kept: with
+ *   w_g[j] the softmax weight of query head g (of KV head h) on slot j of sequence b,
+ *     mass[b][h][j] += sum_g w_g[j] for j < ctx_len[b],
+ *   and the new token's slot j = ctx_len[b] is set: mass to that sum, ids to positions[b] (the tokens that the sequence
+ *   has had before it; the same as ctx_len[b] until the first eviction).
+ *   q:        device [B][num_q_heads][128]; k_new, v_new: device [B][num_kv_heads][128] or both NULL.
+ *   positions: device int32[B].
+ *   out:      device [B][num_q_heads][128] of out_dtype (KVQ_F32 or KVQ_BF16); precision as kvq_window_attn_int4.
+ *   workspace: device, >= kvq_mass_workspace_bytes(B, num_q_heads, num_kv_heads, max_pages_per_seq), 256-byte aligned
+ *             (4 bytes for every query head and slot: the scores of the call).
+ *   Precision of the weights: q~ enters the scores in two fp16 parts (2^-22 of the value), sums are fp32, in an order that
+ *   does not depend on timing. A row that is NaN (see kvq_tree_attn_int4) adds nothing; neither do slots of a page outside
+ *   the pool.
+ *   mass and ids must not overlap one another, the inputs or out. Other arguments, limits and errors as
+ *   kvq_decode_attn_int4 with S = 1.
+ * Requires B*num_kv_heads*max_pages_per_seq <= 2^31.
+ */
+size_t kvq_mass_workspace_bytes(int B, int num_q_heads, int num_kv_heads, int max_pages_per_seq);
+kvq_status kvq_mass_attn_int4(const kvq_int4_cache* cache, const kvq_token_mass* mass, const float* Mq, const float* Mk,
+                              const void* q, kvq_dtype dtype, int B, int num_q_heads, const int32_t* ctx_len,
+                              const int32_t* positions, const void* k_new, const void* v_new, float sm_scale, float eps,
+                              void* out, kvq_dtype out_dtype, void* workspace, size_t workspace_bytes, int32_t* dev_err,
+                              kvq_stream_t stream);
+/* The same with the FWHT prologue (wq, wk: device float[128], 16-byte aligned; kvq_fold_qk_fwht). */
+kvq_status kvq_mass_attn_int4_fwht(const kvq_int4_cache* cache, const kvq_token_mass* mass, const float* wq,
+                                   const float* wk, const void* q, kvq_dtype dtype, int B, int num_q_heads,
+                                   const int32_t* ctx_len, const int32_t* positions, const void* k_new,
+                                   const void* v_new, float sm_scale, float eps, void* out, kvq_dtype out_dtype,
+                                   void* workspace, size_t workspace_bytes, int32_t* dev_err, kvq_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -47,6 +47,11 @@ class Fp8Ring(ctypes.Structure):
                 ("capacity", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
 
 
+class TokenMass(ctypes.Structure):
+    _fields_ = [("mass", ctypes.c_void_p), ("ids", ctypes.c_void_p), ("num_seqs", ctypes.c_int32),
+                ("num_kv_heads", ctypes.c_int32), ("max_tokens", ctypes.c_int32)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is not built: run `python -c 'import __graft_entry__ as g; g.build()'`")
@@ -95,6 +100,16 @@ def _load():
         getattr(L, name).restype = i32
         getattr(L, name).argtypes = [ctypes.POINTER(Int4Cache), vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, f32,
                                      f32, vp, i32, vp, sz, vp, vp]
+    for name in ("kvq_window_attn_int4", "kvq_window_attn_int4_fwht"):
+        getattr(L, name).restype = i32
+        getattr(L, name).argtypes = [ctypes.POINTER(Int4Cache), vp, vp, vp, i32, i32, i32, i32, vp, i32, i32, vp, vp, f32,
+                                     f32, vp, i32, vp, sz, vp, vp]
+    L.kvq_mass_workspace_bytes.restype = sz
+    L.kvq_mass_workspace_bytes.argtypes = [i32, i32, i32, i32]
+    for name in ("kvq_mass_attn_int4", "kvq_mass_attn_int4_fwht"):
+        getattr(L, name).restype = i32
+        getattr(L, name).argtypes = [ctypes.POINTER(Int4Cache), ctypes.POINTER(TokenMass), vp, vp, vp, i32, i32, i32, vp, vp,
+                                     vp, vp, f32, f32, vp, i32, vp, sz, vp, vp]
     L.kvq_tree_attn_fp8_swa.restype = i32
     L.kvq_tree_attn_fp8_swa.argtypes = [ctypes.POINTER(Fp8Ring), vp, i32, i32, i32, i32, vp, vp, i32, vp, vp, f32,
                                         f32, f32, vp, i32, vp, sz, vp, vp]
@@ -569,3 +584,89 @@ def kvq_pages_copy(caches, src, dst, dev_err, count=None, stream=None):
                                 _here(dev, stream))
     if status:
         raise KvqError("kvq_pages_copy", status)
+
+
+# ---------------------------------------------------------------- caches held to a size
+
+def token_mass(mass, ids) -> TokenMass:
+    """Descriptor over caller-owned device tensors: mass float32 and ids int32, both [num_seqs, num_kv_heads, max_tokens]."""
+    torch = _torch()
+    dev = _dev(mass, "mass")
+    num_seqs, num_kv_heads, max_tokens = mass.shape
+    return TokenMass(_is(mass, torch.float32, mass.shape, "mass", dev), _is(ids, torch.int32, mass.shape, "ids", dev), num_seqs,
+                     num_kv_heads, max_tokens)
+
+
+def alloc_token_mass(num_seqs: int, num_kv_heads: int, max_pages_per_seq: int, device="cuda"):
+    """Device tensors for what every slot of a layer's int4 cache has gathered (no mass, tokens in order), and their
+    descriptor."""
+    torch = _torch()
+    n = max_pages_per_seq * PAGE_SIZE
+    mass = torch.zeros((num_seqs, num_kv_heads, n), dtype=torch.float32, device=device)
+    ids = torch.arange(n, dtype=torch.int32, device=device).repeat(num_seqs, num_kv_heads, 1)
+    return {"mass": mass, "ids": ids}, token_mass(mass, ids)
+
+
+def _attn_args(q, ctx_len, out, k_new, v_new, Hkv, shape, new_shape):
+    """(device, dtype code, addresses of ctx_len, k_new, v_new, out's dtype code) of a call whose q and out have `shape`."""
+    torch = _torch()
+    if not (q.dtype is torch.bfloat16 or q.dtype is torch.float32) or q.shape[-1] != HEAD_DIM or not (q.is_cuda and q.is_contiguous()):
+        raise ValueError(f"q must be a contiguous device tensor of fp32 or bf16 with rows of 128, got {q.dtype} {tuple(q.shape)}")
+    if not (out.dtype is torch.bfloat16 or out.dtype is torch.float32):
+        raise ValueError(f"out must be fp32 or bf16, got {out.dtype}")
+    dev = q.get_device()
+    _is(out, out.dtype, shape, "out", dev)
+    kn = None if k_new is None else _is(k_new, q.dtype, new_shape, "k_new", dev)
+    vn = None if v_new is None else _is(v_new, q.dtype, new_shape, "v_new", dev)
+    return (dev, BF16 if q.dtype is torch.bfloat16 else F32, _is(ctx_len, torch.int32, (shape[0],), "ctx_len", dev), kn, vn,
+            BF16 if out.dtype is torch.bfloat16 else F32)
+
+
+def _folds(Mq, Mk, fwht, dev):
+    fold = (HEAD_DIM,) if fwht else (HEAD_DIM, HEAD_DIM)
+    return _is(Mq, _th.float32, fold, "Mq", dev), None if Mk is None else _is(Mk, _th.float32, fold, "Mk", dev)
+
+
+def kvq_window_attn_int4(cache: Int4Cache, Mq, Mk, q, ctx_len, window: int, sinks: int, out, workspace, dev_err, k_new=None,
+                         v_new=None, sm_scale: float = HEAD_DIM ** -0.5, eps: float = 1e-6, stream=None,
+                         fwht: bool = False):
+    """kvq_decode_attn_int4 in which each row sees the last `window` positions and the first `sinks`: q [B, S, Hq, 128]
+    (fp32 or bf16), out of the same shape (fp32 or bf16), workspace as there."""
+    B, S, Hq, D = q.shape
+    dev, dt, ctx, kn, vn, odt = _attn_args(q, ctx_len, out, k_new, v_new, cache.num_kv_heads, q.shape,
+                                           (B, S, cache.num_kv_heads, D))
+    fn = lib.kvq_window_attn_int4_fwht if fwht else lib.kvq_window_attn_int4
+    status = fn(ctypes.byref(cache), *_folds(Mq, Mk, fwht, dev), q.data_ptr(), dt, B, S, Hq, ctx, window, sinks, kn, vn,
+                sm_scale, eps, out.data_ptr(), odt, workspace.data_ptr(), _bytes(workspace, dev), _err(dev_err, dev),
+                _here(dev, stream))
+    if status:
+        raise KvqError("kvq_window_attn_int4_fwht" if fwht else "kvq_window_attn_int4", status)
+
+
+def kvq_mass_workspace_bytes(B: int, num_q_heads: int, num_kv_heads: int, max_pages_per_seq: int) -> int:
+    return int(lib.kvq_mass_workspace_bytes(B, num_q_heads, num_kv_heads, max_pages_per_seq))
+
+
+def alloc_mass_workspace(B: int, num_q_heads: int, num_kv_heads: int, max_tokens: int, device="cuda"):
+    """max_tokens: of the cache's block table, 64 * max_pages_per_seq."""
+    n = kvq_mass_workspace_bytes(B, num_q_heads, num_kv_heads, -(-max_tokens // PAGE_SIZE))
+    if n == 0:
+        raise KvqError("kvq_mass_workspace_bytes", 2)
+    torch = _torch()
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def kvq_mass_attn_int4(cache: Int4Cache, mass: TokenMass, Mq, Mk, q, ctx_len, positions, out, workspace, dev_err,
+                       k_new=None, v_new=None, sm_scale: float = HEAD_DIM ** -0.5, eps: float = 1e-6, stream=None,
+                       fwht: bool = False):
+    """kvq_decode_attn_int4 for one new token per sequence, its weights added to `mass`: q, out [B, Hq, 128] or
+    [B, 1, Hq, 128], k_new, v_new [B, Hkv, 128] or [B, 1, Hkv, 128]; positions int32[B]: the new tokens' numbers."""
+    B, Hq, Hkv = q.shape[0], q.shape[-2], cache.num_kv_heads
+    _need(q.dim() == 3 or q.dim() == 4 and q.shape[1] == 1, "q must be [B, Hq, 128] or [B, 1, Hq, 128]")
+    dev, dt, ctx, kn, vn, odt = _attn_args(q, ctx_len, out, k_new, v_new, Hkv, q.shape, (*q.shape[:-2], Hkv, HEAD_DIM))
+    fn = lib.kvq_mass_attn_int4_fwht if fwht else lib.kvq_mass_attn_int4
+    status = fn(ctypes.byref(cache), ctypes.byref(mass), *_folds(Mq, Mk, fwht, dev), q.data_ptr(), dt, B, Hq, ctx,
+                _is(positions, _th.int32, (B,), "positions", dev), kn, vn, sm_scale, eps, out.data_ptr(), odt,
+                workspace.data_ptr(), _bytes(workspace, dev), _err(dev_err, dev), _here(dev, stream))
+    if status:
+        raise KvqError("kvq_mass_attn_int4_fwht" if fwht else "kvq_mass_attn_int4", status)

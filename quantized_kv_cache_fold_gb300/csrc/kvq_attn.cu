@@ -27,6 +27,15 @@
 //        small), B = 16 tokens x 8 rows of p*s_V in f16 (movmatrix transposes the QK
 //        accumulator), plus sum_j p_j (o_V + 7.5 s_V) added per row; the partial undoes
 //        2^(k - 23) per dim.
+//
+// Two more forms of the int4 kernel serve caches that are held to a size (kvq_window_attn_int4, kvq_mass_attn_int4):
+//   window  the segment's pages are those that hold the first `sinks` tokens and those of the rows' windows; the pages
+//           between are neither read nor counted in the split.
+//   mass    one row per query head. Its weights are added to what every cached token has gathered, so scores are wanted
+//           to fp32: q~ enters as two fp16 parts (22 bits), a second chain of products over the same codes. The scores go
+//           to the workspace, [segment][row][position]; when the join knows a row's sum, mass_kernel turns them into
+//           weights. (Reading the keys a second time instead would move 68 bytes a token and head, scores 40 at 5 rows.)
+// (64 sequences of 5,000-16,384 tokens: window 4,096 with 64 first tokens 44 us; mass 97 us, of which the floor is 21 and 47.)
 
 #include <algorithm>
 #include <cmath>
@@ -102,7 +111,15 @@ struct AttnParams {
   float* out;
   // TREE: bit j of word [b][r]: query row r of sequence b attends to the row at position ctx[b] + j
   const uint64_t* tree_mask;
-  int out_bf16;  // TREE: out holds bf16
+  int out_bf16;  // forms other than the verify block: out holds bf16
+  int sinks;     // window form: first tokens that stay visible
+  // mass form
+  float* scores;     // [B * Hkv][R][max_pages * 64], in powers of two
+  float2* stats;     // [B * Hkv][R]: base and sum of the weights against it
+  float* mass;       // [.][Hkv][mass_len]
+  int32_t* ids;
+  int mass_len;
+  const int32_t* positions;
   int32_t* dev_err;
   int ntg, nkg, nstages, rows_pad;
   int n_cta;
@@ -110,6 +127,10 @@ struct AttnParams {
   // copy, the producer on a stage's release); the drain of copies in flight keeps kWaitLimitNs
   unsigned long long stage_wait_ns;
 };
+
+// What the int4 kernels attend to: a verify block (and the fp8 ring), a tree of drafted tokens, a window with first tokens,
+// or one row whose weights are kept. All but the first share the tree's treatment of weights and outputs (TREE below).
+constexpr int kVerify = 0, kTree = 1, kWindow = 2, kMass = 3;
 
 __host__ __device__ __forceinline__ size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
@@ -152,12 +173,29 @@ __device__ __forceinline__ int eff_ctx(const AttnParams& p, int b, bool& bad, in
   return c;
 }
 
+// Window form: the pages of a sequence, those of the first tokens (`first` of them) and those of its rows' windows (from
+// page `start`), counted through.
+struct WindowPages {
+  int first, start;
+  __device__ __forceinline__ WindowPages(const AttnParams& p, int ctxb) {
+    start = max(0, ctxb - p.window + 1) / kPage;  // row 0 looks back farthest
+    first = min((p.sinks + kPage - 1) / kPage, start);
+  }
+  __device__ __forceinline__ int page(int lp) const { return lp < first ? lp : lp - first + start; }
+};
+
+template <int FORM>
 __device__ __forceinline__ int seg_pages(const AttnParams& p, int ctxb, int fmt) {
+  if (FORM == kWindow) {
+    const WindowPages w(p, ctxb);
+    return w.first + (ctxb + p.S + kPage - 1) / kPage - w.start;
+  }
   return fmt == 0 ? (ctxb + p.S + kPage - 1) / kPage : p.cap / kPage;
 }
 
 // Warp 0 builds pre[b] = sum_{b' < b} np_b' (pre[B] = total pages per KV head) and
 // flags[1] = any clamped context. Other warps return at once.
+template <int FORM>
 __device__ void build_prefix(const AttnParams& p, int fmt, int* pre, volatile int* flags) {
   if (threadIdx.x >= 32) return;
   const int lane = threadIdx.x;
@@ -175,7 +213,7 @@ __device__ void build_prefix(const AttnParams& p, int fmt, int* pre, volatile in
   for (int base = 0; base < p.B; base += 32) {
     const int b = base + lane;
     int np = 0;
-    if (b < p.B) np = seg_pages(p, eff_ctx(p, b, bad, fmt), fmt);
+    if (b < p.B) np = seg_pages<FORM>(p, eff_ctx(p, b, bad, fmt), fmt);
     int incl = np;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -235,13 +273,17 @@ __device__ __forceinline__ bool tree_sees(const AttnParams& p, int b, int r, int
 // of two) and added last, so that a row of one key has an exact P, and code and offset terms cancel as they should.
 constexpr float kTreeLimit = 15.0f, kTreeBelow = 7.0f;
 
+// Mass form: the second part of q~ is multiplied by this, so that fp16 holds it to 11 more bits wherever it holds the first
+// (left as it is it would be subnormal for elements below 1/4), and the sums by its inverse.
+constexpr float kLowScale = 2048.0f;
+
 // Exponent e of s < 2^e for a scale (s >= 0), at least -13 (fp16's smallest normal scale): bounds P by 2^28.
 __device__ __forceinline__ float scale_exponent(float s) { return (float)max((int)(__float_as_uint(s) >> 23) - 126, -13); }
 
 // TREE: that distance, of a row's largest score s and largest score + exponent t (both of the same tokens).
 __device__ __forceinline__ float tree_raise(float s, float t) { return kTreeBelow - ceilf(t - s); }
 
-// Stores n output values; TREE: of the type asked for, and 0 for rows that saw nothing.
+// Stores n output values; TREE (any form but the verify block): of the type asked for, and 0 for rows that saw nothing.
 template <bool TREE>
 __device__ __forceinline__ void store2(const AttnParams& p, size_t at, float x, float y, float lsum) {
   if (TREE) {
@@ -274,7 +316,7 @@ __device__ __forceinline__ int out_dim(int mt, int row) {
 // phase per round), signalling `full`. A page whose block-table entry is out of range is
 // flagged and delivered as invalid (valid[s] = 0, no copy). Waits for its own copies before
 // returning.
-template <int FMT>
+template <int FMT, int FORM>
 __device__ __forceinline__ void produce_pages(const AttnParams& p, const int* pre, uint8_t* stages, uint64_t* full,
                                               uint64_t* empty, volatile int* valid, volatile int* flags, int nst,
                                               long long p0, long long p1, int lane) {
@@ -290,6 +332,10 @@ __device__ __forceinline__ void produce_pages(const AttnParams& p, const int* pr
       int b, h, lp, np;
       decode_page(pre, p.B, p.Hkv, p0 + mine, b, h, lp, np);
       if (FMT == 0) {
+        if (FORM == kWindow) {
+          bool bad = false;
+          lp = WindowPages(p, eff_ctx(p, b, bad, FMT)).page(lp);
+        }
         const int phys = p.block_table[(size_t)b * p.max_pages + lp];
         if (phys >= 0 && phys < p.num_pages)
           src = ((long long)phys * p.Hkv + h) * kStage4;
@@ -338,12 +384,13 @@ __device__ __forceinline__ void produce_pages(const AttnParams& p, const int* pr
 
 // Register caps: the int4 single-tile CTA (5 warps) must fit twice per SM, i.e. 3 warps per
 // SM sub-partition -> at most 170 registers.
-template <int FMT, int NT, bool TREE>
+template <int FMT, int NT, int FORM>
 __global__ void __maxnreg__(NT == 1 ? (FMT == 0 ? KVQ_INT4_MAXREG : 184) : 255)
     attn_kernel(const AttnParams p) {
+  constexpr bool TREE = FORM != kVerify;
   extern __shared__ __align__(128) uint8_t smem[];
   constexpr int kStage = FMT == 0 ? kStage4 : kStage8;
-  constexpr int MTU = NT == 1 ? 4 : 2;  // 16-token m-tiles per online-softmax update
+  constexpr int MTU = NT == 1 && FORM != kMass ? 4 : 2;  // 16-token m-tiles per online-softmax update
   const SmemLayout L(FMT, p.nstages, p.B, p.nkg, p.rows_pad);
   uint8_t* stages = smem + L.stages;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L.full);
@@ -362,7 +409,7 @@ __global__ void __maxnreg__(NT == 1 ? (FMT == 0 ? KVQ_INT4_MAXREG : 184) : 255)
   // page prefix): no kernel of the call writes them, and the grids before the previous one
   // completed before this grid could launch. Everything after the setup waits for the previous
   // grid.
-  build_prefix(p, FMT, pre, flags);
+  build_prefix<FORM>(p, FMT, pre, flags);
   if (threadIdx.x < nst) {
     mbar_init(&full[threadIdx.x], 1);
     mbar_init(&empty[threadIdx.x], p.ntg);
@@ -381,7 +428,7 @@ __global__ void __maxnreg__(NT == 1 ? (FMT == 0 ? KVQ_INT4_MAXREG : 184) : 255)
 
   // ------------------------------------------------------------ producer warp
   if (warp == nwc) {
-    produce_pages<FMT>(p, pre, stages, full, empty, valid, flags, nst, p0, p1, lane);
+    produce_pages<FMT, FORM>(p, pre, stages, full, empty, valid, flags, nst, p0, p1, lane);
     return;
   }
 
@@ -402,6 +449,7 @@ __global__ void __maxnreg__(NT == 1 ? (FMT == 0 ? KVQ_INT4_MAXREG : 184) : 255)
 
     // ---- segment setup: query fragments and per-row limits
     uint32_t qf[NT][8][2];
+    uint32_t ql[FORM == kMass ? NT : 1][8][2];  // what fp16 leaves of q~
     float qs[NT][2];
     int lim_lo[NT][2], lim_hi[NT][2];
 #pragma unroll
@@ -457,6 +505,12 @@ __global__ void __maxnreg__(NT == 1 ? (FMT == 0 ? KVQ_INT4_MAXREG : 184) : 255)
             const int d0 = 8 * wi + 2 * e;
             qf[nt][2 * wi + e][0] = pack_f16x2(qv[d0], qv[d0 + 4]);
             qf[nt][2 * wi + e][1] = pack_f16x2(qv[d0 + 1] * 0.0625f, qv[d0 + 5] * 0.0625f);
+            if (FORM == kMass) {  // the remainder of what the second pair holds too, which is rounded after the division
+              const uint32_t a = qf[nt][2 * wi + e][0], c = qf[nt][2 * wi + e][1];
+              ql[nt][2 * wi + e][0] = pack_f16x2((qv[d0] - h2f_lo(a)) * kLowScale, (qv[d0 + 4] - h2f_hi(a)) * kLowScale);
+              ql[nt][2 * wi + e][1] = pack_f16x2(fmaf(qv[d0 + 1], 0.0625f, -h2f_lo(c)) * kLowScale,
+                                                 fmaf(qv[d0 + 5], 0.0625f, -h2f_hi(c)) * kLowScale);
+            }
           }
       } else {
 #pragma unroll
@@ -476,7 +530,7 @@ __global__ void __maxnreg__(NT == 1 ? (FMT == 0 ? KVQ_INT4_MAXREG : 184) : 255)
         const int r = nC < R ? nC / G : 0;
         const int hi = ctxb + r;  // last visible position
         lim_hi[nt][j] = hi;
-        lim_lo[nt][j] = FMT == 0 ? 0 : max(0, hi - p.window + 1);
+        lim_lo[nt][j] = FMT == 0 && FORM != kWindow ? 0 : max(0, hi - p.window + 1);
       }
     }
 
@@ -500,6 +554,19 @@ __global__ void __maxnreg__(NT == 1 ? (FMT == 0 ? KVQ_INT4_MAXREG : 184) : 255)
         for (int c = 0; c < 4; ++c) acc[nt][i][c] = 0.0f;
     }
 
+    const WindowPages view(p, FORM == kWindow ? ctxb : 0);
+    // mass form: where the scores of this thread's rows go (rows behind R: nowhere)
+    float* srow[NT][2];
+    if (FORM == kMass) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int row = 8 * (tg * NT + nt) + 2 * t + j;
+          srow[nt][j] = row < R ? p.scores + ((size_t)seg * R + row) * ((size_t)p.max_pages * kPage) : nullptr;
+        }
+    }
+
     // fp8 ring: the newest position written and its slot
     const int p_last = ctxb + p.S - 1;
     const int slot_last = FMT == 1 ? p_last % p.cap : 0;
@@ -515,10 +582,11 @@ __global__ void __maxnreg__(NT == 1 ? (FMT == 0 ? KVQ_INT4_MAXREG : 184) : 255)
         flags[0] = 1;
       }
       if (__any_sync(0xffffffffu, flags[0] != 0)) break;
-      const int lp = lp0 + (int)(pg - seg_start);
+      const int lp = FORM == kWindow ? view.page(lp0 + (int)(pg - seg_start)) : lp0 + (int)(pg - seg_start);
       if (valid[s]) {
         const uint8_t* st = stages + (size_t)s * kStage;
-        const bool need_mask = FMT == 1 || (lp + 1) * kPage > ctxb + (TREE ? 0 : 1);
+        const bool need_mask = FMT == 1 || (lp + 1) * kPage > ctxb + (FORM == kTree ? 0 : 1) ||
+                               (FORM == kWindow && lp * kPage < ctxb + p.S - p.window && (lp + 1) * kPage > p.sinks);
 
 #pragma unroll
         for (int mt0 = 0; mt0 < 4; mt0 += MTU) {
@@ -538,6 +606,12 @@ __global__ void __maxnreg__(NT == 1 ? (FMT == 0 ? KVQ_INT4_MAXREG : 184) : 255)
                 kb[u][hh] = ok_;
                 va[u][hh] = sv;
                 vb[u][hh] = fmaf(7.5f, sv, ovv);
+                // a slot that no row sees (unwritten, or between first tokens and window) may hold anything: its weight is 0,
+                // so its value is too
+                if ((FORM == kWindow || FORM == kMass) && need_mask) {
+                  const int pos = lp * kPage + tok;
+                  if (pos >= ctxb + p.S || (FORM == kWindow && pos <= ctxb - p.window && pos >= p.sinks)) va[u][hh] = vb[u][hh] = 0.0f;
+                }
               }
           }
 
@@ -563,13 +637,16 @@ __global__ void __maxnreg__(NT == 1 ? (FMT == 0 ? KVQ_INT4_MAXREG : 184) : 255)
               Bw[u][2] = wb.z;
               Bw[u][3] = wb.w;
             }
-            float d[NT][MTU][4];
+            float d[NT][MTU][4], dl[FORM == kMass ? NT : 1][MTU][4];  // dl: of the second part of q~
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int u = 0; u < MTU; ++u)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) d[nt][u][c] = 0.0f;
+                for (int c = 0; c < 4; ++c) {
+                  d[nt][u][c] = 0.0f;
+                  if (FORM == kMass) dl[nt][u][c] = 0.0f;
+                }
 #pragma unroll
             for (int wi = 0; wi < 4; ++wi) {
               uint32_t ha[MTU][4], hb[MTU][4];
@@ -583,9 +660,21 @@ __global__ void __maxnreg__(NT == 1 ? (FMT == 0 ? KVQ_INT4_MAXREG : 184) : 255)
 #pragma unroll
                 for (int u = 0; u < MTU; ++u)
 #pragma unroll
-                  for (int nt = 0; nt < NT; ++nt)
+                  for (int nt = 0; nt < NT; ++nt) {
                     mma_16816(d[nt][u], ha[u][2 * e], hb[u][2 * e], ha[u][2 * e + 1], hb[u][2 * e + 1],
                               qf[nt][2 * wi + e][0], qf[nt][2 * wi + e][1]);
+                    if (FORM == kMass)
+                      mma_16816(dl[nt][u], ha[u][2 * e], hb[u][2 * e], ha[u][2 * e + 1], hb[u][2 * e + 1],
+                                ql[nt][2 * wi + e][0], ql[nt][2 * wi + e][1]);
+                  }
+            }
+            if (FORM == kMass) {
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int u = 0; u < MTU; ++u)
+#pragma unroll
+                  for (int c = 0; c < 4; ++c) d[nt][u][c] = fmaf(dl[nt][u][c], 1.0f / kLowScale, d[nt][u][c]);
             }
 #pragma unroll
             for (int u = 0; u < MTU; ++u)
@@ -644,9 +733,22 @@ __global__ void __maxnreg__(NT == 1 ? (FMT == 0 ? KVQ_INT4_MAXREG : 184) : 255)
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                   for (int j = 0; j < 2; ++j)
-                    if (TREE ? !tree_sees(p, b, lim_hi[nt][j] - ctxb, ctxb, pos) : (pos < lim_lo[nt][j] || pos > lim_hi[nt][j]))
+                    if (FORM == kTree ? !tree_sees(p, b, lim_hi[nt][j] - ctxb, ctxb, pos)
+                                      : ((pos < lim_lo[nt][j] && !(FORM == kWindow && pos < p.sinks)) || pos > lim_hi[nt][j]))
                       sc[nt][u][2 * hh + j] = -INFINITY;
               }
+          }
+          if (FORM == kMass) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+                if (srow[nt][j])
+#pragma unroll
+                  for (int u = 0; u < MTU; ++u)
+#pragma unroll
+                    for (int hh = 0; hh < 2; ++hh)
+                      srow[nt][j][(size_t)lp * kPage + 16 * (mt0 + u) + g + 8 * hh] = sc[nt][u][2 * hh + j] + muse[nt][j];
           }
 
           // ---- online softmax update
@@ -1045,7 +1147,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
   // The setup (page prefix from the context lengths, barriers, Q' padding, tensor memory) runs
   // while the previous grid, the call's prologue/append kernel, finishes; see attn_kernel. Every
   // grid before it has completed, so no earlier kernel of the stream still holds tensor memory.
-  build_prefix(p, 0, pre, flags);
+  build_prefix<kVerify>(p, 0, pre, flags);
   if (threadIdx.x == 0) {
     for (int s = 0; s < kTcStages; ++s) {
       mbar_init(&full[s], 1);
@@ -1094,7 +1196,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
 
   // ------------------------------------------------------------ producer
   if (warp == 12) {
-    if (active) produce_pages<0>(p, pre, stages, full, empty, valid, flags, kTcStages, p0, p1, lane);
+    if (active) produce_pages<0, kVerify>(p, pre, stages, full, empty, valid, flags, kTcStages, p0, p1, lane);
     return;
   }
 
@@ -1659,11 +1761,12 @@ constexpr int kCombWarps = 8;
 constexpr int kCombChunkWarp = 4;
 constexpr int kCombChunkBlock = 8;
 
-template <int FMT, bool TREE>
+template <int FMT, int FORM>
 __global__ void __launch_bounds__(kCombWarps * 32, 4) combine_rows_kernel(const AttnParams p) {
+  constexpr bool TREE = FORM != kVerify;
   extern __shared__ __align__(16) int cpre[];
   volatile int* flags = cpre + p.B + 1;
-  build_prefix(p, FMT, cpre, flags);
+  build_prefix<FORM>(p, FMT, cpre, flags);
   griddep_wait();
   griddep_launch_dependents();
   __syncthreads();
@@ -1738,14 +1841,16 @@ __global__ void __launch_bounds__(kCombWarps * 32, 4) combine_rows_kernel(const 
     const size_t at = (((size_t)b * p.S + r) * p.Hq + h * p.G + gi) * kD + 2 * lane;
     store2<TREE>(p, at, alo.x, alo.y, lsum);
     store2<TREE>(p, at + 64, ahi.x, ahi.y, lsum);
+    if (FORM == kMass && lane == 0) p.stats[item] = make_float2(M, lsum);
   }
 }
 
-template <int FMT, bool TREE>
+template <int FMT, int FORM>
 __global__ void __launch_bounds__(128, 4) combine_kernel(const AttnParams p) {
+  constexpr bool TREE = FORM != kVerify;
   extern __shared__ __align__(16) int cpre[];
   volatile int* flags = cpre + p.B + 1;
-  build_prefix(p, FMT, cpre, flags);
+  build_prefix<FORM>(p, FMT, cpre, flags);
   griddep_wait();
   griddep_launch_dependents();
   __syncthreads();
@@ -1807,6 +1912,7 @@ __global__ void __launch_bounds__(128, 4) combine_kernel(const AttnParams p) {
     }
     const int r = row / p.G, gi = row - (row / p.G) * p.G;
     const size_t at = (((size_t)b * p.S + r) * p.Hq + h * p.G + gi) * kD + d;
+    if (FORM == kMass && d == 0) p.stats[item] = make_float2(M, lsum);
     if (TREE) {
       const float x = lsum == 0.0f ? 0.0f : a / lsum;  // a row that saw nothing: 0
       if (p.out_bf16) reinterpret_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(x);
@@ -1817,37 +1923,90 @@ __global__ void __launch_bounds__(128, 4) combine_kernel(const AttnParams p) {
   }
 }
 
+// Mass form, after the join: the row's scores become weights w = 2^(score - base) / sum, and their sum over the rows of a KV
+// head is added to what the token has gathered; the new token's place is set, with its number. Four tokens a thread, rows in
+// ascending order, so a token's sum does not depend on timing. A row without weights (nothing visible, or a query that is
+// not finite) adds nothing: one bad step may not make the whole cache's history NaN. Tokens of a page outside the pool have
+// no scores and are passed over. Bound by memory: 4 bytes a row and 8 a token.
+constexpr int kMassThreads = 256;
+constexpr int kMassTokens = 4 * kMassThreads;
+
+__global__ void __launch_bounds__(kMassThreads) mass_kernel(const AttnParams p) {
+  const int chunks = (p.max_pages * kPage + kMassTokens - 1) / kMassTokens;  // of a segment
+  const int seg = blockIdx.x / chunks, b = seg / p.Hkv;
+  const int R = p.R;
+  bool bad = false;
+  const int ctxb = eff_ctx(p, b, bad, 0);
+  const int pos = (blockIdx.x - seg * chunks) * kMassTokens + 4 * threadIdx.x;
+  griddep_wait();
+  griddep_launch_dependents();
+  if (pos > ctxb) return;
+  const int phys = p.block_table[(size_t)b * p.max_pages + pos / kPage];
+  if (phys < 0 || phys >= p.num_pages) return;
+  const size_t row_len = (size_t)p.max_pages * kPage;
+  const float* src = p.scores + (size_t)seg * R * row_len + pos;
+  float w[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int r = 0; r < R; ++r) {
+    const float2 st = p.stats[(size_t)seg * R + r];
+    if (!(st.y > 0.0f && st.y < INFINITY)) continue;  // (uniform over the block)
+    const float4 x = *reinterpret_cast<const float4*>(src + r * row_len);
+    const float inv = 1.0f / st.y;
+    w[0] = fmaf(fast_exp2(x.x - st.x), inv, w[0]);
+    w[1] = fmaf(fast_exp2(x.y - st.x), inv, w[1]);
+    w[2] = fmaf(fast_exp2(x.z - st.x), inv, w[2]);
+    w[3] = fmaf(fast_exp2(x.w - st.x), inv, w[3]);
+  }
+  float* const m = p.mass + (size_t)seg * p.mass_len + pos;
+  if (pos + 3 < ctxb) {
+    float4 old = *reinterpret_cast<const float4*>(m);
+    old.x += w[0];
+    old.y += w[1];
+    old.z += w[2];
+    old.w += w[3];
+    *reinterpret_cast<float4*>(m) = old;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (pos + i < ctxb) m[i] += w[i];
+      if (pos + i == ctxb) {
+        m[i] = w[i];
+        p.ids[(size_t)seg * p.mass_len + pos + i] = p.positions[b];
+      }
+    }
+  }
+}
+
 // Combine launch: a block per item while the items fit in one wave of 4 blocks per SM, else a
 // warp per item over at most one wave.
-template <int FMT, bool TREE>
+template <int FMT, int FORM>
 cudaError_t launch_combine(cudaLaunchConfig_t& cfg, const AttnParams& p, int sm) {
   const long long items = (long long)p.B * p.Hkv * p.R;
   cfg.dynamicSmemBytes = (p.B + 1 + 4) * sizeof(int);
   if (items <= 4LL * sm) {
     cfg.gridDim = dim3((unsigned)std::max<long long>(1, items), 1, 1);
     cfg.blockDim = dim3(128, 1, 1);
-    return cudaLaunchKernelEx(&cfg, combine_kernel<FMT, TREE>, p);
+    return cudaLaunchKernelEx(&cfg, combine_kernel<FMT, FORM>, p);
   }
   cfg.gridDim = dim3((unsigned)std::min<long long>((items + kCombWarps - 1) / kCombWarps, 4LL * sm), 1, 1);
   cfg.blockDim = dim3(kCombWarps * 32, 1, 1);
-  return cudaLaunchKernelEx(&cfg, combine_rows_kernel<FMT, TREE>, p);
+  return cudaLaunchKernelEx(&cfg, combine_rows_kernel<FMT, FORM>, p);
 }
 
 struct DevCache {
   int sm = 0;
-  // by form: int4, fp8 ring, int4 tree
-  bool attr[3][4] = {{false}};
+  // by form: int4, fp8 ring, int4 tree, window, mass
+  bool attr[5][4] = {{false}};
   bool tc_attr[2][4] = {{false}};  // attn_tc_kernel<24 / 32 / 40 / 48>, verify block and tree: shared-memory attribute set
-  size_t occ_smem[3][4] = {{0}};  // occupancy cache: last (smem, threads) queried per instantiation
-  int occ_threads[3][4] = {{0}};
-  int occ[3][4] = {{0}};
+  size_t occ_smem[5][4] = {{0}};  // occupancy cache: last (smem, threads) queried per instantiation
+  int occ_threads[5][4] = {{0}};
+  int occ[5][4] = {{0}};
 };
 DevCache g_dev[64];
 std::mutex g_dev_mu;  // guards g_dev (launch-configuration caches shared by host threads)
 
-template <int FMT, int NT, bool TREE>
+template <int FMT, int NT, int FORM>
 cudaError_t launch_attn_t(AttnParams& p, size_t smem, int threads, long long p_max, cudaStream_t stream) {
-  constexpr int F = TREE ? 2 : FMT;
+  constexpr int F = FORM == kVerify ? FMT : 1 + FORM;
   int dev = 0;
   cudaGetDevice(&dev);
   cudaError_t e = cudaSuccess;
@@ -1861,13 +2020,13 @@ cudaError_t launch_attn_t(AttnParams& p, size_t smem, int threads, long long p_m
       dc.sm = n > 0 ? n : 1;
     }
     if (!dc.attr[F][NT]) {
-      e = cudaFuncSetAttribute(attn_kernel<FMT, NT, TREE>, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024);
+      e = cudaFuncSetAttribute(attn_kernel<FMT, NT, FORM>, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024);
       if (e != cudaSuccess) return e;
       dc.attr[F][NT] = true;
     }
     if (dc.occ_smem[F][NT] != smem || dc.occ_threads[F][NT] != threads) {
       int o = 0;
-      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&o, attn_kernel<FMT, NT, TREE>, threads, smem);
+      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&o, attn_kernel<FMT, NT, FORM>, threads, smem);
       if (e != cudaSuccess) return e;
       dc.occ[F][NT] = std::max(o, 1);
       dc.occ_smem[F][NT] = smem;
@@ -1891,9 +2050,14 @@ cudaError_t launch_attn_t(AttnParams& p, size_t smem, int threads, long long p_m
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, attn_kernel<FMT, NT, TREE>, p);
+  e = cudaLaunchKernelEx(&cfg, attn_kernel<FMT, NT, FORM>, p);
   if (e != cudaSuccess) return e;
-  return launch_combine<FMT, TREE>(cfg, p, sm);
+  e = launch_combine<FMT, FORM>(cfg, p, sm);
+  if (FORM != kMass || e != cudaSuccess) return e;
+  cfg.gridDim = dim3((unsigned)((p.max_pages * kPage + kMassTokens - 1) / kMassTokens * p.B * p.Hkv), 1, 1);
+  cfg.blockDim = dim3(kMassThreads, 1, 1);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, mass_kernel, p);
 }
 
 // int4 with more than 8 query rows per KV head: the tcgen05 kernel (NR = rows rounded up to 8),
@@ -1940,7 +2104,59 @@ cudaError_t launch_tc_t(AttnParams& p, long long p_max, cudaStream_t stream) {
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, attn_tc_kernel<NR, TREE>, p);
   if (e != cudaSuccess) return e;
-  return launch_combine<0, TREE>(cfg, p, sm);
+  return launch_combine<0, TREE ? kTree : kVerify>(cfg, p, sm);
+}
+
+// NT tiles a warp, ntg tile groups, nkg token groups, nst stages (a multiple of nkg, see the static_assert above).
+void shape(AttnParams& p, int NT, int ntg, int nkg, int nst, size_t& smem, int& threads) {
+  p.ntg = ntg;
+  p.nkg = nkg;
+  p.nstages = nst;
+  p.rows_pad = ntg * NT * 8;
+  threads = (ntg * nkg + 1) * 32;
+  smem = SmemLayout(0, nst, p.B, nkg, p.rows_pad).total;
+}
+
+// The window form keeps to the split kernel for every row count: its segments are short, so the tcgen05 kernel's longer
+// start and end would count.
+cudaError_t launch_window(AttnParams& p, const AttnJob& job, cudaStream_t stream) {
+  p.window = job.window;
+  p.sinks = job.sinks;
+  const long long pages = std::min<long long>(p.max_pages, ((long long)job.sinks + kPage - 1) / kPage +
+                                                               ((long long)job.window + p.S - 2) / kPage + 2);
+  const long long p_max = (long long)p.Hkv * p.B * pages;
+  const int ntiles = (p.R + 7) / 8;
+  size_t smem;
+  int threads;
+  if (ntiles == 1) {
+    shape(p, 1, 1, KVQ_TOKEN_GROUPS, KVQ_STAGES_INT4, smem, threads);
+    return launch_attn_t<0, 1, kWindow>(p, smem, threads, p_max, stream);
+  }
+  const int NT = ntiles <= 3 ? ntiles : (ntiles + 1) / 2;
+  if (ntiles <= 3) shape(p, NT, 1, KVQ_TILES3_TOKEN_GROUPS, KVQ_TILES3_STAGES, smem, threads);
+  else shape(p, NT, 2, KVQ_TILES6_TOKEN_GROUPS, KVQ_TILES6_STAGES, smem, threads);
+  return NT == 2 ? launch_attn_t<0, 2, kWindow>(p, smem, threads, p_max, stream)
+                 : launch_attn_t<0, 3, kWindow>(p, smem, threads, p_max, stream);
+}
+
+// Two tiles a warp at most: the second part of q~ takes registers.
+cudaError_t launch_mass(AttnParams& p, const AttnJob& job, long long p_max, cudaStream_t stream) {
+  p.scores = job.scores;
+  p.stats = job.stats;
+  p.mass = job.mass;
+  p.ids = job.ids;
+  p.mass_len = job.mass_len;
+  p.positions = job.positions;
+  const int ntiles = (p.R + 7) / 8;
+  size_t smem;
+  int threads;
+  if (ntiles == 1) {
+    shape(p, 1, 1, KVQ_TOKEN_GROUPS, KVQ_STAGES_INT4, smem, threads);
+    return launch_attn_t<0, 1, kMass>(p, smem, threads, p_max, stream);
+  }
+  if (ntiles == 2) shape(p, 2, 1, KVQ_TILES3_TOKEN_GROUPS, KVQ_TILES3_STAGES, smem, threads);
+  else shape(p, 2, (ntiles + 1) / 2, 2, 6, smem, threads);
+  return launch_attn_t<0, 2, kMass>(p, smem, threads, p_max, stream);
 }
 
 }  // namespace
@@ -1992,6 +2208,8 @@ cudaError_t launch_attention(const AttnJob& job, cudaStream_t stream) {
   p.out_bf16 = job.out_bf16;
   const bool tree = job.tree_mask != nullptr;
   const int ntiles = (p.R + 7) / 8;
+  if (job.fmt == 0 && job.window > 0) return launch_window(p, job, stream);
+  if (job.scores) return launch_mass(p, job, p_max, stream);
   if (job.fmt == 0 && p.R > kTcMinRows) {
     switch ((p.R + 7) / 8) {
       case 3: return tree ? launch_tc_t<24, true>(p, p_max, stream) : launch_tc_t<24, false>(p, p_max, stream);
@@ -2023,18 +2241,18 @@ cudaError_t launch_attention(const AttnJob& job, cudaStream_t stream) {
   const int threads = (p.ntg * p.nkg + 1) * 32;
   const SmemLayout L(job.fmt, p.nstages, p.B, p.nkg, p.rows_pad);
   const size_t smem = L.total;
-  if (tree) return NT == 1 ? launch_attn_t<0, 1, true>(p, smem, threads, p_max, stream) : launch_attn_t<0, 2, true>(p, smem, threads, p_max, stream);
+  if (tree) return NT == 1 ? launch_attn_t<0, 1, kTree>(p, smem, threads, p_max, stream) : launch_attn_t<0, 2, kTree>(p, smem, threads, p_max, stream);
   if (job.fmt == 0) {
     switch (NT) {
-      case 1: return launch_attn_t<0, 1, false>(p, smem, threads, p_max, stream);
-      case 2: return launch_attn_t<0, 2, false>(p, smem, threads, p_max, stream);
-      default: return launch_attn_t<0, 3, false>(p, smem, threads, p_max, stream);
+      case 1: return launch_attn_t<0, 1, kVerify>(p, smem, threads, p_max, stream);
+      case 2: return launch_attn_t<0, 2, kVerify>(p, smem, threads, p_max, stream);
+      default: return launch_attn_t<0, 3, kVerify>(p, smem, threads, p_max, stream);
     }
   }
   switch (NT) {
-    case 1: return launch_attn_t<1, 1, false>(p, smem, threads, p_max, stream);
-    case 2: return launch_attn_t<1, 2, false>(p, smem, threads, p_max, stream);
-    default: return launch_attn_t<1, 3, false>(p, smem, threads, p_max, stream);
+    case 1: return launch_attn_t<1, 1, kVerify>(p, smem, threads, p_max, stream);
+    case 2: return launch_attn_t<1, 2, kVerify>(p, smem, threads, p_max, stream);
+    default: return launch_attn_t<1, 3, kVerify>(p, smem, threads, p_max, stream);
   }
 }
 

@@ -77,7 +77,16 @@ struct AttnJob {
   float* out;
   // A tree of S drafted tokens in place of a verify block (null: none); int4, and rings on the cluster path.
   const uint64_t* tree_mask;
-  int out_bf16;               // with tree_mask: out holds bf16
+  int out_bf16;               // out holds bf16 (with tree_mask, a window over int4, or mass)
+  // int4: a window (`window` > 0) with the first `sinks` tokens visible outside it
+  int sinks;
+  // int4, S == 1: weights added to mass (scores null: not)
+  float* scores;   // workspace, [B * Hkv][Hq / Hkv][max_pages_per_seq * 64]
+  float2* stats;   // workspace, [B * Hkv][Hq / Hkv]
+  float* mass;     // [.][Hkv][mass_len]
+  int32_t* ids;
+  int mass_len;
+  const int32_t* positions;
   float* partials;  // workspace
   int32_t* dev_err;
 };

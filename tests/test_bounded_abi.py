@@ -29,3 +29,66 @@ def prompt(**over):
     (dict(T=0, sinks=-1), INVALID), (dict(T=0), 0)])
 def test_prompt_sinks_refuses(over, want):
     assert prompt(**over) == want
+
+
+ATTN = dict(Mq=0x60000, Mk=0x70000, q=0x80000, dtype=1, B=2, Hq=20, ctx=0x90000, k=None, v=None, sm=0.09, eps=1e-6, out=0xA0000,
+            od=1, ws=0xB0000, n=1 << 40, err=0xC0000)
+BAD_ATTN = [(dict(B=0), INVALID), (dict(B=5), INVALID), (dict(Hq=21), UNSUPPORTED), (dict(Hq=0), UNSUPPORTED), (dict(Hq=196), UNSUPPORTED),
+            (dict(dtype=2), INVALID), (dict(od=2), INVALID), (dict(q=0), INVALID), (dict(q=0x80004), INVALID), (dict(ctx=0), INVALID),
+            (dict(out=0), INVALID), (dict(out=0xA0008), INVALID), (dict(ws=0), INVALID), (dict(ws=0xB0080), INVALID),
+            (dict(n=100), INVALID), (dict(err=0), INVALID), (dict(k=0xD0000), INVALID), (dict(v=0xD0000), INVALID),
+            (dict(k=0xD0008, v=0xE0000), INVALID), (dict(sm=float("nan")), INVALID), (dict(Mq=0), INVALID),
+            (dict(Mq=0x60004), INVALID), (dict(k=0xD0000, v=0xE0000, Mk=0), INVALID), (dict(eps=-1.0), INVALID)]
+
+
+def window(c=None, fn="kvq_window_attn_int4", **over):
+    a = dict(ATTN, S=2, window=100, sinks=4, **{})
+    a.update(over)
+    return getattr(L, fn)(c or cache(), a["Mq"], a["Mk"], a["q"], a["dtype"], a["B"], a["S"], a["Hq"], a["ctx"], a["window"],
+                          a["sinks"], a["k"], a["v"], a["sm"], a["eps"], a["out"], a["od"], a["ws"], a["n"], a["err"], None)
+
+
+@pytest.mark.parametrize("over,want", BAD_ATTN + [
+    (dict(window=0), INVALID), (dict(window=-3), INVALID), (dict(sinks=-1), INVALID), (dict(S=0), UNSUPPORTED),
+    (dict(S=9), UNSUPPORTED), (dict(S=8, Hq=28), UNSUPPORTED)])
+@pytest.mark.parametrize("fn", ["kvq_window_attn_int4", "kvq_window_attn_int4_fwht"])
+def test_window_refuses(over, want, fn):
+    assert window(fn=fn, **over) == want
+
+
+def mass_of(**over):
+    d = dict(mass=0x1000000, ids=0x2000000, num_seqs=4, num_kv_heads=4, max_tokens=512)
+    d.update(over)
+    return kvq.TokenMass(**d)
+
+
+def mass(c=None, m=None, fn="kvq_mass_attn_int4", **over):
+    a = dict(ATTN, pos=0x98000)
+    a.update(over)
+    return getattr(L, fn)(c or cache(), m or mass_of(), a["Mq"], a["Mk"], a["q"], a["dtype"], a["B"], a["Hq"], a["ctx"], a["pos"],
+                          a["k"], a["v"], a["sm"], a["eps"], a["out"], a["od"], a["ws"], a["n"], a["err"], None)
+
+
+@pytest.mark.parametrize("over,want", BAD_ATTN + [(dict(pos=0), INVALID)])
+@pytest.mark.parametrize("fn", ["kvq_mass_attn_int4", "kvq_mass_attn_int4_fwht"])
+def test_mass_refuses(over, want, fn):
+    assert mass(fn=fn, **over) == want
+
+
+@pytest.mark.parametrize("over", [
+    dict(mass=0), dict(ids=0), dict(mass=0x1000008), dict(num_seqs=1), dict(num_kv_heads=2), dict(max_tokens=511),
+    dict(max_tokens=508), dict(max_tokens=514), dict(ids=0x1000000 + 4096), dict(mass=0xA0000 - 4096), dict(ids=0x90000 - 64),
+    dict(ids=0x98000)])
+def test_mass_refuses_descriptors(over):
+    assert mass(m=mass_of(**over)) == INVALID
+
+
+def test_wide_tables_and_workspaces():
+    wide = cache(max_pages_per_seq=1 << 24, num_seqs=1024)
+    assert window(wide, B=1024) == UNSUPPORTED and mass(wide, mass_of(num_seqs=1024, max_tokens=1 << 30), B=1024) == UNSUPPORTED
+    assert window(cache(head_dim=64)) == UNSUPPORTED and mass(cache(page_size=32)) == UNSUPPORTED
+    size = kvq.kvq_mass_workspace_bytes
+    assert size(2, 20, 4, 8) >= kvq.kvq_decode_workspace_bytes(2, 1, 20, 4) + 4 * 2 * 20 * 512
+    assert size(1, 48, 1, 1 << 24) > 2 ** 37
+    for bad in ((0, 20, 4, 8), (2, 21, 4, 8), (2, 20, 4, 0), (2, 196, 4, 8), (1, 20, 4, (1 << 24) + 1), (1024, 20, 4, 1 << 20)):
+        assert size(*bad) == 0
