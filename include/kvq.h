@@ -597,6 +597,32 @@ kvq_status kvq_mass_attn_int4_fwht(const kvq_int4_cache* cache, const kvq_token_
                                    const void* v_new, float sm_scale, float eps, void* out, kvq_dtype out_dtype,
                                    void* workspace, size_t workspace_bytes, int32_t* dev_err, kvq_stream_t stream);
 
+/*
+ * kvq_evict_int4 -- eviction by gathered weight: per layer, sequence b and KV head, of the n = ctx_len[b] slots
+ *   min(n, budget) stay: those whose token is one of the first (ids < sinks) or one of the newest
+ *   (ids >= seen[b] - recent), then those with the largest mass; among equal ones the lower slots (so too where the first
+ *   and newest ones are more than the budget). A NaN mass counts less than any other.
+ *   A kept slot behind the budget moves, with its record, mass and number, into a slot before it that is given up: the i-th
+ *   such slot, ascending, into the i-th one given up. Nothing else changes: slots from the new length on are left as they
+ *   were. What stays is the same set for any order, attention does not ask for one, and every call here that goes on
+ *   with the sequence appends behind the new length. Each KV head keeps its own tokens.
+ *   caches, masses: host arrays of num_caches descriptors (1..KVQ_MAX_CACHES), the layers in the same order; the same
+ *             number of KV heads in all. No layer twice; no overlap of any mass or ids with another or with the lists.
+ *             The pages of an evicted sequence belong to it alone (of forked sequences that share pages the copies come
+ *             first).
+ *   ctx_len, seen: device int32[B]: the cached tokens, and how many tokens the sequence has had in all.
+ *   ctx_out:  device int32[B] or NULL: receives min(ctx_len[b], budget); must not overlap ctx_len or seen. The pages
+ *             behind it can be given back by kvq_pages_free(.., ctx_len, ctx_out, ..).
+ *   A length outside the block table is clamped (KVQ_DEVERR_POS). A move from or to a page outside the pool is passed over
+ *   (KVQ_DEVERR_PAGE): its token is lost.
+ * Requires 1 <= B <= KVQ_MAX_SEQS, budget >= 1, sinks, recent >= 0, 64*max_pages_per_seq <= KVQ_EVICT_MAX_TOKENS, ids
+ * 16-byte aligned.
+ */
+#define KVQ_EVICT_MAX_TOKENS 393216
+kvq_status kvq_evict_int4(const kvq_int4_cache* caches, const kvq_token_mass* masses, int num_caches, int B,
+                          const int32_t* ctx_len, const int32_t* seen, int budget, int sinks, int recent,
+                          int32_t* ctx_out, int32_t* dev_err, kvq_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -21,6 +21,7 @@ PAGE_SIZE = 64
 MAX_SEQS = 1024
 MAX_TREE = 64
 MAX_CACHES = 64
+EVICT_MAX_TOKENS = 393216
 F32, BF16, F16 = 0, 1, 2
 DEVERR_PAGE, DEVERR_POS, DEVERR_NONFINITE, DEVERR_RANGE, DEVERR_TIMEOUT = 0x1, 0x2, 0x4, 0x8, 0x10
 DEVERR_POOL = 0x20
@@ -110,6 +111,8 @@ def _load():
         getattr(L, name).restype = i32
         getattr(L, name).argtypes = [ctypes.POINTER(Int4Cache), ctypes.POINTER(TokenMass), vp, vp, vp, i32, i32, i32, vp, vp,
                                      vp, vp, f32, f32, vp, i32, vp, sz, vp, vp]
+    L.kvq_evict_int4.restype = i32
+    L.kvq_evict_int4.argtypes = [vp, vp, i32, i32, vp, vp, i32, i32, i32, vp, vp, vp]
     L.kvq_tree_attn_fp8_swa.restype = i32
     L.kvq_tree_attn_fp8_swa.argtypes = [ctypes.POINTER(Fp8Ring), vp, i32, i32, i32, i32, vp, vp, i32, vp, vp, f32,
                                         f32, f32, vp, i32, vp, sz, vp, vp]
@@ -670,3 +673,18 @@ def kvq_mass_attn_int4(cache: Int4Cache, mass: TokenMass, Mq, Mk, q, ctx_len, po
                 workspace.data_ptr(), _bytes(workspace, dev), _err(dev_err, dev), _here(dev, stream))
     if status:
         raise KvqError("kvq_mass_attn_int4_fwht" if fwht else "kvq_mass_attn_int4", status)
+
+
+def kvq_evict_int4(caches, masses, ctx_len, seen, budget: int, sinks: int, recent: int, dev_err, ctx_out=None, stream=None):
+    """In every one of the layers `caches` (a list of Int4Cache) with what their slots gathered `masses` (a list of
+    TokenMass), per sequence and KV head: min(ctx_len, budget) slots stay, those of the first `sinks` and the newest
+    `recent` tokens, then those that gathered most. seen: the tokens every sequence has had; ctx_out: the new lengths."""
+    i32, descriptors, held = _torch().int32, _layers(caches, Int4Cache), _layers(masses, TokenMass)
+    _need(len(masses) == len(caches), "one TokenMass for every cache")
+    B, dev = ctx_len.shape[0], _dev(ctx_len, "ctx_len")
+    status = lib.kvq_evict_int4(descriptors, held, len(caches), B, _is(ctx_len, i32, (B,), "ctx_len", dev),
+                                _is(seen, i32, (B,), "seen", dev), budget, sinks, recent,
+                                None if ctx_out is None else _is(ctx_out, i32, (B,), "ctx_out", dev), _err(dev_err, dev),
+                                _here(dev, stream))
+    if status:
+        raise KvqError("kvq_evict_int4", status)

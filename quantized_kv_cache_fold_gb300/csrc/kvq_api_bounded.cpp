@@ -189,4 +189,48 @@ kvq_status kvq_mass_attn_int4_fwht(const kvq_int4_cache* cache, const kvq_token_
                    out_dtype, workspace, workspace_bytes, dev_err, stream, 1);
 }
 
+kvq_status kvq_evict_int4(const kvq_int4_cache* caches, const kvq_token_mass* masses, int num_caches, int B,
+                          const int32_t* ctx_len, const int32_t* seen, int budget, int sinks, int recent,
+                          int32_t* ctx_out, int32_t* dev_err, kvq_stream_t stream) {
+  kvq::EvictJob j{};
+  kvq_status st = kvq::cache_set(caches, num_caches, j.cs);
+  if (st != KVQ_OK) return st;
+  if (!masses || !ctx_len || !seen || !dev_err || B < 1 || B > KVQ_MAX_SEQS) return KVQ_ERR_INVALID_ARG;
+  if (budget < 1 || sinks < 0 || recent < 0) return KVQ_ERR_INVALID_ARG;
+  const size_t lens = 4 * (size_t)B;
+  if (ctx_out && (overlap(ctx_len, lens, ctx_out, lens) || overlap(seen, lens, ctx_out, lens))) return KVQ_ERR_INVALID_ARG;
+  for (int i = 0; i < num_caches; ++i) {
+    if (B > caches[i].num_seqs) return KVQ_ERR_INVALID_ARG;
+    st = check_mass(masses + i, caches + i, B);
+    if (st != KVQ_OK) return st;
+    if (!aligned(masses[i].ids, 16)) return KVQ_ERR_INVALID_ARG;
+    j.mass[i] = masses[i].mass;
+    j.ids[i] = masses[i].ids;
+    j.mass_len[i] = masses[i].max_tokens;
+  }
+  // every list of masses and numbers is written while others are read: all apart
+  if (kvq::repeated(j.cs)) return KVQ_ERR_INVALID_ARG;
+  auto bytes = [&](int i) { return 4 * (size_t)masses[i].num_seqs * masses[i].num_kv_heads * masses[i].max_tokens; };
+  for (int i = 0; i < num_caches; ++i) {
+    for (const void* x : {(const void*)j.mass[i], (const void*)j.ids[i]}) {
+      for (const int32_t* y : {ctx_len, seen, (const int32_t*)ctx_out})
+        if (y && overlap(x, bytes(i), y, lens)) return KVQ_ERR_INVALID_ARG;
+      for (int k = 0; k < i; ++k)
+        if (overlap(x, bytes(i), j.mass[k], bytes(k)) || overlap(x, bytes(i), j.ids[k], bytes(k))) return KVQ_ERR_INVALID_ARG;
+    }
+    if (overlap(j.mass[i], bytes(i), j.ids[i], bytes(i))) return KVQ_ERR_INVALID_ARG;
+    if ((long long)j.cs.max_pages[i] * KVQ_PAGE_SIZE > KVQ_EVICT_MAX_TOKENS) return KVQ_ERR_UNSUPPORTED;
+  }
+  if ((long long)num_caches * B * j.cs.heads > (1LL << 27)) return KVQ_ERR_UNSUPPORTED;
+  j.B = B;
+  j.ctx_len = ctx_len;
+  j.seen = seen;
+  j.budget = budget;
+  j.sinks = sinks;
+  j.recent = recent;
+  j.ctx_out = ctx_out;
+  j.dev_err = dev_err;
+  return from_cuda(kvq::launch_evict(j, (cudaStream_t)stream));
+}
+
 }  // extern "C"

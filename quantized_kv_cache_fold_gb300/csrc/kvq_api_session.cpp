@@ -9,6 +9,40 @@
 #include "kvq.h"
 #include "kvq_internal.h"
 
+namespace kvq {
+
+// Whether two layers of a call are the same memory (a commit would move its records twice at once).
+bool repeated(const CacheSet& cs) {
+  for (int i = 1; i < cs.count; ++i)
+    for (int k = 0; k < i; ++k)
+      if (cs.pages[i] == cs.pages[k]) return true;
+  return false;
+}
+
+// The caches of one call, checked; all of one number of KV heads.
+kvq_status cache_set(const kvq_int4_cache* caches, int num_caches, CacheSet& cs) {
+  if (!caches || num_caches < 1) return KVQ_ERR_INVALID_ARG;
+  if (num_caches > KVQ_MAX_CACHES) return KVQ_ERR_UNSUPPORTED;
+  cs.count = num_caches;
+  cs.heads = caches[0].num_kv_heads;
+  for (int i = 0; i < num_caches; ++i) {
+    const kvq_status st = check_int4_cache(caches + i);
+    if (st != KVQ_OK) return st;
+    if (caches[i].num_kv_heads != cs.heads) return KVQ_ERR_INVALID_ARG;
+    cs.pages[i] = caches[i].pages;
+    cs.table[i] = caches[i].block_table;
+    cs.num_pages[i] = caches[i].num_pages;
+    cs.num_seqs[i] = caches[i].num_seqs;
+    cs.max_pages[i] = caches[i].max_pages_per_seq;
+  }
+  return KVQ_OK;
+}
+
+}  // namespace kvq
+
+using kvq::cache_set;
+using kvq::repeated;
+
 namespace {
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -124,33 +158,6 @@ kvq_status check_commit(int num_caches, int B, int N, const int32_t* ctx, const 
   const size_t n = 4 * (size_t)B;
   if (ctx_out && (overlap(ctx, n, ctx_out, n) || overlap(n_accept, n, ctx_out, n) || overlap(path, n * N, ctx_out, n)))
     return KVQ_ERR_INVALID_ARG;
-  return KVQ_OK;
-}
-
-// Whether two layers of a call are the same memory (a commit would move its records twice at once).
-bool repeated(const kvq::CacheSet& cs) {
-  for (int i = 1; i < cs.count; ++i)
-    for (int k = 0; k < i; ++k)
-      if (cs.pages[i] == cs.pages[k]) return true;
-  return false;
-}
-
-// The caches of one call, checked; all of one number of KV heads.
-kvq_status cache_set(const kvq_int4_cache* caches, int num_caches, kvq::CacheSet& cs) {
-  if (!caches || num_caches < 1) return KVQ_ERR_INVALID_ARG;
-  if (num_caches > KVQ_MAX_CACHES) return KVQ_ERR_UNSUPPORTED;
-  cs.count = num_caches;
-  cs.heads = caches[0].num_kv_heads;
-  for (int i = 0; i < num_caches; ++i) {
-    const kvq_status st = kvq::check_int4_cache(caches + i);
-    if (st != KVQ_OK) return st;
-    if (caches[i].num_kv_heads != cs.heads) return KVQ_ERR_INVALID_ARG;
-    cs.pages[i] = caches[i].pages;
-    cs.table[i] = caches[i].block_table;
-    cs.num_pages[i] = caches[i].num_pages;
-    cs.num_seqs[i] = caches[i].num_seqs;
-    cs.max_pages[i] = caches[i].max_pages_per_seq;
-  }
   return KVQ_OK;
 }
 

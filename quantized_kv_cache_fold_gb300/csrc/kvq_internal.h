@@ -199,6 +199,25 @@ cudaError_t launch_pages_copy(const CacheSet& cs, int n, const int32_t* src, con
 cudaError_t launch_tree_commit(int fmt, const CacheSet& cs, int B, int N, const int32_t* ctx_len, const int32_t* path,
                                const int32_t* n_accept, int32_t* ctx_out, int32_t* dev_err, cudaStream_t stream);
 
+// ---- eviction (kvq_evict.cu)
+struct EvictJob {
+  CacheSet cs;
+  float* mass[KVQ_MAX_CACHES];
+  int32_t* ids[KVQ_MAX_CACHES];
+  int32_t mass_len[KVQ_MAX_CACHES];
+  int32_t B;
+  const int32_t *ctx_len, *seen;
+  int32_t budget, sinks, recent;
+  int32_t* ctx_out;
+  int32_t* dev_err;
+};
+cudaError_t launch_evict(const EvictJob& job, cudaStream_t stream);
+
+// The caches of one call over several layers, checked; all of one number of KV heads.
+kvq_status cache_set(const kvq_int4_cache* caches, int num_caches, CacheSet& cs);
+// Whether two layers of a call are the same memory (their records would be moved twice at once).
+bool repeated(const CacheSet& cs);
+
 // Argument checks shared by the C-ABI translation units.
 kvq_status check_int4_cache(const kvq_int4_cache* c);
 kvq_status check_ring(const kvq_fp8_ring* r);

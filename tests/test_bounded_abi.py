@@ -92,3 +92,37 @@ def test_wide_tables_and_workspaces():
     assert size(1, 48, 1, 1 << 24) > 2 ** 37
     for bad in ((0, 20, 4, 8), (2, 21, 4, 8), (2, 20, 4, 0), (2, 196, 4, 8), (1, 20, 4, (1 << 24) + 1), (1024, 20, 4, 1 << 20)):
         assert size(*bad) == 0
+
+
+def evict(n=2, caches=None, masses=None, **over):
+    a = dict(B=2, ctx=0x90000, seen=0x98000, budget=100, sinks=4, recent=10, out=0xA0000, err=0xC0000)
+    a.update(over)
+    cs = caches or [cache(pages=0x10000 + 0x1000000 * i) for i in range(n)]
+    ms = masses or [mass_of(mass=0x10000000 + 0x200000 * i, ids=0x10100000 + 0x200000 * i) for i in range(n)]
+    return L.kvq_evict_int4(b"".join(cs), b"".join(ms), n, a["B"], a["ctx"], a["seen"], a["budget"], a["sinks"], a["recent"],
+                            a["out"], a["err"], None)
+
+
+@pytest.mark.parametrize("over,want", [
+    (dict(B=0), INVALID), (dict(B=5), INVALID), (dict(ctx=0), INVALID), (dict(seen=0), INVALID), (dict(err=0), INVALID),
+    (dict(budget=0), INVALID), (dict(sinks=-1), INVALID), (dict(recent=-1), INVALID), (dict(out=0x90000), INVALID),
+    (dict(out=0x98004), INVALID), (dict(n=0), INVALID), (dict(n=65), UNSUPPORTED), (dict(ctx=0x10000000 + 64), INVALID),
+    (dict(out=0x10100000), INVALID)])
+def test_evict_refuses(over, want):
+    assert evict(**over) == want
+
+
+def test_evict_refuses_layers():
+    two = [cache(), cache(pages=0x2000000)]
+    assert evict(caches=[cache(), cache()]) == INVALID                       # a layer twice
+    assert evict(caches=[cache(), cache(pages=0x2000000, num_kv_heads=2)]) == INVALID
+    assert evict(caches=[cache(), cache(pages=0x2000000, num_seqs=1)]) == INVALID
+    assert evict(caches=[cache(), cache(pages=0x2000000, head_dim=64)]) == UNSUPPORTED
+    wide = [cache(), cache(pages=0x2000000, max_pages_per_seq=6145)]
+    ok = mass_of()
+    assert evict(caches=wide, masses=[ok, mass_of(mass=0x40000000, ids=0x50000000, max_tokens=6145 * 64)]) == UNSUPPORTED
+    for bad in (dict(mass=0), dict(ids=0), dict(mass=0x1000000 + 4096), dict(ids=0x1000000), dict(ids=0x2000000), dict(mass=0x8),
+                dict(ids=0x40000004), dict(num_seqs=1), dict(num_kv_heads=3), dict(max_tokens=508)):
+        over = dict(mass=0x30000000, ids=0x40000000)
+        over.update(bad)
+        assert evict(caches=two, masses=[ok, mass_of(**over)]) == INVALID, bad
