@@ -598,6 +598,29 @@ kvq_status kvq_mass_attn_int4_fwht(const kvq_int4_cache* cache, const kvq_token_
                                    void* workspace, size_t workspace_bytes, int32_t* dev_err, kvq_stream_t stream);
 
 /*
+ * kvq_prompt_mass -- what the tokens of packed prompts have gathered from their last rows: the mass that a cache filled with
+ *   these prompts starts from. With the softmax weights w of kvq_prompt_attn (no window), for token j of sequence b:
+ *     mass[seq_ids[b]][h][j] = sum over its rows i >= max(j, n - rows) and the query heads g of KV head h of w_ig[j],
+ *     ids[seq_ids[b]][h][j] = j,   j < n = cu_seqlens[b+1] - cu_seqlens[b].
+ *   Both are set, whatever they held; places from n on, and rows that no sequence names, are left as they were.
+ *   q, k:     as kvq_prompt_attn takes them (KVQ_BF16 or KVQ_F16); strides: host int64[4] or NULL (packed), elements
+ *             between tokens and between heads of q, then of k, as there.
+ *   rows:     the rows that count, from the end (<= 0, or n and more: all).
+ *   seq_ids:  device int32[B] or NULL (b). A row outside mass or named before, offsets as kvq_prompt_attn refuses them (but
+ *             sequences may overlap), or a prompt longer than max_tokens: skipped, KVQ_DEVERR_POS.
+ *   workspace: device, >= kvq_prompt_mass_workspace_bytes(T, B, num_q_heads, num_kv_heads, rows), 256-byte aligned;
+ *             contents need no initialisation.
+ *   Precision: products of the 16-bit inputs summed in fp32, weights and sums fp32, in an order that does not depend on
+ *   timing. A row that is not finite (a query, or a key that it sees) adds nothing.
+ * Requires num_q_heads/num_kv_heads <= 64 and otherwise the sizes of kvq_prompt_attn; mass and ids overlap no input.
+ */
+size_t kvq_prompt_mass_workspace_bytes(int T, int B, int num_q_heads, int num_kv_heads, int rows);
+kvq_status kvq_prompt_mass(const void* q, const void* k, kvq_dtype dtype, int T, int B, int num_q_heads, int num_kv_heads,
+                           const int64_t* strides, const int32_t* cu_seqlens, int rows, const int32_t* seq_ids,
+                           float sm_scale, const kvq_token_mass* mass, void* workspace, size_t workspace_bytes,
+                           int32_t* dev_err, kvq_stream_t stream);
+
+/*
  * kvq_evict_int4 -- eviction by gathered weight: per layer, sequence b and KV head, of the n = ctx_len[b] slots
  *   min(n, budget) stay: those whose token is one of the first (ids < sinks) or one of the newest
  *   (ids >= seen[b] - recent), then those with the largest mass; among equal ones the lower slots (so too where the first

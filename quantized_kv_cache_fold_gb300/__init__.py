@@ -111,6 +111,11 @@ def _load():
         getattr(L, name).restype = i32
         getattr(L, name).argtypes = [ctypes.POINTER(Int4Cache), ctypes.POINTER(TokenMass), vp, vp, vp, i32, i32, i32, vp, vp,
                                      vp, vp, f32, f32, vp, i32, vp, sz, vp, vp]
+    L.kvq_prompt_mass_workspace_bytes.restype = sz
+    L.kvq_prompt_mass_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
+    L.kvq_prompt_mass.restype = i32
+    L.kvq_prompt_mass.argtypes = [vp, vp, i32, i32, i32, i32, i32, ctypes.POINTER(i64), vp, i32, vp, f32,
+                                  ctypes.POINTER(TokenMass), vp, sz, vp, vp]
     L.kvq_evict_int4.restype = i32
     L.kvq_evict_int4.argtypes = [vp, vp, i32, i32, vp, vp, i32, i32, i32, vp, vp, vp]
     L.kvq_tree_attn_fp8_swa.restype = i32
@@ -673,6 +678,51 @@ def kvq_mass_attn_int4(cache: Int4Cache, mass: TokenMass, Mq, Mk, q, ctx_len, po
                 workspace.data_ptr(), _bytes(workspace, dev), _err(dev_err, dev), _here(dev, stream))
     if status:
         raise KvqError("kvq_mass_attn_int4_fwht" if fwht else "kvq_mass_attn_int4", status)
+
+
+def kvq_prompt_mass_workspace_bytes(T: int, B: int, num_q_heads: int, num_kv_heads: int, rows: int) -> int:
+    return int(lib.kvq_prompt_mass_workspace_bytes(T, B, num_q_heads, num_kv_heads, rows))
+
+
+def alloc_prompt_mass_workspace(T: int, B: int, num_q_heads: int, num_kv_heads: int, rows: int, device="cuda"):
+    n = kvq_prompt_mass_workspace_bytes(T, B, num_q_heads, num_kv_heads, rows)
+    if n == 0:
+        raise KvqError("kvq_prompt_mass_workspace_bytes", 2)
+    torch = _torch()
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+_Strides4 = ctypes.c_int64 * 4
+
+
+def kvq_prompt_mass(q, k, cu_seqlens, rows: int, mass: TokenMass, workspace, dev_err, seq_ids=None,
+                    sm_scale: float = HEAD_DIM ** -0.5, stream=None):
+    """Sets `mass` to the attention weights that the last `rows` rows (<= 0: all) of each packed prompt put on its tokens.
+    q [T, Hq, 128], k [T, Hkv, 128] and cu_seqlens as kvq_prompt_attn takes them; seq_ids int32[B]: the rows of mass
+    (None: 0, 1, ...)."""
+    torch = _torch()
+    dtype = q.dtype
+    if dtype is not torch.bfloat16 and dtype is not torch.float16:
+        raise TypeError(f"unsupported dtype {dtype}")
+    T, Hq, D = q.shape
+    Hkv = k.shape[1]
+    if not (D == HEAD_DIM and k.shape == (T, Hkv, D)):
+        raise ValueError(f"shapes: q {tuple(q.shape)}, k {tuple(k.shape)}")
+    if not (k.dtype is dtype and q.is_cuda and q.get_device() == k.get_device()):
+        raise ValueError("q and k must be tensors of one dtype on one device")
+    B, dev = cu_seqlens.shape[0] - 1, q.get_device()
+    cu = _is(cu_seqlens, torch.int32, (B + 1,), "cu_seqlens", dev)
+    sq, sk = q.stride(), k.stride()
+    if not sq[2] == sk[2] == 1:
+        raise ValueError("the rows of q and k must be contiguous")
+    # of an extent of one the stride does not matter: the packed one
+    strides = _Strides4(*(x for st, h in ((sq, Hq), (sk, Hkv)) for x in (st[0] if T > 1 else max(1, h) * D, st[1] if h > 1 else D)))
+    status = lib.kvq_prompt_mass(q.data_ptr(), k.data_ptr(), BF16 if dtype is torch.bfloat16 else F16, T, B, Hq, Hkv, strides, cu,
+                                 rows, None if seq_ids is None else _is(seq_ids, torch.int32, (B,), "seq_ids", dev), sm_scale,
+                                 ctypes.byref(mass), workspace.data_ptr(), _bytes(workspace, dev), _err(dev_err, dev),
+                                 _here(dev, stream))
+    if status:
+        raise KvqError("kvq_prompt_mass", status)
 
 
 def kvq_evict_int4(caches, masses, ctx_len, seen, budget: int, sinks: int, recent: int, dev_err, ctx_out=None, stream=None):

@@ -98,7 +98,7 @@ kvq_status window_impl(const kvq_int4_cache* cache, const float* Mq, const float
 
 kvq_status check_mass(const kvq_token_mass* m, const kvq_int4_cache* cache, int B) {
   if (!m || !m->mass || !m->ids || !aligned(m->mass, 16) || !aligned(m->ids, 4)) return KVQ_ERR_INVALID_ARG;
-  if (B > m->num_seqs || m->num_kv_heads < 1 || m->max_tokens < 1 || m->max_tokens % 4) return KVQ_ERR_INVALID_ARG;
+  if (m->num_seqs < 1 || B > m->num_seqs || m->num_kv_heads < 1 || m->max_tokens < 1 || m->max_tokens % 4) return KVQ_ERR_INVALID_ARG;
   if (cache && (m->num_kv_heads != cache->num_kv_heads ||
                 m->max_tokens < (long long)cache->max_pages_per_seq * KVQ_PAGE_SIZE))
     return KVQ_ERR_INVALID_ARG;
@@ -187,6 +187,67 @@ kvq_status kvq_mass_attn_int4_fwht(const kvq_int4_cache* cache, const kvq_token_
                                    void* workspace, size_t workspace_bytes, int32_t* dev_err, kvq_stream_t stream) {
   return mass_impl(cache, mass, wq, wk, q, dtype, B, num_q_heads, ctx_len, positions, k_new, v_new, sm_scale, eps, out,
                    out_dtype, workspace, workspace_bytes, dev_err, stream, 1);
+}
+
+size_t kvq_prompt_mass_workspace_bytes(int T, int B, int num_q_heads, int num_kv_heads, int rows) {
+  if (T < 0 || B < 1 || B > KVQ_MAX_SEQS || num_q_heads < 1 || num_kv_heads < 1 || num_q_heads % num_kv_heads ||
+      num_q_heads / num_kv_heads > 64 || (long long)T * num_q_heads > (1LL << 30))
+    return 0;
+  return kvq::observe_workspace_bytes(T, B, num_q_heads, num_kv_heads, rows);
+}
+
+kvq_status kvq_prompt_mass(const void* q, const void* k, kvq_dtype dtype, int T, int B, int num_q_heads, int num_kv_heads,
+                           const int64_t* strides, const int32_t* cu_seqlens, int rows, const int32_t* seq_ids,
+                           float sm_scale, const kvq_token_mass* mass, void* workspace, size_t workspace_bytes,
+                           int32_t* dev_err, kvq_stream_t stream) {
+  if (dtype == KVQ_F32) return KVQ_ERR_UNSUPPORTED;
+  if (dtype != KVQ_BF16 && dtype != KVQ_F16) return KVQ_ERR_INVALID_ARG;
+  if (num_kv_heads >= 1 && num_q_heads / num_kv_heads > 64) return KVQ_ERR_UNSUPPORTED;
+  const size_t need = kvq_prompt_mass_workspace_bytes(T, B, num_q_heads, num_kv_heads, rows);
+  if (need == 0) return KVQ_ERR_INVALID_ARG;
+  if (!std::isfinite(sm_scale) || !(sm_scale > 0.0f)) return KVQ_ERR_INVALID_ARG;
+  if (T == 0) return KVQ_OK;
+  const kvq_status st = check_mass(mass, nullptr, 0);
+  if (st != KVQ_OK) return st;
+  if (mass->num_kv_heads != num_kv_heads || (!seq_ids && B > mass->num_seqs)) return KVQ_ERR_INVALID_ARG;
+  if (!q || !k || !cu_seqlens || !workspace || !dev_err) return KVQ_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(workspace, 256)) return KVQ_ERR_INVALID_ARG;
+  if (workspace_bytes < need) return KVQ_ERR_INVALID_ARG;
+  const long long D = KVQ_HEAD_DIM;
+  long long s[4] = {D * num_q_heads, D, D * num_kv_heads, D};
+  if (strides)
+    for (int i = 0; i < 4; ++i) {
+      if (strides[i] < 8 || strides[i] % 8 || strides[i] > (1LL << 36)) return KVQ_ERR_INVALID_ARG;
+      s[i] = strides[i];
+    }
+  // mass and ids are written while keys and lists are still read
+  const size_t held = 4 * (size_t)mass->num_seqs * num_kv_heads * mass->max_tokens;
+  const size_t qb = 2 * (size_t)((T - 1) * s[0] + (num_q_heads - 1) * s[1] + D);
+  const size_t kb = 2 * (size_t)((T - 1) * s[2] + (num_kv_heads - 1) * s[3] + D);
+  if (overlap(mass->mass, held, mass->ids, held)) return KVQ_ERR_INVALID_ARG;
+  for (const void* x : {(const void*)mass->mass, (const void*)mass->ids})
+    if (overlap(x, held, q, qb) || overlap(x, held, k, kb) || overlap(x, held, cu_seqlens, 4 * (size_t)(B + 1)) ||
+        (seq_ids && overlap(x, held, seq_ids, 4 * (size_t)B)) || overlap(x, held, workspace, need))
+      return KVQ_ERR_INVALID_ARG;
+  kvq::ObserveJob j{};
+  j.q = q;
+  j.k = k;
+  j.f16 = dtype == KVQ_F16;
+  j.T = T;
+  j.B = B;
+  j.Hq = num_q_heads;
+  j.Hkv = num_kv_heads;
+  j.qs_t = s[0], j.qs_h = s[1], j.ks_t = s[2], j.ks_h = s[3];
+  j.cu_seqlens = cu_seqlens;
+  j.seq_ids = seq_ids;
+  j.rows = rows;
+  j.sm_scale = sm_scale;
+  j.mass = mass->mass;
+  j.ids = mass->ids;
+  j.num_seqs = mass->num_seqs;
+  j.mass_len = mass->max_tokens;
+  j.dev_err = dev_err;
+  return from_cuda(kvq::launch_observe(j, workspace, (cudaStream_t)stream));
 }
 
 kvq_status kvq_evict_int4(const kvq_int4_cache* caches, const kvq_token_mass* masses, int num_caches, int B,

@@ -131,6 +131,31 @@ struct PromptJob {
 };
 cudaError_t launch_prompt(const PromptJob& job, cudaStream_t stream);
 
+// Tensor map (a CUtensorMap) of a [T][heads][128] tensor of 16-bit elements (strides in elements): boxes of box[0] dims x
+// box[1] heads x box[2] tokens, rows swizzled over 128 or 64 bytes, zeros outside.
+cudaError_t tensor_map_16(void* map, bool f16, const void* base, int T, int heads, long long st, long long sh,
+                          const uint32_t (&box)[3], bool swizzle64);
+
+// ---- weights of a prompt's last rows (kvq_observe.cu)
+struct ObserveJob {
+  const void *q, *k;
+  int f16;  // 1: fp16, 0: bf16
+  int T, B, Hq, Hkv;
+  long long qs_t, qs_h, ks_t, ks_h;  // elements
+  const int32_t* cu_seqlens;
+  const int32_t* seq_ids;  // null: sequence b is row b
+  int rows;                // <= 0: all
+  float sm_scale;
+  float* mass;
+  int32_t* ids;
+  int num_seqs, mass_len;
+  float* rec;    // workspace: a record of each query tile
+  float2* part;  // workspace: base and sum of each row and split
+  int32_t* dev_err;
+};
+size_t observe_workspace_bytes(int T, int B, int Hq, int Hkv, int rows);
+cudaError_t launch_observe(const ObserveJob& job, void* workspace, cudaStream_t stream);
+
 // ---- tree attention (kvq_tree.cu)
 struct TreeJob {
   int fmt;  // 0 = int4 paged, 1 = fp8 ring

@@ -696,31 +696,35 @@ cudaError_t encoder(EncodeTiled& f) {
   return cudaSuccess;
 }
 
-// Map of a [T][heads][128] tensor: boxes of 64 dims x 1 head x 128 tokens, 128-byte swizzle, zeros
-// outside (tokens from T on); the output's: 32 dims x 1 head x 32 tokens, 64-byte swizzle.
-bool encode(EncodeTiled f, CUtensorMap* m, bool f16, const void* base, int T, int heads, long long st, long long sh, bool out = false) {
-  const cuuint64_t dims[3] = {kD, (cuuint64_t)heads, (cuuint64_t)T};
-  const cuuint64_t strides[2] = {(cuuint64_t)sh * 2, (cuuint64_t)st * 2};
-  const cuuint32_t box[3] = {out ? 32u : 64u, 1, out ? 32u : (cuuint32_t)kRows}, one[3] = {1, 1, 1};
-  return f(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
-           strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, out ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
-           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 }  // namespace
 
-cudaError_t launch_prompt(const PromptJob& job, cudaStream_t stream) {
+cudaError_t tensor_map_16(void* map, bool f16, const void* base, int T, int heads, long long st, long long sh,
+                          const uint32_t (&box)[3], bool swizzle64) {
   EncodeTiled f;
-  cudaError_t e = encoder(f);
+  const cudaError_t e = encoder(f);
   if (e != cudaSuccess) return e;
+  const cuuint64_t dims[3] = {kD, (cuuint64_t)heads, (cuuint64_t)T};
+  const cuuint64_t strides[2] = {(cuuint64_t)sh * 2, (cuuint64_t)st * 2};
+  const cuuint32_t one[3] = {1, 1, 1};
+  return f(static_cast<CUtensorMap*>(map), f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+           const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+           swizzle64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? cudaSuccess
+             : cudaErrorInvalidValue;
+}
+
+cudaError_t launch_prompt(const PromptJob& job, cudaStream_t stream) {
   PromptParams p;
   p.j = job;
   p.scale2 = job.sm_scale * kLog2e;
-  if (!encode(f, &p.mq, job.f16, job.q, job.T, job.Hq, job.qs_t, job.qs_h) ||
-      !encode(f, &p.mk, job.f16, job.k, job.T, job.Hkv, job.ks_t, job.ks_h) ||
-      !encode(f, &p.mv, job.f16, job.v, job.T, job.Hkv, job.vs_t, job.vs_h) ||
-      !encode(f, &p.mo, job.f16, job.out, job.T, job.Hq, job.os_t, job.os_h, true))
-    return cudaErrorInvalidValue;
+  // the inputs: boxes of 64 dims x 1 head x 128 tokens, zeros outside (tokens from T on); the output: 32 dims x 1 head x 32
+  const uint32_t in[3] = {64, 1, kRows}, out[3] = {32, 1, 32};
+  cudaError_t e = tensor_map_16(&p.mq, job.f16, job.q, job.T, job.Hq, job.qs_t, job.qs_h, in, false);
+  if (e == cudaSuccess) e = tensor_map_16(&p.mk, job.f16, job.k, job.T, job.Hkv, job.ks_t, job.ks_h, in, false);
+  if (e == cudaSuccess) e = tensor_map_16(&p.mv, job.f16, job.v, job.T, job.Hkv, job.vs_t, job.vs_h, in, false);
+  if (e == cudaSuccess) e = tensor_map_16(&p.mo, job.f16, job.out, job.T, job.Hq, job.os_t, job.os_h, out, true);
+  if (e != cudaSuccess) return e;
   const bool sinks = job.window > 0 && job.sinks > 0;
   const int form = 2 * sinks + job.f16;
   const auto kern = sinks ? (job.f16 ? prompt_kernel<true, true> : prompt_kernel<false, true>)

@@ -126,3 +126,38 @@ def test_evict_refuses_layers():
         over = dict(mass=0x30000000, ids=0x40000000)
         over.update(bad)
         assert evict(caches=two, masses=[ok, mass_of(**over)]) == INVALID, bad
+
+
+def observe(strides=None, m=None, **over):
+    import ctypes
+    a = dict(q=0x100000000, k=0x200000000, dtype=kvq.BF16, T=100, B=2, Hq=20, Hkv=4, cu=0x9000, rows=16, seq=0, sm=0.09, ws=0xB0000,
+             n=1 << 30, err=0xC0000)
+    a.update(over)
+    st = (ctypes.c_int64 * 4)(*strides) if strides else None
+    return L.kvq_prompt_mass(a["q"], a["k"], a["dtype"], a["T"], a["B"], a["Hq"], a["Hkv"], st, a["cu"], a["rows"], a["seq"], a["sm"],
+                             m or mass_of(mass=0x300000000, ids=0x400000000), a["ws"], a["n"], a["err"], None)
+
+
+@pytest.mark.parametrize("over,want", [
+    (dict(q=0), INVALID), (dict(k=0), INVALID), (dict(cu=0), INVALID), (dict(ws=0), INVALID), (dict(err=0), INVALID), (dict(dtype=7), INVALID),
+    (dict(dtype=kvq.F32), UNSUPPORTED), (dict(T=-1), INVALID), (dict(B=0), INVALID), (dict(B=5), INVALID), (dict(B=1025, seq=0x8000), INVALID),
+    (dict(Hq=21), INVALID), (dict(Hkv=0), INVALID), (dict(Hq=260), UNSUPPORTED), (dict(T=1 << 27), INVALID), (dict(sm=0.0), INVALID),
+    (dict(sm=float("nan")), INVALID), (dict(q=0x100000008), INVALID), (dict(ws=0xB0010), INVALID), (dict(n=8), INVALID),
+    (dict(Hkv=2), INVALID), (dict(q=0x300000000 + 64), INVALID), (dict(k=0x400000000), INVALID), (dict(seq=0x300000010), INVALID),
+    (dict(T=0), 0)])
+def test_observe_refuses(over, want):
+    assert observe(**over) == want
+
+
+def test_observe_refuses_strides_and_descriptors():
+    packed = [2560, 128, 512, 128]
+    for i in range(4):
+        for bad in (0, -8, 4, 129, 1 << 40):
+            assert observe(packed[:i] + [bad] + packed[i + 1:]) == INVALID
+    for bad in (dict(mass=0), dict(ids=0), dict(max_tokens=510), dict(mass=0x300000004), dict(ids=0x300000000)):
+        over = dict(mass=0x300000000, ids=0x400000000)
+        over.update(bad)
+        assert observe(m=mass_of(**over)) == INVALID
+    size = kvq.kvq_prompt_mass_workspace_bytes
+    assert size(100, 2, 20, 4, 16) > 0 and size(100, 2, 20, 4, 0) > 0
+    assert size(-1, 2, 20, 4, 16) == size(100, 0, 20, 4, 16) == size(100, 2, 20, 3, 16) == size(100, 2, 130, 2, 16) == 0
