@@ -14,10 +14,11 @@ from dataclasses import dataclass
 import numpy as np
 import torch
 
-from . import (HEAD_DIM, MAX_CACHES, PAGE_SIZE, alloc_fp8_ring, alloc_int4_cache, alloc_prompt_workspace, alloc_tree_workspace,
-               alloc_workspace, kvq_build_rotation, kvq_decode_attn_fp8_swa, kvq_decode_attn_int4, kvq_fold_qk,
-               kvq_fold_qk_fwht, kvq_fp8_append, kvq_prompt_attn, kvq_rotate_quant_append, kvq_tree_attn_fp8_swa,
-               kvq_tree_attn_int4, kvq_tree_commit_fp8, kvq_tree_commit_int4)
+from . import (HEAD_DIM, MAX_CACHES, PAGE_SIZE, alloc_fp8_ring, alloc_int4_cache, alloc_mass_workspace, alloc_prompt_mass_workspace,
+               alloc_prompt_workspace, alloc_token_mass, alloc_tree_workspace, alloc_workspace, kvq_build_rotation,
+               kvq_decode_attn_fp8_swa, kvq_decode_attn_int4, kvq_evict_int4, kvq_fold_qk, kvq_fold_qk_fwht, kvq_fp8_append,
+               kvq_mass_attn_int4, kvq_prompt_attn, kvq_prompt_mass, kvq_rotate_quant_append, kvq_tree_attn_fp8_swa,
+               kvq_tree_attn_int4, kvq_tree_commit_fp8, kvq_tree_commit_int4, kvq_window_attn_int4)
 
 
 @dataclass
@@ -28,6 +29,10 @@ class Int4Layer:
     Mk: torch.Tensor  # R, or the FWHT multipliers w_k = s
     R: np.ndarray
     fwht: bool = False
+    window: int = 0       # > 0: rows see the last `window` tokens and the first `sinks` (set_int4_window)
+    sinks: int = 0
+    held: dict = None     # keep_mass: what the cache's slots have gathered, and its descriptor
+    mass: object = None
 
 
 @dataclass
@@ -105,20 +110,32 @@ class DecodeStack:
                 pos = torch.arange(p0, p0 + T, dtype=torch.int32, device=self.device)
                 self.append_int4(l, kbuf[:T], vbuf[:T], seq, pos)
 
-    def decode_layer(self, l, q, ctx, out, k_new=None, v_new=None, q_rot_out=None, stream=None):
+    def decode_layer(self, l, q, ctx, out, k_new=None, v_new=None, q_rot_out=None, stream=None, positions=None):
+        """ctx: the cached tokens; positions: the tokens that the sequences have had, where some layers have evicted any
+        (those that keep mass hold ctx tokens, all others every one)."""
         L = self.layers[l]
-        if isinstance(L, Int4Layer):
+        if isinstance(L, Int4Layer) and (L.mass is not None or L.window) and q_rot_out is not None:
+            raise ValueError("q_rot_out: of layers that see their whole cache only")
+        if isinstance(L, Int4Layer) and L.mass is not None:
+            kvq_mass_attn_int4(L.cache, L.mass, L.Mq, L.Mk, q, ctx, ctx if positions is None else positions, out,
+                               self.mass_workspace, self.dev_err, k_new=k_new, v_new=v_new, stream=stream, fwht=L.fwht)
+            return
+        ctx = ctx if positions is None else positions
+        if isinstance(L, Int4Layer) and L.window:
+            kvq_window_attn_int4(L.cache, L.Mq, L.Mk, q, ctx, L.window, L.sinks, out, self.workspace, self.dev_err,
+                                 k_new=k_new, v_new=v_new, stream=stream, fwht=L.fwht)
+        elif isinstance(L, Int4Layer):
             kvq_decode_attn_int4(L.cache, L.Mq, L.Mk, q, ctx, out, self.workspace, self.dev_err, k_new=k_new,
                                  v_new=v_new, q_rot_out=q_rot_out, stream=stream, fwht=L.fwht)
         else:
             kvq_decode_attn_fp8_swa(L.ring, q, ctx, L.window, L.k_scale, L.v_scale, out, self.workspace,
                                     self.dev_err, k_new=k_new, v_new=v_new, stream=stream)
 
-    def decode_step(self, qs, ctx, outs, k_news=None, v_news=None, stream=None):
-        """One decode step over all layers: qs[l], outs[l], k_news[l], v_news[l] per layer."""
+    def decode_step(self, qs, ctx, outs, k_news=None, v_news=None, stream=None, positions=None):
+        """One decode step over all layers: qs[l], outs[l], k_news[l], v_news[l] per layer; positions as decode_layer."""
         for l in range(len(self.layers)):
             self.decode_layer(l, qs[l], ctx, outs[l], None if k_news is None else k_news[l],
-                              None if v_news is None else v_news[l], stream=stream)
+                              None if v_news is None else v_news[l], stream=stream, positions=positions)
 
     # ---- around decoding
 
@@ -139,8 +156,8 @@ class DecodeStack:
         L = self.layers[l]
         if workspace is None:  # (of 256 bytes, see kvq.h)
             workspace = self._alloc_for(stream, alloc_prompt_workspace, q.shape[0], cu_seqlens.shape[0] - 1, self.Hq, self.Hkv)
-        kvq_prompt_attn(q, k, v, cu_seqlens, out, workspace, self.dev_err,
-                        window=0 if isinstance(L, Int4Layer) else L.window, stream=stream)
+        kvq_prompt_attn(q, k, v, cu_seqlens, out, workspace, self.dev_err, window=L.window,
+                        sinks=L.sinks if isinstance(L, Int4Layer) else 0, stream=stream)
 
     def append_prompt(self, l, k, v, seq_ids, positions, stream=None):
         """Keys (pre-norm in a full-attention layer) and values of prompt tokens into layer l's cache. A ring keeps
@@ -154,6 +171,8 @@ class DecodeStack:
     def tree_layer(self, l, q, ctx, tree_mask, out, workspace, k_new=None, v_new=None, stream=None):
         """Attention of every sequence's tree of drafted tokens in layer l (workspace: alloc_tree_workspace)."""
         L = self.layers[l]
+        if isinstance(L, Int4Layer) and (L.window or L.mass is not None):
+            raise ValueError("a tree sees its layer's whole cache and keeps no mass")
         if isinstance(L, Int4Layer):
             kvq_tree_attn_int4(L.cache, L.Mq, L.Mk, q, ctx, tree_mask, out, workspace, self.dev_err, k_new=k_new,
                                v_new=v_new, stream=stream, fwht=L.fwht)
@@ -176,6 +195,43 @@ class DecodeStack:
             for i in range(0, len(layers), MAX_CACHES):  # as many layers as a call takes
                 commit(layers[i:i + MAX_CACHES], ctx, path, n_accept, self.dev_err, ctx_out=ctx_out, stream=stream)
                 ctx_out = None  # written once
+
+    # ---- caches held to a size
+
+    def set_int4_window(self, l, window, sinks=0):
+        """Rows of full-attention layer l see the last `window` tokens and the first `sinks`, in prompts and decode steps
+        (window 0: all again)."""
+        L = self.layers[l]
+        if not isinstance(L, Int4Layer) or L.mass is not None or window < 0 or sinks < 0:
+            raise ValueError("a window is of an int4 layer that keeps no mass, its sizes not negative")
+        L.window, L.sinks = window, sinks
+
+    def keep_mass(self, layers=None):
+        """From here on the int4 layers `layers` (None: all without a window) keep what their slots gather, and can evict."""
+        layers = [l for l in self.int4_layers() if not self.layers[l].window] if layers is None else layers
+        if any(not isinstance(self.layers[l], Int4Layer) or self.layers[l].window for l in layers):
+            raise ValueError("mass is kept by int4 layers without a window")
+        for l in layers:
+            self.layers[l].held, self.layers[l].mass = alloc_token_mass(self.B, self.Hkv, self.max_pages, self.device)
+        self.mass_workspace = alloc_mass_workspace(self.B, self.Hq, self.Hkv, self.max_pages * PAGE_SIZE, self.device)
+
+    def mass_layers(self):
+        return [l for l in self.int4_layers() if self.layers[l].mass is not None]
+
+    def observe_prompt(self, l, q, k, cu_seqlens, rows, seq_ids=None, workspace=None, stream=None):
+        """Layer l's mass starts from the weights of each prompt's last `rows` rows; q and k as prompt_layer takes them."""
+        if workspace is None:
+            workspace = self._alloc_for(stream, alloc_prompt_mass_workspace, q.shape[0], cu_seqlens.shape[0] - 1, self.Hq, self.Hkv, rows)
+        kvq_prompt_mass(q, k, cu_seqlens, rows, self.layers[l].mass, workspace, self.dev_err, seq_ids=seq_ids, stream=stream)
+
+    def evict(self, ctx, seen, budget, sinks, recent, ctx_out, stream=None):
+        """Every layer that keeps mass evicts down to `budget` tokens a sequence and KV head (kvq_evict_int4); ctx_out: the
+        new lengths."""
+        layers = [self.layers[l] for l in self.mass_layers()]
+        for i in range(0, len(layers), MAX_CACHES):  # as many layers as a call takes
+            some = layers[i:i + MAX_CACHES]
+            kvq_evict_int4([L.cache for L in some], [L.mass for L in some], ctx, seen, budget, sinks, recent, self.dev_err,
+                           ctx_out=None if i else ctx_out, stream=stream)
 
     def read_error(self) -> int:
         return int(self.dev_err.item())
