@@ -93,6 +93,7 @@ kvq_status window_impl(const kvq_int4_cache* cache, const float* Mq, const float
   // positions end at 2^30: wider windows and more first tokens mean the same
   a.window = std::min(window, 1 << 30);
   a.sinks = std::min(sinks, 1 << 30);
+  a.append = k_new != nullptr;
   return from_cuda(kvq::launch_attention(a, (cudaStream_t)stream));
 }
 
@@ -130,9 +131,9 @@ kvq_status mass_impl(const kvq_int4_cache* cache, const kvq_token_mass* mass, co
   st = prologue(cache, Mq, Mk, q, dtype, B, 1, num_q_heads, ctx_len, k_new, v_new, eps, workspace, dev_err, stream, fwht);
   if (st != KVQ_OK) return st;
   kvq::AttnJob a = attn_job(cache, B, 1, num_q_heads, ctx_len, sm_scale, out, out_dtype, workspace, dev_err);
-  uint8_t* at = reinterpret_cast<uint8_t*>(a.partials) + kvq::workspace_partials_bytes(B, 1, num_q_heads, a.Hkv);
-  a.stats = reinterpret_cast<float2*>(at);
-  a.scores = reinterpret_cast<float*>(at + align_up(8 * (size_t)B * num_q_heads));
+  a.append = k_new != nullptr;
+  a.scores = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(a.partials) +
+                                      kvq::workspace_mass_partials_bytes(B, num_q_heads, a.Hkv));
   a.mass = mass->mass;
   a.ids = mass->ids;
   a.mass_len = mass->max_tokens;
@@ -163,11 +164,10 @@ kvq_status kvq_window_attn_int4_fwht(const kvq_int4_cache* cache, const float* w
 }
 
 size_t kvq_mass_workspace_bytes(int B, int num_q_heads, int num_kv_heads, int max_pages_per_seq) {
-  const size_t decode = kvq_decode_workspace_bytes(B, 1, num_q_heads, num_kv_heads);
-  if (decode == 0 || max_pages_per_seq < 1 || max_pages_per_seq > (1 << 24) ||
+  if (kvq_decode_workspace_bytes(B, 1, num_q_heads, num_kv_heads) == 0 || max_pages_per_seq < 1 || max_pages_per_seq > (1 << 24) ||
       (long long)B * num_kv_heads * max_pages_per_seq > (1LL << 31))
     return 0;
-  return decode + align_up(8 * (size_t)B * num_q_heads) +
+  return kvq::workspace_qrot_bytes(B, 1, num_q_heads) + kvq::workspace_mass_partials_bytes(B, num_q_heads, num_kv_heads) +
          align_up(4 * (size_t)B * num_q_heads * KVQ_PAGE_SIZE * max_pages_per_seq);
 }
 

@@ -33,8 +33,7 @@
 //           between are neither read nor counted in the split.
 //   mass    one row per query head. Its weights are added to what every cached token has gathered, so scores are wanted
 //           to fp32: q~ enters as two fp16 parts (22 bits), a second chain of products over the same codes. The scores go
-//           to the workspace, [segment][row][position]; when the join knows a row's sum, mass_kernel turns them into
-//           weights. (Reading the keys a second time instead would move 68 bytes a token and head, scores 40 at 5 rows.)
+//           to the workspace, [segment][row][position]; mass_kernel joins the partials and turns the scores into weights. (Reading the keys a second time instead would move 68 bytes a token and head, scores 40 at 5 rows.)
 // (64 sequences of 5,000-16,384 tokens: window 4,096 with 64 first tokens 44 us; mass 97 us, of which the floor is 21 and 47.)
 
 #include <algorithm>
@@ -112,10 +111,12 @@ struct AttnParams {
   // TREE: bit j of word [b][r]: query row r of sequence b attends to the row at position ctx[b] + j
   const uint64_t* tree_mask;
   int out_bf16;  // forms other than the verify block: out holds bf16
+  int by_group;  // a part a token group (see parts_of):
+  int max_parts; // what the workspace's partials allow,
+  int append;    // whether the prologue appends new rows
   int sinks;     // window form: first tokens that stay visible
   // mass form
   float* scores;     // [B * Hkv][R][max_pages * 64], in powers of two
-  float2* stats;     // [B * Hkv][R]: base and sum of the weights against it
   float* mass;       // [.][Hkv][mass_len]
   int32_t* ids;
   int mass_len;
@@ -256,6 +257,18 @@ __device__ __forceinline__ void decode_page(const int* pre, int B, int Hkv, long
   lp = (int)rem;
 }
 
+// Parts that the P pages of a call are split into: one a CTA, whose token groups join their states on chip, or (by_group) one a
+// token group, each with partials of its own: the mass form, and windows with more than one row tile. What a segment's end costs
+// a CTA with several tiles (the groups' states go through shared memory one after the other, about 5 us with three) is more
+// there than what the join of more partials does: 16 verify blocks of 20 rows, windows of 2,000, short and long: 48 us by
+// CTA, 34 by group. With one tile and windows it is the other way round, 44 us by CTA, 52 by group (64 sequences, windows of
+// 4,096), because the call's workspace has partials for 1,024 parts and 1,216 groups fit the GPU. Part u is that of token
+// group u / n_cta of CTA u mod n_cta, so few parts still spread over the SMs.
+__host__ __device__ constexpr bool by_group(int form, int nt) { return form == kMass || (form == kWindow && nt > 1); }
+__device__ __forceinline__ int parts_of(const AttnParams& p, long long P) {
+  return (int)min((long long)(p.by_group ? min(p.n_cta * p.nkg, p.max_parts) : p.n_cta), P);
+}
+
 // CTA whose page range [floor(i P / n), floor((i+1) P / n)) contains page pg (n <= P).
 __device__ __forceinline__ long long cta_of(long long pg, long long P, int n) { return ((pg + 1) * n - 1) / P; }
 
@@ -382,15 +395,87 @@ __device__ __forceinline__ void produce_pages(const AttnParams& p, const int* pr
   }
 }
 
+// Producer warp of forms with a part a token group: the CTA's parts are copied side by side, page i of every token group's part before
+// page i + 1 of any. Token group w has the stages w, w + nkg, ... to itself, `per` of them. Copies start before the prologue,
+// the grid before this one, is done: it writes no page but those of new rows, and all grids before it have completed.
+template <int FORM>
+__device__ __forceinline__ void produce_parts(const AttnParams& p, const int* pre, uint8_t* stages, uint64_t* full,
+                                              uint64_t* empty, volatile int* valid, volatile int* flags, long long P,
+                                              int parts, int lane) {
+  const uint64_t pol = policy_evict_first();
+  const int nkg = p.nkg, per = p.nstages / nkg;
+  auto start_of = [&](int w) { return P * (w * p.n_cta + (int)blockIdx.x) / parts; };
+  auto pages_of = [&](int w) {
+    const int u = w * p.n_cta + (int)blockIdx.x;
+    return u < parts ? (int)(P * (u + 1) / parts - start_of(w)) : 0;
+  };
+  const int rounds = __reduce_max_sync(0xffffffffu, lane < nkg ? pages_of(lane) : 0);
+  bool waited = false;
+  int done = 0;  // (round, token group) pairs gone through
+  for (int base = 0; base < rounds * nkg; base += 32) {
+    const int mine = base + lane, i = mine / nkg, w = mine - i * nkg;
+    long long src = -2;  // byte offset of the page's block; -1 = invalid page, -2 = none
+    bool fresh = false;  // the page gets new rows
+    if (i < pages_of(w)) {
+      int b, h, lp, np;
+      decode_page(pre, p.B, p.Hkv, start_of(w) + i, b, h, lp, np);
+      bool bad = false;
+      const int ctxb = eff_ctx(p, b, bad, 0);
+      if (FORM == kWindow) lp = WindowPages(p, ctxb).page(lp);
+      fresh = p.append && (lp + 1) * kPage > ctxb;
+      const int phys = __ldcg(p.block_table + (size_t)b * p.max_pages + lp);
+      src = -1;
+      if (phys >= 0 && phys < p.num_pages) src = ((long long)phys * p.Hkv + h) * kStage4;
+      else set_err(p.dev_err, KVQ_DEVERR_PAGE);
+    }
+    const int n = min(32, rounds * nkg - base);
+    const uint32_t written = __ballot_sync(0xffffffffu, fresh);
+    int halt = 0;
+    for (int j = 0; j < n; ++j) {
+      if (!waited && (written >> j & 1u)) {
+        griddep_wait();
+        waited = true;
+      }
+      const long long sj = __shfl_sync(0xffffffffu, src, j);
+      const int ij = (base + j) / nkg, f = ij / per, s = base + j - ij * nkg + nkg * (ij - f * per);
+      if (lane == 0 && !halt && sj > -2) {
+        if (f > 0 && !mbar_wait_bounded(&empty[s], (f - 1) & 1, p.stage_wait_ns)) {
+          set_err(p.dev_err, KVQ_DEVERR_TIMEOUT);
+          flags[0] = 1;
+          halt = 1;
+        } else if (sj < 0) {
+          valid[s] = 0;
+          mbar_arrive(&full[s]);
+        } else {
+          valid[s] = 1;
+          mbar_arrive_expect_tx(&full[s], kStage4);
+          bulk_g2s(stages + (size_t)s * kStage4, p.blocks + sj, kStage4, &full[s], pol);
+        }
+      }
+      if (!halt) done = base + j + 1;
+    }
+    if (__shfl_sync(0xffffffffu, halt | flags[0], 0)) break;
+  }
+  // Do not retire while copies into this CTA's shared memory may be in flight (lane w: those of token group w).
+  done = __shfl_sync(0xffffffffu, done, 0);
+  if (lane < nkg) {
+    const int copied = min(pages_of(lane), done / nkg + (lane < done % nkg));
+    for (int r = 0; r < per && r < copied; ++r)
+      if (!mbar_wait_bounded(&full[lane + nkg * r], ((copied - 1 - r) / per) & 1)) set_err(p.dev_err, KVQ_DEVERR_TIMEOUT);
+  }
+}
+
 // Register caps: the int4 single-tile CTA (5 warps) must fit twice per SM, i.e. 3 warps per
 // SM sub-partition -> at most 170 registers.
 template <int FMT, int NT, int FORM>
 __global__ void __maxnreg__(NT == 1 ? (FMT == 0 ? KVQ_INT4_MAXREG : 184) : 255)
     attn_kernel(const AttnParams p) {
   constexpr bool TREE = FORM != kVerify;
+  constexpr bool PARTS = by_group(FORM, NT);
   extern __shared__ __align__(128) uint8_t smem[];
   constexpr int kStage = FMT == 0 ? kStage4 : kStage8;
   constexpr int MTU = NT == 1 && FORM != kMass ? 4 : 2;  // 16-token m-tiles per online-softmax update
+  const uint64_t keep = FORM == kMass ? policy_evict_last() : 0ull;  // the scores are read again, the pages are not
   const SmemLayout L(FMT, p.nstages, p.B, p.nkg, p.rows_pad);
   uint8_t* stages = smem + L.stages;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L.full);
@@ -416,19 +501,22 @@ __global__ void __maxnreg__(NT == 1 ? (FMT == 0 ? KVQ_INT4_MAXREG : 184) : 255)
   }
   fence_barrier_init();
   __syncthreads();
-  griddep_wait();
-  griddep_launch_dependents();
+  if (!PARTS || warp != nwc) {  // (their producer waits when it has to, see there)
+    griddep_wait();
+    griddep_launch_dependents();
+  }
 
   if (blockIdx.x == 0 && threadIdx.x == 0 && flags[1]) set_err(p.dev_err, KVQ_DEVERR_POS);
   const long long P = (long long)p.Hkv * pre[p.B];
-  const int n_eff = (int)min((long long)p.n_cta, P);
+  const int n_eff = parts_of(p, P);
   if ((int)blockIdx.x >= n_eff) return;
-  const long long p0 = (long long)blockIdx.x * P / n_eff;
-  const long long p1 = (long long)(blockIdx.x + 1) * P / n_eff;
-
   // ------------------------------------------------------------ producer warp
   if (warp == nwc) {
-    produce_pages<FMT, FORM>(p, pre, stages, full, empty, valid, flags, nst, p0, p1, lane);
+    if constexpr (PARTS)
+      produce_parts<FORM>(p, pre, stages, full, empty, valid, flags, P, n_eff, lane);
+    else
+      produce_pages<FMT, FORM>(p, pre, stages, full, empty, valid, flags, nst, (long long)blockIdx.x * P / n_eff,
+                         (long long)(blockIdx.x + 1) * P / n_eff, lane);
     return;
   }
 
@@ -436,6 +524,10 @@ __global__ void __maxnreg__(NT == 1 ? (FMT == 0 ? KVQ_INT4_MAXREG : 184) : 255)
   const int kg = warp / p.ntg, tg = warp - (warp / p.ntg) * p.ntg;
   const int g = lane >> 2, t = lane & 3;
   const int R = p.R, G = p.G;
+  const int part = PARTS ? kg * p.n_cta + (int)blockIdx.x : (int)blockIdx.x;
+  if (PARTS && part >= n_eff) return;
+  const long long p0 = (long long)part * P / n_eff;
+  const long long p1 = (long long)(part + 1) * P / n_eff;
 
   long long seg_start = p0;
   while (seg_start < p1) {
@@ -572,10 +664,10 @@ __global__ void __maxnreg__(NT == 1 ? (FMT == 0 ? KVQ_INT4_MAXREG : 184) : 255)
     const int slot_last = FMT == 1 ? p_last % p.cap : 0;
 
     const int k_beg = (int)(seg_start - p0), k_end = (int)(seg_end - p0);
-    for (int k = k_beg + ((kg - k_beg % p.nkg + p.nkg) % p.nkg); k < k_end; k += p.nkg) {
+    for (int k = PARTS ? k_beg : k_beg + ((kg - k_beg % p.nkg + p.nkg) % p.nkg); k < k_end; k += PARTS ? 1 : p.nkg) {
       const long long pg = p0 + k;
-      const int s = k % nst;
-      const int f = k / nst;
+      const int f = PARTS ? k / (nst / p.nkg) : k / nst;
+      const int s = PARTS ? kg + p.nkg * (k - f * (nst / p.nkg)) : k % nst;
       const bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(&full[s], f & 1, p.stage_wait_ns));
       if (!ok) {
         if (lane == 0) set_err(p.dev_err, KVQ_DEVERR_TIMEOUT);
@@ -748,7 +840,7 @@ __global__ void __maxnreg__(NT == 1 ? (FMT == 0 ? KVQ_INT4_MAXREG : 184) : 255)
                   for (int u = 0; u < MTU; ++u)
 #pragma unroll
                     for (int hh = 0; hh < 2; ++hh)
-                      srow[nt][j][(size_t)lp * kPage + 16 * (mt0 + u) + g + 8 * hh] = sc[nt][u][2 * hh + j] + muse[nt][j];
+                      st_keep(srow[nt][j] + (size_t)lp * kPage + 16 * (mt0 + u) + g + 8 * hh, sc[nt][u][2 * hh + j] + muse[nt][j], keep);
           }
 
           // ---- online softmax update
@@ -902,7 +994,7 @@ __global__ void __maxnreg__(NT == 1 ? (FMT == 0 ? KVQ_INT4_MAXREG : 184) : 255)
     // the last token group down to group 0 through one shared slot per tile group; group 0 then
     // reduces l and the offset term over its lanes and writes the CTA partial.
     float* mslot = red + (size_t)tg * NT * kMergeFloats * 32;
-    for (int kk = p.nkg - 1; kk >= 1; --kk) {
+    for (int kk = PARTS ? 0 : p.nkg - 1; kk >= 1; --kk) {
       if (kg == kk) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -943,8 +1035,8 @@ __global__ void __maxnreg__(NT == 1 ? (FMT == 0 ? KVQ_INT4_MAXREG : 184) : 255)
       }
       named_barrier(1, nwc * 32);
     }
-    if (kg == 0) {
-      float* dstp = p.partials + ((size_t)(blockIdx.x + seg) * R) * kPartialStride;
+    if (PARTS || kg == 0) {
+      float* dstp = p.partials + ((size_t)(part + seg) * R) * kPartialStride;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const int tile = tg * NT + nt;
@@ -1761,9 +1853,147 @@ constexpr int kCombWarps = 8;
 constexpr int kCombChunkWarp = 4;
 constexpr int kCombChunkBlock = 8;
 
+// Item `item` (segment and row) by one warp.
+template <int FORM>
+__device__ __forceinline__ void combine_by_warp(const AttnParams& p, const int* cpre, int item, int lane, long long P, int n_eff) {
+  constexpr bool TREE = FORM != kVerify;
+  constexpr int kChunk = FORM == kWindow ? 2 * kCombChunkWarp : kCombChunkWarp;  // a part a token group: more partials
+  const int R = p.R;
+  const int seg = item / R, row = item - seg * R;
+  const int b = seg / p.Hkv, h = seg - (seg / p.Hkv) * p.Hkv;
+  const int np = cpre[b + 1] - cpre[b];
+  const long long first_pg = (long long)p.Hkv * cpre[b] + (long long)h * np;
+  const int c0 = (int)cta_of(first_pg, P, n_eff), c1 = (int)cta_of(first_pg + np - 1, P, n_eff);
+  float M = -INFINITY, lsum = 0.0f;
+  float2 alo = make_float2(0.0f, 0.0f), ahi = make_float2(0.0f, 0.0f);
+  for (int cb = c0; cb <= c1; cb += kChunk) {
+    float mv[kChunk], lv[kChunk];
+    float2 xl[kChunk], xh[kChunk];
+#pragma unroll
+    for (int k = 0; k < kChunk; ++k) {
+      if (cb + k <= c1) {
+        const float* src = p.partials + ((size_t)(cb + k + seg) * R + row) * kPartialStride;
+        mv[k] = src[0];
+        lv[k] = src[1];
+        xl[k] = *reinterpret_cast<const float2*>(src + 2 + 2 * lane);
+        xh[k] = *reinterpret_cast<const float2*>(src + 66 + 2 * lane);
+      } else {
+        mv[k] = -INFINITY;
+        lv[k] = 0.0f;
+        xl[k] = xh[k] = make_float2(0.0f, 0.0f);
+      }
+    }
+    float Mc = mv[0];
+#pragma unroll
+    for (int k = 1; k < kChunk; ++k) Mc = fmaxf(Mc, mv[k]);
+    if (Mc == -INFINITY) {  // nothing visible in this chunk, or scores that are NaN: their sum is kept
+      if (TREE) {
+#pragma unroll
+        for (int k = 0; k < kChunk; ++k) lsum += lv[k];
+      }
+      continue;
+    }
+    float lc = 0.0f;
+    float2 cl = make_float2(0.0f, 0.0f), ch = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int k = 0; k < kChunk; ++k) {
+      const float w = fast_exp2(mv[k] - Mc);
+      lc += w * lv[k];
+      cl.x += w * xl[k].x;
+      cl.y += w * xl[k].y;
+      ch.x += w * xh[k].x;
+      ch.y += w * xh[k].y;
+    }
+    if (M == -INFINITY) {
+      M = Mc;
+      lsum = lc;
+      alo = cl;
+      ahi = ch;
+    } else {
+      const float Mn = fmaxf(M, Mc);
+      const float so = fast_exp2(M - Mn), sc = fast_exp2(Mc - Mn);
+      lsum = lsum * so + lc * sc;
+      alo.x = alo.x * so + cl.x * sc;
+      alo.y = alo.y * so + cl.y * sc;
+      ahi.x = ahi.x * so + ch.x * sc;
+      ahi.y = ahi.y * so + ch.y * sc;
+      M = Mn;
+    }
+  }
+  const int r = row / p.G, gi = row - (row / p.G) * p.G;
+  const size_t at = (((size_t)b * p.S + r) * p.Hq + h * p.G + gi) * kD + 2 * lane;
+  store2<TREE>(p, at, alo.x, alo.y, lsum);
+  store2<TREE>(p, at + 64, ahi.x, ahi.y, lsum);
+}
+
+// The same by 128 threads, thread d for dim d.
+template <int FORM>
+__device__ __forceinline__ void combine_by_block(const AttnParams& p, const int* cpre, int item, int d, long long P, int n_eff) {
+  constexpr bool TREE = FORM != kVerify;
+  const int R = p.R;
+  const int seg = item / R, row = item - seg * R;
+  const int b = seg / p.Hkv, h = seg - (seg / p.Hkv) * p.Hkv;
+  const int np = cpre[b + 1] - cpre[b];
+  const long long first_pg = (long long)p.Hkv * cpre[b] + (long long)h * np;
+  const int c0 = (int)cta_of(first_pg, P, n_eff), c1 = (int)cta_of(first_pg + np - 1, P, n_eff);
+  float M = -INFINITY, lsum = 0.0f, a = 0.0f;
+  for (int cb = c0; cb <= c1; cb += kCombChunkBlock) {
+    float mv[kCombChunkBlock], lv[kCombChunkBlock], av[kCombChunkBlock];
+#pragma unroll
+    for (int k = 0; k < kCombChunkBlock; ++k) {
+      if (cb + k <= c1) {
+        const float* src = p.partials + ((size_t)(cb + k + seg) * R + row) * kPartialStride;
+        mv[k] = src[0];
+        lv[k] = src[1];
+        av[k] = src[2 + d];
+      } else {
+        mv[k] = -INFINITY;
+        lv[k] = 0.0f;
+        av[k] = 0.0f;
+      }
+    }
+    float Mc = mv[0];
+#pragma unroll
+    for (int k = 1; k < kCombChunkBlock; ++k) Mc = fmaxf(Mc, mv[k]);
+    if (Mc == -INFINITY) {  // nothing visible in this chunk, or scores that are NaN: their sum is kept
+      if (TREE) {
+#pragma unroll
+        for (int k = 0; k < kCombChunkBlock; ++k) lsum += lv[k];
+      }
+      continue;
+    }
+    float lc = 0.0f, ac = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kCombChunkBlock; ++k) {
+      const float w = fast_exp2(mv[k] - Mc);
+      lc += w * lv[k];
+      ac += w * av[k];
+    }
+    if (M == -INFINITY) {
+      M = Mc;
+      lsum = lc;
+      a = ac;
+    } else {
+      const float Mn = fmaxf(M, Mc);
+      const float so = fast_exp2(M - Mn), sc = fast_exp2(Mc - Mn);
+      lsum = lsum * so + lc * sc;
+      a = a * so + ac * sc;
+      M = Mn;
+    }
+  }
+  const int r = row / p.G, gi = row - (row / p.G) * p.G;
+  const size_t at = (((size_t)b * p.S + r) * p.Hq + h * p.G + gi) * kD + d;
+  if (TREE) {
+    const float x = lsum == 0.0f ? 0.0f : a / lsum;  // a row that saw nothing: 0
+    if (p.out_bf16) reinterpret_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(x);
+    else p.out[at] = x;
+  } else {
+    p.out[at] = a / lsum;
+  }
+}
+
 template <int FMT, int FORM>
 __global__ void __launch_bounds__(kCombWarps * 32, 4) combine_rows_kernel(const AttnParams p) {
-  constexpr bool TREE = FORM != kVerify;
   extern __shared__ __align__(16) int cpre[];
   volatile int* flags = cpre + p.B + 1;
   build_prefix<FORM>(p, FMT, cpre, flags);
@@ -1771,207 +2001,193 @@ __global__ void __launch_bounds__(kCombWarps * 32, 4) combine_rows_kernel(const 
   griddep_launch_dependents();
   __syncthreads();
   const int lane = threadIdx.x & 31;
-  const int R = p.R;
   const long long P = (long long)p.Hkv * cpre[p.B];
-  const int n_eff = (int)min((long long)p.n_cta, P);
-  const int n_items = p.B * p.Hkv * R;
-  for (int item = blockIdx.x * kCombWarps + (threadIdx.x >> 5); item < n_items; item += gridDim.x * kCombWarps) {
-    const int seg = item / R, row = item - seg * R;
-    const int b = seg / p.Hkv, h = seg - (seg / p.Hkv) * p.Hkv;
-    const int np = cpre[b + 1] - cpre[b];
-    const long long first_pg = (long long)p.Hkv * cpre[b] + (long long)h * np;
-    const int c0 = (int)cta_of(first_pg, P, n_eff), c1 = (int)cta_of(first_pg + np - 1, P, n_eff);
-    float M = -INFINITY, lsum = 0.0f;
-    float2 alo = make_float2(0.0f, 0.0f), ahi = make_float2(0.0f, 0.0f);
-    for (int cb = c0; cb <= c1; cb += kCombChunkWarp) {
-      float mv[kCombChunkWarp], lv[kCombChunkWarp];
-      float2 xl[kCombChunkWarp], xh[kCombChunkWarp];
-#pragma unroll
-      for (int k = 0; k < kCombChunkWarp; ++k) {
-        if (cb + k <= c1) {
-          const float* src = p.partials + ((size_t)(cb + k + seg) * R + row) * kPartialStride;
-          mv[k] = src[0];
-          lv[k] = src[1];
-          xl[k] = *reinterpret_cast<const float2*>(src + 2 + 2 * lane);
-          xh[k] = *reinterpret_cast<const float2*>(src + 66 + 2 * lane);
-        } else {
-          mv[k] = -INFINITY;
-          lv[k] = 0.0f;
-          xl[k] = xh[k] = make_float2(0.0f, 0.0f);
-        }
-      }
-      float Mc = mv[0];
-#pragma unroll
-      for (int k = 1; k < kCombChunkWarp; ++k) Mc = fmaxf(Mc, mv[k]);
-      if (Mc == -INFINITY) {  // nothing visible in this chunk, or scores that are NaN: their sum is kept
-        if (TREE) {
-#pragma unroll
-          for (int k = 0; k < kCombChunkWarp; ++k) lsum += lv[k];
-        }
-        continue;
-      }
-      float lc = 0.0f;
-      float2 cl = make_float2(0.0f, 0.0f), ch = make_float2(0.0f, 0.0f);
-#pragma unroll
-      for (int k = 0; k < kCombChunkWarp; ++k) {
-        const float w = fast_exp2(mv[k] - Mc);
-        lc += w * lv[k];
-        cl.x += w * xl[k].x;
-        cl.y += w * xl[k].y;
-        ch.x += w * xh[k].x;
-        ch.y += w * xh[k].y;
-      }
-      if (M == -INFINITY) {
-        M = Mc;
-        lsum = lc;
-        alo = cl;
-        ahi = ch;
-      } else {
-        const float Mn = fmaxf(M, Mc);
-        const float so = fast_exp2(M - Mn), sc = fast_exp2(Mc - Mn);
-        lsum = lsum * so + lc * sc;
-        alo.x = alo.x * so + cl.x * sc;
-        alo.y = alo.y * so + cl.y * sc;
-        ahi.x = ahi.x * so + ch.x * sc;
-        ahi.y = ahi.y * so + ch.y * sc;
-        M = Mn;
-      }
-    }
-    const int r = row / p.G, gi = row - (row / p.G) * p.G;
-    const size_t at = (((size_t)b * p.S + r) * p.Hq + h * p.G + gi) * kD + 2 * lane;
-    store2<TREE>(p, at, alo.x, alo.y, lsum);
-    store2<TREE>(p, at + 64, ahi.x, ahi.y, lsum);
-    if (FORM == kMass && lane == 0) p.stats[item] = make_float2(M, lsum);
-  }
+  const int n_eff = parts_of(p, P);
+  const int n_items = p.B * p.Hkv * p.R;
+  for (int item = blockIdx.x * kCombWarps + (threadIdx.x >> 5); item < n_items; item += gridDim.x * kCombWarps)
+    combine_by_warp<FORM>(p, cpre, item, lane, P, n_eff);
 }
 
 template <int FMT, int FORM>
 __global__ void __launch_bounds__(128, 4) combine_kernel(const AttnParams p) {
-  constexpr bool TREE = FORM != kVerify;
   extern __shared__ __align__(16) int cpre[];
   volatile int* flags = cpre + p.B + 1;
   build_prefix<FORM>(p, FMT, cpre, flags);
   griddep_wait();
   griddep_launch_dependents();
   __syncthreads();
-  const int R = p.R;
-  const int n_items = p.B * p.Hkv * R;
+  const int n_items = p.B * p.Hkv * p.R;
   const long long P = (long long)p.Hkv * cpre[p.B];
-  const int n_eff = (int)min((long long)p.n_cta, P);
-  const int d = threadIdx.x;
-  for (int item = blockIdx.x; item < n_items; item += gridDim.x) {
-    const int seg = item / R, row = item - seg * R;
-    const int b = seg / p.Hkv, h = seg - (seg / p.Hkv) * p.Hkv;
-    const int np = cpre[b + 1] - cpre[b];
-    const long long first_pg = (long long)p.Hkv * cpre[b] + (long long)h * np;
-    const int c0 = (int)cta_of(first_pg, P, n_eff), c1 = (int)cta_of(first_pg + np - 1, P, n_eff);
-    float M = -INFINITY, lsum = 0.0f, a = 0.0f;
-    for (int cb = c0; cb <= c1; cb += kCombChunkBlock) {
-      float mv[kCombChunkBlock], lv[kCombChunkBlock], av[kCombChunkBlock];
-#pragma unroll
-      for (int k = 0; k < kCombChunkBlock; ++k) {
-        if (cb + k <= c1) {
-          const float* src = p.partials + ((size_t)(cb + k + seg) * R + row) * kPartialStride;
-          mv[k] = src[0];
-          lv[k] = src[1];
-          av[k] = src[2 + d];
-        } else {
-          mv[k] = -INFINITY;
-          lv[k] = 0.0f;
-          av[k] = 0.0f;
-        }
-      }
-      float Mc = mv[0];
-#pragma unroll
-      for (int k = 1; k < kCombChunkBlock; ++k) Mc = fmaxf(Mc, mv[k]);
-      if (Mc == -INFINITY) {  // nothing visible in this chunk, or scores that are NaN: their sum is kept
-        if (TREE) {
-#pragma unroll
-          for (int k = 0; k < kCombChunkBlock; ++k) lsum += lv[k];
-        }
-        continue;
-      }
-      float lc = 0.0f, ac = 0.0f;
-#pragma unroll
-      for (int k = 0; k < kCombChunkBlock; ++k) {
-        const float w = fast_exp2(mv[k] - Mc);
-        lc += w * lv[k];
-        ac += w * av[k];
-      }
-      if (M == -INFINITY) {
-        M = Mc;
-        lsum = lc;
-        a = ac;
-      } else {
-        const float Mn = fmaxf(M, Mc);
-        const float so = fast_exp2(M - Mn), sc = fast_exp2(Mc - Mn);
-        lsum = lsum * so + lc * sc;
-        a = a * so + ac * sc;
-        M = Mn;
-      }
-    }
-    const int r = row / p.G, gi = row - (row / p.G) * p.G;
-    const size_t at = (((size_t)b * p.S + r) * p.Hq + h * p.G + gi) * kD + d;
-    if (FORM == kMass && d == 0) p.stats[item] = make_float2(M, lsum);
-    if (TREE) {
-      const float x = lsum == 0.0f ? 0.0f : a / lsum;  // a row that saw nothing: 0
-      if (p.out_bf16) reinterpret_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(x);
-      else p.out[at] = x;
-    } else {
-      p.out[at] = a / lsum;
-    }
-  }
+  const int n_eff = parts_of(p, P);
+  for (int item = blockIdx.x; item < n_items; item += gridDim.x) combine_by_block<FORM>(p, cpre, item, threadIdx.x, P, n_eff);
 }
 
-// Mass form, after the join: the row's scores become weights w = 2^(score - base) / sum, and their sum over the rows of a KV
-// head is added to what the token has gathered; the new token's place is set, with its number. Four tokens a thread, rows in
+// Mass form: the masses and the join of the partials, in one launch. The call's pages are split evenly over the blocks: a
+// segment's bases and sums are joined (two floats a partial), the scores become weights w = 2^(score - base) / sum, and
+// their sum over the rows of the KV head is added to what the token has gathered; the new token's place is set, with its
+// number. Four tokens a thread, up to eight rows' scores in flight (the first ones while the sums are joined), rows added in
 // ascending order, so a token's sum does not depend on timing. A row without weights (nothing visible, or a query that is
 // not finite) adds nothing: one bad step may not make the whole cache's history NaN. Tokens of a page outside the pool have
-// no scores and are passed over. Bound by memory: 4 bytes a row and 8 a token.
+// no scores and are passed over. Then outputs, an item (segment and row) a block: the factors of its partials first, so that
+// the sums over them are loads that wait for nothing. Items go to the blocks from the last one on, which have no pages where
+// there are few. Bound by memory: 4 bytes a row and 8 a token, and by the latency of what depends on what.
 constexpr int kMassThreads = 256;
-constexpr int kMassTokens = 4 * kMassThreads;
+constexpr int kMassRows = 8;   // rows in flight
+constexpr int kMassPages = 8;  // pages of a block, at least
 
-__global__ void __launch_bounds__(kMassThreads) mass_kernel(const AttnParams p) {
-  const int chunks = (p.max_pages * kPage + kMassTokens - 1) / kMassTokens;  // of a segment
-  const int seg = blockIdx.x / chunks, b = seg / p.Hkv;
-  const int R = p.R;
-  bool bad = false;
-  const int ctxb = eff_ctx(p, b, bad, 0);
-  const int pos = (blockIdx.x - seg * chunks) * kMassTokens + 4 * threadIdx.x;
+__global__ void __launch_bounds__(kMassThreads, 4) mass_kernel(const AttnParams p) {
+  extern __shared__ __align__(16) int cpre[];
+  volatile int* flags = cpre + p.B + 1;
+  __shared__ float2 stats[kMaxRows];  // base and inverse sum, 0 for a row without weights
+  __shared__ float factor[kMassMaxParts], half[kD], red[2][kMassThreads / 32];
+  build_prefix<kMass>(p, 0, cpre, flags);
   griddep_wait();
   griddep_launch_dependents();
-  if (pos > ctxb) return;
-  const int phys = p.block_table[(size_t)b * p.max_pages + pos / kPage];
-  if (phys < 0 || phys >= p.num_pages) return;
+  __syncthreads();
+  const int R = p.R, t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  const long long P = (long long)p.Hkv * cpre[p.B];
+  const int n_eff = parts_of(p, P);
+  const int blocks = (int)min((long long)gridDim.x, (P + kMassPages - 1) / kMassPages), block = blockIdx.x;
+  const long long p0 = block < blocks ? P * block / blocks : 0, p1 = block < blocks ? P * (block + 1) / blocks : 0;
   const size_t row_len = (size_t)p.max_pages * kPage;
-  const float* src = p.scores + (size_t)seg * R * row_len + pos;
-  float w[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int r = 0; r < R; ++r) {
-    const float2 st = p.stats[(size_t)seg * R + r];
-    if (!(st.y > 0.0f && st.y < INFINITY)) continue;  // (uniform over the block)
-    const float4 x = *reinterpret_cast<const float4*>(src + r * row_len);
-    const float inv = 1.0f / st.y;
-    w[0] = fmaf(fast_exp2(x.x - st.x), inv, w[0]);
-    w[1] = fmaf(fast_exp2(x.y - st.x), inv, w[1]);
-    w[2] = fmaf(fast_exp2(x.z - st.x), inv, w[2]);
-    w[3] = fmaf(fast_exp2(x.w - st.x), inv, w[3]);
-  }
-  float* const m = p.mass + (size_t)seg * p.mass_len + pos;
-  if (pos + 3 < ctxb) {
-    float4 old = *reinterpret_cast<const float4*>(m);
-    old.x += w[0];
-    old.y += w[1];
-    old.z += w[2];
-    old.w += w[3];
-    *reinterpret_cast<float4*>(m) = old;
-  } else {
+  for (long long at = p0; at < p1;) {
+    int b, h, lp0, np;
+    decode_page(cpre, p.B, p.Hkv, at, b, h, lp0, np);
+    const int lp1 = (int)min((long long)np, lp0 + (p1 - at)), seg = b * p.Hkv + h;
+    const long long first = (long long)p.Hkv * cpre[b] + (long long)h * np;
+    const int c0 = (int)cta_of(first, P, n_eff), c1 = (int)cta_of(first + np - 1, P, n_eff);
+    bool bad = false;
+    const int ctxb = eff_ctx(p, b, bad, 0);
+    const int end = min(lp1 * kPage, ctxb + 1);
+    const float* const scores = p.scores + (size_t)seg * R * row_len;
+    float* const mass = p.mass + (size_t)seg * p.mass_len;
+    float4 x[kMassRows], old = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    int phys = -1;
+    auto load = [&](int pos, int r0) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (pos + i < ctxb) m[i] += w[i];
-      if (pos + i == ctxb) {
-        m[i] = w[i];
-        p.ids[(size_t)seg * p.mass_len + pos + i] = p.positions[b];
+      for (int i = 0; i < kMassRows; ++i)
+        if (r0 + i < R) x[i] = __ldcs(reinterpret_cast<const float4*>(scores + (r0 + i) * row_len + pos));
+    };
+    int pos = lp0 * kPage + 4 * t;
+    if (pos < end) {
+      load(pos, 0);
+      old = *reinterpret_cast<const float4*>(mass + pos);
+      phys = p.block_table[(size_t)b * p.max_pages + pos / kPage];
+    }
+    __syncthreads();
+    for (int r = warp; r < R; r += kMassThreads / 32) {
+      float M = -INFINITY, l = 0.0f;
+      for (int c = c0 + lane; c <= c1; c += 32) {
+        const float2 y = *reinterpret_cast<const float2*>(p.partials + ((size_t)(c + seg) * R + r) * kPartialStride);
+        const float Mn = fmaxf(M, y.x);
+        l = Mn > -INFINITY ? l * fast_exp2(M - Mn) + y.y * fast_exp2(y.x - Mn) : l + y.y;
+        M = Mn;
       }
+      const float Mw = warp_max_all(M);
+      l = Mw > -INFINITY ? l * fast_exp2(M - Mw) : l;
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+      if (lane == 0) stats[r] = make_float2(Mw, l > 0.0f && l < INFINITY ? 1.0f / l : 0.0f);
+    }
+    __syncthreads();
+    while (pos < end) {
+      float w[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      for (int r0 = 0; r0 < R; r0 += kMassRows) {
+        if (r0 > 0) load(pos, r0);
+#pragma unroll
+        for (int i = 0; i < kMassRows; ++i) {
+          if (r0 + i >= R) break;
+          const float2 st = stats[r0 + i];
+          if (st.y == 0.0f) continue;
+          w[0] = fmaf(fast_exp2(x[i].x - st.x), st.y, w[0]);
+          w[1] = fmaf(fast_exp2(x[i].y - st.x), st.y, w[1]);
+          w[2] = fmaf(fast_exp2(x[i].z - st.x), st.y, w[2]);
+          w[3] = fmaf(fast_exp2(x[i].w - st.x), st.y, w[3]);
+        }
+      }
+      float* const m = mass + pos;
+      const float o[4] = {old.x, old.y, old.z, old.w};
+      const int here = pos;
+      const bool in_pool = phys >= 0 && phys < p.num_pages;
+      pos += 4 * kMassThreads;
+      if (pos < end) {
+        load(pos, 0);
+        old = *reinterpret_cast<const float4*>(mass + pos);
+        phys = p.block_table[(size_t)b * p.max_pages + pos / kPage];
+      }
+      if (!in_pool) continue;
+      if (here + 3 < ctxb) {
+        *reinterpret_cast<float4*>(m) = make_float4(o[0] + w[0], o[1] + w[1], o[2] + w[2], o[3] + w[3]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (here + i < ctxb) m[i] = o[i] + w[i];
+          if (here + i == ctxb) {
+            m[i] = w[i];
+            p.ids[(size_t)seg * p.mass_len + here + i] = p.positions[b];
+          }
+        }
+      }
+    }
+    at += lp1 - lp0;
+  }
+
+  const int n_items = p.B * p.Hkv * R;
+  for (int item = gridDim.x - 1 - block; item < n_items; item += gridDim.x) {
+    const int seg = item / R, row = item - seg * R, b = seg / p.Hkv, h = seg - b * p.Hkv;
+    const int np = cpre[b + 1] - cpre[b];
+    const long long first = (long long)p.Hkv * cpre[b] + (long long)h * np;
+    const int c0 = (int)cta_of(first, P, n_eff), n = (int)cta_of(first + np - 1, P, n_eff) - c0 + 1;
+    const float* const src = p.partials + ((size_t)(c0 + seg) * R + row) * kPartialStride;
+    const size_t step = (size_t)R * kPartialStride;
+    float M = -INFINITY;
+    __syncthreads();
+    for (int c = t; c < n; c += kMassThreads) M = fmaxf(M, src[c * step]);
+    M = warp_max_all(M);
+    if (lane == 0) red[0][warp] = M;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kMassThreads / 32; ++w) M = fmaxf(M, red[0][w]);
+    float l = 0.0f;
+    for (int c = t; c < n; c += kMassThreads) {
+      const float2 y = *reinterpret_cast<const float2*>(src + c * step);
+      const float f = M > -INFINITY ? fast_exp2(y.x - M) : 0.0f;
+      factor[c] = f;
+      l += M > -INFINITY ? f * y.y : y.y;  // (scores that are NaN: their sum is kept)
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (lane == 0) red[1][warp] = l;
+    __syncthreads();
+    const int d = t % kD, upper = t / kD;  // dim, and which half of the partials
+    const int k0 = upper ? n / 2 : 0, k1 = upper ? n : n / 2;
+    float a = 0.0f;
+    int k = k0;
+    for (; k + 8 <= k1; k += 8) {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = src[(k + i) * step + 2 + d];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) a = factor[k + i] == 0.0f ? a : fmaf(factor[k + i], v[i], a);
+    }
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (k + i < k1) v[i] = src[(k + i) * step + 2 + d];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (k + i < k1 && factor[k + i] != 0.0f) a = fmaf(factor[k + i], v[i], a);
+    if (upper) half[d] = a;
+    __syncthreads();
+    if (!upper) {
+      float sum = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kMassThreads / 32; ++w) sum += red[1][w];
+      const float y = sum == 0.0f ? 0.0f : (a + half[d]) / sum;  // a row that saw nothing: 0
+      const int r = row / p.G;
+      const size_t to = (((size_t)b * p.S + r) * p.Hq + h * p.G + row - r * p.G) * kD + d;
+      if (p.out_bf16) reinterpret_cast<__nv_bfloat16*>(p.out)[to] = __float2bfloat16_rn(y);
+      else p.out[to] = y;
     }
   }
 }
@@ -2052,12 +2268,16 @@ cudaError_t launch_attn_t(AttnParams& p, size_t smem, int threads, long long p_m
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, attn_kernel<FMT, NT, FORM>, p);
   if (e != cudaSuccess) return e;
-  e = launch_combine<FMT, FORM>(cfg, p, sm);
-  if (FORM != kMass || e != cudaSuccess) return e;
-  cfg.gridDim = dim3((unsigned)((p.max_pages * kPage + kMassTokens - 1) / kMassTokens * p.B * p.Hkv), 1, 1);
+  if constexpr (FORM != kMass) {
+    return launch_combine<FMT, FORM>(cfg, p, sm);
+  } else {
+  // as many blocks as there are items and runs of pages, while all are resident at once (four an SM)
+  const long long work = (long long)p.B * p.Hkv * p.R + (p_max + kMassPages - 1) / kMassPages;
+  cfg.gridDim = dim3((unsigned)std::min<long long>(4LL * sm, work), 1, 1);
   cfg.blockDim = dim3(kMassThreads, 1, 1);
-  cfg.dynamicSmemBytes = 0;
+  cfg.dynamicSmemBytes = (p.B + 1 + 4) * sizeof(int);
   return cudaLaunchKernelEx(&cfg, mass_kernel, p);
+  }
 }
 
 // int4 with more than 8 query rows per KV head: the tcgen05 kernel (NR = rows rounded up to 8),
@@ -2122,6 +2342,9 @@ void shape(AttnParams& p, int NT, int ntg, int nkg, int nst, size_t& smem, int& 
 cudaError_t launch_window(AttnParams& p, const AttnJob& job, cudaStream_t stream) {
   p.window = job.window;
   p.sinks = job.sinks;
+  p.append = job.append;
+  p.by_group = by_group(kWindow, p.R > 8 ? 2 : 1);
+  p.max_parts = kMaxCtas;
   const long long pages = std::min<long long>(p.max_pages, ((long long)job.sinks + kPage - 1) / kPage +
                                                                ((long long)job.window + p.S - 2) / kPage + 2);
   const long long p_max = (long long)p.Hkv * p.B * pages;
@@ -2141,8 +2364,10 @@ cudaError_t launch_window(AttnParams& p, const AttnJob& job, cudaStream_t stream
 
 // Two tiles a warp at most: the second part of q~ takes registers.
 cudaError_t launch_mass(AttnParams& p, const AttnJob& job, long long p_max, cudaStream_t stream) {
+  p.append = job.append;
+  p.by_group = by_group(kMass, 1);
+  p.max_parts = kMassMaxParts;
   p.scores = job.scores;
-  p.stats = job.stats;
   p.mass = job.mass;
   p.ids = job.ids;
   p.mass_len = job.mass_len;
@@ -2166,6 +2391,10 @@ std::atomic<unsigned long long> g_stage_wait_ns{kWaitLimitNs};
 void set_stage_wait_limit_ns(unsigned long long ns) { g_stage_wait_ns.store(ns, std::memory_order_relaxed); }
 
 size_t workspace_qrot_bytes(int B, int S, int Hq) { return align_up((size_t)B * S * Hq * kD * 4, 256); }
+
+size_t workspace_mass_partials_bytes(int B, int Hq, int Hkv) {
+  return align_up(((size_t)kMassMaxParts + (size_t)B * Hkv) * (Hq / Hkv) * kPartialStride * 4, 256);
+}
 
 size_t workspace_partials_bytes(int B, int S, int Hq, int Hkv) {
   const int G = Hq / Hkv;

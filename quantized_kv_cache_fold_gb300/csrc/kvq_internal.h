@@ -80,9 +80,9 @@ struct AttnJob {
   int out_bf16;               // out holds bf16 (with tree_mask, a window over int4, or mass)
   // int4: a window (`window` > 0) with the first `sinks` tokens visible outside it
   int sinks;
+  int append;  // with it or with scores: the prologue before appends new rows
   // int4, S == 1: weights added to mass (scores null: not)
   float* scores;   // workspace, [B * Hkv][Hq / Hkv][max_pages_per_seq * 64]
-  float2* stats;   // workspace, [B * Hkv][Hq / Hkv]
   float* mass;     // [.][Hkv][mass_len]
   int32_t* ids;
   int mass_len;
@@ -249,5 +249,7 @@ kvq_status check_ring(const kvq_fp8_ring* r);
 
 size_t workspace_qrot_bytes(int B, int S, int Hq);
 size_t workspace_partials_bytes(int B, int S, int Hq, int Hkv);
+constexpr int kMassMaxParts = 2048;  // parts of a mass call (sizes its partials)
+size_t workspace_mass_partials_bytes(int B, int Hq, int Hkv);
 
 }  // namespace kvq
