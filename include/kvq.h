@@ -606,8 +606,8 @@ kvq_status kvq_mass_attn_int4_fwht(const kvq_int4_cache* cache, const kvq_token_
  *   q, k:     as kvq_prompt_attn takes them (KVQ_BF16 or KVQ_F16); strides: host int64[4] or NULL (packed), elements
  *             between tokens and between heads of q, then of k, as there.
  *   rows:     the rows that count, from the end (<= 0, or n and more: all).
- *   seq_ids:  device int32[B] or NULL (b). A row outside mass or named before, offsets as kvq_prompt_attn refuses them (but
- *             sequences may overlap), or a prompt longer than max_tokens: skipped, KVQ_DEVERR_POS.
+ *   seq_ids:  device int32[B] or NULL (b). A row outside mass or named before, offsets as kvq_prompt_attn refuses them,
+ *             or a prompt longer than max_tokens: skipped, KVQ_DEVERR_POS.
  *   workspace: device, >= kvq_prompt_mass_workspace_bytes(T, B, num_q_heads, num_kv_heads, rows), 256-byte aligned;
  *             contents need no initialisation.
  *   Precision: products of the 16-bit inputs summed in fp32, weights and sums fp32, in an order that does not depend on

@@ -12,14 +12,15 @@
 //   pass B  fixed: 128 keys; streamed: query tiles, each with its a. Thread = key: the sum over all rows, written once.
 //
 // So neither pass exchanges anything between threads, and a's rounding is the only one beside those of the scores and of the
-// power of two. tcgen05 products into four score tiles of tensor memory; two groups of four warps take them in turns.
+// power of two. tcgen05 products into four score tiles of tensor memory; four groups of four warps take them in turns
+// (two groups: 149 us against 138 for 8 prompts; a warp alone waits for tensor memory, then for the power of two).
 //
-//   warps 0-3, 4-7  scores to sums (a lane of tensor memory each), steps of even and odd number
-//   warp 8          tensor-map copies
-//   warp 9          the products (one issuing thread)
+//   warps 0-3, 4-7, 8-11, 12-15  scores to sums (a lane of tensor memory each), every fourth step
+//   warp 16                      tensor-map copies
+//   warp 17                      the products (one issuing thread)
 //
 // Bound by the power of two: one a pair and pass, 16 a cycle and SM (a 128 x 128 tile: 1,024 cycles; its products: 256).
-// 8 prompts of 2,000-32,768 tokens, 20/4 heads, last 64 rows: 149 us; 4 of up to 700, last 16: 14 us.
+// 8 prompts of 2,000-32,768 tokens, 20/4 heads, last 64 rows: 138 us; 4 of up to 700, last 16: 14 us.
 
 #include <algorithm>
 #include <mutex>
@@ -34,7 +35,10 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kRows = 128;                  // rows of a tile
 constexpr int kTileBytes = kRows * kD * 2;  // two 64-dim halves of 128 rows of 128 bytes
 constexpr int kRing = 4;                    // streamed tiles, and score tiles
-constexpr int kThreads = 320;
+constexpr int kGroups = 4;                  // of four warps, a score tile each
+constexpr int kThreads = 128 * kGroups + 64;
+constexpr int kCopyWarp = 4 * kGroups, kIssueWarp = kCopyWarp + 1;
+static_assert(kGroups == kRing, "step k is group k mod kGroups's, in score tile k mod kRing");
 constexpr int kRec = 132;                   // floats of a query tile's record: -a of 128 rows, whether one is not finite
 constexpr float kBaseLag = 30.0f;           // how far (in powers of two) a score may pass the base: sums are fp32
 
@@ -51,7 +55,7 @@ struct Smem {
   uint8_t fixed[2][kTileBytes];
   uint8_t ring[kRing][kTileBytes];
   alignas(16) float rec[kRing][kRec];
-  float2 join[2][kRows];
+  float2 join[2][kGroups - 1][kRows];
   uint64_t fixed_full[2], fixed_empty[2];
   uint64_t ring_full[kRing], ring_empty[kRing], s_full[kRing], s_empty[kRing];
   uint64_t fin;
@@ -118,6 +122,7 @@ __device__ __forceinline__ long long item_at(int k) {
 template <bool B>
 __device__ void lay_out(const ObserveParams& p, Smem& s) {
   const ObserveJob& j = p.j;
+  bool bad = false;
   for (int b = threadIdx.x; b < j.B; b += kThreads) {
     const int lo = j.cu_seqlens[b], hi = j.cu_seqlens[b + 1];
     bool ok = lo >= 0 && hi >= lo && hi <= j.T && hi - lo <= j.mass_len;
@@ -126,9 +131,22 @@ __device__ void lay_out(const ObserveParams& p, Smem& s) {
     if (j.seq_ids)
       for (int a = 0; a < b && ok; ++a) ok = j.seq_ids[a] != row;  // a row named twice: the first counts
     s.n[b] = ok ? hi - lo : 0;
+    bad |= !ok;
     if (!ok && blockIdx.x == 0) set_err(j.dev_err, KVQ_DEVERR_POS);
   }
-  __syncthreads();
+  // Offsets that go back may name tokens twice, and more in all than the workspace is for: sequences that overlap an earlier
+  // one are skipped too.
+  if (__syncthreads_or(bad)) {
+    if (threadIdx.x == 0) {
+      int end = 0;
+      for (int b = 0; b < j.B; ++b) {
+        if (s.n[b] == 0) continue;
+        if (j.cu_seqlens[b] < end) s.n[b] = 0;
+        else end = j.cu_seqlens[b + 1];
+      }
+    }
+    __syncthreads();
+  }
   if (threadIdx.x < 32) {
     const int lane = threadIdx.x;
     int items = 0, tiles = 0;
@@ -184,10 +202,16 @@ __global__ void __launch_bounds__(kThreads, 1) observe_kernel(const __grid_const
     sm.failed = 0;
   }
   fence_barrier_init();
+  if (B) {  // the rows of a streamed tile behind those that copies write
+    const int used = p.qt * (j.Hq / j.Hkv), per = (kRows - used) * 8;  // 16-byte words of a 64-dim half
+    for (int i = threadIdx.x; i < 2 * kRing * per; i += kThreads)
+      reinterpret_cast<uint4*>(sm.ring[i / per >> 1] + (i / per & 1) * (kTileBytes / 2) + used * 128)[i % per] = make_uint4(0u, 0u, 0u, 0u);
+    fence_proxy_async_shared();
+  }
   griddep_wait();
   griddep_launch_dependents();
   lay_out<B>(p, sm);
-  if (warp == 9) tmem_alloc_512(&sm.taddr);
+  if (warp == kIssueWarp) tmem_alloc_512(&sm.taddr);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -195,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1) observe_kernel(const __grid_const
   const int items = sm.items[j.B];
   const int G = j.Hq / j.Hkv, Rq = p.qt * G;  // rows of a query tile in use
 
-  if (warp == 8) {
+  if (warp == kCopyWarp) {
     if (lane == 0) {
       // -------------------------------------------------------------- copies
       fence_proxy_async_global();
@@ -238,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1) observe_kernel(const __grid_const
         for (int u = max(0, k - kRing); u < k; ++u) mbar_wait_bounded(&sm.ring_full[u % kRing], (uint32_t)(u / kRing) & 1u);
       }
     }
-  } else if (warp == 9) {
+  } else if (warp == kIssueWarp) {
     // ---------------------------------------------------------------- products
     constexpr uint32_t kId = umma_idesc_16(F16, kRows, false);
     const uint32_t leader = elect_one();
@@ -288,8 +312,8 @@ __global__ void __launch_bounds__(kThreads, 1) observe_kernel(const __grid_const
       float base = -INFINITY;
       uint64_t l2[2] = {0ull, 0ull};
       for (int u = it.j0; u < it.j1; ++u, ++k) {
-        if ((k & 1) != grp) continue;
-        const int st = k % kRing;
+        if (k % kGroups != grp) continue;
+        const int st = grp;
         ok = __all_sync(0xffffffffu, role_wait(&sm.s_full[st], (uint32_t)(k / kRing) & 1u, failed));
         if (B && ok) ok = __all_sync(0xffffffffu, role_wait(&sm.ring_full[st], (uint32_t)(k / kRing) & 1u, failed));
         if (!ok) break;
@@ -330,7 +354,8 @@ __global__ void __launch_bounds__(kThreads, 1) observe_kernel(const __grid_const
           }
         } else {
           const int q0 = it.first + u * p.qt;                   // the tile's first token
-          const int valid = min(p.qt, it.n - q0) * G;           // its columns in use
+          // its columns in use (of a whole tile all: those behind its rows are zeros, with no weight)
+          const int valid = it.n - q0 >= p.qt ? kRows : (it.n - q0) * G;
           const int from = max(0, it.at + row - q0) * G;        // seen: columns from here on
           const float* rec = sm.rec[st];
           const bool odd = rec[kRows] != 0.0f;
@@ -376,22 +401,30 @@ __global__ void __launch_bounds__(kThreads, 1) observe_kernel(const __grid_const
       }
       // the groups' sums are joined in the first one
       float l = (f2lo(l2[0]) + f2hi(l2[0])) + (f2lo(l2[1]) + f2hi(l2[1]));
-      if (grp == 1) sm.join[i & 1][row] = make_float2(base, l);
-      if (named_barrier_or(1, 256, !ok)) break;
-      if (grp == 1) continue;
-      const float2 other = sm.join[i & 1][row];
+      if (grp > 0) sm.join[i & 1][grp - 1][row] = make_float2(base, l);
+      if (named_barrier_or(1, 128 * kGroups, !ok)) break;
+      if (grp > 0) continue;
+      float2 other[kGroups - 1];
+#pragma unroll
+      for (int q = 0; q < kGroups - 1; ++q) other[q] = sm.join[i & 1][q][row];
       if (B) {
+#pragma unroll
+        for (int q = 0; q < kGroups - 1; ++q) l += other[q].y;
         const int key = it.at + row;
         if (key < it.n) {
           const int sid = j.seq_ids ? j.seq_ids[it.b] : it.b;
           const size_t at = ((size_t)sid * j.Hkv + it.h) * j.mass_len + key;
-          j.mass[at] = l + other.y;
+          j.mass[at] = l;
           j.ids[at] = key;
         }
       } else {
-        const float M = fmaxf(base, other.x);
-        if (M > -INFINITY) l = l * fast_exp2(base - M) + other.y * fast_exp2(other.x - M);
-        else l += other.y;  // nothing seen (0), or scores that are NaN
+        float M = base;
+#pragma unroll
+        for (int q = 0; q < kGroups - 1; ++q) M = fmaxf(M, other[q].x);
+        if (M > -INFINITY) l *= fast_exp2(base - M);
+#pragma unroll
+        for (int q = 0; q < kGroups - 1; ++q)  // nothing seen (0), or scores that are NaN: the sums as they are
+          l += M > -INFINITY ? other[q].y * fast_exp2(other[q].x - M) : other[q].y;
         if (row >= Rq || it.at + row / G >= it.n) l = -1.0f;
         if (p.nsplit > 1) {
           j.part[((size_t)it.split * p.tiles + it.tile) * kRows + row] = make_float2(M, l);
@@ -411,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1) observe_kernel(const __grid_const
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 9) tmem_dealloc_512(tmem);
+  if (warp == kIssueWarp) tmem_dealloc_512(tmem);
   if (threadIdx.x == 0 && *failed) set_err(j.dev_err, KVQ_DEVERR_TIMEOUT);
 }
 

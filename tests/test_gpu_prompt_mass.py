@@ -160,6 +160,14 @@ def test_bad_rows_offsets_and_lengths_are_flagged_and_skipped():
     held = call(q, k, lens, 20, cu=cu, want_err=kvq.DEVERR_POS)
     assert bool(((held["mass"][0, :, :100].double() - want[0][0]).abs() <= want[0][1]).all())
     assert bool(torch.isnan(held["mass"][1]).all()) and bool(torch.isnan(held["mass"][3]).all())
+    # offsets that name the same tokens again and again: more in all than the call's tokens
+    cu = torch.tensor([0, 240] * 40 + [0], dtype=torch.int32, device="cuda")
+    held, _ = kvq.alloc_token_mass(80, 2, 4)
+    held["mass"].fill_(math.nan)
+    call(q, k, lens, 0, held=held, cu=cu, want_err=kvq.DEVERR_POS)
+    whole = reference(q, k, [240], 0)[0]
+    assert bool(((held["mass"][0, :, :240].double() - whole[0]).abs() <= whole[1]).all())
+    assert bool(torch.isnan(held["mass"][1:]).all())
     # a prompt longer than its place
     held, _ = kvq.alloc_token_mass(3, 2, 1)
     held["mass"].fill_(math.nan)
