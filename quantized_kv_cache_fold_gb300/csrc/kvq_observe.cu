@@ -13,14 +13,14 @@
 //
 // So neither pass exchanges anything between threads, and a's rounding is the only one beside those of the scores and of the
 // power of two. tcgen05 products into four score tiles of tensor memory; four groups of four warps take them in turns
-// (two groups: 149 us against 138 for 8 prompts; a warp alone waits for tensor memory, then for the power of two).
+// (two groups: 149 us against 138 for 8 prompts, 127 with fewer runs and sums left without waiting; a warp alone waits for tensor memory, then for the power of two).
 //
 //   warps 0-3, 4-7, 8-11, 12-15  scores to sums (a lane of tensor memory each), every fourth step
 //   warp 16                      tensor-map copies
 //   warp 17                      the products (one issuing thread)
 //
 // Bound by the power of two: one a pair and pass, 16 a cycle and SM (a 128 x 128 tile: 1,024 cycles; its products: 256).
-// 8 prompts of 2,000-32,768 tokens, 20/4 heads, last 64 rows: 138 us; 4 of up to 700, last 16: 14 us.
+// 8 prompts of 2,000-32,768 tokens, 20/4 heads, last 64 rows: 127 us; 4 of up to 700, last 16: 14 us.
 
 #include <algorithm>
 #include <mutex>
@@ -41,6 +41,14 @@ constexpr int kCopyWarp = 4 * kGroups, kIssueWarp = kCopyWarp + 1;
 static_assert(kGroups == kRing, "step k is group k mod kGroups's, in score tile k mod kRing");
 constexpr int kRec = 132;                   // floats of a query tile's record: -a of 128 rows, whether one is not finite
 constexpr float kBaseLag = 30.0f;           // how far (in powers of two) a score may pass the base: sums are fp32
+
+// Named barriers: sums left for group 0, their place free again (each for even and odd items), group 0's own.
+constexpr uint32_t kFullBar = 1, kFreeBar = 3, kRecBar = 5;
+
+// Arrives at a named barrier without waiting; what the thread wrote before is seen by those who wait there.
+__device__ __forceinline__ void named_arrive(uint32_t id, uint32_t nthreads) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
+}
 
 struct ObserveParams {
   CUtensorMap mq, mk;
@@ -305,18 +313,20 @@ __global__ void __launch_bounds__(kThreads, 1) observe_kernel(const __grid_const
     const uint64_t c2 = f2(c, c);
     bool ok = true;
     int k = 0;
-    for (int i = 0; ok; ++i) {
+    // A wait that gives up ends this warp's work, not its part in the barriers below: every warp goes through all items.
+    int i = 0;
+    for (;; ++i) {
       const long long idx = item_at(i);
       if (idx >= items) break;
       const Item it = find_item<B>(p, sm, (int)idx);
       float base = -INFINITY;
       uint64_t l2[2] = {0ull, 0ull};
       for (int u = it.j0; u < it.j1; ++u, ++k) {
-        if (k % kGroups != grp) continue;
+        if (k % kGroups != grp || !ok) continue;
         const int st = grp;
         ok = __all_sync(0xffffffffu, role_wait(&sm.s_full[st], (uint32_t)(k / kRing) & 1u, failed));
         if (B && ok) ok = __all_sync(0xffffffffu, role_wait(&sm.ring_full[st], (uint32_t)(k / kRing) & 1u, failed));
-        if (!ok) break;
+        if (!ok) continue;
         tc_fence_after();
         if (!B) {
           const int hi = it.at + row / G - u * kRows;  // seen: columns up to hi
@@ -401,12 +411,17 @@ __global__ void __launch_bounds__(kThreads, 1) observe_kernel(const __grid_const
       }
       // the groups' sums are joined in the first one
       float l = (f2lo(l2[0]) + f2hi(l2[0])) + (f2lo(l2[1]) + f2hi(l2[1]));
-      if (grp > 0) sm.join[i & 1][grp - 1][row] = make_float2(base, l);
-      if (named_barrier_or(1, 128 * kGroups, !ok)) break;
-      if (grp > 0) continue;
+      if (grp > 0) {  // left for group 0 without waiting for it, two items deep
+        if (i >= 2) named_barrier(kFreeBar + (i & 1), 128 * kGroups);
+        sm.join[i & 1][grp - 1][row] = make_float2(base, l);
+        named_arrive(kFullBar + (i & 1), 128 * kGroups);
+        continue;
+      }
+      named_barrier(kFullBar + (i & 1), 128 * kGroups);
       float2 other[kGroups - 1];
 #pragma unroll
       for (int q = 0; q < kGroups - 1; ++q) other[q] = sm.join[i & 1][q][row];
+      named_arrive(kFreeBar + (i & 1), 128 * kGroups);
       if (B) {
 #pragma unroll
         for (int q = 0; q < kGroups - 1; ++q) l += other[q].y;
@@ -431,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1) observe_kernel(const __grid_const
         } else {
           bool bad;
           const float na = minus_a(M, l, bad);
-          const bool any = named_barrier_or(2, 128, bad);
+          const bool any = named_barrier_or(kRecBar, 128, bad);
           float* const rec = j.rec + (size_t)it.tile * kRec;
           rec[row] = na;
           if (row == 0) rec[kRows] = any ? 1.0f : 0.0f;
@@ -439,6 +454,8 @@ __global__ void __launch_bounds__(kThreads, 1) observe_kernel(const __grid_const
         }
       }
     }
+    if (grp > 0)  // group 0's arrivals for the last two items
+      for (int e = max(0, i - 2); e < i; ++e) named_barrier(kFreeBar + (e & 1), 128 * kGroups);
   }
   __syncwarp();
   tc_fence_before();
@@ -474,13 +491,13 @@ __global__ void __launch_bounds__(kRows) join_kernel(const float2* part, float* 
 std::mutex g_observe_mu;  // guards the cache below
 bool g_observe_attr[64][4] = {{false}};
 
-// Query tiles of a call at most, and the splits of their keys: enough for 16 items an SM while every item keeps about four
+// Query tiles of a call at most, and the splits of their keys: enough for ten items an SM (16: 138 us, six: 135, ten: 129) while every item keeps about four
 // blocks of keys.
 void plan(int T, int B, int Hq, int Hkv, int rows, int& tiles, int& nsplit) {
   const int qt = kRows / (Hq / Hkv);
   const long long seen = rows > 0 ? std::min<long long>(T, (long long)B * rows) : T;
   tiles = (int)((seen / qt + B) * Hkv);
-  const long long want = (16LL * device_sms() + tiles - 1) / tiles;
+  const long long want = (10LL * device_sms() + tiles - 1) / tiles;
   const long long most = std::max<long long>(1, T / ((long long)B * kRows * 4));
   nsplit = (int)std::max<long long>(1, std::min<long long>(std::min(want, most), 64));
 }
@@ -494,7 +511,7 @@ size_t observe_workspace_bytes(int T, int B, int Hq, int Hkv, int rows) {
   const long long tiles = (seen / qt + B) * Hkv;
   const size_t rec = ((size_t)tiles * kRec * 4 + 255) / 256 * 256;
   const long long most = std::max<long long>(1, T / ((long long)B * kRows * 4));
-  const long long splits = std::max<long long>(1, std::min<long long>(std::min<long long>((16LL * 256 + tiles - 1) / tiles, most), 64));
+  const long long splits = std::max<long long>(1, std::min<long long>(std::min<long long>((10LL * 256 + tiles - 1) / tiles, most), 64));
   return rec + (splits > 1 ? (size_t)splits * tiles * kRows * 8 : 0) + 256;
 }
 
