@@ -53,7 +53,7 @@ typedef enum kvq_status {
   KVQ_ERR_SCRATCH_TOO_SMALL = 4 /* kvq_decode_attn_int4_noalloc: request needs more than its fixed scratch */
 } kvq_status;
 
-/* KVQ_F16 is taken by kvq_prompt_attn only. */
+/* KVQ_F16 is taken by the calls over prompts only (kvq_prompt_attn, kvq_prompt_attn_sinks, kvq_prompt_mass). */
 typedef enum kvq_dtype { KVQ_F32 = 0, KVQ_BF16 = 1, KVQ_F16 = 2 } kvq_dtype;
 
 #define KVQ_HEAD_DIM 128

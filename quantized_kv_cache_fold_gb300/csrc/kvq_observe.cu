@@ -131,13 +131,18 @@ template <bool B>
 __device__ void lay_out(const ObserveParams& p, Smem& s) {
   const ObserveJob& j = p.j;
   bool bad = false;
+  if (j.seq_ids)
+    for (int b = threadIdx.x; b < j.B; b += kThreads) s.items[b] = j.seq_ids[b];  // (a place for them meanwhile)
+  __syncthreads();
   for (int b = threadIdx.x; b < j.B; b += kThreads) {
     const int lo = j.cu_seqlens[b], hi = j.cu_seqlens[b + 1];
     bool ok = lo >= 0 && hi >= lo && hi <= j.T && hi - lo <= j.mass_len;
-    const int row = j.seq_ids ? j.seq_ids[b] : b;
+    const int row = j.seq_ids ? s.items[b] : b;
     ok &= row >= 0 && row < j.num_seqs;
-    if (j.seq_ids)
-      for (int a = 0; a < b && ok; ++a) ok = j.seq_ids[a] != row;  // a row named twice: the first counts
+    if (j.seq_ids) {
+#pragma unroll 8
+      for (int a = 0; a < b; ++a) ok &= s.items[a] != row;  // a row named twice: the first counts
+    }
     s.n[b] = ok ? hi - lo : 0;
     bad |= !ok;
     if (!ok && blockIdx.x == 0) set_err(j.dev_err, KVQ_DEVERR_POS);

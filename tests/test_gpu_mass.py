@@ -255,3 +255,61 @@ def test_wide_tables_pass_32_bits():
     torch.cuda.synchronize()
     c.held["mass"].zero_()
     assert torch.equal(c.run(), out) and torch.equal(c.held["mass"][0, 0, :131], held["mass"][0, 0, :131])
+
+
+def test_two_calls_at_once():
+    cases = [MassCase([900, 30, 2000], 20, 4, seed=40 + i) for i in range(2)]
+    for c in cases:
+        c.append()
+    want = [(c.run(append=False), c.held["mass"].clone()) for c in cases]
+    outs, streams = [torch.zeros(3, 20, D, device="cuda") for _ in cases], [torch.cuda.Stream() for _ in cases]
+    for _ in range(3):
+        for c in cases:
+            c.held["mass"].copy_(c.before)
+        torch.cuda.synchronize()
+        for c, o, s in zip(cases, outs, streams):
+            kvq.kvq_mass_attn_int4(c.cache, c.mass, c.Mq, c.Mk, c.q[:, 0], c.ctx_t, c.pos, o, c.ws, c.err, stream=s)
+        torch.cuda.synchronize()
+        for c, o, (w, m) in zip(cases, outs, want):
+            assert torch.equal(o, w) and torch.equal(c.held["mass"], m) and c.err.item() == 0
+
+
+def test_steps_without_a_wait_between():
+    """Steps in a row, each reading what the one before appended and adding to what it left."""
+    got = []
+    for wait in (False, True):
+        c = MassCase([60, 127, 500], 20, 4, seed=43, extra_pages=1)
+        g = torch.Generator(device="cuda").manual_seed(6)
+        ctx = [c.ctx_t + i for i in range(9)]
+        new = [[torch.randn(3, 4, D, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2)] for _ in range(8)]
+        outs = [torch.zeros(3, 20, D, device="cuda") for _ in range(8)]
+        torch.cuda.synchronize()
+        for i in range(8):
+            kvq.kvq_mass_attn_int4(c.cache, c.mass, c.Mq, c.Mk, c.q[:, 0], ctx[i], ctx[i + 1], outs[i], c.ws, c.err, k_new=new[i][0],
+                                   v_new=new[i][1])
+            if wait:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        assert c.err.item() == 0
+        got.append(outs + [c.held["mass"], c.held["ids"], c.tensors["pages"]])
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    assert all(int(got[0][-2][b, h, n + i]) == n + i + 1 for b, n in enumerate((60, 127, 500)) for h in range(4) for i in range(8))
+
+
+def test_tensors_that_do_not_fit():
+    c = MassCase([100, 20], 10, 2, seed=44)
+    out = torch.empty(2, 10, D, device="cuda")
+    args = dict(cache=c.cache, mass=c.mass, Mq=c.Mq, Mk=c.Mk, q=c.q[:, 0], ctx_len=c.ctx_t, positions=c.pos, out=out, workspace=c.ws,
+                dev_err=c.err)
+    for bad in (dict(q=c.q.repeat(1, 2, 1, 1)), dict(q=c.q[:, 0].half()), dict(out=out[:1]), dict(positions=c.pos.long()), dict(positions=c.pos[:1]),
+                dict(k_new=c.k_new, v_new=c.v_new), dict(workspace=c.ws.cpu()), dict(Mk=c.Mk[0])):
+        with pytest.raises(ValueError):
+            kvq.kvq_mass_attn_int4(**{**args, **bad})
+    for bad in (dict(workspace=c.ws[:256]), dict(mass=kvq.token_mass(c.held["mass"][:1], c.held["ids"][:1])),
+                dict(mass=kvq.token_mass(c.held["mass"][:, :1].contiguous(), c.held["ids"][:, :1].contiguous()))):
+        with pytest.raises(kvq.KvqError):
+            kvq.kvq_mass_attn_int4(**{**args, **bad})
+    with pytest.raises(ValueError):
+        kvq.token_mass(c.held["mass"], c.held["ids"].long())
+    with pytest.raises(ValueError):
+        kvq.token_mass(c.held["mass"][:, :, ::2], c.held["ids"][:, :, ::2])

@@ -227,3 +227,19 @@ def test_repeats_stream_graph_and_two_at_once():
             kvq.kvq_prompt_mass(q, k, cu, 64, d, w, err, stream=s)
     equal()
     assert err.item() == 0
+
+
+def test_tensors_that_do_not_fit():
+    q, k, _ = inputs([100, 20], 4, 2, torch.bfloat16, seed=20)
+    held, mass = kvq.alloc_token_mass(2, 2, 2)
+    err, cu = torch.zeros(1, dtype=torch.int32, device="cuda"), offsets([100, 20])
+    args = dict(q=q, k=k, cu_seqlens=cu, rows=16, mass=mass, workspace=kvq.alloc_prompt_mass_workspace(120, 2, 4, 2, 16), dev_err=err)
+    for bad in (dict(k=k.half()), dict(k=k[:100]), dict(cu_seqlens=cu.long()), dict(q=q.transpose(1, 2)), dict(seq_ids=cu),
+                dict(seq_ids=torch.zeros(2, device="cuda"))):
+        with pytest.raises(ValueError):
+            kvq.kvq_prompt_mass(**{**args, **bad})
+    with pytest.raises(TypeError):
+        kvq.kvq_prompt_mass(**{**args, "q": q.float(), "k": k.float()})
+    for bad in (dict(mass=kvq.alloc_token_mass(1, 2, 2)[1]), dict(mass=kvq.alloc_token_mass(2, 1, 2)[1]), dict(workspace=args["workspace"][:256])):
+        with pytest.raises(kvq.KvqError):
+            kvq.kvq_prompt_mass(**{**args, **bad})

@@ -161,3 +161,61 @@ def test_repeats_stream_and_graph():
         torch.cuda.synchronize()
         assert c.err.item() == 0
         assert torch.equal(out, call(c, 513, 17, append=False)) and torch.equal(other, call(c, 2000, 0, append=False))
+
+
+def test_two_calls_at_once():
+    cases = [Int4Case([900, 30, 2000], 4, 20, 4, seed=30 + i) for i in range(2)]
+    for c in cases:
+        c.append()
+    want = [call(c, 300, 5, append=False) for c in cases]
+    outs, ws = [torch.zeros_like(w) for w in want], [kvq.alloc_workspace(3, 4, 20, 4) for _ in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for c, o, w, s in zip(cases, outs, ws, streams):
+            kvq.kvq_window_attn_int4(c.cache, c.Mq, c.Mk, c.q, c.ctx_t, 300, 5, o, w, c.err, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(outs, want)) and all(c.err.item() == 0 for c in cases)
+
+
+@pytest.mark.parametrize("S", [1, 4])
+def test_rows_written_by_the_call_before(S):
+    """A step's rows are appended by the call, the next step's window reads them: steps in a row without a wait between."""
+    c = Int4Case([60, 127, 500], S, 20, 4, seed=33)
+    ws = kvq.alloc_workspace(3, S, 20, 4)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    steps = 8
+    P = c.tensors["block_table"].shape[1]
+    table = torch.arange(3 * (P + 2), dtype=torch.int32, device="cuda").reshape(3, P + 2)
+    tensors, cache = kvq.alloc_int4_cache(3 * (P + 2), 4, table)
+    for b in range(3):
+        tensors["pages"][table[b, :P].long()] = c.tensors["pages"][c.tensors["block_table"][b].long()]
+    new = [[torch.randn(3, S, 4, D, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2)] for _ in range(steps)]
+    ctx = [c.ctx_t + S * i for i in range(steps + 1)]
+    outs = [torch.zeros(3, S, 20, D, device="cuda") for _ in range(steps)]
+    start = tensors["pages"].clone()
+    got = []
+    for wait in (False, True):
+        tensors["pages"].copy_(start)
+        torch.cuda.synchronize()
+        for i in range(steps):
+            kvq.kvq_window_attn_int4(cache, c.Mq, c.Mk, c.q, ctx[i], 70, 3, outs[i], ws, c.err, k_new=new[i][0], v_new=new[i][1])
+            if wait:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        got.append([o.clone() for o in outs])
+    assert all(torch.equal(a, b) for a, b in zip(*got)) and c.err.item() == 0
+
+
+def test_tensors_that_do_not_fit():
+    c = Int4Case([100, 20], 2, 10, 2, seed=34)
+    ws, out = kvq.alloc_workspace(2, 2, 10, 2), torch.empty(2, 2, 10, D, device="cuda")
+    args = dict(cache=c.cache, Mq=c.Mq, Mk=c.Mk, q=c.q, ctx_len=c.ctx_t, window=10, sinks=1, out=out, workspace=ws, dev_err=c.err)
+    for bad in (dict(q=c.q[:, :, :, ::2]), dict(q=c.q.half()), dict(q=c.q.cpu()), dict(out=out[:1]), dict(out=out.half()), dict(ctx_len=c.ctx_t.long()),
+                dict(ctx_len=c.ctx_t[:1]), dict(Mq=c.Mq[:64]), dict(k_new=c.k_new[:, :1], v_new=c.v_new), dict(dev_err=c.err.long()),
+                dict(workspace=ws.cpu())):
+        with pytest.raises(ValueError):
+            kvq.kvq_window_attn_int4(**{**args, **bad})
+    for bad in (dict(window=0), dict(sinks=-1), dict(workspace=ws[:256]), dict(k_new=c.k_new)):
+        with pytest.raises(kvq.KvqError):
+            kvq.kvq_window_attn_int4(**{**args, **bad})
