@@ -11,16 +11,17 @@
 //           Few query tiles see long prompts, so their keys are split over `nsplit` items, joined by join_kernel.
 //   pass B  fixed: 128 keys; streamed: query tiles, each with its a. Thread = key: the sum over all rows, written once.
 //
-// So neither pass exchanges anything between threads, and a's rounding is the only one beside those of the scores and of the
-// power of two. tcgen05 products into four score tiles of tensor memory; four groups of four warps take them in turns
-// (two groups: 149 us against 138 for 8 prompts, 127 with fewer runs and sums left without waiting; a warp alone waits for tensor memory, then for the power of two).
+// a's rounding is the only one beside those of the scores and of the power of two. tcgen05 products into four score tiles of
+// tensor memory, which four groups of four warps take in turns; their sums meet in group 0 at an item's end (two groups: 149
+// us, four: 138, sums left without waiting and ten items an SM: 127, for the 8 prompts below).
 //
 //   warps 0-3, 4-7, 8-11, 12-15  scores to sums (a lane of tensor memory each), every fourth step
 //   warp 16                      tensor-map copies
 //   warp 17                      the products (one issuing thread)
 //
-// Bound by the power of two: one a pair and pass, 16 a cycle and SM (a 128 x 128 tile: 1,024 cycles; its products: 256).
-// 8 prompts of 2,000-32,768 tokens, 20/4 heads, last 64 rows: 127 us; 4 of up to 700, last 16: 14 us.
+// 8 prompts of 2,000-32,768 tokens, 20/4 heads, last 64 rows: 127 us; 4 of up to 700, last 16: 14 us. No unit is full (a 128 x
+// 128 tile: 512 cycles of the power of two, 512 of products, about 880 all in all); bundles of four fixed tiles, which
+// stream every key once, were slower (142; with a scheduling warp 136, but the short prompts then 22).
 
 #include <algorithm>
 #include <mutex>
