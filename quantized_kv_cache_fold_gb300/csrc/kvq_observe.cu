@@ -40,10 +40,12 @@ constexpr int kGroups = 4;                  // of four warps, a score tile each
 constexpr int kThreads = 128 * kGroups + 64;
 constexpr int kCopyWarp = 4 * kGroups, kIssueWarp = kCopyWarp + 1;
 static_assert(kGroups == kRing, "step k is group k mod kGroups's, in score tile k mod kRing");
+constexpr int kItems = 16;                  // items that a warp looks up together, a lane each
 constexpr int kRec = 132;                   // floats of a query tile's record: -a of 128 rows, whether one is not finite
 constexpr float kBaseLag = 30.0f;           // how far (in powers of two) a score may pass the base: sums are fp32
 
-// Named barriers: sums left for group 0, their place free again (each for even and odd items), group 0's own.
+// Named barriers: sums left for the group that joins them, their place free again (each for even and odd items), and one
+// for each group's own.
 constexpr uint32_t kFullBar = 1, kFreeBar = 3, kRecBar = 5;
 
 // Arrives at a named barrier without waiting; what the thread wrote before is seen by those who wait there.
@@ -60,10 +62,23 @@ struct ObserveParams {
   int tiles;   // most query tiles, as the workspace is laid out
 };
 
+struct Item {
+  int n;
+  int start;     // the sequence's first token
+  int sid;       // its row of the masses
+  int h;
+  int first;     // first observed token
+  int tile;      // pass A: this query tile's number in the workspace; pass B: that of the streamed tile 0 of (b, h)
+  int at;        // pass A: first token of the query tile; pass B: first key of the key tile
+  int split;
+  int j0, j1;    // streamed tiles
+};
+
 struct Smem {
   uint8_t fixed[2][kTileBytes];
   uint8_t ring[kRing][kTileBytes];
   alignas(16) float rec[kRing][kRec];
+  Item list[kThreads / 32][kItems];
   float2 join[2][kGroups - 1][kRows];
   uint64_t fixed_full[2], fixed_empty[2];
   uint64_t ring_full[kRing], ring_empty[kRing], s_full[kRing], s_empty[kRing];
@@ -75,15 +90,6 @@ struct Smem {
   int tiles[KVQ_MAX_SEQS + 1];  // first query tile of each
 };
 
-struct Item {
-  int b, h, n;
-  int first;     // first observed token
-  int tile;      // pass A: this query tile's number in the workspace; pass B: that of the streamed tile 0 of (b, h)
-  int at;        // pass A: first token of the query tile; pass B: first key of the key tile
-  int split;
-  int j0, j1;    // streamed tiles
-};
-
 template <bool B>
 __device__ __forceinline__ Item find_item(const ObserveParams& p, const Smem& s, int idx) {
   int lo = 0, hi = p.j.B - 1;
@@ -93,8 +99,9 @@ __device__ __forceinline__ Item find_item(const ObserveParams& p, const Smem& s,
     else hi = mid - 1;
   }
   Item it;
-  it.b = lo;
   it.n = s.n[lo];
+  it.start = p.j.cu_seqlens[lo];
+  it.sid = p.j.seq_ids ? p.j.seq_ids[lo] : lo;
   const int rows = p.j.rows > 0 ? min(p.j.rows, it.n) : it.n;
   it.first = it.n - rows;
   const int tiles = (rows + p.qt - 1) / p.qt;
@@ -125,6 +132,22 @@ __device__ __forceinline__ Item find_item(const ObserveParams& p, const Smem& s,
 __device__ __forceinline__ long long item_at(int k) {
   const int n = gridDim.x, c = blockIdx.x;
   return (long long)k * n + (k & 1 ? n - 1 - c : c);
+}
+
+// Item i of this CTA for a whole warp, which asks for 0, 1, 2, ... in turn: kItems of them are looked up together (one at a
+// time, the search and its divisions took a third of the kernel's time). False behind the last one.
+template <bool B>
+__device__ __forceinline__ bool next_item(const ObserveParams& p, Smem& s, int i, Item& it) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, items = s.items[p.j.B];
+  if ((i & (kItems - 1)) == 0) {
+    __syncwarp();
+    const long long idx = item_at(i + lane);
+    if (lane < kItems && idx < items) s.list[warp][lane] = find_item<B>(p, s, (int)idx);
+    __syncwarp();
+  }
+  if (item_at(i) >= items) return false;
+  it = s.list[warp][i & (kItems - 1)];
+  return true;
 }
 
 // Lengths and first items of the sequences; sequences that a call cannot take are flagged and have none.
@@ -230,51 +253,44 @@ __global__ void __launch_bounds__(kThreads, 1) observe_kernel(const __grid_const
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.taddr;
-  const int items = sm.items[j.B];
   const int G = j.Hq / j.Hkv, Rq = p.qt * G;  // rows of a query tile in use
 
   if (warp == kCopyWarp) {
-    if (lane == 0) {
-      // -------------------------------------------------------------- copies
-      fence_proxy_async_global();
-      bool ok = true;
-      int f = 0, k = 0;
-      auto keys = [&](uint8_t* dst, const Item& it, int tok, uint64_t* bar) {
-        const int s = j.cu_seqlens[it.b];
-        tma_load_3d(dst, &p.mk, 0, it.h, s + tok, bar);
-        tma_load_3d(dst + kTileBytes / 2, &p.mk, 64, it.h, s + tok, bar);
-      };
-      auto queries = [&](uint8_t* dst, const Item& it, int tok, uint64_t* bar) {
-        const int s = j.cu_seqlens[it.b];
-        tma_load_3d(dst, &p.mq, 0, it.h * G, s + tok, bar);
-        tma_load_3d(dst + kTileBytes / 2, &p.mq, 64, it.h * G, s + tok, bar);
-      };
-      for (int i = 0; ok; ++i) {
-        const long long idx = item_at(i);
-        if (idx >= items) break;
-        const Item it = find_item<B>(p, sm, (int)idx);
-        if (it.j0 >= it.j1) continue;
-        if (f >= 2 && !(ok = role_wait(&sm.fixed_empty[f & 1], (uint32_t)((f >> 1) - 1) & 1u, failed))) break;
-        mbar_arrive_expect_tx(&sm.fixed_full[f & 1], B ? kTileBytes : 2 * Rq * 128);
-        if (B) keys(sm.fixed[f & 1], it, it.at, &sm.fixed_full[f & 1]);
-        else queries(sm.fixed[f & 1], it, it.at, &sm.fixed_full[f & 1]);
-        ++f;
-        for (int u = it.j0; u < it.j1; ++u, ++k) {
-          const int st = k % kRing;
-          if (k >= kRing && !(ok = role_wait(&sm.ring_empty[st], (uint32_t)(k / kRing - 1) & 1u, failed))) break;
-          mbar_arrive_expect_tx(&sm.ring_full[st], B ? 2 * Rq * 128 + kRec * 4 : kTileBytes);
-          if (B) {
-            queries(sm.ring[st], it, it.first + u * p.qt, &sm.ring_full[st]);
-            bulk_g2s(sm.rec[st], j.rec + (size_t)(it.tile + u) * kRec, kRec * 4, &sm.ring_full[st], policy_evict_first());
-          } else {
-            keys(sm.ring[st], it, u * kRows, &sm.ring_full[st]);
-          }
+    // ---------------------------------------------------------------- copies (lane 0; the others look items up)
+    fence_proxy_async_global();
+    bool ok = true;
+    int f = 0, k = 0;
+    auto keys = [&](uint8_t* dst, const Item& it, int tok, uint64_t* bar) {
+      tma_load_3d(dst, &p.mk, 0, it.h, it.start + tok, bar);
+      tma_load_3d(dst + kTileBytes / 2, &p.mk, 64, it.h, it.start + tok, bar);
+    };
+    auto queries = [&](uint8_t* dst, const Item& it, int tok, uint64_t* bar) {
+      tma_load_3d(dst, &p.mq, 0, it.h * G, it.start + tok, bar);
+      tma_load_3d(dst + kTileBytes / 2, &p.mq, 64, it.h * G, it.start + tok, bar);
+    };
+    Item it;
+    for (int i = 0; next_item<B>(p, sm, i, it); ++i) {
+      if (lane > 0 || !ok || it.j0 >= it.j1) continue;
+      if (f >= 2 && !(ok = role_wait(&sm.fixed_empty[f & 1], (uint32_t)((f >> 1) - 1) & 1u, failed))) continue;
+      mbar_arrive_expect_tx(&sm.fixed_full[f & 1], B ? kTileBytes : 2 * Rq * 128);
+      if (B) keys(sm.fixed[f & 1], it, it.at, &sm.fixed_full[f & 1]);
+      else queries(sm.fixed[f & 1], it, it.at, &sm.fixed_full[f & 1]);
+      ++f;
+      for (int u = it.j0; u < it.j1; ++u, ++k) {
+        const int st = k % kRing;
+        if (k >= kRing && !(ok = role_wait(&sm.ring_empty[st], (uint32_t)(k / kRing - 1) & 1u, failed))) break;
+        mbar_arrive_expect_tx(&sm.ring_full[st], B ? 2 * Rq * 128 + kRec * 4 : kTileBytes);
+        if (B) {
+          queries(sm.ring[st], it, it.first + u * p.qt, &sm.ring_full[st]);
+          bulk_g2s(sm.rec[st], j.rec + (size_t)(it.tile + u) * kRec, kRec * 4, &sm.ring_full[st], policy_evict_first());
+        } else {
+          keys(sm.ring[st], it, u * kRows, &sm.ring_full[st]);
         }
       }
-      if (!ok) {  // no copy may be in flight when the CTA ends
-        for (int u = max(0, f - 2); u < f; ++u) mbar_wait_bounded(&sm.fixed_full[u & 1], (uint32_t)(u >> 1) & 1u);
-        for (int u = max(0, k - kRing); u < k; ++u) mbar_wait_bounded(&sm.ring_full[u % kRing], (uint32_t)(u / kRing) & 1u);
-      }
+    }
+    if (!ok) {  // no copy may be in flight when the CTA ends
+      for (int u = max(0, f - 2); u < f; ++u) mbar_wait_bounded(&sm.fixed_full[u & 1], (uint32_t)(u >> 1) & 1u);
+      for (int u = max(0, k - kRing); u < k; ++u) mbar_wait_bounded(&sm.ring_full[u % kRing], (uint32_t)(u / kRing) & 1u);
     }
   } else if (warp == kIssueWarp) {
     // ---------------------------------------------------------------- products
@@ -285,10 +301,8 @@ __global__ void __launch_bounds__(kThreads, 1) observe_kernel(const __grid_const
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t ph) { return __all_sync(0xffffffffu, role_wait(bar, ph, failed)) != 0; };
     int f = 0, k = 0;
-    for (int i = 0; ok; ++i) {
-      const long long idx = item_at(i);
-      if (idx >= items) break;
-      const Item it = find_item<B>(p, sm, (int)idx);
+    Item it;
+    for (int i = 0; ok && next_item<B>(p, sm, i, it); ++i) {
       if (it.j0 >= it.j1) continue;
       if (!(ok = wait(&sm.fixed_full[f & 1], (uint32_t)(f >> 1) & 1u))) break;
       const uint64_t a = da + (uint64_t)(uniform(f & 1) * (kTileBytes >> 4));
@@ -321,18 +335,17 @@ __global__ void __launch_bounds__(kThreads, 1) observe_kernel(const __grid_const
     int k = 0;
     // A wait that gives up ends this warp's work, not its part in the barriers below: every warp goes through all items.
     int i = 0;
-    for (;; ++i) {
-      const long long idx = item_at(i);
-      if (idx >= items) break;
-      const Item it = find_item<B>(p, sm, (int)idx);
+    Item it;
+    for (; next_item<B>(p, sm, i, it); ++i) {
       float base = -INFINITY;
       uint64_t l2[2] = {0ull, 0ull};
-      for (int u = it.j0; u < it.j1; ++u, ++k) {
-        if (k % kGroups != grp || !ok) continue;
-        const int st = grp;
-        ok = __all_sync(0xffffffffu, role_wait(&sm.s_full[st], (uint32_t)(k / kRing) & 1u, failed));
-        if (B && ok) ok = __all_sync(0xffffffffu, role_wait(&sm.ring_full[st], (uint32_t)(k / kRing) & 1u, failed));
-        if (!ok) continue;
+      const int k0 = k;
+      k += max(0, it.j1 - it.j0);
+      for (int at = k0 + ((grp - k0) & (kGroups - 1)); at < k && ok; at += kGroups) {  // step at: this group's
+        const int u = it.j0 + at - k0, st = grp;
+        ok = __all_sync(0xffffffffu, role_wait(&sm.s_full[st], (uint32_t)(at / kRing) & 1u, failed));
+        if (B && ok) ok = __all_sync(0xffffffffu, role_wait(&sm.ring_full[st], (uint32_t)(at / kRing) & 1u, failed));
+        if (!ok) break;
         tc_fence_after();
         if (!B) {
           const int hi = it.at + row / G - u * kRows;  // seen: columns up to hi
@@ -415,11 +428,13 @@ __global__ void __launch_bounds__(kThreads, 1) observe_kernel(const __grid_const
           if (B) mbar_arrive(&sm.ring_empty[st]);
         }
       }
-      // the groups' sums are joined in the first one
+      // The groups' sums are joined in one of them, each in its turn. The others leave theirs without waiting, two items deep:
+      // whoever joined item i - 2 knows that its place is free.
       float l = (f2lo(l2[0]) + f2hi(l2[0])) + (f2lo(l2[1]) + f2hi(l2[1]));
-      if (grp > 0) {  // left for group 0 without waiting for it, two items deep
-        if (i >= 2) named_barrier(kFreeBar + (i & 1), 128 * kGroups);
-        sm.join[i & 1][grp - 1][row] = make_float2(base, l);
+      const int to = i % kGroups;
+      if (i >= 2 && grp != (i - 2) % kGroups) named_barrier(kFreeBar + (i & 1), 128 * kGroups);
+      if (grp != to) {
+        sm.join[i & 1][(grp - to - 1) & (kGroups - 1)][row] = make_float2(base, l);
         named_arrive(kFullBar + (i & 1), 128 * kGroups);
         continue;
       }
@@ -433,8 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1) observe_kernel(const __grid_const
         for (int q = 0; q < kGroups - 1; ++q) l += other[q].y;
         const int key = it.at + row;
         if (key < it.n) {
-          const int sid = j.seq_ids ? j.seq_ids[it.b] : it.b;
-          const size_t at = ((size_t)sid * j.Hkv + it.h) * j.mass_len + key;
+          const size_t at = ((size_t)it.sid * j.Hkv + it.h) * j.mass_len + key;
           j.mass[at] = l;
           j.ids[at] = key;
         }
@@ -452,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1) observe_kernel(const __grid_const
         } else {
           bool bad;
           const float na = minus_a(M, l, bad);
-          const bool any = named_barrier_or(kRecBar, 128, bad);
+          const bool any = named_barrier_or(kRecBar + grp, 128, bad);
           float* const rec = j.rec + (size_t)it.tile * kRec;
           rec[row] = na;
           if (row == 0) rec[kRows] = any ? 1.0f : 0.0f;
@@ -460,8 +474,8 @@ __global__ void __launch_bounds__(kThreads, 1) observe_kernel(const __grid_const
         }
       }
     }
-    if (grp > 0)  // group 0's arrivals for the last two items
-      for (int e = max(0, i - 2); e < i; ++e) named_barrier(kFreeBar + (e & 1), 128 * kGroups);
+    for (int e = max(0, i - 2); e < i; ++e)  // the arrivals for the last two items
+      if (grp != e % kGroups) named_barrier(kFreeBar + (e & 1), 128 * kGroups);
   }
   __syncwarp();
   tc_fence_before();
