@@ -34,7 +34,7 @@
 //   mass    one row per query head. Its weights are added to what every cached token has gathered, so scores are wanted
 //           to fp32: q~ enters as two fp16 parts (22 bits), a second chain of products over the same codes. The scores go
 //           to the workspace, [segment][row][position]; mass_kernel joins the partials and turns the scores into weights. (Reading the keys a second time instead would move 68 bytes a token and head, scores 40 at 5 rows.)
-// (64 sequences of 5,000-16,384 tokens: window 4,096 with 64 first tokens 44 us; mass 97 us, of which the floor is 21 and 47.)
+// (64 sequences of 5,000-16,384 tokens: window 4,096 with 64 first tokens 45 us; mass 101 us, of which the floor is 21 and 47.)
 
 #include <algorithm>
 #include <cmath>

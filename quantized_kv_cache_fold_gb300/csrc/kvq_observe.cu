@@ -5,23 +5,26 @@
 //
 // The sums a are needed before the first weight, so the scores are computed twice (2 x 128 operations a pair each time;
 // keeping them would move 8 bytes a pair instead). Both passes are one kernel: a fixed tile of 128 rows stays, tiles of the
-// other side stream through a ring, one thread has one row of the fixed side and all sums stay in it:
+// other side stream through a ring, one thread of each group has one row of the fixed side and keeps its sum:
 //
 //   pass A  fixed: 128 / G tokens of queries with all G heads of a KV head; streamed: keys. Thread = query row: base and sum.
 //           Few query tiles see long prompts, so their keys are split over `nsplit` items, joined by join_kernel.
 //   pass B  fixed: 128 keys; streamed: query tiles, each with its a. Thread = key: the sum over all rows, written once.
 //
 // a's rounding is the only one beside those of the scores and of the power of two. tcgen05 products into four score tiles of
-// tensor memory, which four groups of four warps take in turns; their sums meet in group 0 at an item's end (two groups: 149
-// us, four: 138, sums left without waiting and ten items an SM: 127, for the 8 prompts below).
+// tensor memory, which four groups of four warps take in turns; an item's four sums meet in one of the groups. For the 8
+// prompts below: two groups 149 us, four 138; sums left without waiting and ten items an SM 127; items looked up a warp at a
+// time and joined by the groups in turn 113.
 //
 //   warps 0-3, 4-7, 8-11, 12-15  scores to sums (a lane of tensor memory each), every fourth step
 //   warp 16                      tensor-map copies
 //   warp 17                      the products (one issuing thread)
 //
-// 8 prompts of 2,000-32,768 tokens, 20/4 heads, last 64 rows: 127 us; 4 of up to 700, last 16: 14 us. No unit is full (a 128 x
-// 128 tile: 512 cycles of the power of two, 512 of products, about 880 all in all); bundles of four fixed tiles, which
-// stream every key once, were slower (142; with a scheduling warp 136, but the short prompts then 22).
+// 8 prompts of 2,000-32,768 tokens, 20/4 heads, last 64 rows: 113 us; 4 of up to 700, last 16: 14 us. No unit is full: a 128 x
+// 128 tile takes 1,150 cycles in pass A and 1,450 in pass B, the power of two 512 of them (32 a cycle and SM) and the products
+// as many. The rest is the way from copy to product to sum and back with four score tiles, and pass B's items of three steps.
+// Tried: bundles of four fixed tiles that stream every key once (142; with a scheduling warp 136, but the short prompts then
+// 22), query tiles that stay through pass B (117), four places for the sums (115).
 
 #include <algorithm>
 #include <mutex>
@@ -511,8 +514,8 @@ __global__ void __launch_bounds__(kRows) join_kernel(const float2* part, float* 
 std::mutex g_observe_mu;  // guards the cache below
 bool g_observe_attr[64][4] = {{false}};
 
-// Query tiles of a call at most, and the splits of their keys: enough for ten items an SM (16: 138 us, six: 135, ten: 129) while every item keeps about four
-// blocks of keys.
+// Query tiles of a call at most, and the splits of their keys: enough for ten items an SM (before the last two steps above:
+// six 135 us, ten 129, sixteen 138) while every item keeps about four blocks of keys.
 void plan(int T, int B, int Hq, int Hkv, int rows, int& tiles, int& nsplit) {
   const int qt = kRows / (Hq / Hkv);
   const long long seen = rows > 0 ? std::min<long long>(T, (long long)B * rows) : T;
