@@ -578,8 +578,8 @@ typedef struct kvq_token_mass {
  *   workspace: device, >= kvq_mass_workspace_bytes(B, num_q_heads, num_kv_heads, max_pages_per_seq), 256-byte aligned
  *             (4 bytes for every query head and slot: the scores of the call).
  *   Precision of the weights: q~ enters the scores in two fp16 parts (2^-22 of the value), sums are fp32, in an order that
- *   does not depend on timing. A row that is NaN (see kvq_tree_attn_int4) adds nothing; neither do slots of a page outside
- *   the pool.
+ *   does not depend on timing. A row that is NaN (see kvq_tree_attn_int4) adds nothing; slots of a page outside the
+ *   pool, and all of a sequence whose length is outside its block table (KVQ_DEVERR_POS), are left as they were.
  *   mass and ids must not overlap one another, the inputs or out. Other arguments, limits and errors as
  *   kvq_decode_attn_int4 with S = 1.
  * Requires B*num_kv_heads*max_pages_per_seq <= 2^31.

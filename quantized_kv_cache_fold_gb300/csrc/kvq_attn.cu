@@ -2115,7 +2115,7 @@ __global__ void __launch_bounds__(kMassThreads, 4) mass_kernel(const AttnParams 
         old = *reinterpret_cast<const float4*>(mass + pos);
         phys = p.block_table[(size_t)b * p.max_pages + pos / kPage];
       }
-      if (!in_pool) continue;
+      if (!in_pool || bad) continue;  // (a length outside the cache: nothing was appended, slots keep what they gathered)
       if (here + 3 < ctxb) {
         *reinterpret_cast<float4*>(m) = make_float4(o[0] + w[0], o[1] + w[1], o[2] + w[2], o[3] + w[3]);
       } else {

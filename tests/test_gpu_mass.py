@@ -194,6 +194,22 @@ def test_lengths_outside_the_cache():
     assert torch.equal(c.held["mass"][0, :, 1:], c.before[0, :, 1:])
 
 
+def test_a_full_sequence_keeps_what_it_gathered():
+    """The token that finds no slot is not appended, and the slots' masses and numbers stay."""
+    c = MassCase([127, 100], 10, 2, seed=18)
+    c.append()
+    pages = c.tensors["pages"].clone()
+    full = 64 * c.tensors["block_table"].shape[1]
+    for n in (full, full + 1, 1 << 30):
+        c.ctx_t[0] = n
+        c.err.zero_()
+        c.held["mass"].copy_(c.before)
+        c.run(want_err=kvq.DEVERR_POS)
+        assert torch.equal(c.held["mass"][0], c.before[0]) and bool((c.held["ids"][0] == -7).all())
+        assert torch.equal(c.tensors["pages"], pages)
+        assert not torch.equal(c.held["mass"][1], c.before[1])
+
+
 def test_other_rows_stay():
     """A mass of more sequences and slots than the call's."""
     c = MassCase([200, 90], 10, 2, seed=14)
