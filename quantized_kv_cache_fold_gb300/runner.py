@@ -207,11 +207,12 @@ class DecodeStack:
         L.window, L.sinks = window, sinks
 
     def keep_mass(self, layers=None):
-        """From here on the int4 layers `layers` (None: all without a window) keep what their slots gather, and can evict."""
+        """From here on the int4 layers `layers` (None: all without a window) keep what their slots gather, and can evict. Layers
+        that do already go on."""
         layers = [l for l in self.int4_layers() if not self.layers[l].window] if layers is None else layers
         if any(not isinstance(self.layers[l], Int4Layer) or self.layers[l].window for l in layers):
             raise ValueError("mass is kept by int4 layers without a window")
-        for l in layers:
+        for l in set(layers) - set(self.mass_layers()):
             self.layers[l].held, self.layers[l].mass = alloc_token_mass(self.B, self.Hkv, self.max_pages, self.device)
         self.mass_workspace = alloc_mass_workspace(self.B, self.Hq, self.Hkv, self.max_pages * PAGE_SIZE, self.device)
 
@@ -220,6 +221,8 @@ class DecodeStack:
 
     def observe_prompt(self, l, q, k, cu_seqlens, rows, seq_ids=None, workspace=None, stream=None):
         """Layer l's mass starts from the weights of each prompt's last `rows` rows; q and k as prompt_layer takes them."""
+        if l not in self.mass_layers():
+            raise ValueError("a layer that keeps no mass")
         if workspace is None:
             workspace = self._alloc_for(stream, alloc_prompt_mass_workspace, q.shape[0], cu_seqlens.shape[0] - 1, self.Hq, self.Hkv, rows)
         kvq_prompt_mass(q, k, cu_seqlens, rows, self.layers[l].mass, workspace, self.dev_err, seq_ids=seq_ids, stream=stream)
@@ -228,6 +231,8 @@ class DecodeStack:
         """Every layer that keeps mass evicts down to `budget` tokens a sequence and KV head (kvq_evict_int4); ctx_out: the
         new lengths."""
         layers = [self.layers[l] for l in self.mass_layers()]
+        if not layers:
+            raise ValueError("no layer keeps mass")
         for i in range(0, len(layers), MAX_CACHES):  # as many layers as a call takes
             some = layers[i:i + MAX_CACHES]
             kvq_evict_int4([L.cache for L in some], [L.mass for L in some], ctx, seen, budget, sinks, recent, self.dev_err,

@@ -139,6 +139,20 @@ def test_layers_of_a_kind():
             st.decode_layer(l, None, None, None, q_rot_out=1)
 
 
+def test_stacks_that_keep_no_mass_and_masses_kept_twice():
+    st = DecodeStack(1, 4, 2, 1, 2, n_layers=4, full_every=2, window=64, ring_capacity=64)
+    with pytest.raises(ValueError):
+        st.evict(None, None, 10, 1, 2, None)
+    st.keep_mass([1])
+    for l in (0, 3):
+        with pytest.raises(ValueError):
+            st.observe_prompt(l, None, None, None, 4)
+    held = st.layers[1].held["mass"]
+    held.fill_(2.0)
+    st.keep_mass()
+    assert st.mass_layers() == [1, 3] and st.layers[1].held["mass"] is held and bool((held == 2.0).all())
+
+
 def test_more_layers_than_a_call_takes(monkeypatch):
     calls = []
     monkeypatch.setattr(runner, "kvq_evict_int4", lambda caches, masses, *a, ctx_out, stream: calls.append((list(caches), list(masses), ctx_out, stream)))
