@@ -20,11 +20,13 @@
 //   warp 16                      tensor-map copies
 //   warp 17                      the products (one issuing thread)
 //
-// 8 prompts of 2,000-32,768 tokens, 20/4 heads, last 64 rows: 113 us; 4 of up to 700, last 16: 14 us. No unit is full: a 128 x
-// 128 tile takes 1,150 cycles in pass A and 1,450 in pass B, the power of two 512 of them (32 a cycle and SM) and the products
-// as many. The rest is the way from copy to product to sum and back with four score tiles, and pass B's items of three steps.
+// 8 prompts of 2,000-32,768 tokens, 20/4 heads, last 64 rows: 113 us; 4 of up to 700, last 16: 13 us (14.5 with
+// tensor memory taken and pass B's start behind the wait for the grid before). A pass's first 8,000 cycles go by before its
+// first sums; then a 128 x 128 tile takes 1,100 cycles in pass A and 1,350 in pass B, of which the power of two (32 a cycle
+// and SM) and the products need 512 each, and no unit is full.
 // Tried: bundles of four fixed tiles that stream every key once (142; with a scheduling warp 136, but the short prompts then
-// 22), query tiles that stay through pass B (117), four places for the sums (115).
+// 22), query tiles that stay through pass B (117), four places for the sums (115), a score tile for two groups at once (114),
+// 16 columns loaded ahead (124).
 
 #include <algorithm>
 #include <mutex>
@@ -248,10 +250,16 @@ __global__ void __launch_bounds__(kThreads, 1) observe_kernel(const __grid_const
       reinterpret_cast<uint4*>(sm.ring[i / per >> 1] + (i / per & 1) * (kTileBytes / 2) + used * 128)[i % per] = make_uint4(0u, 0u, 0u, 0u);
     fence_proxy_async_shared();
   }
-  griddep_wait();
+  if (warp == kCopyWarp && lane == 0) {
+    prefetch_tensor_map(&p.mq);
+    prefetch_tensor_map(&p.mk);
+  }
+  if (warp == kIssueWarp) tmem_alloc_512(&sm.taddr);
+  // Pass B needs of what may still run only the records, and waits before it copies the first: whatever came before the
+  // call had ended when pass A let its successors start.
+  if (!B) griddep_wait();
   griddep_launch_dependents();
   lay_out<B>(p, sm);
-  if (warp == kIssueWarp) tmem_alloc_512(&sm.taddr);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -279,6 +287,10 @@ __global__ void __launch_bounds__(kThreads, 1) observe_kernel(const __grid_const
       if (B) keys(sm.fixed[f & 1], it, it.at, &sm.fixed_full[f & 1]);
       else queries(sm.fixed[f & 1], it, it.at, &sm.fixed_full[f & 1]);
       ++f;
+      if (B && k == 0) {
+        griddep_wait();
+        fence_proxy_async_global();
+      }
       for (int u = it.j0; u < it.j1; ++u, ++k) {
         const int st = k % kRing;
         if (k >= kRing && !(ok = role_wait(&sm.ring_empty[st], (uint32_t)(k / kRing - 1) & 1u, failed))) break;
@@ -291,6 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1) observe_kernel(const __grid_const
         }
       }
     }
+    if (B && k == 0) griddep_wait();  // (no record wanted: nothing that comes behind this grid may overtake pass A)
     if (!ok) {  // no copy may be in flight when the CTA ends
       for (int u = max(0, f - 2); u < f; ++u) mbar_wait_bounded(&sm.fixed_full[u & 1], (uint32_t)(u >> 1) & 1u);
       for (int u = max(0, k - kRing); u < k; ++u) mbar_wait_bounded(&sm.ring_full[u % kRing], (uint32_t)(u / kRing) & 1u);

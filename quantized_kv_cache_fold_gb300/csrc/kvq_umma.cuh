@@ -41,6 +41,11 @@ constexpr float kBaseLag = 8.0f, kWeightRaise = 7.0f;
 // Keeps values loaded by tmem_ld*u from being used before the wait after the loads.
 __device__ __forceinline__ void tmem_wait_ld_all() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
+// Fetches a tensor map ahead of its first copy.
+__device__ __forceinline__ void prefetch_tensor_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
 // Box of a 3-D tensor map at (x, y, z) into shared memory, completion counted on `bar`.
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
   asm volatile(
