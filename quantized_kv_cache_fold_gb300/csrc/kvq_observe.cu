@@ -20,13 +20,13 @@
 //   warp 16                      tensor-map copies
 //   warp 17                      the products (one issuing thread)
 //
-// 8 prompts of 2,000-32,768 tokens, 20/4 heads, last 64 rows: 113 us; 4 of up to 700, last 16: 13 us (14.5 with
+// 8 prompts of 2,000-32,768 tokens, 20/4 heads, last 64 rows: 111 us; 4 of up to 700, last 16: 13 us (14.5 with
 // tensor memory taken and pass B's start behind the wait for the grid before). A pass's first 8,000 cycles go by before its
 // first sums; then a 128 x 128 tile takes 1,100 cycles in pass A and 1,350 in pass B, of which the power of two (32 a cycle
 // and SM) and the products need 512 each, and no unit is full.
 // Tried: bundles of four fixed tiles that stream every key once (142; with a scheduling warp 136, but the short prompts then
 // 22), query tiles that stay through pass B (117), four places for the sums (115), a score tile for two groups at once (114),
-// 16 columns loaded ahead (124).
+// 16 columns loaded ahead (124), a maximum looked for only when a sum passes 2^30 (112).
 
 #include <algorithm>
 #include <mutex>
