@@ -611,7 +611,8 @@ kvq_status kvq_mass_attn_int4_fwht(const kvq_int4_cache* cache, const kvq_token_
  *   workspace: device, >= kvq_prompt_mass_workspace_bytes(T, B, num_q_heads, num_kv_heads, rows), 256-byte aligned;
  *             contents need no initialisation.
  *   Precision: products of the 16-bit inputs summed in fp32, weights and sums fp32, in an order that does not depend on
- *   timing. A row that is not finite (a query, or a key that it sees) adds nothing.
+ *   timing. A row whose softmax is NaN (a score that is NaN or +inf, or none above -inf) adds nothing; a score of -inf beside
+ *   others is a weight of 0.
  * Requires num_q_heads/num_kv_heads <= 64 and otherwise the sizes of kvq_prompt_attn; mass and ids overlap no input.
  */
 size_t kvq_prompt_mass_workspace_bytes(int T, int B, int num_q_heads, int num_kv_heads, int rows);

@@ -421,7 +421,11 @@ __global__ void __launch_bounds__(kThreads, 1) observe_kernel(const __grid_const
               na[4 * e + 3] = v.w;
             }
             tmem_wait_ld_all();
-            if (m == ~0u && !odd) {
+            // Rows of zeros fill the end of a whole tile where G does not divide 128, so a quarter that has any ends with one:
+            // its product is NaN for a key with an infinite or NaN element, also where all rows in use have finite sums (scores
+            // of -inf), and only the masked form below leaves it out.
+            const bool nan = (s[31] & 0x7FFFFFFFu) > 0x7F800000u;
+            if (m == ~0u && !odd && !nan) {
 #pragma unroll
               for (int e = 0; e < 16; ++e) {
                 const uint64_t x = fma_f2(f2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), c2, f2(na[2 * e], na[2 * e + 1]));
