@@ -64,6 +64,7 @@ class DecodeStack:
                 tensors, ring = alloc_fp8_ring(B, Hkv, ring_capacity, device)
                 self.layers.append(SwaLayer(tensors, ring, swa_k_scale, swa_v_scale, window))
         self.workspace = alloc_workspace(B, S, Hq, Hkv, device)
+        self.mass_workspace = None  # keep_mass
         self.dev_err = torch.zeros(1, dtype=torch.int32, device=device)
 
     def int4_layers(self):
@@ -140,8 +141,8 @@ class DecodeStack:
     # ---- around decoding
 
     def _alloc_for(self, stream, alloc, *sizes):
-        """A workspace allocated in the order of the stream that will use it (None: the current one; else a stream or its
-        raw handle), so that the allocator hands its memory to nothing else before that stream is done with it."""
+        """A workspace (or what layers keep) allocated in the order of the stream that will use it (None: the current one; else a
+        stream or its raw handle), so that the allocator hands its memory to nothing else before that stream is done with it."""
         if stream is None:
             return alloc(*sizes, self.device)
         if isinstance(stream, int):
@@ -206,15 +207,17 @@ class DecodeStack:
             raise ValueError("a window is of an int4 layer that keeps no mass, its sizes not negative")
         L.window, L.sinks = window, sinks
 
-    def keep_mass(self, layers=None):
+    def keep_mass(self, layers=None, stream=None):
         """From here on the int4 layers `layers` (None: all without a window) keep what their slots gather, and can evict. Layers
-        that do already go on."""
+        that do already go on, and the workspace of the steps stays where it is, so that steps in flight and captured ones may.
+        stream: the one that prompts and steps will run on (None: the current one); what they need is laid out in its order."""
         layers = [l for l in self.int4_layers() if not self.layers[l].window] if layers is None else layers
         if any(not isinstance(self.layers[l], Int4Layer) or self.layers[l].window for l in layers):
             raise ValueError("mass is kept by int4 layers without a window")
+        if self.mass_workspace is None:
+            self.mass_workspace = self._alloc_for(stream, alloc_mass_workspace, self.B, self.Hq, self.Hkv, self.max_pages * PAGE_SIZE)
         for l in set(layers) - set(self.mass_layers()):
-            self.layers[l].held, self.layers[l].mass = alloc_token_mass(self.B, self.Hkv, self.max_pages, self.device)
-        self.mass_workspace = alloc_mass_workspace(self.B, self.Hq, self.Hkv, self.max_pages * PAGE_SIZE, self.device)
+            self.layers[l].held, self.layers[l].mass = self._alloc_for(stream, alloc_token_mass, self.B, self.Hkv, self.max_pages)
 
     def mass_layers(self):
         return [l for l in self.int4_layers() if self.layers[l].mass is not None]
