@@ -557,6 +557,9 @@ kvq_status kvq_window_attn_int4_fwht(const kvq_int4_cache* cache, const float* w
  * mass: device float [num_seqs][num_kv_heads][max_tokens], 16-byte aligned; ids: device int32 of the same shape.
  * max_tokens: a multiple of 4, at least 64*max_pages_per_seq of the cache. The calls read and write only slots below a
  * sequence's length (a mass call: the new token's too).
+ * kvq_mass_attn_int4, kvq_prompt_mass and kvq_evict_int4 keep them; no other call does. Where another one puts tokens into
+ * slots (kvq_rotate_quant_append, a decode, window or tree call with new rows, kvq_tree_commit_int4, kvq_pages_fork), the caller
+ * sets mass and ids there before the next eviction: what they held may be of tokens that have left, or of a session before.
  */
 typedef struct kvq_token_mass {
   float* mass;

@@ -4,7 +4,8 @@ Holds, per layer, the device state of the rotated int4 path (page pool, block ta
 M_q/M_k) or of the FP8 sliding-window path (ring), plus one shared workspace and error
 word; `decode_step` runs every layer of one decode step through the C ABI, in model
 order (Kolibri-1: 50 layers, every fifth one full attention; "Serving Kolibri-1 with a
-4-bit KV cache", section "What we do"). Torch is used for device memory only.
+4-bit KV cache", section "What we do"). Torch is used for device memory and the values that it
+starts with.
 """
 
 from __future__ import annotations
@@ -33,6 +34,7 @@ class Int4Layer:
     sinks: int = 0
     held: dict = None     # keep_mass: what the cache's slots have gathered, and its descriptor
     mass: object = None
+    observed: bool = False  # observe_prompt sets masses of this layer
 
 
 @dataclass
@@ -93,9 +95,32 @@ class DecodeStack:
         L.Mq = torch.from_numpy(Mq).to(self.device)
         L.Mk = torch.from_numpy(Mk).to(self.device)
 
-    def append_int4(self, l, k, v, seq_ids, positions, stream=None):
+    def append_int4(self, l, k, v, seq_ids, positions, stream=None, slots=None, fresh=None):
+        """Tokens into the cache of int4 layer l, each at its position; in a layer that keeps mass at slots (None: the
+        positions), where evictions have made the two differ. There the slots' masses start with the tokens: a slot that holds
+        another number than the token's gets that number, and no mass. fresh: so does every slot, whatever its number (a new
+        session in a row that another has used); None: unless prompts of this layer are observed, where the call that
+        observes them sets the masses, before this one or after it."""
         L = self.layers[l]
-        kvq_rotate_quant_append(L.cache, L.Mk, k, v, seq_ids, positions, self.dev_err, stream=stream, fwht=L.fwht)
+        if L.mass is None or slots is None:
+            slots = positions
+        kvq_rotate_quant_append(L.cache, L.Mk, k, v, seq_ids, slots, self.dev_err, stream=stream, fwht=L.fwht)
+        if L.mass is not None and k.shape[0]:
+            self._on(stream, self._start_masses, L.held["mass"], L.held["ids"], seq_ids, slots, positions,
+                     not L.observed if fresh is None else fresh)
+
+    @staticmethod
+    def _start_masses(mass, ids, seq_ids, slots, numbers, fresh):
+        B, Hkv, N = mass.shape
+        ok = (seq_ids >= 0) & (seq_ids < B) & (slots >= 0) & (slots < N)
+        # the append flags tokens with no place and passes them over; here they do what the first good one does, or (where
+        # none is good) leave some place as it is
+        use = torch.where(ok, torch.arange(ok.shape[0], device=ok.device), ok.to(torch.int32).argmax())
+        row, slot = seq_ids[use].clamp(0, B - 1).long(), slots[use].clamp(0, N - 1).long()
+        at = (row[:, None], torch.arange(Hkv, device=ok.device)[None], slot[:, None])
+        new = ok[use][:, None] & (fresh | (ids[at] != numbers[use][:, None]))
+        mass[at] = torch.where(new, 0.0, mass[at])
+        ids[at] = torch.where(new, numbers[use][:, None], ids[at])
 
     def prefill_int4(self, l, ctx, fill, chunk_tokens=16384, bf16=True):
         """Append positions 0..ctx[b]-1 of every sequence; fill(b, pos0, T, k_out, v_out) writes the
@@ -143,12 +168,16 @@ class DecodeStack:
     def _alloc_for(self, stream, alloc, *sizes):
         """A workspace (or what layers keep) allocated in the order of the stream that will use it (None: the current one; else a
         stream or its raw handle), so that the allocator hands its memory to nothing else before that stream is done with it."""
+        return self._on(stream, alloc, *sizes, self.device)
+
+    @staticmethod
+    def _on(stream, f, *args):
         if stream is None:
-            return alloc(*sizes, self.device)
+            return f(*args)
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream)
         with torch.cuda.stream(stream):
-            return alloc(*sizes, self.device)
+            return f(*args)
 
     def prompt_layer(self, l, q, k, v, cu_seqlens, out, workspace=None, stream=None):
         """Attention of whole prompts, packed end to end, in layer l (windowed in a sliding-window layer);
@@ -160,12 +189,13 @@ class DecodeStack:
         kvq_prompt_attn(q, k, v, cu_seqlens, out, workspace, self.dev_err, window=L.window,
                         sinks=L.sinks if isinstance(L, Int4Layer) else 0, stream=stream)
 
-    def append_prompt(self, l, k, v, seq_ids, positions, stream=None):
+    def append_prompt(self, l, k, v, seq_ids, positions, stream=None, slots=None, fresh=None):
         """Keys (pre-norm in a full-attention layer) and values of prompt tokens into layer l's cache. A ring keeps
-        the last `capacity` positions of a sequence: pass no more of them in one call."""
+        the last `capacity` positions of a sequence: pass no more of them in one call. slots, fresh: of layers that keep
+        mass, as append_int4 takes them."""
         L = self.layers[l]
         if isinstance(L, Int4Layer):
-            self.append_int4(l, k, v, seq_ids, positions, stream=stream)
+            self.append_int4(l, k, v, seq_ids, positions, stream=stream, slots=slots, fresh=fresh)
         else:
             kvq_fp8_append(L.ring, k, v, seq_ids, positions, L.k_scale, L.v_scale, self.dev_err, stream=stream)
 
@@ -226,6 +256,7 @@ class DecodeStack:
         """Layer l's mass starts from the weights of each prompt's last `rows` rows; q and k as prompt_layer takes them."""
         if l not in self.mass_layers():
             raise ValueError("a layer that keeps no mass")
+        self.layers[l].observed = True
         if workspace is None:
             workspace = self._alloc_for(stream, alloc_prompt_mass_workspace, q.shape[0], cu_seqlens.shape[0] - 1, self.Hq, self.Hkv, rows)
         kvq_prompt_mass(q, k, cu_seqlens, rows, self.layers[l].mass, workspace, self.dev_err, seq_ids=seq_ids, stream=stream)
