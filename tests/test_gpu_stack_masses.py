@@ -298,3 +298,40 @@ def test_a_captured_append_starts_masses():
         mass[1, :, 70:110], ids[1, :, 70:110] = 3.0, -5
         assert bool((mass == 3.0).all()) and bool((ids == -5).all())
     assert st.read_error() == 0
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(20, 4), (2, 2)])
+def test_every_step_gathers_a_row_of_weights_a_query_head(Hq, Hkv):
+    """decode_step over all layers, after an eviction of observed prompts: what the heads of a group put out adds up to their
+    number, step by step, beside what the prompts' rows had left."""
+    B, lens, G = 2, [300, 260], Hq // Hkv
+    s = Session(B, 6, n_layers=6, Hq=Hq, Hkv=Hkv, seed=7)
+    st = s.st
+    st.set_int4_window(3, 100, 7)
+    st.keep_mass()
+    T = sum(lens)
+    row, pos = i32([b for b in range(B) for _ in range(lens[b])]), i32([p for b in range(B) for p in range(lens[b])])
+    for l in range(6):
+        q, k, v = s.rand(T, Hq, D), s.rand(T, Hkv, D), s.rand(T, Hkv, D)
+        keep = torch.ones_like(pos, dtype=torch.bool) if l in st.int4_layers() else pos >= i32(lens)[row.long()] - 100
+        if l in st.mass_layers():
+            st.observe_prompt(l, q, k, i32([0, lens[0], T]), 32)
+        st.append_prompt(l, k[keep].contiguous(), v[keep].contiguous(), row[keep].contiguous(), pos[keep].contiguous())
+    st.evict(i32(lens), i32(lens), 200, 4, 16, out := i32([0] * B))
+    ctx, seen = out.tolist(), list(lens)
+
+    def sums():
+        return torch.stack([torch.stack([st.layers[l].held["mass"][b, :, :ctx[b]].double().sum(-1) for b in range(B)]) for l in st.mass_layers()])
+
+    at = sums()
+    assert float(at.min()) > G  # the prompts' rows
+    for _ in range(10):
+        qs, outs, ks, vs = s.step_inputs()
+        st.decode_step(qs, i32(ctx), outs, ks, vs, positions=i32(seen))
+        ctx, seen = [c + 1 for c in ctx], [c + 1 for c in seen]
+        was, at = at, sums()
+        # a row's weights add up to 1 but for the powers of two and the division (2^-19), the stored scores (half a step of
+        # values below 32, times ln 2: 2^-20) and the sum below the division (300 half steps); a mass's addition takes half a
+        # step of it, and all masses of a head are 32 G + 10 G at most
+        assert float((at - was - G).abs().max()) < G * (2.0 ** -19 + 2.0 ** -20 + 300 * 2.0 ** -24) + 42 * G * 2.0 ** -24
+    assert st.read_error() == 0
