@@ -220,7 +220,10 @@ class DecodeStack:
                             None if v_news is None else v_news[l], stream=stream)
 
     def commit_tree(self, ctx, path, n_accept, ctx_out, stream=None):
-        """The accepted branch of every tree becomes context in all layers; ctx_out: the new lengths."""
+        """The accepted branch of every tree becomes context in all layers; ctx_out: the new lengths. (Layers that keep mass
+        take no trees: records would move without their masses, and by lengths that are not theirs after an eviction.)"""
+        if self.mass_layers():
+            raise ValueError("a layer that keeps mass takes no trees, and commits none")
         for commit, layers in ((kvq_tree_commit_int4, [self.layers[l].cache for l in self.int4_layers()]),
                                (kvq_tree_commit_fp8, [self.layers[l].ring for l in self.swa_layers()])):
             for i in range(0, len(layers), MAX_CACHES):  # as many layers as a call takes

@@ -118,3 +118,20 @@ def test_layers_without_mass_append_at_the_positions(monkeypatch):
     for l in range(2):
         st.append_prompt(l, k, k, "seq", "positions", slots="slots", fresh=True)
     assert to == ["positions"] * 2
+
+
+def test_commit_is_refused_where_a_layer_keeps_mass(fake, monkeypatch):
+    """Records would move without their masses, and by lengths that are not the layer's after an eviction."""
+    calls = []
+    for name in ("kvq_tree_commit_int4", "kvq_tree_commit_fp8"):
+        monkeypatch.setattr(runner, name, lambda *a, **k: calls.append(a))
+    st = stack()
+    st.set_int4_window(1, 64, 4)
+    st.keep_mass([3])
+    with pytest.raises(ValueError):
+        st.commit_tree(None, None, None, None)
+    assert not calls
+    windows = stack()  # (verify blocks go through windows, and their records lie at their positions)
+    windows.set_int4_window(1, 64, 4)
+    windows.commit_tree("ctx", "path", "n", "out")
+    assert len(calls) == 2
