@@ -528,7 +528,11 @@ kvq_status kvq_pages_copy(const kvq_int4_cache* caches, int num_caches, int n, c
  * kvq_window_attn_int4 -- kvq_decode_attn_int4 with a window and a few first tokens that stay visible: query row r of
  *   sequence b, at position i = ctx_len[b] + r, attends to positions max(0, i-window+1)..i and to 0..min(sinks, i+1)-1
  *   (each once, where the two meet). Pages that hold neither a first token nor one of the rows' windows are not read, and
- *   their block-table entries may be anything: a session's pages between the two may be given back.
+ *   their block-table entries may be anything: a session's pages between the two may be given back (where all layers that
+ *   share the block table have such windows), by kvq_pages_free with len_old = 64*floor((ctx_len-window+1)/64) of the
+ *   next call (0 below 0) and len_new = sinks, or the len_old of the time before once that is more. A session that has given
+ *   some back ends by two such calls, from ctx_len to that len_new and from min(sinks, ctx_len) to 0 (one from ctx_len to 0,
+ *   and a fork, flag the -1 entries between), and its windows grow no wider.
  *   out:      device [B][S][num_q_heads][128] of out_dtype (KVQ_F32 or KVQ_BF16). A row that sees nothing (its pages
  *             outside the pool) gives 0.
  *   workspace: as for kvq_decode_attn_int4 (kvq_decode_workspace_bytes).
@@ -639,7 +643,8 @@ kvq_status kvq_prompt_mass(const void* q, const void* k, kvq_dtype dtype, int T,
  *             first).
  *   ctx_len, seen: device int32[B]: the cached tokens, and how many tokens the sequence has had in all.
  *   ctx_out:  device int32[B] or NULL: receives min(ctx_len[b], budget); must not overlap ctx_len or seen. The pages
- *             behind it can be given back by kvq_pages_free(.., ctx_len, ctx_out, ..).
+ *             behind it can be given back by kvq_pages_free(.., ctx_len, ctx_out, ..), once all layers that share the
+ *             block table have evicted.
  *   A length outside the block table is clamped (KVQ_DEVERR_POS). A move from or to a page outside the pool is passed over
  *   (KVQ_DEVERR_PAGE): its token is lost.
  * Requires 1 <= B <= KVQ_MAX_SEQS, budget >= 1, sinks, recent >= 0, 64*max_pages_per_seq <= KVQ_EVICT_MAX_TOKENS, ids
