@@ -589,7 +589,7 @@ typedef struct kvq_token_mass {
  *   pool, and all of a sequence whose length is outside its block table (KVQ_DEVERR_POS), are left as they were.
  *   mass and ids must not overlap one another, the inputs or out. Other arguments, limits and errors as
  *   kvq_decode_attn_int4 with S = 1.
- * Requires B*num_kv_heads*max_pages_per_seq <= 2^31.
+ * Requires B*num_kv_heads*max_pages_per_seq <= 2^31, B*(max_pages_per_seq+2) <= 2^31, max_pages_per_seq <= 2^24.
  */
 size_t kvq_mass_workspace_bytes(int B, int num_q_heads, int num_kv_heads, int max_pages_per_seq);
 kvq_status kvq_mass_attn_int4(const kvq_int4_cache* cache, const kvq_token_mass* mass, const float* Mq, const float* Mk,
@@ -647,8 +647,8 @@ kvq_status kvq_prompt_mass(const void* q, const void* k, kvq_dtype dtype, int T,
  *             block table have evicted.
  *   A length outside the block table is clamped (KVQ_DEVERR_POS). A move from or to a page outside the pool is passed over
  *   (KVQ_DEVERR_PAGE): its token is lost.
- * Requires 1 <= B <= KVQ_MAX_SEQS, budget >= 1, sinks, recent >= 0, 64*max_pages_per_seq <= KVQ_EVICT_MAX_TOKENS, ids
- * 16-byte aligned.
+ * Requires 1 <= B <= KVQ_MAX_SEQS, budget >= 1, sinks, recent >= 0, 64*max_pages_per_seq <= KVQ_EVICT_MAX_TOKENS,
+ * num_caches*B*num_kv_heads <= 2^27, ids 16-byte aligned.
  */
 #define KVQ_EVICT_MAX_TOKENS 393216
 kvq_status kvq_evict_int4(const kvq_int4_cache* caches, const kvq_token_mass* masses, int num_caches, int B,

@@ -33,8 +33,10 @@
 //           between are neither read nor counted in the split.
 //   mass    one row per query head. Its weights are added to what every cached token has gathered, so scores are wanted
 //           to fp32: q~ enters as two fp16 parts (22 bits), a second chain of products over the same codes. The scores go
-//           to the workspace, [segment][row][position]; mass_kernel joins the partials and turns the scores into weights. (Reading the keys a second time instead would move 68 bytes a token and head, scores 40 at 5 rows.)
-// (64 sequences of 5,000-16,384 tokens: window 4,096 with 64 first tokens 45 us; mass 101 us, of which the floor is 21 and 47.)
+//           to the workspace, [segment][row][position]; mass_kernel joins the partials and turns the scores into weights.
+//           (Reading the keys a second time instead would move 68 bytes a token and head, scores 40 at 5 rows.)
+// (64 sequences: window 4,096 with 64 first tokens over 5,000-16,384 tokens 45 us, floor 21; mass over 4,096-16,384 101 us,
+// floor 47; appending the new rows in the call changes neither, the FWHT prologue takes 4 us less.)
 
 #include <algorithm>
 #include <cmath>
@@ -262,8 +264,11 @@ __device__ __forceinline__ void decode_page(const int* pre, int B, int Hkv, long
 // a CTA with several tiles (the groups' states go through shared memory one after the other, about 5 us with three) is more
 // there than what the join of more partials does: 16 verify blocks of 20 rows, windows of 2,000, short and long: 48 us by
 // CTA, 34 by group. With one tile and windows it is the other way round, 44 us by CTA, 52 by group (64 sequences, windows of
-// 4,096), because the call's workspace has partials for 1,024 parts and 1,216 groups fit the GPU. Part u is that of token
-// group u / n_cta of CTA u mod n_cta, so few parts still spread over the SMs.
+// 4,096), because the call's workspace has partials for 1,024 parts and 1,216 groups fit the GPU. Mass by group and by CTA:
+// one sequence of 4,096 16.5 and 17.9 us, one of 65,536 34.4 and 25.7, 16 of 4,096-16,384 40.9 and 40.9, 64 of them 100.9
+// and 98.5, 128 of them 182.5 and 177.8; 64 of 1,000-2,000 40.2 and 45.0, 256 of 500-1,000 75.3 and 90.2: what groups cost
+// where segments are long (more partials to join) is less than what they save where they are short. Part u is that of
+// token group u / n_cta of CTA u mod n_cta, so few parts still spread over the SMs.
 __host__ __device__ constexpr bool by_group(int form, int nt) { return form == kMass || (form == kWindow && nt > 1); }
 __device__ __forceinline__ int parts_of(const AttnParams& p, long long P) {
   return (int)min((long long)(p.by_group ? min(p.n_cta * p.nkg, p.max_parts) : p.n_cta), P);
@@ -1857,7 +1862,9 @@ constexpr int kCombChunkBlock = 8;
 template <int FORM>
 __device__ __forceinline__ void combine_by_warp(const AttnParams& p, const int* cpre, int item, int lane, long long P, int n_eff) {
   constexpr bool TREE = FORM != kVerify;
-  constexpr int kChunk = FORM == kWindow ? 2 * kCombChunkWarp : kCombChunkWarp;  // a part a token group: more partials
+  // Windows: parts by token group have more partials a segment. (Eight in flight cost 52 bytes of spills; the form is the same
+  // for one row tile, whose parts are by CTA.)
+  constexpr int kChunk = FORM == kWindow ? 2 * kCombChunkWarp : kCombChunkWarp;
   const int R = p.R;
   const int seg = item / R, row = item - seg * R;
   const int b = seg / p.Hkv, h = seg - (seg / p.Hkv) * p.Hkv;

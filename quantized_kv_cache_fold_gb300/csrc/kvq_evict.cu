@@ -18,9 +18,10 @@
 // What bounds it: records lie apart (64 bytes of K, of V, and two words in lines of their own), so a move costs about 400
 // bytes of memory reads, and the moves of all pairs together run at 8 to 13 thousand a us however many are in flight; the
 // selection before it by instructions and barriers, so as many CTAs as fit share an SM: parts of up to 2,560 slots have 64
-// threads and 17 CTAs an SM. 64 sequences cut from 2,112 to 2,048 slots, 10 layers, 4 heads: 36 us of the kernel (load
-// 6, selection 5, lists 4, moves 9, all CTAs at once); 4 of 20,000-32,768 cut to 2,048: 63 us. The first form (three counting
-// passes over all 32 bits, lists by votes of 32 slots, records one after the other) took 102 and 153 us.
+// threads, 17 CTAs an SM up to 2,176 slots and 15 at 2,560. 64 sequences cut from 2,112 to 2,048 slots, 10 layers, 4 heads:
+// 36 us of the kernel (load 6, selection 5, lists 4, moves 9, all CTAs at once; the rest starts and barriers); 4 of
+// 20,000-32,768 cut to 2,048: 63 us. The first form (three counting passes over all 32 bits, lists by votes of 32 slots,
+// records one after the other) took 102 and 153 us.
 
 #include <cooperative_groups.h>
 
@@ -129,7 +130,9 @@ __device__ __forceinline__ Limit find_limit(EvictSmem<T>& s, const uint32_t* key
   for (int pass = 0;; ++pass) {
     // The first time, if it is one of the larger half, only the top 2^27 keys (16 factors of two) are told apart, and those
     // below not counted at all: masses reach far down, and the buckets of the whole range would hold too many of the upper
-    // ones (2,048 of 32,768: one pass fewer, 9 -> 7 us; 2,048 of 2,112: one more, 5 -> 10 us).
+    // ones (2,048 of 32,768: one pass fewer, 9 -> 7 us; 2,048 of 2,112, the other half: one more, 5 -> 10 us). The whole
+    // call, with and without, masses a fourth power of even ones: 655 of 32,768 (160 pairs) 50 and 56 us, 14,745 of them 142
+    // and 152; 163 of 8,192 (640 pairs) 72 and 79; 132 of 2,112 (2,560 pairs) 66 and 66; 4,096 of 65,536 (80 pairs) 83 and 81.
     const uint32_t base = pass == 0 && rank <= have / 2 && hi - lo >= 1u << 27 ? hi - ((1u << 27) - 1u) : lo;
     const int shift = max(0, 32 - kBits - __clz((int)(hi - base)));
     if (pass > 0) {
@@ -472,6 +475,12 @@ cudaError_t launch_evict(const EvictJob& job, cudaStream_t stream) {
   // are too many pairs for that, as few as hold the keys.
   auto shape = [&](int C, EvictParams& p, int& threads) {
     p.slots = ((width + C - 1) / C + 4 + 127) / 128 * 128;  // a part is at most width / C, rounded up to 4
+    // Threads by a part's slots: fewer where many small parts share an SM. Measured with 2,560 pairs cut by 64 slots: parts of
+    // 512 slots 21 us with 64 threads, 29 with 256; 1,088: 29 and 33; 2,112: 40 and 40; 2,560: 52 and 44; parts of 6,144: 62
+    // with 256, 92 with 512; 10,240: 101 and 113; 12,800: 134 and 132; cut to half 8,448: 543 and 449, 12,800: 812 and 669.
+    // The borders look at neither the pairs nor the cut: 64 threads are slower where many records move (2,112 slots cut to
+    // half: 156 us, 256 threads 119; 4,096 in clusters of two, cut by 64: 101 and 52, to half: 369 and 220) or few pairs
+    // leave SMs idle (160 pairs of 2,112 slots: 20 and 13).
     threads = p.slots <= 2560 ? 64 : p.slots <= 8448 ? 256 : kEvictMaxThreads;
     const long long by_smem = 227 * 1024 / (long long)(evict_smem(p.slots, threads) + 1024);
     return device_sms() * std::min<long long>(by_smem, resident_of(threads));

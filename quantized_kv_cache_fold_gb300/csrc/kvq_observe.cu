@@ -20,7 +20,7 @@
 //   warp 16                      tensor-map copies
 //   warp 17                      the products (one issuing thread)
 //
-// 8 prompts of 2,000-32,768 tokens, 20/4 heads, last 64 rows: 111 us; 4 of up to 700, last 16: 13 us (14.5 with
+// 8 prompts of 2,000-32,768 tokens, 20/4 heads, last 64 rows: 112 us; 4 of up to 700, last 16: 13 us (14.5 with
 // tensor memory taken and pass B's start behind the wait for the grid before). A pass's first 8,000 cycles go by before its
 // first sums; then a 128 x 128 tile takes 1,100 cycles in pass A and 1,350 in pass B, of which the power of two (32 a cycle
 // and SM) and the products need 512 each, and no unit is full.

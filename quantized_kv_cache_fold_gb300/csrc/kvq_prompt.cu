@@ -48,7 +48,7 @@
 // First tokens that stay visible: an item's blocks are those that hold them, then its window's (where the two meet, one
 // run). The blocks between are neither loaded nor multiplied. A form of its own (SINKS), so that the other keeps its code.
 // 24 prompts of 100-4,000 tokens, window 513, 64 first tokens: 181 us; one of 32,768, fp16, window 4,096, 4 first tokens:
-// 951 us, 1.36 PFLOP/s; 4 of up to 300: 13 us.
+// 940-962 us, 1.34-1.37 PFLOP/s; 4 of up to 300: 13 us.
 //
 // Work order: items by descending row tile, so the longest run first, heads of a tile next to each other (they share
 // K and V in L2); CTAs take them in turns, back and forth (c, 2n-1-c, 2n+c, ...), which evens out the descending
