@@ -561,9 +561,10 @@ kvq_status kvq_window_attn_int4_fwht(const kvq_int4_cache* cache, const float* w
  * mass: device float [num_seqs][num_kv_heads][max_tokens], 16-byte aligned; ids: device int32 of the same shape.
  * max_tokens: a multiple of 4, at least 64*max_pages_per_seq of the cache. The calls read and write only slots below a
  * sequence's length (a mass call: the new token's too).
- * kvq_mass_attn_int4, kvq_prompt_mass and kvq_evict_int4 keep them; no other call does. Where another one puts tokens into
- * slots (kvq_rotate_quant_append, a decode, window or tree call with new rows, kvq_tree_commit_int4, kvq_pages_fork), the caller
- * sets mass and ids there before the next eviction: what they held may be of tokens that have left, or of a session before.
+ * kvq_mass_attn_int4, kvq_prompt_mass and kvq_evict_int4 keep them. Where another call puts tokens into slots
+ * (kvq_rotate_quant_append, a decode, window or tree call with new rows, kvq_tree_commit_int4, kvq_pages_fork), mass and ids
+ * there are the caller's to set before the next eviction, by kvq_mass_start or from those of other slots: what they held may be
+ * of tokens that have left, or of a session before.
  */
 typedef struct kvq_token_mass {
   float* mass;
@@ -603,6 +604,17 @@ kvq_status kvq_mass_attn_int4_fwht(const kvq_int4_cache* cache, const kvq_token_
                                    const int32_t* ctx_len, const int32_t* positions, const void* k_new,
                                    const void* v_new, float sm_scale, float eps, void* out, kvq_dtype out_dtype,
                                    void* workspace, size_t workspace_bytes, int32_t* dev_err, kvq_stream_t stream);
+
+/*
+ * kvq_mass_start -- tokens that another call has put into slots start their masses: for t < T and every KV head h, slot
+ *   j = slots[t] of sequence q = seq_ids[t] gets mass[q][h][j] = 0 and ids[q][h][j] = numbers[t], unless `fresh` is 0 and ids
+ *   is that number already (where a call over the prompt has set both). fresh other than 0: whatever the slots held.
+ *   seq_ids, slots, numbers: device int32[T]. A token whose row or slot is outside mass is passed over (KVQ_DEVERR_POS). No
+ *             slot is named twice with different numbers. mass and ids must not overlap one another or the lists.
+ * Requires 0 <= T (0 is a no-op), T*num_kv_heads <= 2^30.
+ */
+kvq_status kvq_mass_start(const kvq_token_mass* mass, int T, const int32_t* seq_ids, const int32_t* slots,
+                          const int32_t* numbers, int fresh, int32_t* dev_err, kvq_stream_t stream);
 
 /*
  * kvq_prompt_mass -- what the tokens of packed prompts have gathered from their last rows: the mass that a cache filled with

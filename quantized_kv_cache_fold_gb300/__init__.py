@@ -111,6 +111,8 @@ def _load():
         getattr(L, name).restype = i32
         getattr(L, name).argtypes = [ctypes.POINTER(Int4Cache), ctypes.POINTER(TokenMass), vp, vp, vp, i32, i32, i32, vp, vp,
                                      vp, vp, f32, f32, vp, i32, vp, sz, vp, vp]
+    L.kvq_mass_start.restype = i32
+    L.kvq_mass_start.argtypes = [ctypes.POINTER(TokenMass), i32, vp, vp, vp, i32, vp, vp]
     L.kvq_prompt_mass_workspace_bytes.restype = sz
     L.kvq_prompt_mass_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
     L.kvq_prompt_mass.restype = i32
@@ -678,6 +680,16 @@ def kvq_mass_attn_int4(cache: Int4Cache, mass: TokenMass, Mq, Mk, q, ctx_len, po
                 workspace.data_ptr(), _bytes(workspace, dev), _err(dev_err, dev), _here(dev, stream))
     if status:
         raise KvqError("kvq_mass_attn_int4_fwht" if fwht else "kvq_mass_attn_int4", status)
+
+
+def kvq_mass_start(mass: TokenMass, seq_ids, slots, numbers, dev_err, fresh: bool = False, stream=None):
+    """Tokens that another call has put into `slots` of sequences seq_ids (all int32[T]) start with no mass and their numbers,
+    but where a slot has its token's number already (fresh: there too)."""
+    i32, T, dev = _torch().int32, seq_ids.shape[0], _dev(seq_ids, "seq_ids")
+    status = lib.kvq_mass_start(ctypes.byref(mass), T, *(_is(x, i32, (T,), name, dev) for x, name in (
+        (seq_ids, "seq_ids"), (slots, "slots"), (numbers, "numbers"))), int(fresh), _err(dev_err, dev), _here(dev, stream))
+    if status:
+        raise KvqError("kvq_mass_start", status)
 
 
 def kvq_prompt_mass_workspace_bytes(T: int, B: int, num_q_heads: int, num_kv_heads: int, rows: int) -> int:

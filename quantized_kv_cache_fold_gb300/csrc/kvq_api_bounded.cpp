@@ -189,6 +189,21 @@ kvq_status kvq_mass_attn_int4_fwht(const kvq_int4_cache* cache, const kvq_token_
                    out_dtype, workspace, workspace_bytes, dev_err, stream, 1);
 }
 
+kvq_status kvq_mass_start(const kvq_token_mass* mass, int T, const int32_t* seq_ids, const int32_t* slots,
+                          const int32_t* numbers, int fresh, int32_t* dev_err, kvq_stream_t stream) {
+  const kvq_status st = check_mass(mass, nullptr, 0);
+  if (st != KVQ_OK) return st;
+  if (T < 0 || (long long)T * mass->num_kv_heads > (1LL << 30)) return KVQ_ERR_INVALID_ARG;
+  if (T == 0) return KVQ_OK;
+  if (!seq_ids || !slots || !numbers || !dev_err) return KVQ_ERR_INVALID_ARG;
+  const size_t held = 4 * (size_t)mass->num_seqs * mass->num_kv_heads * mass->max_tokens, lists = 4 * (size_t)T;
+  if (overlap(mass->mass, held, mass->ids, held)) return KVQ_ERR_INVALID_ARG;
+  for (const void* x : {(const void*)mass->mass, (const void*)mass->ids})
+    for (const int32_t* y : {seq_ids, slots, numbers})
+      if (overlap(x, held, y, lists)) return KVQ_ERR_INVALID_ARG;
+  return from_cuda(kvq::launch_mass_start(*mass, T, seq_ids, slots, numbers, fresh, dev_err, (cudaStream_t)stream));
+}
+
 size_t kvq_prompt_mass_workspace_bytes(int T, int B, int num_q_heads, int num_kv_heads, int rows) {
   if (T < 0 || B < 1 || B > KVQ_MAX_SEQS || num_q_heads < 1 || num_kv_heads < 1 || num_q_heads % num_kv_heads ||
       num_q_heads / num_kv_heads > 64 || (long long)T * num_q_heads > (1LL << 30))

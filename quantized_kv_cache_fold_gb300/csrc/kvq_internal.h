@@ -237,6 +237,8 @@ struct EvictJob {
   int32_t* dev_err;
 };
 cudaError_t launch_evict(const EvictJob& job, cudaStream_t stream);
+cudaError_t launch_mass_start(const kvq_token_mass& mass, int T, const int32_t* seq_ids, const int32_t* slots, const int32_t* numbers,
+                              int fresh, int32_t* dev_err, cudaStream_t stream);
 
 // The caches of one call over several layers, checked; all of one number of KV heads.
 kvq_status cache_set(const kvq_int4_cache* caches, int num_caches, CacheSet& cs);

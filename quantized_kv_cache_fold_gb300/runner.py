@@ -4,8 +4,7 @@ Holds, per layer, the device state of the rotated int4 path (page pool, block ta
 M_q/M_k) or of the FP8 sliding-window path (ring), plus one shared workspace and error
 word; `decode_step` runs every layer of one decode step through the C ABI, in model
 order (Kolibri-1: 50 layers, every fifth one full attention; "Serving Kolibri-1 with a
-4-bit KV cache", section "What we do"). Torch is used for device memory and the values that it
-starts with.
+4-bit KV cache", section "What we do"). Torch is used for device memory only.
 """
 
 from __future__ import annotations
@@ -18,8 +17,8 @@ import torch
 from . import (HEAD_DIM, MAX_CACHES, PAGE_SIZE, alloc_fp8_ring, alloc_int4_cache, alloc_mass_workspace, alloc_prompt_mass_workspace,
                alloc_prompt_workspace, alloc_token_mass, alloc_tree_workspace, alloc_workspace, kvq_build_rotation,
                kvq_decode_attn_fp8_swa, kvq_decode_attn_int4, kvq_evict_int4, kvq_fold_qk, kvq_fold_qk_fwht, kvq_fp8_append,
-               kvq_mass_attn_int4, kvq_prompt_attn, kvq_prompt_mass, kvq_rotate_quant_append, kvq_tree_attn_fp8_swa,
-               kvq_tree_attn_int4, kvq_tree_commit_fp8, kvq_tree_commit_int4, kvq_window_attn_int4)
+               kvq_mass_attn_int4, kvq_mass_start, kvq_prompt_attn, kvq_prompt_mass, kvq_rotate_quant_append,
+               kvq_tree_attn_fp8_swa, kvq_tree_attn_int4, kvq_tree_commit_fp8, kvq_tree_commit_int4, kvq_window_attn_int4)
 
 
 @dataclass
@@ -105,22 +104,9 @@ class DecodeStack:
         if L.mass is None or slots is None:
             slots = positions
         kvq_rotate_quant_append(L.cache, L.Mk, k, v, seq_ids, slots, self.dev_err, stream=stream, fwht=L.fwht)
-        if L.mass is not None and k.shape[0]:
-            self._on(stream, self._start_masses, L.held["mass"], L.held["ids"], seq_ids, slots, positions,
-                     not L.observed if fresh is None else fresh)
-
-    @staticmethod
-    def _start_masses(mass, ids, seq_ids, slots, numbers, fresh):
-        B, Hkv, N = mass.shape
-        ok = (seq_ids >= 0) & (seq_ids < B) & (slots >= 0) & (slots < N)
-        # the append flags tokens with no place and passes them over; here they do what the first good one does, or (where
-        # none is good) leave some place as it is
-        use = torch.where(ok, torch.arange(ok.shape[0], device=ok.device), ok.to(torch.int32).argmax())
-        row, slot = seq_ids[use].clamp(0, B - 1).long(), slots[use].clamp(0, N - 1).long()
-        at = (row[:, None], torch.arange(Hkv, device=ok.device)[None], slot[:, None])
-        new = ok[use][:, None] & (fresh | (ids[at] != numbers[use][:, None]))
-        mass[at] = torch.where(new, 0.0, mass[at])
-        ids[at] = torch.where(new, numbers[use][:, None], ids[at])
+        if L.mass is not None:
+            lists = (x if x.shape[0] == k.shape[0] else x[:k.shape[0]] for x in (seq_ids, slots, positions))
+            kvq_mass_start(L.mass, *lists, self.dev_err, fresh=not L.observed if fresh is None else fresh, stream=stream)
 
     def prefill_int4(self, l, ctx, fill, chunk_tokens=16384, bf16=True):
         """Append positions 0..ctx[b]-1 of every sequence; fill(b, pos0, T, k_out, v_out) writes the
@@ -168,16 +154,12 @@ class DecodeStack:
     def _alloc_for(self, stream, alloc, *sizes):
         """A workspace (or what layers keep) allocated in the order of the stream that will use it (None: the current one; else a
         stream or its raw handle), so that the allocator hands its memory to nothing else before that stream is done with it."""
-        return self._on(stream, alloc, *sizes, self.device)
-
-    @staticmethod
-    def _on(stream, f, *args):
         if stream is None:
-            return f(*args)
+            return alloc(*sizes, self.device)
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream)
         with torch.cuda.stream(stream):
-            return f(*args)
+            return alloc(*sizes, self.device)
 
     def prompt_layer(self, l, q, k, v, cu_seqlens, out, workspace=None, stream=None):
         """Attention of whole prompts, packed end to end, in layer l (windowed in a sliding-window layer);

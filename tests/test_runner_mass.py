@@ -54,59 +54,35 @@ def test_memory_is_taken_once_and_in_the_order_of_the_stream(fake, stream):
     assert st.mass_layers() == [1, 3, 5]
 
 
-def appended(st, monkeypatch, seq, pos, slots=None, fresh=None, call="append_prompt"):
-    """What the layer's slots hold after an append, and the slots that its records went to."""
-    to = []
-    monkeypatch.setattr(runner, "kvq_rotate_quant_append", lambda c, M, k, v, s, p, err, stream, fwht: to.append((s.tolist(), p.tolist(), stream)))
-    i32 = lambda x: None if x is None else torch.tensor(x, dtype=torch.int32)  # noqa: E731
-    k = torch.zeros(len(seq), 2, 128)
-    getattr(st, call)(1, k, k, i32(seq), i32(pos), slots=i32(slots), fresh=fresh)
-    assert to == [(seq, pos if slots is None else slots, None)]
-    return st.layers[1].held
-
-
 @pytest.mark.parametrize("call", ["append_prompt", "append_int4"])
-@pytest.mark.parametrize("slots,fresh,observed", [
-    ([100, 101, 5], None, False), ([100, 101, 5], None, True), ([100, 101, 5], True, True), ([100, 101, 5], False, False),
-    (None, None, False), (None, None, True), (None, True, True), (None, False, False)])
-def test_masses_of_appended_tokens(fake, monkeypatch, call, slots, fresh, observed):
-    """Rows that another session has used: numbers in another order, and masses, at every slot."""
+@pytest.mark.parametrize("stream", [None, 77])
+@pytest.mark.parametrize("slots", [None, [100, 101, 5]])
+@pytest.mark.parametrize("fresh,observed,want", [(None, False, True), (None, True, False), (True, True, True), (False, False, False)])
+def test_masses_of_appended_tokens(fake, monkeypatch, call, stream, slots, fresh, observed, want):
+    """Behind the records, on their stream, at their slots, with the tokens' numbers."""
+    calls = []
+    monkeypatch.setattr(runner, "kvq_rotate_quant_append", lambda c, M, k, v, seq, pos, err, stream, fwht: calls.append((seq, pos, stream)))
+    monkeypatch.setattr(runner, "kvq_mass_start", lambda m, seq, slot, num, err, fresh, stream: calls.append((m, seq, slot, num, err, fresh, stream)))
     st = stack()
     st.keep_mass([1])
-    L = st.layers[1]
-    held = L.held
-    g = torch.Generator().manual_seed(1)
-    held["mass"].copy_(torch.rand(held["mass"].shape, generator=g) + 1)
-    held["ids"].copy_(torch.randint(1000, held["ids"].shape, generator=g, dtype=torch.int32))
-    seq, pos = [0, 0, 2], [120, 121, 122]
-    held["ids"][0, :, 121] = 121  # one slot holds its token's number already (as a call that observes the prompt leaves it)
-    held["ids"][2, 1, 5] = 122
-    L.observed = observed
-    mass, ids = held["mass"].clone(), held["ids"].clone()
-    appended(st, monkeypatch, seq, pos, slots, fresh, call)
-    for b, p, s in zip(seq, pos, slots or pos):
-        for h in range(2):
-            if not (not observed if fresh is None else fresh) and ids[b, h, s] == p:
-                continue
-            mass[b, h, s], ids[b, h, s] = 0.0, p
-    assert torch.equal(held["mass"], mass) and torch.equal(held["ids"], ids)
+    st.layers[1].observed = observed
+    seq, pos = (torch.tensor(x, dtype=torch.int32) for x in ([0, 0, 2, 1], [120, 121, 122, 123]))
+    at = pos if slots is None else torch.tensor(slots + [6], dtype=torch.int32)
+    k = torch.zeros(3, 2, 128)  # (lists may be longer than the tokens)
+    getattr(st, call)(1, k, k, seq, pos, stream=stream, slots=None if slots is None else at, fresh=fresh)
+    (seq1, to, on), (mass, seq2, slot, num, err, how, on2) = calls
+    assert seq1 is seq and to is at and on == on2 == stream and mass is st.layers[1].mass and err is st.dev_err and how is want
+    assert [x.tolist() for x in (seq2, slot, num)] == [x[:3].tolist() for x in (seq, at, pos)]
 
 
-def test_tokens_without_a_place(fake, monkeypatch):
-    """The append flags them; no slot's mass changes for them."""
+def test_prompts_that_are_observed(fake, monkeypatch):
+    monkeypatch.setattr(runner, "kvq_prompt_mass", lambda *a, **k: None)
+    monkeypatch.setattr(runner, "alloc_prompt_mass_workspace", lambda *a: None)
     st = stack()
-    st.keep_mass([1])
-    held = st.layers[1].held
-    held["mass"].fill_(2.0)
-    mass, ids = held["mass"].clone(), held["ids"].clone()
-    appended(st, monkeypatch, [-1, 3, 0, 1], [5, 5, -2, 128])
-    assert torch.equal(held["mass"], mass) and torch.equal(held["ids"], ids)
-    appended(st, monkeypatch, [7, 1, 2, 0], [500, 6, 1 << 30, 9], [3, 6, 128, -1])
-    mass[1, :, 6] = 0.0
-    ids[1, :, 6] = 6
-    assert torch.equal(held["mass"], mass) and torch.equal(held["ids"], ids)
-    appended(st, monkeypatch, [], [])
-    assert torch.equal(held["mass"], mass)
+    st.keep_mass()
+    q = torch.zeros(3, 4, 128)
+    st.observe_prompt(1, q, q[:, :2], torch.zeros(2, dtype=torch.int32), 4)
+    assert [st.layers[l].observed for l in st.int4_layers()] == [True, False]
 
 
 def test_layers_without_mass_append_at_the_positions(monkeypatch):
